@@ -97,6 +97,7 @@ typedef enum {
 /* Limits (LORA_ERR_UNSUPPORTED beyond them). */
 #define LORA_MAX_GROUPS 8
 #define LORA_MAX_RANK 1024
+#define LORA_MAX_POOL 16384 /* adapters of a lora_pool */
 
 /*
  * One adapter of a stacked layer (q/k/v or gate/up), covering the output
@@ -403,6 +404,88 @@ int lora_linear_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void
 
 /* Workspace bytes of lora_linear_bwd (transposed copies, the rank-wide intermediates, partial sums). */
 size_t lora_linear_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank, int32_t want_dx);
+
+/*
+ * A pool of adapters of one layer, from which each token takes its own
+ * (lora_linear_routed_fwd / _bwd): n_adapters slots of one size, the pool kept
+ * on the device and filled by the caller. Host struct, device pointers.
+ */
+typedef struct lora_pool {
+  const void* A;          /* [n_adapters, rank, K] bf16                                       */
+  const void* B;          /* [n_adapters, N, rank] bf16                                       */
+  const float* scales;    /* [n_adapters]: (alpha / rank) . strength of each                  */
+  const int32_t* ranks;   /* [n_adapters]: the adapter's rank within its slot, or NULL: `rank` */
+  int32_t n_adapters;     /* 0 <= n_adapters <= LORA_MAX_POOL                                 */
+  int32_t rank;           /* rank of a slot, a multiple of 8                                  */
+  int64_t reserved;       /* set to 0 */
+} lora_pool;
+
+/*
+ * lora_linear_routed_fwd -- one LoRA linear layer for a batch whose tokens
+ * belong to different requests, each with its own adapter (SGLang PR #43501,
+ * Motivation and Modifications: the scale is honoured per request; here the
+ * adapter is too):
+ *
+ *     y[t] = x[t] . W^T + b + t~_t . B_a^T,   t~_t = RN_bf16(s_t . (x[t] . A_a^T)),
+ *     a = token_adapter[t],  s_t = RN_f32(scales[a] . token_scale[t])
+ *
+ *   token_adapter  [T] int32 (device). A token whose index is outside
+ *                  [0, n_adapters) (-1 by convention), whose s_t is +-0 or
+ *                  whose adapter's rank is <= 0 gets the base output. May be
+ *                  NULL when n_adapters is 0
+ *   token_scale    [T] fp32 (device), the request scale of each token, or NULL (1)
+ *   bias, y, ldx, ldy, workspace  as lora_linear_fwd; x, W, bias and y are bf16
+ *   workspace      at least lora_linear_routed_workspace_size(...) bytes
+ * ranks[a] is taken up to the slot's rank and rounded up to a multiple of 8:
+ * rows of A and columns of B between an adapter's rank and that multiple must
+ * hold zeros, those behind it are never read. The values behind the device
+ * pointers are read by the kernels alone (a captured call takes the routing
+ * that they hold at each replay); they cannot be refused, and an adapter or
+ * scale that is not finite reaches the outputs of its own tokens and no others.
+ * Tokens may come in any order; the adapter costs least where tokens of one
+ * adapter lie next to one another.
+ * T == 0 is a valid no-op. LORA_ERR_ALIGN unless x, W, A, B and the workspace
+ * are 16-byte aligned and K, ldx and the slot rank are multiples of 8.
+ * The output of a token depends on the other tokens of the batch in its last
+ * bit only (the order of the fp32 sums); the same call gives the same bits.
+ */
+int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                           const void* bias, const lora_pool* pool, const int32_t* token_adapter,
+                           const float* token_scale, void* y, int64_t ldy, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_linear_routed_fwd; 0 when T, K or N <= 0. */
+size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank);
+
+/*
+ * lora_linear_routed_bwd -- gradients of lora_linear_routed_fwd for an output
+ * gradient dy, the base weight and bias frozen (Unsloth fast-LoRA chapter,
+ * sections 2 and 4, per adapter):
+ *
+ *     u_t = s_t . (dy[t] . B_a),  dx[t] = RN_bf16(dy[t] . W + RN_bf16(u_t) . A_a),
+ *     dA_a = sum over a's tokens of u_t^T . x[t],
+ *     dB_a = sum over a's tokens of dy[t]^T . (s_t . x[t] . A_a^T)
+ *
+ *   x [T, K] (ldx), W [N, K], dy [T, N] (lddy) bf16, 16-byte aligned; K, N, ldx, lddy multiples of 8;
+ *   pool, token_adapter and token_scale as in the forward call
+ *   dx [T, K] bf16 (row stride lddx), dA [n_adapters, rank, K], dB [n_adapters, N, rank] fp32: each
+ *   optional (NULL = not computed; W may be NULL without dx)
+ * Every element of the outputs is written: an adapter without tokens gets zeros, and so do the rows of
+ * dA and columns of dB from the adapter's rank on. dA and dB sum in fp32 over the adapter's tokens in
+ * order, u_t and s_t x A^T taken as a bf16 pair hi + lo (about 16 bits; one bf16 would leave the fp32
+ * gradients 8). An adapter's gradients depend on its own tokens only.
+ *   workspace  at least lora_linear_routed_bwd_workspace_size(..., dx != NULL) bytes
+ * T == 0 writes zero gradients. LORA_ERR_UNSUPPORTED above about 65000 adapters and 4096-token chunks
+ * together.
+ */
+int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                           const lora_pool* pool, const int32_t* token_adapter, const float* token_scale,
+                           const void* dy, int64_t lddy, void* dx, int64_t lddx, float* dA, float* dB,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_linear_routed_bwd (transposed copies, rank-wide intermediates, partial sums). */
+size_t lora_linear_routed_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank,
+                                             int32_t want_dx);
 
 /*
  * Workspace bytes a call with T tokens, K inputs and N outputs needs for

@@ -33,6 +33,8 @@ __all__ = [
     "lora_status_string",
     "lora_device_check", "lora_mfma_probe", "lora_linear_fwd_noalloc", "LORA_NOALLOC_SCRATCH_BYTES", "lora_linear", "lora_linear_stacked", "lora_linear_nf4", "dense_patch",
     "LoraGroup", "hip_runtimes_mapped",
+    "LoraPool", "lora_linear_routed_fwd", "lora_linear_routed_workspace_size", "lora_linear_routed_bwd",
+    "lora_linear_routed_bwd_workspace_size", "lora_linear_routed", "lora_linear_routed_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora_mi355x.so")
@@ -63,6 +65,12 @@ class LoraAdapter(ctypes.Structure):
     """C ``lora_adapter``: one of several adapters on one layer."""
     _fields_ = [("A", _p), ("B", _p), ("B_bias", _p), ("rank", _i32), ("reserved", _i32), ("alpha", _f64),
                 ("strength", _f64), ("col_offset", _i64), ("n_cols", _i64)]
+
+
+class LoraPool(ctypes.Structure):
+    """C ``lora_pool``: the adapters from which the tokens of a routed call take theirs."""
+    _fields_ = [("A", _p), ("B", _p), ("scales", _p), ("ranks", _p), ("n_adapters", _i32), ("rank", _i32),
+                ("reserved", _i64)]
 
 
 _lib.lora_linear_fwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _i32, _i32, _f64, _f64, _f64,
@@ -101,6 +109,16 @@ _lib.lora_linear_bwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p, _i32, _
 _lib.lora_linear_bwd.restype = ctypes.c_int
 _lib.lora_linear_bwd_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32]
 _lib.lora_linear_bwd_workspace_size.restype = _sz
+_lib.lora_linear_routed_fwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, ctypes.POINTER(LoraPool), _p, _p, _p,
+                                        _i64, _p, _sz, _p]
+_lib.lora_linear_routed_fwd.restype = ctypes.c_int
+_lib.lora_linear_routed_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32]
+_lib.lora_linear_routed_workspace_size.restype = _sz
+_lib.lora_linear_routed_bwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, ctypes.POINTER(LoraPool), _p, _p, _p, _i64,
+                                        _p, _i64, _p, _p, _p, _sz, _p]
+_lib.lora_linear_routed_bwd.restype = ctypes.c_int
+_lib.lora_linear_routed_bwd_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
+_lib.lora_linear_routed_bwd_workspace_size.restype = _sz
 _lib.lora_merge_apply.argtypes = [_p, _i32, _i64, _i64, _p, _p, _i32, _i32, _f64, _f64, _i32, _p]
 _lib.lora_merge_apply.restype = ctypes.c_int
 _lib.lora_linear_nf4_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
@@ -171,6 +189,27 @@ def lora_linear_bwd(x, T, K, ldx, W, N, A, B, rank, alpha, strength, request_sca
 
 def lora_linear_bwd_workspace_size(T, K, N, rank, want_dx=True) -> int:
     return int(_lib.lora_linear_bwd_workspace_size(T, K, N, rank, 1 if want_dx else 0))
+
+
+def lora_linear_routed_fwd(x, T, K, ldx, W, N, bias, pool, token_adapter, token_scale, y, ldy, workspace,
+                           workspace_bytes, stream):
+    return _check(_lib.lora_linear_routed_fwd(x, T, K, ldx, W, N, bias, ctypes.byref(pool), token_adapter, token_scale,
+                                              y, ldy, workspace, workspace_bytes, stream), "lora_linear_routed_fwd")
+
+
+def lora_linear_routed_workspace_size(T, K, N, n_adapters, rank) -> int:
+    return int(_lib.lora_linear_routed_workspace_size(T, K, N, n_adapters, rank))
+
+
+def lora_linear_routed_bwd(x, T, K, ldx, W, N, pool, token_adapter, token_scale, dy, lddy, dx, lddx, dA, dB,
+                           workspace, workspace_bytes, stream):
+    return _check(_lib.lora_linear_routed_bwd(x, T, K, ldx, W, N, ctypes.byref(pool), token_adapter, token_scale, dy,
+                                              lddy, dx, lddx, dA, dB, workspace, workspace_bytes, stream),
+                  "lora_linear_routed_bwd")
+
+
+def lora_linear_routed_bwd_workspace_size(T, K, N, n_adapters, rank, want_dx=True) -> int:
+    return int(_lib.lora_linear_routed_bwd_workspace_size(T, K, N, n_adapters, rank, 1 if want_dx else 0))
 
 
 def lora_merge_apply(W, w_dtype, N, K, A, B, rank, adapter_dtype, alpha, strength, quality, stream):
@@ -389,6 +428,113 @@ def lora_linear_backward(x, W, A, B, dy, alpha, strength=1.0, request_scale=1.0,
                     float(strength), float(request_scale), dy.data_ptr(), lddy, _ptr(dx), K, _ptr(dA), _ptr(dB),
                     _ptr(db), _ptr(t_tilde), ldt, ws.data_ptr(), ws.numel(), _stream(stream))
     return dx, dA, dB, db
+
+
+def _of(t, name, shape, dtype, device):
+    """The tensor checked: contiguous, of this shape and type, on the call's device (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    return t
+
+
+def _rows(t, name, shape, device):
+    """Row stride of a bf16 matrix of this shape with unit column stride on the call's device."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+    if t.numel() and t.stride(1) != 1 and t.shape[1] != 1:  # (one column may carry any stride)
+        raise ValueError(f"{name} must have unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8  # (and so may one row)
+
+
+def _routed_args(x, W, A, B, scales, token_adapter, token_scale, ranks):
+    """Checks shared by the routed calls; returns T, K, N and the C pool."""
+    dev = x.device
+    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [T, K], A [n, rank, K] and B [n, N, rank]")
+    T, K = x.shape
+    n, R, _ = A.shape
+    N = B.shape[1]
+    _of(A, "A", (n, R, K), torch.bfloat16, dev)
+    _of(B, "B", (n, N, R), torch.bfloat16, dev)
+    _of(scales, "scales", (n,), torch.float32, dev)
+    _of(token_adapter, "token_adapter", (T,), torch.int32, dev)
+    _of(token_scale, "token_scale", (T,), torch.float32, dev)
+    _of(ranks, "ranks", (n,), torch.int32, dev)
+    if W is not None:
+        _of(W, "W", (N, K), torch.bfloat16, dev)
+    return T, K, N, LoraPool(_ptr(A), _ptr(B), _ptr(scales), _ptr(ranks), n, R, 0)
+
+
+def _bytes_on(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace
+
+
+def _stream_on(device, stream):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def lora_linear_routed(x, W, b, A, B, scales, token_adapter, token_scale=None, ranks=None, out=None, workspace=None,
+                       stream=None):
+    """A linear layer whose tokens take their adapters from a pool (bf16; returns ``out``):
+    y[t] = x[t].W^T + b + s_t (x[t].A_a^T).B_a^T with a = token_adapter[t], s_t = scales[a] token_scale[t].
+
+    A [n, rank, K] and B [n, N, rank] are the pool, ``scales`` fp32 [n], ``token_adapter`` int32 [T]
+    (-1: no adapter), ``token_scale`` fp32 [T] or None, ``ranks`` int32 [n] or None (see lora_linear_routed_fwd)."""
+    T, K, N, pool = _routed_args(x, W, A, B, scales, token_adapter, token_scale, ranks)
+    dev = x.device
+    ldx = _rows(x, "x", (T, K), dev)
+    _of(b, "b", (N,), torch.bfloat16, dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        ldy = _rows(out, "out", (T, N), dev)
+        ws = _bytes_on(workspace, lora_linear_routed_workspace_size(T, K, N, A.shape[0], A.shape[1]), dev)
+        lora_linear_routed_fwd(x.data_ptr(), T, K, ldx, W.data_ptr(), N, _ptr(b), pool, token_adapter.data_ptr(),
+                               _ptr(token_scale), out.data_ptr(), ldy, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    return out
+
+
+def lora_linear_routed_backward(x, W, A, B, dy, scales, token_adapter, token_scale=None, ranks=None,
+                                want=("dx", "dA", "dB"), dx=None, dA=None, dB=None, workspace=None, stream=None):
+    """Gradients of ``lora_linear_routed`` for the output gradient ``dy``: returns (dx, dA, dB), each
+    None unless named in ``want`` (dx bf16 [T, K]; dA [n, rank, K] and dB [n, N, rank] fp32, written
+    whole into the given tensors when there are any)."""
+    T, K, N, pool = _routed_args(x, W, A, B, scales, token_adapter, token_scale, ranks)
+    n, R, _ = A.shape
+    dev = x.device
+    ldx, lddy = _rows(x, "x", (T, K), dev), _rows(dy, "dy", (T, N), dev)
+    with torch.cuda.device(dev):
+        if "dx" not in want:
+            dx = None
+        elif dx is None:
+            dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        lddx = _rows(dx, "dx", (T, K), dev) if dx is not None else K
+        grads = []
+        for name, t, shape in (("dA", dA, (n, R, K)), ("dB", dB, (n, N, R))):
+            if name not in want:
+                t = None
+            elif t is None:
+                t = torch.empty(shape, dtype=torch.float32, device=dev)
+            grads.append(_of(t, name, shape, torch.float32, dev))
+        dA, dB = grads
+        ws = _bytes_on(workspace, lora_linear_routed_bwd_workspace_size(T, K, N, n, R, dx is not None), dev)
+        lora_linear_routed_bwd(x.data_ptr(), T, K, ldx, _ptr(W), N, pool, token_adapter.data_ptr(),
+                               _ptr(token_scale), dy.data_ptr(), lddy, _ptr(dx), lddx, _ptr(dA), _ptr(dB),
+                               ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    return dx, dA, dB
 
 
 def dense_patch(dst, src, strength, mode="add", stream=None):

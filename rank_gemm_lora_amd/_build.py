@@ -34,6 +34,8 @@ SOURCES = {
     "patch.hip": ["-ffp-contract=off"],
     "probe.hip": [],
     "noalloc.hip": [],
+    "routed.hip": [],
+    "routed_api.cpp": [],
     "api.cpp": [],
 }
 

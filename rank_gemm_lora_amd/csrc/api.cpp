@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "backward.hpp"
+#include "checks.hpp"
 #include "lora_mi355x.h"
 #include "launch.hpp"
 
@@ -17,34 +18,18 @@ namespace {
 using lora::Elt;
 using lora::GroupDev;
 using lora::LinearProblem;
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-  bool empty() const { return lo == hi; }
-};
-
-Span span2d(const void* p, int64_t rows, int64_t ld, int64_t cols, int esize) {
-  Span s;
-  if (p == nullptr || rows <= 0 || cols <= 0) return s;
-  s.lo = reinterpret_cast<uintptr_t>(p);
-  s.hi = s.lo + static_cast<uintptr_t>(((rows - 1) * ld + cols) * esize);
-  return s;
-}
-
-bool overlaps(const Span& a, const Span& b) {
-  return !a.empty() && !b.empty() && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void* p, uintptr_t a) { return p == nullptr || reinterpret_cast<uintptr_t>(p) % a == 0; }
+using lora::aligned;
+using lora::kMaxRowBytes;
+using lora::overlaps;
+using lora::round_up;
+using lora::Span;
+using lora::span2d;
 
 bool dtype_ok(int d) { return d == LORA_F32 || d == LORA_BF16; }
 Elt to_elt(int d) { return d == LORA_BF16 ? Elt::BF16 : Elt::F32; }
 int esz(int d) { return d == LORA_BF16 ? 2 : 4; }
 
 bool finite_scale(double v) { return std::isfinite(v); }
-
-// The staging kernels address one tile of rows with 32-bit byte offsets.
-constexpr int64_t kMaxRowBytes = int64_t(1) << 22;
 
 // Adapter description shared by the linear entry points.
 struct Adapter {
@@ -87,9 +72,6 @@ int fill_groups(LinearProblem& p, const Adapter* ads, int n, double request_scal
   p.ldt = tcol;
   return LORA_OK;
 }
-
-constexpr size_t kWsAlign = 256;
-size_t round_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
 // Workspace layout of a call. Usually t~ [T, sum r_pad] in the adapter dtype.
 // Lossless fp32 adapters on bf16 activations: t~ [T, 3 sum r_pad] bf16, then the

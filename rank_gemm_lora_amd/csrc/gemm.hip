@@ -1224,9 +1224,10 @@ __device__ __forceinline__ void epilogue_lds16s(const f32x4 (&acc)[P::NI][P::NJ]
 // K-extension plan of one adapter group for one output tile: where its t~
 // columns and B rows are, which tile rows its B rows cover, and how many
 // 64-k stages its padded rank takes.
+// ldb: bytes from one B row to the next (rkb, except in a pool slot wider than its adapter's rank).
 struct ExtPlan {
   const char* B;
-  int tcb, tpb, rkb, n_cols, lo, hi, sh, ns;
+  int tcb, tpb, rkb, ldb, n_cols, lo, hi, sh, ns;
 };
 
 // Copies of K-extension stage e of group g through precomputed per-lane
@@ -1238,9 +1239,158 @@ __device__ __forceinline__ void ext_stage_loads(const ExtPlan& g, int e, const T
 #pragma unroll
   for (int l = 0; l < TileOffsets<P, P::BM>::N; ++l) ot.load_one(l, xdst, tr, g.tcb + e * P::RB);
   TileOffsets<P, P::BN> ob;
-  ob.init(static_cast<uint32_t>(g.rkb), g.lo, g.hi, g.sh);
-  const __amdgpu_buffer_rsrc_t br = make_rsrc(g.B, static_cast<uint32_t>(g.n_cols) * static_cast<uint32_t>(g.rkb));
+  ob.init(static_cast<uint32_t>(g.ldb), g.lo, g.hi, g.sh);
+  const __amdgpu_buffer_rsrc_t br = make_rsrc(g.B, static_cast<uint32_t>(g.n_cols) * static_cast<uint32_t>(g.ldb));
   ob.load(wdst, br, e * P::RB, (e + 1) * P::RB > g.rkb, g.rkb);
+}
+
+__device__ __forceinline__ int routed_rank(const RoutedGemm& rt, int a) {
+  return rt.ranks != nullptr ? __builtin_amdgcn_readfirstlane((min(rt.ranks[a], rt.rank) + 7) & ~7) : rt.rank;
+}
+
+// Routed: how this tile's adapters are met. All of its tokens with one adapter: its K-extension plan
+// (the pool slot's rows n0 .., its rank padded to 64-k stages), false. No adapter at all: no plan,
+// false. Otherwise true: the updates are added after the loop.
+template <class P>
+__device__ __forceinline__ bool routed_plan(const LinearProblem& p, int64_t m0, int64_t n0, int rows_m, int rows_n,
+                                            int lane, ExtPlan& e) {
+  constexpr int NBLK = P::BM / kRouteBlock;
+  const int nb = (rows_m + kRouteBlock - 1) / kRouteBlock;
+  const int f = p.rt.blk[m0 / kRouteBlock + min(lane % NBLK, nb - 1)];
+  const int a = __builtin_amdgcn_readfirstlane(f);
+  if (__builtin_amdgcn_ballot_w64(f != a) != 0 || a == -2) return true;
+  if (a < 0) return false;
+  const int rank = routed_rank(p.rt, a);
+  e.B = static_cast<const char*>(p.rt.B) + static_cast<int64_t>(a) * p.N * p.rt.rank * 2;
+  e.tcb = 0;
+  e.ns = (rank * 2 + P::RB - 1) / P::RB;
+  e.tpb = e.ns * P::RB;
+  e.rkb = rank * 2;
+  e.ldb = p.rt.rank * 2;
+  e.n_cols = static_cast<int>(p.N);
+  e.lo = 0;
+  e.hi = rows_n;
+  e.sh = static_cast<int>(n0);
+  return false;
+}
+
+// acc += t~ . B_a^T for the tokens of this wave's block (first token mw, first output nw), each with
+// its own adapter, in ascending adapter order. An adapter's B rows are loaded once per 64 ranks
+// straight into MFMA operands (lane (r, q): ranks 8q .. +7 of output 16 i + r) and used for every
+// 16-token block that holds one of its tokens; the block's other tokens enter as zeros of t~. A zero
+// times an infinite or NaN weight would be NaN, so that one request's broken adapter would reach the
+// outputs of others: such weights (found by the largest magnitude of the loaded operands) enter as
+// zeros, and true is returned: routed_broken then puts their outputs right. (Adding the product to the
+// adapter's own lanes by VALU instead spilled 1223 registers of the 256 x 256 tile.)
+template <class P>
+__device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const LinearProblem& p, int64_t mw,
+                                             int64_t nw, int lane) {
+  const int r = lane & 15, q = lane >> 4;
+  int id[P::NJ];
+#pragma unroll
+  for (int j = 0; j < P::NJ; ++j) {
+    const int64_t m = mw + j * 16 + r;
+    id[j] = m < p.T ? p.rt.eid[m] : -1;
+  }
+  const uint32_t ldb = static_cast<uint32_t>(p.rt.rank * 2), ldt_b = static_cast<uint32_t>(p.ldt * 2);
+  const int rows_n = static_cast<int>(min<int64_t>(P::WN, p.N - nw));
+  const int rows_m = static_cast<int>(min<int64_t>(P::WM, p.T - mw));
+  if (rows_n <= 0 || rows_m <= 0) return false;
+  const __amdgpu_buffer_rsrc_t tr =
+      make_rsrc(static_cast<const char*>(p.work) + mw * p.ldt * 2, static_cast<uint32_t>(rows_m) * ldt_b);
+  bool broken = false;
+  int prev = -1;
+  while (true) {
+    int a = 0x7fffffff;  // the smallest adapter of the wave's tokens after prev
+#pragma unroll
+    for (int j = 0; j < P::NJ; ++j) a = id[j] > prev ? min(a, id[j]) : a;
+#pragma unroll
+    for (int s = 1; s < 16; s *= 2) a = min(a, __shfl_xor(a, s));
+    a = __builtin_amdgcn_readfirstlane(a);
+    if (a == 0x7fffffff) break;
+    prev = a;
+    const int rank = routed_rank(p.rt, a);
+    const __amdgpu_buffer_rsrc_t br =
+        make_rsrc(static_cast<const char*>(p.rt.B) + (static_cast<int64_t>(a) * p.N + nw) * ldb,
+                  static_cast<uint32_t>(rows_n) * ldb);
+    for (int c0 = 0; c0 < rank; c0 += 64) {
+      u32x4 w[P::NI][2];
+#pragma unroll
+      for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = c0 + 32 * h + 8 * q;
+          const uint32_t off = k < rank ? static_cast<uint32_t>(i * 16 + r) * ldb + k * 2 : 0x80000000u;
+          w[i][h] = __builtin_amdgcn_raw_buffer_load_b128(br, off, 0, 0);
+        }
+      u16x2 top = {0, 0};
+#pragma unroll
+      for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[i][h][e] & 0x7fff7fffu));
+      if (__builtin_amdgcn_ballot_w64(max(top[0], top[1]) >= 0x7f80) != 0) {
+        broken = true;
+#pragma unroll
+        for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((w[i][h][e] & 0x7f80u) == 0x7f80u) w[i][h][e] &= 0xffff0000u;
+              if ((w[i][h][e] & 0x7f800000u) == 0x7f800000u) w[i][h][e] &= 0xffffu;
+            }
+      }
+#pragma unroll
+      for (int j = 0; j < P::NJ; ++j) {
+        const bool mine = id[j] == a;
+        if (__builtin_amdgcn_ballot_w64(mine) == 0) continue;
+        bf16x8 t[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = c0 + 32 * h + 8 * q;
+          const uint32_t off = mine && k < rank ? static_cast<uint32_t>(j * 16 + r) * ldt_b + k * 2 : 0x80000000u;
+          t[h] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(tr, off, 0, 0));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < P::NI; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][h]), t[h], acc[i][j],
+                                                                0, 0, 0);
+      }
+    }
+  }
+  return broken;
+}
+
+// The outputs of this wave's block that an infinite or NaN adapter weight reaches, after the block was
+// written without such weights: t~ . B_a[n]^T over the whole row (infinite or NaN) is added to them.
+template <class P>
+__device__ __forceinline__ void routed_broken(const LinearProblem& p, int64_t mw, int64_t nw, int lane) {
+  wait_vmem();  // this wave's output stores
+  const int rows_n = static_cast<int>(min<int64_t>(P::WN, p.N - nw));
+  const int rows_m = static_cast<int>(min<int64_t>(P::WM, p.T - mw));
+  for (int i = 0; i < rows_m; ++i) {
+    const int64_t m = mw + i;
+    const int a = __builtin_amdgcn_readfirstlane(p.rt.eid[m]);
+    if (a < 0) continue;
+    const int rank = routed_rank(p.rt, a);
+    const bf16_bits* t = static_cast<const bf16_bits*>(p.work) + m * p.ldt;
+    for (int n = lane; n < rows_n; n += 64) {
+      const bf16_bits* b = static_cast<const bf16_bits*>(p.rt.B) + (static_cast<int64_t>(a) * p.N + nw + n) * p.rt.rank;
+      bool bad = false;
+      float dot = 0.f;
+      for (int k = 0; k < rank; ++k) {
+        bad = bad || (b[k] & 0x7f80) == 0x7f80;
+        dot += bf16_to_f32(t[k]) * bf16_to_f32(b[k]);
+      }
+      bf16_bits* y = static_cast<bf16_bits*>(p.y) + m * p.ldy + nw + n;
+      if (bad) *y = f32_to_bf16_rne(bf16_to_f32(*y) + dot);
+    }
+  }
 }
 
 // Stage t of the 16 x 16 kernel is 2 NB MFMA bundles (NB = NI NJ per k-step: 64 for
@@ -1260,7 +1410,10 @@ __device__ __forceinline__ void ext_stage_loads(const ExtPlan& g, int e, const T
 // during stage t in sub-steps of a few VALU instructions, one or two per MFMA bundle, and each
 // word written into the slot that the barrier of stage t releases, where the copies would have
 // gone. The weight is the panel kernel's, bit for bit, and so is the result.
-template <class P, bool NF4 = false>
+// ROUTED: the tokens take their adapters from a pool (p.rt). A tile whose tokens all take the same
+// adapter is the one-adapter case, K-extension and all, its B found from the tile; any other tile
+// runs without extension stages and adds its adapters' updates after the loop (routed_mixed).
+template <class P, bool NF4 = false, bool ROUTED = false>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearProblem p, int mt, int nt) {
   static_assert(P::WAVES == 4, "schedule written for 4 waves");
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
@@ -1332,13 +1485,14 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
     }
   }
   auto ext_group = [&](int gi) {
-    ExtPlan e{nullptr, 0, 0, 0, 0, 0, 0, 0, 0};
+    ExtPlan e{nullptr, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (gi < p.n_groups) {
       const GroupDev& g = p.g[gi];
       e.B = static_cast<const char*>(g.B);
       e.tcb = g.t_col * 2;
       e.tpb = g.r_pad * 2;
       e.rkb = g.rank * 2;
+      e.ldb = e.rkb;
       e.n_cols = static_cast<int>(g.n_cols);
       e.lo = static_cast<int>(max<int64_t>(0, g.col_off - n0));
       e.hi = static_cast<int>(min<int64_t>(rows_n, g.col_off + g.n_cols - n0));
@@ -1347,7 +1501,9 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
     }
     return e;
   };
-  const ExtPlan eg0 = ext_group(gs0), eg1 = ext_group(gs1);
+  ExtPlan eg0 = ext_group(gs0), eg1 = ext_group(gs1);
+  bool mixed = false;
+  if constexpr (ROUTED) mixed = routed_plan<P>(p, m0, n0, rows_m, rows_n, lane, eg0);
   // Stage order: the K-extension stages first, then the main stages (s >= NE is main stage s - NE).
   const int NE = eg0.ns + eg1.ns;
   const int NS = NE + nk;
@@ -1362,13 +1518,13 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
   TileOffsets<P, P::BN> ob0, ob1;
   if constexpr (!NF4) {
     oxe.init(ldt_b, 0, rows_m, 0);
-    ob0.init(static_cast<uint32_t>(eg0.rkb), eg0.lo, eg0.hi, eg0.sh);
-    ob1.init(static_cast<uint32_t>(eg1.rkb), eg1.lo, eg1.hi, eg1.sh);
+    ob0.init(static_cast<uint32_t>(eg0.ldb), eg0.lo, eg0.hi, eg0.sh);
+    ob1.init(static_cast<uint32_t>(eg1.ldb), eg1.lo, eg1.hi, eg1.sh);
   }
   const __amdgpu_buffer_rsrc_t br0 =
-      make_rsrc(eg0.B, static_cast<uint32_t>(eg0.n_cols) * static_cast<uint32_t>(eg0.rkb));
+      make_rsrc(eg0.B, static_cast<uint32_t>(eg0.n_cols) * static_cast<uint32_t>(eg0.ldb));
   const __amdgpu_buffer_rsrc_t br1 =
-      make_rsrc(eg1.B, static_cast<uint32_t>(eg1.n_cols) * static_cast<uint32_t>(eg1.rkb));
+      make_rsrc(eg1.B, static_cast<uint32_t>(eg1.n_cols) * static_cast<uint32_t>(eg1.ldb));
   // this lane's 16-byte chunk of a B row, the same in every copy instruction of a unit (each
   // instruction covers whole swizzle periods of rows)
   static_assert((P::WAVES * 64 / P::CPR / P::RPL) % P::CPR == 0, "one chunk per lane across a unit");
@@ -1395,8 +1551,8 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
     if (!is_w) {
       dma_one<P, P::BM>(l, dst, tr, ldt_b, 0, rows_m, 0, g.tcb + e * P::RB, g.tcb + g.tpb);
     } else {
-      const __amdgpu_buffer_rsrc_t br = make_rsrc(g.B, static_cast<uint32_t>(g.n_cols) * static_cast<uint32_t>(g.rkb));
-      dma_one<P, P::BN>(l, dst, br, static_cast<uint32_t>(g.rkb), g.lo, g.hi, g.sh, e * P::RB, g.rkb);
+      const __amdgpu_buffer_rsrc_t br = make_rsrc(g.B, static_cast<uint32_t>(g.n_cols) * static_cast<uint32_t>(g.ldb));
+      dma_one<P, P::BN>(l, dst, br, static_cast<uint32_t>(g.ldb), g.lo, g.hi, g.sh, e * P::RB, g.rkb);
     }
   };
 
@@ -1673,16 +1829,23 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
     mfma_frags16<P>(acc, fr[1]);
   }
 
+  bool broken = false;
+  if constexpr (ROUTED) {
+    if (mixed) broken = routed_mixed<P>(acc, p, m0 + wm0, n0 + wn0, lane);
+  }
   __syncthreads();  // every wave is done reading the ring; LDS becomes the staging area
   if constexpr (P::WM == 128) epilogue_lds16<P>(acc, p, m0, n0, wm0, wn0, lane, wave, smem);
   else epilogue_lds16s<P>(acc, p, m0, n0, wm0, wn0, lane, wave, smem);
+  if constexpr (ROUTED) {
+    if (broken) routed_broken<P>(p, m0 + wm0, n0 + wn0, lane);
+  }
 }
 
-template <class P, bool NF4 = false>
+template <class P, bool NF4 = false, bool ROUTED = false>
 hipError_t launch_flow16(const LinearProblem& p, hipStream_t s) {
   const int mt = static_cast<int>((p.T + P::BM - 1) / P::BM);
   const int nt = static_cast<int>((p.N + P::BN - 1) / P::BN);
-  hipLaunchKernelGGL((gemm_flow16_kernel<P, NF4>), dim3(mt * nt), dim3(P::THREADS), 0, s, p, mt, nt);
+  hipLaunchKernelGGL((gemm_flow16_kernel<P, NF4, ROUTED>), dim3(mt * nt), dim3(P::THREADS), 0, s, p, mt, nt);
   return hipGetLastError();
 }
 
@@ -1723,6 +1886,8 @@ template __global__ void gemm_flow16_kernel<Flow16Cfg>(LinearProblem, int, int);
 template __global__ void gemm_flow16_kernel<Flow16SCfg>(LinearProblem, int, int);
 template __global__ void gemm_flow16_kernel<Flow16SCfg, true>(LinearProblem, int, int);
 template __global__ void gemm_flow16_kernel<Flow16Cfg, true>(LinearProblem, int, int);
+template __global__ void gemm_flow16_kernel<Flow16Cfg, false, true>(LinearProblem, int, int);
+template __global__ void gemm_flow16_kernel<Flow16SCfg, false, true>(LinearProblem, int, int);
 
 hipError_t launch(const LinearProblem& p, hipStream_t s) {
   if (max_groups_per_tile(p, Flow16Cfg::BN) <= 2) {
@@ -1741,6 +1906,7 @@ hipError_t launch(const LinearProblem& p, hipStream_t s) {
     const double est256 = 4.0 * static_cast<double>((t256 + cus - 1) / (cus > 0 ? cus : 1));
     const double est128 = 2.0 / 0.85 * static_cast<double>((t128 + 2 * cus - 1) / (cus > 0 ? 2 * cus : 1));
     const bool small = p.tile == 2 || (p.tile == 0 && cus > 0 && est128 < est256);
+    if (p.routed) return small ? launch_flow16<Flow16SCfg, false, true>(p, s) : launch_flow16<Flow16Cfg, false, true>(p, s);
     if (p.nf4) return small ? launch_flow16<Flow16SCfg, true>(p, s) : launch_flow16<Flow16Cfg, true>(p, s);
     return small ? launch_flow16<Flow16SCfg>(p, s) : launch_flow16<Flow16Cfg>(p, s);
   }
@@ -2550,6 +2716,8 @@ hipError_t launch_bias32(const LinearProblem& p, hipStream_t s) {
   hipLaunchKernelGGL(bias32_kernel, dim3(static_cast<unsigned>((p.N + 255) / 256)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
+
+hipError_t launch_routed_gemm(const LinearProblem& p, hipStream_t s) { return pipe::launch(p, s); }
 
 hipError_t launch_lossless(const LinearProblem& p, hipStream_t s, int phase) {
   if (p.T == 0) return hipSuccess;

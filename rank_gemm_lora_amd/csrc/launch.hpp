@@ -128,6 +128,28 @@ inline bool split_fp32_adapter(Elt act, Elt adapter, bool nf4) {
   return act == Elt::BF16 && adapter == Elt::F32 && !nf4;
 }
 
+// Which adapter of a pool each token takes (the routed calls), as the kernels see it. All pointers
+// are device memory; the values behind them are not known on the host, so the kernels check them.
+struct Routing {
+  const int32_t* token_adapter;  // [T]; outside [0, n_adapters): no adapter
+  const float* token_scale;      // [T] or null
+  const float* scales;           // [n_adapters]
+  const int32_t* ranks;          // [n_adapters] or null (all `rank`)
+  int32_t n_adapters;
+  int32_t rank;                  // rows of a slot of A, columns of a slot of B (a multiple of 8)
+};
+
+// The routed GEMM's view of its pool: B [n_adapters, N, rank] and what the routed producer left in
+// the workspace (t~ [T, ldt] in LinearProblem::work).
+struct RoutedGemm {
+  const void* B;
+  const int32_t* eid;   // [T]: the token's adapter, -1 none
+  const int32_t* blk;   // [ceil(T / 16)]: the block's adapter, -1 none at all, -2 several
+  const int32_t* ranks;
+  int32_t rank;
+};
+constexpr int kRouteBlock = 16;  // tokens per entry of blk
+
 struct LinearProblem {
   const void* x; int64_t ldx;
   const void* W;                                  // [N, K] act dtype (unused for 4-bit)
@@ -147,12 +169,17 @@ struct LinearProblem {
   void* work;        // t workspace, [T, ldt] in adapter dtype
   int64_t ldt;       // sum of r_pad over groups
   int tile;          // output tile of the hot GEMM: 0 chosen from the shape, 1 256 x 256, 2 128 x 128
+  bool routed;       // the adapter comes from rt by token (n_groups == 0)
+  RoutedGemm rt;
 };
 
 // Lossless tier: t~ = RN_adt(s . x A^T) into the workspace, then the fused GEMM.
 // phase 0 runs both, 1 only the rank-wide producer, 2 only the fused GEMM
 // (which reads the t~ a phase-1 call left in the workspace).
 hipError_t launch_lossless(const LinearProblem& p, hipStream_t s, int phase = 0);
+
+// Routed: the hot GEMM with its tokens' own adapters (bf16; p.routed, t~ in p.work).
+hipError_t launch_routed_gemm(const LinearProblem& p, hipStream_t s);
 
 // Lossless with legacy lora_B biases: p.bias32 = fp32(b) + u_g . fp32(c_g) summed in group order,
 // u_g = strength_g . request_scale (the legacy vector does not take alpha / rank).

@@ -1,0 +1,284 @@
+// C-ABI of the routed linear layer (tokens take their adapters from a pool): argument validation,
+// workspace layout and the order of the launches. Every check runs before any launch.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "backward.hpp"
+#include "checks.hpp"
+#include "lora_mi355x.h"
+#include "routed.hpp"
+
+namespace {
+
+using lora::aligned;
+using lora::Elt;
+using lora::kMaxRowBytes;
+using lora::LinearProblem;
+using lora::overlaps;
+using lora::round_up;
+using lora::Span;
+using lora::span2d;
+
+struct Take {  // regions of a workspace, each 256-byte aligned
+  size_t off = 0;
+  size_t operator()(size_t n) {
+    const size_t o = off;
+    off = round_up(off + n);
+    return o;
+  }
+};
+
+struct FwdLayout {
+  size_t t = 0, eid = 0, blk = 0, total = 0;
+};
+
+FwdLayout fwd_layout(int64_t T, int64_t rp) {
+  FwdLayout L;
+  Take take;
+  L.t = take(static_cast<size_t>(T) * rp * 2);
+  L.eid = take(static_cast<size_t>(T) * 4);
+  L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
+  L.total = take.off;
+  return L;
+}
+
+struct BwdLayout {
+  size_t wt = 0, bt = 0, at = 0, u = 0, ulo = 0, t = 0, tlo = 0, eid = 0, blk = 0, perm = 0, off = 0, items = 0,
+         part = 0, total = 0;
+  int32_t chunk = 0;
+  int64_t n_items = 0;
+};
+
+BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool want_dx) {
+  BwdLayout L;
+  Take take;
+  const int64_t rp = lora::rank_pad(R);
+  if (want_dx) {
+    L.wt = take(static_cast<size_t>(K) * N * 2);
+    L.at = take(static_cast<size_t>(n) * K * R * 2);
+  }
+  L.bt = take(static_cast<size_t>(n) * N * R * 2);
+  const size_t tb = static_cast<size_t>(T) * rp * 2;
+  L.u = take(tb);
+  L.ulo = take(tb);
+  L.t = take(tb);
+  L.tlo = take(tb);
+  L.eid = take(static_cast<size_t>(T) * 4);
+  L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
+  L.perm = take(static_cast<size_t>(T) * 4);
+  L.off = take(static_cast<size_t>(n + 1) * 4);
+  const int64_t wide = std::max(K, N);
+  L.chunk = lora::route_chunk(T, (wide + lora::kRtI - 1) / lora::kRtI * ((R + lora::kRtJ - 1) / lora::kRtJ));
+  L.n_items = lora::route_items(T, n, L.chunk);
+  L.items = take(static_cast<size_t>(L.n_items) * sizeof(lora::RouteItem));
+  L.part = take(static_cast<size_t>(lora::route_parts(T, L.chunk)) * wide * R * 4);
+  L.total = take.off;
+  return L;
+}
+
+constexpr int64_t kMaxTokens = int64_t(1) << 31;
+
+// Checks of the pool and the routing that both directions share.
+int check_pool(const lora_pool* pool, const int32_t* token_adapter, const float* token_scale, int64_t T, int64_t K,
+               int64_t N) {
+  if (pool == nullptr) return LORA_ERR_NULL_PTR;
+  if (pool->n_adapters < 0 || pool->rank < 1 || pool->reserved != 0) return LORA_ERR_SHAPE;
+  if (pool->n_adapters > LORA_MAX_POOL || pool->rank > LORA_MAX_RANK || T >= kMaxTokens || K * 4 > kMaxRowBytes ||
+      N * 4 > kMaxRowBytes)
+    return LORA_ERR_UNSUPPORTED;
+  if (pool->n_adapters > 0) {
+    if (pool->A == nullptr || pool->B == nullptr || pool->scales == nullptr) return LORA_ERR_NULL_PTR;
+    if (T > 0 && token_adapter == nullptr) return LORA_ERR_NULL_PTR;
+  }
+  if (pool->rank % 8 != 0 || !aligned(pool->A, 16) || !aligned(pool->B, 16) || !aligned(pool->scales, 4) ||
+      !aligned(pool->ranks, 4) || !aligned(token_adapter, 4) || !aligned(token_scale, 4))
+    return LORA_ERR_ALIGN;
+  return LORA_OK;
+}
+
+lora::Routing routing(const lora_pool* pool, const int32_t* token_adapter, const float* token_scale) {
+  lora::Routing rt;
+  rt.token_adapter = token_adapter;
+  rt.token_scale = token_scale;
+  rt.scales = pool->scales;
+  rt.ranks = pool->ranks;
+  rt.n_adapters = pool->n_adapters;
+  rt.rank = pool->rank;
+  return rt;
+}
+
+// Everything a routed call reads that depends on the pool and the routing.
+void pool_spans(const lora_pool* pool, const int32_t* token_adapter, const float* token_scale, int64_t T, int64_t K,
+                int64_t N, Span (&s)[6]) {
+  const int64_t n = pool->n_adapters, R = pool->rank;
+  s[0] = span2d(pool->A, 1, n * R * K, n * R * K, 2);
+  s[1] = span2d(pool->B, 1, n * R * N, n * R * N, 2);
+  s[2] = span2d(pool->scales, 1, n, n, 4);
+  s[3] = span2d(pool->ranks, 1, n, n, 4);
+  s[4] = n > 0 ? span2d(token_adapter, 1, T, T, 4) : Span{};
+  s[5] = n > 0 ? span2d(token_scale, 1, T, T, 4) : Span{};
+}
+
+LinearProblem gemm_problem(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                           const void* bias, void* y, int64_t ldy, const uint16_t* t, const void* B,
+                           const int32_t* eid, const int32_t* blk, const lora_pool* pool) {
+  LinearProblem p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x; p.ldx = ldx; p.W = W; p.bias = bias; p.y = y; p.ldy = ldy; p.T = T; p.N = N; p.K = K;
+  p.act = Elt::BF16; p.adapter = Elt::BF16;
+  p.work = const_cast<uint16_t*>(t); p.ldt = lora::rank_pad(pool->rank);
+  p.routed = true;
+  p.rt.B = B; p.rt.eid = eid; p.rt.blk = blk; p.rt.ranks = pool->ranks; p.rt.rank = pool->rank;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                           const void* bias, const lora_pool* pool, const int32_t* token_adapter,
+                           const float* token_scale, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (T < 0 || K < 1 || N < 1 || ldx < K || ldy < N) return LORA_ERR_SHAPE;
+  if (ldx * 2 > kMaxRowBytes || ldy * 2 > kMaxRowBytes) return LORA_ERR_UNSUPPORTED;
+  if (W == nullptr || (T > 0 && (x == nullptr || y == nullptr))) return LORA_ERR_NULL_PTR;
+  int st = check_pool(pool, token_adapter, token_scale, T, K, N);
+  if (st != LORA_OK) return st;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(y, 2) || !aligned(bias, 2) || !aligned(workspace, 16) ||
+      K % 8 != 0 || ldx % 8 != 0)
+    return LORA_ERR_ALIGN;
+  if (T == 0) return LORA_OK;
+  const FwdLayout L = fwd_layout(T, lora::rank_pad(pool->rank));
+  if (workspace == nullptr || workspace_bytes < L.total) return LORA_ERR_WORKSPACE;
+  Span in[6];
+  pool_spans(pool, token_adapter, token_scale, T, K, N, in);
+  const Span sy = span2d(y, T, ldy, N, 2);
+  const Span sw{reinterpret_cast<uintptr_t>(workspace), reinterpret_cast<uintptr_t>(workspace) + L.total};
+  const Span base[3] = {span2d(x, T, ldx, K, 2), span2d(W, N, K, K, 2), span2d(bias, 1, N, N, 2)};
+  if (overlaps(sy, sw)) return LORA_ERR_OVERLAP;
+  for (const Span& s : base)
+    if (overlaps(sy, s) || overlaps(sw, s)) return LORA_ERR_OVERLAP;
+  for (const Span& s : in)
+    if (overlaps(sy, s) || overlaps(sw, s)) return LORA_ERR_OVERLAP;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  lora::RoutedDown d;
+  std::memset(&d, 0, sizeof(d));
+  d.x = static_cast<const uint16_t*>(x); d.ldx = ldx; d.T = T; d.K = K;
+  d.A = static_cast<const uint16_t*>(pool->A);
+  d.rt = routing(pool, token_adapter, token_scale);
+  d.hi = reinterpret_cast<uint16_t*>(ws + L.t); d.ldt = lora::rank_pad(pool->rank);
+  d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
+  d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
+  if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
+  const LinearProblem p = gemm_problem(x, T, K, ldx, W, N, bias, y, ldy, d.hi, pool->B, d.eid, d.blk, pool);
+  return lora::launch_routed_gemm(p, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank) {
+  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1) return 0;
+  return fwd_layout(T, lora::rank_pad(rank)).total;
+}
+
+int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                           const lora_pool* pool, const int32_t* token_adapter, const float* token_scale,
+                           const void* dy, int64_t lddy, void* dx, int64_t lddx, float* dA, float* dB,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || K < 1 || N < 1 || ldx < K || lddy < N || (dx != nullptr && lddx < K)) return LORA_ERR_SHAPE;
+  if (ldx * 2 > kMaxRowBytes || lddy * 2 > kMaxRowBytes || (dx != nullptr && lddx * 2 > kMaxRowBytes))
+    return LORA_ERR_UNSUPPORTED;
+  if ((dx != nullptr && W == nullptr) || (T > 0 && (x == nullptr || dy == nullptr))) return LORA_ERR_NULL_PTR;
+  int st = check_pool(pool, token_adapter, token_scale, T, K, N);
+  if (st != LORA_OK) return st;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(dy, 16) || !aligned(dx, 2) || !aligned(dA, 4) ||
+      !aligned(dB, 4) || !aligned(workspace, 16) || K % 8 != 0 || N % 8 != 0 || ldx % 8 != 0 || lddy % 8 != 0)
+    return LORA_ERR_ALIGN;
+  const int64_t n = pool->n_adapters, R = pool->rank;
+  const BwdLayout L = T > 0 ? bwd_layout(T, K, N, n, R, dx != nullptr) : BwdLayout{};
+  if (L.n_items > 65535) return LORA_ERR_UNSUPPORTED;
+  if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
+  Span in[6];
+  pool_spans(pool, token_adapter, token_scale, T, K, N, in);
+  const Span sw = L.total ? Span{reinterpret_cast<uintptr_t>(workspace),
+                                 reinterpret_cast<uintptr_t>(workspace) + L.total} : Span{};
+  const Span outs[4] = {span2d(dx, T, lddx, K, 2), span2d(dA, 1, n * R * K, n * R * K, 4),
+                        span2d(dB, 1, n * R * N, n * R * N, 4), sw};
+  const Span base[3] = {span2d(x, T, ldx, K, 2), span2d(W, N, K, K, 2), span2d(dy, T, lddy, N, 2)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& s : base)
+      if (overlaps(outs[i], s)) return LORA_ERR_OVERLAP;
+    for (const Span& s : in)
+      if (overlaps(outs[i], s)) return LORA_ERR_OVERLAP;
+    for (int j = i + 1; j < 4; ++j)
+      if (overlaps(outs[i], outs[j])) return LORA_ERR_OVERLAP;
+  }
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool grads = n > 0 && (dA != nullptr || dB != nullptr);
+  if (T == 0) {  // an empty batch: zero gradients
+    hipError_t e = hipSuccess;
+    if (dA != nullptr) e = lora::zero_fill(dA, n * R * K, s);
+    if (e == hipSuccess && dB != nullptr) e = lora::zero_fill(dB, n * R * N, s);
+    return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+  }
+  if (dx == nullptr && !grads) return LORA_OK;
+  char* ws = static_cast<char*>(workspace);
+  auto at16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
+  auto at32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+  const int64_t rp = lora::rank_pad(R);
+  hipError_t e = hipSuccess;
+  // the forward's operand layouts for the input dy: B^T [R, N] and A^T [K, R] of every slot, W^T [K, N]
+  if (n > 0) e = lora::transpose_slots(static_cast<const uint16_t*>(pool->B), static_cast<int>(n), N, R, at16(L.bt), s);
+  if (e == hipSuccess && dx != nullptr) {
+    if (n > 0) e = lora::transpose_slots(static_cast<const uint16_t*>(pool->A), static_cast<int>(n), R, K, at16(L.at), s);
+    if (e == hipSuccess) e = lora::transpose_slots(static_cast<const uint16_t*>(W), 1, N, K, at16(L.wt), s);
+  }
+  if (e != hipSuccess) return LORA_ERR_HIP;
+  lora::RoutedDown d;
+  std::memset(&d, 0, sizeof(d));
+  d.x = static_cast<const uint16_t*>(dy); d.ldx = lddy; d.T = T; d.K = N;
+  d.A = at16(L.bt);
+  d.rt = routing(pool, token_adapter, token_scale);
+  d.hi = at16(L.u); d.lo = at16(L.ulo); d.ldt = rp;
+  d.eid = at32(L.eid); d.blk = at32(L.blk);
+  if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
+  if (dx != nullptr) {
+    const LinearProblem p =
+        gemm_problem(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, d.hi, at16(L.at), d.eid, d.blk, pool);
+    if (lora::launch_routed_gemm(p, s) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (!grads) return LORA_OK;
+  lora::RoutePlan plan{d.eid, T, static_cast<int32_t>(n), L.chunk, at32(L.perm), at32(L.off),
+                       reinterpret_cast<lora::RouteItem*>(ws + L.items), L.n_items};
+  if (lora::launch_route_plan(plan, s) != hipSuccess) return LORA_ERR_HIP;
+  lora::RoutedContract c;
+  c.ldt = rp; c.rank = static_cast<int32_t>(R); c.plan = &plan;
+  c.part = reinterpret_cast<float*>(ws + L.part);
+  if (dB != nullptr) {
+    d.x = static_cast<const uint16_t*>(x); d.ldx = ldx; d.K = K;
+    d.A = static_cast<const uint16_t*>(pool->A);
+    d.hi = at16(L.t); d.lo = at16(L.tlo);
+    if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
+    c.P = static_cast<const uint16_t*>(dy); c.ldp = lddy; c.M = N;
+    c.hi = d.hi; c.lo = d.lo; c.out = dB; c.transpose = false;
+    if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (dA != nullptr) {
+    c.P = static_cast<const uint16_t*>(x); c.ldp = ldx; c.M = K;
+    c.hi = at16(L.u); c.lo = at16(L.ulo); c.out = dA; c.transpose = true;
+    if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
+  }
+  return LORA_OK;
+}
+
+size_t lora_linear_routed_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank,
+                                             int32_t want_dx) {
+  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1) return 0;
+  return bwd_layout(T, K, N, n_adapters, rank, want_dx != 0).total;
+}
+
+}  // extern "C"
