@@ -181,11 +181,12 @@ def _prepare_adamw(c, g, normal):
         def block_views(t):
             return None if t is None else [t[s // BLOCK:s // BLOCK + -(-k // BLOCK)] for s, k in zip(starts, sizes)]
 
-        st["opt"] = rg.LoraAdamW(views(st["param"]), master=views(st["master"]), state_bits=c["bits"], lr=st["lr"],
-                                 betas=(st["beta1"], st["beta2"]), eps=st["eps"], weight_decay=st["wd"],
+        # the optimizer over the tensors and the buffers that the backward calls leave their gradients in
+        st["opt"] = rg.LoraAdamW(views(st["param"]), views(st["grad"]), master=views(st["master"]),
+                                 state_bits=c["bits"], lr=st["lr"], betas=(st["beta1"], st["beta2"]), eps=st["eps"],
+                                 weight_decay=st["wd"],
                                  state=dict(m=views(st["m"]), v=views(st["v"]), m_scale=block_views(st.get("m_scale")),
                                             v_scale=block_views(st.get("v_scale")), step=st["step"]))
-        st["grads"] = views(st["grad"])
     return st
 
 
@@ -280,7 +281,7 @@ def run(state):
     if st["op"] == "adamw":
         st["step"] += 1
         if own:
-            st["opt"].step(st["grads"])
+            st["opt"].step()
         else:
             _plain_adamw(st)
         return _adamw_outputs(st)
