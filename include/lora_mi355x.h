@@ -488,6 +488,70 @@ size_t lora_linear_routed_bwd_workspace_size(int64_t T, int64_t K, int64_t N, in
                                              int32_t want_dx);
 
 /*
+ * lora_adamw -- one AdamW step over all of a model's adapter tensors at once
+ * (Unsloth fast-LoRA chapter, section 4: the gradients dA and dB are what the
+ * optimizer of a LoRA fine-tune steps on), the moments in 32 bits or in 8:
+ *
+ *     g = grad_scale . grad
+ *     m <- beta1 . m + g . (1 - beta1),   v <- beta2 . v + (g . g) . (1 - beta2)
+ *     p <- p . (1 - lr . weight_decay) - (m / (sqrt(v) / sqrt(1 - beta2^step) + eps)) . lr / (1 - beta1^step)
+ *
+ * each operation in fp32, rounded once, in the order written (a division by a
+ * constant is a product with its reciprocal, each constant formed in fp64 and
+ * rounded once).
+ */
+typedef struct lora_adamw_tensor {
+  void* param;       /* [n] param dtype                                                            */
+  float* master;     /* [n] fp32 values of a bf16 param, or NULL. Given, the step reads and writes */
+                     /* these, and param becomes their rounded copy (not read)                     */
+  const void* grad;  /* [n] gradient dtype                                                         */
+  void* m;           /* first moment: [n] fp32, or e4m3 codes (uint8)                              */
+  void* v;           /* second moment: [n] fp32, or e4m3 codes of its square root                  */
+  float* m_scale;    /* 8-bit: [ceil(n / 256)], else NULL                                          */
+  float* v_scale;    /* 8-bit: [ceil(n / 256)], else NULL                                          */
+  int64_t n;         /* elements; 0 is a valid empty tensor                                        */
+} lora_adamw_tensor;
+
+/* Filled by lora_adamw_plan on the host; pass it on unchanged. */
+typedef struct lora_adamw_plan_t {
+  void* table;
+  int64_t n_blocks;
+  int32_t n_tensors, chunk, param_dtype, grad_dtype, state_bits, reserved;
+} lora_adamw_plan_t;
+
+/*
+ * lora_adamw_plan -- checks the tensors (HOST array) and writes what a step
+ * needs of them to `table`, device memory of lora_adamw_table_size() bytes
+ * that the caller keeps, 16-byte aligned, together with the tensors' buffers
+ * (gradient buffers included: each step reads what they hold then) for as
+ * long as it steps with this plan. One set of dtypes per plan; parameters
+ * with settings of their own take a plan of their own.
+ *   param_dtype, grad_dtype  LORA_F32 or LORA_BF16
+ *   state_bits  32, or 8: a stored code c of a block of 256 elements means
+ *               c . scale (m) and (c . scale)^2 (v). A step writes scale =
+ *               largest magnitude / 448 and RN_e4m3(x . (448 / largest)), a
+ *               positive root at least as the smallest e4m3; a block whose
+ *               values are all below 2^-100 holds zeros. Zeros are a valid start
+ * Nothing written may overlap anything else (LORA_ERR_OVERLAP); natural
+ * alignment suffices (16-byte aligned buffers are faster).
+ */
+size_t lora_adamw_table_size(const lora_adamw_tensor* tensors, int32_t n_tensors);
+int lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n_tensors, int32_t param_dtype, int32_t grad_dtype,
+                    int32_t state_bits, void* table, size_t table_bytes, lora_adamw_plan_t* plan, void* stream);
+
+/*
+ * lora_adamw_step -- the step, one launch.
+ *   step     1 for the first step
+ *   lr_step  NULL, or DEVICE {lr, step} (two doubles, 8-byte aligned), read by the kernel in place of lr
+ *            and step, so that a captured step follows a schedule
+ *   beta1, beta2 in [0, 1), eps, weight_decay, lr >= 0, step >= 1: else LORA_ERR_UNSUPPORTED;
+ *   LORA_ERR_NONFINITE for a NaN or infinite one
+ * A gradient that is not finite makes its element's state so, and with 8-bit moments its block's.
+ */
+int lora_adamw_step(const lora_adamw_plan_t* plan, double lr, double beta1, double beta2, double eps,
+                    double weight_decay, int64_t step, const double* lr_step, double grad_scale, void* stream);
+
+/*
  * Workspace bytes a call with T tokens, K inputs and N outputs needs for
  * adapters of the given ranks (`ranks` is a HOST array of n_ranks entries: one
  * for lora_linear_fwd and lora_linear_nf4_fwd, one per group for

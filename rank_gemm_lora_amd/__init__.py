@@ -35,6 +35,7 @@ __all__ = [
     "LoraGroup", "hip_runtimes_mapped",
     "LoraPool", "lora_linear_routed_fwd", "lora_linear_routed_workspace_size", "lora_linear_routed_bwd",
     "lora_linear_routed_bwd_workspace_size", "lora_linear_routed", "lora_linear_routed_backward",
+    "LoraAdamWTensor", "LoraAdamWPlan", "lora_adamw_table_size", "lora_adamw_plan", "lora_adamw_step", "LoraAdamW",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora_mi355x.so")
@@ -71,6 +72,18 @@ class LoraPool(ctypes.Structure):
     """C ``lora_pool``: the adapters from which the tokens of a routed call take theirs."""
     _fields_ = [("A", _p), ("B", _p), ("scales", _p), ("ranks", _p), ("n_adapters", _i32), ("rank", _i32),
                 ("reserved", _i64)]
+
+
+class LoraAdamWTensor(ctypes.Structure):
+    """C ``lora_adamw_tensor``: one tensor of an AdamW step."""
+    _fields_ = [("param", _p), ("master", _p), ("grad", _p), ("m", _p), ("v", _p), ("m_scale", _p), ("v_scale", _p),
+                ("n", _i64)]
+
+
+class LoraAdamWPlan(ctypes.Structure):
+    """C ``lora_adamw_plan_t``, filled by ``lora_adamw_plan``."""
+    _fields_ = [("table", _p), ("n_blocks", _i64), ("n_tensors", _i32), ("chunk", _i32), ("param_dtype", _i32),
+                ("grad_dtype", _i32), ("state_bits", _i32), ("reserved", _i32)]
 
 
 _lib.lora_linear_fwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _i32, _i32, _f64, _f64, _f64,
@@ -119,6 +132,13 @@ _lib.lora_linear_routed_bwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, ctypes.P
 _lib.lora_linear_routed_bwd.restype = ctypes.c_int
 _lib.lora_linear_routed_bwd_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
 _lib.lora_linear_routed_bwd_workspace_size.restype = _sz
+_lib.lora_adamw_table_size.argtypes = [ctypes.POINTER(LoraAdamWTensor), _i32]
+_lib.lora_adamw_table_size.restype = _sz
+_lib.lora_adamw_plan.argtypes = [ctypes.POINTER(LoraAdamWTensor), _i32, _i32, _i32, _i32, _p, _sz,
+                                 ctypes.POINTER(LoraAdamWPlan), _p]
+_lib.lora_adamw_plan.restype = ctypes.c_int
+_lib.lora_adamw_step.argtypes = [ctypes.POINTER(LoraAdamWPlan), _f64, _f64, _f64, _f64, _f64, _i64, _p, _f64, _p]
+_lib.lora_adamw_step.restype = ctypes.c_int
 _lib.lora_merge_apply.argtypes = [_p, _i32, _i64, _i64, _p, _p, _i32, _i32, _f64, _f64, _i32, _p]
 _lib.lora_merge_apply.restype = ctypes.c_int
 _lib.lora_linear_nf4_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
@@ -210,6 +230,23 @@ def lora_linear_routed_bwd(x, T, K, ldx, W, N, pool, token_adapter, token_scale,
 
 def lora_linear_routed_bwd_workspace_size(T, K, N, n_adapters, rank, want_dx=True) -> int:
     return int(_lib.lora_linear_routed_bwd_workspace_size(T, K, N, n_adapters, rank, 1 if want_dx else 0))
+
+
+def lora_adamw_table_size(tensors) -> int:
+    arr = (LoraAdamWTensor * max(1, len(tensors)))(*tensors)
+    return int(_lib.lora_adamw_table_size(arr, len(tensors)))
+
+
+def lora_adamw_plan(tensors, param_dtype, grad_dtype, state_bits, table, table_bytes, stream) -> LoraAdamWPlan:
+    arr, plan = (LoraAdamWTensor * max(1, len(tensors)))(*tensors), LoraAdamWPlan()
+    _check(_lib.lora_adamw_plan(arr, len(tensors), param_dtype, grad_dtype, state_bits, table, table_bytes,
+                                ctypes.byref(plan), stream), "lora_adamw_plan")
+    return plan
+
+
+def lora_adamw_step(plan, lr, beta1, beta2, eps, weight_decay, step, lr_step, grad_scale, stream):
+    return _check(_lib.lora_adamw_step(ctypes.byref(plan), lr, beta1, beta2, eps, weight_decay, step, lr_step,
+                                       grad_scale, stream), "lora_adamw_step")
 
 
 def lora_merge_apply(W, w_dtype, N, K, A, B, rank, adapter_dtype, alpha, strength, quality, stream):
@@ -535,6 +572,82 @@ def lora_linear_routed_backward(x, W, A, B, dy, scales, token_adapter, token_sca
                                _ptr(token_scale), dy.data_ptr(), lddy, _ptr(dx), lddx, _ptr(dA), _ptr(dB),
                                ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev, stream))
     return dx, dA, dB
+
+
+class LoraAdamW:
+    """AdamW over many tensors, one launch per step (see lora_adamw_step).
+
+    ``params``: list of tensors of one dtype (bf16 or fp32), stepped in place; ``grads``: their gradient
+    buffers (fp32 or bf16, the same shapes), read at every step: the backward calls write into them
+    (``lora_linear_routed_backward(..., dA=, dB=)``). ``master``: True for fp32 masters of bf16 parameters
+    (made from them), a list of tensors, or None. ``state_bits``: 32, or 8 for e4m3 moments with an fp32
+    scale per 256 elements. ``state``: a dict as ``state()`` returns it, taken over (not copied); None
+    starts at zero. ``lr_step``: optional fp64 device tensor {lr, step} that the kernel reads in place of
+    ``lr`` and the step count, for captured steps. lr, betas, eps and weight_decay may be changed between
+    steps. The optimizer keeps the tensors; their buffers must stay where they are."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, master=None,
+                 state_bits=32, state=None, lr_step=None, stream=None):
+        params, grads = list(params), list(grads)
+        if not params or len(grads) != len(params):
+            raise ValueError("LoraAdamW needs parameters and one gradient buffer for each")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        dev = params[0].device
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits, self.device = state_bits, dev
+        self.lr_step = _of(lr_step, "lr_step", (2,), torch.float64, dev)
+        if master is True:
+            master = [p.float() for p in params]
+        state = {} if state is None else state
+        mdt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        flat = lambda p: (p.numel(),)  # noqa: E731
+        blocks = lambda p: (-(-p.numel() // 256),)  # noqa: E731
+
+        def lists(name, dtype, shape):
+            ts = state.get(name)
+            if ts is None:
+                ts = [torch.zeros(shape(p), dtype=dtype, device=dev) for p in params]
+            if len(ts) != len(params):
+                raise ValueError(f"{name} must hold one tensor per parameter")
+            return [_of(t.view(-1), f"{name}[{i}]", shape(p), dtype, dev) for i, (t, p) in enumerate(zip(ts, params))]
+
+        self.m, self.v = lists("m", mdt, flat), lists("v", mdt, flat)
+        self.m_scale = self.v_scale = None
+        if state_bits == 8:
+            self.m_scale, self.v_scale = lists("m_scale", torch.float32, blocks), lists("v_scale", torch.float32, blocks)
+        self.step_count = int(state.get("step", 0))
+        for i, (p, g) in enumerate(zip(params, grads)):
+            _of(p, f"params[{i}]", p.shape, params[0].dtype, dev)
+            _of(g, f"grads[{i}]", p.shape, grads[0].dtype, dev)
+        if master is not None:
+            if len(master) != len(params):
+                raise ValueError("master must hold one tensor per parameter")
+            for i, (p, t) in enumerate(zip(params, master)):
+                _of(t, f"master[{i}]", p.shape, torch.float32, dev)
+        self.params, self.grads, self.master = params, grads, master
+        none = [None] * len(params)
+        ts = [LoraAdamWTensor(_ptr(p), _ptr(w), _ptr(g), _ptr(m), _ptr(v), _ptr(ms), _ptr(vs), p.numel())
+              for p, w, g, m, v, ms, vs in zip(params, master or none, grads, self.m, self.v, self.m_scale or none,
+                                               self.v_scale or none)]
+        need = lora_adamw_table_size(ts)
+        with torch.cuda.device(dev):
+            self._table = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            self._plan = lora_adamw_plan(ts, _dt(params[0]), _dt(grads[0]), state_bits, self._table.data_ptr(),
+                                         self._table.numel(), _stream_on(dev, stream))
+
+    def step(self, grad_scale=1.0, stream=None):
+        """One step on the gradients that the buffers hold (on the stream that runs it)."""
+        count = self.step_count + 1
+        with torch.cuda.device(self.device):
+            lora_adamw_step(self._plan, float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps),
+                            float(self.weight_decay), count, _ptr(self.lr_step), float(grad_scale),
+                            _stream_on(self.device, stream))
+        self.step_count = count
+
+    def state(self):
+        """The moments (the tensors themselves) and the step count, as ``state=`` takes them."""
+        return dict(m=self.m, v=self.v, m_scale=self.m_scale, v_scale=self.v_scale, step=self.step_count)
 
 
 def dense_patch(dst, src, strength, mode="add", stream=None):

@@ -3,7 +3,7 @@
     python rank_gemm_lora_amd/_build.py [-v]
 
 Every kernel is compiled for gfx950 only. Files whose arithmetic must follow
-an exact rounding sequence (the exact tier, the dense patch) are compiled with
+an exact rounding sequence (the exact tier, the dense patch, the AdamW step) are compiled with
 floating-point contraction off. All HIP code is built without packed-fp32
 instructions (the compiler then never emits v_pk_{add,mul,fma}_f32).
 """
@@ -36,6 +36,8 @@ SOURCES = {
     "noalloc.hip": [],
     "routed.hip": [],
     "routed_api.cpp": [],
+    "adamw.hip": ["-ffp-contract=off"],
+    "adamw_api.cpp": [],
     "api.cpp": [],
 }
 
