@@ -472,8 +472,7 @@ size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_
  *   optional (NULL = not computed; W may be NULL without dx)
  * Every element of the outputs is written: an adapter without tokens gets zeros, and so do the rows of
  * dA and columns of dB from the adapter's rank on. dA and dB sum in fp32 over the adapter's tokens in
- * order, u_t and s_t x A^T taken as a bf16 pair hi + lo (about 16 bits; one bf16 would leave the fp32
- * gradients 8). An adapter's gradients depend on its own tokens only.
+ * order, u_t and s_t x A^T taken in fp32 (as three bf16 terms). An adapter's gradients depend on its own tokens only.
  *   workspace  at least lora_linear_routed_bwd_workspace_size(..., dx != NULL) bytes
  * T == 0 writes zero gradients. LORA_ERR_UNSUPPORTED above about 65000 adapters and 4096-token chunks
  * together.

@@ -29,6 +29,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "routed_dev.hpp"
 
 namespace lora {
 namespace {
@@ -1244,10 +1245,6 @@ __device__ __forceinline__ void ext_stage_loads(const ExtPlan& g, int e, const T
   ob.load(wdst, br, e * P::RB, (e + 1) * P::RB > g.rkb, g.rkb);
 }
 
-__device__ __forceinline__ int routed_rank(const RoutedGemm& rt, int a) {
-  return rt.ranks != nullptr ? __builtin_amdgcn_readfirstlane((min(rt.ranks[a], rt.rank) + 7) & ~7) : rt.rank;
-}
-
 // Routed: how this tile's adapters are met. All of its tokens with one adapter: its K-extension plan
 // (the pool slot's rows n0 .., its rank padded to 64-k stages), false. No adapter at all: no plan,
 // false. Otherwise true: the updates are added after the loop.
@@ -1260,7 +1257,7 @@ __device__ __forceinline__ bool routed_plan(const LinearProblem& p, int64_t m0, 
   const int a = __builtin_amdgcn_readfirstlane(f);
   if (__builtin_amdgcn_ballot_w64(f != a) != 0 || a == -2) return true;
   if (a < 0) return false;
-  const int rank = routed_rank(p.rt, a);
+  const int rank = route_rank(p.rt.ranks, p.rt.rank, a);
   e.B = static_cast<const char*>(p.rt.B) + static_cast<int64_t>(a) * p.N * p.rt.rank * 2;
   e.tcb = 0;
   e.ns = (rank * 2 + P::RB - 1) / P::RB;
@@ -1309,7 +1306,7 @@ __device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const L
     a = __builtin_amdgcn_readfirstlane(a);
     if (a == 0x7fffffff) break;
     prev = a;
-    const int rank = routed_rank(p.rt, a);
+    const int rank = route_rank(p.rt.ranks, p.rt.rank, a);
     const __amdgpu_buffer_rsrc_t br =
         make_rsrc(static_cast<const char*>(p.rt.B) + (static_cast<int64_t>(a) * p.N + nw) * ldb,
                   static_cast<uint32_t>(rows_n) * ldb);
@@ -1322,6 +1319,17 @@ __device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const L
           const int k = c0 + 32 * h + 8 * q;
           const uint32_t off = k < rank ? static_cast<uint32_t>(i * 16 + r) * ldb + k * 2 : 0x80000000u;
           w[i][h] = __builtin_amdgcn_raw_buffer_load_b128(br, off, 0, 0);
+        }
+      // (all t~ loads before the first wait, other tokens' out of range: one after the other they cost the
+      // block a memory latency per 16 tokens)
+      bf16x8 t[P::NJ][2];
+#pragma unroll
+      for (int j = 0; j < P::NJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = c0 + 32 * h + 8 * q;
+          const uint32_t off = id[j] == a && k < rank ? static_cast<uint32_t>(j * 16 + r) * ldt_b + k * 2 : 0x80000000u;
+          t[j][h] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(tr, off, 0, 0));
         }
       u16x2 top = {0, 0};
 #pragma unroll
@@ -1338,27 +1346,16 @@ __device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const L
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((w[i][h][e] & 0x7f80u) == 0x7f80u) w[i][h][e] &= 0xffff0000u;
-              if ((w[i][h][e] & 0x7f800000u) == 0x7f800000u) w[i][h][e] &= 0xffffu;
-            }
+            for (int e = 0; e < 4; ++e) w[i][h][e] = finite_pair(w[i][h][e]);
       }
 #pragma unroll
       for (int j = 0; j < P::NJ; ++j) {
-        const bool mine = id[j] == a;
-        if (__builtin_amdgcn_ballot_w64(mine) == 0) continue;
-        bf16x8 t[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = c0 + 32 * h + 8 * q;
-          const uint32_t off = mine && k < rank ? static_cast<uint32_t>(j * 16 + r) * ldt_b + k * 2 : 0x80000000u;
-          t[h] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(tr, off, 0, 0));
-        }
+        if (__builtin_amdgcn_ballot_w64(id[j] == a) == 0) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < P::NI; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][h]), t[h], acc[i][j],
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][h]), t[j][h], acc[i][j],
                                                                 0, 0, 0);
       }
     }
@@ -1377,7 +1374,7 @@ __device__ __forceinline__ void routed_broken(const LinearProblem& p, int64_t mw
     const int64_t m = mw + i;
     const int a = __builtin_amdgcn_readfirstlane(p.rt.eid[m]);
     if (a < 0) continue;
-    const int rank = routed_rank(p.rt, a);
+    const int rank = route_rank(p.rt.ranks, p.rt.rank, a);
     const bf16_bits* t = static_cast<const bf16_bits*>(p.work) + m * p.ldt;
     for (int n = lane; n < rows_n; n += 64) {
       const bf16_bits* b = static_cast<const bf16_bits*>(p.rt.B) + (static_cast<int64_t>(a) * p.N + nw + n) * p.rt.rank;
@@ -2147,6 +2144,85 @@ hipError_t launch(const LinearProblem& p, hipStream_t s) {
   return narrow ? launch_cfg<DP64, false>(p, s) : launch_cfg<DP128, false>(p, s);
 }
 
+// Routed producer, blocks of 128 tokens with few adapters (RingBlock): the same ring over the rows of a
+// pool slot, once per adapter of the block, whose own tokens keep the result. Grid: (blocks, adapter rows,
+// adapter of the block x split).
+template <class DP>
+__global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDown p) {
+  using P = DP;
+  static_assert(P::BM == kRingBlock, "one ring tile per block of tokens");
+  __shared__ __attribute__((aligned(1024))) char smem[P::S * P::STAGE_BYTES];
+  const int nth = blockIdx.z / p.splits, split = blockIdx.z - nth * p.splits;
+  const RingBlock* rb = p.ring + blockIdx.x;
+  if (nth >= __builtin_amdgcn_readfirstlane(rb->n)) return;
+  const int a = __builtin_amdgcn_readfirstlane(rb->id[nth]);  // (in a scalar register: the resources need it there)
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
+  const int rows_m = static_cast<int>(min<int64_t>(P::BM, p.T - m0));
+  const int rank = route_rank(p.rt.ranks, p.rt.rank, a);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
+  const int q0 = blockIdx.y * P::BN;
+  const int rows_q = max(0, min(P::BN, rank - q0));
+  const int kb_total = static_cast<int>(p.K * 2);
+  const int nk = (kb_total + P::RB - 1) / P::RB;
+  const bool k_tail = (kb_total % P::RB) != 0;
+  const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), lda_b = static_cast<uint32_t>(p.K * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+  const __amdgpu_buffer_rsrc_t ar =
+      make_rsrc(p.A + (static_cast<int64_t>(a) * p.rt.rank + q0) * p.K, static_cast<uint32_t>(rows_q) * lda_b);
+  TileOffsets<P, P::BM> ox;
+  TileOffsets<P, P::BN> oa;
+  ox.init(ldx_b, 0, rows_m, 0);
+  oa.init(lda_b, 0, rows_q, 0);
+  const int s_lo = split * p.ks;
+  const int ns = min(nk, s_lo + p.ks) - s_lo;
+  auto issue = [&](int st) {
+    char* bx = smem + (st % P::S) * P::STAGE_BYTES;
+    const bool tail = k_tail && s_lo + st == nk - 1;
+    ox.load(bx, xr, (s_lo + st) * P::RB, tail, kb_total);
+    oa.load(bx + P::X_BYTES, ar, (s_lo + st) * P::RB, tail, kb_total);
+  };
+  f32x16 acc[P::NI][P::NJ];
+  pipe_loop<P>(acc, smem, ns, issue, wn0, wm0, lane);
+
+  const int r = lane & 31, h = lane >> 5;
+  const int64_t m = m0 + wm0 + r;
+  if (m >= p.T || p.eid[m] != a) return;
+  if (p.splits > 1) {
+    float* part = p.tpart + (split * p.T + m) * p.ldt;
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        const int q = q0 + wn0 + i * 32 + gq * 8 + h * 4;
+        if (q >= p.ldt) continue;
+        *reinterpret_cast<f32x4*>(part + q) =
+            f32x4{acc[i][0][gq * 4], acc[i][0][gq * 4 + 1], acc[i][0][gq * 4 + 2], acc[i][0][gq * 4 + 3]};
+      }
+    return;
+  }
+  float s;
+  route(p.rt, m, p.T, s);
+#pragma unroll
+  for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+    for (int gq = 0; gq < 4; ++gq) {
+      const int q = q0 + wn0 + i * 32 + gq * 8 + h * 4;
+      if (q >= p.ldt) continue;
+      const float t[4] = {acc[i][0][gq * 4] * s, acc[i][0][gq * 4 + 1] * s, acc[i][0][gq * 4 + 2] * s,
+                          acc[i][0][gq * 4 + 3] * s};
+      put_rank_wide<4>(p, m * p.ldt + q, t);
+    }
+}
+
+template <class DP>
+hipError_t launch_ring_cfg(const RoutedDown& p, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.T + DP::BM - 1) / DP::BM), static_cast<unsigned>((p.ldt + DP::BN - 1) / DP::BN),
+                  static_cast<unsigned>(p.splits * kRingAdapters));
+  hipLaunchKernelGGL((routed_ring_kernel<DP>), grid, dim3(DP::THREADS), 0, s, p);
+  return hipGetLastError();
+}
+
 // fp32 adapter on bf16 activations: t~ as hi | hi | lo from the split copies of A
 hipError_t launch_split(const LinearProblem& p, hipStream_t s) { return launch_cfg<DP128, true>(p, s); }
 }  // namespace down
@@ -2715,6 +2791,11 @@ __global__ __launch_bounds__(256) void bias32_kernel(LinearProblem p) {
 hipError_t launch_bias32(const LinearProblem& p, hipStream_t s) {
   hipLaunchKernelGGL(bias32_kernel, dim3(static_cast<unsigned>((p.N + 255) / 256)), dim3(256), 0, s, p);
   return hipGetLastError();
+}
+
+hipError_t launch_routed_ring(const RoutedDown& p, hipStream_t s) {
+  return p.ldt <= pipe::down::DP64::BN ? pipe::down::launch_ring_cfg<pipe::down::DP64>(p, s)
+                                       : pipe::down::launch_ring_cfg<pipe::down::DP128>(p, s);
 }
 
 hipError_t launch_routed_gemm(const LinearProblem& p, hipStream_t s) { return pipe::launch(p, s); }

@@ -9,84 +9,175 @@
 #include "routed.hpp"
 
 #include "common.hpp"
+#include "routed_dev.hpp"
 
 namespace lora {
 namespace {
 
 constexpr uint32_t kOutOfRange = 0x80000000u;  // a buffer offset past every range: the load returns zeros
 
-// The adapter of token t and its scale; -1 (the base output) past the last token, for an index outside
-// the pool, a zero scale or a rank of zero.
-__device__ __forceinline__ int route(const Routing& rt, int64_t t, int64_t T, float& s) {
-  s = 0.f;
-  if (t >= T || rt.n_adapters == 0) return -1;
-  const int a = rt.token_adapter[t];
-  if (static_cast<uint32_t>(a) >= static_cast<uint32_t>(rt.n_adapters)) return -1;
-  s = rt.scales[a];
-  if (rt.token_scale != nullptr) s *= rt.token_scale[t];
-  if (s == 0.f || (rt.ranks != nullptr && rt.ranks[a] <= 0)) return -1;
-  return a;
+// ---------------------------------------------------------------------------
+// What a block of 128 tokens takes (RingBlock), eid and blk, before the ring runs.
+__global__ __launch_bounds__(64) void route_blocks_kernel(RoutedDown p) {
+  const int lane = threadIdx.x;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRingBlock;
+  int id[2];
+  uint64_t todo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t m = m0 + 64 * h + lane;
+    float s;
+    id[h] = route(p.rt, m, p.T, s);
+    todo[h] = __builtin_amdgcn_ballot_w64(id[h] >= 0);
+    if (m < p.T) p.eid[m] = id[h];
+    // blk: lanes 16 b .. of the half; the block's first token decides
+    const int first = __shfl(id[h], lane & ~15);
+    const uint64_t differ = __builtin_amdgcn_ballot_w64(m < p.T && id[h] != first);
+    if ((lane & 15) == 0 && m < p.T)
+      p.blk[m / kRouteBlock] = (differ >> lane & 0xffffu) == 0 ? first : -2;
+  }
+  RingBlock b{0, {-1, -1, -1, -1}};
+#pragma unroll
+  for (int k = 0; k < kRingAdapters; ++k) {
+    if (todo[0] == 0 && todo[1] == 0) break;
+    const int a = todo[0] != 0 ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(todo[0]))
+                               : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(todo[1]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) todo[h] &= ~__builtin_amdgcn_ballot_w64(id[h] == a);
+    b.id[k] = a;
+    b.n = k + 1;
+  }
+  if (todo[0] != 0 || todo[1] != 0) b.n = -1;
+  if (lane == 0) p.ring[blockIdx.x] = b;
 }
 
-// ---------------------------------------------------------------------------
-// Rank-wide producer. Workgroup: one block of 16 tokens, 64 ranks, every gridDim.z-th of the block's
-// distinct adapters; 8 waves split K and add their sums through LDS in wave order. Operands go from
-// global memory straight into MFMA fragments (lane (r, q): 8 consecutive k of adapter row r / token r);
-// all 16 tokens are multiplied, and the rows of the adapter's own tokens are kept.
-constexpr int kDownWaves = 8;
+// t of the tokens whose sums are in n parts (the ring's splits, or parts without the ring), added in order and
+// scaled. 32 threads a token and 64 ranks.
+__global__ __launch_bounds__(256) void down_join_kernel(RoutedDown p, int n) {
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (m >= p.T) return;
+  const int64_t at = m * p.ldt + blockIdx.y * 64 + 2 * (threadIdx.x & 31);
+  f32x2 w[8];  // (all parts' loads before their adds; a part past the last reads the last again, unused)
+#pragma unroll
+  for (int z = 0; z < 8; ++z) w[z] = *reinterpret_cast<const f32x2*>(p.tpart + min(z, n - 1) * p.T * p.ldt + at);
+  if (p.eid[m] < 0 || (p.splits > 0 && p.ring[m / kRingBlock].n < 0)) return;
+  float v[2] = {0.f, 0.f}, s;
+#pragma unroll
+  for (int z = 0; z < 8; ++z)
+    if (z < n) {
+      v[0] += w[z][0];
+      v[1] += w[z][1];
+    }
+  route(p.rt, m, p.T, s);
+  v[0] *= s;
+  v[1] *= s;
+  put_rank_wide<2>(p, at, v);
+}
 
-__global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown p) {
-  __shared__ f32x4 red[kDownWaves][4][64];
+// Rank-wide producer without the ring. Workgroup: one block of 16 tokens, 64 ranks, one slot's share of
+// the block's distinct adapters, one part of K; 8 waves split that and add their sums through LDS in wave order. Operands go
+// from global memory straight into MFMA fragments (lane (r, q): 8 consecutive k of adapter row r / token
+// r), the next 128 k (64 above 32 ranks) in flight during the MFMAs of these; all 16 tokens are multiplied, and the rows of the adapter's own tokens are kept. Up to 256 tokens the
+// blocks are of the tokens sorted by adapter (every workgroup sorts them for itself, counting the tokens
+// before each), which leaves a block the fewest adapters. Beside the ring, a workgroup looks through blocks gridDim.x apart for
+// those that the ring left.
+// acc[b] += rows 16 b .. of A times the tokens over [k_lo, k_hi), groups of 32 ST k.
+template <int NRB, int ST>
+__device__ __forceinline__ void down_product(f32x4 (&acc)[4], __amdgpu_buffer_rsrc_t xr, __amdgpu_buffer_rsrc_t ar,
+                                             uint32_t x_off, uint32_t a_off, uint32_t lda_b, int64_t k_lo,
+                                             int64_t k_hi, int q) {
+  struct {
+    u32x4 x[ST], a[ST][NRB];
+  } f[2];
+  auto load = [&](int i, int64_t kg) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st) {
+      const int64_t k = kg + 32 * st + 8 * q;
+      const bool in = k < k_hi;
+      f[i].x[st] =
+          __builtin_amdgcn_raw_buffer_load_b128(xr, in ? x_off + static_cast<uint32_t>(k * 2) : kOutOfRange, 0, 0);
+#pragma unroll
+      for (int b = 0; b < NRB; ++b)
+        f[i].a[st][b] = __builtin_amdgcn_raw_buffer_load_b128(
+            ar, in ? a_off + b * 16 * lda_b + static_cast<uint32_t>(k * 2) : kOutOfRange, 0, 0);
+    }
+  };
+  auto mma = [&](int i) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int b = 0; b < NRB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f[i].a[st][b]),
+                                                         __builtin_bit_cast(bf16x8, f[i].x[st]), acc[b], 0, 0, 0);
+  };
+  // (loads past k_hi read zeros, so both halves run unconditionally)
+  load(0, k_lo);
+  for (int64_t kg = k_lo; kg < k_hi; kg += 64 * ST) {
+    load(1, kg + 32 * ST);
+    mma(0);
+    load(0, kg + 64 * ST);
+    mma(1);
+  }
+}
+
+// Up to 256 tokens: adapter, scale and token of each place of the order by adapter (a token's place is
+// the number of tokens before it; with one block the order does not matter and is the tokens' own).
+struct SortedTokens {
+  int key[kFewMaxT], id[kFewMaxT], token[kFewMaxT];
+  float scale[kFewMaxT];
+};
+// order: the sorted tokens, of which `block` is one (null: blocks are of the tokens as they come).
+__device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f32x4 (&red)[kDownWaves][4][64],
+                                           const SortedTokens* order) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRouteBlock;
+  const int64_t t0 = block * kRouteBlock;
   const int rows = static_cast<int>(min<int64_t>(kRouteBlock, p.T - t0));
+  int64_t token = t0 + r;
   float s;
-  const int id = route(p.rt, t0 + r, p.T, s);
+  int id;
+  if (order != nullptr) {
+    token = r < rows ? order->token[t0 + r] : p.T;
+    id = r < rows ? order->id[t0 + r] : -1;
+    s = r < rows ? order->scale[t0 + r] : 0.f;
+  } else {
+    id = route(p.rt, token, p.T, s);
+  }
   uint32_t todo = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(id >= 0)) & 0xffffu;
-  if (wave == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-    if (q == 0 && r < rows) p.eid[t0 + r] = id;
+  if (p.splits == 0 && wave == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     const int first = __builtin_amdgcn_readfirstlane(id);
+    if (q == 0 && r < rows) p.eid[token] = id;
     const bool same = __builtin_amdgcn_ballot_w64(r < rows && id != first) == 0;
-    if (lane == 0) p.blk[blockIdx.x] = same ? first : -2;
+    if (lane == 0) p.blk[block] = same ? first : -2;
   }
   const int q0 = blockIdx.y * 64;
-  const int64_t kper = ((p.K + kDownWaves - 1) / kDownWaves + 31) / 32 * 32;
-  const int64_t k_lo = wave * kper, k_hi = min<int64_t>(p.K, k_lo + kper);
+  const int slots = static_cast<int>(gridDim.z) / p.parts;
+  const int slot = static_cast<int>(blockIdx.z) % slots, part = static_cast<int>(blockIdx.z) / slots;
+  const int shares = kDownWaves * p.parts;
+  const int64_t kper = ((p.K + shares - 1) / shares + 31) / 32 * 32;
+  const int64_t k_lo = (part * kDownWaves + wave) * kper, k_hi = min<int64_t>(p.K, k_lo + kper);
   const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), lda_b = static_cast<uint32_t>(p.K * 2);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + t0 * p.ldx, static_cast<uint32_t>(rows) * ldx_b);
+  // (sorted: rows of all of x, at most 256 of 4 MB; a place past the last reads zeros)
+  const __amdgpu_buffer_rsrc_t xr = order == nullptr
+                                        ? make_rsrc(p.x + t0 * p.ldx, static_cast<uint32_t>(rows) * ldx_b)
+                                        : make_rsrc(p.x, static_cast<uint32_t>(p.T) * ldx_b);
+  const uint32_t x_off = static_cast<uint32_t>(order == nullptr ? r : token) * ldx_b,
+                 a_off = static_cast<uint32_t>(r) * lda_b;
   int nth = 0;
   while (todo != 0) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
     todo &= ~static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(id == a));
-    if (nth++ % static_cast<int>(gridDim.z) != static_cast<int>(blockIdx.z)) continue;
-    const int rank =
-        p.rt.ranks != nullptr ? __builtin_amdgcn_readfirstlane((min(p.rt.ranks[a], p.rt.rank) + 7) & ~7) : p.rt.rank;
+    if (nth++ % slots != slot) continue;
+    const int rank = route_rank(p.rt.ranks, p.rt.rank, a);
     const int rows_a = max(0, min(64, rank - q0));
-    const int nrb = (rows_a + 15) / 16;
     const __amdgpu_buffer_rsrc_t ar =
         make_rsrc(p.A + (static_cast<int64_t>(a) * p.rt.rank + q0) * p.K, static_cast<uint32_t>(rows_a) * lda_b);
     f32x4 acc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t kg = k_lo; kg < k_hi; kg += 128) {
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        const int64_t k = kg + 32 * st + 8 * q;
-        const bool in = k < k_hi;
-        const bf16x8 xf = __builtin_bit_cast(
-            bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
-                        xr, in ? static_cast<uint32_t>(r) * ldx_b + static_cast<uint32_t>(k * 2) : kOutOfRange, 0, 0));
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (b >= nrb) continue;
-          const uint32_t off = static_cast<uint32_t>(b * 16 + r) * lda_b + static_cast<uint32_t>(k * 2);
-          const bf16x8 af = __builtin_bit_cast(
-              bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ar, in ? off : kOutOfRange, 0, 0));
-          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, xf, acc[b], 0, 0, 0);
-        }
-      }
-    }
+    if (rows_a > 32) down_product<4, 2>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
+    else if (rows_a > 16) down_product<2, 4>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
+    else if (rows_a > 0) down_product<1, 4>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
 #pragma unroll
     for (int b = 0; b < 4; ++b) red[wave][b][lane] = acc[b];
     __syncthreads();
@@ -95,25 +186,352 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown
       f32x4 v = red[0][wave][lane];
 #pragma unroll
       for (int w = 1; w < kDownWaves; ++w) v += red[w][wave][lane];
-      v *= s;
-      uint2 hi;
-      hi.x = pack_bf16x2(v[0], v[1]);
-      hi.y = pack_bf16x2(v[2], v[3]);
-      const int64_t at = (t0 + r) * p.ldt + q0 + wave * 16 + 4 * q;
-      *reinterpret_cast<uint2*>(p.hi + at) = hi;
-      if (p.lo != nullptr) {
-        float l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t h = e < 2 ? hi.x : hi.y;
-          const float hf = __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16);
-          l[e] = __builtin_isfinite(hf) ? v[e] - hf : 0.f;
-        }
-        *reinterpret_cast<uint2*>(p.lo + at) = uint2{pack_bf16x2(l[0], l[1]), pack_bf16x2(l[2], l[3])};
+      const int64_t at = token * p.ldt + q0 + wave * 16 + 4 * q;
+      if (p.parts > 1) {
+        *reinterpret_cast<f32x4*>(p.tpart + part * p.T * p.ldt + at) = v;
+      } else {
+        const float t[4] = {v[0] * s, v[1] * s, v[2] * s, v[3] * s};
+        put_rank_wide<4>(p, at, t);
       }
     }
     __syncthreads();
   }
+}
+
+__device__ __forceinline__ void sort_tokens(const RoutedDown& p, SortedTokens& o) {
+  static_assert(64 * kDownWaves == 2 * kFewMaxT, "two threads a token");
+  const int t = threadIdx.x % kFewMaxT, half = threadIdx.x / kFewMaxT, T = static_cast<int>(p.T);
+  float s;
+  const uint32_t key = static_cast<uint32_t>(route(p.rt, t, p.T, s));  // (-1, no adapter: last)
+  int place = t;
+  if (T > kRouteBlock) {
+    if (half == 0) o.key[t] = static_cast<int>(key);
+    __syncthreads();
+    // this thread's half of the tokens before t (entries past T hold the last key and come after every token)
+    const int mid = (T + 7) / 8 * 4;
+    place = 0;
+#pragma unroll 4
+    for (int u = half * mid; u < (half == 0 ? mid : T); u += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(o.key + u);
+      place += (k.x < key || (k.x == key && u < t)) + (k.y < key || (k.y == key && u + 1 < t)) +
+               (k.z < key || (k.z == key && u + 2 < t)) + (k.w < key || (k.w == key && u + 3 < t));
+    }
+    if (half == 1) o.id[t] = place;
+    __syncthreads();
+    if (half == 0) place += o.id[t];
+    __syncthreads();
+  }
+  if (half == 0 && t < T) {
+    o.id[place] = static_cast<int>(key);
+    o.token[place] = t;
+    o.scale[place] = s;
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown p) {
+  __shared__ f32x4 red[kDownWaves][4][64];
+  if (p.order != nullptr) {
+    __shared__ __attribute__((aligned(16))) SortedTokens sorted;
+    sort_tokens(p, sorted);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && static_cast<int>(threadIdx.x) < p.T)
+      p.order[threadIdx.x] = sorted.token[threadIdx.x], p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
+    down_block(p, blockIdx.x, red, &sorted);
+    return;
+  }
+  if (p.splits == 0) {
+    down_block(p, blockIdx.x, red, nullptr);
+    return;
+  }
+  // blocks blockIdx.x, + gridDim.x, ..: 64 at a time, one per lane (every wave the same)
+  const int64_t n = (p.T + kRouteBlock - 1) / kRouteBlock;
+  for (int64_t base = blockIdx.x; base < n; base += 64 * static_cast<int64_t>(gridDim.x)) {
+    const int64_t mine = base + (threadIdx.x & 63) * static_cast<int64_t>(gridDim.x);
+    uint64_t left = __builtin_amdgcn_ballot_w64(mine < n && p.ring[mine * kRouteBlock / kRingBlock].n < 0);
+    while (left != 0) {
+      const int i = __builtin_ctzll(left);
+      left &= left - 1;
+      down_block(p, base + i * static_cast<int64_t>(gridDim.x), red, nullptr);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: y = RN(x.W^T + t~.B^T + b). Workgroup: 64 outputs x BM tokens, one of S parts of K; 4 waves.
+// Stages of 64 k (128 bytes of every row of x and W) go through a ring of D LDS slots filled by
+// buffer_load .. lds, D - 1 of them in flight; 16-byte chunk c of row r lies at c ^ ((r / 2) % 8), so that a
+// wave's 16-byte reads spread over the banks. (A first form fed the MFMAs straight from memory: 16 rows of
+// 64 bytes an instruction. 64 tokens, 4096 -> 14336, took 60 us that way.)
+// The adapters come first: each adapter of each 16 tokens (a unit) is one wave's, its product over the tile's
+// 64 outputs formed apart and the rows of the adapter's own tokens put into an LDS tile (in ring slots not
+// yet in use) from which the sums start, so nothing of one adapter meets another's tokens. Units are dealt to
+// the waves of all S parts.
+// S > 1: the parts' sums meet in the workspace and few_finish_kernel adds them. (Added by the last of a
+// tile's workgroups to arrive they cost more: the device-scope fences around the arrival count write back
+// and drop an XCD's L2 every time. 1 token, 4096 -> 14336: 98 us against 31 with the second launch.)
+constexpr int kFewN = 64, kFewRow = 128;
+
+template <int BM>
+struct FewCfg {
+  static constexpr int XR = BM < 32 ? 32 : BM;  // staged rows of x (one copy instruction a wave at least)
+  static constexpr int WAVES_M = BM >= 64 ? 2 : 1, WAVES_N = 4 / WAVES_M;
+  static constexpr int TB = BM / WAVES_M / 16, NB = kFewN / WAVES_N / 16;  // 16 x 16 blocks of a wave
+  static constexpr int STAGE = (XR + kFewN) * kFewRow;
+  static constexpr int LPS = (XR + kFewN) / 8 / 4;  // copy instructions of a wave and stage (8 rows each)
+  static constexpr int DELTA_SLOTS = (BM * kFewN * 4 + STAGE - 1) / STAGE;
+};
+
+// Element of the adapters' tile: 4 outputs 4 c .. of token row; the groups of 4 XOR-swizzled by row, so that
+// the 16 tokens of an access spread over the banks.
+__device__ __forceinline__ f32x4* few_delta(char* tile, int row, int c) {
+  return reinterpret_cast<f32x4*>(tile) + row * (kFewN / 4) + (c ^ (row & 15));
+}
+
+// y of a token at 4 outputs of a tile, from nl on: the sums, the bias and one rounding.
+__device__ __forceinline__ void few_store(const RoutedFew& p, f32x4 v, int64_t token, int64_t n0, int rows_n, int nl) {
+  if (nl >= rows_n) return;
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (nl + e < rows_n) v[e] += bf16_to_f32(p.bias[n0 + nl + e]);
+  }
+  uint16_t* y = p.y + token * p.ldy + n0 + nl;
+  const uint2 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  if (reinterpret_cast<uintptr_t>(y) % 8 == 0 && nl + 4 <= rows_n) {
+    *reinterpret_cast<uint2*>(y) = o;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (nl + e < rows_n) y[e] = static_cast<uint16_t>((e < 2 ? o.x : o.y) >> (16 * (e & 1)));
+  }
+}
+
+// The adapters of a tile: units part, part + parts, .. of its list, two in flight at a time, 32 ranks of each
+// at a time. (Code that runs once costs its fetch: eight units at a time, unrolled, took 1-3 us longer on
+// every small call and gained nothing on large ones. 64 tokens of 64 adapters, 4096 -> 14336: 57.7 us against
+// 57.7; 16 of 16: 44.1 against 48.5.)
+__device__ __forceinline__ void few_adapters(const RoutedFew& p, char* delta, const int* ids, const int* tok,
+                                             const int* units, int n_units, int64_t n0, int rows_n, int part, int parts) {
+  constexpr int P = 2;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const uint32_t ldb = static_cast<uint32_t>(p.rt.rank * 2), ldt_b = static_cast<uint32_t>(p.ldt * 2);
+  const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.hi, static_cast<uint32_t>(p.T) * ldt_b);
+  const __amdgpu_buffer_rsrc_t mr = make_rsrc(p.mid, static_cast<uint32_t>(p.T) * ldt_b);
+  for (int u0 = part; u0 < n_units; u0 += P * parts) {
+    int row[P], rank[P], most = 0;
+    bool mine[P];
+    uint32_t trow[P];
+    __amdgpu_buffer_rsrc_t br[P];
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const int at = u0 + u * parts;
+      const bool in = at < n_units;
+      const int unit = __builtin_amdgcn_readfirstlane(units[in ? at : u0]);  // first row, and the rank above bit 8
+      const int first = unit & 255;
+      const int a = __builtin_amdgcn_readfirstlane(ids[first]);
+      row[u] = (first & ~15) + r;
+      mine[u] = in && ids[row[u]] == a;
+      rank[u] = in ? unit >> 8 : 0;
+      most = max(most, rank[u]);
+      trow[u] = static_cast<uint32_t>(tok[row[u]]) * ldt_b;
+      br[u] = make_rsrc(static_cast<const bf16_bits*>(p.rt.B) + (static_cast<int64_t>(a) * p.N + n0) * p.rt.rank,
+                        static_cast<uint32_t>(rows_n) * ldb);
+    }
+    for (int c0 = 0; c0 < most; c0 += 32) {
+      u32x4 w[P][4], t[P][2];
+      const int k = c0 + 8 * q;
+#pragma unroll
+      for (int u = 0; u < P; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[u][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              br[u], k < rank[u] ? static_cast<uint32_t>(16 * i + r) * ldb + k * 2 : kOutOfRange, 0, 0);
+        const uint32_t off = mine[u] && k < rank[u] ? trow[u] + k * 2 : kOutOfRange;
+        t[u][0] = __builtin_amdgcn_raw_buffer_load_b128(hr, off, 0, 0);
+        t[u][1] = __builtin_amdgcn_raw_buffer_load_b128(mr, off, 0, 0);
+      }
+      // (a unit's rows start at zero and are this wave's alone)
+#pragma unroll
+      for (int u = 0; u < P; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[u][i]),
+                                                        __builtin_bit_cast(bf16x8, t[u][k2]), d, 0, 0, 0);
+          if (mine[u]) *few_delta(delta, row[u], 4 * i + q) += d;
+        }
+    }
+  }
+}
+
+template <int BM, int D>
+__global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt, int S, int per) {
+  using C = FewCfg<BM>;
+  constexpr int TB = C::TB, NB = C::NB;
+  // (one LDS object: with several the compiler waits for every copy in flight before each LDS read, a memory
+  // latency a stage. 1 token, 4096 -> 14336, no adapter: 42 us a call, 31 without)
+  __shared__ __attribute__((aligned(1024))) char ring[D * C::STAGE + 3 * BM * 4 + 16];
+  char* const delta = ring + (D - C::DELTA_SLOTS) * C::STAGE;
+  int* const ids = reinterpret_cast<int*>(ring + D * C::STAGE);  // adapter of each row of the tile (rows are
+  int* const tok = ids + BM;                                     // places of p.order), its token,
+  int* const units = tok + BM;                                   // and the first row and rank of each unit
+  int* const n_units = units + BM;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  // the token tiles of one stretch of the weight follow one another on one XCD, in whose L2 it stays
+  const int G = gridDim.x, pid = blockIdx.x, xcd = pid % 8;
+  const int L = xcd * (G / 8) + min(xcd, G % 8) + pid / 8;
+  const int tile = L / S, split = L - tile * S;
+  const int tile_n = tile / tt, tile_m = tile - tile_n * tt;
+  // (consecutive L: parts of one tile; the token tiles of one stretch of W next)
+  const int64_t n0 = static_cast<int64_t>(tile_n) * kFewN, m0 = static_cast<int64_t>(tile_m) * BM;
+  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(BM, p.T - m0));
+  const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), ldw_b = static_cast<uint32_t>(p.K * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, static_cast<uint32_t>(p.T) * ldx_b);
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.W + n0 * p.K, static_cast<uint32_t>(rows_n) * ldw_b);
+  const int kb_lo = split * per * kFewRow, kb_hi = min(static_cast<int>(p.K * 2), kb_lo + per * kFewRow);
+  const int ns = (kb_hi - kb_lo + kFewRow - 1) / kFewRow;
+  // (tiles start their K loops apart where x stays in an XCD's L2: in step they read the same few memory
+  // channels at a time when the weight's rows are a power of two apart)
+  const int rot = p.T * p.K <= (1 << 19) ? 5 * tile % ns : 0;
+  // this lane's part of each copy instruction (8 rows, x first, then W): its chunk's byte offset in part
+  // `split` at stage 0; rows past the tile's are out of the resource's range and read as zeros
+  uint32_t from[C::LPS];
+  int cb[C::LPS];
+#pragma unroll
+  for (int it = 0; it < C::LPS; ++it) {
+    const int group = it * 4 + wave;
+    const bool is_w = group >= C::XR / 8;
+    const int row = (is_w ? group - C::XR / 8 : group) * 8 + (lane >> 3);
+    cb[it] = kb_lo + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    if (is_w) from[it] = row < rows_n ? static_cast<uint32_t>(row) * ldw_b : kOutOfRange;
+    else if (BM == 16) from[it] = row < rows_m ? static_cast<uint32_t>(row) * ldx_b : kOutOfRange;  // (order is the tokens')
+    else from[it] = row < rows_m ? static_cast<uint32_t>(p.order[m0 + row]) * ldx_b : kOutOfRange;
+  }
+  auto issue = [&](int st) {
+    char* dst = ring + (st % D) * C::STAGE;
+    const int at = st + rot < ns ? st + rot : st + rot - ns;
+    const int kb = st < ns ? at * kFewRow : 1 << 30;  // (past the last: nothing)
+#pragma unroll
+    for (int it = 0; it < C::LPS; ++it) {
+      const int group = it * 4 + wave;
+      const bool is_w = group >= C::XR / 8;
+      const uint32_t off = cb[it] + kb < kb_hi ? from[it] + static_cast<uint32_t>(cb[it] + kb) : kOutOfRange;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_w ? wr : xr, (lds_void*)(dst + group * 1024), 16, off, 0, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int st = 0; st < D - C::DELTA_SLOTS; ++st) issue(st);
+
+  if (tid < BM) {
+    tok[tid] = tid < rows_m ? p.order[m0 + tid] : 0;
+    ids[tid] = tid < rows_m ? p.order[p.T + m0 + tid] : -1;
+  }
+  for (int i = tid; i < BM * kFewN / 4; i += 256) reinterpret_cast<f32x4*>(delta)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  lds_barrier();
+  // units: rows in adapter order, so a unit starts where the adapter or the block of 16 changes (16 rows in
+  // token order: where an adapter shows first)
+  if (wave == 0) {
+    int n = 0;
+#pragma unroll
+    for (int h = 0; h < (BM + 63) / 64; ++h) {
+      const int i = 64 * h + lane;
+      bool start = i < BM && ids[i] >= 0 && (i % 16 == 0 || ids[i] != ids[i - 1]);
+      if constexpr (BM == 16) {
+        for (int e = 0; e + 1 < BM; ++e) start = start && !(e < i && ids[e] == ids[i]);
+      }
+      const uint64_t m = __builtin_amdgcn_ballot_w64(start);
+      if (start) {
+        const int rank = p.rt.ranks != nullptr ? (min(p.rt.ranks[ids[i]], p.rt.rank) + 7) & ~7 : p.rt.rank;
+        units[n + __popcll(m & ((1ull << lane) - 1))] = i | rank << 8;
+      }
+      n += __popcll(m);
+    }
+    if (lane == 0) *n_units = n;
+  }
+  lds_barrier();
+  const int nu = __builtin_amdgcn_readfirstlane(*n_units);
+  few_adapters(p, delta, ids, tok, units, nu, n0, rows_n, split * 4 + wave, 4 * S);
+
+  // lane (r, q) of block (i, j): outputs wn0 + 16 i + 4 q .. +3 of token wm0 + 16 j + r
+  const int wm0 = (wave % C::WAVES_M) * (TB * 16), wn0 = (wave / C::WAVES_M) * (NB * 16);
+  f32x4 acc[NB][TB];
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j) acc[i][j] = *few_delta(delta, wm0 + 16 * j + r, wn0 / 4 + 4 * i + q);
+  if constexpr (C::DELTA_SLOTS > 1) {
+    lds_barrier();
+#pragma unroll
+    for (int st = D - C::DELTA_SLOTS; st < D - 1; ++st) issue(st);
+  }
+  const uint32_t chunk = static_cast<uint32_t>((q ^ ((r >> 1) & 7)) * 16);
+  const uint32_t xo = static_cast<uint32_t>((wm0 + r) * kFewRow) + chunk;
+  const uint32_t wo = static_cast<uint32_t>((C::XR + wn0 + r) * kFewRow) + chunk;
+  for (int st = 0; st < ns; ++st) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vmem((D - 2) * C::LPS));
+    lds_barrier();  // stage st landed for every wave; all are done with the slot of stage st - 1
+    issue(st + D - 1);
+    const char* sp = ring + (st % D) * C::STAGE;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 wf[NB], xf[TB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) wf[i] = *reinterpret_cast<const bf16x8*>(sp + ((wo ^ (kk * 64u)) + i * 16 * kFewRow));
+#pragma unroll
+      for (int j = 0; j < TB; ++j) xf[j] = *reinterpret_cast<const bf16x8*>(sp + ((xo ^ (kk * 64u)) + j * 16 * kFewRow));
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i], xf[j], acc[i][j], 0, 0, 0);
+    }
+  }
+  wait_vmem();  // (copies past the end)
+
+  if (S > 1) {
+    float* mine = p.part + (static_cast<int64_t>(tile) * S + split) * (BM * kFewN) + wave * (NB * TB * 256) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < TB; ++j) *reinterpret_cast<f32x4*>(mine + (i * TB + j) * 256) = acc[i][j];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+      if (wm0 + 16 * j + r < rows_m) few_store(p, acc[i][j], tok[wm0 + 16 * j + r], n0, rows_n, wn0 + 16 * i + 4 * q);
+}
+
+// The parts of a tile added in order. Workgroup: one tile's 16 x 16 block per wave.
+template <int BM>
+__global__ __launch_bounds__(256) void few_finish_kernel(RoutedFew p, int tt, int S) {
+  using C = FewCfg<BM>;
+  const int lane = threadIdx.x & 63;
+  const int b = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // block of the tile
+  const int tile = blockIdx.x, tile_n = tile / tt, tile_m = tile - tile_n * tt;
+  const int64_t n0 = static_cast<int64_t>(tile_n) * kFewN, m0 = static_cast<int64_t>(tile_m) * BM;
+  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(BM, p.T - m0));
+  const float* all = p.part + static_cast<int64_t>(tile) * S * (BM * kFewN) + b * 256 + lane * 4;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  // (eight parts' loads at a time before their adds; a part past the last reads the last again, unused)
+  for (int z = 0; z < S; z += 8) {
+    f32x4 w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w[k] = *reinterpret_cast<const f32x4*>(all + static_cast<int64_t>(min(z + k, S - 1)) * (BM * kFewN));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (z + k < S) v += w[k];
+  }
+  const int wave = b / (C::NB * C::TB), i = b % (C::NB * C::TB) / C::TB, j = b % C::TB;
+  const int wm0 = (wave % C::WAVES_M) * (C::TB * 16), wn0 = (wave / C::WAVES_M) * (C::NB * 16);
+  const int row = wm0 + 16 * j + (lane & 15);
+  if (row < rows_m) few_store(p, v, p.order[m0 + row], n0, rows_n, wn0 + 16 * i + 4 * (lane >> 4));
 }
 
 // ---------------------------------------------------------------------------
@@ -173,8 +591,8 @@ __global__ __launch_bounds__(1024) void route_plan_kernel(RoutePlan p) {
 // Contraction over an adapter's tokens: grid (256 columns of P, item, 64 ranks), tokens in steps of 64
 // gathered through perm. Both operands are token-major and are transposed on the way to LDS (a thread
 // turns 8 tokens x 8 columns in registers); lane (r, q) of the MFMA then reads 8 consecutive tokens of
-// one column. The rank-wide operand is hi + lo, both multiplied into the same fp32 sum: gradients keep
-// about 16 bits of it.
+// one column. The rank-wide operand is hi + mid + lo, all multiplied into the same fp32 sum: the gradients
+// see it in fp32 (hi + lo alone left them at 2-3e-6 of their norm, against 0.3-1.2e-6 this way).
 __device__ __forceinline__ int tsw(int row, int piece) { return row * 8 + (piece ^ ((row ^ (row >> 3)) & 7)); }
 
 __device__ __forceinline__ void transpose_to_lds(char* dst, const u32x4 (&v)[8], int c, int g) {
@@ -192,7 +610,7 @@ __device__ __forceinline__ void transpose_to_lds(char* dst, const u32x4 (&v)[8],
 
 struct ContractArgs {
   const bf16_bits* P; int64_t ldp, M;
-  const bf16_bits *hi, *lo; int64_t ldt;
+  const bf16_bits* q[3]; int64_t ldt;  // hi, mid, lo
   int rank;
   const int32_t* perm;
   const RouteItem* items;
@@ -202,7 +620,7 @@ struct ContractArgs {
 template <bool TRANSPOSE>
 __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
   __shared__ __attribute__((aligned(256))) char pb[kRtI * kRtT * 2];
-  __shared__ __attribute__((aligned(256))) char qb[2][kRtJ * kRtT * 2];
+  __shared__ __attribute__((aligned(256))) char qb[3][kRtJ * kRtT * 2];
   __shared__ int32_t tok[kRouteMaxChunk];
   const RouteItem it = p.items[blockIdx.y];
   const int cnt = it.hi - it.lo;
@@ -218,8 +636,8 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;  // P: columns i0 + 8 c .. +7, tokens 8 g .. +7 of the step
   const bool pcol = i0 + 8 * c < p.M;
   const bf16_bits* pcolp = p.P + i0 + 8 * c;
-  const int qc = threadIdx.x & 7, qg = (threadIdx.x >> 3) & 7;  // threads < 128: hi (wave 0), lo (wave 1)
-  const bf16_bits* qcolp = (wave == 0 ? p.hi : p.lo) + j0 + 8 * qc;
+  const int qc = threadIdx.x & 7, qg = (threadIdx.x >> 3) & 7;  // waves 0, 1, 2: hi, mid, lo
+  const bf16_bits* qcolp = p.q[min(wave, 2)] + j0 + 8 * qc;
   u32x4 pv[8], qv[8];
   auto load = [&](int step) {
 #pragma unroll
@@ -228,7 +646,7 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
       pv[e] = u32x4{0u, 0u, 0u, 0u};
       if (pcol && i < cnt) pv[e] = *reinterpret_cast<const u32x4*>(pcolp + tok[i] * p.ldp);
     }
-    if (wave < 2) {
+    if (wave < 3) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = step * kRtT + 8 * qg + e;
@@ -245,7 +663,7 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
   load(0);
   for (int step = 0; step < nsteps; ++step) {
     transpose_to_lds(pb, pv, c, g);
-    if (wave < 2) transpose_to_lds(qb[wave], qv, qc, qg);
+    if (wave < 3) transpose_to_lds(qb[wave], qv, qc, qg);
     __syncthreads();
     if (step + 1 < nsteps) load(step + 1);
 #pragma unroll
@@ -257,12 +675,12 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
 #pragma unroll
       for (int jb = 0; jb < 4; ++jb) {
         if (jb >= nj) continue;
-        const bf16x8 bh = *reinterpret_cast<const bf16x8*>(qb[0] + tsw(jb * 16 + r, 4 * kk + q) * 16);
-        const bf16x8 bl = *reinterpret_cast<const bf16x8*>(qb[1] + tsw(jb * 16 + r, 4 * kk + q) * 16);
 #pragma unroll
-        for (int ib = 0; ib < 4; ++ib) {
-          acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bh, acc[ib][jb], 0, 0, 0);
-          acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bl, acc[ib][jb], 0, 0, 0);
+        for (int k = 0; k < 3; ++k) {
+          const bf16x8 b = *reinterpret_cast<const bf16x8*>(qb[k] + tsw(jb * 16 + r, 4 * kk + q) * 16);
+#pragma unroll
+          for (int ib = 0; ib < 4; ++ib)
+            acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], b, acc[ib][jb], 0, 0, 0);
         }
       }
     }
@@ -309,11 +727,51 @@ __global__ __launch_bounds__(256) void routed_reduce_kernel(const float* __restr
 hipError_t launch_routed_down(const RoutedDown& p, hipStream_t s) {
   if (p.T <= 0) return hipSuccess;
   const unsigned blocks = static_cast<unsigned>((p.T + kRouteBlock - 1) / kRouteBlock);
-  const int most = p.rt.n_adapters < kRouteBlock ? (p.rt.n_adapters > 0 ? p.rt.n_adapters : 1) : kRouteBlock;
-  const unsigned slots = static_cast<unsigned>(p.T <= 1024 ? most : 1);
-  hipLaunchKernelGGL(routed_down_kernel, dim3(blocks, static_cast<unsigned>((p.rt.rank + 63) / 64), slots),
-                     dim3(64 * kDownWaves), 0, s, p);
+  const unsigned groups = static_cast<unsigned>((p.rt.rank + 63) / 64);
+  auto join = [&](int n) {
+    hipLaunchKernelGGL(down_join_kernel, dim3(static_cast<unsigned>((p.T + 7) / 8), groups), dim3(256), 0, s, p, n);
+    return hipGetLastError();
+  };
+  if (p.splits == 0) {
+    const unsigned z = static_cast<unsigned>(down_slots(p.T, p.rt.n_adapters) * p.parts);
+    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks, groups, z), dim3(64 * kDownWaves), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && p.parts > 1 ? join(p.parts) : e;
+  }
+  hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(p.T))), dim3(64), 0, s, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  e = launch_routed_ring(p, s);
+  if (e != hipSuccess) return e;
+  if (p.splits > 1) {
+    e = join(p.splits);
+    if (e != hipSuccess) return e;
+  }
+  if (p.rt.n_adapters > kRingAdapters)  // (a block of fewer adapters is always the ring's)
+    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks < 512 ? blocks : 512, groups, 1), dim3(64 * kDownWaves), 0, s, p);
   return hipGetLastError();
+}
+
+namespace {
+template <int BM, int D>
+hipError_t few(const RoutedFew& p, const FewPlan& f, hipStream_t s) {
+  hipLaunchKernelGGL((routed_few_kernel<BM, D>), dim3(static_cast<unsigned>(f.tiles * f.splits)), dim3(256), 0, s, p,
+                     f.token_tiles, f.splits, f.stages);
+  if (f.splits > 1)
+    hipLaunchKernelGGL((few_finish_kernel<BM>), dim3(static_cast<unsigned>(f.tiles), BM * kFewN / 1024), dim3(256), 0, s,
+                       p, f.token_tiles, f.splits);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s) {
+  const FewPlan f = few_plan(p.T, p.K, p.N);
+  switch (f.bm) {
+    case 16: return few<16, 6>(p, f, s);
+    case 32: return few<32, 6>(p, f, s);
+    case 64: return few<64, 4>(p, f, s);
+    default: return few<128, 3>(p, f, s);
+  }
 }
 
 hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s) {
@@ -322,7 +780,7 @@ hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s) {
 }
 
 hipError_t launch_routed_contract(const RoutedContract& p, hipStream_t s) {
-  const ContractArgs a{p.P, p.ldp, p.M, p.hi, p.lo, p.ldt, p.rank, p.plan->perm, p.plan->items, p.part, p.out};
+  const ContractArgs a{p.P, p.ldp, p.M, {p.hi, p.mid, p.lo}, p.ldt, p.rank, p.plan->perm, p.plan->items, p.part, p.out};
   const dim3 grid(static_cast<unsigned>((p.M + kRtI - 1) / kRtI), static_cast<unsigned>(p.plan->n_items),
                   static_cast<unsigned>((p.rank + kRtJ - 1) / kRtJ));
   if (p.transpose) hipLaunchKernelGGL(routed_tn_kernel<true>, grid, dim3(256), 0, s, a);

@@ -6,20 +6,129 @@
 
 namespace lora {
 
-// Rank-wide producer: t = s_t . x[t] A_a^T of every token's own adapter a, as hi = RN_bf16(t) and,
-// where lo is not null, RN_bf16(t - hi). Writes eid and blk (RoutedGemm) too.
+// Rank-wide producer: t = s_t . x[t] A_a^T of every token's own adapter a, as hi = RN_bf16(t) and, where
+// mid is not null, the rest of its 24 bits in mid and lo. Writes eid and blk (RoutedGemm) too.
+// With many tokens (splits > 0) a block of 128 tokens with up to four adapters is multiplied by a ring of
+// LDS stages, once per adapter, K in `splits` parts of ks stages of 64; the other blocks, and all blocks of
+// fewer tokens, 16 tokens at a time straight from memory.
+struct RingBlock {
+  int32_t n;      // adapters of the block's tokens, -1: more than kRingAdapters
+  int32_t id[4];
+};
+constexpr int kRingAdapters = 4;
 struct RoutedDown {
   const uint16_t* x; int64_t ldx;
   int64_t T, K;
   const uint16_t* A;   // [n_adapters, rank, K]
   Routing rt;
-  uint16_t* hi;        // [T, ldt]; a token's row is written up to its adapter's rank, then zeros to a
-  uint16_t* lo;        // multiple of 64; not at all without an adapter
+  uint16_t* hi;        // [T, ldt]; the row of a token with an adapter is written whole (zeros behind the
+  uint16_t *mid, *lo;  // adapter's rank), another token's not at all
   int64_t ldt;         // rank_pad(rank)
   int32_t* eid;        // [T]
   int32_t* blk;        // [ceil(T / 16)]
+  int splits, ks;      // of the ring (0: not used)
+  int parts;           // without the ring: workgroups that share K (1: none)
+  RingBlock* ring;     // [ceil(T / 128)]
+  float* tpart;        // splits > 1, parts > 1: partial sums [splits or parts, T, ldt]
+  int32_t* order;      // not null (T <= kFewMaxT): the tokens sorted by adapter go there, [2, T]: the token of
+                       // each place, then its adapter; in token order within one adapter, those without an
+                       // adapter last (up to 16 tokens: as they come). The blocks of 16 are of this order
 };
+constexpr int kRingBlock = 128;
+constexpr int64_t kRingMinT = 1025;
+inline int64_t ring_blocks(int64_t T) { return T >= kRingMinT ? (T + kRingBlock - 1) / kRingBlock : 0; }
+// The ring's split of K, from T and K alone: a workgroup fills a compute unit (120 KB of LDS), so the time goes
+// as the rounds of 256 workgroups over the splits; each split adds its partial sums (taken as 4%). At least
+// 4 stages a split. (18871 tokens, K 8960: 148 blocks in one part about 150 us, in 5 parts 95.)
+inline void ring_plan(int64_t T, int64_t K, int* splits, int* ks) {
+  *splits = *ks = 0;
+  if (T < kRingMinT) return;
+  const int64_t mt = ring_blocks(T), nk = (K * 2 + 127) / 128;
+  double best = 0;
+  for (int s = 1; s <= kMaxProducerSplits && (s == 1 || nk / s >= 4); ++s) {
+    const double cost = static_cast<double>((mt * s + 255) / 256) / s * (1 + 0.04 * (s - 1));
+    if (s > 1 && cost >= best) continue;
+    best = cost;
+    *ks = static_cast<int>((nk + s - 1) / s);
+    *splits = static_cast<int>((nk + *ks - 1) / *ks);
+  }
+}
+inline size_t ring_bytes(int64_t T, int64_t K, int64_t ldt) {
+  int S, ks;
+  ring_plan(T, K, &S, &ks);
+  return S > 1 ? static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(ldt) * 4 : 0;
+}
+// Adapters that a block of 16 tokens can hold.
+inline int down_slots(int64_t T, int n_adapters) {
+  const int64_t m = T < kRouteBlock ? T : kRouteBlock;
+  return static_cast<int>(n_adapters < m ? (n_adapters > 0 ? n_adapters : 1) : m);
+}
+// Parts of K of the producer without the ring: the fewest estimated microseconds. A wave has 256 k (128 above
+// 32 ranks) in flight, each such round about 1.5 us; joining parts takes a launch of 3.5 us; more than 256
+// workgroups do not help (sorted blocks hold about as many adapters as there are blocks and adapters).
+inline int down_parts(int64_t T, int64_t K, int64_t rank, int n_adapters) {
+  if (T >= kRingMinT) return 1;
+  const int64_t blocks = (T + kRouteBlock - 1) / kRouteBlock, slots = down_slots(T, n_adapters);
+  const int64_t units = blocks * slots < blocks + n_adapters ? blocks * slots : blocks + n_adapters;
+  const int64_t wgs = units * ((rank + 63) / 64), round = 8 * (rank > 32 ? 128 : 256);
+  int best = 1;
+  double cost = 1.5 * static_cast<double>((K + round - 1) / round);
+  for (int s = 2; s <= 8 && s * wgs <= 256; ++s) {
+    const double c = 1.5 * static_cast<double>((K + s * round - 1) / (s * round)) + 3.5;
+    if (c < cost) best = s, cost = c;
+  }
+  return best;
+}
+inline size_t down_bytes(int64_t T, int64_t K, int64_t rank, int n_adapters) {
+  const int s = down_parts(T, K, rank, n_adapters);
+  return s > 1 ? static_cast<size_t>(s) * static_cast<size_t>(T) * static_cast<size_t>(rank_pad(rank)) * 4 : 0;
+}
+hipError_t launch_routed_ring(const RoutedDown& p, hipStream_t s);  // (gemm.hip)
 hipError_t launch_routed_down(const RoutedDown& p, hipStream_t s);
+
+constexpr int kDownWaves = 8;
+// Few tokens: base product, adapters and bias in one kernel over a ring of LDS stages (t~ from the
+// rank-wide producer as hi and mid).
+// Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
+// 4096 -> 14336: 68 against 76 us), with mixed ones it is slower up to there and beyond (121 against 86 us).
+constexpr int64_t kFewMaxT = 256;
+struct FewPlan {
+  int bm;            // tokens of a tile
+  int token_tiles;
+  int64_t tiles;     // all tiles (64 outputs each)
+  int splits, stages;  // parts of K, 64-k stages of each
+};
+// Token tiles of 16, 32, 64 or 128; K in as many parts as bring two workgroups to each of 256 compute
+// units, at least 4 stages each.
+inline FewPlan few_plan(int64_t T, int64_t K, int64_t N) {
+  FewPlan f;
+  f.bm = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
+  f.token_tiles = static_cast<int>((T + f.bm - 1) / f.bm);
+  f.tiles = (N + 63) / 64 * f.token_tiles;
+  const int64_t nk = (K + 63) / 64;
+  int64_t s = 512 / f.tiles;
+  s = s > 16 ? 16 : s;
+  s = s > nk / 4 ? nk / 4 : s;
+  s = s < 1 ? 1 : s;
+  f.stages = static_cast<int>((nk + s - 1) / s);
+  f.splits = static_cast<int>((nk + f.stages - 1) / f.stages);
+  return f;
+}
+inline size_t few_part_bytes(const FewPlan& f) {
+  return f.splits > 1 ? static_cast<size_t>(f.tiles) * f.splits * f.bm * 64 * 4 : 0;
+}
+struct RoutedFew {
+  const uint16_t* x; int64_t ldx;
+  const uint16_t* W;
+  const uint16_t* bias;
+  uint16_t* y; int64_t ldy;
+  int64_t T, K, N;
+  const uint16_t *hi, *mid; int64_t ldt;
+  RoutedGemm rt;
+  const int32_t* order;  // [2, T]: the producer's
+  float* part;           // [tiles, splits, bm, 64]
+};
+hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s);
 
 // Tokens sorted by adapter (in token order within one), and the work items of a contraction over
 // them: sorted positions are cut into chunks of `chunk`, an item is one adapter's part of one chunk.
@@ -56,11 +165,11 @@ inline int32_t route_chunk(int64_t T, int64_t tiles) {
   return static_cast<int32_t>(c < 256 ? 256 : (c > kRouteMaxChunk ? kRouteMaxChunk : c));
 }
 
-// out[a] = sum over a's tokens of P[t] (x) (hi + lo)[t]: [M, rank] row-major, or [rank, M] with
+// out[a] = sum over a's tokens of P[t] (x) (hi + mid + lo)[t]: [M, rank] row-major, or [rank, M] with
 // transpose. Adapters without tokens get zeros.
 struct RoutedContract {
   const uint16_t* P; int64_t ldp, M;
-  const uint16_t *hi, *lo; int64_t ldt;
+  const uint16_t *hi, *mid, *lo; int64_t ldt;
   int32_t rank;
   const RoutePlan* plan;
   float* part;         // [route_parts, M, rank_pad]

@@ -30,23 +30,43 @@ struct Take {  // regions of a workspace, each 256-byte aligned
   }
 };
 
+// Partial sums of the few-token kernel for T tokens, K inputs and N outputs.
+size_t few_bytes(int64_t T, int64_t K, int64_t N) {
+  return T <= lora::kFewMaxT ? lora::few_part_bytes(lora::few_plan(T, K, N)) : 0;
+}
+
+// Partial sums of the rank-wide producer for T tokens and K inputs.
+size_t join_bytes(int64_t T, int64_t K, int64_t n, int64_t R) {
+  return std::max(lora::ring_bytes(T, K, lora::rank_pad(R)), lora::down_bytes(T, K, R, static_cast<int>(n)));
+}
+
+void plan_down(lora::RoutedDown& d) {
+  lora::ring_plan(d.T, d.K, &d.splits, &d.ks);
+  d.parts = lora::down_parts(d.T, d.K, d.rt.rank, d.rt.n_adapters);
+}
+
 struct FwdLayout {
-  size_t t = 0, eid = 0, blk = 0, total = 0;
+  size_t t[3] = {0, 0, 0}, eid = 0, blk = 0, ring = 0, part = 0, few = 0, order = 0, total = 0;
 };
 
-FwdLayout fwd_layout(int64_t T, int64_t rp) {
+FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   FwdLayout L;
+  const int64_t rp = lora::rank_pad(R);
   Take take;
-  L.t = take(static_cast<size_t>(T) * rp * 2);
+  L.few = take(few_bytes(T, K, N));
+  for (int i = 0; i < (T <= lora::kFewMaxT ? 3 : 1); ++i) L.t[i] = take(static_cast<size_t>(T) * rp * 2);
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
+  if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
+  L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
+  L.part = take(join_bytes(T, K, n, R));
   L.total = take.off;
   return L;
 }
 
 struct BwdLayout {
-  size_t wt = 0, bt = 0, at = 0, u = 0, ulo = 0, t = 0, tlo = 0, eid = 0, blk = 0, perm = 0, off = 0, items = 0,
-         part = 0, total = 0;
+  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, tpart = 0, eid = 0, blk = 0, ring = 0, perm = 0, off = 0, items = 0,
+         part = 0, few = 0, order = 0, total = 0;
   int32_t chunk = 0;
   int64_t n_items = 0;
 };
@@ -56,17 +76,19 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   Take take;
   const int64_t rp = lora::rank_pad(R);
   if (want_dx) {
+    L.few = take(few_bytes(T, N, K));
     L.wt = take(static_cast<size_t>(K) * N * 2);
     L.at = take(static_cast<size_t>(n) * K * R * 2);
   }
   L.bt = take(static_cast<size_t>(n) * N * R * 2);
   const size_t tb = static_cast<size_t>(T) * rp * 2;
-  L.u = take(tb);
-  L.ulo = take(tb);
-  L.t = take(tb);
-  L.tlo = take(tb);
+  for (size_t& o : L.u) o = take(tb);
+  for (size_t& o : L.t) o = take(tb);
+  L.tpart = take(std::max(join_bytes(T, N, n, R), join_bytes(T, K, n, R)));
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
+  if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
+  L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
   L.perm = take(static_cast<size_t>(T) * 4);
   L.off = take(static_cast<size_t>(n + 1) * 4);
   const int64_t wide = std::max(K, N);
@@ -121,17 +143,32 @@ void pool_spans(const lora_pool* pool, const int32_t* token_adapter, const float
   s[5] = n > 0 ? span2d(token_scale, 1, T, T, 4) : Span{};
 }
 
-LinearProblem gemm_problem(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
-                           const void* bias, void* y, int64_t ldy, const uint16_t* t, const void* B,
-                           const int32_t* eid, const int32_t* blk, const lora_pool* pool) {
+// The base product with the second adapter product, over what the producer `d` wrote; B [n, N, rank].
+hipError_t launch_product(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N, const void* bias,
+                          void* y, int64_t ldy, const lora::RoutedDown& d, const void* B, const lora_pool* pool,
+                          void* part, hipStream_t s) {
+  lora::RoutedGemm rt;
+  rt.B = B; rt.eid = d.eid; rt.blk = d.blk; rt.ranks = pool->ranks; rt.rank = pool->rank;
+  if (T <= lora::kFewMaxT) {
+    lora::RoutedFew f;
+    f.x = static_cast<const uint16_t*>(x); f.ldx = ldx;
+    f.W = static_cast<const uint16_t*>(W);
+    f.bias = static_cast<const uint16_t*>(bias);
+    f.y = static_cast<uint16_t*>(y); f.ldy = ldy;
+    f.T = T; f.K = K; f.N = N;
+    f.hi = d.hi; f.mid = d.mid; f.ldt = d.ldt;
+    f.rt = rt;
+    f.part = static_cast<float*>(part); f.order = d.order;
+    return lora::launch_routed_few(f, s);
+  }
   LinearProblem p;
   std::memset(&p, 0, sizeof(p));
   p.x = x; p.ldx = ldx; p.W = W; p.bias = bias; p.y = y; p.ldy = ldy; p.T = T; p.N = N; p.K = K;
   p.act = Elt::BF16; p.adapter = Elt::BF16;
-  p.work = const_cast<uint16_t*>(t); p.ldt = lora::rank_pad(pool->rank);
+  p.work = d.hi; p.ldt = d.ldt;
   p.routed = true;
-  p.rt.B = B; p.rt.eid = eid; p.rt.blk = blk; p.rt.ranks = pool->ranks; p.rt.rank = pool->rank;
-  return p;
+  p.rt = rt;
+  return lora::launch_routed_gemm(p, s);
 }
 
 }  // namespace
@@ -151,7 +188,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
       K % 8 != 0 || ldx % 8 != 0)
     return LORA_ERR_ALIGN;
   if (T == 0) return LORA_OK;
-  const FwdLayout L = fwd_layout(T, lora::rank_pad(pool->rank));
+  const FwdLayout L = fwd_layout(T, K, N, pool->n_adapters, pool->rank);
   if (workspace == nullptr || workspace_bytes < L.total) return LORA_ERR_WORKSPACE;
   Span in[6];
   pool_spans(pool, token_adapter, token_scale, T, K, N, in);
@@ -171,17 +208,22 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   d.x = static_cast<const uint16_t*>(x); d.ldx = ldx; d.T = T; d.K = K;
   d.A = static_cast<const uint16_t*>(pool->A);
   d.rt = routing(pool, token_adapter, token_scale);
-  d.hi = reinterpret_cast<uint16_t*>(ws + L.t); d.ldt = lora::rank_pad(pool->rank);
+  d.hi = reinterpret_cast<uint16_t*>(ws + L.t[0]); d.ldt = lora::rank_pad(pool->rank);
+  const bool few = T <= lora::kFewMaxT;
+  if (T <= lora::kFewMaxT) d.order = reinterpret_cast<int32_t*>(ws + L.order);
+  if (few) d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]), d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
   d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
+  plan_down(d);
+  d.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
+  d.tpart = reinterpret_cast<float*>(ws + L.part);
   if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
-  const LinearProblem p = gemm_problem(x, T, K, ldx, W, N, bias, y, ldy, d.hi, pool->B, d.eid, d.blk, pool);
-  return lora::launch_routed_gemm(p, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+  return launch_product(x, T, K, ldx, W, N, bias, y, ldy, d, pool->B, pool, ws + L.few, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
 size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank) {
   if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1) return 0;
-  return fwd_layout(T, lora::rank_pad(rank)).total;
+  return fwd_layout(T, K, N, n_adapters, rank).total;
 }
 
 int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
@@ -243,13 +285,16 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   d.x = static_cast<const uint16_t*>(dy); d.ldx = lddy; d.T = T; d.K = N;
   d.A = at16(L.bt);
   d.rt = routing(pool, token_adapter, token_scale);
-  d.hi = at16(L.u); d.lo = at16(L.ulo); d.ldt = rp;
+  d.hi = at16(L.u[0]); d.mid = at16(L.u[1]); d.lo = at16(L.u[2]); d.ldt = rp;
   d.eid = at32(L.eid); d.blk = at32(L.blk);
+  if (T <= lora::kFewMaxT) d.order = at32(L.order);
+  plan_down(d);
+  d.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
+  d.tpart = reinterpret_cast<float*>(ws + L.tpart);
   if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
   if (dx != nullptr) {
-    const LinearProblem p =
-        gemm_problem(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, d.hi, at16(L.at), d.eid, d.blk, pool);
-    if (lora::launch_routed_gemm(p, s) != hipSuccess) return LORA_ERR_HIP;
+    if (launch_product(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, d, at16(L.at), pool, ws + L.few, s) != hipSuccess)
+      return LORA_ERR_HIP;
   }
   if (!grads) return LORA_OK;
   lora::RoutePlan plan{d.eid, T, static_cast<int32_t>(n), L.chunk, at32(L.perm), at32(L.off),
@@ -261,15 +306,16 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   if (dB != nullptr) {
     d.x = static_cast<const uint16_t*>(x); d.ldx = ldx; d.K = K;
     d.A = static_cast<const uint16_t*>(pool->A);
-    d.hi = at16(L.t); d.lo = at16(L.tlo);
+    d.hi = at16(L.t[0]); d.mid = at16(L.t[1]); d.lo = at16(L.t[2]);
+    plan_down(d);
     if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
     c.P = static_cast<const uint16_t*>(dy); c.ldp = lddy; c.M = N;
-    c.hi = d.hi; c.lo = d.lo; c.out = dB; c.transpose = false;
+    c.hi = d.hi; c.mid = d.mid; c.lo = d.lo; c.out = dB; c.transpose = false;
     if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
   }
   if (dA != nullptr) {
     c.P = static_cast<const uint16_t*>(x); c.ldp = ldx; c.M = K;
-    c.hi = at16(L.u); c.lo = at16(L.ulo); c.out = dA; c.transpose = true;
+    c.hi = at16(L.u[0]); c.mid = at16(L.u[1]); c.lo = at16(L.u[2]); c.out = dA; c.transpose = true;
     if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
   }
   return LORA_OK;

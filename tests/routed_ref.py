@@ -22,8 +22,9 @@ def case(T, K, N, n, R, seed, layout="mixed", bias=True, ranks=False, tscale=Tru
     if layout == "mixed":
         ids = rng.integers(0, max(n, 1), T)
         ids[rng.random(T) < none] = -1
-    else:
-        ids = np.repeat(rng.integers(-1, max(n, 1), T), rng.integers(1, 90, T))[:T]
+    else:  # requests of up to 90 tokens ("packed") or of several blocks of 128 ("long")
+        most = 90 if layout == "packed" else 900
+        ids = np.repeat(rng.integers(-1, max(n, 1), T), rng.integers(1, most, T))[:T]
     d["ids"] = torch.from_numpy(ids if n else np.full(T, -1)).to(torch.int32)
     if ranks:
         d["ranks"] = torch.from_numpy(rng.integers(1, R // 8 + 1, n) * 8).to(torch.int32)
@@ -101,14 +102,14 @@ def backward(d):
         mag[rows] += u.abs() @ A.abs()
         terms[rows] += r
         ub[rows] += (u.abs() * U16 + umag * (N + 3) * U32 * (1 + U16)) @ A.abs()
-        # hi + lo: each rounded to bf16, lo at most 2^-8 of the value
-        eu = u.abs() * U16 * U16 + umag * (N + 3) * U32
-        et = t.abs() * U16 * U16 + tmag * (K + 3) * U32
+        # hi + mid + lo: each rounded to bf16, and at most 2^-8 of the one before
+        eu = u.abs() * U16 ** 3 + umag * (N + 3) * U32
+        et = t.abs() * U16 ** 3 + tmag * (K + 3) * U32
         dA[a, :r] = u.T @ xa
         dB[a, :, :r] = dya.T @ t
-        # 2 c products (hi and lo apart) and the joins of the chunks, at most c of them
-        bA[a, :r] = eu.T @ xa.abs() + (3 * c + 2) * U32 * ((u.abs() * (1 + 2 * U16) + eu).T @ xa.abs())
-        bB[a, :, :r] = dya.abs().T @ et + (3 * c + 2) * U32 * (dya.abs().T @ (t.abs() * (1 + 2 * U16) + et))
+        # 3 c products (hi, mid and lo apart) and the joins of the chunks, at most c of them
+        bA[a, :r] = eu.T @ xa.abs() + (4 * c + 2) * U32 * ((u.abs() * (1 + 2 * U16) + eu).T @ xa.abs())
+        bB[a, :, :r] = dya.abs().T @ et + (4 * c + 2) * U32 * (dya.abs().T @ (t.abs() * (1 + 2 * U16) + et))
     off = ub + (terms + 2) * U32 * (mag + ub)
     return (dx, dA, dB), (off + U16 * (dx.abs() + off), bA, bB)
 

@@ -125,6 +125,9 @@ FWD = [
     (65, 520, 300, 7, 72, "mixed"), (129, 1544, 64, 3, 64, "packed"), (200, 72, 520, 5, 136, "mixed"),
     (300, 256, 513, 2, 64, "packed"), (257, 64, 256, 1, 16, "packed"), (1000, 136, 264, 6, 40, "packed"),
     (700, 328, 1100, 9, 128, "packed"), (33, 64, 48, 0, 8, "mixed"), (1030, 96, 2304, 300, 8, "mixed"),
+    (1025, 2056, 72, 2, 64, "long"), (3001, 584, 260, 4, 136, "long"), (5000, 1032, 1100, 3, 24, "long"),
+    (16500, 72, 40, 3, 72, "long"), (16500, 200, 24, 1, 64, "long"), (2100, 1160, 72, 30, 40, "packed"),
+    (9000, 64, 24, 7, 72, "mixed"),
 ]
 
 
@@ -244,7 +247,8 @@ BWD = [
     (1, 8, 8, 1, 8, "mixed"), (5, 128, 96, 3, 16, "mixed"), (17, 264, 200, 40, 8, "mixed"),
     (64, 512, 304, 9, 32, "mixed"), (129, 136, 64, 3, 64, "packed"), (300, 256, 520, 2, 72, "packed"),
     (1000, 136, 264, 6, 40, "packed"), (2500, 64, 48, 3, 16, "packed"), (5000, 40, 24, 2, 8, "packed"),
-    (33, 64, 48, 0, 8, "mixed"), (700, 72, 528, 5, 136, "mixed"),
+    (33, 64, 48, 0, 8, "mixed"), (700, 72, 528, 5, 136, "mixed"), (1100, 520, 1032, 3, 64, "long"),
+    (3001, 264, 136, 4, 136, "long"), (16500, 40, 72, 2, 24, "long"),
 ]
 
 
