@@ -17,6 +17,7 @@ not given, and call the C functions on the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -469,26 +470,26 @@ def lora_linear_backward(x, W, A, B, dy, alpha, strength=1.0, request_scale=1.0,
 
 def _of(t, name, shape, dtype, device):
     """The tensor checked: contiguous, of this shape and type, on the call's device (None passes)."""
-    if t is None:
-        return None
+    if t is None or (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return t
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, x on {device}")
-    return t
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _rows(t, name, shape, device):
     """Row stride of a bf16 matrix of this shape with unit column stride on the call's device."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or t.device != device:
+    if t.shape != shape or t.device != device:
         raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
-    if t.numel() and t.stride(1) != 1 and t.shape[1] != 1:  # (one column may carry any stride)
+    rows, cols = shape
+    ld, unit = t.stride()
+    if unit != 1 and cols != 1 and rows * cols != 0:  # (one column may carry any stride)
         raise ValueError(f"{name} must have unit column stride")
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8  # (and so may one row)
+    return ld if rows > 1 else -(-cols // 8) * 8  # (and so may one row)
 
 
 def _routed_args(x, W, A, B, scales, token_adapter, token_scale, ranks):
@@ -518,8 +519,23 @@ def _bytes_on(workspace, need, device):
     return workspace
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_on(device, stream):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:  # (the handle alone, without a Stream object)
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device made current for a call (a context only where it is not already)."""
+    return _HERE if device.type != "cuda" or device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def lora_linear_routed(x, W, b, A, B, scales, token_adapter, token_scale=None, ranks=None, out=None, workspace=None,
@@ -533,7 +549,7 @@ def lora_linear_routed(x, W, b, A, B, scales, token_adapter, token_scale=None, r
     dev = x.device
     ldx = _rows(x, "x", (T, K), dev)
     _of(b, "b", (N,), torch.bfloat16, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
         ldy = _rows(out, "out", (T, N), dev)
@@ -553,7 +569,7 @@ def lora_linear_routed_backward(x, W, A, B, dy, scales, token_adapter, token_sca
     n, R, _ = A.shape
     dev = x.device
     ldx, lddy = _rows(x, "x", (T, K), dev), _rows(dy, "dy", (T, N), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         if "dx" not in want:
             dx = None
         elif dx is None:
@@ -631,7 +647,7 @@ class LoraAdamW:
               for p, w, g, m, v, ms, vs in zip(params, master or none, grads, self.m, self.v, self.m_scale or none,
                                                self.v_scale or none)]
         need = lora_adamw_table_size(ts)
-        with torch.cuda.device(dev):
+        with _on(dev):
             self._table = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
             self._plan = lora_adamw_plan(ts, _dt(params[0]), _dt(grads[0]), state_bits, self._table.data_ptr(),
                                          self._table.numel(), _stream_on(dev, stream))
@@ -639,7 +655,7 @@ class LoraAdamW:
     def step(self, grad_scale=1.0, stream=None):
         """One step on the gradients that the buffers hold (on the stream that runs it)."""
         count = self.step_count + 1
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             lora_adamw_step(self._plan, float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps),
                             float(self.weight_decay), count, _ptr(self.lr_step), float(grad_scale),
                             _stream_on(self.device, stream))

@@ -535,55 +535,95 @@ __global__ __launch_bounds__(256) void few_finish_kernel(RoutedFew p, int tt, in
 }
 
 // ---------------------------------------------------------------------------
-// Tokens sorted by adapter: workgroup a finds its adapter's tokens. The 16 waves take consecutive
-// stretches of the tokens; a first pass counts (tokens of lower adapters give the start, wave counts the
-// places), a second writes. No atomics: the order is the tokens' own.
+// Tokens sorted by adapter: workgroup a finds its adapter's tokens. The 16 waves take consecutive stretches of
+// the tokens, eight loads of 64 in flight; a first pass counts the tokens of every adapter before it (one LDS
+// atomic for each adapter among 64 tokens; integers, so their order does not show), from which follow its place
+// among tokens and items, and its own by wave; a second writes them, in token order.
 __global__ __launch_bounds__(1024) void route_plan_kernel(RoutePlan p) {
-  __shared__ int below[16], mine[16];
+  extern __shared__ int counts[];  // [n_adapters]
+  __shared__ int sums[5][16], mine[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int a = blockIdx.x;
   const int64_t per = ((p.T + 15) / 16 + 63) / 64 * 64;
   const int64_t lo = wave * per, hi = min<int64_t>(p.T, lo + per);
-  int nb = 0, nm = 0;
-  for (int64_t t = lo; t < hi; t += 64) {
-    const int id = t + lane < hi ? p.eid[t + lane] : -1;
-    nb += __popcll(__builtin_amdgcn_ballot_w64(id >= 0 && id < a));
-    nm += __popcll(__builtin_amdgcn_ballot_w64(id == a));
-  }
-  if (lane == 0) below[wave] = nb, mine[wave] = nm;
+  for (int i = threadIdx.x; i < p.n_adapters; i += 1024) counts[i] = 0;
   __syncthreads();
-  int start = 0, count = 0, at = 0;
+  int nm = 0;
+  for (int64_t t = lo; t < hi; t += 512) {
+    int id[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) id[k] = t + 64 * k + lane < hi ? p.eid[t + 64 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint64_t todo = __builtin_amdgcn_ballot_w64(id[k] >= 0 && id[k] < a);
+      while (todo != 0) {
+        const int b = __builtin_amdgcn_readlane(id[k], __builtin_ctzll(todo));
+        const uint64_t m = __builtin_amdgcn_ballot_w64(id[k] == b);
+        todo &= ~m;
+        if (lane == 0) atomicAdd(&counts[b], __popcll(m));
+      }
+      nm += __popcll(__builtin_amdgcn_ballot_w64(id[k] == a));
+    }
+  }
+  if (lane == 0) mine[wave] = nm;
+  __syncthreads();
+  // of the adapters before a: tokens, and for each table items and slots of partial sums
+  int v[5] = {0, 0, 0, 0, 0};
+  for (int i = threadIdx.x; i < a; i += 1024) {
+    v[0] += counts[i];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = max(1, (counts[i] + p.table[h].chunk - 1) / p.table[h].chunk);
+      v[1 + 2 * h] += k;
+      v[2 + 2 * h] += k > 1 ? k : 0;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v[k] += __shfl_xor(v[k], d);
+    if (lane == 0) sums[k][wave] = v[k];
+  }
+  __syncthreads();
+  int before[5] = {0, 0, 0, 0, 0}, count = 0, at = 0;
   for (int w = 0; w < 16; ++w) {
-    start += below[w];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) before[k] += sums[k][w];
     if (w < wave) at += mine[w];
     count += mine[w];
   }
+  const int start = before[0];
   at += start;
-  for (int64_t t = lo; t < hi; t += 64) {
-    const int id = t + lane < hi ? p.eid[t + lane] : -1;
-    const uint64_t m = __builtin_amdgcn_ballot_w64(id == a);
-    if (id == a) p.perm[at + __popcll(m & ((1ull << lane) - 1))] = static_cast<int32_t>(t + lane);
-    at += __popcll(m);
+  for (int64_t t = lo; t < hi; t += 512) {
+    int id[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) id[k] = t + 64 * k + lane < hi ? p.eid[t + 64 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint64_t m = __builtin_amdgcn_ballot_w64(id[k] == a);
+      if (id[k] == a) p.perm[at + __popcll(m & ((1ull << lane) - 1))] = static_cast<int32_t>(t + 64 * k + lane);
+      at += __popcll(m);
+    }
   }
-  const int end = start + count, c = p.chunk;
-  if (threadIdx.x == 0) {
-    p.off[a] = start;
-    if (a == p.n_adapters - 1) p.off[a + 1] = end;
-  }
-  // items a + j for the chunks j from the one that holds `start` to the one that holds `end`: the next
-  // adapter's first item follows, so the items of all adapters fill their table without a gap
-  const int j0 = start / c, j1 = end / c;
-  const bool several = count > 0 && (end - 1) / c != j0;
-  for (int j = j0 + threadIdx.x; j <= j1; j += 1024) {
-    RouteItem it;
-    it.adapter = a;
-    it.lo = max(start, j * c);
-    it.hi = max(it.lo, min(end, (j + 1) * c));
-    it.part = several ? 2 * j + (j == j0 ? 1 : 0) : -1;
-    p.items[a + j] = it;
-  }
-  if (a == p.n_adapters - 1) {  // places behind the last item (tokens without an adapter)
-    for (int64_t z = static_cast<int64_t>(a) + j1 + 1 + threadIdx.x; z < p.n_items; z += 1024) p.items[z] = RouteItem{0, 0, 0, -1};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const RouteTable& tb = p.table[h];
+    const int item = before[1 + 2 * h], slot = before[2 + 2 * h];
+    const int k = max(1, (count + tb.chunk - 1) / tb.chunk);
+    for (int i = threadIdx.x; i < k; i += 1024) {
+      RouteItem it;
+      it.adapter = a;
+      it.lo = start + static_cast<int>(static_cast<int64_t>(count) * i / k);
+      it.hi = start + static_cast<int>(static_cast<int64_t>(count) * (i + 1) / k);
+      it.part = k > 1 ? slot + i : -1;
+      tb.items[item + i] = it;
+    }
+    if (threadIdx.x == 0) tb.first[a] = item;
+    if (a == p.n_adapters - 1) {
+      if (threadIdx.x == 0) tb.first[a + 1] = item + k;
+      for (int64_t z = item + k + static_cast<int64_t>(threadIdx.x); z < tb.n_items; z += 1024)
+        tb.items[z] = RouteItem{0, 0, 0, -1};
+    }
   }
 }
 
@@ -689,37 +729,49 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
   // lane (r, q) of block (ib, jb) holds D[i = 64 wave + 16 ib + 4 q + e][j = 16 jb + r]
   float* dst = it.part < 0 ? p.out + static_cast<int64_t>(it.adapter) * p.M * p.rank
                            : p.part + static_cast<int64_t>(it.part) * p.M * p.rank;
+  const bool quads = reinterpret_cast<uintptr_t>(dst) % 16 == 0;
 #pragma unroll
   for (int ib = 0; ib < 4; ++ib) {
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       const int j = j0 + jb * 16 + r;
       if (j >= p.rank) continue;
+      const int64_t i = i0 + wave * 64 + ib * 16 + 4 * q;
+      if (i >= p.M) continue;  // (M is a multiple of 8: all four or none)
+      if (TRANSPOSE && quads) {
+        *reinterpret_cast<f32x4*>(dst + j * p.M + i) = acc[ib][jb];
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = i0 + wave * 64 + ib * 16 + 4 * q + e;
-        if (i < p.M) dst[TRANSPOSE ? j * p.M + i : i * p.rank + j] = acc[ib][jb][e];
+        for (int e = 0; e < 4; ++e) dst[TRANSPOSE ? j * p.M + i + e : (i + e) * p.rank + j] = acc[ib][jb][e];
       }
     }
   }
 }
 
-// Gradients of adapters with several items: their partial sums in chunk order. Adapters without tokens: zeros.
+// Gradients of adapters with several items: their partial sums in order. Adapters without tokens: zeros. Four
+// elements a thread.
 __global__ __launch_bounds__(256) void routed_reduce_kernel(const float* __restrict__ part, int64_t n,
-                                                            const int32_t* __restrict__ off, int chunk,
+                                                            const int32_t* __restrict__ first,
+                                                            const RouteItem* __restrict__ items,
                                                             float* __restrict__ out) {
   const int a = blockIdx.y;
-  const int lo = off[a], hi = off[a + 1];
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int lo = first[a], k = first[a + 1] - lo;
+  const RouteItem it = items[lo];
+  if (k == 1 && it.hi > it.lo) return;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;  // (n is a multiple of 64)
   if (i >= n) return;
-  float v = 0.f;
-  if (hi > lo) {
-    const int j0 = lo / chunk, j1 = (hi - 1) / chunk;
-    if (j0 == j1) return;
-    v = part[(2 * static_cast<int64_t>(j0) + 1) * n + i];
-    for (int j = j0 + 1; j <= j1; ++j) v += part[2 * static_cast<int64_t>(j) * n + i];
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (k > 1) {
+    const float* src = part + it.part * n + i;
+    for (int z = 0; z < k; ++z) v += *reinterpret_cast<const f32x4*>(src + z * n);
   }
-  out[static_cast<int64_t>(a) * n + i] = v;
+  float* dst = out + static_cast<int64_t>(a) * n + i;
+  if (reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
+    *reinterpret_cast<f32x4*>(dst) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dst[e] = v[e];
+  }
 }
 
 }  // namespace
@@ -738,9 +790,12 @@ hipError_t launch_routed_down(const RoutedDown& p, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     return e == hipSuccess && p.parts > 1 ? join(p.parts) : e;
   }
-  hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(p.T))), dim3(64), 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (!p.routed) {
+    hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(p.T))), dim3(64), 0, s, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   e = launch_routed_ring(p, s);
   if (e != hipSuccess) return e;
   if (p.splits > 1) {
@@ -775,13 +830,14 @@ hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s) {
 }
 
 hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s) {
-  hipLaunchKernelGGL(route_plan_kernel, dim3(static_cast<unsigned>(p.n_adapters)), dim3(1024), 0, s, p);
+  hipLaunchKernelGGL(route_plan_kernel, dim3(static_cast<unsigned>(p.n_adapters)), dim3(1024),
+                     static_cast<size_t>(p.n_adapters) * 4, s, p);
   return hipGetLastError();
 }
 
 hipError_t launch_routed_contract(const RoutedContract& p, hipStream_t s) {
-  const ContractArgs a{p.P, p.ldp, p.M, {p.hi, p.mid, p.lo}, p.ldt, p.rank, p.plan->perm, p.plan->items, p.part, p.out};
-  const dim3 grid(static_cast<unsigned>((p.M + kRtI - 1) / kRtI), static_cast<unsigned>(p.plan->n_items),
+  const ContractArgs a{p.P, p.ldp, p.M, {p.hi, p.mid, p.lo}, p.ldt, p.rank, p.perm, p.table.items, p.part, p.out};
+  const dim3 grid(static_cast<unsigned>((p.M + kRtI - 1) / kRtI), static_cast<unsigned>(p.table.n_items),
                   static_cast<unsigned>((p.rank + kRtJ - 1) / kRtJ));
   if (p.transpose) hipLaunchKernelGGL(routed_tn_kernel<true>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(routed_tn_kernel<false>, grid, dim3(256), 0, s, a);
@@ -789,8 +845,8 @@ hipError_t launch_routed_contract(const RoutedContract& p, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int64_t n = p.M * p.rank;
   hipLaunchKernelGGL(routed_reduce_kernel,
-                     dim3(static_cast<unsigned>((n + 255) / 256), static_cast<unsigned>(p.plan->n_adapters)), dim3(256),
-                     0, s, p.part, n, p.plan->off, p.plan->chunk, p.out);
+                     dim3(static_cast<unsigned>((n / 4 + 255) / 256), static_cast<unsigned>(p.n_adapters)),
+                     dim3(256), 0, s, p.part, n, p.table.first, p.table.items, p.out);
   return hipGetLastError();
 }
 

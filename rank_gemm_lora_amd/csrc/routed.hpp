@@ -29,6 +29,7 @@ struct RoutedDown {
   int splits, ks;      // of the ring (0: not used)
   int parts;           // without the ring: workgroups that share K (1: none)
   RingBlock* ring;     // [ceil(T / 128)]
+  bool routed;         // eid, blk and ring are there already, from a call with the same routing
   float* tpart;        // splits > 1, parts > 1: partial sums [splits or parts, T, ldt]
   int32_t* order;      // not null (T <= kFewMaxT): the tokens sorted by adapter go there, [2, T]: the token of
                        // each place, then its adapter; in token order within one adapter, those without an
@@ -99,7 +100,8 @@ struct FewPlan {
   int splits, stages;  // parts of K, 64-k stages of each
 };
 // Token tiles of 16, 32, 64 or 128; K in as many parts as bring two workgroups to each of 256 compute
-// units, at least 4 stages each.
+// units, at least 4 stages each. Up to 24 stages stay in one part: the second launch costs what it saves
+// (1 token, 1536 -> 1536: figures beside few_finish_kernel).
 inline FewPlan few_plan(int64_t T, int64_t K, int64_t N) {
   FewPlan f;
   f.bm = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
@@ -109,7 +111,7 @@ inline FewPlan few_plan(int64_t T, int64_t K, int64_t N) {
   int64_t s = 512 / f.tiles;
   s = s > 16 ? 16 : s;
   s = s > nk / 4 ? nk / 4 : s;
-  s = s < 1 ? 1 : s;
+  s = s < 1 || nk <= 24 ? 1 : s;
   f.stages = static_cast<int>((nk + s - 1) / s);
   f.splits = static_cast<int>((nk + f.stages - 1) / f.stages);
   return f;
@@ -130,39 +132,39 @@ struct RoutedFew {
 };
 hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s);
 
-// Tokens sorted by adapter (in token order within one), and the work items of a contraction over
-// them: sorted positions are cut into chunks of `chunk`, an item is one adapter's part of one chunk.
-// Item z = a + (index of its chunk), so every item has a place known without counting; items[z] is
-// empty (lo == hi) where adapter and chunk do not meet.
+// Tokens sorted by adapter (in token order within one), and the work items of a contraction over them: an
+// adapter's tokens in ceil(count / chunk) items of nearly equal length (one, empty, without tokens), the
+// items of all adapters one behind the other.
 struct RouteItem {
   int32_t adapter, lo, hi;
-  int32_t part;  // where its partial sums go: -1 straight to the gradient (the adapter has one item), else a slot
+  int32_t part;  // where its partial sums go: -1 straight to the gradient (the adapter's only item), else a slot
+};
+struct RouteTable {
+  int32_t chunk;
+  int32_t* first;      // [n_adapters + 1]: the first item of each adapter
+  RouteItem* items;    // [n_items], the places behind the last item empty
+  int64_t n_items;     // route_items(T, n_adapters, chunk)
 };
 struct RoutePlan {
   const int32_t* eid; int64_t T;
   int32_t n_adapters;
-  int32_t chunk;
   int32_t* perm;       // [T]
-  int32_t* off;        // [n_adapters + 1]
-  RouteItem* items;    // [n_items]
-  int64_t n_items;     // route_items(T, n_adapters, chunk)
+  RouteTable table[2]; // one for each gradient: their widths ask for chunks of their own
 };
 constexpr int kRouteMaxChunk = 4096;  // positions of an item that a workgroup keeps in LDS
-inline int64_t route_chunks(int64_t T, int64_t chunk) { return (T + chunk - 1) / chunk; }
 inline int64_t route_items(int64_t T, int64_t n, int64_t chunk) { return n + T / chunk + 1; }
-// Slots of partial sums: a chunk holds at most two items of adapters with more than one (the end of
-// one, the start of another).
-inline int64_t route_parts(int64_t T, int64_t chunk) { return 2 * route_chunks(T, chunk); }
+// Slots of partial sums, counted over the items of adapters with more than one: k > 1 items hold more than
+// (k - 1) chunk >= k chunk / 2 tokens, so there are at most 2 T / chunk.
+inline int64_t route_parts(int64_t T, int64_t chunk) { return 2 * (T / chunk) + 1; }
 hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s);
 
-// Contraction chunk for outputs of `tiles` workgroups each (the wider of the two gradients).
+// Most tokens of an item for an output of `tiles` workgroups: about two
+// workgroups for each of 256 compute units if the adapters were one, and items long enough that the partial
+// sums of adapters with several stay few.
 constexpr int kRtI = 256, kRtJ = 64, kRtT = 64;
 inline int32_t route_chunk(int64_t T, int64_t tiles) {
-  int64_t s = 1024 / (tiles > 0 ? tiles : 1);
-  s = s < 1 ? 1 : (s > 64 ? 64 : s);
-  int64_t c = (T + s - 1) / s;
-  c = (c + kRtT - 1) / kRtT * kRtT;
-  return static_cast<int32_t>(c < 256 ? 256 : (c > kRouteMaxChunk ? kRouteMaxChunk : c));
+  int64_t c = (T * tiles / 512 + kRtT - 1) / kRtT * kRtT;
+  return static_cast<int32_t>(c < 512 ? 512 : (c > kRouteMaxChunk ? kRouteMaxChunk : c));
 }
 
 // out[a] = sum over a's tokens of P[t] (x) (hi + mid + lo)[t]: [M, rank] row-major, or [rank, M] with
@@ -171,8 +173,10 @@ struct RoutedContract {
   const uint16_t* P; int64_t ldp, M;
   const uint16_t *hi, *mid, *lo; int64_t ldt;
   int32_t rank;
-  const RoutePlan* plan;
-  float* part;         // [route_parts, M, rank_pad]
+  const int32_t* perm;
+  RouteTable table;
+  int32_t n_adapters;
+  float* part;         // [route_parts, M, rank]
   float* out;
   bool transpose;
 };

@@ -65,10 +65,13 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
 }
 
 struct BwdLayout {
-  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, tpart = 0, eid = 0, blk = 0, ring = 0, perm = 0, off = 0, items = 0,
+  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, tpart = 0, eid = 0, blk = 0, ring = 0, perm = 0,
          part = 0, few = 0, order = 0, total = 0;
-  int32_t chunk = 0;
-  int64_t n_items = 0;
+  struct {
+    size_t first = 0, items = 0;
+    int32_t chunk = 0;
+    int64_t n_items = 0;
+  } table[2];  // dA, dB
 };
 
 BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool want_dx) {
@@ -90,12 +93,17 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
   L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
   L.perm = take(static_cast<size_t>(T) * 4);
-  L.off = take(static_cast<size_t>(n + 1) * 4);
-  const int64_t wide = std::max(K, N);
-  L.chunk = lora::route_chunk(T, (wide + lora::kRtI - 1) / lora::kRtI * ((R + lora::kRtJ - 1) / lora::kRtJ));
-  L.n_items = lora::route_items(T, n, L.chunk);
-  L.items = take(static_cast<size_t>(L.n_items) * sizeof(lora::RouteItem));
-  L.part = take(static_cast<size_t>(lora::route_parts(T, L.chunk)) * wide * R * 4);
+  size_t part = 0;
+  for (int h = 0; h < 2; ++h) {
+    auto& tb = L.table[h];
+    const int64_t M = h == 0 ? K : N;
+    tb.chunk = lora::route_chunk(T, (M + lora::kRtI - 1) / lora::kRtI * ((R + lora::kRtJ - 1) / lora::kRtJ));
+    tb.n_items = lora::route_items(T, n, tb.chunk);
+    tb.first = take(static_cast<size_t>(n + 1) * 4);
+    tb.items = take(static_cast<size_t>(tb.n_items) * sizeof(lora::RouteItem));
+    part = std::max(part, static_cast<size_t>(lora::route_parts(T, tb.chunk)) * M * R * 4);
+  }
+  L.part = take(part);
   L.total = take.off;
   return L;
 }
@@ -241,7 +249,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
     return LORA_ERR_ALIGN;
   const int64_t n = pool->n_adapters, R = pool->rank;
   const BwdLayout L = T > 0 ? bwd_layout(T, K, N, n, R, dx != nullptr) : BwdLayout{};
-  if (L.n_items > 65535) return LORA_ERR_UNSUPPORTED;
+  if (L.table[0].n_items > 65535 || L.table[1].n_items > 65535) return LORA_ERR_UNSUPPORTED;
   if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
   Span in[6];
   pool_spans(pool, token_adapter, token_scale, T, K, N, in);
@@ -297,25 +305,31 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
       return LORA_ERR_HIP;
   }
   if (!grads) return LORA_OK;
-  lora::RoutePlan plan{d.eid, T, static_cast<int32_t>(n), L.chunk, at32(L.perm), at32(L.off),
-                       reinterpret_cast<lora::RouteItem*>(ws + L.items), L.n_items};
+  lora::RoutePlan plan;
+  plan.eid = d.eid; plan.T = T; plan.n_adapters = static_cast<int32_t>(n); plan.perm = at32(L.perm);
+  for (int h = 0; h < 2; ++h)
+    plan.table[h] = lora::RouteTable{L.table[h].chunk, at32(L.table[h].first),
+                                     reinterpret_cast<lora::RouteItem*>(ws + L.table[h].items), L.table[h].n_items};
   if (lora::launch_route_plan(plan, s) != hipSuccess) return LORA_ERR_HIP;
   lora::RoutedContract c;
-  c.ldt = rp; c.rank = static_cast<int32_t>(R); c.plan = &plan;
+  c.ldt = rp; c.rank = static_cast<int32_t>(R); c.perm = plan.perm; c.n_adapters = plan.n_adapters;
   c.part = reinterpret_cast<float*>(ws + L.part);
   if (dB != nullptr) {
     d.x = static_cast<const uint16_t*>(x); d.ldx = ldx; d.K = K;
     d.A = static_cast<const uint16_t*>(pool->A);
     d.hi = at16(L.t[0]); d.mid = at16(L.t[1]); d.lo = at16(L.t[2]);
     plan_down(d);
+    d.routed = true;
     if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
     c.P = static_cast<const uint16_t*>(dy); c.ldp = lddy; c.M = N;
     c.hi = d.hi; c.mid = d.mid; c.lo = d.lo; c.out = dB; c.transpose = false;
+    c.table = plan.table[1];
     if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
   }
   if (dA != nullptr) {
     c.P = static_cast<const uint16_t*>(x); c.ldp = ldx; c.M = K;
     c.hi = at16(L.u[0]); c.mid = at16(L.u[1]); c.lo = at16(L.u[2]); c.out = dA; c.transpose = true;
+    c.table = plan.table[0];
     if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
   }
   return LORA_OK;
