@@ -26,11 +26,8 @@ namespace {
 // 64 x 64 tiles through LDS: coalesced reads of src rows and writes of dst rows.
 __global__ __launch_bounds__(256) void transpose_pad_kernel(const bf16_bits* __restrict__ src, int64_t lds_,
                                                             int64_t R, int64_t C, bf16_bits* __restrict__ dst,
-                                                            int64_t Rpad, int64_t Cpad, int64_t src_slot,
-                                                            int64_t dst_slot) {
+                                                            int64_t Rpad, int64_t Cpad) {
   __shared__ bf16_bits tile[64][66];
-  src += blockIdx.z * src_slot;
-  dst += blockIdx.z * dst_slot;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int i = ty; i < 64; i += 4) {
@@ -50,14 +47,9 @@ __global__ __launch_bounds__(256) void transpose_pad_kernel(const bf16_bits* __r
 // 16-byte stores of consecutive rows stay aligned). Needs C, ld and Rpad multiples of 8 and
 // 16-byte aligned src and dst. Measured on MI355X: B^T of 8960 x 64 2.6 against 5.3 us, W^T of
 // 8960 x 1536 11.6 against 18.7 us; the same bytes.
-__global__ __launch_bounds__(256) void transpose_pad16_kernel(const bf16_bits* __restrict__ src, int64_t lds_,
-                                                              int64_t R, int64_t C, bf16_bits* __restrict__ dst,
-                                                              int64_t Rpad, int64_t Cpad, int64_t src_slot,
-                                                              int64_t dst_slot) {
-  __shared__ __attribute__((aligned(16))) bf16_bits tile[64][72];
-  src += blockIdx.z * src_slot;
-  dst += blockIdx.z * dst_slot;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
+__device__ __forceinline__ void transpose_tile16(const bf16_bits* __restrict__ src, int64_t lds_, int64_t R, int64_t C,
+                                                 bf16_bits* __restrict__ dst, int64_t Rpad, int64_t Cpad, int64_t r0,
+                                                 int64_t c0, bf16_bits (&tile)[64][72]) {
   const int pc = threadIdx.x & 7, rr = threadIdx.x >> 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -83,20 +75,38 @@ __global__ __launch_bounds__(256) void transpose_pad16_kernel(const bf16_bits* _
   }
 }
 
-// (slots > 1: as many matrices, src_slot and dst_slot elements apart)
+__global__ __launch_bounds__(256) void transpose_pad16_kernel(const bf16_bits* __restrict__ src, int64_t lds_,
+                                                              int64_t R, int64_t C, bf16_bits* __restrict__ dst,
+                                                              int64_t Rpad, int64_t Cpad) {
+  __shared__ __attribute__((aligned(16))) bf16_bits tile[64][72];
+  transpose_tile16(src, lds_, R, C, dst, Rpad, Cpad, static_cast<int64_t>(blockIdx.x) * 64,
+                   static_cast<int64_t>(blockIdx.y) * 64, tile);
+}
+
+// Several stacks of matrices in one launch: workgroups [first, next first) are a stack's 64 x 64 tiles.
+struct TransposeStacks {
+  TransposeStack s[kTransposeStacks];
+  int64_t first[kTransposeStacks + 1];
+};
+__global__ __launch_bounds__(256) void transpose_stacks_kernel(TransposeStacks a) {
+  __shared__ __attribute__((aligned(16))) bf16_bits tile[64][72];
+  int k = 0;
+#pragma unroll
+  for (int i = 1; i < kTransposeStacks; ++i) k = blockIdx.x >= a.first[i] ? i : k;
+  const TransposeStack& s = a.s[k];
+  const int64_t tr = (s.R + 63) / 64, tc = (s.C + 63) / 64, b = blockIdx.x - a.first[k];
+  const int64_t slot = b / (tr * tc), rest = b - slot * (tr * tc);
+  transpose_tile16(s.src + slot * s.R * s.C, s.C, s.R, s.C, s.dst + slot * s.R * s.C, s.R, s.C, rest % tr * 64,
+                   rest / tr * 64, tile);
+}
+
 hipError_t transpose_pad_impl(const bf16_bits* src, int64_t ld, int64_t R, int64_t C, bf16_bits* dst, int64_t Rpad,
-                              int64_t Cpad, hipStream_t s, int slots = 1, int64_t src_slot = 0,
-                              int64_t dst_slot = 0) {
-  const dim3 grid(static_cast<unsigned>((Rpad + 63) / 64), static_cast<unsigned>((Cpad + 63) / 64),
-                  static_cast<unsigned>(slots));
-  const bool wide = C % 8 == 0 && ld % 8 == 0 && Rpad % 8 == 0 && src_slot % 8 == 0 && dst_slot % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
+                              int64_t Cpad, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((Rpad + 63) / 64), static_cast<unsigned>((Cpad + 63) / 64));
+  const bool wide = C % 8 == 0 && ld % 8 == 0 && Rpad % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(dst) % 16 == 0;
-  if (wide)
-    hipLaunchKernelGGL(transpose_pad16_kernel, grid, dim3(256), 0, s, src, ld, R, C, dst, Rpad, Cpad, src_slot,
-                       dst_slot);
-  else
-    hipLaunchKernelGGL(transpose_pad_kernel, grid, dim3(256), 0, s, src, ld, R, C, dst, Rpad, Cpad, src_slot,
-                       dst_slot);
+  if (wide) hipLaunchKernelGGL(transpose_pad16_kernel, grid, dim3(256), 0, s, src, ld, R, C, dst, Rpad, Cpad);
+  else hipLaunchKernelGGL(transpose_pad_kernel, grid, dim3(256), 0, s, src, ld, R, C, dst, Rpad, Cpad);
   return hipGetLastError();
 }
 
@@ -283,8 +293,19 @@ hipError_t transpose_pad(const uint16_t* src, int64_t ld, int64_t R, int64_t C, 
   return transpose_pad_impl(src, ld, R, C, dst, Rpad, Cpad, s);
 }
 
-hipError_t transpose_slots(const uint16_t* src, int slots, int64_t R, int64_t C, uint16_t* dst, hipStream_t s) {
-  return transpose_pad_impl(src, C, R, C, dst, R, C, s, slots, R * C, R * C);
+hipError_t transpose_stacks(const TransposeStack* stacks, int n, hipStream_t s) {
+  TransposeStacks a;
+  int64_t blocks = 0;
+  for (int i = 0; i < kTransposeStacks; ++i) {
+    a.s[i] = i < n ? stacks[i] : TransposeStack{nullptr, nullptr, 0, 0, 0};
+    a.first[i] = i < n ? blocks : (int64_t(1) << 62);
+    if (i < n) blocks += stacks[i].slots * ((stacks[i].R + 63) / 64) * ((stacks[i].C + 63) / 64);
+  }
+  a.first[kTransposeStacks] = blocks;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(transpose_stacks_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 // Token chunks of a contraction over T tokens with `tiles` workgroups per chunk: at most 512

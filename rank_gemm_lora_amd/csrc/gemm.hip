@@ -2148,11 +2148,13 @@ hipError_t launch(const LinearProblem& p, hipStream_t s) {
 // pool slot, once per adapter of the block, whose own tokens keep the result. Grid: (blocks, adapter rows,
 // adapter of the block x split).
 template <class DP>
-__global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDown p) {
+__global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDowns ps) {
   using P = DP;
   static_assert(P::BM == kRingBlock, "one ring tile per block of tokens");
   __shared__ __attribute__((aligned(1024))) char smem[P::S * P::STAGE_BYTES];
-  const int nth = blockIdx.z / p.splits, split = blockIdx.z - nth * p.splits;
+  const int job = static_cast<int>(blockIdx.z) >= ps.z0 ? 1 : 0, z = blockIdx.z - job * ps.z0;
+  const RoutedDown& p = ps.d[job];
+  const int nth = z / p.splits, split = z - nth * p.splits;
   const RingBlock* rb = p.ring + blockIdx.x;
   if (nth >= __builtin_amdgcn_readfirstlane(rb->n)) return;
   const int a = __builtin_amdgcn_readfirstlane(rb->id[nth]);  // (in a scalar register: the resources need it there)
@@ -2216,9 +2218,11 @@ __global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDown p) 
 }
 
 template <class DP>
-hipError_t launch_ring_cfg(const RoutedDown& p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.T + DP::BM - 1) / DP::BM), static_cast<unsigned>((p.ldt + DP::BN - 1) / DP::BN),
-                  static_cast<unsigned>(p.splits * kRingAdapters));
+hipError_t launch_ring_cfg(RoutedDowns p, hipStream_t s) {
+  p.z0 = p.d[0].splits * kRingAdapters;
+  const int z = p.z0 + (p.n > 1 ? p.d[1].splits * kRingAdapters : 0);
+  const dim3 grid(static_cast<unsigned>((p.d[0].T + DP::BM - 1) / DP::BM),
+                  static_cast<unsigned>((p.d[0].ldt + DP::BN - 1) / DP::BN), static_cast<unsigned>(z));
   hipLaunchKernelGGL((routed_ring_kernel<DP>), grid, dim3(DP::THREADS), 0, s, p);
   return hipGetLastError();
 }
@@ -2793,8 +2797,8 @@ hipError_t launch_bias32(const LinearProblem& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_routed_ring(const RoutedDown& p, hipStream_t s) {
-  return p.ldt <= pipe::down::DP64::BN ? pipe::down::launch_ring_cfg<pipe::down::DP64>(p, s)
+hipError_t launch_routed_ring(RoutedDowns p, hipStream_t s) {
+  return p.d[0].ldt <= pipe::down::DP64::BN ? pipe::down::launch_ring_cfg<pipe::down::DP64>(p, s)
                                        : pipe::down::launch_ring_cfg<pipe::down::DP128>(p, s);
 }
 

@@ -51,9 +51,12 @@ __global__ __launch_bounds__(64) void route_blocks_kernel(RoutedDown p) {
   if (lane == 0) p.ring[blockIdx.x] = b;
 }
 
-// t of the tokens whose sums are in n parts (the ring's splits, or parts without the ring), added in order and
+// t of the tokens whose sums are in parts (the ring's splits, or parts without the ring), added in order and
 // scaled. 32 threads a token and 64 ranks.
-__global__ __launch_bounds__(256) void down_join_kernel(RoutedDown p, int n) {
+__global__ __launch_bounds__(256) void down_join_kernel(RoutedDowns ps) {
+  const RoutedDown& p = ps.d[blockIdx.z];
+  const int n = p.splits > 0 ? p.splits : p.parts;
+  if (n <= 1) return;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (m >= p.T) return;
   const int64_t at = m * p.ldt + blockIdx.y * 64 + 2 * (threadIdx.x & 31);
@@ -126,9 +129,10 @@ struct SortedTokens {
   int key[kFewMaxT], id[kFewMaxT], token[kFewMaxT];
   float scale[kFewMaxT];
 };
-// order: the sorted tokens, of which `block` is one (null: blocks are of the tokens as they come).
+// order: the sorted tokens, of which `block` is one (null: blocks are of the tokens as they come). Adapters slot,
+// slot + slots, .. of the block; part `part` of K; tell: eid and blk are this workgroup's to write.
 __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f32x4 (&red)[kDownWaves][4][64],
-                                           const SortedTokens* order) {
+                                           const SortedTokens* order, int slot, int slots, int part, bool tell) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int64_t t0 = block * kRouteBlock;
@@ -144,15 +148,13 @@ __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f
     id = route(p.rt, token, p.T, s);
   }
   uint32_t todo = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(id >= 0)) & 0xffffu;
-  if (p.splits == 0 && wave == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+  if (tell && wave == 0) {
     const int first = __builtin_amdgcn_readfirstlane(id);
     if (q == 0 && r < rows) p.eid[token] = id;
     const bool same = __builtin_amdgcn_ballot_w64(r < rows && id != first) == 0;
     if (lane == 0) p.blk[block] = same ? first : -2;
   }
   const int q0 = blockIdx.y * 64;
-  const int slots = static_cast<int>(gridDim.z) / p.parts;
-  const int slot = static_cast<int>(blockIdx.z) % slots, part = static_cast<int>(blockIdx.z) / slots;
   const int shares = kDownWaves * p.parts;
   const int64_t kper = ((p.K + shares - 1) / shares + 31) / 32 * 32;
   const int64_t k_lo = (part * kDownWaves + wave) * kper, k_hi = min<int64_t>(p.K, k_lo + kper);
@@ -229,18 +231,23 @@ __device__ __forceinline__ void sort_tokens(const RoutedDown& p, SortedTokens& o
   __syncthreads();
 }
 
-__global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown p) {
+__global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDowns ps) {
   __shared__ f32x4 red[kDownWaves][4][64];
-  if (p.order != nullptr) {
-    __shared__ __attribute__((aligned(16))) SortedTokens sorted;
-    sort_tokens(p, sorted);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && static_cast<int>(threadIdx.x) < p.T)
-      p.order[threadIdx.x] = sorted.token[threadIdx.x], p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
-    down_block(p, blockIdx.x, red, &sorted);
-    return;
-  }
+  __shared__ __attribute__((aligned(16))) SortedTokens sorted;
+  const int job = static_cast<int>(blockIdx.z) >= ps.z0 ? 1 : 0, z = blockIdx.z - job * ps.z0;
+  const RoutedDown& p = ps.d[job];
   if (p.splits == 0) {
-    down_block(p, blockIdx.x, red, nullptr);
+    const int slots = ps.slots;
+    const bool tell = blockIdx.y == 0 && blockIdx.z == 0;
+    const bool sort = p.order != nullptr;
+    if (sort) {
+      sort_tokens(p, sorted);
+      if (blockIdx.x == 0 && tell && static_cast<int>(threadIdx.x) < p.T) {
+        p.order[threadIdx.x] = sorted.token[threadIdx.x];
+        p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
+      }
+    }
+    down_block(p, blockIdx.x, red, sort ? &sorted : nullptr, z % slots, slots, z / slots, tell);
     return;
   }
   // blocks blockIdx.x, + gridDim.x, ..: 64 at a time, one per lane (every wave the same)
@@ -251,7 +258,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown
     while (left != 0) {
       const int i = __builtin_ctzll(left);
       left &= left - 1;
-      down_block(p, base + i * static_cast<int64_t>(gridDim.x), red, nullptr);
+      down_block(p, base + i * static_cast<int64_t>(gridDim.x), red, nullptr, 0, 1, 0, false);
     }
   }
 }
@@ -648,29 +655,23 @@ __device__ __forceinline__ void transpose_to_lds(char* dst, const u32x4 (&v)[8],
   }
 }
 
-struct ContractArgs {
-  const bf16_bits* P; int64_t ldp, M;
-  const bf16_bits* q[3]; int64_t ldt;  // hi, mid, lo
-  int rank;
-  const int32_t* perm;
-  const RouteItem* items;
-  float *part, *out;
-};
-
-template <bool TRANSPOSE>
-__global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
+__global__ __launch_bounds__(256, 2) void routed_tn_kernel(RoutedContracts ps) {
   __shared__ __attribute__((aligned(256))) char pb[kRtI * kRtT * 2];
   __shared__ __attribute__((aligned(256))) char qb[3][kRtJ * kRtT * 2];
   __shared__ int32_t tok[kRouteMaxChunk];
-  const RouteItem it = p.items[blockIdx.y];
+  const int job = static_cast<int>(blockIdx.x) >= ps.tiles0 ? 1 : 0;
+  const RoutedContract& p = ps.c[job];
+  if (blockIdx.y >= p.table.n_items) return;
+  const RouteItem it = p.table.items[blockIdx.y];
   const int cnt = it.hi - it.lo;
   if (cnt <= 0) return;
+  const int rank = ps.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kRtI;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x - job * ps.tiles0) * kRtI;
   const int j0 = blockIdx.z * kRtJ;
-  const int nj = (min(kRtJ, p.rank - j0) + 15) / 16;
-  for (int i = threadIdx.x; i < cnt; i += 256) tok[i] = p.perm[it.lo + i];
+  const int nj = (min(kRtJ, rank - j0) + 15) / 16;
+  for (int i = threadIdx.x; i < cnt; i += 256) tok[i] = ps.perm[it.lo + i];
   __syncthreads();
   const int nsteps = (cnt + kRtT - 1) / kRtT;
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;  // P: columns i0 + 8 c .. +7, tokens 8 g .. +7 of the step
@@ -727,22 +728,22 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
     __syncthreads();
   }
   // lane (r, q) of block (ib, jb) holds D[i = 64 wave + 16 ib + 4 q + e][j = 16 jb + r]
-  float* dst = it.part < 0 ? p.out + static_cast<int64_t>(it.adapter) * p.M * p.rank
-                           : p.part + static_cast<int64_t>(it.part) * p.M * p.rank;
+  float* dst = it.part < 0 ? p.out + static_cast<int64_t>(it.adapter) * p.M * rank
+                           : p.part + static_cast<int64_t>(it.part) * p.M * rank;
   const bool quads = reinterpret_cast<uintptr_t>(dst) % 16 == 0;
 #pragma unroll
   for (int ib = 0; ib < 4; ++ib) {
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       const int j = j0 + jb * 16 + r;
-      if (j >= p.rank) continue;
+      if (j >= rank) continue;
       const int64_t i = i0 + wave * 64 + ib * 16 + 4 * q;
       if (i >= p.M) continue;  // (M is a multiple of 8: all four or none)
-      if (TRANSPOSE && quads) {
+      if (p.transpose && quads) {
         *reinterpret_cast<f32x4*>(dst + j * p.M + i) = acc[ib][jb];
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[TRANSPOSE ? j * p.M + i + e : (i + e) * p.rank + j] = acc[ib][jb][e];
+        for (int e = 0; e < 4; ++e) dst[p.transpose ? j * p.M + i + e : (i + e) * rank + j] = acc[ib][jb][e];
       }
     }
   }
@@ -750,22 +751,21 @@ __global__ __launch_bounds__(256, 2) void routed_tn_kernel(ContractArgs p) {
 
 // Gradients of adapters with several items: their partial sums in order. Adapters without tokens: zeros. Four
 // elements a thread.
-__global__ __launch_bounds__(256) void routed_reduce_kernel(const float* __restrict__ part, int64_t n,
-                                                            const int32_t* __restrict__ first,
-                                                            const RouteItem* __restrict__ items,
-                                                            float* __restrict__ out) {
+__global__ __launch_bounds__(256) void routed_reduce_kernel(RoutedContracts ps) {
+  const RoutedContract& p = ps.c[blockIdx.z];
+  const int64_t n = p.M * ps.rank;
   const int a = blockIdx.y;
-  const int lo = first[a], k = first[a + 1] - lo;
-  const RouteItem it = items[lo];
-  if (k == 1 && it.hi > it.lo) return;
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;  // (n is a multiple of 64)
   if (i >= n) return;
+  const int lo = p.table.first[a], k = p.table.first[a + 1] - lo;
+  const RouteItem it = p.table.items[lo];
+  if (k == 1 && it.hi > it.lo) return;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   if (k > 1) {
-    const float* src = part + it.part * n + i;
+    const float* src = p.part + it.part * n + i;
     for (int z = 0; z < k; ++z) v += *reinterpret_cast<const f32x4*>(src + z * n);
   }
-  float* dst = out + static_cast<int64_t>(a) * n + i;
+  float* dst = p.out + static_cast<int64_t>(a) * n + i;
   if (reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
     *reinterpret_cast<f32x4*>(dst) = v;
   } else {
@@ -776,35 +776,36 @@ __global__ __launch_bounds__(256) void routed_reduce_kernel(const float* __restr
 
 }  // namespace
 
-hipError_t launch_routed_down(const RoutedDown& p, hipStream_t s) {
-  if (p.T <= 0) return hipSuccess;
-  const unsigned blocks = static_cast<unsigned>((p.T + kRouteBlock - 1) / kRouteBlock);
-  const unsigned groups = static_cast<unsigned>((p.rt.rank + 63) / 64);
-  auto join = [&](int n) {
-    hipLaunchKernelGGL(down_join_kernel, dim3(static_cast<unsigned>((p.T + 7) / 8), groups), dim3(256), 0, s, p, n);
-    return hipGetLastError();
-  };
-  if (p.splits == 0) {
-    const unsigned z = static_cast<unsigned>(down_slots(p.T, p.rt.n_adapters) * p.parts);
-    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks, groups, z), dim3(64 * kDownWaves), 0, s, p);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess && p.parts > 1 ? join(p.parts) : e;
-  }
+hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
+  const RoutedDown& d = p.d[0];
+  if (d.T <= 0) return hipSuccess;
+  const unsigned blocks = static_cast<unsigned>((d.T + kRouteBlock - 1) / kRouteBlock);
+  const unsigned groups = static_cast<unsigned>((d.rt.rank + 63) / 64), jobs = static_cast<unsigned>(p.n);
+  bool join = false;
+  for (int i = 0; i < p.n; ++i) join = join || p.d[i].splits > 1 || (p.d[i].splits == 0 && p.d[i].parts > 1);
   hipError_t e = hipSuccess;
-  if (!p.routed) {
-    hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(p.T))), dim3(64), 0, s, p);
+  if (d.splits == 0) {
+    const int slots = down_slots(d.T, d.rt.n_adapters);
+    p.slots = slots;
+    p.z0 = slots * d.parts;
+    const int z = p.z0 + (p.n > 1 ? slots * p.d[1].parts : 0);
+    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks, groups, static_cast<unsigned>(z)), dim3(64 * kDownWaves), 0, s, p);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  } else {
+    hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(d.T))), dim3(64), 0, s, d);
+    e = hipGetLastError();
+    if (e == hipSuccess) e = launch_routed_ring(p, s);
   }
-  e = launch_routed_ring(p, s);
-  if (e != hipSuccess) return e;
-  if (p.splits > 1) {
-    e = join(p.splits);
-    if (e != hipSuccess) return e;
+  if (e == hipSuccess && join) {
+    hipLaunchKernelGGL(down_join_kernel, dim3(static_cast<unsigned>((d.T + 7) / 8), groups, jobs), dim3(256), 0, s, p);
+    e = hipGetLastError();
   }
-  if (p.rt.n_adapters > kRingAdapters)  // (a block of fewer adapters is always the ring's)
-    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks < 512 ? blocks : 512, groups, 1), dim3(64 * kDownWaves), 0, s, p);
-  return hipGetLastError();
+  if (e == hipSuccess && d.splits > 0 && d.rt.n_adapters > kRingAdapters) {  // (fewer adapters: always the ring's)
+    p.z0 = 1;
+    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks < 512 ? blocks : 512, groups, jobs), dim3(64 * kDownWaves), 0, s, p);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 namespace {
@@ -835,18 +836,22 @@ hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_routed_contract(const RoutedContract& p, hipStream_t s) {
-  const ContractArgs a{p.P, p.ldp, p.M, {p.hi, p.mid, p.lo}, p.ldt, p.rank, p.perm, p.table.items, p.part, p.out};
-  const dim3 grid(static_cast<unsigned>((p.M + kRtI - 1) / kRtI), static_cast<unsigned>(p.table.n_items),
-                  static_cast<unsigned>((p.rank + kRtJ - 1) / kRtJ));
-  if (p.transpose) hipLaunchKernelGGL(routed_tn_kernel<true>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(routed_tn_kernel<false>, grid, dim3(256), 0, s, a);
+hipError_t launch_routed_contract(RoutedContracts p, hipStream_t s) {
+  int64_t tiles = 0, items = 0, n = 0;
+  for (int i = 0; i < p.n; ++i) {
+    if (i == 1) p.tiles0 = static_cast<int>(tiles);
+    tiles += (p.c[i].M + kRtI - 1) / kRtI;
+    items = p.c[i].table.n_items > items ? p.c[i].table.n_items : items;
+    n = p.c[i].M * p.rank > n ? p.c[i].M * p.rank : n;
+  }
+  if (p.n == 1) p.tiles0 = static_cast<int>(tiles);
+  hipLaunchKernelGGL(routed_tn_kernel, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(items),
+                                            static_cast<unsigned>((p.rank + kRtJ - 1) / kRtJ)), dim3(256), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t n = p.M * p.rank;
-  hipLaunchKernelGGL(routed_reduce_kernel,
-                     dim3(static_cast<unsigned>((n / 4 + 255) / 256), static_cast<unsigned>(p.n_adapters)),
-                     dim3(256), 0, s, p.part, n, p.table.first, p.table.items, p.out);
+  hipLaunchKernelGGL(routed_reduce_kernel, dim3(static_cast<unsigned>((n / 4 + 255) / 256),
+                                                static_cast<unsigned>(p.n_adapters), static_cast<unsigned>(p.n)),
+                     dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

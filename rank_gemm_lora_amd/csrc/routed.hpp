@@ -29,7 +29,6 @@ struct RoutedDown {
   int splits, ks;      // of the ring (0: not used)
   int parts;           // without the ring: workgroups that share K (1: none)
   RingBlock* ring;     // [ceil(T / 128)]
-  bool routed;         // eid, blk and ring are there already, from a call with the same routing
   float* tpart;        // splits > 1, parts > 1: partial sums [splits or parts, T, ldt]
   int32_t* order;      // not null (T <= kFewMaxT): the tokens sorted by adapter go there, [2, T]: the token of
                        // each place, then its adapter; in token order within one adapter, those without an
@@ -84,8 +83,14 @@ inline size_t down_bytes(int64_t T, int64_t K, int64_t rank, int n_adapters) {
   const int s = down_parts(T, K, rank, n_adapters);
   return s > 1 ? static_cast<size_t>(s) * static_cast<size_t>(T) * static_cast<size_t>(rank_pad(rank)) * 4 : 0;
 }
-hipError_t launch_routed_ring(const RoutedDown& p, hipStream_t s);  // (gemm.hip)
-hipError_t launch_routed_down(const RoutedDown& p, hipStream_t s);
+// One product, or two of the same tokens and routing (x against A, dy against B^T) in the same launches. z0:
+// the first's share of the grid's z; slots: workgroups that share a block's adapters without the ring.
+struct RoutedDowns {
+  RoutedDown d[2];
+  int n, z0, slots;
+};
+hipError_t launch_routed_ring(RoutedDowns p, hipStream_t s);  // (gemm.hip)
+hipError_t launch_routed_down(RoutedDowns p, hipStream_t s);
 
 constexpr int kDownWaves = 8;
 // Few tokens: base product, adapters and bias in one kernel over a ring of LDS stages (t~ from the
@@ -168,18 +173,21 @@ inline int32_t route_chunk(int64_t T, int64_t tiles) {
 }
 
 // out[a] = sum over a's tokens of P[t] (x) (hi + mid + lo)[t]: [M, rank] row-major, or [rank, M] with
-// transpose. Adapters without tokens get zeros.
+// transpose. Adapters without tokens get zeros. One contraction, or two of the same pool in the same launches.
 struct RoutedContract {
   const uint16_t* P; int64_t ldp, M;
-  const uint16_t *hi, *mid, *lo; int64_t ldt;
-  int32_t rank;
-  const int32_t* perm;
+  const uint16_t* q[3]; int64_t ldt;  // hi, mid, lo
   RouteTable table;
-  int32_t n_adapters;
   float* part;         // [route_parts, M, rank]
   float* out;
   bool transpose;
 };
-hipError_t launch_routed_contract(const RoutedContract& p, hipStream_t s);
+struct RoutedContracts {
+  RoutedContract c[2];
+  int n, tiles0;       // tiles0: the first's share of the grid's x
+  int32_t rank, n_adapters;
+  const int32_t* perm;
+};
+hipError_t launch_routed_contract(RoutedContracts p, hipStream_t s);
 
 }  // namespace lora

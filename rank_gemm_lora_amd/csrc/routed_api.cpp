@@ -65,8 +65,8 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
 }
 
 struct BwdLayout {
-  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, tpart = 0, eid = 0, blk = 0, ring = 0, perm = 0,
-         part = 0, few = 0, order = 0, total = 0;
+  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, upart = 0, tpart = 0, eid = 0, blk = 0, ring = 0, perm = 0,
+         part[2] = {0, 0}, few = 0, order = 0, total = 0;
   struct {
     size_t first = 0, items = 0;
     int32_t chunk = 0;
@@ -87,13 +87,13 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   const size_t tb = static_cast<size_t>(T) * rp * 2;
   for (size_t& o : L.u) o = take(tb);
   for (size_t& o : L.t) o = take(tb);
-  L.tpart = take(std::max(join_bytes(T, N, n, R), join_bytes(T, K, n, R)));
+  L.upart = take(join_bytes(T, N, n, R));
+  L.tpart = take(join_bytes(T, K, n, R));
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
   L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
   L.perm = take(static_cast<size_t>(T) * 4);
-  size_t part = 0;
   for (int h = 0; h < 2; ++h) {
     auto& tb = L.table[h];
     const int64_t M = h == 0 ? K : N;
@@ -101,9 +101,8 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
     tb.n_items = lora::route_items(T, n, tb.chunk);
     tb.first = take(static_cast<size_t>(n + 1) * 4);
     tb.items = take(static_cast<size_t>(tb.n_items) * sizeof(lora::RouteItem));
-    part = std::max(part, static_cast<size_t>(lora::route_parts(T, tb.chunk)) * M * R * 4);
+    L.part[h] = take(static_cast<size_t>(lora::route_parts(T, tb.chunk)) * M * R * 4);
   }
-  L.part = take(part);
   L.total = take.off;
   return L;
 }
@@ -225,7 +224,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   plan_down(d);
   d.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
   d.tpart = reinterpret_cast<float*>(ws + L.part);
-  if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
+  if (lora::launch_routed_down(lora::RoutedDowns{{d, d}, 1, 0, 0}, s) != hipSuccess) return LORA_ERR_HIP;
   return launch_product(x, T, K, ldx, W, N, bias, y, ldy, d, pool->B, pool, ws + L.few, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
@@ -280,59 +279,59 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   auto at16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
   auto at32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
   const int64_t rp = lora::rank_pad(R);
-  hipError_t e = hipSuccess;
   // the forward's operand layouts for the input dy: B^T [R, N] and A^T [K, R] of every slot, W^T [K, N]
-  if (n > 0) e = lora::transpose_slots(static_cast<const uint16_t*>(pool->B), static_cast<int>(n), N, R, at16(L.bt), s);
-  if (e == hipSuccess && dx != nullptr) {
-    if (n > 0) e = lora::transpose_slots(static_cast<const uint16_t*>(pool->A), static_cast<int>(n), R, K, at16(L.at), s);
-    if (e == hipSuccess) e = lora::transpose_slots(static_cast<const uint16_t*>(W), 1, N, K, at16(L.wt), s);
-  }
-  if (e != hipSuccess) return LORA_ERR_HIP;
-  lora::RoutedDown d;
-  std::memset(&d, 0, sizeof(d));
-  d.x = static_cast<const uint16_t*>(dy); d.ldx = lddy; d.T = T; d.K = N;
-  d.A = at16(L.bt);
-  d.rt = routing(pool, token_adapter, token_scale);
-  d.hi = at16(L.u[0]); d.mid = at16(L.u[1]); d.lo = at16(L.u[2]); d.ldt = rp;
-  d.eid = at32(L.eid); d.blk = at32(L.blk);
-  if (T <= lora::kFewMaxT) d.order = at32(L.order);
-  plan_down(d);
-  d.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
-  d.tpart = reinterpret_cast<float*>(ws + L.tpart);
-  if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
+  lora::TransposeStack stacks[3];
+  int n_stacks = 0;
+  if (n > 0 && (dx != nullptr || dA != nullptr))
+    stacks[n_stacks++] = lora::TransposeStack{static_cast<const uint16_t*>(pool->B), at16(L.bt), N, R, n};
+  if (n > 0 && dx != nullptr)
+    stacks[n_stacks++] = lora::TransposeStack{static_cast<const uint16_t*>(pool->A), at16(L.at), R, K, n};
+  if (dx != nullptr) stacks[n_stacks++] = lora::TransposeStack{static_cast<const uint16_t*>(W), at16(L.wt), N, K, 1};
+  if (lora::transpose_stacks(stacks, n_stacks, s) != hipSuccess) return LORA_ERR_HIP;
+  // u over dy and B^T, t over x and A
+  lora::RoutedDown du, dt;
+  std::memset(&du, 0, sizeof(du));
+  du.T = T;
+  du.rt = routing(pool, token_adapter, token_scale);
+  du.ldt = rp;
+  du.eid = at32(L.eid); du.blk = at32(L.blk);
+  if (T <= lora::kFewMaxT) du.order = at32(L.order);
+  du.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
+  dt = du;
+  du.x = static_cast<const uint16_t*>(dy); du.ldx = lddy; du.K = N;
+  du.A = at16(L.bt);
+  du.hi = at16(L.u[0]); du.mid = at16(L.u[1]); du.lo = at16(L.u[2]);
+  du.tpart = reinterpret_cast<float*>(ws + L.upart);
+  dt.x = static_cast<const uint16_t*>(x); dt.ldx = ldx; dt.K = K;
+  dt.A = static_cast<const uint16_t*>(pool->A);
+  dt.hi = at16(L.t[0]); dt.mid = at16(L.t[1]); dt.lo = at16(L.t[2]);
+  dt.tpart = reinterpret_cast<float*>(ws + L.tpart);
+  plan_down(du);
+  plan_down(dt);
+  const bool want_u = dx != nullptr || dA != nullptr, want_t = dB != nullptr && n > 0;
+  lora::RoutedDowns downs{{want_u ? du : dt, dt}, want_u && want_t ? 2 : 1, 0, 0};
+  if (lora::launch_routed_down(downs, s) != hipSuccess) return LORA_ERR_HIP;
   if (dx != nullptr) {
-    if (launch_product(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, d, at16(L.at), pool, ws + L.few, s) != hipSuccess)
+    if (launch_product(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, du, at16(L.at), pool, ws + L.few, s) != hipSuccess)
       return LORA_ERR_HIP;
   }
   if (!grads) return LORA_OK;
   lora::RoutePlan plan;
-  plan.eid = d.eid; plan.T = T; plan.n_adapters = static_cast<int32_t>(n); plan.perm = at32(L.perm);
+  plan.eid = du.eid; plan.T = T; plan.n_adapters = static_cast<int32_t>(n); plan.perm = at32(L.perm);
   for (int h = 0; h < 2; ++h)
     plan.table[h] = lora::RouteTable{L.table[h].chunk, at32(L.table[h].first),
                                      reinterpret_cast<lora::RouteItem*>(ws + L.table[h].items), L.table[h].n_items};
   if (lora::launch_route_plan(plan, s) != hipSuccess) return LORA_ERR_HIP;
-  lora::RoutedContract c;
-  c.ldt = rp; c.rank = static_cast<int32_t>(R); c.perm = plan.perm; c.n_adapters = plan.n_adapters;
-  c.part = reinterpret_cast<float*>(ws + L.part);
-  if (dB != nullptr) {
-    d.x = static_cast<const uint16_t*>(x); d.ldx = ldx; d.K = K;
-    d.A = static_cast<const uint16_t*>(pool->A);
-    d.hi = at16(L.t[0]); d.mid = at16(L.t[1]); d.lo = at16(L.t[2]);
-    plan_down(d);
-    d.routed = true;
-    if (lora::launch_routed_down(d, s) != hipSuccess) return LORA_ERR_HIP;
-    c.P = static_cast<const uint16_t*>(dy); c.ldp = lddy; c.M = N;
-    c.hi = d.hi; c.mid = d.mid; c.lo = d.lo; c.out = dB; c.transpose = false;
-    c.table = plan.table[1];
-    if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
-  }
-  if (dA != nullptr) {
-    c.P = static_cast<const uint16_t*>(x); c.ldp = ldx; c.M = K;
-    c.hi = at16(L.u[0]); c.mid = at16(L.u[1]); c.lo = at16(L.u[2]); c.out = dA; c.transpose = true;
-    c.table = plan.table[0];
-    if (lora::launch_routed_contract(c, s) != hipSuccess) return LORA_ERR_HIP;
-  }
-  return LORA_OK;
+  lora::RoutedContracts c;
+  std::memset(&c, 0, sizeof(c));
+  c.rank = static_cast<int32_t>(R); c.n_adapters = plan.n_adapters; c.perm = plan.perm;
+  if (dA != nullptr)
+    c.c[c.n++] = lora::RoutedContract{static_cast<const uint16_t*>(x), ldx, K, {du.hi, du.mid, du.lo}, rp, plan.table[0],
+                                      reinterpret_cast<float*>(ws + L.part[0]), dA, true};
+  if (dB != nullptr)
+    c.c[c.n++] = lora::RoutedContract{static_cast<const uint16_t*>(dy), lddy, N, {dt.hi, dt.mid, dt.lo}, rp, plan.table[1],
+                                      reinterpret_cast<float*>(ws + L.part[1]), dB, false};
+  return lora::launch_routed_contract(c, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
 size_t lora_linear_routed_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank,
