@@ -264,7 +264,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: y = RN(x.W^T + t~.B^T + b). Workgroup: 64 outputs x BM tokens, one of S parts of K; 4 waves.
+// Few tokens: y = RN(x.W^T + t~.B^T + b). Workgroup: 64 outputs x BM tokens, one of S parts of K; 4 waves, 8
+// from 64 tokens on (64 tokens of 64 adapters, 4096 -> 14336: 56 against 60 us a call).
 // Stages of 64 k (128 bytes of every row of x and W) go through a ring of D LDS slots filled by
 // buffer_load .. lds, D - 1 of them in flight; 16-byte chunk c of row r lies at c ^ ((r / 2) % 8), so that a
 // wave's 16-byte reads spread over the banks. (A first form fed the MFMAs straight from memory: 16 rows of
@@ -278,13 +279,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDown
 // and drop an XCD's L2 every time. 1 token, 4096 -> 14336: 98 us against 31 with the second launch.)
 constexpr int kFewN = 64, kFewRow = 128;
 
-template <int BM>
+template <int BM, int WAVES>
 struct FewCfg {
   static constexpr int XR = BM < 32 ? 32 : BM;  // staged rows of x (one copy instruction a wave at least)
-  static constexpr int WAVES_M = BM >= 64 ? 2 : 1, WAVES_N = 4 / WAVES_M;
+  static constexpr int WAVES_M = (BM >= 64 ? 2 : 1) * WAVES / 4, WAVES_N = WAVES / WAVES_M;
   static constexpr int TB = BM / WAVES_M / 16, NB = kFewN / WAVES_N / 16;  // 16 x 16 blocks of a wave
   static constexpr int STAGE = (XR + kFewN) * kFewRow;
-  static constexpr int LPS = (XR + kFewN) / 8 / 4;  // copy instructions of a wave and stage (8 rows each)
+  static constexpr int LPS = (XR + kFewN) / 8 / WAVES;  // copy instructions of a wave and stage (8 rows each)
   static constexpr int DELTA_SLOTS = (BM * kFewN * 4 + STAGE - 1) / STAGE;
 };
 
@@ -373,9 +374,9 @@ __device__ __forceinline__ void few_adapters(const RoutedFew& p, char* delta, co
   }
 }
 
-template <int BM, int D>
-__global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt, int S, int per) {
-  using C = FewCfg<BM>;
+template <int BM, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, int tt, int S, int per) {
+  using C = FewCfg<BM, WAVES>;
   constexpr int TB = C::TB, NB = C::NB;
   // (one LDS object: with several the compiler waits for every copy in flight before each LDS read, a memory
   // latency a stage. 1 token, 4096 -> 14336, no adapter: 42 us a call, 31 without)
@@ -403,18 +404,19 @@ __global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt,
   // (tiles start their K loops apart where x stays in an XCD's L2: in step they read the same few memory
   // channels at a time when the weight's rows are a power of two apart)
   const int rot = p.T * p.K <= (1 << 19) ? 5 * tile % ns : 0;
+  const bool sorted = BM > 16 && p.order != nullptr;  // (up to 16 tokens the order is the tokens')
   // this lane's part of each copy instruction (8 rows, x first, then W): its chunk's byte offset in part
   // `split` at stage 0; rows past the tile's are out of the resource's range and read as zeros
   uint32_t from[C::LPS];
   int cb[C::LPS];
 #pragma unroll
   for (int it = 0; it < C::LPS; ++it) {
-    const int group = it * 4 + wave;
+    const int group = it * WAVES + wave;
     const bool is_w = group >= C::XR / 8;
     const int row = (is_w ? group - C::XR / 8 : group) * 8 + (lane >> 3);
     cb[it] = kb_lo + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
     if (is_w) from[it] = row < rows_n ? static_cast<uint32_t>(row) * ldw_b : kOutOfRange;
-    else if (BM == 16) from[it] = row < rows_m ? static_cast<uint32_t>(row) * ldx_b : kOutOfRange;  // (order is the tokens')
+    else if (!sorted) from[it] = row < rows_m ? static_cast<uint32_t>(m0 + row) * ldx_b : kOutOfRange;
     else from[it] = row < rows_m ? static_cast<uint32_t>(p.order[m0 + row]) * ldx_b : kOutOfRange;
   }
   auto issue = [&](int st) {
@@ -423,7 +425,7 @@ __global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt,
     const int kb = st < ns ? at * kFewRow : 1 << 30;  // (past the last: nothing)
 #pragma unroll
     for (int it = 0; it < C::LPS; ++it) {
-      const int group = it * 4 + wave;
+      const int group = it * WAVES + wave;
       const bool is_w = group >= C::XR / 8;
       const uint32_t off = cb[it] + kb < kb_hi ? from[it] + static_cast<uint32_t>(cb[it] + kb) : kOutOfRange;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(is_w ? wr : xr, (lds_void*)(dst + group * 1024), 16, off, 0, 0, 0);
@@ -433,22 +435,19 @@ __global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt,
   for (int st = 0; st < D - C::DELTA_SLOTS; ++st) issue(st);
 
   if (tid < BM) {
-    tok[tid] = tid < rows_m ? p.order[m0 + tid] : 0;
-    ids[tid] = tid < rows_m ? p.order[p.T + m0 + tid] : -1;
+    tok[tid] = tid >= rows_m ? 0 : (sorted ? p.order[m0 + tid] : static_cast<int>(m0) + tid);
+    ids[tid] = tid >= rows_m ? -1 : (sorted ? p.order[p.T + m0 + tid] : p.rt.eid[m0 + tid]);
   }
-  for (int i = tid; i < BM * kFewN / 4; i += 256) reinterpret_cast<f32x4*>(delta)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = tid; i < BM * kFewN / 4; i += 64 * WAVES) reinterpret_cast<f32x4*>(delta)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   lds_barrier();
-  // units: rows in adapter order, so a unit starts where the adapter or the block of 16 changes (16 rows in
-  // token order: where an adapter shows first)
+  // units: where an adapter shows first in a block of 16 (in adapter order: where it changes)
   if (wave == 0) {
     int n = 0;
 #pragma unroll
     for (int h = 0; h < (BM + 63) / 64; ++h) {
       const int i = 64 * h + lane;
-      bool start = i < BM && ids[i] >= 0 && (i % 16 == 0 || ids[i] != ids[i - 1]);
-      if constexpr (BM == 16) {
-        for (int e = 0; e + 1 < BM; ++e) start = start && !(e < i && ids[e] == ids[i]);
-      }
+      bool start = i < BM && ids[i] >= 0;
+      for (int e = 1; e < (sorted ? 2 : 16); ++e) start = start && !(i % 16 >= e && ids[max(i - e, 0)] == ids[i]);
       const uint64_t m = __builtin_amdgcn_ballot_w64(start);
       if (start) {
         const int rank = p.rt.ranks != nullptr ? (min(p.rt.ranks[ids[i]], p.rt.rank) + 7) & ~7 : p.rt.rank;
@@ -460,7 +459,7 @@ __global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt,
   }
   lds_barrier();
   const int nu = __builtin_amdgcn_readfirstlane(*n_units);
-  few_adapters(p, delta, ids, tok, units, nu, n0, rows_n, split * 4 + wave, 4 * S);
+  few_adapters(p, delta, ids, tok, units, nu, n0, rows_n, split * WAVES + wave, WAVES * S);
 
   // lane (r, q) of block (i, j): outputs wn0 + 16 i + 4 q .. +3 of token wm0 + 16 j + r
   const int wm0 = (wave % C::WAVES_M) * (TB * 16), wn0 = (wave / C::WAVES_M) * (NB * 16);
@@ -515,9 +514,9 @@ __global__ __launch_bounds__(256, 2) void routed_few_kernel(RoutedFew p, int tt,
 }
 
 // The parts of a tile added in order. Workgroup: one tile's 16 x 16 block per wave.
-template <int BM>
+template <int BM, int WAVES>
 __global__ __launch_bounds__(256) void few_finish_kernel(RoutedFew p, int tt, int S) {
-  using C = FewCfg<BM>;
+  using C = FewCfg<BM, WAVES>;
   const int lane = threadIdx.x & 63;
   const int b = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // block of the tile
   const int tile = blockIdx.x, tile_n = tile / tt, tile_m = tile - tile_n * tt;
@@ -538,7 +537,8 @@ __global__ __launch_bounds__(256) void few_finish_kernel(RoutedFew p, int tt, in
   const int wave = b / (C::NB * C::TB), i = b % (C::NB * C::TB) / C::TB, j = b % C::TB;
   const int wm0 = (wave % C::WAVES_M) * (C::TB * 16), wn0 = (wave / C::WAVES_M) * (C::NB * 16);
   const int row = wm0 + 16 * j + (lane & 15);
-  if (row < rows_m) few_store(p, v, p.order[m0 + row], n0, rows_n, wn0 + 16 * i + 4 * (lane >> 4));
+  if (row < rows_m)
+    few_store(p, v, p.order != nullptr ? p.order[m0 + row] : m0 + row, n0, rows_n, wn0 + 16 * i + 4 * (lane >> 4));
 }
 
 // ---------------------------------------------------------------------------
@@ -809,12 +809,12 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
 }
 
 namespace {
-template <int BM, int D>
+template <int BM, int D, int WAVES>
 hipError_t few(const RoutedFew& p, const FewPlan& f, hipStream_t s) {
-  hipLaunchKernelGGL((routed_few_kernel<BM, D>), dim3(static_cast<unsigned>(f.tiles * f.splits)), dim3(256), 0, s, p,
+  hipLaunchKernelGGL((routed_few_kernel<BM, D, WAVES>), dim3(static_cast<unsigned>(f.tiles * f.splits)), dim3(64 * WAVES), 0, s, p,
                      f.token_tiles, f.splits, f.stages);
   if (f.splits > 1)
-    hipLaunchKernelGGL((few_finish_kernel<BM>), dim3(static_cast<unsigned>(f.tiles), BM * kFewN / 1024), dim3(256), 0, s,
+    hipLaunchKernelGGL((few_finish_kernel<BM, WAVES>), dim3(static_cast<unsigned>(f.tiles), BM * kFewN / 1024), dim3(256), 0, s,
                        p, f.token_tiles, f.splits);
   return hipGetLastError();
 }
@@ -823,10 +823,10 @@ hipError_t few(const RoutedFew& p, const FewPlan& f, hipStream_t s) {
 hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s) {
   const FewPlan f = few_plan(p.T, p.K, p.N);
   switch (f.bm) {
-    case 16: return few<16, 6>(p, f, s);
-    case 32: return few<32, 6>(p, f, s);
-    case 64: return few<64, 4>(p, f, s);
-    default: return few<128, 3>(p, f, s);
+    case 16: return few<16, 6, 4>(p, f, s);
+    case 32: return few<32, 6, 4>(p, f, s);
+    case 64: return few<64, 4, 8>(p, f, s);
+    default: return few<128, 3, 8>(p, f, s);
   }
 }
 

@@ -98,6 +98,11 @@ constexpr int kDownWaves = 8;
 // Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
 // 4096 -> 14336: 68 against 76 us), with mixed ones it is slower up to there and beyond (121 against 86 us).
 constexpr int64_t kFewMaxT = 256;
+// Beyond it, up to 1024 tokens, the few-token kernel still takes outputs so narrow that the hot GEMM's 128 x 128
+// tiles would leave half of the compute units without one (tokens as they come, not sorted).
+inline bool few_path(int64_t T, int64_t N) {
+  return T <= kFewMaxT || (T < kRingMinT && (T + 127) / 128 * ((N + 127) / 128) <= 128);
+}
 struct FewPlan {
   int bm;            // tokens of a tile
   int token_tiles;
@@ -132,7 +137,7 @@ struct RoutedFew {
   int64_t T, K, N;
   const uint16_t *hi, *mid; int64_t ldt;
   RoutedGemm rt;
-  const int32_t* order;  // [2, T]: the producer's
+  const int32_t* order;  // [2, T]: the producer's, null above kFewMaxT
   float* part;           // [tiles, splits, bm, 64]
 };
 hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s);

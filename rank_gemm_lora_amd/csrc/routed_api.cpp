@@ -32,7 +32,7 @@ struct Take {  // regions of a workspace, each 256-byte aligned
 
 // Partial sums of the few-token kernel for T tokens, K inputs and N outputs.
 size_t few_bytes(int64_t T, int64_t K, int64_t N) {
-  return T <= lora::kFewMaxT ? lora::few_part_bytes(lora::few_plan(T, K, N)) : 0;
+  return lora::few_path(T, N) ? lora::few_part_bytes(lora::few_plan(T, K, N)) : 0;
 }
 
 // Partial sums of the rank-wide producer for T tokens and K inputs.
@@ -54,7 +54,7 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   const int64_t rp = lora::rank_pad(R);
   Take take;
   L.few = take(few_bytes(T, K, N));
-  for (int i = 0; i < (T <= lora::kFewMaxT ? 3 : 1); ++i) L.t[i] = take(static_cast<size_t>(T) * rp * 2);
+  for (int i = 0; i < (lora::few_path(T, N) ? 3 : 1); ++i) L.t[i] = take(static_cast<size_t>(T) * rp * 2);
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
@@ -156,7 +156,7 @@ hipError_t launch_product(const void* x, int64_t T, int64_t K, int64_t ldx, cons
                           void* part, hipStream_t s) {
   lora::RoutedGemm rt;
   rt.B = B; rt.eid = d.eid; rt.blk = d.blk; rt.ranks = pool->ranks; rt.rank = pool->rank;
-  if (T <= lora::kFewMaxT) {
+  if (lora::few_path(T, N)) {
     lora::RoutedFew f;
     f.x = static_cast<const uint16_t*>(x); f.ldx = ldx;
     f.W = static_cast<const uint16_t*>(W);
@@ -216,7 +216,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   d.A = static_cast<const uint16_t*>(pool->A);
   d.rt = routing(pool, token_adapter, token_scale);
   d.hi = reinterpret_cast<uint16_t*>(ws + L.t[0]); d.ldt = lora::rank_pad(pool->rank);
-  const bool few = T <= lora::kFewMaxT;
+  const bool few = lora::few_path(T, N);
   if (T <= lora::kFewMaxT) d.order = reinterpret_cast<int32_t*>(ws + L.order);
   if (few) d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]), d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
