@@ -123,8 +123,8 @@ __device__ __forceinline__ void down_product(f32x4 (&acc)[4], __amdgpu_buffer_rs
   }
 }
 
-// Up to 256 tokens: adapter, scale and token of each place of the order by adapter (a token's place is
-// the number of tokens before it; with one block the order does not matter and is the tokens' own).
+// Up to 256 tokens: adapter, scale and token of each place of the order by adapter (a token's place is the
+// number of tokens before it).
 struct SortedTokens {
   int key[kFewMaxT], id[kFewMaxT], token[kFewMaxT];
   float scale[kFewMaxT];
@@ -205,24 +205,21 @@ __device__ __forceinline__ void sort_tokens(const RoutedDown& p, SortedTokens& o
   const int t = threadIdx.x % kFewMaxT, half = threadIdx.x / kFewMaxT, T = static_cast<int>(p.T);
   float s;
   const uint32_t key = static_cast<uint32_t>(route(p.rt, t, p.T, s));  // (-1, no adapter: last)
-  int place = t;
-  if (T > kRouteBlock) {
-    if (half == 0) o.key[t] = static_cast<int>(key);
-    __syncthreads();
-    // this thread's half of the tokens before t (entries past T hold the last key and come after every token)
-    const int mid = (T + 7) / 8 * 4;
-    place = 0;
+  if (half == 0) o.key[t] = static_cast<int>(key);
+  __syncthreads();
+  // this thread's half of the tokens before t (entries past T hold the last key and come after every token)
+  const int mid = (T + 7) / 8 * 4;
+  int place = 0;
 #pragma unroll 4
-    for (int u = half * mid; u < (half == 0 ? mid : T); u += 4) {
-      const uint4 k = *reinterpret_cast<const uint4*>(o.key + u);
-      place += (k.x < key || (k.x == key && u < t)) + (k.y < key || (k.y == key && u + 1 < t)) +
-               (k.z < key || (k.z == key && u + 2 < t)) + (k.w < key || (k.w == key && u + 3 < t));
-    }
-    if (half == 1) o.id[t] = place;
-    __syncthreads();
-    if (half == 0) place += o.id[t];
-    __syncthreads();
+  for (int u = half * mid; u < (half == 0 ? mid : T); u += 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(o.key + u);
+    place += (k.x < key || (k.x == key && u < t)) + (k.y < key || (k.y == key && u + 1 < t)) +
+             (k.z < key || (k.z == key && u + 2 < t)) + (k.w < key || (k.w == key && u + 3 < t));
   }
+  if (half == 1) o.id[t] = place;
+  __syncthreads();
+  if (half == 0) place += o.id[t];
+  __syncthreads();
   if (half == 0 && t < T) {
     o.id[place] = static_cast<int>(key);
     o.token[place] = t;
@@ -231,34 +228,38 @@ __device__ __forceinline__ void sort_tokens(const RoutedDown& p, SortedTokens& o
   __syncthreads();
 }
 
+enum { kDownPlain = 0, kDownSorted = 1, kDownBeside = 2 };  // blocks as they come, sorted, those the ring left
+
+template <int MODE>
 __global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDowns ps) {
   __shared__ f32x4 red[kDownWaves][4][64];
-  __shared__ __attribute__((aligned(16))) SortedTokens sorted;
   const int job = static_cast<int>(blockIdx.z) >= ps.z0 ? 1 : 0, z = blockIdx.z - job * ps.z0;
   const RoutedDown& p = ps.d[job];
-  if (p.splits == 0) {
-    const int slots = ps.slots;
+  if constexpr (MODE == kDownBeside) {
+    // blocks blockIdx.x, + gridDim.x, ..: 64 at a time, one per lane (every wave the same)
+    const int64_t n = (p.T + kRouteBlock - 1) / kRouteBlock;
+    for (int64_t base = blockIdx.x; base < n; base += 64 * static_cast<int64_t>(gridDim.x)) {
+      const int64_t mine = base + (threadIdx.x & 63) * static_cast<int64_t>(gridDim.x);
+      uint64_t left = __builtin_amdgcn_ballot_w64(mine < n && p.ring[mine * kRouteBlock / kRingBlock].n < 0);
+      while (left != 0) {
+        const int i = __builtin_ctzll(left);
+        left &= left - 1;
+        down_block(p, base + i * static_cast<int64_t>(gridDim.x), red, nullptr, 0, 1, 0, false);
+      }
+    }
+  } else {
     const bool tell = blockIdx.y == 0 && blockIdx.z == 0;
-    const bool sort = p.order != nullptr;
-    if (sort) {
+    const int slot = z % ps.slots, part = z / ps.slots;
+    if constexpr (MODE == kDownSorted) {
+      __shared__ __attribute__((aligned(16))) SortedTokens sorted;
       sort_tokens(p, sorted);
       if (blockIdx.x == 0 && tell && static_cast<int>(threadIdx.x) < p.T) {
         p.order[threadIdx.x] = sorted.token[threadIdx.x];
         p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
       }
-    }
-    down_block(p, blockIdx.x, red, sort ? &sorted : nullptr, z % slots, slots, z / slots, tell);
-    return;
-  }
-  // blocks blockIdx.x, + gridDim.x, ..: 64 at a time, one per lane (every wave the same)
-  const int64_t n = (p.T + kRouteBlock - 1) / kRouteBlock;
-  for (int64_t base = blockIdx.x; base < n; base += 64 * static_cast<int64_t>(gridDim.x)) {
-    const int64_t mine = base + (threadIdx.x & 63) * static_cast<int64_t>(gridDim.x);
-    uint64_t left = __builtin_amdgcn_ballot_w64(mine < n && p.ring[mine * kRouteBlock / kRingBlock].n < 0);
-    while (left != 0) {
-      const int i = __builtin_ctzll(left);
-      left &= left - 1;
-      down_block(p, base + i * static_cast<int64_t>(gridDim.x), red, nullptr, 0, 1, 0, false);
+      down_block(p, blockIdx.x, red, &sorted, slot, ps.slots, part, tell);
+    } else {
+      down_block(p, blockIdx.x, red, nullptr, slot, ps.slots, part, tell);
     }
   }
 }
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, 
   // (tiles start their K loops apart where x stays in an XCD's L2: in step they read the same few memory
   // channels at a time when the weight's rows are a power of two apart)
   const int rot = p.T * p.K <= (1 << 19) ? 5 * tile % ns : 0;
-  const bool sorted = BM > 16 && p.order != nullptr;  // (up to 16 tokens the order is the tokens')
+  const bool sorted = BM > 16 && p.order != nullptr;
   // this lane's part of each copy instruction (8 rows, x first, then W): its chunk's byte offset in part
   // `split` at stage 0; rows past the tile's are out of the resource's range and read as zeros
   uint32_t from[C::LPS];
@@ -789,7 +790,9 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
     p.slots = slots;
     p.z0 = slots * d.parts;
     const int z = p.z0 + (p.n > 1 ? slots * p.d[1].parts : 0);
-    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks, groups, static_cast<unsigned>(z)), dim3(64 * kDownWaves), 0, s, p);
+    const dim3 grid(blocks, groups, static_cast<unsigned>(z));
+    if (d.order != nullptr) hipLaunchKernelGGL(routed_down_kernel<kDownSorted>, grid, dim3(64 * kDownWaves), 0, s, p);
+    else hipLaunchKernelGGL(routed_down_kernel<kDownPlain>, grid, dim3(64 * kDownWaves), 0, s, p);
     e = hipGetLastError();
   } else {
     hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(d.T))), dim3(64), 0, s, d);
@@ -802,7 +805,8 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
   }
   if (e == hipSuccess && d.splits > 0 && d.rt.n_adapters > kRingAdapters) {  // (fewer adapters: always the ring's)
     p.z0 = 1;
-    hipLaunchKernelGGL(routed_down_kernel, dim3(blocks < 512 ? blocks : 512, groups, jobs), dim3(64 * kDownWaves), 0, s, p);
+    hipLaunchKernelGGL(routed_down_kernel<kDownBeside>, dim3(blocks < 512 ? blocks : 512, groups, jobs),
+                       dim3(64 * kDownWaves), 0, s, p);
     e = hipGetLastError();
   }
   return e;

@@ -30,9 +30,9 @@ struct RoutedDown {
   int parts;           // without the ring: workgroups that share K (1: none)
   RingBlock* ring;     // [ceil(T / 128)]
   float* tpart;        // splits > 1, parts > 1: partial sums [splits or parts, T, ldt]
-  int32_t* order;      // not null (T <= kFewMaxT): the tokens sorted by adapter go there, [2, T]: the token of
+  int32_t* order;      // not null (sorts_tokens(T)): the tokens sorted by adapter go there, [2, T]: the token of
                        // each place, then its adapter; in token order within one adapter, those without an
-                       // adapter last (up to 16 tokens: as they come). The blocks of 16 are of this order
+                       // adapter last. The blocks of 16 are of this order
 };
 constexpr int kRingBlock = 128;
 constexpr int64_t kRingMinT = 1025;
@@ -98,6 +98,8 @@ constexpr int kDownWaves = 8;
 // Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
 // 4096 -> 14336: 68 against 76 us), with mixed ones it is slower up to there and beyond (121 against 86 us).
 constexpr int64_t kFewMaxT = 256;
+// (one block of 16 is as good in any order)
+inline bool sorts_tokens(int64_t T) { return T > kRouteBlock && T <= kFewMaxT; }
 // Beyond it, up to 1024 tokens, the few-token kernel still takes outputs so narrow that the hot GEMM's 128 x 128
 // tiles would leave half of the compute units without one (tokens as they come, not sorted).
 inline bool few_path(int64_t T, int64_t N) {
@@ -137,7 +139,7 @@ struct RoutedFew {
   int64_t T, K, N;
   const uint16_t *hi, *mid; int64_t ldt;
   RoutedGemm rt;
-  const int32_t* order;  // [2, T]: the producer's, null above kFewMaxT
+  const int32_t* order;  // [2, T]: the producer's, null without one
   float* part;           // [tiles, splits, bm, 64]
 };
 hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s);

@@ -57,7 +57,7 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   for (int i = 0; i < (lora::few_path(T, N) ? 3 : 1); ++i) L.t[i] = take(static_cast<size_t>(T) * rp * 2);
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
-  if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
+  if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
   L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
   L.part = take(join_bytes(T, K, n, R));
   L.total = take.off;
@@ -91,7 +91,7 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   L.tpart = take(join_bytes(T, K, n, R));
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
-  if (T <= lora::kFewMaxT) L.order = take(static_cast<size_t>(T) * 8);
+  if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
   L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
   L.perm = take(static_cast<size_t>(T) * 4);
   for (int h = 0; h < 2; ++h) {
@@ -217,7 +217,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   d.rt = routing(pool, token_adapter, token_scale);
   d.hi = reinterpret_cast<uint16_t*>(ws + L.t[0]); d.ldt = lora::rank_pad(pool->rank);
   const bool few = lora::few_path(T, N);
-  if (T <= lora::kFewMaxT) d.order = reinterpret_cast<int32_t*>(ws + L.order);
+  if (lora::sorts_tokens(T)) d.order = reinterpret_cast<int32_t*>(ws + L.order);
   if (few) d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]), d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
   d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
@@ -295,7 +295,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   du.rt = routing(pool, token_adapter, token_scale);
   du.ldt = rp;
   du.eid = at32(L.eid); du.blk = at32(L.blk);
-  if (T <= lora::kFewMaxT) du.order = at32(L.order);
+  if (lora::sorts_tokens(T)) du.order = at32(L.order);
   du.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
   dt = du;
   du.x = static_cast<const uint16_t*>(dy); du.ldx = lddy; du.K = N;
