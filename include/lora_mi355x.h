@@ -97,7 +97,7 @@ typedef enum {
 /* Limits (LORA_ERR_UNSUPPORTED beyond them). */
 #define LORA_MAX_GROUPS 8
 #define LORA_MAX_RANK 1024
-#define LORA_MAX_POOL 16384 /* adapters of a lora_pool */
+#define LORA_MAX_POOL 8192 /* adapters of a lora_pool */
 
 /*
  * One adapter of a stacked layer (q/k/v or gate/up), covering the output
@@ -446,6 +446,7 @@ typedef struct lora_pool {
  * adapter lie next to one another.
  * T == 0 is a valid no-op. LORA_ERR_ALIGN unless x, W, A, B and the workspace
  * are 16-byte aligned and K, ldx and the slot rank are multiples of 8.
+ * LORA_ERR_UNSUPPORTED from 2^26 tokens on.
  * The output of a token depends on the other tokens of the batch in its last
  * bit only (the order of the fp32 sums); the same call gives the same bits.
  */
@@ -454,7 +455,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
                            const float* token_scale, void* y, int64_t ldy, void* workspace,
                            size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of lora_linear_routed_fwd; 0 when T, K or N <= 0. */
+/* Workspace bytes of lora_linear_routed_fwd; 0 when T, K or N <= 0 or a size is beyond the call's limits. */
 size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank);
 
 /*
@@ -472,10 +473,10 @@ size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_
  *   optional (NULL = not computed; W may be NULL without dx)
  * Every element of the outputs is written: an adapter without tokens gets zeros, and so do the rows of
  * dA and columns of dB from the adapter's rank on. dA and dB sum in fp32 over the adapter's tokens in
- * order, u_t and s_t x A^T taken in fp32 (as three bf16 terms). An adapter's gradients depend on its own tokens only.
+ * order, u_t and s_t x A^T taken in fp32 (as three bf16 terms). An adapter's gradients depend on its own
+ * tokens only.
  *   workspace  at least lora_linear_routed_bwd_workspace_size(..., dx != NULL) bytes
- * T == 0 writes zero gradients. LORA_ERR_UNSUPPORTED above about 65000 adapters and 4096-token chunks
- * together.
+ * T == 0 writes zero gradients.
  */
 int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
                            const lora_pool* pool, const int32_t* token_adapter, const float* token_scale,

@@ -533,8 +533,13 @@ def _stream_on(device, stream):
 _HERE = contextlib.nullcontext()
 
 
-def _on(device):
-    """The device made current for a call (a context only where it is not already)."""
+def _on(device, stream=None):
+    """The device, and a stream that is named, made current for a call: what the call allocates then belongs to
+    the stream that uses it. (A context only where one is needed.)"""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        return torch.cuda.stream(stream)
     return _HERE if device.type != "cuda" or device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
@@ -549,7 +554,7 @@ def lora_linear_routed(x, W, b, A, B, scales, token_adapter, token_scale=None, r
     dev = x.device
     ldx = _rows(x, "x", (T, K), dev)
     _of(b, "b", (N,), torch.bfloat16, dev)
-    with _on(dev):
+    with _on(dev, stream):
         if out is None:
             out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
         ldy = _rows(out, "out", (T, N), dev)
@@ -569,7 +574,7 @@ def lora_linear_routed_backward(x, W, A, B, dy, scales, token_adapter, token_sca
     n, R, _ = A.shape
     dev = x.device
     ldx, lddy = _rows(x, "x", (T, K), dev), _rows(dy, "dy", (T, N), dev)
-    with _on(dev):
+    with _on(dev, stream):
         if "dx" not in want:
             dx = None
         elif dx is None:
@@ -599,7 +604,8 @@ class LoraAdamW:
     (made from them), a list of tensors, or None. ``state_bits``: 32, or 8 for e4m3 moments with an fp32
     scale per 256 elements. ``state``: a dict as ``state()`` returns it, taken over (not copied); None
     starts at zero. ``lr_step``: optional fp64 device tensor {lr, step} that the kernel reads in place of
-    ``lr`` and the step count, for captured steps. lr, betas, eps and weight_decay may be changed between
+    ``lr`` and the step count, for captured steps (``state()["step"]`` counts the calls of ``step``, not
+    replays). lr, betas, eps and weight_decay may be changed between
     steps. The optimizer keeps the tensors; their buffers must stay where they are."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, master=None,
@@ -647,15 +653,20 @@ class LoraAdamW:
               for p, w, g, m, v, ms, vs in zip(params, master or none, grads, self.m, self.v, self.m_scale or none,
                                                self.v_scale or none)]
         need = lora_adamw_table_size(ts)
-        with _on(dev):
+        with _on(dev, stream):
             self._table = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
             self._plan = lora_adamw_plan(ts, _dt(params[0]), _dt(grads[0]), state_bits, self._table.data_ptr(),
                                          self._table.numel(), _stream_on(dev, stream))
+        if dev.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            # (the table, new masters and new moments are there for a step on any stream)
+            torch.cuda.current_stream(dev).synchronize()
+            if stream is not None:
+                stream.synchronize()
 
     def step(self, grad_scale=1.0, stream=None):
         """One step on the gradients that the buffers hold (on the stream that runs it)."""
         count = self.step_count + 1
-        with _on(self.device):
+        with _on(self.device, stream):
             lora_adamw_step(self._plan, float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps),
                             float(self.weight_decay), count, _ptr(self.lr_step), float(grad_scale),
                             _stream_on(self.device, stream))

@@ -26,6 +26,7 @@ struct AdamShare {
 // Elements per workgroup. Large totals take 8192 (the look-up of the share and of its tensor is paid once
 // per 8192 elements), small ones 2048, so that a single layer's tensors still spread over many compute units.
 inline int32_t adam_chunk(int64_t total) { return total >= (int64_t(1) << 22) ? 8192 : 2048; }
+constexpr int64_t kAdamMaxBlocks = (int64_t(1) << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 inline size_t adam_table_shares(int32_t n) { return (static_cast<size_t>(n) * sizeof(AdamTensor) + 255) / 256 * 256; }
 
 // Rounded constants of one step (fp32), or the doubles from which the kernel forms them with the

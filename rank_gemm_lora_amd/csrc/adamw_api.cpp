@@ -23,9 +23,11 @@ Span span(const void* p, int64_t n, int64_t esize) {
   return s;
 }
 
+constexpr int64_t kMaxElements = int64_t(1) << 36;  // (workgroups of 256: a launch has at most 2^32 threads)
+
 int64_t total_of(const lora_adamw_tensor* t, int32_t n) {
   int64_t total = 0;
-  for (int32_t i = 0; i < n; ++i) total += std::max<int64_t>(0, t[i].n);
+  for (int32_t i = 0; i < n && total <= kMaxElements; ++i) total += std::clamp<int64_t>(t[i].n, 0, kMaxElements + 1);
   return total;
 }
 
@@ -40,14 +42,12 @@ size_t table_bytes_of(const lora_adamw_tensor* t, int32_t n) {
          static_cast<size_t>(blocks_of(t, n, lora::adam_chunk(total_of(t, n)))) * sizeof(lora::AdamShare);
 }
 
-constexpr int64_t kMaxElements = int64_t(1) << 40;
-
 }  // namespace
 
 extern "C" {
 
 size_t lora_adamw_table_size(const lora_adamw_tensor* tensors, int32_t n_tensors) {
-  if (n_tensors <= 0 || tensors == nullptr) return 0;
+  if (n_tensors <= 0 || tensors == nullptr || total_of(tensors, n_tensors) > kMaxElements) return 0;
   return table_bytes_of(tensors, n_tensors);
 }
 
@@ -77,7 +77,7 @@ int lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n_tensors, int32_t
   if (!aligned(table, 16)) return LORA_ERR_ALIGN;
   const int32_t chunk = lora::adam_chunk(total);
   const int64_t blocks = blocks_of(tensors, n_tensors, chunk);
-  if (blocks > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  if (blocks > lora::kAdamMaxBlocks) return LORA_ERR_UNSUPPORTED;
   const size_t need = n_tensors > 0 ? table_bytes_of(tensors, n_tensors) : 0;
   if (need > 0 && (table == nullptr || table_bytes < need)) return LORA_ERR_WORKSPACE;
 
@@ -139,7 +139,7 @@ int lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n_tensors, int32_t
 int lora_adamw_step(const lora_adamw_plan_t* plan, double lr, double beta1, double beta2, double eps,
                     double weight_decay, int64_t step, const double* lr_step, double grad_scale, void* stream) {
   if (plan == nullptr) return LORA_ERR_NULL_PTR;
-  if (plan->reserved != 0 || plan->n_blocks < 0 || plan->n_blocks > INT32_MAX || plan->n_tensors < 0)
+  if (plan->reserved != 0 || plan->n_blocks < 0 || plan->n_blocks > lora::kAdamMaxBlocks || plan->n_tensors < 0)
     return LORA_ERR_SHAPE;
   if (plan->n_blocks > 0 && plan->table == nullptr) return LORA_ERR_NULL_PTR;
   if ((plan->param_dtype != LORA_F32 && plan->param_dtype != LORA_BF16) ||

@@ -193,6 +193,7 @@ struct RoutedContracts {
   RoutedContract c[2];
   int n, tiles0;       // tiles0: the first's share of the grid's x
   int32_t rank, n_adapters;
+  const int32_t* ranks;  // of each adapter, or null
   const int32_t* perm;
 };
 hipError_t launch_routed_contract(RoutedContracts p, hipStream_t s);

@@ -107,16 +107,21 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   return L;
 }
 
-constexpr int64_t kMaxTokens = int64_t(1) << 31;
+// (a launch has at most 2^32 threads; and items of a contraction, n_adapters + T / 4096 + 1 with so many tokens,
+// stay below the 65535 of a grid's y)
+constexpr int64_t kMaxTokens = int64_t(1) << 26;
+static_assert(LORA_MAX_POOL + kMaxTokens / lora::kRouteMaxChunk + 1 < 65535, "items of a contraction");
+
+bool in_limits(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
+  return T < kMaxTokens && K <= kMaxRowBytes / 4 && N <= kMaxRowBytes / 4 && n <= LORA_MAX_POOL && R <= LORA_MAX_RANK;
+}
 
 // Checks of the pool and the routing that both directions share.
 int check_pool(const lora_pool* pool, const int32_t* token_adapter, const float* token_scale, int64_t T, int64_t K,
                int64_t N) {
   if (pool == nullptr) return LORA_ERR_NULL_PTR;
   if (pool->n_adapters < 0 || pool->rank < 1 || pool->reserved != 0) return LORA_ERR_SHAPE;
-  if (pool->n_adapters > LORA_MAX_POOL || pool->rank > LORA_MAX_RANK || T >= kMaxTokens || K * 4 > kMaxRowBytes ||
-      N * 4 > kMaxRowBytes)
-    return LORA_ERR_UNSUPPORTED;
+  if (!in_limits(T, K, N, pool->n_adapters, pool->rank)) return LORA_ERR_UNSUPPORTED;
   if (pool->n_adapters > 0) {
     if (pool->A == nullptr || pool->B == nullptr || pool->scales == nullptr) return LORA_ERR_NULL_PTR;
     if (T > 0 && token_adapter == nullptr) return LORA_ERR_NULL_PTR;
@@ -187,7 +192,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
                            const float* token_scale, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
                            void* stream) {
   if (T < 0 || K < 1 || N < 1 || ldx < K || ldy < N) return LORA_ERR_SHAPE;
-  if (ldx * 2 > kMaxRowBytes || ldy * 2 > kMaxRowBytes) return LORA_ERR_UNSUPPORTED;
+  if (ldx > kMaxRowBytes / 2 || ldy > kMaxRowBytes / 2) return LORA_ERR_UNSUPPORTED;
   if (W == nullptr || (T > 0 && (x == nullptr || y == nullptr))) return LORA_ERR_NULL_PTR;
   int st = check_pool(pool, token_adapter, token_scale, T, K, N);
   if (st != LORA_OK) return st;
@@ -229,7 +234,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
 }
 
 size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank) {
-  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1) return 0;
+  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1 || !in_limits(T, K, N, n_adapters, rank)) return 0;
   return fwd_layout(T, K, N, n_adapters, rank).total;
 }
 
@@ -238,7 +243,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
                            const void* dy, int64_t lddy, void* dx, int64_t lddx, float* dA, float* dB,
                            void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || K < 1 || N < 1 || ldx < K || lddy < N || (dx != nullptr && lddx < K)) return LORA_ERR_SHAPE;
-  if (ldx * 2 > kMaxRowBytes || lddy * 2 > kMaxRowBytes || (dx != nullptr && lddx * 2 > kMaxRowBytes))
+  if (ldx > kMaxRowBytes / 2 || lddy > kMaxRowBytes / 2 || (dx != nullptr && lddx > kMaxRowBytes / 2))
     return LORA_ERR_UNSUPPORTED;
   if ((dx != nullptr && W == nullptr) || (T > 0 && (x == nullptr || dy == nullptr))) return LORA_ERR_NULL_PTR;
   int st = check_pool(pool, token_adapter, token_scale, T, K, N);
@@ -248,7 +253,6 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
     return LORA_ERR_ALIGN;
   const int64_t n = pool->n_adapters, R = pool->rank;
   const BwdLayout L = T > 0 ? bwd_layout(T, K, N, n, R, dx != nullptr) : BwdLayout{};
-  if (L.table[0].n_items > 65535 || L.table[1].n_items > 65535) return LORA_ERR_UNSUPPORTED;
   if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
   Span in[6];
   pool_spans(pool, token_adapter, token_scale, T, K, N, in);
@@ -324,7 +328,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   if (lora::launch_route_plan(plan, s) != hipSuccess) return LORA_ERR_HIP;
   lora::RoutedContracts c;
   std::memset(&c, 0, sizeof(c));
-  c.rank = static_cast<int32_t>(R); c.n_adapters = plan.n_adapters; c.perm = plan.perm;
+  c.rank = static_cast<int32_t>(R); c.ranks = pool->ranks; c.n_adapters = plan.n_adapters; c.perm = plan.perm;
   if (dA != nullptr)
     c.c[c.n++] = lora::RoutedContract{static_cast<const uint16_t*>(x), ldx, K, {du.hi, du.mid, du.lo}, rp, plan.table[0],
                                       reinterpret_cast<float*>(ws + L.part[0]), dA, true};
@@ -336,7 +340,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
 
 size_t lora_linear_routed_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank,
                                              int32_t want_dx) {
-  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1) return 0;
+  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1 || !in_limits(T, K, N, n_adapters, rank)) return 0;
   return bwd_layout(T, K, N, n_adapters, rank, want_dx != 0).total;
 }
 

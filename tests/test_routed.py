@@ -88,6 +88,21 @@ def test_empty_calls_and_workspace_queries():
     assert bwd(W=None, dx=None, wsb=qb(64, 128, 96, 4, 16, False) - 1) == WS
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=8193), UNSUP), (dict(T=1 << 26), UNSUP), (dict(K=1 << 62, ldx=1 << 62, lddx=1 << 62), UNSUP),
+    (dict(ldx=(1 << 63) - 8), UNSUP), (dict(N=1 << 62, ldy=1 << 62, lddy=1 << 62), UNSUP),
+])
+def test_sizes_beyond_the_limits(kw, code):
+    """Sizes whose bytes would pass 63 bits among them; the workspace queries know no size for them."""
+    f = {k: v for k, v in kw.items() if k not in ("lddx", "lddy")}
+    b = {k: v for k, v in kw.items() if k != "ldy"}
+    assert fwd(**{"T": 64, **f}) == code and bwd(**b) == code
+    if "n" in kw or "T" in kw or "K" in kw or "N" in kw:
+        args = (kw.get("T", 64), kw.get("K", 128), kw.get("N", 96), kw.get("n", 4), 16)
+        assert rg.lora_linear_routed_workspace_size(*args) == 0
+        assert rg.lora_linear_routed_bwd_workspace_size(*args) == 0
+
+
 def test_tensor_helpers_refuse():
     d = rr.case(8, 32, 24, 2, 8, 0)
     args = lambda **k: {**dict(x=d["x"], W=d["W"], b=d["b"], A=d["A"], B=d["B"], scales=d["scales"],  # noqa: E731
@@ -360,3 +375,76 @@ def test_two_streams_and_repeats_give_the_same_bits():
     for ref, outs in zip(refs, got):
         for o in outs:
             assert all(torch.equal(a, b) for a, b in zip(o, ref))
+
+
+@pytest.mark.gpu
+def test_rows_of_x_far_apart():
+    """Rows of 4 MB: x spans more than 32 bits of bytes, tokens as they come and sorted."""
+    say("routed wide rows")
+    ld = 1 << 21
+    wide = torch.empty((1024, ld), dtype=torch.bfloat16, device=DEV)
+    for T in (1023, 200, 12):
+        d = rr.case(T, 64, 72, 5, 16, T, "mixed")
+        g = gpu(d)
+        wide[:T, :64] = g["x"]
+        g["x"] = wide[:T, :64]
+        rr.check(run_fwd(g), *rr.forward(d), f"y, {T}")
+    d = rr.case(1023, 72, 64, 5, 16, 4, "mixed")  # and of dy
+    g = gpu(d)
+    wide[:1023, :64] = g["dy"]
+    g["dy"] = wide[:1023, :64]
+    want, bounds = rr.backward(d)
+    for got, w, b, what in zip(run_bwd(g), want, bounds, ("dx", "dA", "dB")):
+        rr.check(got, w, b, what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [30, 1500])
+def test_the_largest_pool(T):
+    say("routed largest pool", T)
+    d = rr.case(T, 24, 16, 8192, 8, T, "mixed")
+    d["ids"][0], d["ids"][1] = 8191, 0
+    g = gpu(d)
+    rr.check(run_fwd(g), *rr.forward(d), "y")
+    want, bounds = rr.backward(d)
+    for got, w, b, what in zip(run_bwd(g), want, bounds, ("dx", "dA", "dB")):
+        rr.check(got, w, b, what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [20, 1200])
+def test_broken_tokens_leave_the_rest_of_a_slot_at_zero(T):
+    """Infinite and NaN tokens: other tokens' outputs and other adapters' gradients keep their bits, and what lies
+    behind the adapter's rank stays zero."""
+    say("routed broken tokens", T)
+    d = rr.case(T, 96, 72, 3, 32, T, "mixed")
+    d["ids"][:3] = torch.tensor([0, 1, 2])
+    d["ranks"] = torch.tensor([16, 32, 8], dtype=torch.int32)
+    live = torch.arange(32)[None, :] < d["ranks"][:, None]
+    d["A"], d["B"] = d["A"] * live[:, :, None], d["B"] * live[:, None, :]
+    g = gpu(d)
+    y0, (dx0, dA0, dB0) = run_fwd(g), run_bwd(g)
+    g["x"][0, 5], g["x"][0, 6] = float("inf"), float("nan")
+    g["dy"][0, 7] = float("inf")
+    y1, (dx1, dA1, dB1) = run_fwd(g), run_bwd(g)
+    assert torch.equal(y0[1:], y1[1:]) and torch.equal(dx0[1:], dx1[1:])
+    assert torch.equal(dA0[1:], dA1[1:]) and torch.equal(dB0[1:], dB1[1:])
+    assert not bool(dA1[0, 16:].any()) and not bool(dB1[0, :, 16:].any())
+    assert not bool(torch.isfinite(y1[0]).any()) and not bool(torch.isfinite(dA1[0, :16, 5]).any())
+
+
+@pytest.mark.gpu
+def test_calls_on_a_named_stream():
+    """stream=: the call's own tensors belong to that stream; a stream of no device of the tensors is refused."""
+    say("routed named stream")
+    d = rr.case(300, 128, 264, 5, 24, 1, "mixed")
+    g = gpu(d)
+    ref = (run_fwd(g), *run_bwd(g))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(run_fwd(g, stream=side), *run_bwd(g, stream=side)) for _ in range(3)]
+    side.synchronize()
+    for outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+    with pytest.raises(ValueError):
+        rg.lora_linear_routed(*(d[k] for k in ("x", "W", "b", "A", "B", "scales", "ids")), stream=side)
