@@ -1927,6 +1927,9 @@ namespace down {
 // ring, ~64 KB of x in flight per CU) when every group's padded rank is 64, else 128.
 using DP64 = PCfg<128, 64, 32, 64, 128, 5>;
 using DP128 = PCfg<128, 128, 32, 128, 128, 4>;
+// The routed producer's: two workgroups on a compute unit, since a block's adapters make several and others have
+// nothing to do (18871 tokens, widths 8960 and 1536: 112 us against 127 with five stages and one workgroup).
+using RP64 = PCfg<128, 64, 32, 64, 128, 3>;
 
 // One pipelined K loop over NS stages for config P; issue(s) fills ring slot s % S.
 template <class P, class Issue>
@@ -2144,9 +2147,11 @@ hipError_t launch(const LinearProblem& p, hipStream_t s) {
   return narrow ? launch_cfg<DP64, false>(p, s) : launch_cfg<DP128, false>(p, s);
 }
 
-// Routed producer, blocks of 128 tokens with few adapters (RingBlock): the same ring over the rows of a
-// pool slot, once per adapter of the block, whose own tokens keep the result. Grid: (blocks, adapter rows,
-// adapter of the block x split).
+// Routed producer, blocks of 128 tokens with few adapters: the same ring over the rows of a pool slot, once
+// per adapter of the block, whose own tokens keep the result. Grid: (blocks, adapter rows, adapter of the
+// block x split). (All of a block on one XCD costs more: 4977 tokens, K 8960: 43 us against 36; the blocks of
+// several adapters meet on some.) Each workgroup finds the block's adapters for itself (a launch for it costs
+// 5 us, this 1-2), and one of them writes eid, blk and ring for the kernels behind.
 template <class DP>
 __global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDowns ps) {
   using P = DP;
@@ -2155,13 +2160,43 @@ __global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDowns ps
   const int job = static_cast<int>(blockIdx.z) >= ps.z0 ? 1 : 0, z = blockIdx.z - job * ps.z0;
   const RoutedDown& p = ps.d[job];
   const int nth = z / p.splits, split = z - nth * p.splits;
-  const RingBlock* rb = p.ring + blockIdx.x;
-  if (nth >= __builtin_amdgcn_readfirstlane(rb->n)) return;
-  const int a = __builtin_amdgcn_readfirstlane(rb->id[nth]);  // (in a scalar register: the resources need it there)
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int id[2];
+  uint64_t todo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float s;
+    id[h] = route(p.rt, m0 + 64 * h + lane, p.T, s);
+    todo[h] = __builtin_amdgcn_ballot_w64(id[h] >= 0);
+  }
+  int n = 0, a = -1;  // adapters, and the nth of them in the order of the tokens
+#pragma unroll
+  for (int k = 0; k < kRingAdapters; ++k) {
+    if ((todo[0] | todo[1]) == 0) break;
+    const int b = todo[0] != 0 ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(todo[0]))
+                               : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(todo[1]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) todo[h] &= ~__builtin_amdgcn_ballot_w64(id[h] == b);
+    if (k == nth) a = b;
+    n = k + 1;
+  }
+  if ((todo[0] | todo[1]) != 0) n = -1;
+  if (blockIdx.y == 0 && blockIdx.z == 0 && wave == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t m = m0 + 64 * h + lane;
+      // blk: lanes 16 b .. of the half; the block's first token decides
+      const int first = __shfl(id[h], lane & ~15);
+      const uint64_t differ = __builtin_amdgcn_ballot_w64(m < p.T && id[h] != first);
+      if (m < p.T) p.eid[m] = id[h];
+      if (m < p.T && (lane & 15) == 0) p.blk[m / kRouteBlock] = (differ >> lane & 0xffffu) == 0 ? first : -2;
+    }
+    if (lane == 0) p.ring[blockIdx.x] = n;
+  }
+  if (nth >= n) return;
   const int rows_m = static_cast<int>(min<int64_t>(P::BM, p.T - m0));
   const int rank = route_rank(p.rt.ranks, p.rt.rank, a);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int q0 = blockIdx.y * P::BN;
   const int rows_q = max(0, min(P::BN, rank - q0));
@@ -2189,7 +2224,8 @@ __global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDowns ps
 
   const int r = lane & 31, h = lane >> 5;
   const int64_t m = m0 + wm0 + r;
-  if (m >= p.T || p.eid[m] != a) return;
+  static_assert(P::WM == 32, "a wave's tokens lie in one half of the block");
+  if (__shfl(wm0 < 64 ? id[0] : id[1], (wm0 & 63) + r) != a) return;  // (-1 past the last token)
   if (p.splits > 1) {
     float* part = p.tpart + (split * p.T + m) * p.ldt;
 #pragma unroll
@@ -2798,8 +2834,8 @@ hipError_t launch_bias32(const LinearProblem& p, hipStream_t s) {
 }
 
 hipError_t launch_routed_ring(RoutedDowns p, hipStream_t s) {
-  return p.d[0].ldt <= pipe::down::DP64::BN ? pipe::down::launch_ring_cfg<pipe::down::DP64>(p, s)
-                                       : pipe::down::launch_ring_cfg<pipe::down::DP128>(p, s);
+  return p.d[0].ldt <= pipe::down::RP64::BN ? pipe::down::launch_ring_cfg<pipe::down::RP64>(p, s)
+                                            : pipe::down::launch_ring_cfg<pipe::down::DP128>(p, s);
 }
 
 hipError_t launch_routed_gemm(const LinearProblem& p, hipStream_t s) { return pipe::launch(p, s); }

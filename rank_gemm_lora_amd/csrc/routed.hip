@@ -16,67 +16,6 @@ namespace {
 
 constexpr uint32_t kOutOfRange = 0x80000000u;  // a buffer offset past every range: the load returns zeros
 
-// ---------------------------------------------------------------------------
-// What a block of 128 tokens takes (RingBlock), eid and blk, before the ring runs.
-__global__ __launch_bounds__(64) void route_blocks_kernel(RoutedDown p) {
-  const int lane = threadIdx.x;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRingBlock;
-  int id[2];
-  uint64_t todo[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t m = m0 + 64 * h + lane;
-    float s;
-    id[h] = route(p.rt, m, p.T, s);
-    todo[h] = __builtin_amdgcn_ballot_w64(id[h] >= 0);
-    if (m < p.T) p.eid[m] = id[h];
-    // blk: lanes 16 b .. of the half; the block's first token decides
-    const int first = __shfl(id[h], lane & ~15);
-    const uint64_t differ = __builtin_amdgcn_ballot_w64(m < p.T && id[h] != first);
-    if ((lane & 15) == 0 && m < p.T)
-      p.blk[m / kRouteBlock] = (differ >> lane & 0xffffu) == 0 ? first : -2;
-  }
-  RingBlock b{0, {-1, -1, -1, -1}};
-#pragma unroll
-  for (int k = 0; k < kRingAdapters; ++k) {
-    if (todo[0] == 0 && todo[1] == 0) break;
-    const int a = todo[0] != 0 ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(todo[0]))
-                               : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(todo[1]));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) todo[h] &= ~__builtin_amdgcn_ballot_w64(id[h] == a);
-    b.id[k] = a;
-    b.n = k + 1;
-  }
-  if (todo[0] != 0 || todo[1] != 0) b.n = -1;
-  if (lane == 0) p.ring[blockIdx.x] = b;
-}
-
-// t of the tokens whose sums are in parts (the ring's splits, or parts without the ring), added in order and
-// scaled. 32 threads a token and 64 ranks.
-__global__ __launch_bounds__(256) void down_join_kernel(RoutedDowns ps) {
-  const RoutedDown& p = ps.d[blockIdx.z];
-  const int n = p.splits > 0 ? p.splits : p.parts;
-  if (n <= 1) return;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (m >= p.T) return;
-  const int64_t at = m * p.ldt + blockIdx.y * 64 + 2 * (threadIdx.x & 31);
-  f32x2 w[8];  // (all parts' loads before their adds; a part past the last reads the last again, unused)
-#pragma unroll
-  for (int z = 0; z < 8; ++z) w[z] = *reinterpret_cast<const f32x2*>(p.tpart + min(z, n - 1) * p.T * p.ldt + at);
-  if (p.eid[m] < 0 || (p.splits > 0 && p.ring[m / kRingBlock].n < 0)) return;
-  float v[2] = {0.f, 0.f}, s;
-#pragma unroll
-  for (int z = 0; z < 8; ++z)
-    if (z < n) {
-      v[0] += w[z][0];
-      v[1] += w[z][1];
-    }
-  route(p.rt, m, p.T, s);
-  v[0] *= s;
-  v[1] *= s;
-  put_rank_wide<2>(p, at, v);
-}
-
 // Rank-wide producer without the ring. Workgroup: one block of 16 tokens, 64 ranks, one slot's share of the
 // block's distinct adapters, one part of K; 8 waves split that and add their sums through LDS in wave order.
 // Operands go from global memory straight into MFMA fragments (lane (r, q): 8 consecutive k of adapter row r /
@@ -231,39 +170,78 @@ __device__ __forceinline__ void sort_tokens(const RoutedDown& p, SortedTokens& o
   __syncthreads();
 }
 
-enum { kDownPlain = 0, kDownSorted = 1, kDownBeside = 2 };  // blocks as they come, sorted, those the ring left
-
-template <int MODE>
+template <bool SORTED>
 __global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDowns ps) {
   __shared__ f32x4 red[kDownWaves][4][64];
   const int job = static_cast<int>(blockIdx.z) >= ps.z0 ? 1 : 0, z = blockIdx.z - job * ps.z0;
   const RoutedDown& p = ps.d[job];
-  if constexpr (MODE == kDownBeside) {
-    // blocks blockIdx.x, + gridDim.x, ..: 64 at a time, one per lane (every wave the same)
-    const int64_t n = (p.T + kRouteBlock - 1) / kRouteBlock;
-    for (int64_t base = blockIdx.x; base < n; base += 64 * static_cast<int64_t>(gridDim.x)) {
-      const int64_t mine = base + (threadIdx.x & 63) * static_cast<int64_t>(gridDim.x);
-      uint64_t left = __builtin_amdgcn_ballot_w64(mine < n && p.ring[mine * kRouteBlock / kRingBlock].n < 0);
-      while (left != 0) {
-        const int i = __builtin_ctzll(left);
-        left &= left - 1;
-        down_block(p, base + i * static_cast<int64_t>(gridDim.x), red, nullptr, 0, 1, 0, false);
-      }
+  const bool tell = blockIdx.y == 0 && blockIdx.z == 0;
+  const int slot = z % ps.slots, part = z / ps.slots;
+  if constexpr (SORTED) {
+    __shared__ __attribute__((aligned(16))) SortedTokens sorted;
+    sort_tokens(p, sorted);
+    if (blockIdx.x == 0 && tell && static_cast<int>(threadIdx.x) < p.T) {
+      p.order[threadIdx.x] = sorted.token[threadIdx.x];
+      p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
     }
+    down_block(p, blockIdx.x, red, &sorted, slot, ps.slots, part, tell);
   } else {
-    const bool tell = blockIdx.y == 0 && blockIdx.z == 0;
-    const int slot = z % ps.slots, part = z / ps.slots;
-    if constexpr (MODE == kDownSorted) {
-      __shared__ __attribute__((aligned(16))) SortedTokens sorted;
-      sort_tokens(p, sorted);
-      if (blockIdx.x == 0 && tell && static_cast<int>(threadIdx.x) < p.T) {
-        p.order[threadIdx.x] = sorted.token[threadIdx.x];
-        p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
-      }
-      down_block(p, blockIdx.x, red, &sorted, slot, ps.slots, part, tell);
-    } else {
-      down_block(p, blockIdx.x, red, nullptr, slot, ps.slots, part, tell);
+    down_block(p, blockIdx.x, red, nullptr, slot, ps.slots, part, tell);
+  }
+}
+
+// t of the tokens whose sums are in parts (the ring's splits, or parts without the ring), added in order and
+// scaled. 32 threads a token and 64 ranks, kDownWaves * 2 tokens a workgroup.
+__device__ __forceinline__ void down_join(const RoutedDown& p, int64_t group) {
+  const int n = p.splits > 0 ? p.splits : p.parts;
+  if (n <= 1) return;
+  const int64_t m = group * (2 * kDownWaves) + (threadIdx.x >> 5);
+  if (m >= p.T) return;
+  const int64_t at = m * p.ldt + blockIdx.y * 64 + 2 * (threadIdx.x & 31);
+  f32x2 w[8];  // (all parts' loads before their adds; a part past the last reads the last again, unused)
+#pragma unroll
+  for (int z = 0; z < 8; ++z) w[z] = *reinterpret_cast<const f32x2*>(p.tpart + min(z, n - 1) * p.T * p.ldt + at);
+  if (p.eid[m] < 0 || (p.splits > 0 && p.ring[m / kRingBlock] < 0)) return;
+  float v[2] = {0.f, 0.f}, s;
+#pragma unroll
+  for (int z = 0; z < 8; ++z)
+    if (z < n) {
+      v[0] += w[z][0];
+      v[1] += w[z][1];
     }
+  route(p.rt, m, p.T, s);
+  v[0] *= s;
+  v[1] *= s;
+  put_rank_wide<2>(p, at, v);
+}
+
+// The blocks of 16 that the ring did not take: blocks blockIdx.x, + stride, ..; 64 at a time are looked at, one per
+// lane (every wave the same).
+__device__ __forceinline__ void down_beside(const RoutedDown& p, f32x4 (&red)[kDownWaves][4][64], int64_t stride) {
+  const int64_t n = (p.T + kRouteBlock - 1) / kRouteBlock;
+  for (int64_t base = blockIdx.x; base < n; base += 64 * stride) {
+    const int64_t mine = base + (threadIdx.x & 63) * stride;
+    uint64_t left = __builtin_amdgcn_ballot_w64(mine < n && p.ring[mine * kRouteBlock / kRingBlock] < 0);
+    while (left != 0) {
+      const int i = __builtin_ctzll(left);
+      left &= left - 1;
+      down_block(p, base + i * stride, red, nullptr, 0, 1, 0, false);
+    }
+  }
+}
+
+// What the first launch left: with BESIDE the blocks of 16 that the ring did not take (workgroups below `beside`),
+// and the sums in parts (the others).
+template <bool BESIDE>
+__global__ __launch_bounds__(64 * kDownWaves) void routed_rest_kernel(RoutedDowns ps, int beside) {
+  const RoutedDown& p = ps.d[blockIdx.z];
+  if (static_cast<int>(blockIdx.x) >= beside) {
+    down_join(p, blockIdx.x - beside);
+    return;
+  }
+  if constexpr (BESIDE) {
+    __shared__ f32x4 red[kDownWaves][4][64];
+    down_beside(p, red, beside);
   }
 }
 
@@ -803,22 +781,26 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
     p.z0 = slots * d.parts;
     const int z = p.z0 + (p.n > 1 ? slots * p.d[1].parts : 0);
     const dim3 grid(blocks, groups, static_cast<unsigned>(z));
-    if (d.order != nullptr) hipLaunchKernelGGL(routed_down_kernel<kDownSorted>, grid, dim3(64 * kDownWaves), 0, s, p);
-    else hipLaunchKernelGGL(routed_down_kernel<kDownPlain>, grid, dim3(64 * kDownWaves), 0, s, p);
+    if (d.order != nullptr) hipLaunchKernelGGL(routed_down_kernel<true>, grid, dim3(64 * kDownWaves), 0, s, p);
+    else hipLaunchKernelGGL(routed_down_kernel<false>, grid, dim3(64 * kDownWaves), 0, s, p);
     e = hipGetLastError();
   } else {
-    hipLaunchKernelGGL(route_blocks_kernel, dim3(static_cast<unsigned>(ring_blocks(d.T))), dim3(64), 0, s, d);
-    e = hipGetLastError();
-    if (e == hipSuccess) e = launch_routed_ring(p, s);
+    e = launch_routed_ring(p, s);
   }
-  if (e == hipSuccess && join) {
-    hipLaunchKernelGGL(down_join_kernel, dim3(static_cast<unsigned>((d.T + 7) / 8), groups, jobs), dim3(256), 0, s, p);
+  // (up to kRingAdapters adapters every block is the ring's)
+  const unsigned beside = d.splits > 0 && d.rt.n_adapters > kRingAdapters ? (blocks < 512 ? blocks : 512) : 0;
+  const unsigned joins = join ? static_cast<unsigned>((d.T + 2 * kDownWaves - 1) / (2 * kDownWaves)) : 0;
+  // (one launch for both where it is short: 4977 tokens 7.2 us against 5.4 + 4.7; the registers of the blocks slow
+  // many joins down: 18871 tokens, both products, 26 us against 15.4 + 4.8)
+  const bool apart = d.T > 8192;
+  if (e == hipSuccess && beside > 0) {
+    const unsigned x = beside + (apart ? 0 : joins);
+    hipLaunchKernelGGL(routed_rest_kernel<true>, dim3(x, groups, jobs), dim3(64 * kDownWaves), 0, s, p,
+                       static_cast<int>(beside));
     e = hipGetLastError();
   }
-  if (e == hipSuccess && d.splits > 0 && d.rt.n_adapters > kRingAdapters) {  // (fewer adapters: always the ring's)
-    p.z0 = 1;
-    hipLaunchKernelGGL(routed_down_kernel<kDownBeside>, dim3(blocks < 512 ? blocks : 512, groups, jobs),
-                       dim3(64 * kDownWaves), 0, s, p);
+  if (e == hipSuccess && joins > 0 && (apart || beside == 0)) {
+    hipLaunchKernelGGL(routed_rest_kernel<false>, dim3(joins, groups, jobs), dim3(64 * kDownWaves), 0, s, p, 0);
     e = hipGetLastError();
   }
   return e;

@@ -11,10 +11,6 @@ namespace lora {
 // With many tokens (splits > 0) a block of 128 tokens with up to four adapters is multiplied by a ring of
 // LDS stages, once per adapter, K in `splits` parts of ks stages of 64; the other blocks, and all blocks of
 // fewer tokens, 16 tokens at a time straight from memory.
-struct RingBlock {
-  int32_t n;      // adapters of the block's tokens, -1: more than kRingAdapters
-  int32_t id[4];
-};
 constexpr int kRingAdapters = 4;
 struct RoutedDown {
   const uint16_t* x; int64_t ldx;
@@ -28,7 +24,7 @@ struct RoutedDown {
   int32_t* blk;        // [ceil(T / 16)]
   int splits, ks;      // of the ring (0: not used)
   int parts;           // without the ring: workgroups that share K (1: none)
-  RingBlock* ring;     // [ceil(T / 128)]
+  int32_t* ring;       // [ceil(T / 128)]: adapters of the block's tokens, -1: more than kRingAdapters
   float* tpart;        // splits > 1, parts > 1: partial sums [splits or parts, T, ldt]
   int32_t* order;      // not null (sorts_tokens(T)): the tokens sorted by adapter go there, [2, T]: the token of
                        // each place, then its adapter; in token order within one adapter, those without an

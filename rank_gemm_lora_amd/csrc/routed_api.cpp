@@ -58,7 +58,7 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
-  L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
+  L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * 4);
   L.part = take(join_bytes(T, K, n, R));
   L.total = take.off;
   return L;
@@ -92,7 +92,7 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
-  L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * sizeof(lora::RingBlock));
+  L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * 4);
   L.perm = take(static_cast<size_t>(T) * 4);
   for (int h = 0; h < 2; ++h) {
     auto& tb = L.table[h];
@@ -227,7 +227,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
   d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
   plan_down(d);
-  d.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
+  d.ring = reinterpret_cast<int32_t*>(ws + L.ring);
   d.tpart = reinterpret_cast<float*>(ws + L.part);
   if (lora::launch_routed_down(lora::RoutedDowns{{d, d}, 1, 0, 0}, s) != hipSuccess) return LORA_ERR_HIP;
   return launch_product(x, T, K, ldx, W, N, bias, y, ldy, d, pool->B, pool, ws + L.few, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
@@ -300,7 +300,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   du.ldt = rp;
   du.eid = at32(L.eid); du.blk = at32(L.blk);
   if (lora::sorts_tokens(T)) du.order = at32(L.order);
-  du.ring = reinterpret_cast<lora::RingBlock*>(ws + L.ring);
+  du.ring = reinterpret_cast<int32_t*>(ws + L.ring);
   dt = du;
   du.x = static_cast<const uint16_t*>(dy); du.ldx = lddy; du.K = N;
   du.A = at16(L.bt);

@@ -62,7 +62,7 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t) {
     if (i > 0) continue;
     inside(d.eid, static_cast<size_t>(d.T) * 4, "eid", true);
     inside(d.blk, static_cast<size_t>((d.T + 15) / 16) * 4, "blk", true);
-    if (d.splits > 0) inside(d.ring, static_cast<size_t>(ring_blocks(d.T)) * sizeof(RingBlock), "ring", true);
+    if (d.splits > 0) inside(d.ring, static_cast<size_t>(ring_blocks(d.T)) * 4, "ring", true);
     if (d.order != nullptr) inside(d.order, static_cast<size_t>(d.T) * 8, "order", true);
     if (sorts_tokens(d.T) != (d.order != nullptr)) fail("order given where it is used");
   }
