@@ -17,6 +17,7 @@
 #include "backward.hpp"
 
 #include "common.hpp"
+#include "transpose_dev.hpp"
 
 namespace lora {
 namespace {
@@ -41,63 +42,12 @@ __global__ __launch_bounds__(256) void transpose_pad_kernel(const bf16_bits* __r
   }
 }
 
-// The same transpose with 16-byte accesses: a thread reads one 8-element piece of a source row
-// (8 threads per 64-element tile row, 32 rows per pass) and writes one 8-element piece of a
-// destination row, gathered from 8 rows of the tile in LDS (rows padded to 72 elements so that
-// 16-byte stores of consecutive rows stay aligned). Needs C, ld and Rpad multiples of 8 and
-// 16-byte aligned src and dst. Measured on MI355X: B^T of 8960 x 64 2.6 against 5.3 us, W^T of
-// 8960 x 1536 11.6 against 18.7 us; the same bytes.
-__device__ __forceinline__ void transpose_tile16(const bf16_bits* __restrict__ src, int64_t lds_, int64_t R, int64_t C,
-                                                 bf16_bits* __restrict__ dst, int64_t Rpad, int64_t Cpad, int64_t r0,
-                                                 int64_t c0, bf16_bits (&tile)[64][72]) {
-  const int pc = threadIdx.x & 7, rr = threadIdx.x >> 3;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = rr + 32 * h;
-    const int64_t r = r0 + i, c = c0 + pc * 8;
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (r < R && c < C) v = *reinterpret_cast<const u32x4*>(src + r * lds_ + c);
-    *reinterpret_cast<u32x4*>(&tile[i][pc * 8]) = v;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int j = rr + 32 * h;  // destination row c0 + j, elements r0 + 8 pc .. + 7
-    const int64_t c = c0 + j, r = r0 + pc * 8;
-    if (c < Cpad && r < Rpad) {
-      u32x4 o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = static_cast<uint32_t>(tile[pc * 8 + 2 * e][j]) |
-               (static_cast<uint32_t>(tile[pc * 8 + 2 * e + 1][j]) << 16);
-      *reinterpret_cast<u32x4*>(dst + c * Rpad + r) = o;
-    }
-  }
-}
-
 __global__ __launch_bounds__(256) void transpose_pad16_kernel(const bf16_bits* __restrict__ src, int64_t lds_,
                                                               int64_t R, int64_t C, bf16_bits* __restrict__ dst,
                                                               int64_t Rpad, int64_t Cpad) {
   __shared__ __attribute__((aligned(16))) bf16_bits tile[64][72];
   transpose_tile16(src, lds_, R, C, dst, Rpad, Cpad, static_cast<int64_t>(blockIdx.x) * 64,
-                   static_cast<int64_t>(blockIdx.y) * 64, tile);
-}
-
-// Several stacks of matrices in one launch: workgroups [first, next first) are a stack's 64 x 64 tiles.
-struct TransposeStacks {
-  TransposeStack s[kTransposeStacks];
-  int64_t first[kTransposeStacks + 1];
-};
-__global__ __launch_bounds__(256) void transpose_stacks_kernel(TransposeStacks a) {
-  __shared__ __attribute__((aligned(16))) bf16_bits tile[64][72];
-  int k = 0;
-#pragma unroll
-  for (int i = 1; i < kTransposeStacks; ++i) k = blockIdx.x >= a.first[i] ? i : k;
-  const TransposeStack& s = a.s[k];
-  const int64_t tr = (s.R + 63) / 64, tc = (s.C + 63) / 64, b = blockIdx.x - a.first[k];
-  const int64_t slot = b / (tr * tc), rest = b - slot * (tr * tc);
-  transpose_tile16(s.src + slot * s.R * s.C, s.C, s.R, s.C, s.dst + slot * s.R * s.C, s.R, s.C, rest % tr * 64,
-                   rest / tr * 64, tile);
+                   static_cast<int64_t>(blockIdx.y) * 64, tile, threadIdx.x);
 }
 
 hipError_t transpose_pad_impl(const bf16_bits* src, int64_t ld, int64_t R, int64_t C, bf16_bits* dst, int64_t Rpad,
@@ -291,21 +241,6 @@ hipError_t zero_fill(float* dst, int64_t n, hipStream_t s) {
 hipError_t transpose_pad(const uint16_t* src, int64_t ld, int64_t R, int64_t C, uint16_t* dst, int64_t Rpad,
                          int64_t Cpad, hipStream_t s) {
   return transpose_pad_impl(src, ld, R, C, dst, Rpad, Cpad, s);
-}
-
-hipError_t transpose_stacks(const TransposeStack* stacks, int n, hipStream_t s) {
-  TransposeStacks a;
-  int64_t blocks = 0;
-  for (int i = 0; i < kTransposeStacks; ++i) {
-    a.s[i] = i < n ? stacks[i] : TransposeStack{nullptr, nullptr, 0, 0, 0};
-    a.first[i] = i < n ? blocks : (int64_t(1) << 62);
-    if (i < n) blocks += stacks[i].slots * ((stacks[i].R + 63) / 64) * ((stacks[i].C + 63) / 64);
-  }
-  a.first[kTransposeStacks] = blocks;
-  if (blocks == 0) return hipSuccess;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(transpose_stacks_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
-  return hipGetLastError();
 }
 
 // Token chunks of a contraction over T tokens with `tiles` workgroups per chunk: at most 512

@@ -9,16 +9,6 @@ namespace lora {
 hipError_t transpose_pad(const uint16_t* src, int64_t ld, int64_t R, int64_t C, uint16_t* dst, int64_t Rpad,
                          int64_t Cpad, hipStream_t s);
 
-// dst[i] [C, R] = src[i] [R, C] transposed for i < slots; contiguous, 16-byte aligned, R and C multiples of 8.
-// Up to kTransposeStacks such stacks in one launch.
-struct TransposeStack {
-  const uint16_t* src;
-  uint16_t* dst;
-  int64_t R, C, slots;
-};
-constexpr int kTransposeStacks = 3;
-hipError_t transpose_stacks(const TransposeStack* stacks, int n, hipStream_t s);
-
 // dst[0 .. n) = 0.0f by a kernel (a memset node in a captured HIP graph is avoided).
 hipError_t zero_fill(float* dst, int64_t n, hipStream_t s);
 

@@ -9,7 +9,9 @@
 #include "routed.hpp"
 
 #include "common.hpp"
+#include "lora_mi355x.h"
 #include "routed_dev.hpp"
+#include "transpose_dev.hpp"
 
 namespace lora {
 namespace {
@@ -526,15 +528,14 @@ __global__ __launch_bounds__(256) void few_finish_kernel(RoutedFew p, int tt, in
 }
 
 // ---------------------------------------------------------------------------
-// Tokens sorted by adapter: workgroup a finds its adapter's tokens. The 16 waves take consecutive stretches of
-// the tokens, eight loads of 64 in flight; a first pass counts the tokens of every adapter before it (one LDS
-// atomic for each adapter among 64 tokens; integers, so their order does not show), from which follow its place
-// among tokens and items, and its own by wave; a second writes them, in token order.
-__global__ __launch_bounds__(1024) void route_plan_kernel(RoutePlan p) {
-  extern __shared__ int counts[];  // [n_adapters]
-  __shared__ int sums[5][16], mine[16];
+// What the backward's other launches need first: the transposed operands and the plan of the contractions.
+//
+// The plan, tokens sorted by adapter: workgroup a finds its adapter's tokens. The 16 waves take consecutive
+// stretches of the tokens, eight loads of 64 in flight; a first pass counts the tokens of every adapter before it
+// (one LDS atomic for each adapter among 64 tokens; integers, so their order does not show), from which follow its
+// place among tokens and items, and its own by wave; a second writes them, in token order.
+__device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* counts, int (&sums)[5][16], int (&mine)[16]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int a = blockIdx.x;
   const int64_t per = ((p.T + 15) / 16 + 63) / 64 * 64;
   const int64_t lo = wave * per, hi = min<int64_t>(p.T, lo + per);
   for (int i = threadIdx.x; i < p.n_adapters; i += 1024) counts[i] = 0;
@@ -543,7 +544,12 @@ __global__ __launch_bounds__(1024) void route_plan_kernel(RoutePlan p) {
   for (int64_t t = lo; t < hi; t += 512) {
     int id[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) id[k] = t + 64 * k + lane < hi ? p.eid[t + 64 * k + lane] : -1;
+    for (int k = 0; k < 8; ++k) {
+      float scale;
+      const int64_t at = t + 64 * k + lane;
+      if (p.eid == nullptr) id[k] = route(p.rt, at, hi, scale);
+      else id[k] = at < hi ? p.eid[at] : -1;
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint64_t todo = __builtin_amdgcn_ballot_w64(id[k] >= 0 && id[k] < a);
@@ -588,7 +594,12 @@ __global__ __launch_bounds__(1024) void route_plan_kernel(RoutePlan p) {
   for (int64_t t = lo; t < hi; t += 512) {
     int id[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) id[k] = t + 64 * k + lane < hi ? p.eid[t + 64 * k + lane] : -1;
+    for (int k = 0; k < 8; ++k) {
+      float scale;
+      const int64_t at = t + 64 * k + lane;
+      if (p.eid == nullptr) id[k] = route(p.rt, at, hi, scale);
+      else id[k] = at < hi ? p.eid[at] : -1;
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint64_t m = __builtin_amdgcn_ballot_w64(id[k] == a);
@@ -616,6 +627,42 @@ __global__ __launch_bounds__(1024) void route_plan_kernel(RoutePlan p) {
         tb.items[z] = RouteItem{0, 0, 0, -1};
     }
   }
+}
+
+struct RoutePrepare {
+  RoutePlan plan;
+  TransposeStack s[kTransposeStacks];
+  int64_t first[kTransposeStacks + 1];  // 64 x 64 tiles [first, next first) are a stack's
+};
+
+// Workgroups below n_adapters (with PLAN): the plan; the others: transposes, TILES of them by 256 threads each.
+template <bool PLAN, int TILES>
+__global__ __launch_bounds__(256 * TILES) void route_prepare_kernel(RoutePrepare p) {
+  static_assert(!PLAN || TILES == 4, "the plan's 16 waves");
+  __shared__ __attribute__((aligned(16))) union {
+    bf16_bits tile[TILES][64][72];
+    int counts[PLAN ? LORA_MAX_POOL : 1];
+  } u;
+  if constexpr (PLAN) {
+    __shared__ int sums[5][16], mine[16];
+    if (static_cast<int>(blockIdx.x) < p.plan.n_adapters) {
+      route_plan(p.plan, blockIdx.x, u.counts, sums, mine);
+      return;
+    }
+  }
+  const int part = threadIdx.x >> 8;
+  const int64_t b = static_cast<int64_t>(blockIdx.x - p.plan.n_adapters) * TILES + part;
+  int k = 0;
+#pragma unroll
+  for (int i = 1; i < kTransposeStacks; ++i) k = b >= p.first[i] ? i : k;
+  const TransposeStack& s = p.s[k];
+  const int64_t tr = (s.R + 63) / 64, tc = (s.C + 63) / 64, at = b - p.first[k];
+  const int64_t slot = at / (tr * tc), rest = at - slot * (tr * tc);
+  // (past the last tile: no rows, nothing read or written)
+  const bool in = b < p.first[kTransposeStacks];
+  transpose_tile16(s.src + (in ? slot : 0) * s.R * s.C, s.C, in ? s.R : 0, in ? s.C : 0,
+                   s.dst + (in ? slot : 0) * s.R * s.C, in ? s.R : 0, in ? s.C : 0, rest % tr * 64, rest / tr * 64,
+                   u.tile[part], threadIdx.x & 255);
 }
 
 // ---------------------------------------------------------------------------
@@ -828,9 +875,23 @@ hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s) {
   }
 }
 
-hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s) {
-  hipLaunchKernelGGL(route_plan_kernel, dim3(static_cast<unsigned>(p.n_adapters)), dim3(1024),
-                     static_cast<size_t>(p.n_adapters) * 4, s, p);
+hipError_t launch_route_prepare(const RoutePlan& plan, const TransposeStack* stacks, int n, hipStream_t s) {
+  RoutePrepare p;
+  p.plan = plan;
+  int64_t tiles = 0;
+  for (int i = 0; i < kTransposeStacks; ++i) {
+    p.s[i] = i < n ? stacks[i] : TransposeStack{nullptr, nullptr, 64, 64, 0};
+    p.first[i] = i < n ? tiles : (int64_t(1) << 62);
+    if (i < n) tiles += stacks[i].slots * ((stacks[i].R + 63) / 64) * ((stacks[i].C + 63) / 64);
+  }
+  p.first[kTransposeStacks] = tiles;
+  const int per = plan.n_adapters > 0 ? 4 : 1;  // (transposes alone, 27 MB: 20.5 us one to a workgroup, 25 four)
+  const int64_t blocks = plan.n_adapters + (tiles + per - 1) / per;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(static_cast<unsigned>(256 * per));
+  if (plan.n_adapters > 0) hipLaunchKernelGGL((route_prepare_kernel<true, 4>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((route_prepare_kernel<false, 1>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

@@ -154,8 +154,9 @@ struct RouteTable {
   int64_t n_items;     // route_items(T, n_adapters, chunk)
 };
 struct RoutePlan {
-  const int32_t* eid; int64_t T;
-  int32_t n_adapters;
+  Routing rt; int64_t T;
+  const int32_t* eid;  // the producer's, or null: the plan looks up the tokens' adapters itself
+  int32_t n_adapters;  // 0: no plan
   int32_t* perm;       // [T]
   RouteTable table[2]; // one for each gradient: their widths ask for chunks of their own
 };
@@ -164,7 +165,18 @@ inline int64_t route_items(int64_t T, int64_t n, int64_t chunk) { return n + T /
 // Slots of partial sums, counted over the items of adapters with more than one: k > 1 items hold more than
 // (k - 1) chunk >= k chunk / 2 tokens, so there are at most 2 T / chunk.
 inline int64_t route_parts(int64_t T, int64_t chunk) { return 2 * (T / chunk) + 1; }
-hipError_t launch_route_plan(const RoutePlan& p, hipStream_t s);
+// dst[i] [C, R] = src[i] [R, C] transposed for i < slots; contiguous, 16-byte aligned, R and C multiples of 8.
+struct TransposeStack {
+  const uint16_t* src;
+  uint16_t* dst;
+  int64_t R, C, slots;
+};
+constexpr int kTransposeStacks = 3;
+// The plan and n <= kTransposeStacks stacks in one launch, for which the plan does without eid. Up to 1024 tokens
+// (a load of each wave's): 333 tokens 8.1 us against 6.3 + 6.1 apart. With more its chains of look-ups are longer
+// than the transposes (18871 tokens: 44 us against 20.5 + 12.8) and it follows the producer.
+constexpr int64_t kPlanFirstT = 1024;
+hipError_t launch_route_prepare(const RoutePlan& p, const TransposeStack* stacks, int n, hipStream_t s);
 
 // Most tokens of an item for an output of `tiles` workgroups: about two
 // workgroups for each of 256 compute units if the adapters were one, and items long enough that the partial

@@ -291,7 +291,15 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   if (n > 0 && dx != nullptr)
     stacks[n_stacks++] = lora::TransposeStack{static_cast<const uint16_t*>(pool->A), at16(L.at), R, K, n};
   if (dx != nullptr) stacks[n_stacks++] = lora::TransposeStack{static_cast<const uint16_t*>(W), at16(L.wt), N, K, 1};
-  if (lora::transpose_stacks(stacks, n_stacks, s) != hipSuccess) return LORA_ERR_HIP;
+  lora::RoutePlan plan;
+  plan.rt = routing(pool, token_adapter, token_scale);
+  const bool plan_first = T <= lora::kPlanFirstT;
+  plan.eid = plan_first ? nullptr : at32(L.eid);
+  plan.T = T; plan.n_adapters = grads && plan_first ? static_cast<int32_t>(n) : 0; plan.perm = at32(L.perm);
+  for (int h = 0; h < 2; ++h)
+    plan.table[h] = lora::RouteTable{L.table[h].chunk, at32(L.table[h].first),
+                                     reinterpret_cast<lora::RouteItem*>(ws + L.table[h].items), L.table[h].n_items};
+  if (lora::launch_route_prepare(plan, stacks, n_stacks, s) != hipSuccess) return LORA_ERR_HIP;
   // u over dy and B^T, t over x and A
   lora::RoutedDown du, dt;
   std::memset(&du, 0, sizeof(du));
@@ -320,12 +328,8 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
       return LORA_ERR_HIP;
   }
   if (!grads) return LORA_OK;
-  lora::RoutePlan plan;
-  plan.eid = du.eid; plan.T = T; plan.n_adapters = static_cast<int32_t>(n); plan.perm = at32(L.perm);
-  for (int h = 0; h < 2; ++h)
-    plan.table[h] = lora::RouteTable{L.table[h].chunk, at32(L.table[h].first),
-                                     reinterpret_cast<lora::RouteItem*>(ws + L.table[h].items), L.table[h].n_items};
-  if (lora::launch_route_plan(plan, s) != hipSuccess) return LORA_ERR_HIP;
+  plan.n_adapters = static_cast<int32_t>(n);
+  if (!plan_first && lora::launch_route_prepare(plan, nullptr, 0, s) != hipSuccess) return LORA_ERR_HIP;
   lora::RoutedContracts c;
   std::memset(&c, 0, sizeof(c));
   c.rank = static_cast<int32_t>(R); c.ranks = pool->ranks; c.n_adapters = plan.n_adapters; c.perm = plan.perm;

@@ -39,12 +39,6 @@ void inside(const void* p, size_t n, const char* what, bool keep = false) {
 
 namespace lora {
 hipError_t zero_fill(float*, int64_t, hipStream_t) { return hipSuccess; }
-hipError_t transpose_stacks(const TransposeStack* s, int n, hipStream_t) {
-  ++launches;
-  if (n < 0 || n > kTransposeStacks) fail("transpose count");
-  for (int i = 0; i < n; ++i) inside(s[i].dst, static_cast<size_t>(s[i].slots) * s[i].R * s[i].C * 2, "transposed copy", true);
-  return hipSuccess;
-}
 hipError_t launch_routed_down(RoutedDowns p, hipStream_t) {
   ++launches;
   if (p.n < 1 || p.n > 2) fail("producer count");
@@ -82,8 +76,11 @@ hipError_t launch_routed_gemm(const LinearProblem& p, hipStream_t) {
   if (!p.routed || p.n_groups != 0) fail("gemm problem");
   return hipSuccess;
 }
-hipError_t launch_route_plan(const RoutePlan& p, hipStream_t) {
+hipError_t launch_route_prepare(const RoutePlan& p, const TransposeStack* s, int n, hipStream_t) {
   ++launches;
+  if (n < 0 || n > kTransposeStacks) fail("transpose count");
+  for (int i = 0; i < n; ++i) inside(s[i].dst, static_cast<size_t>(s[i].slots) * s[i].R * s[i].C * 2, "transposed copy", true);
+  if (p.n_adapters == 0) return hipSuccess;
   inside(p.perm, static_cast<size_t>(p.T) * 4, "perm", true);
   for (const RouteTable& t : p.table) {
     if (t.chunk < 64 || t.chunk > kRouteMaxChunk) fail("chunk");
