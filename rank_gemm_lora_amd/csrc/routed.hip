@@ -75,8 +75,10 @@ struct SortedTokens {
 };
 // order: the sorted tokens, of which `block` is one (null: blocks are of the tokens as they come). Adapters slot,
 // slot + slots, .. of the block; part `part` of K; tell: eid and blk are this workgroup's to write.
+// FAT: twice the loads in flight where the adapter has more than 16 ranks (154 registers against 128).
+template <bool FAT>
 __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f32x4 (&red)[kDownWaves][4][64],
-                                           const SortedTokens* order, int slot, int slots, int part, bool tell) {
+                                           const SortedTokens* order, int q0, int slot, int slots, int part, bool tell) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int64_t t0 = block * kRouteBlock;
@@ -98,7 +100,6 @@ __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f
     const bool same = __builtin_amdgcn_ballot_w64(r < rows && id != first) == 0;
     if (lane == 0) p.blk[block] = same ? first : -2;
   }
-  const int q0 = blockIdx.y * 64;
   const int shares = kDownWaves * p.parts;
   const int64_t kper = ((p.K + shares - 1) / shares + 31) / 32 * 32;
   const int64_t k_lo = (part * kDownWaves + wave) * kper, k_hi = min<int64_t>(p.K, k_lo + kper);
@@ -121,8 +122,8 @@ __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f
     f32x4 acc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (rows_a > 32) down_product<4, 2>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
-    else if (rows_a > 16) down_product<2, 4>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
+    if (rows_a > 32) down_product<4, FAT ? 2 : 1>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
+    else if (rows_a > 16) down_product<2, FAT ? 4 : 2>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
     else if (rows_a > 0) down_product<1, 4>(acc, xr, ar, x_off, a_off, lda_b, k_lo, k_hi, q);
 #pragma unroll
     for (int b = 0; b < 4; ++b) red[wave][b][lane] = acc[b];
@@ -172,24 +173,32 @@ __device__ __forceinline__ void sort_tokens(const RoutedDown& p, SortedTokens& o
   __syncthreads();
 }
 
-template <bool SORTED>
-__global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDowns ps) {
-  __shared__ f32x4 red[kDownWaves][4][64];
-  const int job = static_cast<int>(blockIdx.z) >= ps.z0 ? 1 : 0, z = blockIdx.z - job * ps.z0;
+// Workgroup (block, 64 ranks from q0, job and share) of the producer; mem: LDS of DownMem.
+struct DownMem {
+  f32x4 red[kDownWaves][4][64];
+  SortedTokens sorted;
+};
+template <bool FAT>
+__device__ __forceinline__ void down_group(const RoutedDowns& ps, DownMem& mem, int block, int group, int z) {
+  const int job = z >= ps.z0 ? 1 : 0;
   const RoutedDown& p = ps.d[job];
-  const bool tell = blockIdx.y == 0 && blockIdx.z == 0;
+  const bool tell = group == 0 && z == 0;
+  z -= job * ps.z0;
   const int slot = z % ps.slots, part = z / ps.slots;
-  if constexpr (SORTED) {
-    __shared__ __attribute__((aligned(16))) SortedTokens sorted;
-    sort_tokens(p, sorted);
-    if (blockIdx.x == 0 && tell && static_cast<int>(threadIdx.x) < p.T) {
-      p.order[threadIdx.x] = sorted.token[threadIdx.x];
-      p.order[p.T + threadIdx.x] = sorted.id[threadIdx.x];
+  const bool sorted = p.order != nullptr;
+  if (sorted) {
+    sort_tokens(p, mem.sorted);
+    if (block == 0 && tell && static_cast<int>(threadIdx.x) < p.T) {
+      p.order[threadIdx.x] = mem.sorted.token[threadIdx.x];
+      p.order[p.T + threadIdx.x] = mem.sorted.id[threadIdx.x];
     }
-    down_block(p, blockIdx.x, red, &sorted, slot, ps.slots, part, tell);
-  } else {
-    down_block(p, blockIdx.x, red, nullptr, slot, ps.slots, part, tell);
   }
+  down_block<FAT>(p, block, mem.red, sorted ? &mem.sorted : nullptr, group * 64, slot, ps.slots, part, tell);
+}
+
+__global__ __launch_bounds__(64 * kDownWaves) void routed_down_kernel(RoutedDowns ps) {
+  __shared__ __attribute__((aligned(16))) DownMem mem;
+  down_group<true>(ps, mem, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // t of the tokens whose sums are in parts (the ring's splits, or parts without the ring), added in order and
@@ -227,7 +236,7 @@ __device__ __forceinline__ void down_beside(const RoutedDown& p, f32x4 (&red)[kD
     while (left != 0) {
       const int i = __builtin_ctzll(left);
       left &= left - 1;
-      down_block(p, base + i * stride, red, nullptr, 0, 1, 0, false);
+      down_block<true>(p, base + i * stride, red, nullptr, blockIdx.y * 64, 0, 1, 0, false);
     }
   }
 }
@@ -248,29 +257,28 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_rest_kernel(RoutedDown
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: y = RN(x.W^T + t~.B^T + b). Workgroup: 64 outputs x BM tokens, one of S parts of K; 4 waves, 8
-// from 64 tokens on (64 tokens of 64 adapters, 4096 -> 14336: 56 against 60 us a call).
-// Stages of 64 k (128 bytes of every row of x and W) go through a ring of D LDS slots filled by
-// buffer_load .. lds, D - 1 of them in flight; 16-byte chunk c of row r lies at c ^ ((r / 2) % 8), so that a
-// wave's 16-byte reads spread over the banks. (A first form fed the MFMAs straight from memory: 16 rows of
-// 64 bytes an instruction. 64 tokens, 4096 -> 14336, took 60 us that way.)
-// The adapters come first: each adapter of each 16 tokens (a unit) is one wave's, its product over the tile's
-// 64 outputs formed apart and the rows of the adapter's own tokens put into an LDS tile (in ring slots not
-// yet in use) from which the sums start, so nothing of one adapter meets another's tokens. Units are dealt to
-// the waves of all S parts.
-// S > 1: the parts' sums meet in the workspace and few_finish_kernel adds them. (Added by the last of a
-// tile's workgroups to arrive they cost more: the device-scope fences around the arrival count write back
-// and drop an XCD's L2 every time. 1 token, 4096 -> 14336: 98 us against 31 with the second launch.)
+// Few tokens: y = RN(x.W^T + t~.B^T + b) in two launches. The first forms t~ and, in other workgroups, the base
+// product: neither needs the other, and the chain of look-ups and loads behind t~ (5 to 14 us) passes while the
+// weight streams. The second adds the base product's parts and each token's adapter.
+// (Adapters first and the base product in the same accumulators, after the producer, took: FEWFIGURES.)
+//
+// Base product: workgroup of 8 waves: 64 outputs x BM tokens, one of S parts of K. Stages of 64 k (128 bytes of
+// every row of x and W) go through a ring of D LDS slots filled by buffer_load .. lds, D - 1 of them in flight;
+// 16-byte chunk c of row r lies at c ^ ((r / 2) % 8), so that a wave's 16-byte reads spread over the banks. (A
+// first form fed the MFMAs straight from memory: 16 rows of 64 bytes an instruction. 64 tokens, 4096 -> 14336,
+// took 60 us that way.) Up to 32 tokens four waves take the first half of a stage's k and four the second, each
+// a part of its own.
 constexpr int kFewN = 64, kFewRow = 128;
 
-template <int BM, int WAVES>
+template <int BM>
 struct FewCfg {
+  static constexpr int WAVES = kDownWaves, KH = few_halves(BM);
   static constexpr int XR = BM < 32 ? 32 : BM;  // staged rows of x (one copy instruction a wave at least)
-  static constexpr int WAVES_M = (BM >= 64 ? 2 : 1) * WAVES / 4, WAVES_N = WAVES / WAVES_M;
+  static constexpr int WAVES_M = KH == 2 ? 1 : 4, WAVES_N = WAVES / KH / WAVES_M;
   static constexpr int TB = BM / WAVES_M / 16, NB = kFewN / WAVES_N / 16;  // 16 x 16 blocks of a wave
   static constexpr int STAGE = (XR + kFewN) * kFewRow;
-  static constexpr int LPS = (XR + kFewN) / 8 / WAVES;  // copy instructions of a wave and stage (8 rows each)
-  static constexpr int DELTA_SLOTS = (BM * kFewN * 4 + STAGE - 1) / STAGE;
+  static constexpr int LOADERS = KH == 2 ? 4 : 8;  // waves that copy
+  static constexpr int LPS = (XR + kFewN) / 8 / LOADERS;  // copy instructions of such a wave and stage (8 rows each)
 };
 
 // Element of the adapters' tile: 4 outputs 4 c .. of token row; the groups of 4 XOR-swizzled by row, so that
@@ -358,22 +366,25 @@ __device__ __forceinline__ void few_adapters(const RoutedFew& p, char* delta, co
   }
 }
 
-template <int BM, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, int tt, int S, int per) {
-  using C = FewCfg<BM, WAVES>;
+template <int BM, int D>
+__global__ __launch_bounds__(64 * kDownWaves, 4) void routed_few_kernel(RoutedFew p, RoutedDowns ps, int downs, int tt, int S,
+                                                                       int per) {
+  using C = FewCfg<BM>;
   constexpr int TB = C::TB, NB = C::NB;
   // (one LDS object: with several the compiler waits for every copy in flight before each LDS read, a memory
   // latency a stage. 1 token, 4096 -> 14336, no adapter: 42 us a call, 31 without)
-  __shared__ __attribute__((aligned(1024))) char ring[D * C::STAGE + 3 * BM * 4 + 16];
-  char* const delta = ring + (D - C::DELTA_SLOTS) * C::STAGE;
-  int* const ids = reinterpret_cast<int*>(ring + D * C::STAGE);  // adapter of each row of the tile (rows are
-  int* const tok = ids + BM;                                     // places of p.order), its token,
-  int* const units = tok + BM;                                   // and the first row and rank of each unit
-  int* const n_units = units + BM;
+  __shared__ __attribute__((aligned(1024))) char ring[D * C::STAGE];
+  static_assert(sizeof(DownMem) <= sizeof(ring), "the producer's LDS");
+  if (static_cast<int>(blockIdx.x) < downs) {
+    const int blocks = static_cast<int>((p.T + kRouteBlock - 1) / kRouteBlock), groups = (p.rt.rank + 63) / 64;
+    const int i = blockIdx.x / blocks;
+    down_group<false>(ps, *reinterpret_cast<DownMem*>(ring), blockIdx.x - i * blocks, i % groups, i / groups);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4;
   // the token tiles of one stretch of the weight follow one another on one XCD, in whose L2 it stays
-  const int G = gridDim.x, pid = blockIdx.x, xcd = pid % 8;
+  const int G = gridDim.x - downs, pid = blockIdx.x - downs, xcd = pid % 8;
   const int L = xcd * (G / 8) + min(xcd, G % 8) + pid / 8;
   const int tile = L / S, split = L - tile * S;
   const int tile_n = tile / tt, tile_m = tile - tile_n * tt;
@@ -381,10 +392,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, 
   const int64_t n0 = static_cast<int64_t>(tile_n) * kFewN, m0 = static_cast<int64_t>(tile_m) * BM;
   const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(BM, p.T - m0));
   const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), ldw_b = static_cast<uint32_t>(p.K * 2);
-  // (sorted: rows of all of x, at most 256 of 4 MB; else the tile's)
-  const bool sorted = BM > 16 && p.order != nullptr;
-  const __amdgpu_buffer_rsrc_t xr = sorted ? make_rsrc(p.x, static_cast<uint32_t>(p.T) * ldx_b)
-                                           : make_rsrc(p.x + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.W + n0 * p.K, static_cast<uint32_t>(rows_n) * ldw_b);
   const int kb_lo = split * per * kFewRow, kb_hi = min(static_cast<int>(p.K * 2), kb_lo + per * kFewRow);
   const int ns = (kb_hi - kb_lo + kFewRow - 1) / kFewRow;
@@ -397,69 +405,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, 
   int cb[C::LPS];
 #pragma unroll
   for (int it = 0; it < C::LPS; ++it) {
-    const int group = it * WAVES + wave;
+    const int group = it * C::LOADERS + wave;
     const bool is_w = group >= C::XR / 8;
     const int row = (is_w ? group - C::XR / 8 : group) * 8 + (lane >> 3);
     cb[it] = kb_lo + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-    if (is_w) from[it] = row < rows_n ? static_cast<uint32_t>(row) * ldw_b : kOutOfRange;
-    else if (!sorted) from[it] = row < rows_m ? static_cast<uint32_t>(row) * ldx_b : kOutOfRange;
-    else from[it] = row < rows_m ? static_cast<uint32_t>(p.order[m0 + row]) * ldx_b : kOutOfRange;
+    from[it] = row < (is_w ? rows_n : rows_m) ? static_cast<uint32_t>(row) * (is_w ? ldw_b : ldx_b) : kOutOfRange;
   }
   auto issue = [&](int st) {
+    if (C::LOADERS < C::WAVES && wave >= C::LOADERS) return;
     char* dst = ring + (st % D) * C::STAGE;
     const int at = st + rot < ns ? st + rot : st + rot - ns;
     const int kb = st < ns ? at * kFewRow : 1 << 30;  // (past the last: nothing)
 #pragma unroll
     for (int it = 0; it < C::LPS; ++it) {
-      const int group = it * WAVES + wave;
+      const int group = it * C::LOADERS + wave;
       const bool is_w = group >= C::XR / 8;
       const uint32_t off = cb[it] + kb < kb_hi ? from[it] + static_cast<uint32_t>(cb[it] + kb) : kOutOfRange;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(is_w ? wr : xr, (lds_void*)(dst + group * 1024), 16, off, 0, 0, 0);
     }
   };
 #pragma unroll
-  for (int st = 0; st < D - C::DELTA_SLOTS; ++st) issue(st);
-
-  if (tid < BM) {
-    tok[tid] = tid >= rows_m ? 0 : (sorted ? p.order[m0 + tid] : static_cast<int>(m0) + tid);
-    ids[tid] = tid >= rows_m ? -1 : (sorted ? p.order[p.T + m0 + tid] : p.rt.eid[m0 + tid]);
-  }
-  for (int i = tid; i < BM * kFewN / 4; i += 64 * WAVES) reinterpret_cast<f32x4*>(delta)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  lds_barrier();
-  // units: where an adapter shows first in a block of 16 (in adapter order: where it changes)
-  if (wave == 0) {
-    int n = 0;
-#pragma unroll
-    for (int h = 0; h < (BM + 63) / 64; ++h) {
-      const int i = 64 * h + lane;
-      bool start = i < BM && ids[i] >= 0;
-      for (int e = 1; e < (sorted ? 2 : 16); ++e) start = start && !(i % 16 >= e && ids[max(i - e, 0)] == ids[i]);
-      const uint64_t m = __builtin_amdgcn_ballot_w64(start);
-      if (start) {
-        const int rank = p.rt.ranks != nullptr ? (min(p.rt.ranks[ids[i]], p.rt.rank) + 7) & ~7 : p.rt.rank;
-        units[n + __popcll(m & ((1ull << lane) - 1))] = i | rank << 8;
-      }
-      n += __popcll(m);
-    }
-    if (lane == 0) *n_units = n;
-  }
-  lds_barrier();
-  const int nu = __builtin_amdgcn_readfirstlane(*n_units);
-  few_adapters(p, delta, ids, tok, units, nu, n0, rows_n, split * WAVES + wave, WAVES * S);
+  for (int st = 0; st < D - 1; ++st) issue(st);
 
   // lane (r, q) of block (i, j): outputs wn0 + 16 i + 4 q .. +3 of token wm0 + 16 j + r
-  const int wm0 = (wave % C::WAVES_M) * (TB * 16), wn0 = (wave / C::WAVES_M) * (NB * 16);
+  const int half = wave / (C::WAVES / C::KH), w = wave % (C::WAVES / C::KH);
+  const int wm0 = (w % C::WAVES_M) * (TB * 16), wn0 = (w / C::WAVES_M) * (NB * 16);
   f32x4 acc[NB][TB];
-  lds_barrier();
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < TB; ++j) acc[i][j] = *few_delta(delta, wm0 + 16 * j + r, wn0 / 4 + 4 * i + q);
-  if constexpr (C::DELTA_SLOTS > 1) {
-    lds_barrier();
-#pragma unroll
-    for (int st = D - C::DELTA_SLOTS; st < D - 1; ++st) issue(st);
-  }
+    for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint32_t chunk = static_cast<uint32_t>((q ^ ((r >> 1) & 7)) * 16);
   const uint32_t xo = static_cast<uint32_t>((wm0 + r) * kFewRow) + chunk;
   const uint32_t wo = static_cast<uint32_t>((C::XR + wn0 + r) * kFewRow) + chunk;
@@ -469,12 +444,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, 
     issue(st + D - 1);
     const char* sp = ring + (st % D) * C::STAGE;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int k = 0; k < 2 / C::KH; ++k) {
+      const uint32_t kk = static_cast<uint32_t>(C::KH == 2 ? half : k) * 64u;
       bf16x8 wf[NB], xf[TB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i) wf[i] = *reinterpret_cast<const bf16x8*>(sp + ((wo ^ (kk * 64u)) + i * 16 * kFewRow));
+      for (int i = 0; i < NB; ++i) wf[i] = *reinterpret_cast<const bf16x8*>(sp + ((wo ^ kk) + i * 16 * kFewRow));
 #pragma unroll
-      for (int j = 0; j < TB; ++j) xf[j] = *reinterpret_cast<const bf16x8*>(sp + ((xo ^ (kk * 64u)) + j * 16 * kFewRow));
+      for (int j = 0; j < TB; ++j) xf[j] = *reinterpret_cast<const bf16x8*>(sp + ((xo ^ kk) + j * 16 * kFewRow));
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -484,47 +460,62 @@ __global__ __launch_bounds__(64 * WAVES, 2) void routed_few_kernel(RoutedFew p, 
   }
   wait_vmem();  // (copies past the end)
 
-  if (S > 1) {
-    float* mine = p.part + (static_cast<int64_t>(tile) * S + split) * (BM * kFewN) + wave * (NB * TB * 256) + lane * 4;
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int j = 0; j < TB; ++j) *reinterpret_cast<f32x4*>(mine + (i * TB + j) * 256) = acc[i][j];
-    return;
-  }
+  float* mine = p.part + ((static_cast<int64_t>(tile_n) * S + split) * C::KH + half) * p.T * kFewN;
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < TB; ++j)
-      if (wm0 + 16 * j + r < rows_m) few_store(p, acc[i][j], tok[wm0 + 16 * j + r], n0, rows_n, wn0 + 16 * i + 4 * q);
+    for (int j = 0; j < TB; ++j) {
+      const int row = wm0 + 16 * j + r;
+      if (row < rows_m) *reinterpret_cast<f32x4*>(mine + (m0 + row) * kFewN + wn0 + 16 * i + 4 * q) = acc[i][j];
+    }
 }
 
-// The parts of a tile added in order. Workgroup: one tile's 16 x 16 block per wave.
-template <int BM, int WAVES>
-__global__ __launch_bounds__(256) void few_finish_kernel(RoutedFew p, int tt, int S) {
-  using C = FewCfg<BM, WAVES>;
-  const int lane = threadIdx.x & 63;
-  const int b = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // block of the tile
-  const int tile = blockIdx.x, tile_n = tile / tt, tile_m = tile - tile_n * tt;
-  const int64_t n0 = static_cast<int64_t>(tile_n) * kFewN, m0 = static_cast<int64_t>(tile_m) * BM;
-  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(BM, p.T - m0));
-  const float* all = p.part + static_cast<int64_t>(tile) * S * (BM * kFewN) + b * 256 + lane * 4;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  // (eight parts' loads at a time before their adds; a part past the last reads the last again, unused)
-  for (int z = 0; z < S; z += 8) {
-    f32x4 w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      w[k] = *reinterpret_cast<const f32x4*>(all + static_cast<int64_t>(min(z + k, S - 1)) * (BM * kFewN));
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (z + k < S) v += w[k];
+// Workgroup: 64 outputs x FB tokens (places of the sorted order, where there is one). Each adapter of each 16
+// tokens (a unit) is one wave's, its product over the 64 outputs formed apart and the rows of the adapter's own
+// tokens put into an LDS tile, so nothing of one adapter meets another's tokens. The parts of the base product
+// are added in order, then the adapter's sum and the bias; their loads are in flight meanwhile.
+template <int FB>
+__global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int parts) {
+  __shared__ __attribute__((aligned(16))) char delta[FB * kFewN * 4];
+  __shared__ int ids[FB], tok[FB], units[FB], n_units;  // adapter and token of each row; first row and rank of each unit
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kFewN, m0 = static_cast<int64_t>(blockIdx.y) * FB;
+  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(FB, p.T - m0));
+  const bool sorted = p.order != nullptr;
+  const int row = tid >> 4, c = tid & 15;  // this thread's token and 4 outputs
+  const int64_t place = m0 + min(row, rows_m - 1), token = sorted ? p.order[place] : place;
+  if (tid < FB) {
+    tok[tid] = tid >= rows_m ? 0 : (sorted ? p.order[m0 + tid] : static_cast<int>(m0) + tid);
+    ids[tid] = tid >= rows_m ? -1 : (sorted ? p.order[p.T + m0 + tid] : p.rt.eid[m0 + tid]);
   }
-  const int wave = b / (C::NB * C::TB), i = b % (C::NB * C::TB) / C::TB, j = b % C::TB;
-  const int wm0 = (wave % C::WAVES_M) * (C::TB * 16), wn0 = (wave / C::WAVES_M) * (C::NB * 16);
-  const int row = wm0 + 16 * j + (lane & 15);
-  if (row < rows_m)
-    few_store(p, v, p.order != nullptr ? p.order[m0 + row] : m0 + row, n0, rows_n, wn0 + 16 * i + 4 * (lane >> 4));
+  *few_delta(delta, row, c) = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float* base = p.part + (static_cast<int64_t>(blockIdx.x) * parts * p.T + token) * kFewN + 4 * c;
+  f32x4 w[8];  // (a part past the last reads the last again, unused)
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const f32x4*>(base + min(k, parts - 1) * p.T * kFewN);
+  lds_barrier();
+  // units: where an adapter shows first in a block of 16 (in adapter order: where it changes)
+  if (wave == 0) {
+    bool start = lane < FB && ids[lane % FB] >= 0;
+    for (int e = 1; e < (sorted ? 2 : 16); ++e)
+      start = start && !(lane % 16 >= e && ids[max(lane % FB - e, 0)] == ids[lane % FB]);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(start);
+    if (start) {
+      const int a = ids[lane];
+      const int rank = p.rt.ranks != nullptr ? (min(p.rt.ranks[a], p.rt.rank) + 7) & ~7 : p.rt.rank;
+      units[__popcll(m & ((1ull << lane) - 1))] = lane | rank << 8;
+    }
+    if (lane == 0) n_units = __popcll(m);
+  }
+  lds_barrier();
+  few_adapters(p, delta, ids, tok, units, __builtin_amdgcn_readfirstlane(n_units), n0, rows_n, wave, FB / 4);
+  lds_barrier();
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < parts) v += w[k];
+  for (int k = 8; k < parts; ++k) v += *reinterpret_cast<const f32x4*>(base + k * p.T * kFewN);
+  if (row < rows_m) few_store(p, v + *few_delta(delta, row, c), token, n0, rows_n, 4 * c);
 }
 
 // ---------------------------------------------------------------------------
@@ -814,6 +805,14 @@ __global__ __launch_bounds__(256) void routed_reduce_kernel(RoutedContracts ps) 
 
 }  // namespace
 
+// The producer without the ring: slots and z0 of p, returns the workgroups of a block and 64 ranks.
+static unsigned down_shares(RoutedDowns& p) {
+  const RoutedDown& d = p.d[0];
+  p.slots = down_slots(d.T, d.rt.n_adapters, d.order != nullptr);
+  p.z0 = p.slots * d.parts;
+  return static_cast<unsigned>(p.z0 + (p.n > 1 ? p.slots * p.d[1].parts : 0));
+}
+
 hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
   const RoutedDown& d = p.d[0];
   if (d.T <= 0) return hipSuccess;
@@ -823,13 +822,8 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
   for (int i = 0; i < p.n; ++i) join = join || p.d[i].splits > 1 || (p.d[i].splits == 0 && p.d[i].parts > 1);
   hipError_t e = hipSuccess;
   if (d.splits == 0) {
-    const int slots = down_slots(d.T, d.rt.n_adapters);
-    p.slots = slots;
-    p.z0 = slots * d.parts;
-    const int z = p.z0 + (p.n > 1 ? slots * p.d[1].parts : 0);
-    const dim3 grid(blocks, groups, static_cast<unsigned>(z));
-    if (d.order != nullptr) hipLaunchKernelGGL(routed_down_kernel<true>, grid, dim3(64 * kDownWaves), 0, s, p);
-    else hipLaunchKernelGGL(routed_down_kernel<false>, grid, dim3(64 * kDownWaves), 0, s, p);
+    const dim3 grid(blocks, groups, down_shares(p));
+    hipLaunchKernelGGL(routed_down_kernel, grid, dim3(64 * kDownWaves), 0, s, p);
     e = hipGetLastError();
   } else {
     e = launch_routed_ring(p, s);
@@ -854,24 +848,28 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
 }
 
 namespace {
-template <int BM, int D, int WAVES>
-hipError_t few(const RoutedFew& p, const FewPlan& f, hipStream_t s) {
-  hipLaunchKernelGGL((routed_few_kernel<BM, D, WAVES>), dim3(static_cast<unsigned>(f.tiles * f.splits)), dim3(64 * WAVES), 0, s, p,
-                     f.token_tiles, f.splits, f.stages);
-  if (f.splits > 1)
-    hipLaunchKernelGGL((few_finish_kernel<BM, WAVES>), dim3(static_cast<unsigned>(f.tiles), BM * kFewN / 1024), dim3(256), 0, s,
-                       p, f.token_tiles, f.splits);
+template <int BM, int D>
+hipError_t few(const RoutedFew& p, RoutedDowns downs, const FewPlan& f, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((p.T + kRouteBlock - 1) / kRouteBlock);
+  const unsigned first = blocks * static_cast<unsigned>((p.rt.rank + 63) / 64) * down_shares(downs);
+  hipLaunchKernelGGL((routed_few_kernel<BM, D>), dim3(first + static_cast<unsigned>(f.tiles * f.splits)),
+                     dim3(64 * kDownWaves), 0, s, p, downs, static_cast<int>(first), f.token_tiles, f.splits, f.stages);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned x = static_cast<unsigned>(f.tiles / f.token_tiles);
+  if (BM == 16) hipLaunchKernelGGL((few_finish_kernel<16>), dim3(x), dim3(256), 0, s, p, f.parts);
+  else hipLaunchKernelGGL((few_finish_kernel<32>), dim3(x, static_cast<unsigned>((p.T + 31) / 32)), dim3(512), 0, s, p, f.parts);
   return hipGetLastError();
 }
 }  // namespace
 
-hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s) {
+hipError_t launch_routed_few(const RoutedFew& p, const RoutedDowns& downs, hipStream_t s) {
   const FewPlan f = few_plan(p.T, p.K, p.N);
   switch (f.bm) {
-    case 16: return few<16, 6, 4>(p, f, s);
-    case 32: return few<32, 6, 4>(p, f, s);
-    case 64: return few<64, 4, 8>(p, f, s);
-    default: return few<128, 3, 8>(p, f, s);
+    case 16: return few<16, 6>(p, downs, f, s);
+    case 32: return few<32, 6>(p, downs, f, s);
+    case 64: return few<64, 4>(p, downs, f, s);
+    default: return few<128, 3>(p, downs, f, s);
   }
 }
 

@@ -30,6 +30,12 @@ struct RoutedDown {
                        // each place, then its adapter; in token order within one adapter, those without an
                        // adapter last. The blocks of 16 are of this order
 };
+// Few tokens: t~ (as hi and mid) and the base product over a ring of LDS stages in one launch, then the sum.
+// Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
+// 4096 -> 14336: 68 against 76 us), with mixed ones it is slower up to there and beyond (121 against 86 us).
+constexpr int64_t kFewMaxT = 256;
+// (one block of 16 is as good in any order)
+inline bool sorts_tokens(int64_t T) { return T > kRouteBlock && T <= kFewMaxT; }
 constexpr int kRingBlock = 128;
 constexpr int64_t kRingMinT = 1025;
 inline int64_t ring_blocks(int64_t T) { return T >= kRingMinT ? (T + kRingBlock - 1) / kRingBlock : 0; }
@@ -54,17 +60,20 @@ inline size_t ring_bytes(int64_t T, int64_t K, int64_t ldt) {
   ring_plan(T, K, &S, &ks);
   return S > 1 ? static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(ldt) * 4 : 0;
 }
-// Adapters that a block of 16 tokens can hold.
-inline int down_slots(int64_t T, int n_adapters) {
-  const int64_t m = T < kRouteBlock ? T : kRouteBlock;
-  return static_cast<int>(n_adapters < m ? (n_adapters > 0 ? n_adapters : 1) : m);
+// Workgroups that share the adapters of a block of 16 tokens: as many as it can hold, in sorted blocks (which
+// hold about as many adapters together as there are blocks and adapters) one more than their mean.
+inline int down_slots(int64_t T, int n_adapters, bool sorted) {
+  const int64_t m = T < kRouteBlock ? T : kRouteBlock, blocks = (T + kRouteBlock - 1) / kRouteBlock;
+  int64_t n = n_adapters < m ? (n_adapters > 0 ? n_adapters : 1) : m;
+  if (sorted && (n_adapters + blocks - 1) / blocks + 1 < n) n = (n_adapters + blocks - 1) / blocks + 1;
+  return static_cast<int>(n);
 }
 // Parts of K of the producer without the ring: the fewest estimated microseconds. A wave has 256 k (128 above
 // 32 ranks) in flight, each such round about 1.5 us; joining parts takes a launch of 3.5 us; more than 256
 // workgroups do not help (sorted blocks hold about as many adapters as there are blocks and adapters).
 inline int down_parts(int64_t T, int64_t K, int64_t rank, int n_adapters) {
   if (T >= kRingMinT) return 1;
-  const int64_t blocks = (T + kRouteBlock - 1) / kRouteBlock, slots = down_slots(T, n_adapters);
+  const int64_t blocks = (T + kRouteBlock - 1) / kRouteBlock, slots = down_slots(T, n_adapters, sorts_tokens(T));
   const int64_t units = blocks * slots < blocks + n_adapters ? blocks * slots : blocks + n_adapters;
   const int64_t wgs = units * ((rank + 63) / 64), round = 8 * (rank > 32 ? 128 : 256);
   int best = 1;
@@ -89,27 +98,22 @@ hipError_t launch_routed_ring(RoutedDowns p, hipStream_t s);  // (gemm.hip)
 hipError_t launch_routed_down(RoutedDowns p, hipStream_t s);
 
 constexpr int kDownWaves = 8;
-// Few tokens: base product, adapters and bias in one kernel over a ring of LDS stages (t~ from the
-// rank-wide producer as hi and mid).
-// Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
-// 4096 -> 14336: 68 against 76 us), with mixed ones it is slower up to there and beyond (121 against 86 us).
-constexpr int64_t kFewMaxT = 256;
-// (one block of 16 is as good in any order)
-inline bool sorts_tokens(int64_t T) { return T > kRouteBlock && T <= kFewMaxT; }
 // Beyond it, up to 1024 tokens, the few-token kernel still takes outputs so narrow that the hot GEMM's 128 x 128
 // tiles would leave half of the compute units without one (tokens as they come, not sorted).
 inline bool few_path(int64_t T, int64_t N) {
   return T <= kFewMaxT || (T < kRingMinT && (T + 127) / 128 * ((N + 127) / 128) <= 128);
 }
+// Parts that one workgroup of the base product writes: halves of a stage's k up to 32 tokens.
+constexpr int few_halves(int bm) { return bm < 64 ? 2 : 1; }
 struct FewPlan {
   int bm;            // tokens of a tile
   int token_tiles;
   int64_t tiles;     // all tiles (64 outputs each)
   int splits, stages;  // parts of K, 64-k stages of each
+  int parts;           // partial sums of an output
 };
 // Token tiles of 16, 32, 64 or 128; K in as many parts as bring two workgroups to each of 256 compute
-// units, at least 4 stages each. Up to 24 stages stay in one part: the second launch costs what it saves
-// (1 token, 1536 -> 1536: figures beside few_finish_kernel).
+// units, at least 4 stages each.
 inline FewPlan few_plan(int64_t T, int64_t K, int64_t N) {
   FewPlan f;
   f.bm = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
@@ -117,15 +121,16 @@ inline FewPlan few_plan(int64_t T, int64_t K, int64_t N) {
   f.tiles = (N + 63) / 64 * f.token_tiles;
   const int64_t nk = (K + 63) / 64;
   int64_t s = 512 / f.tiles;
-  s = s > 16 ? 16 : s;
+  s = s > 8 ? 8 : s;
   s = s > nk / 4 ? nk / 4 : s;
-  s = s < 1 || nk <= 24 ? 1 : s;
+  s = s < 1 ? 1 : s;
   f.stages = static_cast<int>((nk + s - 1) / s);
   f.splits = static_cast<int>((nk + f.stages - 1) / f.stages);
+  f.parts = f.splits * few_halves(f.bm);
   return f;
 }
-inline size_t few_part_bytes(const FewPlan& f) {
-  return f.splits > 1 ? static_cast<size_t>(f.tiles) * f.splits * f.bm * 64 * 4 : 0;
+inline size_t few_part_bytes(const FewPlan& f, int64_t T) {
+  return static_cast<size_t>(f.tiles / f.token_tiles) * f.parts * static_cast<size_t>(T) * 64 * 4;
 }
 struct RoutedFew {
   const uint16_t* x; int64_t ldx;
@@ -136,9 +141,9 @@ struct RoutedFew {
   const uint16_t *hi, *mid; int64_t ldt;
   RoutedGemm rt;
   const int32_t* order;  // [2, T]: the producer's, null without one
-  float* part;           // [tiles, splits, bm, 64]
+  float* part;           // [ceil(N / 64), parts, T, 64]
 };
-hipError_t launch_routed_few(const RoutedFew& p, hipStream_t s);
+hipError_t launch_routed_few(const RoutedFew& p, const RoutedDowns& downs, hipStream_t s);
 
 // Tokens sorted by adapter (in token order within one), and the work items of a contraction over them: an
 // adapter's tokens in ceil(count / chunk) items of nearly equal length (one, empty, without tokens), the

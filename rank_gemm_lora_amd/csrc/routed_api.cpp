@@ -32,7 +32,7 @@ struct Take {  // regions of a workspace, each 256-byte aligned
 
 // Partial sums of the few-token kernel for T tokens, K inputs and N outputs.
 size_t few_bytes(int64_t T, int64_t K, int64_t N) {
-  return lora::few_path(T, N) ? lora::few_part_bytes(lora::few_plan(T, K, N)) : 0;
+  return lora::few_path(T, N) ? lora::few_part_bytes(lora::few_plan(T, K, N), T) : 0;
 }
 
 // Partial sums of the rank-wide producer for T tokens and K inputs.
@@ -40,9 +40,10 @@ size_t join_bytes(int64_t T, int64_t K, int64_t n, int64_t R) {
   return std::max(lora::ring_bytes(T, K, lora::rank_pad(R)), lora::down_bytes(T, K, R, static_cast<int>(n)));
 }
 
-void plan_down(lora::RoutedDown& d) {
+// few: it runs beside the base product of the few-token kernel (in one part: its time passes there).
+void plan_down(lora::RoutedDown& d, bool few) {
   lora::ring_plan(d.T, d.K, &d.splits, &d.ks);
-  d.parts = lora::down_parts(d.T, d.K, d.rt.rank, d.rt.n_adapters);
+  d.parts = few ? 1 : lora::down_parts(d.T, d.K, d.rt.rank, d.rt.n_adapters);
 }
 
 struct FwdLayout {
@@ -155,10 +156,11 @@ void pool_spans(const lora_pool* pool, const int32_t* token_adapter, const float
   s[5] = n > 0 ? span2d(token_scale, 1, T, T, 4) : Span{};
 }
 
-// The base product with the second adapter product, over what the producer `d` wrote; B [n, N, rank].
-hipError_t launch_product(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N, const void* bias,
-                          void* y, int64_t ldy, const lora::RoutedDown& d, const void* B, const lora_pool* pool,
-                          void* part, hipStream_t s) {
+// The rank-wide products and the base product with the adapters of the first of them; B [n, N, rank].
+hipError_t launch_layer(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N, const void* bias,
+                        void* y, int64_t ldy, const lora::RoutedDowns& downs, const void* B, const lora_pool* pool,
+                        void* part, hipStream_t s) {
+  const lora::RoutedDown& d = downs.d[0];
   lora::RoutedGemm rt;
   rt.B = B; rt.eid = d.eid; rt.blk = d.blk; rt.ranks = pool->ranks; rt.rank = pool->rank;
   if (lora::few_path(T, N)) {
@@ -171,8 +173,10 @@ hipError_t launch_product(const void* x, int64_t T, int64_t K, int64_t ldx, cons
     f.hi = d.hi; f.mid = d.mid; f.ldt = d.ldt;
     f.rt = rt;
     f.part = static_cast<float*>(part); f.order = d.order;
-    return lora::launch_routed_few(f, s);
+    return lora::launch_routed_few(f, downs, s);
   }
+  const hipError_t e = lora::launch_routed_down(downs, s);
+  if (e != hipSuccess) return e;
   LinearProblem p;
   std::memset(&p, 0, sizeof(p));
   p.x = x; p.ldx = ldx; p.W = W; p.bias = bias; p.y = y; p.ldy = ldy; p.T = T; p.N = N; p.K = K;
@@ -226,11 +230,12 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   if (few) d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]), d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
   d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
-  plan_down(d);
+  plan_down(d, few);
   d.ring = reinterpret_cast<int32_t*>(ws + L.ring);
   d.tpart = reinterpret_cast<float*>(ws + L.part);
-  if (lora::launch_routed_down(lora::RoutedDowns{{d, d}, 1, 0, 0}, s) != hipSuccess) return LORA_ERR_HIP;
-  return launch_product(x, T, K, ldx, W, N, bias, y, ldy, d, pool->B, pool, ws + L.few, s) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+  const lora::RoutedDowns downs{{d, d}, 1, 0, 0};
+  return launch_layer(x, T, K, ldx, W, N, bias, y, ldy, downs, pool->B, pool, ws + L.few, s) == hipSuccess
+             ? LORA_OK : LORA_ERR_HIP;
 }
 
 size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank) {
@@ -318,15 +323,15 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   dt.A = static_cast<const uint16_t*>(pool->A);
   dt.hi = at16(L.t[0]); dt.mid = at16(L.t[1]); dt.lo = at16(L.t[2]);
   dt.tpart = reinterpret_cast<float*>(ws + L.tpart);
-  plan_down(du);
-  plan_down(dt);
+  const bool few = dx != nullptr && lora::few_path(T, K);
+  plan_down(du, few);
+  plan_down(dt, few);
   const bool want_u = dx != nullptr || dA != nullptr, want_t = dB != nullptr && n > 0;
   lora::RoutedDowns downs{{want_u ? du : dt, dt}, want_u && want_t ? 2 : 1, 0, 0};
-  if (lora::launch_routed_down(downs, s) != hipSuccess) return LORA_ERR_HIP;
-  if (dx != nullptr) {
-    if (launch_product(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, du, at16(L.at), pool, ws + L.few, s) != hipSuccess)
-      return LORA_ERR_HIP;
-  }
+  const hipError_t e = dx != nullptr ? launch_layer(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, downs, at16(L.at),
+                                                    pool, ws + L.few, s)
+                                     : lora::launch_routed_down(downs, s);
+  if (e != hipSuccess) return LORA_ERR_HIP;
   if (!grads) return LORA_OK;
   plan.n_adapters = static_cast<int32_t>(n);
   if (!plan_first && lora::launch_route_prepare(plan, nullptr, 0, s) != hipSuccess) return LORA_ERR_HIP;

@@ -39,8 +39,7 @@ void inside(const void* p, size_t n, const char* what, bool keep = false) {
 
 namespace lora {
 hipError_t zero_fill(float*, int64_t, hipStream_t) { return hipSuccess; }
-hipError_t launch_routed_down(RoutedDowns p, hipStream_t) {
-  ++launches;
+static void check_downs(const RoutedDowns& p) {
   if (p.n < 1 || p.n > 2) fail("producer count");
   for (int i = 0; i < p.n; ++i) {
     const RoutedDown& d = p.d[i];
@@ -60,14 +59,21 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t) {
     if (d.order != nullptr) inside(d.order, static_cast<size_t>(d.T) * 8, "order", true);
     if (sorts_tokens(d.T) != (d.order != nullptr)) fail("order given where it is used");
   }
+}
+hipError_t launch_routed_down(RoutedDowns p, hipStream_t) {
+  ++launches;
+  check_downs(p);
   return hipSuccess;
 }
-hipError_t launch_routed_few(const RoutedFew& p, hipStream_t) {
+hipError_t launch_routed_few(const RoutedFew& p, const RoutedDowns& downs, hipStream_t) {
   ++launches;
+  check_downs(downs);
+  for (int i = 0; i < downs.n; ++i)
+    if (downs.d[i].splits != 0 || downs.d[i].parts != 1) fail("a producer beside the base product is in one part");
   const FewPlan f = few_plan(p.T, p.K, p.N);
   const int64_t nk = (p.K + 63) / 64;
   if (static_cast<int64_t>(f.splits) * f.stages < nk || static_cast<int64_t>(f.splits - 1) * f.stages >= nk) fail("parts of K");
-  if (f.splits > 1) inside(p.part, few_part_bytes(f), "tile partial sums", true);
+  inside(p.part, few_part_bytes(f, p.T), "partial sums of the base product", true);
   if (p.mid == nullptr) fail("mid");
   return hipSuccess;
 }
