@@ -260,7 +260,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_rest_kernel(RoutedDown
 // Few tokens: y = RN(x.W^T + t~.B^T + b) in two launches. The first forms t~ and, in other workgroups, the base
 // product: neither needs the other, and the chain of look-ups and loads behind t~ (5 to 14 us) passes while the
 // weight streams. The second adds the base product's parts and each token's adapter.
-// (Adapters first and the base product in the same accumulators, after the producer, took: FEWFIGURES.)
+// (Adapters first and the base product in the same accumulators, after the producer: 64 tokens of 64 adapters,
+// 4096 -> 14336, 54.8 us against 42.9; 203 of 32, 1536 -> 8960, 39.0 against 32.6; one token, 1536 -> 1536, 14.8
+// against 11.8; only 256 of 64, 4096 -> 14336, 85 against 90.)
 //
 // Base product: workgroup of 8 waves: 64 outputs x BM tokens, one of S parts of K. Stages of 64 k (128 bytes of
 // every row of x and W) go through a ring of D LDS slots filled by buffer_load .. lds, D - 1 of them in flight;
@@ -805,36 +807,35 @@ __global__ __launch_bounds__(256) void routed_reduce_kernel(RoutedContracts ps) 
 
 }  // namespace
 
-// The producer without the ring: slots and z0 of p, returns the workgroups of a block and 64 ranks.
+// The producer without the ring: slots and z0 of p, returns the workgroups of a block and 64 ranks. Slots for
+// blocks of twice the mean while the workgroups stay below 96 and pass beside others (203 tokens of 32 adapters,
+// 1536 -> 8960: 31.9 us against 34.4 with one more than the mean; 256 of 16 in five parts, 8960 -> 1536: 43.1
+// against 41.7).
 static unsigned down_shares(RoutedDowns& p) {
   const RoutedDown& d = p.d[0];
-  p.slots = down_slots(d.T, d.rt.n_adapters, d.order != nullptr);
+  const int64_t units = (d.T + kRouteBlock - 1) / kRouteBlock * ((d.rt.rank + 63) / 64);
+  const int64_t parts = d.parts + (p.n > 1 ? p.d[1].parts : 0);
+  p.slots = down_slots(d.T, d.rt.n_adapters, d.order != nullptr, 2);
+  if (units * p.slots * parts > 96) p.slots = down_slots(d.T, d.rt.n_adapters, d.order != nullptr, 1);
   p.z0 = p.slots * d.parts;
-  return static_cast<unsigned>(p.z0 + (p.n > 1 ? p.slots * p.d[1].parts : 0));
+  return static_cast<unsigned>(p.slots * parts);
 }
 
-hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
+// What the first launch of a producer leaves.
+static hipError_t launch_rest(const RoutedDowns& p, hipStream_t s) {
   const RoutedDown& d = p.d[0];
-  if (d.T <= 0) return hipSuccess;
   const unsigned blocks = static_cast<unsigned>((d.T + kRouteBlock - 1) / kRouteBlock);
   const unsigned groups = static_cast<unsigned>((d.rt.rank + 63) / 64), jobs = static_cast<unsigned>(p.n);
   bool join = false;
   for (int i = 0; i < p.n; ++i) join = join || p.d[i].splits > 1 || (p.d[i].splits == 0 && p.d[i].parts > 1);
-  hipError_t e = hipSuccess;
-  if (d.splits == 0) {
-    const dim3 grid(blocks, groups, down_shares(p));
-    hipLaunchKernelGGL(routed_down_kernel, grid, dim3(64 * kDownWaves), 0, s, p);
-    e = hipGetLastError();
-  } else {
-    e = launch_routed_ring(p, s);
-  }
   // (up to kRingAdapters adapters every block is the ring's)
   const unsigned beside = d.splits > 0 && d.rt.n_adapters > kRingAdapters ? (blocks < 512 ? blocks : 512) : 0;
   const unsigned joins = join ? static_cast<unsigned>((d.T + 2 * kDownWaves - 1) / (2 * kDownWaves)) : 0;
   // (one launch for both where it is short: 4977 tokens 7.2 us against 5.4 + 4.7; the registers of the blocks slow
   // many joins down: 18871 tokens, both products, 26 us against 15.4 + 4.8)
   const bool apart = d.T > 8192;
-  if (e == hipSuccess && beside > 0) {
+  hipError_t e = hipSuccess;
+  if (beside > 0) {
     const unsigned x = beside + (apart ? 0 : joins);
     hipLaunchKernelGGL(routed_rest_kernel<true>, dim3(x, groups, jobs), dim3(64 * kDownWaves), 0, s, p,
                        static_cast<int>(beside));
@@ -847,6 +848,21 @@ hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
   return e;
 }
 
+hipError_t launch_routed_down(RoutedDowns p, hipStream_t s) {
+  const RoutedDown& d = p.d[0];
+  if (d.T <= 0) return hipSuccess;
+  hipError_t e = hipSuccess;
+  if (d.splits == 0) {
+    const dim3 grid(static_cast<unsigned>((d.T + kRouteBlock - 1) / kRouteBlock),
+                    static_cast<unsigned>((d.rt.rank + 63) / 64), down_shares(p));
+    hipLaunchKernelGGL(routed_down_kernel, grid, dim3(64 * kDownWaves), 0, s, p);
+    e = hipGetLastError();
+  } else {
+    e = launch_routed_ring(p, s);
+  }
+  return e != hipSuccess ? e : launch_rest(p, s);
+}
+
 namespace {
 template <int BM, int D>
 hipError_t few(const RoutedFew& p, RoutedDowns downs, const FewPlan& f, hipStream_t s) {
@@ -855,6 +871,7 @@ hipError_t few(const RoutedFew& p, RoutedDowns downs, const FewPlan& f, hipStrea
   hipLaunchKernelGGL((routed_few_kernel<BM, D>), dim3(first + static_cast<unsigned>(f.tiles * f.splits)),
                      dim3(64 * kDownWaves), 0, s, p, downs, static_cast<int>(first), f.token_tiles, f.splits, f.stages);
   hipError_t e = hipGetLastError();
+  if (e == hipSuccess) e = launch_rest(downs, s);
   if (e != hipSuccess) return e;
   const unsigned x = static_cast<unsigned>(f.tiles / f.token_tiles);
   if (BM == 16) hipLaunchKernelGGL((few_finish_kernel<16>), dim3(x), dim3(256), 0, s, p, f.parts);

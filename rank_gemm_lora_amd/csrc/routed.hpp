@@ -61,19 +61,19 @@ inline size_t ring_bytes(int64_t T, int64_t K, int64_t ldt) {
   return S > 1 ? static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(ldt) * 4 : 0;
 }
 // Workgroups that share the adapters of a block of 16 tokens: as many as it can hold, in sorted blocks (which
-// hold about as many adapters together as there are blocks and adapters) one more than their mean.
-inline int down_slots(int64_t T, int n_adapters, bool sorted) {
+// hold about as many adapters together as there are blocks and adapters) one more than `times` their mean.
+inline int down_slots(int64_t T, int n_adapters, bool sorted, int times) {
   const int64_t m = T < kRouteBlock ? T : kRouteBlock, blocks = (T + kRouteBlock - 1) / kRouteBlock;
-  int64_t n = n_adapters < m ? (n_adapters > 0 ? n_adapters : 1) : m;
-  if (sorted && (n_adapters + blocks - 1) / blocks + 1 < n) n = (n_adapters + blocks - 1) / blocks + 1;
-  return static_cast<int>(n);
+  const int64_t n = n_adapters < m ? (n_adapters > 0 ? n_adapters : 1) : m;
+  const int64_t mean = times * ((n_adapters + blocks - 1) / blocks) + 1;
+  return static_cast<int>(sorted && mean < n ? mean : n);
 }
 // Parts of K of the producer without the ring: the fewest estimated microseconds. A wave has 256 k (128 above
 // 32 ranks) in flight, each such round about 1.5 us; joining parts takes a launch of 3.5 us; more than 256
 // workgroups do not help (sorted blocks hold about as many adapters as there are blocks and adapters).
 inline int down_parts(int64_t T, int64_t K, int64_t rank, int n_adapters) {
   if (T >= kRingMinT) return 1;
-  const int64_t blocks = (T + kRouteBlock - 1) / kRouteBlock, slots = down_slots(T, n_adapters, sorts_tokens(T));
+  const int64_t blocks = (T + kRouteBlock - 1) / kRouteBlock, slots = down_slots(T, n_adapters, sorts_tokens(T), 1);
   const int64_t units = blocks * slots < blocks + n_adapters ? blocks * slots : blocks + n_adapters;
   const int64_t wgs = units * ((rank + 63) / 64), round = 8 * (rank > 32 ? 128 : 256);
   int best = 1;
@@ -84,9 +84,24 @@ inline int down_parts(int64_t T, int64_t K, int64_t rank, int n_adapters) {
   }
   return best;
 }
-inline size_t down_bytes(int64_t T, int64_t K, int64_t rank, int n_adapters) {
-  const int s = down_parts(T, K, rank, n_adapters);
-  return s > 1 ? static_cast<size_t>(s) * static_cast<size_t>(T) * static_cast<size_t>(rank_pad(rank)) * 4 : 0;
+// Of K inputs beside a base product of K0 inputs and N outputs: one part if its time passes there, else the fewest
+// estimated microseconds. Beside the weight's stream and with fewer loads in flight (256 k up to 16 ranks, 128 up
+// to 32, else 64) a round is about 4 us up to 16 ranks, 2.5 above; the launch that joins parts 5.
+// (256 tokens, 8960 -> 1536, rank 64: 95 us in one part, 42 in five.)
+inline int down_parts_beside(int64_t K, int64_t K0, int64_t N, int64_t rank) {
+  const int64_t round = 8 * (rank > 32 ? 64 : (rank > 16 ? 128 : 256));
+  const double each = rank > 16 ? 2.5 : 4.0, base = 4 + static_cast<double>(K0 * N * 2) / 3.5e6;
+  int best = 1;
+  double cost = 0;
+  for (int s = 1; s <= 8; ++s) {
+    const double over = each * static_cast<double>((K + s * round - 1) / (s * round)) - base;
+    const double c = (over < 0 ? 0 : over) + (s > 1 ? 5 : 0);
+    if (s == 1 || c < cost) best = s, cost = c;
+  }
+  return best;
+}
+inline size_t part_bytes(int parts, int64_t T, int64_t rank) {
+  return parts > 1 ? static_cast<size_t>(parts) * static_cast<size_t>(T) * static_cast<size_t>(rank_pad(rank)) * 4 : 0;
 }
 // One product, or two of the same tokens and routing (x against A, dy against B^T) in the same launches. z0:
 // the first's share of the grid's z; slots: workgroups that share a block's adapters without the ring.

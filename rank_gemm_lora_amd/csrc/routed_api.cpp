@@ -35,15 +35,18 @@ size_t few_bytes(int64_t T, int64_t K, int64_t N) {
   return lora::few_path(T, N) ? lora::few_part_bytes(lora::few_plan(T, K, N), T) : 0;
 }
 
-// Partial sums of the rank-wide producer for T tokens and K inputs.
-size_t join_bytes(int64_t T, int64_t K, int64_t n, int64_t R) {
-  return std::max(lora::ring_bytes(T, K, lora::rank_pad(R)), lora::down_bytes(T, K, R, static_cast<int>(n)));
+// How the rank-wide product of K inputs is shared: the ring, or parts. N: outputs of the base product of the
+// few-token kernel beside which it runs, K0 its inputs (0: none).
+int parts_of(int64_t T, int64_t K, int64_t n, int64_t R, int64_t K0, int64_t N) {
+  return K0 > 0 && lora::few_path(T, N) ? lora::down_parts_beside(K, K0, N, R)
+                                        : lora::down_parts(T, K, R, static_cast<int>(n));
 }
-
-// few: it runs beside the base product of the few-token kernel (in one part: its time passes there).
-void plan_down(lora::RoutedDown& d, bool few) {
+size_t join_bytes(int64_t T, int64_t K, int64_t n, int64_t R, int64_t K0, int64_t N) {
+  return std::max(lora::ring_bytes(T, K, lora::rank_pad(R)), lora::part_bytes(parts_of(T, K, n, R, K0, N), T, R));
+}
+void plan_down(lora::RoutedDown& d, int64_t K0, int64_t N) {
   lora::ring_plan(d.T, d.K, &d.splits, &d.ks);
-  d.parts = few ? 1 : lora::down_parts(d.T, d.K, d.rt.rank, d.rt.n_adapters);
+  d.parts = parts_of(d.T, d.K, d.rt.n_adapters, d.rt.rank, K0, N);
 }
 
 struct FwdLayout {
@@ -60,7 +63,7 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
   L.ring = take(static_cast<size_t>(lora::ring_blocks(T)) * 4);
-  L.part = take(join_bytes(T, K, n, R));
+  L.part = take(join_bytes(T, K, n, R, K, N));
   L.total = take.off;
   return L;
 }
@@ -88,8 +91,9 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R, bool
   const size_t tb = static_cast<size_t>(T) * rp * 2;
   for (size_t& o : L.u) o = take(tb);
   for (size_t& o : L.t) o = take(tb);
-  L.upart = take(join_bytes(T, N, n, R));
-  L.tpart = take(join_bytes(T, K, n, R));
+  // (dx: a layer of N inputs and K outputs)
+  L.upart = take(join_bytes(T, N, n, R, want_dx ? N : 0, K));
+  L.tpart = take(join_bytes(T, K, n, R, want_dx ? N : 0, K));
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
@@ -230,7 +234,7 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   if (few) d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]), d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
   d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
-  plan_down(d, few);
+  plan_down(d, K, N);
   d.ring = reinterpret_cast<int32_t*>(ws + L.ring);
   d.tpart = reinterpret_cast<float*>(ws + L.part);
   const lora::RoutedDowns downs{{d, d}, 1, 0, 0};
@@ -323,9 +327,8 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   dt.A = static_cast<const uint16_t*>(pool->A);
   dt.hi = at16(L.t[0]); dt.mid = at16(L.t[1]); dt.lo = at16(L.t[2]);
   dt.tpart = reinterpret_cast<float*>(ws + L.tpart);
-  const bool few = dx != nullptr && lora::few_path(T, K);
-  plan_down(du, few);
-  plan_down(dt, few);
+  plan_down(du, dx != nullptr ? N : 0, K);
+  plan_down(dt, dx != nullptr ? N : 0, K);
   const bool want_u = dx != nullptr || dA != nullptr, want_t = dB != nullptr && n > 0;
   lora::RoutedDowns downs{{want_u ? du : dt, dt}, want_u && want_t ? 2 : 1, 0, 0};
   const hipError_t e = dx != nullptr ? launch_layer(dy, T, N, lddy, at16(L.wt), K, nullptr, dx, lddx, downs, at16(L.at),

@@ -69,7 +69,7 @@ hipError_t launch_routed_few(const RoutedFew& p, const RoutedDowns& downs, hipSt
   ++launches;
   check_downs(downs);
   for (int i = 0; i < downs.n; ++i)
-    if (downs.d[i].splits != 0 || downs.d[i].parts != 1) fail("a producer beside the base product is in one part");
+    if (downs.d[i].splits != 0) fail("a producer beside the base product has no ring");
   const FewPlan f = few_plan(p.T, p.K, p.N);
   const int64_t nk = (p.K + 63) / 64;
   if (static_cast<int64_t>(f.splits) * f.stages < nk || static_cast<int64_t>(f.splits - 1) * f.stages >= nk) fail("parts of K");
