@@ -500,20 +500,29 @@ def _routed_args(x, W, A, B, scales, token_adapter, token_scale, ranks):
     T, K = x.shape
     n, R, _ = A.shape
     N = B.shape[1]
-    _of(A, "A", (n, R, K), torch.bfloat16, dev)
-    _of(B, "B", (n, N, R), torch.bfloat16, dev)
-    _of(scales, "scales", (n,), torch.float32, dev)
-    _of(token_adapter, "token_adapter", (T,), torch.int32, dev)
-    _of(token_scale, "token_scale", (T,), torch.float32, dev)
-    _of(ranks, "ranks", (n,), torch.int32, dev)
-    if W is not None:
-        _of(W, "W", (N, K), torch.bfloat16, dev)
-    return T, K, N, LoraPool(_ptr(A), _ptr(B), _ptr(scales), _ptr(ranks), n, R, 0)
+    at, bf = x.get_device(), torch.bfloat16
+    if not (A.dtype is bf and B.dtype is bf and scales.dtype is torch.float32 and token_adapter.dtype is torch.int32
+            and A.get_device() == B.get_device() == scales.get_device() == token_adapter.get_device() == at
+            and A.is_contiguous() and B.is_contiguous() and scales.is_contiguous() and token_adapter.is_contiguous()
+            and A.shape[2] == K and B.shape == (n, N, R) and scales.shape == (n,) and token_adapter.shape == (T,)
+            and (W is None or (W.dtype is bf and W.get_device() == at and W.is_contiguous() and W.shape == (N, K)))):
+        _of(A, "A", (n, R, K), bf, dev)  # (these say what is wrong; a call that is right passes in 1-2 us less)
+        _of(B, "B", (n, N, R), bf, dev)
+        _of(scales, "scales", (n,), torch.float32, dev)
+        _of(token_adapter, "token_adapter", (T,), torch.int32, dev)
+        if W is not None:
+            _of(W, "W", (N, K), bf, dev)
+    if token_scale is not None:
+        _of(token_scale, "token_scale", (T,), torch.float32, dev)
+    if ranks is not None:
+        _of(ranks, "ranks", (n,), torch.int32, dev)
+    return T, K, N, LoraPool(A.data_ptr(), B.data_ptr(), scales.data_ptr(), _ptr(ranks), n, R, 0)
 
 
-def _bytes_on(workspace, need, device):
+def _bytes_on(workspace, size, args, device):
+    """The workspace given, checked, or one of size(*args) bytes. (Its length is checked by the call.)"""
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return torch.empty(max(size(*args), 1), dtype=torch.uint8, device=device)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {device}")
     return workspace
@@ -553,12 +562,14 @@ def lora_linear_routed(x, W, b, A, B, scales, token_adapter, token_scale=None, r
     T, K, N, pool = _routed_args(x, W, A, B, scales, token_adapter, token_scale, ranks)
     dev = x.device
     ldx = _rows(x, "x", (T, K), dev)
-    _of(b, "b", (N,), torch.bfloat16, dev)
+    if b is not None:
+        _of(b, "b", (N,), torch.bfloat16, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-        ldy = _rows(out, "out", (T, N), dev)
-        ws = _bytes_on(workspace, lora_linear_routed_workspace_size(T, K, N, A.shape[0], A.shape[1]), dev)
+            out, ldy = torch.empty((T, N), dtype=torch.bfloat16, device=dev), N
+        else:
+            ldy = _rows(out, "out", (T, N), dev)
+        ws = _bytes_on(workspace, _lib.lora_linear_routed_workspace_size, (T, K, N, pool.n_adapters, pool.rank), dev)
         lora_linear_routed_fwd(x.data_ptr(), T, K, ldx, W.data_ptr(), N, _ptr(b), pool, token_adapter.data_ptr(),
                                _ptr(token_scale), out.data_ptr(), ldy, ws.data_ptr(),
                                ws.numel() * ws.element_size(), _stream_on(dev, stream))
@@ -588,7 +599,7 @@ def lora_linear_routed_backward(x, W, A, B, dy, scales, token_adapter, token_sca
                 t = torch.empty(shape, dtype=torch.float32, device=dev)
             grads.append(_of(t, name, shape, torch.float32, dev))
         dA, dB = grads
-        ws = _bytes_on(workspace, lora_linear_routed_bwd_workspace_size(T, K, N, n, R, dx is not None), dev)
+        ws = _bytes_on(workspace, _lib.lora_linear_routed_bwd_workspace_size, (T, K, N, n, R, dx is not None), dev)
         lora_linear_routed_bwd(x.data_ptr(), T, K, ldx, _ptr(W), N, pool, token_adapter.data_ptr(),
                                _ptr(token_scale), dy.data_ptr(), lddy, _ptr(dx), lddx, _ptr(dA), _ptr(dB),
                                ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev, stream))
