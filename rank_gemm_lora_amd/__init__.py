@@ -9,11 +9,14 @@ without the built library raises.
 Low-level functions carry the C names and take plain integers for pointers:
 ``lora_linear_fwd``, ``lora_linear_stacked_fwd``, ``lora_linear_nf4_fwd`` (and
 ``lora_linear_nf4_fwd_ex``, which names where the 4-bit weight is dequantized),
-``dense_patch_apply``, ``lora_linear_workspace_size``, ``lora_status_string``,
+``lora_linear_routed_fwd``, ``lora_linear_routed_bwd``, ``lora_adamw_plan``,
+``lora_adamw_step``, ``dense_patch_apply``, ``lora_linear_workspace_size``, ``lora_status_string``,
 ``lora_device_check``. Tensor-level helpers (``lora_linear``,
-``lora_linear_stacked``, ``lora_linear_nf4``, ``dense_patch``) check that the
-tensors sit on one device, allocate the output and workspace with torch when
-not given, and call the C functions on the current stream.
+``lora_linear_stacked``, ``lora_linear_nf4``, ``lora_linear_routed``,
+``lora_linear_routed_backward``, ``dense_patch``) check that the tensors sit on
+one device, allocate the output and workspace with torch when not given, and
+call the C functions on the current stream. ``LoraAdamW`` holds the moments and
+the plan of ``lora_adamw_step``.
 """
 from __future__ import annotations
 

@@ -369,8 +369,8 @@ __device__ __forceinline__ void few_adapters(const RoutedFew& p, char* delta, co
 }
 
 template <int BM, int D>
-__global__ __launch_bounds__(64 * kDownWaves, 4) void routed_few_kernel(RoutedFew p, RoutedDowns ps, int downs, int tt, int S,
-                                                                       int per) {
+__global__ __launch_bounds__(64 * kDownWaves, 4) void routed_few_kernel(RoutedFew p, RoutedDowns ps, int downs, int tt,
+                                                                       int S, int per) {
   using C = FewCfg<BM>;
   constexpr int TB = C::TB, NB = C::NB;
   // (one LDS object: with several the compiler waits for every copy in flight before each LDS read, a memory
@@ -392,7 +392,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void routed_few_kernel(RoutedFe
   const int tile_n = tile / tt, tile_m = tile - tile_n * tt;
   // (consecutive L: parts of one tile; the token tiles of one stretch of W next)
   const int64_t n0 = static_cast<int64_t>(tile_n) * kFewN, m0 = static_cast<int64_t>(tile_m) * BM;
-  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(BM, p.T - m0));
+  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0));
+  const int rows_m = static_cast<int>(min<int64_t>(BM, p.T - m0));
   const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), ldw_b = static_cast<uint32_t>(p.K * 2);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.W + n0 * p.K, static_cast<uint32_t>(rows_n) * ldw_b);
@@ -479,10 +480,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void routed_few_kernel(RoutedFe
 template <int FB>
 __global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int parts) {
   __shared__ __attribute__((aligned(16))) char delta[FB * kFewN * 4];
-  __shared__ int ids[FB], tok[FB], units[FB], n_units;  // adapter and token of each row; first row and rank of each unit
+  // adapter and token of each row, first row and rank of each unit
+  __shared__ int ids[FB], tok[FB], units[FB], n_units;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kFewN, m0 = static_cast<int64_t>(blockIdx.y) * FB;
-  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0)), rows_m = static_cast<int>(min<int64_t>(FB, p.T - m0));
+  const int rows_n = static_cast<int>(min<int64_t>(kFewN, p.N - n0));
+  const int rows_m = static_cast<int>(min<int64_t>(FB, p.T - m0));
   const bool sorted = p.order != nullptr;
   const int row = tid >> 4, c = tid & 15;  // this thread's token and 4 outputs
   const int64_t place = m0 + min(row, rows_m - 1), token = sorted ? p.order[place] : place;
@@ -527,7 +530,8 @@ __global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int pa
 // stretches of the tokens, eight loads of 64 in flight; a first pass counts the tokens of every adapter before it
 // (one LDS atomic for each adapter among 64 tokens; integers, so their order does not show), from which follow its
 // place among tokens and items, and its own by wave; a second writes them, in token order.
-__device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* counts, int (&sums)[5][16], int (&mine)[16]) {
+__device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* counts, int (&sums)[5][16],
+                                           int (&mine)[16]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t per = ((p.T + 15) / 16 + 63) / 64 * 64;
   const int64_t lo = wave * per, hi = min<int64_t>(p.T, lo + per);
@@ -874,8 +878,9 @@ hipError_t few(const RoutedFew& p, RoutedDowns downs, const FewPlan& f, hipStrea
   if (e == hipSuccess) e = launch_rest(downs, s);
   if (e != hipSuccess) return e;
   const unsigned x = static_cast<unsigned>(f.tiles / f.token_tiles);
-  if (BM == 16) hipLaunchKernelGGL((few_finish_kernel<16>), dim3(x), dim3(256), 0, s, p, f.parts);
-  else hipLaunchKernelGGL((few_finish_kernel<32>), dim3(x, static_cast<unsigned>((p.T + 31) / 32)), dim3(512), 0, s, p, f.parts);
+  const unsigned y = static_cast<unsigned>((p.T + 31) / 32);
+  if (BM == 16) hipLaunchKernelGGL(few_finish_kernel<16>, dim3(x), dim3(256), 0, s, p, f.parts);
+  else hipLaunchKernelGGL(few_finish_kernel<32>, dim3(x, y), dim3(512), 0, s, p, f.parts);
   return hipGetLastError();
 }
 }  // namespace

@@ -32,7 +32,7 @@ struct RoutedDown {
 };
 // Few tokens: t~ (as hi and mid) and the base product over a ring of LDS stages in one launch, then the sum.
 // Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
-// 4096 -> 14336: 68 against 76 us), with mixed ones it is slower up to there and beyond (121 against 86 us).
+// 4096 -> 14336: 68 against 77 us), with mixed ones it is slower up to there and beyond (121 against 90 us).
 constexpr int64_t kFewMaxT = 256;
 // (one block of 16 is as good in any order)
 inline bool sorts_tokens(int64_t T) { return T > kRouteBlock && T <= kFewMaxT; }

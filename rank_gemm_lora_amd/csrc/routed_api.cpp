@@ -69,8 +69,8 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
 }
 
 struct BwdLayout {
-  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, upart = 0, tpart = 0, eid = 0, blk = 0, ring = 0, perm = 0,
-         part[2] = {0, 0}, few = 0, order = 0, total = 0;
+  size_t wt = 0, bt = 0, at = 0, u[3] = {0, 0, 0}, t[3] = {0, 0, 0}, upart = 0, tpart = 0, eid = 0, blk = 0;
+  size_t ring = 0, perm = 0, part[2] = {0, 0}, few = 0, order = 0, total = 0;
   struct {
     size_t first = 0, items = 0;
     int32_t chunk = 0;

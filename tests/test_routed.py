@@ -378,6 +378,23 @@ def test_two_streams_and_repeats_give_the_same_bits():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,n,R,layout", [
+    (200, 8968, 136, 5, 72, "mixed"), (20, 9000, 72, 6, 16, "mixed"), (16, 9000, 64, 16, 16, "mixed"),
+    (700, 8200, 200, 9, 40, "packed"), (150, 72, 8200, 5, 72, "mixed"), (256, 1544, 2056, 40, 24, "mixed"),
+    (1, 9000, 8, 1, 136, "mixed"), (300, 4104, 3000, 7, 16, "packed"),
+])
+def test_long_sums_beside_the_base_product(T, K, N, n, R, layout):
+    """Rank-wide products in several parts, in one product of the backward or in both."""
+    say("routed long sums", T, K, N, n, R, layout)
+    d = rr.case(T, K, N, n, R, T + K, layout, ranks=True)
+    g = gpu(d)
+    rr.check(run_fwd(g), *rr.forward(d), "y")
+    want, bounds = rr.backward(d)
+    for got, w, b, what in zip(run_bwd(g), want, bounds, ("dx", "dA", "dB")):
+        rr.check(got, w, b, what)
+
+
+@pytest.mark.gpu
 def test_rows_of_x_far_apart():
     """Rows of 4 MB: x spans more than 32 bits of bytes, tokens as they come and sorted."""
     say("routed wide rows")
