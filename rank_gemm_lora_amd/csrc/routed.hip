@@ -308,13 +308,12 @@ __device__ __forceinline__ void few_store(const RoutedFew& p, f32x4 v, int64_t t
   }
 }
 
-// The adapters of a tile: units part, part + parts, .. of its list, two in flight at a time, 32 ranks of each
-// at a time. (Code that runs once costs its fetch: eight units at a time, unrolled, took 1-3 us longer on
-// every small call and gained nothing on large ones. 64 tokens of 64 adapters, 4096 -> 14336: 57.7 us against
-// 57.7; 16 of 16: 44.1 against 48.5.)
+// The adapters of a tile: units part, part + parts, .. of its list, P in flight at a time, 32 ranks of each at a
+// time. (Code that runs once costs its fetch: eight units at a time, unrolled, took 1-3 us longer on every small
+// call and gained nothing on large ones.)
+template <int P>
 __device__ __forceinline__ void few_adapters(const RoutedFew& p, char* delta, const int* ids, const int* tok,
                                              const int* units, int n_units, int64_t n0, int rows_n, int part, int parts) {
-  constexpr int P = 2;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const uint32_t ldb = static_cast<uint32_t>(p.rt.rank * 2), ldt_b = static_cast<uint32_t>(p.ldt * 2);
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.hi, static_cast<uint32_t>(p.T) * ldt_b);
@@ -476,7 +475,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void routed_few_kernel(RoutedFe
 // Workgroup: 64 outputs x FB tokens (places of the sorted order, where there is one). Each adapter of each 16
 // tokens (a unit) is one wave's, its product over the 64 outputs formed apart and the rows of the adapter's own
 // tokens put into an LDS tile, so nothing of one adapter meets another's tokens. The parts of the base product
-// are added in order, then the adapter's sum and the bias; their loads are in flight meanwhile.
+// are added in order, then the adapter's sum and the bias; the loads of the first of them are in flight meanwhile.
+// 16 tokens have up to 16 parts and few workgroups: two units and eight parts in flight; more tokens have few parts
+// and workgroups to fill the card, whose registers count: one unit and four parts (203 tokens of 32 adapters,
+// 1536 -> 8960, a call: 32.6 -> 30.0 us; with 16 tokens that way 25.0 -> 26.3, 8960 -> 1536).
 template <int FB>
 __global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int parts) {
   __shared__ __attribute__((aligned(16))) char delta[FB * kFewN * 4];
@@ -495,9 +497,10 @@ __global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int pa
   }
   *few_delta(delta, row, c) = f32x4{0.f, 0.f, 0.f, 0.f};
   const float* base = p.part + (static_cast<int64_t>(blockIdx.x) * parts * p.T + token) * kFewN + 4 * c;
-  f32x4 w[8];  // (a part past the last reads the last again, unused)
+  constexpr int FW = FB == 16 ? 8 : 4;
+  f32x4 w[FW];  // (a part past the last reads the last again, unused)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const f32x4*>(base + min(k, parts - 1) * p.T * kFewN);
+  for (int k = 0; k < FW; ++k) w[k] = *reinterpret_cast<const f32x4*>(base + min(k, parts - 1) * p.T * kFewN);
   lds_barrier();
   // units: where an adapter shows first in a block of 16 (in adapter order: where it changes)
   if (wave == 0) {
@@ -513,13 +516,13 @@ __global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int pa
     if (lane == 0) n_units = __popcll(m);
   }
   lds_barrier();
-  few_adapters(p, delta, ids, tok, units, __builtin_amdgcn_readfirstlane(n_units), n0, rows_n, wave, FB / 4);
+  few_adapters<FB == 16 ? 2 : 1>(p, delta, ids, tok, units, __builtin_amdgcn_readfirstlane(n_units), n0, rows_n, wave, FB / 4);
   lds_barrier();
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
+  for (int k = 0; k < FW; ++k)
     if (k < parts) v += w[k];
-  for (int k = 8; k < parts; ++k) v += *reinterpret_cast<const f32x4*>(base + k * p.T * kFewN);
+  for (int k = FW; k < parts; ++k) v += *reinterpret_cast<const f32x4*>(base + k * p.T * kFewN);
   if (row < rows_m) few_store(p, v + *few_delta(delta, row, c), token, n0, rows_n, 4 * c);
 }
 
