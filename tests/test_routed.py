@@ -465,3 +465,19 @@ def test_calls_on_a_named_stream():
         assert all(torch.equal(a, b) for a, b in zip(outs, ref))
     with pytest.raises(ValueError):
         rg.lora_linear_routed(*(d[k] for k in ("x", "W", "b", "A", "B", "scales", "ids")), stream=side)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,n,R,layout", [
+    (2100001, 16, 24, 3, 8, "long"), (3, 8, 1 << 20, 2, 8, "mixed"), (3, 1 << 20, 8, 2, 8, "mixed"),
+    (1030, 1 << 16, 8, 2, 8, "long"), (1030, 8, 1 << 16, 6, 8, "mixed"),
+])
+def test_the_largest_extents(T, K, N, n, R, layout):
+    """Millions of tokens, and the widest inputs and outputs."""
+    say("routed extents", T, K, N, n, R, layout)
+    d = rr.case(T, K, N, n, R, 11, layout)
+    g = gpu(d)
+    rr.check(run_fwd(g), *rr.forward(d), "y")
+    want, bounds = rr.backward(d)
+    for got, w, b, what in zip(run_bwd(g), want, bounds, ("dx", "dA", "dB")):
+        rr.check(got, w, b, what)
