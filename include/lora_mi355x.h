@@ -529,7 +529,8 @@ typedef struct lora_adamw_plan_t {
  *   param_dtype, grad_dtype  LORA_F32 or LORA_BF16
  *   state_bits  32, or 8: a stored code c of a block of 256 elements means
  *               c . scale (m) and (c . scale)^2 (v). A step writes scale =
- *               largest magnitude / 448 and RN_e4m3(x . (448 / largest)), a
+ *               largest magnitude . RN(1 / 448) and
+ *               RN_e4m3(x . (448 . RN(1 / largest))), a
  *               positive root at least as the smallest e4m3; a block whose
  *               values are all below 2^-100 holds zeros. Zeros are a valid start
  * Nothing written may overlap anything else (LORA_ERR_OVERLAP); natural

@@ -6,7 +6,7 @@
 //
 // every operation in fp32, rounded once, in this order (built with floating-point contraction off).
 // Moments in 8 bits: m and sqrt(v) as e4m3 with one fp32 scale per 256 elements, scale = largest
-// magnitude / 448; a value x is stored as RN_e4m3(x . (448 / largest)). The root is stored rather
+// magnitude . RN(1 / 448); a value x is stored as RN_e4m3(x . (448 . RN(1 / largest))). The root is stored rather
 // than v, whose range is the square of what 8 bits hold. A positive root never becomes zero (it takes
 // the smallest e4m3, 2^-9): rounded down to zero it would leave eps alone under the update. The step
 // itself uses the new moments before they are rounded.
@@ -126,8 +126,10 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float& scale) {
   for (int s = 1; s < 32; s *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), s)));
   const float t = __uint_as_float(top);
   const bool some = !(t < 0x1p-100f);
-  scale = some ? t / 448.f : 0.f;
-  const float inv = some ? 448.f / t : 0.f;
+  // (products with reciprocals, as the constants of the step are: true divisions here put a code in 10^7 on the
+  // other side of a tie from what tensor libraries write for the same division by a number)
+  scale = some ? t * (1.f / 448.f) : 0.f;
+  const float inv = some ? (1.f / t) * 448.f : 0.f;
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = x[e] * inv;
