@@ -530,9 +530,11 @@ __global__ __launch_bounds__(FB * 16) void few_finish_kernel(RoutedFew p, int pa
 // What the backward's other launches need first: the transposed operands and the plan of the contractions.
 //
 // The plan, tokens sorted by adapter: workgroup a finds its adapter's tokens. The 16 waves take consecutive
-// stretches of the tokens, eight loads of 64 in flight; a first pass counts the tokens of every adapter before it
+// stretches of the tokens, LOADS of 64 in flight; a first pass counts the tokens of every adapter before it
 // (one LDS atomic for each adapter among 64 tokens; integers, so their order does not show), from which follow its
-// place among tokens and items, and its own by wave; a second writes them, in token order.
+// place among tokens and items, and its own by wave; a second writes them, in token order. LOADS 1: before the
+// producer, from the routing itself; 8: from eid.
+template <int LOADS>
 __device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* counts, int (&sums)[5][16],
                                            int (&mine)[16]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -541,17 +543,17 @@ __device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* count
   for (int i = threadIdx.x; i < p.n_adapters; i += 1024) counts[i] = 0;
   __syncthreads();
   int nm = 0;
-  for (int64_t t = lo; t < hi; t += 512) {
-    int id[8];
+  for (int64_t t = lo; t < hi; t += 64 * LOADS) {
+    int id[LOADS];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < LOADS; ++k) {
       float scale;
       const int64_t at = t + 64 * k + lane;
-      if (p.eid == nullptr) id[k] = route(p.rt, at, hi, scale);
+      if constexpr (LOADS == 1) id[k] = route(p.rt, at, hi, scale);
       else id[k] = at < hi ? p.eid[at] : -1;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < LOADS; ++k) {
       uint64_t todo = __builtin_amdgcn_ballot_w64(id[k] >= 0 && id[k] < a);
       while (todo != 0) {
         const int b = __builtin_amdgcn_readlane(id[k], __builtin_ctzll(todo));
@@ -583,6 +585,7 @@ __device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* count
   }
   __syncthreads();
   int before[5] = {0, 0, 0, 0, 0}, count = 0, at = 0;
+#pragma unroll 2
   for (int w = 0; w < 16; ++w) {
 #pragma unroll
     for (int k = 0; k < 5; ++k) before[k] += sums[k][w];
@@ -591,17 +594,17 @@ __device__ __forceinline__ void route_plan(const RoutePlan& p, int a, int* count
   }
   const int start = before[0];
   at += start;
-  for (int64_t t = lo; t < hi; t += 512) {
-    int id[8];
+  for (int64_t t = lo; t < hi; t += 64 * LOADS) {
+    int id[LOADS];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < LOADS; ++k) {
       float scale;
       const int64_t at = t + 64 * k + lane;
-      if (p.eid == nullptr) id[k] = route(p.rt, at, hi, scale);
+      if constexpr (LOADS == 1) id[k] = route(p.rt, at, hi, scale);
       else id[k] = at < hi ? p.eid[at] : -1;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < LOADS; ++k) {
       const uint64_t m = __builtin_amdgcn_ballot_w64(id[k] == a);
       if (id[k] == a) p.perm[at + __popcll(m & ((1ull << lane) - 1))] = static_cast<int32_t>(t + 64 * k + lane);
       at += __popcll(m);
@@ -635,18 +638,19 @@ struct RoutePrepare {
   int64_t first[kTransposeStacks + 1];  // 64 x 64 tiles [first, next first) are a stack's
 };
 
-// Workgroups below n_adapters (with PLAN): the plan; the others: transposes, TILES of them by 256 threads each.
-template <bool PLAN, int TILES>
-__global__ __launch_bounds__(256 * TILES) void route_prepare_kernel(RoutePrepare p) {
-  static_assert(!PLAN || TILES == 4, "the plan's 16 waves");
+// Workgroups below n_adapters (with LOADS): the plan; the others (TRANSPOSE): tiles, TILES of them by 256 threads
+// each.
+template <bool TRANSPOSE, int LOADS>
+__global__ __launch_bounds__(LOADS > 0 ? 1024 : 256, LOADS == 8 ? 4 : 8) void route_prepare_kernel(RoutePrepare p) {
+  constexpr int TILES = LOADS > 0 ? 4 : 1;
   __shared__ __attribute__((aligned(16))) union {
     bf16_bits tile[TILES][64][72];
-    int counts[PLAN ? LORA_MAX_POOL : 1];
+    int counts[LOADS > 0 ? LORA_MAX_POOL : 1];
   } u;
-  if constexpr (PLAN) {
+  if constexpr (LOADS > 0) {
     __shared__ int sums[5][16], mine[16];
-    if (static_cast<int>(blockIdx.x) < p.plan.n_adapters) {
-      route_plan(p.plan, blockIdx.x, u.counts, sums, mine);
+    if (!TRANSPOSE || static_cast<int>(blockIdx.x) < p.plan.n_adapters) {
+      route_plan<LOADS>(p.plan, blockIdx.x, u.counts, sums, mine);
       return;
     }
   }
@@ -913,8 +917,9 @@ hipError_t launch_route_prepare(const RoutePlan& plan, const TransposeStack* sta
   if (blocks == 0) return hipSuccess;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(static_cast<unsigned>(256 * per));
-  if (plan.n_adapters > 0) hipLaunchKernelGGL((route_prepare_kernel<true, 4>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((route_prepare_kernel<false, 1>), grid, block, 0, s, p);
+  if (plan.n_adapters == 0) hipLaunchKernelGGL((route_prepare_kernel<true, 0>), grid, block, 0, s, p);
+  else if (plan.eid == nullptr) hipLaunchKernelGGL((route_prepare_kernel<true, 1>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((route_prepare_kernel<false, 8>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

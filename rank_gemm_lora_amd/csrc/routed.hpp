@@ -193,8 +193,8 @@ struct TransposeStack {
   int64_t R, C, slots;
 };
 constexpr int kTransposeStacks = 3;
-// The plan and n <= kTransposeStacks stacks in one launch, for which the plan does without eid. Up to 1024 tokens
-// (a load of each wave's): 333 tokens 8.1 us against 6.3 + 6.1 apart. With more its chains of look-ups are longer
+// The plan from eid; or n <= kTransposeStacks stacks; or both in one launch, for which the plan does without eid. Up to 1024 tokens
+// (a load of each wave's): 333 tokens 7.8 us against 6.3 + 6.1 apart. With more its chains of look-ups are longer
 // than the transposes (18871 tokens: 44 us against 20.5 + 12.8) and it follows the producer.
 constexpr int64_t kPlanFirstT = 1024;
 hipError_t launch_route_prepare(const RoutePlan& p, const TransposeStack* stacks, int n, hipStream_t s);
