@@ -2255,8 +2255,9 @@ __global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDowns ps
 
 template <class DP>
 hipError_t launch_ring_cfg(RoutedDowns p, hipStream_t s) {
-  p.z0 = p.d[0].splits * kRingAdapters;
-  const int z = p.z0 + (p.n > 1 ? p.d[1].splits * kRingAdapters : 0);
+  const int most = p.d[0].rt.n_adapters < kRingAdapters ? max(1, p.d[0].rt.n_adapters) : kRingAdapters;
+  p.z0 = p.d[0].splits * most;
+  const int z = p.z0 + (p.n > 1 ? p.d[1].splits * most : 0);
   const dim3 grid(static_cast<unsigned>((p.d[0].T + DP::BM - 1) / DP::BM),
                   static_cast<unsigned>((p.d[0].ldt + DP::BN - 1) / DP::BN), static_cast<unsigned>(z));
   hipLaunchKernelGGL((routed_ring_kernel<DP>), grid, dim3(DP::THREADS), 0, s, p);

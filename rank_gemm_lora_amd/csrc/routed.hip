@@ -226,17 +226,20 @@ __device__ __forceinline__ void down_join(const RoutedDown& p, int64_t group) {
   put_rank_wide<2>(p, at, v);
 }
 
-// The blocks of 16 that the ring did not take: blocks blockIdx.x, + stride, ..; 64 at a time are looked at, one per
-// lane (every wave the same).
-__device__ __forceinline__ void down_beside(const RoutedDown& p, f32x4 (&red)[kDownWaves][4][64], int64_t stride) {
+// The blocks of 16 that the ring did not take: blocks first, + stride, ..; 64 at a time are looked at, one per lane
+// (every wave the same). kBesideSlots workgroups share a block's adapters (2000 tokens of 16 mixed adapters,
+// 4096 -> 4096: 142 us a call against 204 with one).
+constexpr int kBesideSlots = 4;
+__device__ __forceinline__ void down_beside(const RoutedDown& p, f32x4 (&red)[kDownWaves][4][64], int64_t first,
+                                            int64_t stride, int slot) {
   const int64_t n = (p.T + kRouteBlock - 1) / kRouteBlock;
-  for (int64_t base = blockIdx.x; base < n; base += 64 * stride) {
+  for (int64_t base = first; base < n; base += 64 * stride) {
     const int64_t mine = base + (threadIdx.x & 63) * stride;
     uint64_t left = __builtin_amdgcn_ballot_w64(mine < n && p.ring[mine * kRouteBlock / kRingBlock] < 0);
     while (left != 0) {
       const int i = __builtin_ctzll(left);
       left &= left - 1;
-      down_block<true>(p, base + i * stride, red, nullptr, blockIdx.y * 64, 0, 1, 0, false);
+      down_block<true>(p, base + i * stride, red, nullptr, blockIdx.y * 64, slot, kBesideSlots, 0, false);
     }
   }
 }
@@ -252,7 +255,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void routed_rest_kernel(RoutedDown
   }
   if constexpr (BESIDE) {
     __shared__ f32x4 red[kDownWaves][4][64];
-    down_beside(p, red, beside);
+    down_beside(p, red, blockIdx.x / kBesideSlots, beside / kBesideSlots, blockIdx.x % kBesideSlots);
   }
 }
 
@@ -840,7 +843,8 @@ static hipError_t launch_rest(const RoutedDowns& p, hipStream_t s) {
   bool join = false;
   for (int i = 0; i < p.n; ++i) join = join || p.d[i].splits > 1 || (p.d[i].splits == 0 && p.d[i].parts > 1);
   // (up to kRingAdapters adapters every block is the ring's)
-  const unsigned beside = d.splits > 0 && d.rt.n_adapters > kRingAdapters ? (blocks < 512 ? blocks : 512) : 0;
+  const unsigned beside =
+      d.splits > 0 && d.rt.n_adapters > kRingAdapters ? kBesideSlots * (blocks < 128 ? blocks : 128) : 0;
   const unsigned joins = join ? static_cast<unsigned>((d.T + 2 * kDownWaves - 1) / (2 * kDownWaves)) : 0;
   // (one launch for both where it is short: 4977 tokens 7.2 us against 5.4 + 4.7; the registers of the blocks slow
   // many joins down: 18871 tokens, both products, 26 us against 15.4 + 4.8)

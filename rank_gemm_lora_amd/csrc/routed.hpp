@@ -8,10 +8,12 @@ namespace lora {
 
 // Rank-wide producer: t = s_t . x[t] A_a^T of every token's own adapter a, as hi = RN_bf16(t) and, where
 // mid is not null, the rest of its 24 bits in mid and lo. Writes eid and blk (RoutedGemm) too.
-// With many tokens (splits > 0) a block of 128 tokens with up to four adapters is multiplied by a ring of
+// With many tokens (splits > 0) a block of 128 tokens with up to kRingAdapters is multiplied by a ring of
 // LDS stages, once per adapter, K in `splits` parts of ks stages of 64; the other blocks, and all blocks of
 // fewer tokens, 16 tokens at a time straight from memory.
-constexpr int kRingAdapters = 4;
+// (9000 tokens that take 6 adapters in turn, 8960 -> 1536, rank 64: 378 us with all of a block's adapters in the ring,
+// 859 with blocks of more than four left to the 16-token form; 16 instead of 8 costs the launches of others 1%)
+constexpr int kRingAdapters = 8;
 struct RoutedDown {
   const uint16_t* x; int64_t ldx;
   int64_t T, K;
@@ -193,9 +195,9 @@ struct TransposeStack {
   int64_t R, C, slots;
 };
 constexpr int kTransposeStacks = 3;
-// The plan from eid; or n <= kTransposeStacks stacks; or both in one launch, for which the plan does without eid. Up to 1024 tokens
-// (a load of each wave's): 333 tokens 7.8 us against 6.3 + 6.1 apart. With more its chains of look-ups are longer
-// than the transposes (18871 tokens: 44 us against 20.5 + 12.8) and it follows the producer.
+// The plan from eid; or n <= kTransposeStacks stacks; or both in one launch, for which the plan does without eid:
+// up to 1024 tokens (a load of each wave's): 333 tokens 7.8 us against 6.3 + 6.1 apart. With more its chains of
+// look-ups are longer than the transposes (18871 tokens: 44 us against 20.5 + 12.8) and it follows the producer.
 constexpr int64_t kPlanFirstT = 1024;
 hipError_t launch_route_prepare(const RoutePlan& p, const TransposeStack* stacks, int n, hipStream_t s);
 
