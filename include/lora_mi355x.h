@@ -426,8 +426,10 @@ typedef struct lora_pool {
  * Motivation and Modifications: the scale is honoured per request; here the
  * adapter is too):
  *
- *     y[t] = x[t] . W^T + b + t~_t . B_a^T,   t~_t = RN_bf16(s_t . (x[t] . A_a^T)),
+ *     y[t] = RN_bf16(x[t] . W^T + b + t~_t . B_a^T),   t~_t = s_t . (x[t] . A_a^T),
  *     a = token_adapter[t],  s_t = RN_f32(scales[a] . token_scale[t])
+ *
+ * sums in fp32, t~_t kept as two bf16 terms (within 2^-16 of each of its elements)
  *
  *   token_adapter  [T] int32 (device). A token whose index is outside
  *                  [0, n_adapters) (-1 by convention), whose s_t is +-0 or
@@ -447,8 +449,10 @@ typedef struct lora_pool {
  * T == 0 is a valid no-op. LORA_ERR_ALIGN unless x, W, A, B and the workspace
  * are 16-byte aligned and K, ldx and the slot rank are multiples of 8.
  * LORA_ERR_UNSUPPORTED from 2^26 tokens on.
- * The output of a token depends on the other tokens of the batch in its last
- * bit only (the order of the fp32 sums); the same call gives the same bits.
+ * The same call gives the same bits. The number of tokens, and the adapters of
+ * a token's neighbours, choose the order of the fp32 sums: outputs of one token
+ * in two batches differ by no more than the roundings above (2^-16 of
+ * sum |t~_t| |B_a|, the fp32 sums' own, and then the one to bf16).
  */
 int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
                            const void* bias, const lora_pool* pool, const int32_t* token_adapter,
@@ -463,7 +467,7 @@ size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_
  * gradient dy, the base weight and bias frozen (Unsloth fast-LoRA chapter,
  * sections 2 and 4, per adapter):
  *
- *     u_t = s_t . (dy[t] . B_a),  dx[t] = RN_bf16(dy[t] . W + RN_bf16(u_t) . A_a),
+ *     u_t = s_t . (dy[t] . B_a),  dx[t] = RN_bf16(dy[t] . W + u_t . A_a)  (u_t as two bf16 terms there),
  *     dA_a = sum over a's tokens of u_t^T . x[t],
  *     dB_a = sum over a's tokens of dy[t]^T . (s_t . x[t] . A_a^T)
  *

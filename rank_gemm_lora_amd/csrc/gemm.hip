@@ -1246,8 +1246,8 @@ __device__ __forceinline__ void ext_stage_loads(const ExtPlan& g, int e, const T
 }
 
 // Routed: how this tile's adapters are met. All of its tokens with one adapter: its K-extension plan
-// (the pool slot's rows n0 .., its rank padded to 64-k stages), false. No adapter at all: no plan,
-// false. Otherwise true: the updates are added after the loop.
+// (the pool slot's rows n0 .., its rank padded to 64-k stages; once for each term of t~), false. No
+// adapter at all: no plan, false. Otherwise true: the updates are added after the loop.
 template <class P>
 __device__ __forceinline__ bool routed_plan(const LinearProblem& p, int64_t m0, int64_t n0, int rows_m, int rows_n,
                                             int lane, ExtPlan& e) {
@@ -1274,7 +1274,8 @@ __device__ __forceinline__ bool routed_plan(const LinearProblem& p, int64_t m0, 
 // acc += t~ . B_a^T for the tokens of this wave's block (first token mw, first output nw), each with
 // its own adapter, in ascending adapter order. An adapter's B rows are loaded once per 64 ranks
 // straight into MFMA operands (lane (r, q): ranks 8q .. +7 of output 16 i + r) and used for every
-// 16-token block that holds one of its tokens; the block's other tokens enter as zeros of t~. A zero
+// 16-token block that holds one of its tokens, with both terms of t~ (the second one's loads take the first
+// one's registers, each behind the MFMAs that used them); the block's other tokens enter as zeros of t~. A zero
 // times an infinite or NaN weight would be NaN, so that one request's broken adapter would reach the
 // outputs of others: such weights (found by the largest magnitude of the loaded operands) enter as
 // zeros, and true is returned: routed_broken then puts their outputs right. (Adding the product to the
@@ -1293,8 +1294,9 @@ __device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const L
   const int rows_n = static_cast<int>(min<int64_t>(P::WN, p.N - nw));
   const int rows_m = static_cast<int>(min<int64_t>(P::WM, p.T - mw));
   if (rows_n <= 0 || rows_m <= 0) return false;
-  const __amdgpu_buffer_rsrc_t tr =
-      make_rsrc(static_cast<const char*>(p.work) + mw * p.ldt * 2, static_cast<uint32_t>(rows_m) * ldt_b);
+  const __amdgpu_buffer_rsrc_t tr[2] = {
+      make_rsrc(static_cast<const char*>(p.work) + mw * p.ldt * 2, static_cast<uint32_t>(rows_m) * ldt_b),
+      make_rsrc(static_cast<const char*>(p.rt.mid) + mw * p.ldt * 2, static_cast<uint32_t>(rows_m) * ldt_b)};
   bool broken = false;
   int prev = -1;
   while (true) {
@@ -1323,14 +1325,18 @@ __device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const L
       // (all t~ loads before the first wait, other tokens' out of range: one after the other they cost the
       // block a memory latency per 16 tokens)
       bf16x8 t[P::NJ][2];
-#pragma unroll
-      for (int j = 0; j < P::NJ; ++j)
+      auto load_t = [&](int j, int term) {
+        const int l = term == 0 ? lane : opaque_int(lane);  // (offsets formed again, not kept over the MFMAs: registers)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int k = c0 + 32 * h + 8 * q;
-          const uint32_t off = id[j] == a && k < rank ? static_cast<uint32_t>(j * 16 + r) * ldt_b + k * 2 : 0x80000000u;
-          t[j][h] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(tr, off, 0, 0));
+          const int k = c0 + 32 * h + 8 * (l >> 4);
+          const uint32_t off =
+              id[j] == a && k < rank ? static_cast<uint32_t>(j * 16 + (l & 15)) * ldt_b + k * 2 : 0x80000000u;
+          t[j][h] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(tr[term], off, 0, 0));
         }
+      };
+#pragma unroll
+      for (int j = 0; j < P::NJ; ++j) load_t(j, 0);
       u16x2 top = {0, 0};
 #pragma unroll
       for (int i = 0; i < P::NI; ++i)
@@ -1349,15 +1355,18 @@ __device__ __forceinline__ bool routed_mixed(f32x4 (&acc)[P::NI][P::NJ], const L
             for (int e = 0; e < 4; ++e) w[i][h][e] = finite_pair(w[i][h][e]);
       }
 #pragma unroll
-      for (int j = 0; j < P::NJ; ++j) {
-        if (__builtin_amdgcn_ballot_w64(id[j] == a) == 0) continue;
+      for (int term = 0; term < 2; ++term)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < P::NJ; ++j) {
+          if (__builtin_amdgcn_ballot_w64(id[j] == a) == 0) continue;
 #pragma unroll
-          for (int i = 0; i < P::NI; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][h]), t[j][h], acc[i][j],
-                                                                0, 0, 0);
-      }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < P::NI; ++i)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][h]), t[j][h], acc[i][j],
+                                                                  0, 0, 0);
+          if (term == 0) load_t(j, 1);
+        }
     }
   }
   return broken;
@@ -1408,8 +1417,8 @@ __device__ __forceinline__ void routed_broken(const LinearProblem& p, int64_t mw
 // word written into the slot that the barrier of stage t releases, where the copies would have
 // gone. The weight is the panel kernel's, bit for bit, and so is the result.
 // ROUTED: the tokens take their adapters from a pool (p.rt). A tile whose tokens all take the same
-// adapter is the one-adapter case, K-extension and all, its B found from the tile; any other tile
-// runs without extension stages and adds its adapters' updates after the loop (routed_mixed).
+// adapter is the one-adapter case, its B found from the tile, with t~'s two terms as two groups of
+// K-extension stages over the same B; any other tile runs without extension stages and adds its adapters' updates after the loop (routed_mixed).
 template <class P, bool NF4 = false, bool ROUTED = false>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearProblem p, int mt, int nt) {
   static_assert(P::WAVES == 4, "schedule written for 4 waves");
@@ -1500,13 +1509,19 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
   };
   ExtPlan eg0 = ext_group(gs0), eg1 = ext_group(gs1);
   bool mixed = false;
-  if constexpr (ROUTED) mixed = routed_plan<P>(p, m0, n0, rows_m, rows_n, lane, eg0);
+  if constexpr (ROUTED) {
+    mixed = routed_plan<P>(p, m0, n0, rows_m, rows_n, lane, eg0);
+    eg1 = eg0;
+  }
   // Stage order: the K-extension stages first, then the main stages (s >= NE is main stage s - NE).
   const int NE = eg0.ns + eg1.ns;
   const int NS = NE + nk;
   const int NU = 2 * NS;
   const __amdgpu_buffer_rsrc_t tr =
       make_rsrc(static_cast<const char*>(p.work) + m0 * p.ldt * 2, static_cast<uint32_t>(rows_m) * ldt_b);
+  // (of the second group: routed, the second term)
+  const __amdgpu_buffer_rsrc_t tr1 =
+      ROUTED ? make_rsrc(static_cast<const char*>(p.rt.mid) + m0 * p.ldt * 2, static_cast<uint32_t>(rows_m) * ldt_b) : tr;
   // K-extension stages after the prologue's (more than two): per-lane copy offsets of the t~ rows
   // and of the B rows of each of the tile's two groups, computed once per tile, so that a copy
   // takes a select and a K-tail mask instead of its whole offset arithmetic (a 4-bit weight, with
@@ -1516,7 +1531,8 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
   if constexpr (!NF4) {
     oxe.init(ldt_b, 0, rows_m, 0);
     ob0.init(static_cast<uint32_t>(eg0.ldb), eg0.lo, eg0.hi, eg0.sh);
-    ob1.init(static_cast<uint32_t>(eg1.ldb), eg1.lo, eg1.hi, eg1.sh);
+    if constexpr (ROUTED) ob1 = ob0;
+    else ob1.init(static_cast<uint32_t>(eg1.ldb), eg1.lo, eg1.hi, eg1.sh);
   }
   const __amdgpu_buffer_rsrc_t br0 =
       make_rsrc(eg0.B, static_cast<uint32_t>(eg0.n_cols) * static_cast<uint32_t>(eg0.ldb));
@@ -1546,7 +1562,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
     const ExtPlan& g = second ? eg1 : eg0;
     const int e = second ? s - eg0.ns : s;
     if (!is_w) {
-      dma_one<P, P::BM>(l, dst, tr, ldt_b, 0, rows_m, 0, g.tcb + e * P::RB, g.tcb + g.tpb);
+      dma_one<P, P::BM>(l, dst, second ? tr1 : tr, ldt_b, 0, rows_m, 0, g.tcb + e * P::RB, g.tcb + g.tpb);
     } else {
       const __amdgpu_buffer_rsrc_t br = make_rsrc(g.B, static_cast<uint32_t>(g.n_cols) * static_cast<uint32_t>(g.ldb));
       dma_one<P, P::BN>(l, dst, br, static_cast<uint32_t>(g.ldb), g.lo, g.hi, g.sh, e * P::RB, g.rkb);
@@ -1622,7 +1638,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
     } else if (eg0.ns == 2) {
       ext_stage_loads<P>(eg0, 1, ot, tr, smem + 2 * P::SLOT_BYTES, smem + 3 * P::SLOT_BYTES);
     } else {
-      ext_stage_loads<P>(eg1, 0, ot, tr, smem + 2 * P::SLOT_BYTES, smem + 3 * P::SLOT_BYTES);
+      ext_stage_loads<P>(eg1, 0, ot, tr1, smem + 2 * P::SLOT_BYTES, smem + 3 * P::SLOT_BYTES);
     }
   } else {
     for (int u = 0; u < 4; ++u)
@@ -1730,7 +1746,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void gemm_flow16_kernel(LinearP
       }
       if (m % LS == LS / 2) {
         if constexpr (EXT && NF4) issue_load(2 * t + 4, m / LS);
-        else if constexpr (EXT) oxe.load_one(m / LS, xdst, tr, kbx2);
+        else if constexpr (EXT) oxe.load_one(m / LS, xdst, g2 ? tr1 : tr, kbx2);
         else ox.load_one(m / LS, xdst, xr, kb2);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -1888,21 +1904,7 @@ template __global__ void gemm_flow16_kernel<Flow16SCfg, false, true>(LinearProbl
 
 hipError_t launch(const LinearProblem& p, hipStream_t s) {
   if (max_groups_per_tile(p, Flow16Cfg::BN) <= 2) {
-    // The output tile (both give the same bits): 256 x 256, one workgroup per CU, or 128 x 128,
-    // two per CU. The larger does more MFMA work per LDS byte; the smaller ran at 0.77-0.92 of
-    // its rate on MI355X (1536- and 8960-wide inputs) but fills the last wave of tiles better and
-    // pads fewer rows when T is not a multiple of 256. Estimated time, in units of one 128 x 128
-    // tile's MFMA work (padding included) at the larger tile's rate: waves of 256 x 256 tiles
-    // (one per CU) take 4 each, waves of 128 x 128 tiles (two per CU at 0.85 of the rate) take
-    // 2 / 0.85. The smaller is taken when its estimate is lower (or when asked for). With T a
-    // multiple of 256 this is the smaller tile's wave fill, discounted by 0.85, beating the
-    // larger's; up to 128 tokens the smaller always wins (the larger's rows are half padding).
-    const int64_t cus = device_cus();
-    const int64_t t256 = ((p.T + 255) / 256) * ((p.N + 255) / 256);
-    const int64_t t128 = ((p.T + 127) / 128) * ((p.N + 127) / 128);
-    const double est256 = 4.0 * static_cast<double>((t256 + cus - 1) / (cus > 0 ? cus : 1));
-    const double est128 = 2.0 / 0.85 * static_cast<double>((t128 + 2 * cus - 1) / (cus > 0 ? 2 * cus : 1));
-    const bool small = p.tile == 2 || (p.tile == 0 && cus > 0 && est128 < est256);
+    const bool small = p.tile == 2 || (p.tile == 0 && small_tile(p.T, p.N, device_cus()));
     if (p.routed) return small ? launch_flow16<Flow16SCfg, false, true>(p, s) : launch_flow16<Flow16Cfg, false, true>(p, s);
     if (p.nf4) return small ? launch_flow16<Flow16SCfg, true>(p, s) : launch_flow16<Flow16Cfg, true>(p, s);
     return small ? launch_flow16<Flow16SCfg>(p, s) : launch_flow16<Flow16Cfg>(p, s);

@@ -140,9 +140,10 @@ struct Routing {
 };
 
 // The routed GEMM's view of its pool: B [n_adapters, N, rank] and what the routed producer left in
-// the workspace (t~ [T, ldt] in LinearProblem::work).
+// the workspace (t~ [T, ldt] as two bf16 terms: the first in LinearProblem::work, the second in mid).
 struct RoutedGemm {
   const void* B;
+  const void* mid;
   const int32_t* eid;   // [T]: the token's adapter, -1 none
   const int32_t* blk;   // [ceil(T / 16)]: the block's adapter, -1 none at all, -2 several
   const int32_t* ranks;
@@ -177,6 +178,23 @@ struct LinearProblem {
 // phase 0 runs both, 1 only the rank-wide producer, 2 only the fused GEMM
 // (which reads the t~ a phase-1 call left in the workspace).
 hipError_t launch_lossless(const LinearProblem& p, hipStream_t s, int phase = 0);
+
+// The hot GEMM's output tile (both give the same bits): 256 x 256, one workgroup per CU, or 128 x 128 (true),
+// two per CU. The larger does more MFMA work per LDS byte; the smaller ran at 0.77-0.92 of
+// its rate on MI355X (1536- and 8960-wide inputs) but fills the last wave of tiles better and
+// pads fewer rows when T is not a multiple of 256. Estimated time, in units of one 128 x 128
+// tile's MFMA work (padding included) at the larger tile's rate: waves of 256 x 256 tiles
+// (one per CU) take 4 each, waves of 128 x 128 tiles (two per CU at 0.85 of the rate) take
+// 2 / 0.85. The smaller is taken when its estimate is lower (or when asked for). With T a
+// multiple of 256 this is the smaller tile's wave fill, discounted by 0.85, beating the
+// larger's; up to 128 tokens the smaller always wins (the larger's rows are half padding).
+inline bool small_tile(int64_t T, int64_t N, int64_t cus) {
+  const int64_t t256 = ((T + 255) / 256) * ((N + 255) / 256);
+  const int64_t t128 = ((T + 127) / 128) * ((N + 127) / 128);
+  const double est256 = 4.0 * static_cast<double>((t256 + cus - 1) / (cus > 0 ? cus : 1));
+  const double est128 = 2.0 / 0.85 * static_cast<double>((t128 + 2 * cus - 1) / (cus > 0 ? 2 * cus : 1));
+  return cus > 0 && est128 < est256;
+}
 
 // Routed: the hot GEMM with its tokens' own adapters (bf16; p.routed, t~ in p.work).
 hipError_t launch_routed_gemm(const LinearProblem& p, hipStream_t s);

@@ -6,8 +6,10 @@
 
 namespace lora {
 
-// Rank-wide producer: t = s_t . x[t] A_a^T of every token's own adapter a, as hi = RN_bf16(t) and, where
-// mid is not null, the rest of its 24 bits in mid and lo. Writes eid and blk (RoutedGemm) too.
+// Rank-wide producer: t = s_t . x[t] A_a^T of every token's own adapter a, as hi = RN_bf16(t), mid =
+// RN_bf16(t - hi) and, with three terms, the rest of its 24 bits in lo. The layer's second product takes two
+// terms (hi alone left 2^-8 of every rank's part in an output that two terms round once; as the base product's
+// operands they are multiplied exactly), the gradients' contractions three. Writes eid and blk (RoutedGemm) too.
 // With many tokens (splits > 0) a block of 128 tokens with up to kRingAdapters is multiplied by a ring of
 // LDS stages, once per adapter, K in `splits` parts of ks stages of 64; the other blocks, and all blocks of
 // fewer tokens, 16 tokens at a time straight from memory.
@@ -21,6 +23,7 @@ struct RoutedDown {
   Routing rt;
   uint16_t* hi;        // [T, ldt]; the row of a token with an adapter is written whole (zeros behind the
   uint16_t *mid, *lo;  // adapter's rank), another token's not at all
+  int terms;           // 2: hi and mid, 3: lo too
   int64_t ldt;         // rank_pad(rank)
   int32_t* eid;        // [T]
   int32_t* blk;        // [ceil(T / 16)]

@@ -58,7 +58,7 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   const int64_t rp = lora::rank_pad(R);
   Take take;
   L.few = take(few_bytes(T, K, N));
-  for (int i = 0; i < (lora::few_path(T, N) ? 3 : 1); ++i) L.t[i] = take(static_cast<size_t>(T) * rp * 2);
+  for (size_t& o : L.t) o = take(static_cast<size_t>(T) * rp * 2);
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
@@ -166,7 +166,7 @@ hipError_t launch_layer(const void* x, int64_t T, int64_t K, int64_t ldx, const 
                         void* part, hipStream_t s) {
   const lora::RoutedDown& d = downs.d[0];
   lora::RoutedGemm rt;
-  rt.B = B; rt.eid = d.eid; rt.blk = d.blk; rt.ranks = pool->ranks; rt.rank = pool->rank;
+  rt.B = B; rt.mid = d.mid; rt.eid = d.eid; rt.blk = d.blk; rt.ranks = pool->ranks; rt.rank = pool->rank;
   if (lora::few_path(T, N)) {
     lora::RoutedFew f;
     f.x = static_cast<const uint16_t*>(x); f.ldx = ldx;
@@ -229,9 +229,10 @@ int lora_linear_routed_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   d.A = static_cast<const uint16_t*>(pool->A);
   d.rt = routing(pool, token_adapter, token_scale);
   d.hi = reinterpret_cast<uint16_t*>(ws + L.t[0]); d.ldt = lora::rank_pad(pool->rank);
-  const bool few = lora::few_path(T, N);
   if (lora::sorts_tokens(T)) d.order = reinterpret_cast<int32_t*>(ws + L.order);
-  if (few) d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]), d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
+  d.mid = reinterpret_cast<uint16_t*>(ws + L.t[1]);
+  d.lo = reinterpret_cast<uint16_t*>(ws + L.t[2]);
+  d.terms = 2;
   d.eid = reinterpret_cast<int32_t*>(ws + L.eid);
   d.blk = reinterpret_cast<int32_t*>(ws + L.blk);
   plan_down(d, K, N);
@@ -314,7 +315,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   std::memset(&du, 0, sizeof(du));
   du.T = T;
   du.rt = routing(pool, token_adapter, token_scale);
-  du.ldt = rp;
+  du.ldt = rp; du.terms = 3;
   du.eid = at32(L.eid); du.blk = at32(L.blk);
   if (lora::sorts_tokens(T)) du.order = at32(L.order);
   du.ring = reinterpret_cast<int32_t*>(ws + L.ring);

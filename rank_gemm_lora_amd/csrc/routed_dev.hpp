@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
   return v;
 }
 
-// NV consecutive scaled values t of one token (at element `at`) as bf16: hi alone, or hi + mid + lo, which
+// NV consecutive scaled values t of one token (at element `at`) as bf16: hi + mid, or hi + mid + lo, which
 // together hold all 24 bits of t (each the nearest bf16 of what the ones before it leave; nothing behind a
 // value that is not finite). NV is 2 or 4.
 template <int NV>
@@ -65,7 +65,7 @@ __device__ __forceinline__ void put_rank_wide(const RoutedDown& p, int64_t at, c
   uint16_t* const dst[3] = {p.hi, p.mid, p.lo};
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    if (k > 0 && p.mid == nullptr) break;
+    if (k == p.terms) break;
     if constexpr (NV == 4) *reinterpret_cast<uint2*>(dst[k] + at) = uint2{w[k][0], w[k][1]};
     else *reinterpret_cast<uint32_t*>(dst[k] + at) = w[k][0];
   }
