@@ -2243,15 +2243,15 @@ __global__ __launch_bounds__(DP::THREADS) void routed_ring_kernel(RoutedDowns ps
   }
   float s;
   route(p.rt, m, p.T, s);
+  const int live = route_live(p.rt.ranks, p.rt.rank, a);
 #pragma unroll
   for (int i = 0; i < P::NI; ++i)
 #pragma unroll
     for (int gq = 0; gq < 4; ++gq) {
       const int q = q0 + wn0 + i * 32 + gq * 8 + h * 4;
       if (q >= p.ldt) continue;
-      const float t[4] = {acc[i][0][gq * 4] * s, acc[i][0][gq * 4 + 1] * s, acc[i][0][gq * 4 + 2] * s,
-                          acc[i][0][gq * 4 + 3] * s};
-      put_rank_wide<4>(p, m * p.ldt + q, t);
+      const float t[4] = {acc[i][0][gq * 4], acc[i][0][gq * 4 + 1], acc[i][0][gq * 4 + 2], acc[i][0][gq * 4 + 3]};
+      put_rank_wide<4>(p, m * p.ldt + q, q, live, t, s);
     }
 }
 

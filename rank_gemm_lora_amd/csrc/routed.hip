@@ -75,7 +75,7 @@ struct SortedTokens {
 };
 // order: the sorted tokens, of which `block` is one (null: blocks are of the tokens as they come). Adapters slot,
 // slot + slots, .. of the block; part `part` of K; tell: eid and blk are this workgroup's to write.
-// FAT: twice the loads in flight where the adapter has more than 16 ranks (154 registers against 128).
+// FAT: twice the loads in flight where the adapter has more than 16 ranks (160 registers against 117).
 template <bool FAT>
 __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f32x4 (&red)[kDownWaves][4][64],
                                            const SortedTokens* order, int q0, int slot, int slots, int part, bool tell) {
@@ -137,8 +137,8 @@ __device__ __forceinline__ void down_block(const RoutedDown& p, int64_t block, f
       if (p.parts > 1) {
         *reinterpret_cast<f32x4*>(p.tpart + part * p.T * p.ldt + at) = v;
       } else {
-        const float t[4] = {v[0] * s, v[1] * s, v[2] * s, v[3] * s};
-        put_rank_wide<4>(p, at, t);
+        const float t[4] = {v[0], v[1], v[2], v[3]};
+        put_rank_wide<4>(p, at, q0 + wave * 16 + 4 * q, route_live(p.rt.ranks, p.rt.rank, a), t, s);
       }
     }
     __syncthreads();
@@ -208,11 +208,13 @@ __device__ __forceinline__ void down_join(const RoutedDown& p, int64_t group) {
   if (n <= 1) return;
   const int64_t m = group * (2 * kDownWaves) + (threadIdx.x >> 5);
   if (m >= p.T) return;
-  const int64_t at = m * p.ldt + blockIdx.y * 64 + 2 * (threadIdx.x & 31);
+  const int q = blockIdx.y * 64 + 2 * (threadIdx.x & 31);
+  const int64_t at = m * p.ldt + q;
   f32x2 w[8];  // (all parts' loads before their adds; a part past the last reads the last again, unused)
 #pragma unroll
   for (int z = 0; z < 8; ++z) w[z] = *reinterpret_cast<const f32x2*>(p.tpart + min(z, n - 1) * p.T * p.ldt + at);
-  if (p.eid[m] < 0 || (p.splits > 0 && p.ring[m / kRingBlock] < 0)) return;
+  const int a = p.eid[m];
+  if (a < 0 || (p.splits > 0 && p.ring[m / kRingBlock] < 0)) return;
   float v[2] = {0.f, 0.f}, s;
 #pragma unroll
   for (int z = 0; z < 8; ++z)
@@ -221,9 +223,7 @@ __device__ __forceinline__ void down_join(const RoutedDown& p, int64_t group) {
       v[1] += w[z][1];
     }
   route(p.rt, m, p.T, s);
-  v[0] *= s;
-  v[1] *= s;
-  put_rank_wide<2>(p, at, v);
+  put_rank_wide<2>(p, at, q, route_live(p.rt.ranks, p.rt.rank, a), v, s);
 }
 
 // The blocks of 16 that the ring did not take: blocks first, + stride, ..; 64 at a time are looked at, one per lane

@@ -24,6 +24,12 @@ __device__ __forceinline__ int route_rank(const int32_t* ranks, int rank, int a)
   return ranks != nullptr ? __builtin_amdgcn_readfirstlane((min(ranks[a], rank) + 7) & ~7) : rank;
 }
 
+// Its rank itself: what lies behind is zeros in t, whatever x and the scale are (an infinite x times the zeros
+// that pad a rank to 8, to the slot or to 64 would be NaN there, and so would the token's outputs).
+__device__ __forceinline__ int route_live(const int32_t* ranks, int rank, int a) {
+  return ranks != nullptr ? min(ranks[a], rank) : rank;
+}
+
 typedef __attribute__((address_space(3))) void lds_void;
 
 // s_waitcnt immediate: at most n vector memory operations outstanding, other counters not waited for.
@@ -44,15 +50,15 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
   return v;
 }
 
-// NV consecutive scaled values t of one token (at element `at`) as bf16: hi + mid, or hi + mid + lo, which
+// NV consecutive values v of one token, scaled by s, from rank q (at element `at`) on, zeros from rank `live` on, as bf16: hi + mid, or hi + mid + lo, which
 // together hold all 24 bits of t (each the nearest bf16 of what the ones before it leave; nothing behind a
 // value that is not finite). NV is 2 or 4.
 template <int NV>
-__device__ __forceinline__ void put_rank_wide(const RoutedDown& p, int64_t at, const float (&t)[NV]) {
+__device__ __forceinline__ void put_rank_wide(const RoutedDown& p, int64_t at, int q, int live, const float (&v)[NV], float s) {
   uint32_t w[3][NV / 2];
 #pragma unroll
   for (int e = 0; e < NV; e += 2) {
-    float a = t[e], b = t[e + 1];
+    float a = q + e < live ? v[e] * s : 0.f, b = q + e + 1 < live ? v[e + 1] * s : 0.f;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const uint32_t h = pack_bf16x2(a, b);

@@ -154,3 +154,41 @@ def test_a_token_in_batches_of_two_sizes(small, large, N):
     rr.check(b, y[:small], bound[:small], "in the batch")
     rr.check(a, y[:small], bound[:small], "alone")
     assert bool(((a - b).abs() <= 2 * bound[:small]).all())
+
+
+# ----------------------------------------------------------------------------- infinite tokens
+
+INFINITE = [
+    (3, 72, 40, 2, 24, "mixed", "few"), (100, 72, 200, 3, 40, "mixed", "few"), (200, 9000, 72, 3, 24, "mixed", "few"),
+    (300, 72, 5600, 3, 40, "mixed", "128"), (1100, 72, 304, 1, 8, "long", "128"), (1100, 1160, 304, 2, 72, "long", "128"),
+    (1100, 72, 304, 20, 24, "mixed", "128"), (3001, 72, 2904, 2, 24, "long", "256"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,n,R,layout,route", INFINITE)
+@pytest.mark.parametrize("ranks", [False, True])
+def test_an_infinite_token_meets_no_padding(T, K, N, n, R, layout, route, ranks):
+    """Positive weights and one infinite input: the outputs are infinite, and a NaN among them would come from the
+    zeros that pad a rank (to the slot, to 8 or to 64). Ranks that are no multiples of 8 among them."""
+    say("routed infinite token", T, K, N, n, R, layout, route, ranks)
+    d = rr.case(T, K, N, n, R, T, layout, none=0.0)
+    d["ids"] %= n
+    if ranks:
+        d["ranks"] = torch.tensor([R - 3 - 2 * (i % 2) for i in range(n)], dtype=torch.int32)
+    live = torch.arange(R)[None, :] < (torch.full((n,), R) if d["ranks"] is None else d["ranks"])[:, None]
+    for k in ("W", "A", "B"):
+        d[k] = d[k].abs().clamp_min(0.01)
+    d["A"], d["B"] = d["A"] * live[:, :, None], d["B"] * live[:, None, :]
+    assert way(T, N) == route
+    g = gpu(d)
+    rows = [0, T // 2, T - 1]
+    y0, dx0 = run_fwd(g), run_bwd(g, want=("dx",))[0]
+    g["x"][rows, 5] = float("inf")
+    g["dy"][rows, 7] = float("inf")
+    y1, dx1 = run_fwd(g), run_bwd(g, want=("dx",))[0]
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[rows] = False
+    for a, b in ((y0, y1), (dx0, dx1)):
+        assert torch.equal(a[rest], b[rest])
+        assert bool((b[rows] == float("inf")).all()), b[rows]
