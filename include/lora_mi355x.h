@@ -480,9 +480,7 @@ size_t lora_linear_routed_workspace_size(int64_t T, int64_t K, int64_t N, int32_
  * order, u_t and s_t x A^T taken in fp32 (as three bf16 terms). An adapter's gradients depend on its own
  * tokens only.
  *   workspace  at least lora_linear_routed_bwd_workspace_size(..., dx != NULL) bytes
- * T == 0 writes zero gradients. LORA_ERR_UNSUPPORTED where A and B of all slots, and W, take 2^24 or more
- * tiles of 64 x 64 (their transposed copies are one launch; A and W count with dx alone, and four tiles
- * for each slot).
+ * T == 0 writes zero gradients.
  */
 int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
                            const lora_pool* pool, const int32_t* token_adapter, const float* token_scale,

@@ -121,13 +121,6 @@ bool in_limits(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   return T < kMaxTokens && K <= kMaxRowBytes / 4 && N <= kMaxRowBytes / 4 && n <= LORA_MAX_POOL && R <= LORA_MAX_RANK;
 }
 
-// The backward's transposes, 64 x 64 tiles of which a workgroup of 1024 threads takes four, beside one for each
-// adapter, are one launch.
-bool transposes_in_limits(int64_t K, int64_t N, int64_t n, int64_t R, bool want_dx) {
-  const int64_t k = (K + 63) / 64, m = (N + 63) / 64, r = (R + 63) / 64;
-  return n * r * m + (want_dx ? n * r * k + k * m : 0) + 4 * n < int64_t(1) << 24;
-}
-
 // Checks of the pool and the routing that both directions share.
 int check_pool(const lora_pool* pool, const int32_t* token_adapter, const float* token_scale, int64_t T, int64_t K,
                int64_t N) {
@@ -265,7 +258,6 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
   if ((dx != nullptr && W == nullptr) || (T > 0 && (x == nullptr || dy == nullptr))) return LORA_ERR_NULL_PTR;
   int st = check_pool(pool, token_adapter, token_scale, T, K, N);
   if (st != LORA_OK) return st;
-  if (!transposes_in_limits(K, N, pool->n_adapters, pool->rank, dx != nullptr)) return LORA_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(W, 16) || !aligned(dy, 16) || !aligned(dx, 2) || !aligned(dA, 4) ||
       !aligned(dB, 4) || !aligned(workspace, 16) || K % 8 != 0 || N % 8 != 0 || ldx % 8 != 0 || lddy % 8 != 0)
     return LORA_ERR_ALIGN;
@@ -361,9 +353,7 @@ int lora_linear_routed_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, con
 
 size_t lora_linear_routed_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t n_adapters, int32_t rank,
                                              int32_t want_dx) {
-  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1 || !in_limits(T, K, N, n_adapters, rank) ||
-      !transposes_in_limits(K, N, n_adapters, rank, want_dx != 0))
-    return 0;
+  if (T <= 0 || K <= 0 || N <= 0 || n_adapters < 0 || rank < 1 || !in_limits(T, K, N, n_adapters, rank)) return 0;
   return bwd_layout(T, K, N, n_adapters, rank, want_dx != 0).total;
 }
 

@@ -14,7 +14,7 @@ import torch
 
 import rank_gemm_lora_amd as rg
 from tests import routed_ref as rr
-from tests.test_routed import DEV, UNSUP, WS, bwd, gpu, run_bwd, run_fwd, say
+from tests.test_routed import DEV, gpu, run_bwd, run_fwd, say
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
@@ -447,21 +447,3 @@ def test_a_large_batch_on_a_pool_beyond_32_bit_offsets():
     ids = torch.where(g["ids"] < 0, -1, g["ids"] + (n - 2)).to(torch.int32)
     y = rg.lora_linear_routed(g["x"], g["W"], g["b"], Ap, Bp, sc, ids, token_scale=g["token_scale"])
     rr.check(y, *forward(d), "y")
-
-
-# ----------------------------------------------------------------------------- sizes that a launch cannot hold
-
-def test_pools_whose_transposes_pass_a_launch_are_refused():
-    """The backward's copies of A and B go in tiles of 64 x 64, a launch holds fewer than 2^24 of them. (The largest
-    pool that is taken reaches the launch, which has no GPU here.)"""
-    q = rg.lora_linear_routed_bwd_workspace_size
-    for T in (64, 2000):
-        for kw in (dict(n=8192, R=8, K=1 << 17, ldx=1 << 17, lddx=1 << 17, N=8, lddy=8),
-                   dict(n=8192, R=8, N=1 << 17, lddy=1 << 17, K=8, ldx=8, lddx=8)):
-            assert bwd(T=T, wsb=1 << 35, **kw) == UNSUP
-            assert q(T, kw["K"], kw["N"], 8192, 8) == 0
-        ok = dict(n=8190, R=8, K=1 << 16, ldx=1 << 16, lddx=1 << 16, N=8, lddy=8)
-        assert bwd(T=T, wsb=q(T, ok["K"], ok["N"], 8190, 8) - 1, **ok) == WS
-    # without dx A is not transposed, without dA (and dx) nor is B
-    wide = dict(n=8192, R=8, K=1 << 17, ldx=1 << 17, N=8, lddy=8, dx=None)
-    assert bwd(wsb=0, **wide) == WS and q(64, 1 << 17, 8, 8192, 8, False) > 0
