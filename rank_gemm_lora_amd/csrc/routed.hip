@@ -639,6 +639,7 @@ struct RoutePrepare {
   RoutePlan plan;
   TransposeStack s[kTransposeStacks];
   int64_t first[kTransposeStacks + 1];  // 64 x 64 tiles [first, next first) are a stack's
+  int64_t at;                           // workgroups of the launches before this one
 };
 
 // Workgroups below n_adapters (with LOADS): the plan; the others (TRANSPOSE): tiles, TILES of them by 256 threads
@@ -652,13 +653,13 @@ __global__ __launch_bounds__(LOADS > 0 ? 1024 : 256, LOADS == 8 ? 4 : 8) void ro
   } u;
   if constexpr (LOADS > 0) {
     __shared__ int sums[5][16], mine[16];
-    if (!TRANSPOSE || static_cast<int>(blockIdx.x) < p.plan.n_adapters) {
+    if (!TRANSPOSE || p.at + blockIdx.x < p.plan.n_adapters) {
       route_plan<LOADS>(p.plan, blockIdx.x, u.counts, sums, mine);
       return;
     }
   }
   const int part = threadIdx.x >> 8;
-  const int64_t b = static_cast<int64_t>(blockIdx.x - p.plan.n_adapters) * TILES + part;
+  const int64_t b = (p.at + blockIdx.x - p.plan.n_adapters) * TILES + part;
   int k = 0;
 #pragma unroll
   for (int i = 1; i < kTransposeStacks; ++i) k = b >= p.first[i] ? i : k;
@@ -918,13 +919,18 @@ hipError_t launch_route_prepare(const RoutePlan& plan, const TransposeStack* sta
   p.first[kTransposeStacks] = tiles;
   const int per = plan.n_adapters > 0 ? 4 : 1;  // (transposes alone, 27 MB: 20.5 us one to a workgroup, 25 four)
   const int64_t blocks = plan.n_adapters + (tiles + per - 1) / per;
-  if (blocks == 0) return hipSuccess;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(static_cast<unsigned>(256 * per));
-  if (plan.n_adapters == 0) hipLaunchKernelGGL((route_prepare_kernel<true, 0>), grid, block, 0, s, p);
-  else if (plan.eid == nullptr) hipLaunchKernelGGL((route_prepare_kernel<true, 1>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((route_prepare_kernel<false, 8>), grid, block, 0, s, p);
-  return hipGetLastError();
+  // (a launch has fewer than 2^32 threads: the copies of a pool of 2^24 tiles and more take several)
+  const int64_t most = (int64_t(1) << 31) / (256 * per);
+  for (p.at = 0; p.at < blocks; p.at += most) {
+    const int64_t left = blocks - p.at;
+    const dim3 grid(static_cast<unsigned>(left < most ? left : most)), block(static_cast<unsigned>(256 * per));
+    if (plan.n_adapters == 0) hipLaunchKernelGGL((route_prepare_kernel<true, 0>), grid, block, 0, s, p);
+    else if (plan.eid == nullptr) hipLaunchKernelGGL((route_prepare_kernel<true, 1>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((route_prepare_kernel<false, 8>), grid, block, 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_routed_contract(RoutedContracts p, hipStream_t s) {

@@ -447,3 +447,28 @@ def test_a_large_batch_on_a_pool_beyond_32_bit_offsets():
     ids = torch.where(g["ids"] < 0, -1, g["ids"] + (n - 2)).to(torch.int32)
     y = rg.lora_linear_routed(g["x"], g["W"], g["b"], Ap, Bp, sc, ids, token_scale=g["token_scale"])
     rr.check(y, *forward(d), "y")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("want", [("dx",), ("dx", "dA")])
+def test_transposed_copies_of_several_launches(want):
+    """A pool of 17 GB whose copies take more than 2^24 tiles of 64 x 64, the threads of one launch; with dA the
+    plan goes before them."""
+    say("routed copies of several launches", want)
+    T, n, R, K, N = 40, 8192, 8, 1 << 17, 8
+    slots = torch.tensor([0, 5000, n - 1], dtype=torch.int32)
+    d = rr.case(T, K, N, 3, R, 2, "mixed")
+    g = gpu(d)
+    Ap = torch.zeros((n, R, K), dtype=torch.bfloat16, device=DEV)
+    Bp = torch.zeros((n, N, R), dtype=torch.bfloat16, device=DEV)
+    sc = torch.ones(n, device=DEV)
+    at = slots.to(DEV).long()
+    Ap[at], Bp[at], sc[at] = g["A"], g["B"], g["scales"]
+    ids = torch.where(d["ids"] < 0, -1, slots[d["ids"].clamp_min(0).long()]).to(torch.int32).to(DEV)
+    dx, dA, _ = rg.lora_linear_routed_backward(g["x"], g["W"], Ap, Bp, g["dy"], sc, ids, token_scale=g["token_scale"],
+                                               want=want)
+    rr.check(dx, *gradient(d), "dx")
+    if dA is not None:
+        rr.check(dA[at], rr.backward(d)[0][1], rr.backward(d)[1][1], "dA")
+        dA[at] = 0
+        assert all(not bool(part.any()) for part in dA.split(512))
