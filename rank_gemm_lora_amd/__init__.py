@@ -620,7 +620,7 @@ class LoraAdamW:
     starts at zero. ``lr_step``: optional fp64 device tensor {lr, step} that the kernel reads in place of
     ``lr`` and the step count, for captured steps (``state()["step"]`` counts the calls of ``step``, not
     replays). lr, betas, eps and weight_decay may be changed between
-    steps. The optimizer keeps the tensors; their buffers must stay where they are."""
+    steps. The optimizer keeps the tensors; their buffers must stay where they are. It is made outside of captures."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, master=None,
                  state_bits=32, state=None, lr_step=None, stream=None):
@@ -630,6 +630,8 @@ class LoraAdamW:
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
         dev = params[0].device
+        if dev.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("LoraAdamW cannot be made during a capture: every replay would start it anew")
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits, self.device = state_bits, dev
         self.lr_step = _of(lr_step, "lr_step", (2,), torch.float64, dev)
@@ -671,7 +673,7 @@ class LoraAdamW:
             self._table = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
             self._plan = lora_adamw_plan(ts, _dt(params[0]), _dt(grads[0]), state_bits, self._table.data_ptr(),
                                          self._table.numel(), _stream_on(dev, stream))
-        if dev.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        if dev.type == "cuda":
             # (the table, new masters and new moments are there for a step on any stream)
             torch.cuda.current_stream(dev).synchronize()
             if stream is not None:
