@@ -440,10 +440,11 @@ typedef struct lora_pool {
  *   workspace      at least lora_linear_routed_workspace_size(...) bytes
  * ranks[a] is taken up to the slot's rank and rounded up to a multiple of 8:
  * rows of A and columns of B between an adapter's rank and that multiple must
- * hold zeros, those behind it are never read. The values behind the device
+ * hold zeros; the values of those behind it are never used. The values behind the device
  * pointers are read by the kernels alone (a captured call takes the routing
  * that they hold at each replay); they cannot be refused, and an adapter or
- * scale that is not finite reaches the outputs of its own tokens and no others.
+ * scale that is not finite reaches the outputs of its own tokens and no others
+ * (as infinities or NaN).
  * Tokens may come in any order; the adapter costs least where tokens of one
  * adapter lie next to one another.
  * T == 0 is a valid no-op. LORA_ERR_ALIGN unless x, W, A, B and the workspace
@@ -548,7 +549,7 @@ int lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n_tensors, int32_t
  * lora_adamw_step -- the step, one launch.
  *   step     1 for the first step
  *   lr_step  NULL, or DEVICE {lr, step} (two doubles, 8-byte aligned), read by the kernel in place of lr
- *            and step, so that a captured step follows a schedule
+ *            and step, so that a captured step follows a schedule (values there cannot be refused)
  *   beta1, beta2 in [0, 1), eps, weight_decay, lr >= 0, step >= 1: else LORA_ERR_UNSUPPORTED;
  *   LORA_ERR_NONFINITE for a NaN or infinite one
  * A gradient that is not finite makes its element's state so, and with 8-bit moments its block's.

@@ -24,8 +24,8 @@ constexpr uint32_t kOutOfRange = 0x80000000u;  // a buffer offset past every ran
 // token r), the next 128 k (64 above 32 ranks) in flight during the MFMAs of these; all 16 tokens are
 // multiplied, and the rows of the adapter's own tokens are kept. From 17 to 256 tokens the blocks are of the
 // tokens sorted by adapter (every workgroup sorts them for itself, counting the tokens before each), which
-// leaves a block the fewest adapters. Beside the ring, a workgroup looks through blocks gridDim.x apart for
-// those that the ring left. Bound by the latency of dependent loads (routing, then operands), not by bytes:
+// leaves a block the fewest adapters. Beside the ring, kBesideSlots workgroups at a time look through blocks a
+// stride apart for those that the ring left (down_beside). Bound by the latency of dependent loads (routing, then operands), not by bytes:
 // 5.4 us for one token of K 1536, rank 16.
 //
 // acc[b] += rows 16 b .. of A times the tokens over [k_lo, k_hi), groups of 32 ST k.
@@ -228,7 +228,7 @@ __device__ __forceinline__ void down_join(const RoutedDown& p, int64_t group) {
 
 // The blocks of 16 that the ring did not take: blocks first, + stride, ..; 64 at a time are looked at, one per lane
 // (every wave the same). kBesideSlots workgroups share a block's adapters (2000 tokens of 16 mixed adapters,
-// 4096 -> 4096: 142 us a call against 204 with one).
+// 4096 -> 4096: 155 us a call against 209 with one).
 constexpr int kBesideSlots = 4;
 __device__ __forceinline__ void down_beside(const RoutedDown& p, f32x4 (&red)[kDownWaves][4][64], int64_t first,
                                             int64_t stride, int slot) {

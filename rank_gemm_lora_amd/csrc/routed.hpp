@@ -13,8 +13,8 @@ namespace lora {
 // With many tokens (splits > 0) a block of 128 tokens with up to kRingAdapters is multiplied by a ring of
 // LDS stages, once per adapter, K in `splits` parts of ks stages of 64; the other blocks, and all blocks of
 // fewer tokens, 16 tokens at a time straight from memory.
-// (9000 tokens that take 6 adapters in turn, 8960 -> 1536, rank 64: 378 us with all of a block's adapters in the ring,
-// 859 with blocks of more than four left to the 16-token form; 16 instead of 8 costs the launches of others 1%)
+// (9000 tokens that take 6 adapters in turn, 8960 -> 1536, rank 64: 367 us with all of a block's adapters in the ring,
+// 926 with blocks of more than four left to the 16-token form; 16 instead of 8 costs the launches of others 1%)
 constexpr int kRingAdapters = 8;
 struct RoutedDown {
   const uint16_t* x; int64_t ldx;
@@ -36,8 +36,9 @@ struct RoutedDown {
                        // adapter last. The blocks of 16 are of this order
 };
 // Few tokens: t~ (as hi and mid) and the base product over a ring of LDS stages in one launch, then the sum.
-// Above it the hot GEMM: with every token on one adapter it would be faster from about 128 tokens on (256 tokens,
-// 4096 -> 14336: 68 against 77 us), with mixed ones it is slower up to there and beyond (121 against 90 us).
+// Above it the hot GEMM: with every token on one adapter it would be a little faster from somewhere between 192 and
+// 256 tokens on (4096 -> 14336, rank 16: 66 against 59 us, 67 against 71), with mixed ones it is slower there and
+// beyond (256 tokens: of 8 adapters 81 against 72 us, of 64 136 against 86).
 constexpr int64_t kFewMaxT = 256;
 // (one block of 16 is as good in any order)
 inline bool sorts_tokens(int64_t T) { return T > kRouteBlock && T <= kFewMaxT; }

@@ -58,7 +58,7 @@ FwdLayout fwd_layout(int64_t T, int64_t K, int64_t N, int64_t n, int64_t R) {
   const int64_t rp = lora::rank_pad(R);
   Take take;
   L.few = take(few_bytes(T, K, N));
-  for (size_t& o : L.t) o = take(static_cast<size_t>(T) * rp * 2);
+  for (size_t& o : L.t) o = take(static_cast<size_t>(T) * rp * 2);  // (the third place is the gradients': not written)
   L.eid = take(static_cast<size_t>(T) * 4);
   L.blk = take(static_cast<size_t>((T + lora::kRouteBlock - 1) / lora::kRouteBlock) * 4);
   if (lora::sorts_tokens(T)) L.order = take(static_cast<size_t>(T) * 8);
