@@ -558,6 +558,98 @@ int lora_adamw_step(const lora_adamw_plan_t* plan, double lr, double beta1, doub
                     double weight_decay, int64_t step, const double* lr_step, double grad_scale, void* stream);
 
 /*
+ * A fine-tuning step beside the plain linear layer: dropout before an adapter,
+ * and the gated half of a feed-forward block with adapters on both projections
+ * (Unsloth fast-LoRA chapter, sections 2 to 4: closed-form gradients of the
+ * adapters, the base weight frozen). bf16; x, W, A, B, dy / dh and the
+ * workspace 16-byte aligned, K, ldx, lddy / lddh and the ranks multiples of 8,
+ * and N / F too in the backward calls (else LORA_ERR_ALIGN). Rank-wide
+ * intermediates are kept as two bf16 terms (within 2^-16 of each element), sums
+ * are fp32, and the same call gives the same bits. An adapter with a combined
+ * scale of +-0 is inactive: its gradients are zeros.
+ *   grad_dtype  of dA and dB: LORA_F32 or LORA_BF16 (rounded once; 4-byte aligned in both)
+ * LORA_ERR_UNSUPPORTED from 2^26 tokens on. T == 0 is a valid call (zero gradients).
+ */
+
+/*
+ * lora_linear_dropout_fwd -- y = x.W^T + b + s . (D(x).A^T).B^T with dropout in
+ * front of the adapter, D(x) = x . keep / (1 - p'), and its gradients:
+ *
+ *     u = s/(1-p') . dy.B,  dx = dy.W + keep . (u.A),  dA = u^T.(x . keep),  dB = dy^T.(s D(x).A^T)
+ *
+ * keep[t, k] is a function of (seed, offset, t K/8 + k/8, k % 8) alone, the same
+ * in both calls, and is never stored: the four words of Philox-4x32 (Salmon et
+ * al., SC'11) with 7 rounds, key = seed, counter = {t K/8 + k/8, offset} (each
+ * 64 bits, low word first), give 16 bits to each of the 8 elements 8 (k/8) .. + 7
+ * of token t, element 2 i + h bits 16 h .. + 15 of word i; kept where they are at
+ * least p' 65536, p' = round(65536 p) / 65536.
+ *   p       0 <= p, p' < 1 (else LORA_ERR_UNSUPPORTED); p' = 0 keeps everything
+ *   rng     NULL, or DEVICE {seed, offset} (8-byte aligned), read by the kernels in place of the two
+ *           arguments, so that a captured call draws anew where the caller advances the offset
+ *   A, B    required; other arguments as lora_linear_fwd / lora_linear_bwd (dx, dA, dB optional)
+ */
+int lora_linear_dropout_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                            const void* bias, const void* A, const void* B, int32_t rank, double alpha,
+                            double strength, double request_scale, double p, uint64_t seed, uint64_t offset,
+                            const uint64_t* rng, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                            void* stream);
+int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
+                            const void* A, const void* B, int32_t rank, double alpha, double strength,
+                            double request_scale, double p, uint64_t seed, uint64_t offset, const uint64_t* rng,
+                            const void* dy, int64_t lddy, void* dx, int64_t lddx, void* dA, void* dB,
+                            int32_t grad_dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of the two calls; the backward's covers the forward's. */
+size_t lora_linear_dropout_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank);
+size_t lora_linear_dropout_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank);
+
+/* g . sigmoid(g), g . Phi(g), and g . (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+typedef enum { LORA_ACT_SILU = 0, LORA_ACT_GELU = 1, LORA_ACT_GELU_TANH = 2 } lora_activation;
+
+/* Both projections of a gated feed-forward block. Host struct, device pointers. */
+typedef struct lora_gated_layer {
+  const void *W_gate, *W_up; /* [F, K] each                                                   */
+  const void *b_gate, *b_up; /* [F] each, or NULL                                             */
+  const void *A_gate, *B_gate, *A_up, *B_up; /* [rank, K] and [F, rank], or both NULL: no adapter */
+  int32_t rank_gate, rank_up;
+  double alpha_gate, alpha_up;
+} lora_gated_layer;
+
+/*
+ * lora_gated_fwd -- h = act(g) . u in one GEMM, with
+ *
+ *     g = x.W_gate^T + b_gate + s_gate . (x.A_gate^T).B_gate^T,  u likewise with the up projection
+ *
+ * s = (alpha / rank) . strength . request_scale. g and u stay in fp32 and h is
+ * rounded once.
+ *   h       [T, F], row stride ldh >= F
+ *   saved   NULL, or device memory of lora_gated_saved_size() bytes, 16-byte aligned, that
+ *           the call fills for lora_gated_bwd (g and u in fp32; its layout is the library's own)
+ *
+ * lora_gated_bwd -- for an output gradient dh:
+ *
+ *     dg = RN_bf16(dh . u . act'(g)),  du = RN_bf16(dh . act(g)),  v = s . d.B of each,
+ *     dx = dg.W_gate + du.W_up + v_gate.A_gate + v_up.A_up,  dA = v^T.x,  dB = d^T.(s x.A^T)
+ *
+ *   saved   as a forward call with the same x, layer and scales filled it, or NULL: the
+ *           forward GEMM runs once more (and the workspace holds what it keeps)
+ *   dx, dA_*, dB_*  each optional (NULL = not computed)
+ * dg and du are rounded to bf16 for the products that follow: the gradients are off by
+ * those roundings whatever grad_dtype is.
+ */
+int lora_gated_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* layer, int64_t F,
+                   int32_t act, double strength, double request_scale, void* h, int64_t ldh, void* saved,
+                   void* workspace, size_t workspace_bytes, void* stream);
+int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* layer, int64_t F,
+                   int32_t act, double strength, double request_scale, const void* dh, int64_t lddh,
+                   const void* saved, void* dx, int64_t lddx, void* dA_gate, void* dB_gate, void* dA_up, void* dB_up,
+                   int32_t grad_dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of the forward's workspace, of `saved`, and of the backward's workspace (which covers the
+ * forward's); ranks 0 for no adapter. */
+size_t lora_gated_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up);
+size_t lora_gated_saved_size(int64_t T, int64_t F, int32_t rank_gate, int32_t rank_up);
+size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up);
+
+/*
  * Workspace bytes a call with T tokens, K inputs and N outputs needs for
  * adapters of the given ranks (`ranks` is a HOST array of n_ranks entries: one
  * for lora_linear_fwd and lora_linear_nf4_fwd, one per group for

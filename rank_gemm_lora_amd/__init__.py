@@ -39,6 +39,10 @@ __all__ = [
     "LoraGroup", "hip_runtimes_mapped",
     "LoraPool", "lora_linear_routed_fwd", "lora_linear_routed_workspace_size", "lora_linear_routed_bwd",
     "lora_linear_routed_bwd_workspace_size", "lora_linear_routed", "lora_linear_routed_backward",
+    "LoraGatedLayer", "LORA_ACT_SILU", "LORA_ACT_GELU", "LORA_ACT_GELU_TANH", "lora_gated_fwd", "lora_gated_bwd",
+    "lora_gated_workspace_size", "lora_gated_saved_size", "lora_gated_bwd_workspace_size", "lora_gated",
+    "lora_gated_backward", "lora_linear_dropout_fwd", "lora_linear_dropout_bwd", "lora_linear_dropout_workspace_size",
+    "lora_linear_dropout_bwd_workspace_size", "lora_linear_dropout", "lora_linear_dropout_backward",
     "LoraAdamWTensor", "LoraAdamWPlan", "lora_adamw_table_size", "lora_adamw_plan", "lora_adamw_step", "LoraAdamW",
 ]
 
@@ -50,6 +54,8 @@ LORA_PATCH_ADD, LORA_PATCH_REPLACE = 0, 1
 LORA_NF4_AUTO, LORA_NF4_PANEL, LORA_NF4_IN_GEMM = 0, 1, 2
 _DEQUANT = {"auto": LORA_NF4_AUTO, "panel": LORA_NF4_PANEL, "in_gemm": LORA_NF4_IN_GEMM}
 _QUALITY = {"lossless": LORA_LOSSLESS, "exact": LORA_EXACT}
+LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = 0, 1, 2
+_ACT = {"silu": LORA_ACT_SILU, "gelu": LORA_ACT_GELU, "gelu_tanh": LORA_ACT_GELU_TANH}
 _MODE = {"add": LORA_PATCH_ADD, "replace": LORA_PATCH_REPLACE}
 
 if not os.path.exists(LIB_PATH):
@@ -58,6 +64,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 _p, _i64, _i32, _f64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double, ctypes.c_size_t
+_u64 = ctypes.c_uint64
 
 
 class LoraGroup(ctypes.Structure):
@@ -76,6 +83,13 @@ class LoraPool(ctypes.Structure):
     """C ``lora_pool``: the adapters from which the tokens of a routed call take theirs."""
     _fields_ = [("A", _p), ("B", _p), ("scales", _p), ("ranks", _p), ("n_adapters", _i32), ("rank", _i32),
                 ("reserved", _i64)]
+
+
+class LoraGatedLayer(ctypes.Structure):
+    """C ``lora_gated_layer``: both projections of a gated feed-forward block."""
+    _fields_ = [("W_gate", _p), ("W_up", _p), ("b_gate", _p), ("b_up", _p), ("A_gate", _p), ("B_gate", _p),
+                ("A_up", _p), ("B_up", _p), ("rank_gate", _i32), ("rank_up", _i32), ("alpha_gate", _f64),
+                ("alpha_up", _f64)]
 
 
 class LoraAdamWTensor(ctypes.Structure):
@@ -136,6 +150,23 @@ _lib.lora_linear_routed_bwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, ctypes.P
 _lib.lora_linear_routed_bwd.restype = ctypes.c_int
 _lib.lora_linear_routed_bwd_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
 _lib.lora_linear_routed_bwd_workspace_size.restype = _sz
+_lib.lora_linear_dropout_fwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _i32, _f64, _f64, _f64, _f64, _u64,
+                                         _u64, _p, _p, _i64, _p, _sz, _p]
+_lib.lora_linear_dropout_fwd.restype = ctypes.c_int
+_lib.lora_linear_dropout_bwd.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p, _i32, _f64, _f64, _f64, _f64, _u64, _u64,
+                                         _p, _p, _i64, _p, _i64, _p, _p, _i32, _p, _sz, _p]
+_lib.lora_linear_dropout_bwd.restype = ctypes.c_int
+_lib.lora_gated_fwd.argtypes = [_p, _i64, _i64, _i64, ctypes.POINTER(LoraGatedLayer), _i64, _i32, _f64, _f64, _p, _i64,
+                                _p, _p, _sz, _p]
+_lib.lora_gated_fwd.restype = ctypes.c_int
+_lib.lora_gated_bwd.argtypes = [_p, _i64, _i64, _i64, ctypes.POINTER(LoraGatedLayer), _i64, _i32, _f64, _f64, _p, _i64,
+                                _p, _p, _i64, _p, _p, _p, _p, _i32, _p, _sz, _p]
+_lib.lora_gated_bwd.restype = ctypes.c_int
+for _f in (_lib.lora_linear_dropout_workspace_size, _lib.lora_linear_dropout_bwd_workspace_size):
+    _f.argtypes, _f.restype = [_i64, _i64, _i64, _i32], _sz
+for _f in (_lib.lora_gated_workspace_size, _lib.lora_gated_bwd_workspace_size):
+    _f.argtypes, _f.restype = [_i64, _i64, _i64, _i32, _i32], _sz
+_lib.lora_gated_saved_size.argtypes, _lib.lora_gated_saved_size.restype = [_i64, _i64, _i32, _i32], _sz
 _lib.lora_adamw_table_size.argtypes = [ctypes.POINTER(LoraAdamWTensor), _i32]
 _lib.lora_adamw_table_size.restype = _sz
 _lib.lora_adamw_plan.argtypes = [ctypes.POINTER(LoraAdamWTensor), _i32, _i32, _i32, _i32, _p, _sz,
@@ -234,6 +265,53 @@ def lora_linear_routed_bwd(x, T, K, ldx, W, N, pool, token_adapter, token_scale,
 
 def lora_linear_routed_bwd_workspace_size(T, K, N, n_adapters, rank, want_dx=True) -> int:
     return int(_lib.lora_linear_routed_bwd_workspace_size(T, K, N, n_adapters, rank, 1 if want_dx else 0))
+
+
+def lora_linear_dropout_fwd(x, T, K, ldx, W, N, bias, A, B, rank, alpha, strength, request_scale, p, seed, offset, rng, y,
+                            ldy, workspace, workspace_bytes, stream):
+    return _check(_lib.lora_linear_dropout_fwd(x, T, K, ldx, W, N, bias, A, B, rank, alpha, strength, request_scale, p,
+                                               seed, offset, rng, y, ldy, workspace, workspace_bytes, stream),
+                  "lora_linear_dropout_fwd")
+
+
+def lora_linear_dropout_bwd(x, T, K, ldx, W, N, A, B, rank, alpha, strength, request_scale, p, seed, offset, rng, dy,
+                            lddy, dx, lddx, dA, dB, grad_dtype, workspace, workspace_bytes, stream):
+    return _check(_lib.lora_linear_dropout_bwd(x, T, K, ldx, W, N, A, B, rank, alpha, strength, request_scale, p, seed,
+                                               offset, rng, dy, lddy, dx, lddx, dA, dB, grad_dtype, workspace,
+                                               workspace_bytes, stream), "lora_linear_dropout_bwd")
+
+
+def lora_linear_dropout_workspace_size(T, K, N, rank) -> int:
+    return int(_lib.lora_linear_dropout_workspace_size(T, K, N, rank))
+
+
+def lora_linear_dropout_bwd_workspace_size(T, K, N, rank) -> int:
+    return int(_lib.lora_linear_dropout_bwd_workspace_size(T, K, N, rank))
+
+
+def lora_gated_fwd(x, T, K, ldx, layer, F, act, strength, request_scale, h, ldh, saved, workspace, workspace_bytes,
+                   stream):
+    return _check(_lib.lora_gated_fwd(x, T, K, ldx, ctypes.byref(layer), F, act, strength, request_scale, h, ldh, saved,
+                                      workspace, workspace_bytes, stream), "lora_gated_fwd")
+
+
+def lora_gated_bwd(x, T, K, ldx, layer, F, act, strength, request_scale, dh, lddh, saved, dx, lddx, dA_gate, dB_gate,
+                   dA_up, dB_up, grad_dtype, workspace, workspace_bytes, stream):
+    return _check(_lib.lora_gated_bwd(x, T, K, ldx, ctypes.byref(layer), F, act, strength, request_scale, dh, lddh, saved,
+                                      dx, lddx, dA_gate, dB_gate, dA_up, dB_up, grad_dtype, workspace, workspace_bytes,
+                                      stream), "lora_gated_bwd")
+
+
+def lora_gated_workspace_size(T, K, F, rank_gate, rank_up) -> int:
+    return int(_lib.lora_gated_workspace_size(T, K, F, rank_gate, rank_up))
+
+
+def lora_gated_saved_size(T, F, rank_gate, rank_up) -> int:
+    return int(_lib.lora_gated_saved_size(T, F, rank_gate, rank_up))
+
+
+def lora_gated_bwd_workspace_size(T, K, F, rank_gate, rank_up) -> int:
+    return int(_lib.lora_gated_bwd_workspace_size(T, K, F, rank_gate, rank_up))
 
 
 def lora_adamw_table_size(tensors) -> int:
@@ -607,6 +685,173 @@ def lora_linear_routed_backward(x, W, A, B, dy, scales, token_adapter, token_sca
                                _ptr(token_scale), dy.data_ptr(), lddy, _ptr(dx), lddx, _ptr(dA), _ptr(dB),
                                ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev, stream))
     return dx, dA, dB
+
+
+def _dropout_args(x, W, A, B, rng):
+    dev, bf = x.device, torch.bfloat16
+    if x.dim() != 2 or A.dim() != 2 or B.dim() != 2:
+        raise ValueError("x must be [T, K], A [rank, K] and B [N, rank]")
+    T, K = x.shape
+    R, N = A.shape[0], B.shape[0]
+    _of(A, "A", (R, K), bf, dev)
+    _of(B, "B", (N, R), bf, dev)
+    _of(W, "W", (N, K), bf, dev)
+    if rng is not None and (rng.dtype not in (torch.int64, torch.uint64) or rng.shape != (2,) or rng.device != dev
+                            or not rng.is_contiguous()):
+        raise ValueError(f"rng must hold two 64-bit integers (seed, offset) on {dev}")
+    return T, K, N, R
+
+
+_U64 = 2 ** 64 - 1
+
+
+def lora_linear_dropout(x, W, b, A, B, alpha, p, seed, offset=0, strength=1.0, request_scale=1.0, rng=None, out=None,
+                        workspace=None, stream=None):
+    """y = x.W^T + b + s.(D(x).A^T).B^T with dropout D in front of the adapter (bf16; returns ``out``).
+
+    What is kept is a function of (seed, offset, element): ``lora_linear_dropout_backward`` with the same two forms it
+    again. Another step or layer takes another offset. ``rng``: optional int64 device tensor (seed, offset) that the
+    kernels read in place of the two numbers, for captured calls."""
+    T, K, N, R = _dropout_args(x, W, A, B, rng)
+    dev = x.device
+    ldx = _rows(x, "x", (T, K), dev)
+    if b is not None:
+        _of(b, "b", (N,), torch.bfloat16, dev)
+    with _on(dev, stream):
+        if out is None:
+            out, ldy = torch.empty((T, N), dtype=torch.bfloat16, device=dev), N
+        else:
+            ldy = _rows(out, "out", (T, N), dev)
+        ws = _bytes_on(workspace, _lib.lora_linear_dropout_workspace_size, (T, K, N, R), dev)
+        lora_linear_dropout_fwd(x.data_ptr(), T, K, ldx, W.data_ptr(), N, _ptr(b), A.data_ptr(), B.data_ptr(), R,
+                                float(alpha), float(strength), float(request_scale), float(p), int(seed) & _U64,
+                                int(offset) & _U64, _ptr(rng), out.data_ptr(), ldy, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    return out
+
+
+def _grad(t, name, shape, dtype, device, wanted):
+    if not wanted:
+        return None
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _of(t, name, shape, dtype, device)
+
+
+def lora_linear_dropout_backward(x, W, A, B, dy, alpha, p, seed, offset=0, strength=1.0, request_scale=1.0, rng=None,
+                                 want=("dx", "dA", "dB"), dx=None, dA=None, dB=None, grad_dtype=torch.float32,
+                                 workspace=None, stream=None):
+    """Gradients of ``lora_linear_dropout`` for the output gradient ``dy``: returns (dx, dA, dB), each None unless named
+    in ``want`` (dx bf16; dA and dB in ``grad_dtype``, fp32 or bf16, into the given tensors when there are any)."""
+    T, K, N, R = _dropout_args(x, W, A, B, rng)
+    dev = x.device
+    ldx, lddy = _rows(x, "x", (T, K), dev), _rows(dy, "dy", (T, N), dev)
+    with _on(dev, stream):
+        if "dx" not in want:
+            dx = None
+        elif dx is None:
+            dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        lddx = _rows(dx, "dx", (T, K), dev) if dx is not None else K
+        dA = _grad(dA, "dA", (R, K), grad_dtype, dev, "dA" in want)
+        dB = _grad(dB, "dB", (N, R), grad_dtype, dev, "dB" in want)
+        ws = _bytes_on(workspace, _lib.lora_linear_dropout_bwd_workspace_size, (T, K, N, R), dev)
+        lora_linear_dropout_bwd(x.data_ptr(), T, K, ldx, _ptr(W), N, A.data_ptr(), B.data_ptr(), R, float(alpha),
+                                float(strength), float(request_scale), float(p), int(seed) & _U64, int(offset) & _U64,
+                                _ptr(rng), dy.data_ptr(), lddy, _ptr(dx), lddx, _ptr(dA), _ptr(dB), _GRAD[grad_dtype],
+                                ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev, stream))
+    return dx, dA, dB
+
+
+_GRAD = {torch.float32: LORA_F32, torch.bfloat16: LORA_BF16}
+
+
+def _gated_args(x, W_gate, W_up, gate, up, b_gate, b_up):
+    """Checks shared by the gated calls; returns T, K, F and the C layer."""
+    dev, bf = x.device, torch.bfloat16
+    if x.dim() != 2 or W_gate.dim() != 2:
+        raise ValueError("x must be [T, K] and the weights [F, K]")
+    T, K = x.shape
+    F = W_gate.shape[0]
+    _of(W_gate, "W_gate", (F, K), bf, dev)
+    _of(W_up, "W_up", (F, K), bf, dev)
+    if b_gate is not None:
+        _of(b_gate, "b_gate", (F,), bf, dev)
+    if b_up is not None:
+        _of(b_up, "b_up", (F,), bf, dev)
+    sides = []
+    for name, a in (("gate", gate), ("up", up)):
+        if a is None:
+            sides.append((None, None, 0, 0.0))
+            continue
+        A, B = a["A"], a["B"]
+        R = A.shape[0]
+        _of(A, f"{name}['A']", (R, K), bf, dev)
+        _of(B, f"{name}['B']", (F, R), bf, dev)
+        sides.append((A.data_ptr(), B.data_ptr(), R, float(a["alpha"])))
+    (ag, bg, rg, alg), (au, bu, ru, alu) = sides
+    return T, K, F, LoraGatedLayer(W_gate.data_ptr(), W_up.data_ptr(), _ptr(b_gate), _ptr(b_up), ag, bg, au, bu, rg, ru,
+                                   alg, alu)
+
+
+def lora_gated(x, W_gate, W_up, gate=None, up=None, b_gate=None, b_up=None, act="silu", strength=1.0, request_scale=1.0,
+               out=None, save=False, saved=None, workspace=None, stream=None):
+    """h = act(x.W_gate^T + b_gate + its adapter) . (x.W_up^T + b_up + its adapter), bf16, in one GEMM.
+
+    ``gate`` and ``up``: dicts with A [rank, K], B [F, rank] and alpha, or None; ``act``: "silu", "gelu" or
+    "gelu_tanh". Returns ``out``, or with ``save`` (out, saved): what ``lora_gated_backward`` then need not compute
+    again (``saved``: uint8 tensor of ``lora_gated_saved_size`` bytes to fill)."""
+    T, K, F, layer = _gated_args(x, W_gate, W_up, gate, up, b_gate, b_up)
+    dev = x.device
+    ldx = _rows(x, "x", (T, K), dev)
+    with _on(dev, stream):
+        if out is None:
+            out, ldh = torch.empty((T, F), dtype=torch.bfloat16, device=dev), F
+        else:
+            ldh = _rows(out, "out", (T, F), dev)
+        ws = _bytes_on(workspace, _lib.lora_gated_workspace_size, (T, K, F, layer.rank_gate, layer.rank_up), dev)
+        if save or saved is not None:
+            need = lora_gated_saved_size(T, F, layer.rank_gate, layer.rank_up)
+            if saved is None:
+                saved = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            _saved_of(saved, need, dev)
+        lora_gated_fwd(x.data_ptr(), T, K, ldx, layer, F, _ACT[act], float(strength), float(request_scale),
+                       out.data_ptr(), ldh, _ptr(saved), ws.data_ptr(), ws.numel() * ws.element_size(),
+                       _stream_on(dev, stream))
+    return out if saved is None else (out, saved)
+
+
+def _saved_of(saved, need, device):
+    if saved.dtype != torch.uint8 or saved.device != device or not saved.is_contiguous() or saved.numel() < need:
+        raise ValueError(f"saved must be a contiguous uint8 tensor of at least {need} bytes on {device}")
+
+
+def lora_gated_backward(x, W_gate, W_up, gate, up, dh, b_gate=None, b_up=None, act="silu", strength=1.0,
+                        request_scale=1.0, saved=None, want=("dx", "dA", "dB"), dx=None, dA_gate=None, dB_gate=None,
+                        dA_up=None, dB_up=None, grad_dtype=torch.float32, workspace=None, stream=None):
+    """Gradients of ``lora_gated`` for the output gradient ``dh``: (dx, dA_gate, dB_gate, dA_up, dB_up), each None unless
+    named in ``want`` ("dA" and "dB" name both projections') and its adapter is there. ``saved``: what the forward call
+    returned, or None to run its GEMM again."""
+    T, K, F, layer = _gated_args(x, W_gate, W_up, gate, up, b_gate, b_up)
+    dev = x.device
+    ldx, lddh = _rows(x, "x", (T, K), dev), _rows(dh, "dh", (T, F), dev)
+    rg, ru = layer.rank_gate, layer.rank_up
+    if saved is not None:
+        _saved_of(saved, lora_gated_saved_size(T, F, rg, ru), dev)
+    with _on(dev, stream):
+        if "dx" not in want:
+            dx = None
+        elif dx is None:
+            dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        lddx = _rows(dx, "dx", (T, K), dev) if dx is not None else K
+        a, b = "dA" in want, "dB" in want
+        dA_gate = _grad(dA_gate, "dA_gate", (rg, K), grad_dtype, dev, a and gate is not None)
+        dB_gate = _grad(dB_gate, "dB_gate", (F, rg), grad_dtype, dev, b and gate is not None)
+        dA_up = _grad(dA_up, "dA_up", (ru, K), grad_dtype, dev, a and up is not None)
+        dB_up = _grad(dB_up, "dB_up", (F, ru), grad_dtype, dev, b and up is not None)
+        ws = _bytes_on(workspace, _lib.lora_gated_bwd_workspace_size, (T, K, F, rg, ru), dev)
+        lora_gated_bwd(x.data_ptr(), T, K, ldx, layer, F, _ACT[act], float(strength), float(request_scale),
+                       dh.data_ptr(), lddh, _ptr(saved), _ptr(dx), lddx, _ptr(dA_gate), _ptr(dB_gate), _ptr(dA_up),
+                       _ptr(dB_up), _GRAD[grad_dtype], ws.data_ptr(), ws.numel() * ws.element_size(),
+                       _stream_on(dev, stream))
+    return dx, dA_gate, dB_gate, dA_up, dB_up
 
 
 class LoraAdamW:

@@ -34,6 +34,8 @@ SOURCES = {
     "patch.hip": ["-ffp-contract=off"],
     "probe.hip": [],
     "noalloc.hip": [],
+    "step.hip": [],
+    "step_api.cpp": [],
     "routed.hip": [],
     "routed_api.cpp": [],
     "adamw.hip": ["-ffp-contract=off"],

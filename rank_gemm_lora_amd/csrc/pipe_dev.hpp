@@ -287,10 +287,16 @@ __device__ __forceinline__ u32x4 unswap_halves(u32x4 v, int sw) {
   return sw ? u32x4{v[2], v[3], v[0], v[1]} : v;
 }
 
-// One pipelined K loop over NS stages for config P; issue(s) fills ring slot s % S.
-template <class P, class Issue>
+struct NoTouch {
+  template <class F>
+  __device__ __forceinline__ void operator()(F&, int, int) const {}
+};
+
+// One pipelined K loop over NS stages for config P; issue(s) fills ring slot s % S. touch(f, s, kk) may change the
+// fragments of k-step kk of stage s before they are multiplied.
+template <class P, class Issue, class Touch = NoTouch>
 __device__ __forceinline__ void pipe_loop(f32x16 (&acc)[P::NI][P::NJ], char* smem, int NS, Issue&& issue,
-                                          int wn0, int wm0, int lane) {
+                                          int wn0, int wm0, int lane, Touch touch = Touch{}) {
 #pragma unroll
   for (int i = 0; i < P::NI; ++i)
 #pragma unroll
@@ -315,6 +321,7 @@ __device__ __forceinline__ void pipe_loop(f32x16 (&acc)[P::NI][P::NJ], char* sme
         if (steady) issue(j + P::S);
         load_frags<P>(fr[(kk + 1) & 1], smem + ((j + 1) % P::S) * P::STAGE_BYTES, 0, wn0, wm0, lane);
       }
+      touch(fr[kk & 1], j, kk);
       mfma_frags<P>(acc, fr[kk & 1]);
       interleave_reads_with_mfma<P>();
     }
@@ -326,6 +333,7 @@ __device__ __forceinline__ void pipe_loop(f32x16 (&acc)[P::NI][P::NJ], char* sme
 #pragma unroll
   for (int kk = 0; kk < P::KK; ++kk) {
     if (kk + 1 < P::KK) load_frags<P>(fr[(kk + 1) & 1], st, kk + 1, wn0, wm0, lane);
+    touch(fr[kk & 1], NS - 1, kk);
     mfma_frags<P>(acc, fr[kk & 1]);
   }
 }

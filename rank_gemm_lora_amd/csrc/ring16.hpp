@@ -1,0 +1,255 @@
+// The 16 x 16 x 32 MFMA ring of the hot GEMM (five LDS slots, x and W units of 64 contraction indices, copies and
+// fragment reads spread over the MFMA bundles) as a loop over stages whose operands an `Op` names, for the kernels of a
+// training step: their operands come from several places (gate and up weights, adapters behind a base weight) and
+// their epilogues differ.
+//
+// acc[i][j] += W-side block i . x-side block j over NS stages. x units are always rows of tokens, contiguous along the
+// contraction. W units come in two forms:
+//   NT  rows of outputs, contiguous along the contraction (a weight as the forward reads it)
+//   NN  rows of the contraction, contiguous along the outputs (the same weight as its input gradient reads it): staged
+//       as [64 k][BN] and read with the transposing LDS read, so no transposed copy of the weight is made.
+//       (The hot backward's copy of W^T costs a read and a write of the weight in every call.)
+//
+// An Op has
+//   void seek(int s)               makes the copies below those of stage s (called in ascending order from 0; stages past
+//                                  the last must read as zeros: they are copied all the same, so that the loop has one
+//                                  form and its wait counts are constant)
+//   void load_x(int l, char* dst)  copy instruction l of NL of the x unit, and of the W unit
+//   void load_w(int l, char* dst)
+//   void before(int t, acc)        runs before the MFMAs of stage t
+#pragma once
+
+#include "pipe_dev.hpp"
+
+namespace lora {
+namespace {
+namespace pipe {
+
+// 256 x 256 tiles, one workgroup on a compute unit, and 128 x 128 tiles, two (as the hot GEMM's).
+using Ring256 = QCfg<256, 256, 128, 128, 128, 5>;
+using Ring128 = QCfg<128, 128, 64, 64, 128, 5, 2>;
+
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// A row or a chunk that does not exist gets this added to its offset: past every resource (at most 2^30 bytes: 256
+// rows of 4 MB), and a missing row and a missing chunk together do not wrap around.
+constexpr uint32_t kMissing = 0x40000000u;
+
+template <class P>
+constexpr int ring_loads() { return P::BM * P::CPR / 64 / P::WAVES; }
+
+__device__ __forceinline__ int ring_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+template <class P>
+__device__ __forceinline__ void ring_copy(int l, char* dst, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+  const int slot0 = (l * P::WAVES + ring_wave()) * 64;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + slot0 * 16), 16, off, 0, 0, 0);
+}
+
+// This lane's 16-byte chunk of a 128-byte row, in bytes (the same in every copy instruction of a unit).
+template <class P>
+__device__ __forceinline__ uint32_t ring_chunk() {
+  const int lane = threadIdx.x & 63;
+  return static_cast<uint32_t>(((lane & 7) ^ (((ring_wave() * 8 + (lane >> 3)) >> 1) & 7)) * 16);
+}
+
+// Per-lane offsets of a unit whose tile row R is source row R (rows from `valid` on are missing).
+template <class P>
+struct NtRows {
+  static constexpr int N = ring_loads<P>();
+  uint32_t v[N];
+  __device__ __forceinline__ void init(uint32_t ld_bytes, int valid) {
+    const int lane = opaque_int(threadIdx.x & 63);
+    const int r0 = ring_wave() * 8 + (lane >> 3);
+    const uint32_t c = ring_chunk<P>();
+#pragma unroll
+    for (int l = 0; l < N; ++l) {
+      const int row = l * P::WAVES * 8 + r0;
+      v[l] = row < valid ? static_cast<uint32_t>(row) * ld_bytes + c : kMissing;
+    }
+  }
+};
+
+// Per-lane offsets of an NN unit: tile row k is source row k of the stage (the resource ends behind its last row), and
+// 32-byte granule g of it sits at g ^ f(k), f(k) = (k & 3) | (k >> 3 & 1) << 2: the eight rows that half a wave's
+// transposing read touches then lie in eight different granules of the 256 bytes of the banks.
+template <class P>
+struct NnRows {
+  static constexpr int N = ring_loads<P>();
+  static constexpr int LPR = P::BN * 2 / 16;  // lanes (16-byte pieces) per row
+  uint32_t v[N];
+  int row[N];
+  __device__ __forceinline__ void init(uint32_t ld_bytes, int cols_valid) {
+    const int lane = opaque_int(threadIdx.x & 63);
+#pragma unroll
+    for (int l = 0; l < N; ++l) {
+      const int sl = (l * P::WAVES + ring_wave()) * 64 + lane;
+      const int k = sl / LPR, p = sl % LPR;
+      const int f = (k & 3) | (((k >> 3) & 1) << 2);
+      const int col = (((p >> 1) ^ f) * 2 + (p & 1)) * 8;
+      row[l] = k;
+      v[l] = col < cols_valid ? static_cast<uint32_t>(k) * ld_bytes + static_cast<uint32_t>(col) * 2 : kMissing;
+    }
+  }
+};
+
+template <class P, bool NN>
+struct RingFrags {
+  uint32_t x, w;  // byte offsets of this lane's first fragment in an x / a W unit
+  __device__ __forceinline__ void init(int wm0, int wn0) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const FragOffsets o = frag_offsets<P>(wn0, wm0, lane);
+    x = o.x;
+    if (NN) {
+      // a transposing read gives lane (r, q) rows 8 q .. + 3 of column r where it names row 8 q + r / 4, columns 4 (r % 4)
+      const int f = (r >> 2) | ((q & 1) << 2);
+      w = static_cast<uint32_t>((8 * q + (r >> 2)) * P::BN * 2 + (((wn0 / 16) ^ f) * 32) + (r & 3) * 8);
+    } else {
+      w = o.w;
+    }
+  }
+  __device__ __forceinline__ bf16x8 read_x(const char* xs, int j, int kk) const {
+    return *(const bf16x8*)(xs + (x ^ (kk ? 64u : 0u)) + j * 2048);
+  }
+  __device__ __forceinline__ bf16x8 read_w(const char* ws, int i, int kk) const {
+    if constexpr (!NN) return *(const bf16x8*)(ws + (w ^ (kk ? 64u : 0u)) + i * 2048);
+    else {
+      const char* at = ws + (w ^ static_cast<uint32_t>(i << 5)) + kk * 32 * P::BN * 2;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * P::BN * 2));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// The loop. Behind it the LDS is free (every copy has landed, every wave has read its last fragments).
+// (Schedule as the hot GEMM's: x of stage t + 2 is copied beside k-step 0, W beside k-step 1, into the slots that the
+// barriers of stages t - 1 and t release; the wait of stage t leaves the x copies of stage t + 2 in flight.)
+template <class P, bool NN, class Op>
+__device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int NS, char* smem, int wm0, int wn0) {
+  static_assert(P::WAVES == 4, "schedule written for 4 waves");
+  constexpr int NL = ring_loads<P>(), NB = P::NI * P::NJ, RS = NB / (P::NI + P::NJ), LS = NB / NL;
+  static_assert(NB % (P::NI + P::NJ) == 0 && NB % NL == 0 && LS % 2 == 0 && RS >= 2, "bundle schedule");
+#pragma unroll
+  for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < P::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    op.seek(s);
+#pragma unroll
+    for (int l = 0; l < NL; ++l) op.load_x(l, smem + 2 * s * P::SLOT_BYTES);
+#pragma unroll
+    for (int l = 0; l < NL; ++l) op.load_w(l, smem + (2 * s + 1) * P::SLOT_BYTES);
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * NL));  // stage 0 landed
+  stage_barrier();
+  RingFrags<P, NN> rf;
+  rf.init(wm0, wn0);
+  Frags16<P> fr[2];
+  // fragment f of a k-step, in order of first use: a0, b0 .. b(NJ-1), a1 .. a(NI-1)
+  auto read_frag = [&](Frags16<P>& d, int f, const char* xs, const char* ws, int kk) {
+    if (f == 0 || f > P::NJ) {
+      const int ia = f == 0 ? 0 : f - P::NJ;
+      d.a[ia] = rf.read_w(ws, ia, kk);
+    } else {
+      d.b[f - 1] = rf.read_x(xs, f - 1, kk);
+    }
+  };
+#pragma unroll
+  for (int f = 0; f < P::NI + P::NJ; ++f) read_frag(fr[0], f, smem, smem + P::SLOT_BYTES, 0);
+  int a = 0;  // slot of x of stage t
+  for (int t = 0; t < NS; ++t) {
+    op.before(t, acc);
+    op.seek(t + 2);
+    const int b1 = a == 4 ? 0 : a + 1;      // W of stage t
+    const int a2 = a >= 3 ? a - 3 : a + 2;  // x of stage t + 1
+    const int b2 = a2 == 4 ? 0 : a2 + 1;    // W of stage t + 1
+    const int a3 = b2 == 4 ? 0 : b2 + 1;    // x of stage t + 2
+    const char* xs = smem + a * P::SLOT_BYTES;
+    const char* ws = smem + b1 * P::SLOT_BYTES;
+    const char* xs2 = smem + a2 * P::SLOT_BYTES;
+    const char* ws2 = smem + b2 * P::SLOT_BYTES;
+    char* const xdst = smem + a3 * P::SLOT_BYTES;
+    char* const wdst = smem + a * P::SLOT_BYTES;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < NB; ++m) {
+      const int i = m / P::NJ, j = m % P::NJ;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[0].a[i], fr[0].b[j], acc[i][j], 0, 0, 0);
+      if (m % RS == 0) read_frag(fr[1], m / RS, xs, ws, 1);
+      if (m % LS == LS / 2) op.load_x(m / LS, xdst);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int m = 0; m < NB; ++m) {
+      const int i = m / P::NJ, j = m % P::NJ;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[1].a[i], fr[1].b[j], acc[i][j], 0, 0, 0);
+      if (m == 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL));
+        stage_barrier();  // stage t + 1 landed and visible; every wave is done reading stage t
+      } else if (m % RS == 1) {
+        read_frag(fr[0], m / RS, xs2, ws2, 0);
+      }
+      if (m % LS == LS / 2) op.load_w(m / LS, wdst);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    a = a2;
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  __syncthreads();
+}
+
+// The tile of this workgroup: m-tiles in groups of GROUP_M over all n-tiles, a run of them to each XCD.
+struct RingTile {
+  int m, n;
+  __device__ __forceinline__ RingTile(int pid, int mt, int nt, int group) {
+    const int L = xcd_remap(pid, mt * nt);
+    const int gsize = group * nt;
+    const int grp = L / gsize, first = grp * group;
+    const int gm = min(group, mt - first), within = L - grp * gsize;
+    m = first + within % gm;
+    n = within / gm;
+  }
+};
+
+// bf16 outputs of a wave's block through LDS: `put` 4 consecutive columns of a row, then `store` the block as whole
+// rows of 16-byte pieces. COLS columns, 16-byte chunks XOR-swizzled by row.
+template <int ROWS, int COLS>
+struct BlockOut {
+  static constexpr int RBY = COLS * 2, CH = RBY / 16, RPL = 256 / RBY > 0 ? 256 / RBY : 1;
+  char* st;  // ROWS * RBY bytes of this wave's own
+  __device__ __forceinline__ static int at(int row, int chunk) {
+    return row * RBY + ((chunk ^ ((row / RPL) & (CH - 1))) * 16);
+  }
+  __device__ __forceinline__ void put(int row, int col, uint32_t lo, uint32_t hi) const {
+    *reinterpret_cast<uint2*>(st + at(row, col >> 3) + (col & 4) * 2) = uint2{lo, hi};
+  }
+  // rows [0, rows) and columns [0, cols) of the block exist; y is its first element
+  __device__ __forceinline__ void store(bf16_bits* y, int64_t ldy, int rows, int cols) const {
+    const int lane = threadIdx.x & 63, c = lane % CH, r0 = lane / CH;
+    const bool wide = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0 && cols >= COLS;
+#pragma unroll 4
+    for (int it = 0; it < ROWS * CH / 64; ++it) {
+      const int row = it * (64 / CH) + r0;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(st + at(row, c));
+      if (row >= rows) continue;
+      bf16_bits* dst = y + row * ldy + c * 8;
+      if (wide) {
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c * 8 + e < cols) dst[e] = static_cast<bf16_bits>(v[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  }
+};
+
+}  // namespace pipe
+}  // namespace
+}  // namespace lora

@@ -1,0 +1,855 @@
+// Kernels of a fine-tuning step, bf16: the linear layer with dropout before its adapter, and the gated half of a
+// feed-forward block whose two projections carry adapters, forward and backward, the base weights frozen.
+//
+//   dropout   t = s x' A^T, x' = x . keep                      rank_nt_kernel (the mask formed on its x fragments)
+//             y = x W^T + b + t B^T                            ring_kernel NT, t as extension stages
+//             u = s dy B                                       rank_nn_kernel
+//             dx = dy W + keep . (u A)                         ring_kernel NN, the mask between extension and base stages
+//             dA = u^T x', dB = dy^T t                         contract_kernel (the mask on the staged x)
+//   gated     h = act(x Wg^T + bg + tg Bg^T) . (x Wu^T + bu + tu Bu^T)      gated_kernel: one GEMM, one rounding
+//             dg = dh u act'(g), du = dh act(g)                gated_grad_kernel, from g and u as the forward kept them
+//             v = s d B, dx = dg Wg + du Wu + vg Ag + vu Au, dA = v^T x, dB = d^T t        as above
+//
+// Rank-wide rows are two bf16 terms (step.hpp); every sum is fp32.
+#include "common.hpp"
+#include "dropout_dev.hpp"
+#include "launch.hpp"
+#include "ring16.hpp"
+#include "step.hpp"
+
+namespace lora {
+namespace {
+using namespace pipe;
+
+// ---------------------------------------------------------------------------
+// Rank-wide product over rows contiguous along the contraction (the forward's): 128 tokens and BN adapter rows per
+// workgroup through the LDS ring of the one-adapter producer, K split over grid z; fp32 partial sums. HBM-bound: x is
+// read once (R <= 128).
+using RankNarrow = PCfg<128, 64, 32, 64, 128, 5>;   // up to 64 columns
+using RankWide = PCfg<128, 128, 32, 128, 128, 4>;
+
+template <class P, bool DROP>
+__global__ __launch_bounds__(P::THREADS) void rank_nt_kernel(RankProduct p, int ks) {
+  __shared__ __attribute__((aligned(1024))) char smem[P::S * P::STAGE_BYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm0 = wave * P::WM;
+  const int R = p.rank[0] + p.rank[1], q0 = blockIdx.y * P::BN;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
+  const int rows_m = static_cast<int>(min<int64_t>(P::BM, p.T - m0));
+  const int kb_total = static_cast<int>(p.K * 2), nk = (kb_total + P::RB - 1) / P::RB;
+  const bool k_tail = kb_total % P::RB != 0;
+  const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), lda_b = static_cast<uint32_t>(p.K * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x[0] + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+  const __amdgpu_buffer_rsrc_t ar0 = make_rsrc(p.A[0], static_cast<uint32_t>(p.rank[0]) * lda_b);
+  const __amdgpu_buffer_rsrc_t ar1 = make_rsrc(p.A[1], static_cast<uint32_t>(p.rank[1]) * lda_b);
+  TileOffsets<P, P::BM> ox;
+  ox.init(ldx_b, 0, rows_m, 0);
+  // adapter rows q0 .. : a copy instruction takes 8 of them, all of one adapter (ranks are multiples of 8)
+  constexpr int NA = TileOffsets<P, P::BN>::N;
+  uint32_t va[NA];
+#pragma unroll
+  for (int l = 0; l < NA; ++l) {
+    const int row = (l * P::WAVES + wave) * 8 + (lane >> 3), g = q0 + row;
+    const uint32_t c = static_cast<uint32_t>(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+    va[l] = g < R ? static_cast<uint32_t>(g < p.rank[0] ? g : g - p.rank[0]) * lda_b + c : 0x80000000u;
+  }
+  const int s_lo = static_cast<int>(blockIdx.z) * ks, ns = min(nk, s_lo + ks) - s_lo;
+  auto issue = [&](int s) {
+    char* bx = smem + (s % P::S) * P::STAGE_BYTES;
+    const int kb = (s_lo + s) * P::RB;
+    const bool tail = k_tail && s_lo + s == nk - 1;
+    ox.load(bx, xr, kb, tail, kb_total);
+#pragma unroll
+    for (int l = 0; l < NA; ++l) {
+      const int slot0 = (l * P::WAVES + wave) * 64;
+      uint32_t v = va[l];
+      if (tail) {
+        const int row = (l * P::WAVES + wave) * 8 + (lane >> 3);
+        if (kb + ((lane & 7) ^ ((row >> 1) & 7)) * 16 >= kb_total) v = 0x80000000u;
+      }
+      const bool second = q0 + (l * P::WAVES + wave) * 8 >= p.rank[0];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? ar1 : ar0, (lds_void*)(bx + P::X_BYTES + slot0 * 16), 16, v, kb,
+                                               0, 0);
+    }
+  };
+  f32x16 acc[P::NI][P::NJ];
+  if constexpr (DROP) {
+    // lane (r, h) holds block 2 kk + h (of 8) of the stage of token wm0 + r: one call of the generator
+    Dropper d;
+    d.init(p.drop, p.K);
+    const int64_t row0 = (m0 + wm0 + (lane & 31)) * d.blocks + s_lo * 8 + (lane >> 5);
+    auto touch = [&](Frags<P>& f, int s, int kk) {
+      const u32x4 w = philox7(static_cast<uint64_t>(row0 + s * 8 + kk * 2), d.seed, d.offset);
+      u32x4 v = __builtin_bit_cast(u32x4, f.b[0]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] &= d.mask(w[e]);
+      f.b[0] = __builtin_bit_cast(bf16x8, v);
+    };
+    static_assert(P::NJ == 1, "one token per lane");
+    pipe_loop<P>(acc, smem, ns, issue, 0, wm0, lane, touch);
+  } else {
+    pipe_loop<P>(acc, smem, ns, issue, 0, wm0, lane);
+  }
+  // lane (r, h) holds adapter rows q0 + 32 i + 8 g + 4 h + e of token wm0 + r
+  const int r = lane & 31, h = lane >> 5;
+  const int64_t m = m0 + wm0 + r;
+  if (m >= p.T) return;
+  float* row = p.part + (static_cast<int64_t>(blockIdx.z) * p.T + m) * R;
+#pragma unroll
+  for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int q = q0 + i * 32 + g * 8 + h * 4;
+      if (q < R)
+        *reinterpret_cast<f32x4*>(row + q) =
+            f32x4{acc[i][0][g * 4], acc[i][0][g * 4 + 1], acc[i][0][g * 4 + 2], acc[i][0][g * 4 + 3]};
+    }
+}
+
+// tt = the two terms of scale . sum of the splits, in order; zeros behind them. 4 columns per thread.
+__global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct p, int S) {
+  const int R = p.rank[0] + p.rank[1], ldt = static_cast<int>((2 * R + 63) / 64 * 64), quads = ldt / 4;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (idx >= p.T * quads) return;
+  const int64_t t = idx / quads;
+  const int c = static_cast<int>(idx - t * quads) * 4;
+  uint2 w = {0u, 0u};
+  if (c < 2 * R) {
+    const bool mid = c >= R;
+    const int q = mid ? c - R : c;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < S; ++z) v += *reinterpret_cast<const f32x4*>(p.part + (z * p.T + t) * R + q);
+    v *= q < p.rank[0] ? p.scale[0] : p.scale[1];
+    w = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    if (mid) {
+      // (a sum that overflows has its infinity in the first term: the second is zero there, not inf - inf)
+      float lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t b = e < 2 ? w.x : w.y;
+        const float hi = __uint_as_float(e & 1 ? b & 0xffff0000u : b << 16);
+        lo[e] = __builtin_isfinite(hi) ? v[e] - hi : 0.f;
+      }
+      w = uint2{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+    }
+  }
+  *reinterpret_cast<uint2*>(p.tt + t * ldt + c) = w;
+}
+
+// ---------------------------------------------------------------------------
+// Operands of the ring GEMMs.
+
+// NT: rows of outputs. DUAL: the tile's rows are blocks of 16 gate rows and 16 up rows in turn, so that a lane holds the
+// gate and the up value of the same four outputs in acc[2 i] and acc[2 i + 1]; a copy instruction's 8 rows then belong
+// to one projection, the same for all of a wave's (waves 0 and 1 copy gate rows, 2 and 3 up rows).
+template <class P, bool DUAL>
+struct NtOp {
+  __amdgpu_buffer_rsrc_t xr, wr, xm, tr, wm, br;
+  uint32_t ldx_b, ldw_b, ldt_b, ldb_b, ax, aw, c16;
+  int NE, hi, seg, kb_total, rows_m, rows_n, per, ph0, ph1, lo;
+  NtRows<P> vx, vw;
+  __device__ __forceinline__ void init(const RingArgs& p, int64_t m0, int64_t n0, int s_lo, int s_hi) {
+    const int side = DUAL ? ring_wave() >> 1 : 0;
+    rows_m = static_cast<int>(min<int64_t>(P::BM, p.T - m0));
+    rows_n = static_cast<int>(min<int64_t>(DUAL ? P::BN / 2 : P::BN, p.N - n0));
+    kb_total = static_cast<int>(p.K[0] * 2);
+    ldx_b = static_cast<uint32_t>(p.ldx * 2);
+    ldw_b = static_cast<uint32_t>(p.K[0] * 2);
+    ldt_b = static_cast<uint32_t>(p.ldt * 2);
+    ldb_b = static_cast<uint32_t>(p.re[side] * 2);
+    xm = make_rsrc(p.x[0] + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+    wm = make_rsrc(p.W[side] + n0 * p.K[0], static_cast<uint32_t>(rows_n) * ldw_b);
+    tr = make_rsrc(p.tt + m0 * p.ldt, static_cast<uint32_t>(rows_m) * ldt_b);
+    br = make_rsrc(p.E[side] + n0 * p.re[side], static_cast<uint32_t>(rows_n) * ldb_b);
+    NE = p.tt != nullptr ? static_cast<int>(p.ldt / 64) : 0;
+    per = (p.re[0] + p.re[1]) * 2;  // bytes of a term's columns; this side's are [ph0, ph1) of them
+    ph0 = side ? p.re[0] * 2 : 0;
+    ph1 = ph0 + p.re[side] * 2;
+    c16 = ring_chunk<P>();
+    lo = s_lo;
+    hi = s_hi;
+    seg = -1;
+  }
+  __device__ __forceinline__ void w_rows(uint32_t ld) {
+    if constexpr (!DUAL) vw.init(ld, rows_n);
+    else {
+      const int lane = opaque_int(threadIdx.x & 63);
+      const int r0 = (ring_wave() & 1) * 8 + (lane >> 3);
+#pragma unroll
+      for (int l = 0; l < NtRows<P>::N; ++l) {
+        const int row = l * 16 + r0;
+        vw.v[l] = row < rows_n ? static_cast<uint32_t>(row) * ld + c16 : kMissing;
+      }
+    }
+  }
+  __device__ __forceinline__ void seek(int t) {
+    const int s = lo + t;
+    if (s < NE && s < hi) {
+      if (seg != 0) {
+        seg = 0;
+        xr = tr;
+        wr = br;
+        vx.init(ldt_b, rows_m);
+        w_rows(ldb_b);
+      }
+      ax = static_cast<uint32_t>(s) * 128u;
+      const int b = s * 128 + static_cast<int>(c16), ph = b < per ? b : b - per;
+      aw = b < 2 * per && ph >= ph0 && ph < ph1 ? static_cast<uint32_t>(ph - ph0) - c16 : kMissing;
+    } else {
+      if (seg != 1) {
+        seg = 1;
+        xr = xm;
+        wr = wm;
+        vx.init(ldx_b, rows_m);
+        w_rows(ldw_b);
+      }
+      const int kb = (s - NE) * 128;
+      ax = aw = s < hi && kb + static_cast<int>(c16) < kb_total ? static_cast<uint32_t>(kb) : kMissing;
+    }
+  }
+  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
+  __device__ __forceinline__ void load_w(int l, char* d) const { ring_copy<P>(l, d, wr, vw.v[l] + aw); }
+  __device__ __forceinline__ void before(int, f32x4 (&)[P::NI][P::NJ]) const {}
+};
+
+// NN: rows of the contraction. Extension rows are the adapters' A rows, once for each term; a copy instruction's rows
+// (2 or 4 of 8 consecutive ones) belong to one adapter.
+template <class P>
+struct NnOp {
+  const uint16_t *x[2], *W[2], *E[2];
+  const uint16_t* tt;
+  __amdgpu_buffer_rsrc_t xr, wr, er0, er1;
+  uint32_t ldx_b, ldw_b, ldt_b, ax, c16;
+  int64_t ldw;
+  int K[2], re0, per, NE, n0s, hi, seg, rows_m, cols, lo, second;
+  NtRows<P> vx;
+  NnRows<P> vw;
+  // x_i [T, K_i] (from row m0 on), W_i [K_i, N], E_i [re_i, N] (columns from n0 on)
+  __device__ __forceinline__ void init(const uint16_t* const* xs, int64_t ldx, const uint16_t* const* Ws, const int64_t* Ks,
+                                       int n_seg, const uint16_t* tt_, int64_t ldt, const uint16_t* const* Es,
+                                       const int* re, int64_t T, int64_t N, int64_t m0, int64_t n0, int s_lo, int s_hi) {
+    rows_m = static_cast<int>(min<int64_t>(P::BM, T - m0));
+    cols = static_cast<int>(min<int64_t>(P::BN, N - n0));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool on = i < n_seg;
+      x[i] = on ? xs[i] + m0 * ldx : nullptr;
+      W[i] = on ? Ws[i] + n0 : nullptr;
+      K[i] = on ? static_cast<int>(Ks[i]) : 0;
+      E[i] = Es[i] + n0;
+    }
+    ldx_b = static_cast<uint32_t>(ldx * 2);
+    ldt_b = static_cast<uint32_t>(ldt * 2);
+    ldw = N;
+    ldw_b = static_cast<uint32_t>(N * 2);
+    tt = tt_ + m0 * ldt;
+    NE = tt_ != nullptr ? static_cast<int>(ldt / 64) : 0;
+    re0 = re[0];
+    per = re[0] + re[1];
+    er0 = make_rsrc(E[0], re[0] > 0 ? static_cast<uint32_t>(re[0] - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    er1 = make_rsrc(E[1], re[1] > 0 ? static_cast<uint32_t>(re[1] - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    n0s = (K[0] + 63) / 64;
+    c16 = ring_chunk<P>();
+    lo = s_lo;
+    hi = s_hi;
+    seg = -1;
+    second = 0;
+  }
+  __device__ __forceinline__ void seek(int t) {
+    const int s = lo + t;
+    if (s < NE && s < hi) {
+      if (seg != 0) {
+        xr = make_rsrc(tt, static_cast<uint32_t>(rows_m) * ldt_b);
+        vx.init(ldt_b, rows_m);
+      }
+      seg = 0;
+      ax = static_cast<uint32_t>(s) * 128u;
+      vw.init(0u, cols);  // (the columns' part; missing ones keep kMissing)
+      second = 0;
+#pragma unroll
+      for (int l = 0; l < NnRows<P>::N; ++l) {
+        const int vr = s * 64 + vw.row[l], ph = vr < per ? vr : vr - per;
+        const bool is2 = ph >= re0;
+        vw.v[l] = vr < 2 * per ? vw.v[l] + static_cast<uint32_t>(is2 ? ph - re0 : ph) * ldw_b : kMissing;
+        second |= (__builtin_amdgcn_readfirstlane(is2 ? 1 : 0)) << l;
+      }
+    } else {
+      const int ms = s - NE;
+      const int sg = ms < n0s ? 1 : 2;
+      if (seg != sg) {
+        if (seg < 1) {
+          vx.init(ldx_b, rows_m);
+          vw.init(ldw_b, cols);
+        }
+        seg = sg;
+        xr = make_rsrc(x[sg - 1], static_cast<uint32_t>(rows_m) * ldx_b);
+        second = 0;
+      }
+      const int k0 = (sg == 1 ? ms : ms - n0s) * 64;
+      const int left = s < hi ? min(64, K[sg - 1] - k0) : 0;
+      ax = static_cast<int>(c16) < left * 2 ? static_cast<uint32_t>(k0) * 2u : kMissing;
+      wr = make_rsrc(W[sg - 1] + (left > 0 ? static_cast<int64_t>(k0) * ldw : 0),
+                     left > 0 ? static_cast<uint32_t>(left - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    }
+  }
+  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
+  __device__ __forceinline__ void load_w(int l, char* d) const {
+    if (seg == 0) ring_copy<P>(l, d, (second >> l) & 1 ? er1 : er0, vw.v[l]);
+    else ring_copy<P>(l, d, wr, vw.v[l]);
+  }
+  __device__ __forceinline__ void before(int, f32x4 (&)[P::NI][P::NJ]) const {}
+};
+
+// Partial sums of a wave's block.
+template <class P>
+__device__ __forceinline__ void store_part(const f32x4 (&acc)[P::NI][P::NJ], float* part, int64_t ld, int64_t m0,
+                                           int64_t n0, int64_t T, int64_t N) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < P::NJ; ++j) {
+    const int64_t m = m0 + j * 16 + r;
+    if (m >= T) continue;
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i) {
+      const int64_t n = n0 + i * 16 + q * 4;
+      float* dst = part + m * ld + n;
+      if (ld % 4 == 0 && n + 3 < N) {
+        *reinterpret_cast<f32x4*>(dst) = acc[i][j];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) dst[e] = acc[i][j][e];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void load_bias4(float (&bv)[4], const uint16_t* bias, int64_t n, int64_t N) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) bv[e] = bias != nullptr && n + e < N ? bf16_to_f32(bias[n + e]) : 0.f;
+}
+
+template <class P>
+__device__ __forceinline__ void store_block(const f32x4 (&acc)[P::NI][P::NJ], const RingArgs& p, int64_t m0, int64_t n0,
+                                            char* smem) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  BlockOut<P::WM, P::WN> out{smem + ring_wave() * P::WM * P::WN * 2};
+#pragma unroll
+  for (int i = 0; i < P::NI; ++i) {
+    float bv[4];
+    load_bias4(bv, p.bias[0], n0 + i * 16 + q * 4, p.N);
+#pragma unroll
+    for (int j = 0; j < P::NJ; ++j)
+      out.put(j * 16 + r, i * 16 + q * 4, pack_bf16x2(acc[i][j][0] + bv[0], acc[i][j][1] + bv[1]),
+              pack_bf16x2(acc[i][j][2] + bv[2], acc[i][j][3] + bv[3]));
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (m0 < p.T && n0 < p.N)
+    out.store(p.y + m0 * p.ldy + n0, p.ldy, static_cast<int>(min<int64_t>(P::WM, p.T - m0)),
+              static_cast<int>(min<int64_t>(P::WN, p.N - n0)));
+}
+
+// acc = 0 where the element of the [T, N] tensor is dropped. A lane holds 4 columns, half of a call's 8: lanes q and
+// q ^ 1 make the calls of blocks i and i + 1 and exchange halves.
+template <class P>
+__device__ __forceinline__ void drop_block(f32x4 (&acc)[P::NI][P::NJ], const Dropper& d, int64_t m0, int64_t n0) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const bool odd = (q & 1) != 0;
+#pragma unroll
+  for (int j = 0; j < P::NJ; ++j) {
+    const int64_t row = (m0 + j * 16 + r) * d.blocks + n0 / 8 + (q >> 1);
+#pragma unroll
+    for (int i = 0; i < P::NI; i += 2) {
+      // lane q makes block i + (q & 1), keeps its own half and gives the other
+      const u32x4 w = philox7(static_cast<uint64_t>(row + (i + (odd ? 1 : 0)) * 2), d.seed, d.offset);
+      const uint32_t give0 = odd ? w[0] : w[2], give1 = odd ? w[1] : w[3];
+      const uint32_t got0 = __shfl_xor(give0, 16), got1 = __shfl_xor(give1, 16);
+      // an even lane's columns are the first half of both blocks, an odd lane's the second half
+      const uint32_t a0 = d.mask(odd ? got0 : w[0]), a1 = d.mask(odd ? got1 : w[1]);
+      const uint32_t b0 = d.mask(odd ? w[2] : got0), b1 = d.mask(odd ? w[3] : got1);
+      const uint32_t ms[2][2] = {{a0, a1}, {b0, b1}};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool keep = ((ms[h][e >> 1] >> (16 * (e & 1))) & 1u) != 0;
+          acc[i + h][j][e] = keep ? acc[i + h][j][e] : 0.f;
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <class P>
+struct DropNnOp : NnOp<P> {
+  Dropper d;
+  int64_t mw, nw;
+  int at;  // before this stage (counted from the split's first)
+  __device__ __forceinline__ void before(int t, f32x4 (&acc)[P::NI][P::NJ]) const {
+    if (t == at) drop_block<P>(acc, d, mw, nw);
+  }
+};
+
+enum { kFormNt = 0, kFormNn = 1, kFormNnDrop = 2 };
+
+// One layer, grid (tiles, splits).
+template <class P, int FORM>
+__global__ __launch_bounds__(P::THREADS, P::OCC) void ring_kernel(RingArgs p, int mt, int nt, int NS) {
+  __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
+  const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
+  const int wave = ring_wave();
+  const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
+  const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * P::BN;
+  const int s_lo = static_cast<int>(blockIdx.y) * p.ks, s_hi = min(NS, s_lo + p.ks);
+  f32x4 acc[P::NI][P::NJ];
+  if constexpr (FORM == kFormNt) {
+    NtOp<P, false> op;
+    op.init(p, m0, n0, s_lo, s_hi);
+    ring_run<P, false>(acc, op, s_hi - s_lo, smem, wm0, wn0);
+  } else if constexpr (FORM == kFormNn) {
+    NnOp<P> op;
+    op.init(p.x, p.ldx, p.W, p.K, p.n_seg, p.tt, p.ldt, p.E, p.re, p.T, p.N, m0, n0, s_lo, s_hi);
+    ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
+  } else {
+    DropNnOp<P> op;
+    op.init(p.x, p.ldx, p.W, p.K, p.n_seg, p.tt, p.ldt, p.E, p.re, p.T, p.N, m0, n0, s_lo, s_hi);
+    op.d.init(p.drop, p.N);
+    op.mw = m0 + wm0;
+    op.nw = n0 + wn0;
+    op.at = op.NE > s_lo ? op.NE - s_lo : -1;
+    ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
+    if (op.at >= s_hi - s_lo) drop_block<P>(acc, op.d, op.mw, op.nw);  // (this split ends before the base stages)
+  }
+  if (p.S > 1) store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.y) * p.T * p.N, p.N, m0 + wm0, n0 + wn0, p.T, p.N);
+  else store_block<P>(acc, p, m0 + wm0, n0 + wn0, smem);
+}
+
+// y = the splits' sum in order + bias. 4 columns per thread.
+__global__ __launch_bounds__(256) void ring_finish_kernel(RingArgs p) {
+  const int64_t quads = (p.N + 3) / 4, idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (idx >= p.T * quads) return;
+  const int64_t t = idx / quads, n = (idx - t * quads) * 4;
+  const float* src = p.part + t * p.N + n;
+  uint16_t* dst = p.y + t * p.ldy + n;
+  float bv[4];
+  load_bias4(bv, p.bias[0], n, p.N);
+  if (p.N % 4 == 0) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < p.S; ++z) v += *reinterpret_cast<const f32x4*>(src + z * p.T * p.N);
+    const uint2 w = {pack_bf16x2(v[0] + bv[0], v[1] + bv[1]), pack_bf16x2(v[2] + bv[2], v[3] + bv[3])};
+    if (reinterpret_cast<uintptr_t>(dst) % 8 == 0) {
+      *reinterpret_cast<uint2*>(dst) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dst[e] = static_cast<uint16_t>((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (n + e >= p.N) break;
+    float v = 0.f;
+    for (int z = 0; z < p.S; ++z) v += src[z * p.T * p.N + e];
+    dst[e] = f32_to_bf16_rne(v + bv[e]);
+  }
+}
+
+// Rank-wide product over rows of the contraction (the gradient's, B [K, rank] as it lies): 128 tokens and up to 128
+// columns of one adapter per workgroup, K split over grid z. Most of the MFMA's columns are empty for small ranks;
+// the kernel is bound by reading x.
+__global__ __launch_bounds__(Ring128::THREADS, Ring128::OCC) void rank_nn_kernel(RankProduct p, int ks, int tiles0) {
+  using P = Ring128;
+  __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
+  const int side = static_cast<int>(blockIdx.y) >= tiles0 ? 1 : 0;
+  const int wave = ring_wave();
+  const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
+  const int64_t n0 = static_cast<int64_t>(static_cast<int>(blockIdx.y) - (side ? tiles0 : 0)) * P::BN;
+  const int NS = static_cast<int>((p.K + 63) / 64), s_lo = static_cast<int>(blockIdx.z) * ks, s_hi = min(NS, s_lo + ks);
+  const uint16_t *xs[2] = {p.x[side], nullptr}, *Ws[2] = {p.A[side], nullptr}, *Es[2] = {nullptr, nullptr};
+  const int64_t Ks[2] = {p.K, 0};
+  const int re[2] = {0, 0};
+  NnOp<P> op;
+  op.init(xs, p.ldx, Ws, Ks, 1, nullptr, 0, Es, re, p.T, p.rank[side], m0, n0, s_lo, s_hi);
+  f32x4 acc[P::NI][P::NJ];
+  ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
+  const int R = p.rank[0] + p.rank[1], c0 = side ? p.rank[0] : 0;
+  store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.z) * p.T * R + c0, R, m0 + wm0, n0 + wn0, p.T, p.rank[side]);
+}
+
+// ---------------------------------------------------------------------------
+// The gated feed-forward.
+
+// act(g) and act'(g). exp2 and the reciprocal are the hardware's (within 1 last bit of fp32 each).
+__device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896f); }
+
+template <int ACT, bool GRAD>
+__device__ __forceinline__ void act_of(float g, float& a, float& da) {
+  if constexpr (ACT == 0) {  // g sigmoid(g)
+    const float s = __builtin_amdgcn_rcpf(1.f + fast_exp(-g));
+    a = g * s;
+    if (GRAD) da = s * (1.f + g * (1.f - s));
+  } else if constexpr (ACT == 1) {
+    // g Phi(g): the tail Phi(-|g|) = erfc(|g| / sqrt 2) / 2 by formula 7.1.26 of Abramowitz and Stegun (error of erf at
+    // most 1.5e-7), whose exponential is also the derivative's density
+    const float z = __builtin_fabsf(g) * 0.70710678118655f;
+    const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * z), e = fast_exp(-z * z);
+    const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float tail = 0.5f * poly * e, cdf = g < 0.f ? tail : 1.f - tail;
+    a = g * cdf;
+    if (GRAD) da = cdf + g * e * 0.39894228040143f;
+  } else {  // g sigmoid(2 c (g + 0.044715 g^3)), which is g (1 + tanh(c (..))) / 2
+    const float c2 = 1.59576912160573f, g2 = g * g;
+    const float s = __builtin_amdgcn_rcpf(1.f + fast_exp(-c2 * g * (1.f + 0.044715f * g2)));
+    a = g * s;
+    if (GRAD) da = s + g * s * (1.f - s) * c2 * (1.f + 0.134145f * g2);
+  }
+}
+
+template <class P, int ACT>
+__device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][P::NJ], const RingArgs& p, int64_t m0, int64_t n0,
+                                            char* smem) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  BlockOut<P::WM, P::WN / 2> out{smem + ring_wave() * P::WM * P::WN};
+  const int64_t fb = (p.N + 15) / 16;
+#pragma unroll
+  for (int i = 0; i < P::NI / 2; ++i) {
+    float bg[4], bu[4];
+    const int64_t n = n0 + i * 16 + q * 4;
+    load_bias4(bg, p.bias[0], n, p.N);
+    load_bias4(bu, p.bias[1], n, p.N);
+#pragma unroll
+    for (int j = 0; j < P::NJ; ++j) {
+      f32x4 g, u;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = acc[2 * i][j][e] + bg[e];
+        u[e] = acc[2 * i + 1][j][e] + bu[e];
+        float a, da;
+        act_of<ACT, false>(g[e], a, da);
+        v[e] = a * u[e];
+      }
+      out.put(j * 16 + r, i * 16 + q * 4, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      if (p.saved != nullptr && m0 + j * 16 < p.T && n0 + i * 16 < p.N) {
+        float* b = p.saved + (((m0 >> 4) + j) * fb + (n0 >> 4) + i) * 512 + lane * 4;
+        __builtin_nontemporal_store(g, reinterpret_cast<f32x4*>(b));
+        __builtin_nontemporal_store(u, reinterpret_cast<f32x4*>(b + 256));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (p.y != nullptr && m0 < p.T && n0 < p.N)
+    out.store(p.y + m0 * p.ldy + n0, p.ldy, static_cast<int>(min<int64_t>(P::WM, p.T - m0)),
+              static_cast<int>(min<int64_t>(P::WN / 2, p.N - n0)));
+}
+
+// BN / 2 outputs per tile: gate and up blocks of 16 rows in turn.
+template <class P, int ACT>
+__global__ __launch_bounds__(P::THREADS, P::OCC) void gated_kernel(RingArgs p, int mt, int nt, int NS) {
+  __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
+  const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
+  const int wave = ring_wave();
+  const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
+  const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * (P::BN / 2);
+  f32x4 acc[P::NI][P::NJ];
+  NtOp<P, true> op;
+  op.init(p, m0, n0, 0, NS);
+  ring_run<P, false>(acc, op, NS, smem, wm0, wn0);
+  gated_store<P, ACT>(acc, p, m0 + wm0, n0 + wn0 / 2, smem);
+}
+
+// dg and du: a wave takes 16 tokens x 64 columns, from the blocks that the forward kept.
+template <int ACT>
+__global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
+                                                         int64_t lddh, int64_t T, int64_t F, uint16_t* __restrict__ dg,
+                                                         uint16_t* __restrict__ du) {
+  __shared__ __attribute__((aligned(16))) char smem[4][2][16 * 64 * 2];
+  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, n0 = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 64;
+  if (n0 >= F) return;
+  const int64_t fb = (F + 15) / 16, m = min<int64_t>(m0 + r, T - 1);
+  BlockOut<16, 64> og{smem[wave][0]}, ou{smem[wave][1]};
+  f32x4 g[4], u[4];
+  uint2 d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + i * 16;
+    if (n >= F) continue;
+    const float* b = saved + ((m0 >> 4) * fb + (n >> 4)) * 512 + lane * 4;
+    g[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(b));
+    u[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(b + 256));
+    // (F is a multiple of 8, and so is the row stride: 8 bytes never cross the end)
+    d[i] = n + q * 4 < F ? *reinterpret_cast<const uint2*>(dh + m * lddh + n + q * 4) : uint2{0u, 0u};
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n0 + i * 16 >= F) continue;
+    const float dv[4] = {__uint_as_float(d[i].x << 16), __uint_as_float(d[i].x & 0xffff0000u),
+                         __uint_as_float(d[i].y << 16), __uint_as_float(d[i].y & 0xffff0000u)};
+    float vg[4], vu[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a, da;
+      act_of<ACT, true>(g[i][e], a, da);
+      vg[e] = dv[e] * u[i][e] * da;
+      vu[e] = dv[e] * a;
+    }
+    og.put(r, i * 16 + q * 4, pack_bf16x2(vg[0], vg[1]), pack_bf16x2(vg[2], vg[3]));
+    ou.put(r, i * 16 + q * 4, pack_bf16x2(vu[0], vu[1]), pack_bf16x2(vu[2], vu[3]));
+  }
+  const int rows = static_cast<int>(min<int64_t>(16, T - m0)), cols = static_cast<int>(min<int64_t>(64, F - n0));
+  og.store(dg + m0 * F + n0, F, rows, cols);
+  ou.store(du + m0 * F + n0, F, rows, cols);
+}
+
+// ---------------------------------------------------------------------------
+// Token contraction: 256 rows of P^T x 64 columns of Q per workgroup, 64 tokens per stage, a ring of three stages
+// [64 t][256] of P and [64 t][64 first terms | 64 second terms] of Q, both read with the transposing LDS read. Token
+// chunks over grid y leave fp32 partial sums that contract_reduce_kernel adds in order. HBM-bound: P is read once.
+constexpr int kCtP = kCtT * kCtI * 2, kCtQ = kCtT * 2 * kCtJ * 2, kCtStage = kCtP + kCtQ;
+
+template <bool DROP>
+__global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_t chunk, int slices0) {
+  __shared__ __attribute__((aligned(1024))) char smem[3 * kCtStage];
+  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const int ti = static_cast<int>(blockIdx.z) >= slices0 ? 1 : 0;
+  const ContractTask& k = p.task[ti];
+  const int j0 = (static_cast<int>(blockIdx.z) - (ti ? slices0 : 0)) * kCtJ, jn = min(kCtJ, k.J - j0), nj = (jn + 15) / 16;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kCtI;
+  const int cols = static_cast<int>(min<int64_t>(kCtI, p.M - i0));
+  const int z = blockIdx.y;
+  const int64_t t_lo = z * chunk, t_hi = min<int64_t>(p.T, t_lo + chunk);
+  const int nst = t_hi > t_lo ? static_cast<int>((t_hi - t_lo + kCtT - 1) / kCtT) : 0;
+  const uint32_t ldp_b = static_cast<uint32_t>(k.ldp * 2), ldt_b = static_cast<uint32_t>(p.ldt * 2);
+  // per-lane offsets: 8 instructions of P (2 rows of 512 bytes each), 4 of Q (4 rows of 256)
+  uint32_t vp[8], vq[4];
+  int prow[8], pcol[8];
+#pragma unroll
+  for (int l = 0; l < 8; ++l) {
+    const int sl = (l * 4 + wave) * 64 + lane, t = sl / 32, pc = sl % 32, f = (t & 3) | (((t >> 3) & 1) << 2);
+    const int col = (((pc >> 1) ^ f) * 2 + (pc & 1)) * 8;
+    vp[l] = col < cols ? static_cast<uint32_t>(t) * ldp_b + col * 2 : kMissing;
+    prow[l] = t;
+    pcol[l] = col;
+  }
+#pragma unroll
+  for (int l = 0; l < 4; ++l) {
+    const int sl = (l * 4 + wave) * 64 + lane, t = sl / 16, pc = sl % 16, f = (t & 3) | (((t >> 3) & 1) << 2);
+    const int col = (((pc >> 1) ^ f) * 2 + (pc & 1)) * 8, c = col & 63;
+    vq[l] = c < jn ? static_cast<uint32_t>(t) * ldt_b + static_cast<uint32_t>((col < 64 ? 0 : p.R) + k.q_col + j0 + c) * 2
+                   : kMissing;
+  }
+  auto issue = [&](int s) {
+    char* b = smem + (s % 3) * kCtStage;
+    const int64_t t0 = t_lo + static_cast<int64_t>(s) * kCtT;
+    const int rows = s < nst ? static_cast<int>(min<int64_t>(kCtT, t_hi - t0)) : 0;
+    const int64_t at = rows > 0 ? t0 : 0;
+    const __amdgpu_buffer_rsrc_t pr = make_rsrc(
+        k.P + at * k.ldp + i0, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldp_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    const __amdgpu_buffer_rsrc_t qr = make_rsrc(p.tt + at * p.ldt, static_cast<uint32_t>(rows) * ldt_b);
+#pragma unroll
+    for (int l = 0; l < 8; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (lds_void*)(b + (l * 4 + wave) * 1024), 16, vp[l], 0, 0, 0);
+#pragma unroll
+    for (int l = 0; l < 4; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, (lds_void*)(b + kCtP + (l * 4 + wave) * 1024), 16, vq[l], 0, 0, 0);
+  };
+  Dropper d;
+  if constexpr (DROP) d.init(p.drop, p.M);
+  f32x4 acc[4][kCtJ / 16];
+#pragma unroll
+  for (int ib = 0; ib < 4; ++ib)
+#pragma unroll
+    for (int jb = 0; jb < kCtJ / 16; ++jb) acc[ib][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int f = (r >> 2) | ((q & 1) << 2);
+  const uint32_t pa = static_cast<uint32_t>((8 * q + (r >> 2)) * 512 + (((wave * 4) ^ f) * 32) + (r & 3) * 8);
+  const uint32_t qa = static_cast<uint32_t>((8 * q + (r >> 2)) * 256 + f * 32 + (r & 3) * 8);
+  auto tr_frag = [](const char* at, int row4) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + row4));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  issue(0);
+  issue(1);
+  for (int s = 0; s < nst; ++s) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(12));  // stage s landed; s + 1 may be in flight
+    stage_barrier();                             // (and every wave is done reading stage s - 1)
+    issue(s + 2);
+    char* b = smem + (s % 3) * kCtStage;
+    if constexpr (DROP) {
+#pragma unroll
+      for (int l = 0; l < 8; ++l) {
+        u32x4* at = reinterpret_cast<u32x4*>(b + ((l * 4 + wave) * 64 + lane) * 16);
+        *at &= d.masks(t_lo + static_cast<int64_t>(s) * kCtT + prow[l], (i0 + pcol[l]) / 8);
+      }
+      stage_barrier();
+    }
+    const char *pb = b, *qb = b + kCtP;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 af[4];
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) af[ib] = tr_frag(pb + (pa ^ static_cast<uint32_t>(ib << 5)) + kk * 32 * 512, 4 * 512);
+#pragma unroll
+      for (int jb = 0; jb < kCtJ / 16; ++jb) {
+        if (jb >= nj) continue;
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const bf16x8 bq = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)) + kk * 32 * 256, 4 * 256);
+#pragma unroll
+          for (int ib = 0; ib < 4; ++ib)
+            acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq, acc[ib][jb], 0, 0, 0);
+        }
+      }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  // lane (r, q) of block (ib, jb): rows i = 64 wave + 16 ib + 4 q + e of P^T, column j = 16 jb + r
+  float* part = p.part + (ti ? static_cast<int64_t>(S) * p.M * p.task[0].J : 0) + static_cast<int64_t>(z) * p.M * k.J;
+#pragma unroll
+  for (int jb = 0; jb < kCtJ / 16; ++jb) {
+    const int j = j0 + jb * 16 + r;
+    if (j >= k.J || jb >= nj) continue;
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      const int64_t i = i0 + wave * 64 + ib * 16 + 4 * q;
+      if (i >= p.M) continue;  // (M is a multiple of 8: four rows exist together)
+      if (p.transposed) {
+        *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(j) * p.M + i) = acc[ib][jb];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[(i + e) * k.J + j] = acc[ib][jb][e];
+      }
+    }
+  }
+}
+
+// The chunks' sum in order, 4 elements per thread (M and J are multiples of 8). Grid y: task.
+__global__ __launch_bounds__(256) void contract_reduce_kernel(Contract p, int S) {
+  const int ti = blockIdx.y;
+  const ContractTask& k = p.task[ti];
+  const int64_t n = p.M * k.J, idx = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (idx >= n) return;
+  const float* src = p.part + (ti ? static_cast<int64_t>(S) * p.M * p.task[0].J : 0) + idx;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int z = 0; z < S; ++z) v += *reinterpret_cast<const f32x4*>(src + z * n);
+  const int64_t cut = p.transposed ? static_cast<int64_t>(k.split) * p.M : n;
+  void* out = idx < cut ? k.out[0] : k.out[1];
+  const int64_t at = idx < cut ? idx : idx - cut;
+  if (out == nullptr) return;
+  if (p.out_bf16) {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+    if (reinterpret_cast<uintptr_t>(o) % 8 == 0) {
+      *reinterpret_cast<uint2*>(o) = uint2{lo, hi};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+    }
+  } else {
+    float* o = static_cast<float*>(out) + at;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = v[e];
+  }
+}
+
+unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+int step_cus() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+  return n;
+}
+
+}  // namespace
+
+hipError_t launch_rank_product(const RankProduct& p, bool nn, hipStream_t s) {
+  const int64_t R0 = p.rank[0], R1 = p.rank[1], R = R0 + R1;
+  int S, ks;
+  rank_plan(p.T, p.K, rank_tasks(R0, R1, nn), &S, &ks);
+  if (nn) {
+    const int t0 = static_cast<int>((R0 + 127) / 128);
+    hipLaunchKernelGGL(rank_nn_kernel, dim3(blocks_of(p.T, 128), static_cast<unsigned>(rank_tasks(R0, R1, true)),
+                                            static_cast<unsigned>(S)), dim3(256), 0, s, p, ks, t0);
+  } else {
+    const bool narrow = R <= 64;
+    const dim3 grid(blocks_of(p.T, 128), blocks_of(R, narrow ? 64 : 128), static_cast<unsigned>(S));
+    const bool drop = p.drop.thr != 0;
+    if (narrow && drop) hipLaunchKernelGGL((rank_nt_kernel<RankNarrow, true>), grid, dim3(256), 0, s, p, ks);
+    else if (narrow) hipLaunchKernelGGL((rank_nt_kernel<RankNarrow, false>), grid, dim3(256), 0, s, p, ks);
+    else if (drop) hipLaunchKernelGGL((rank_nt_kernel<RankWide, true>), grid, dim3(256), 0, s, p, ks);
+    else hipLaunchKernelGGL((rank_nt_kernel<RankWide, false>), grid, dim3(256), 0, s, p, ks);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(rank_finish_kernel, dim3(blocks_of(p.T * (pair_ld(R) / 4), 256)), dim3(256), 0, s, p, S);
+  return hipGetLastError();
+}
+
+template <class P, int FORM>
+hipError_t launch_ring_cfg(const RingArgs& p, int NS, hipStream_t s) {
+  const int mt = static_cast<int>((p.T + P::BM - 1) / P::BM), nt = static_cast<int>((p.N + P::BN - 1) / P::BN);
+  hipLaunchKernelGGL((ring_kernel<P, FORM>), dim3(static_cast<unsigned>(mt * nt), static_cast<unsigned>(p.S)),
+                     dim3(P::THREADS), 0, s, p, mt, nt, NS);
+  return hipGetLastError();
+}
+
+hipError_t launch_ring(const RingArgs& a, bool nn, hipStream_t s) {
+  RingArgs p = a;
+  const int NS = static_cast<int>(ring_stages(p));
+  ring_plan(p.T, p.N, NS, &p.S, &p.ks);
+  const bool small = p.S > 1 || small_tile(p.T, p.N, step_cus());
+  const bool drop = p.drop.thr != 0;
+  hipError_t e;
+  if (!nn) e = small ? launch_ring_cfg<Ring128, kFormNt>(p, NS, s) : launch_ring_cfg<Ring256, kFormNt>(p, NS, s);
+  else if (!drop) e = small ? launch_ring_cfg<Ring128, kFormNn>(p, NS, s) : launch_ring_cfg<Ring256, kFormNn>(p, NS, s);
+  else e = small ? launch_ring_cfg<Ring128, kFormNnDrop>(p, NS, s) : launch_ring_cfg<Ring256, kFormNnDrop>(p, NS, s);
+  if (e != hipSuccess || p.S == 1) return e;
+  hipLaunchKernelGGL(ring_finish_kernel, dim3(blocks_of(p.T * ((p.N + 3) / 4), 256)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <class P>
+hipError_t launch_gated_cfg(const RingArgs& p, hipStream_t s) {
+  const int mt = static_cast<int>((p.T + P::BM - 1) / P::BM), nt = static_cast<int>((2 * p.N + P::BN - 1) / P::BN);
+  const int NS = static_cast<int>(ring_stages(p));
+  const dim3 grid(static_cast<unsigned>(mt * nt)), block(P::THREADS);
+  if (p.act == 0) hipLaunchKernelGGL((gated_kernel<P, 0>), grid, block, 0, s, p, mt, nt, NS);
+  else if (p.act == 1) hipLaunchKernelGGL((gated_kernel<P, 1>), grid, block, 0, s, p, mt, nt, NS);
+  else hipLaunchKernelGGL((gated_kernel<P, 2>), grid, block, 0, s, p, mt, nt, NS);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated(const RingArgs& p, hipStream_t s) {
+  return small_tile(p.T, 2 * p.N, step_cus()) ? launch_gated_cfg<Ring128>(p, s) : launch_gated_cfg<Ring256>(p, s);
+}
+
+hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,
+                             uint16_t* dg, uint16_t* du, hipStream_t s) {
+  const dim3 grid(blocks_of(T, 16), blocks_of(F, 256)), block(256);
+  if (act == 0) hipLaunchKernelGGL(gated_grad_kernel<0>, grid, block, 0, s, saved, dh, lddh, T, F, dg, du);
+  else if (act == 1) hipLaunchKernelGGL(gated_grad_kernel<1>, grid, block, 0, s, saved, dh, lddh, T, F, dg, du);
+  else hipLaunchKernelGGL(gated_grad_kernel<2>, grid, block, 0, s, saved, dh, lddh, T, F, dg, du);
+  return hipGetLastError();
+}
+
+hipError_t launch_contract(const Contract& p, hipStream_t s) {
+  const int64_t J0 = p.task[0].J, J1 = p.n_tasks > 1 ? p.task[1].J : 0, slices = contract_slices(J0, J1);
+  int S;
+  int64_t chunk;
+  contract_plan(p.T, p.M, slices, &S, &chunk);
+  const dim3 grid(blocks_of(p.M, kCtI), static_cast<unsigned>(S), static_cast<unsigned>(slices));
+  const int s0 = static_cast<int>(contract_slices(J0, 0));
+  if (p.drop.thr != 0) hipLaunchKernelGGL(contract_kernel<true>, grid, dim3(256), 0, s, p, S, chunk, s0);
+  else hipLaunchKernelGGL(contract_kernel<false>, grid, dim3(256), 0, s, p, S, chunk, s0);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(contract_reduce_kernel, dim3(blocks_of(p.M * (J0 > J1 ? J0 : J1), 1024), static_cast<unsigned>(p.n_tasks)),
+                     dim3(256), 0, s, p, S);
+  return hipGetLastError();
+}
+
+}  // namespace lora

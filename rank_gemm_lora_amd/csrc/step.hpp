@@ -1,0 +1,149 @@
+// Internal interface of the kernels of a fine-tuning step (step.hip: linear layers with dropout before the adapter and
+// the gated feed-forward; loss.hip: the vocabulary loss) for the C-ABI host code (step_api.cpp).
+#pragma once
+
+#include "launch.hpp"
+
+namespace lora {
+
+// Dropout of an adapter's input. thr of 65536 outcomes drop an element; 0: none.
+struct Drop {
+  uint32_t thr;
+  uint64_t seed, offset;
+  const uint64_t* rng;  // device {seed, offset} in place of the two, or null
+};
+
+// A rank-wide product's row: R columns (the adapters side by side) as two bf16 terms, hi = RN(v) then mid = RN(v - hi),
+// zeros up to a multiple of 64. (One term alone leaves 2^-9 of every rank's part in an output that is rounded once.)
+inline int64_t pair_ld(int64_t R) { return (2 * R + 63) / 64 * 64; }
+
+// ---------------------------------------------------------------- rank-wide products
+// tt[t] = scale . x[t] . A^T (x masked by drop when given) for up to two adapters side by side, or with `nn`
+// scale . x_i[t] . B_i for B_i [K, rank_i] (the gradient's side: every adapter has its own x).
+struct RankProduct {
+  const uint16_t* x[2]; int64_t ldx;
+  const uint16_t* A[2];   // [rank, K], or nn: [K, rank]
+  int rank[2];            // rank[1] 0: one adapter
+  float scale[2];
+  int64_t T, K;
+  Drop drop;
+  float* part;            // [S, T, R]
+  uint16_t* tt;           // [T, pair_ld(R)]
+};
+// Splits of K, fixed by the sizes: enough workgroups of 128 tokens for two on each of 256 compute units, at least 4
+// stages of 64 each.
+constexpr int kRankMaxSplits = 16;
+inline void rank_plan(int64_t T, int64_t K, int64_t tasks, int* S, int* ks) {
+  const int64_t mt = (T + 127) / 128 * tasks, nk = (K + 63) / 64;
+  int64_t s = mt > 0 ? 512 / mt : 1;
+  const int64_t smax = nk / 4 > 1 ? nk / 4 : 1;
+  s = s < 1 ? 1 : (s > kRankMaxSplits ? kRankMaxSplits : s);
+  s = s > smax ? smax : s;
+  *ks = static_cast<int>((nk + s - 1) / s);
+  *S = static_cast<int>((nk + *ks - 1) / *ks);
+}
+inline int64_t rank_tasks(int64_t R0, int64_t R1, bool nn) {
+  return nn ? (R0 + 127) / 128 + (R1 + 127) / 128 : (R0 + R1 + 127) / 128;
+}
+inline size_t rank_part_bytes(int64_t T, int64_t K, int64_t R0, int64_t R1, bool nn) {
+  int S, ks;
+  rank_plan(T, K, rank_tasks(R0, R1, nn), &S, &ks);
+  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R0 + R1) * 4;
+}
+hipError_t launch_rank_product(const RankProduct& p, bool nn, hipStream_t s);
+
+// ---------------------------------------------------------------- ring GEMMs
+// y [T, N] = sum over segments of x_i . W_i (NT: W [N, K], NN: W [K, N]) + tt . [E; E] (tt as above; NT: E_i [N, rank_i],
+// NN: E_i [rank_i, N]) + bias. With `drop` (NN) the extension's part is masked as the [T, N] tensor it is a gradient of.
+struct RingArgs {
+  const uint16_t* x[2]; int64_t ldx;
+  const uint16_t* W[2];
+  int64_t K[2]; int n_seg;
+  const uint16_t* tt; int64_t ldt;
+  const uint16_t* E[2]; int re[2];
+  const uint16_t* bias[2];
+  int64_t T, N;
+  uint16_t* y; int64_t ldy;
+  Drop drop;
+  float* part;    // S > 1: [S, T, N] fp32
+  int S, ks;      // splits of the stages, ks each
+  float* saved;   // gated: where the forward leaves g and u, or null
+  int act;
+};
+inline int64_t ring_stages(const RingArgs& p) {
+  int64_t n = p.tt != nullptr ? p.ldt / 64 : 0;
+  for (int i = 0; i < p.n_seg; ++i) n += (p.K[i] + 63) / 64;
+  return n;
+}
+// Splits of a layer whose tiles leave compute units idle: 128 x 128 tiles, two on each of 256 units, at least 8 stages
+// each (fp32 partial sums cost a write and a read of T N 4 bytes per split).
+constexpr int kRingMaxSplits = 16;
+inline void ring_plan(int64_t T, int64_t N, int64_t stages, int* S, int* ks) {
+  const int64_t tiles = (T + 127) / 128 * ((N + 127) / 128);
+  int64_t s = tiles > 0 ? 512 / tiles : 1;
+  const int64_t smax = stages / 8 > 1 ? stages / 8 : 1;
+  s = s < 1 ? 1 : (s > kRingMaxSplits ? kRingMaxSplits : s);
+  s = s > smax ? smax : s;
+  *ks = static_cast<int>((stages + s - 1) / s);
+  if (*ks < 1) *ks = 1;
+  *S = static_cast<int>((stages + *ks - 1) / *ks);
+}
+inline size_t ring_part_bytes(int64_t T, int64_t N, int64_t stages) {
+  int S, ks;
+  ring_plan(T, N, stages, &S, &ks);
+  return S > 1 ? static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(N) * 4 : 0;
+}
+hipError_t launch_ring(const RingArgs& p, bool nn, hipStream_t s);     // (plans the splits itself: p.part holds them)
+// h = act(g) . u: W[0], E[0], bias[0] the gate's, [1] the up projection's; N columns of each; one segment.
+hipError_t launch_gated(const RingArgs& p, hipStream_t s);
+
+// g and u as the forward keeps them: fp32, in blocks of 16 tokens x 16 columns as the MFMA leaves them (block (a, b):
+// 256 values of g, then 256 of u; lane l = 16 q + r holds token r, columns 4 q .. + 3).
+inline int64_t gated_blocks(int64_t n) { return (n + 15) / 16; }
+inline size_t gated_saved_bytes(int64_t T, int64_t F) {
+  return static_cast<size_t>(gated_blocks(T)) * static_cast<size_t>(gated_blocks(F)) * 512 * 4;
+}
+// dg = dh . u . act'(g) and du = dh . act(g), bf16 [T, F] each.
+hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,
+                             uint16_t* dg, uint16_t* du, hipStream_t s);
+
+// ---------------------------------------------------------------- token contractions
+// out_i [J, M] (transposed: one adapter's rows behind the other's) or [M, J] = P^T . Q over the tokens, Q the columns
+// q_col .. of a rank-wide product's rows (both terms). P masked by drop when given.
+struct ContractTask {
+  const uint16_t* P; int64_t ldp;
+  int q_col, J;
+  void* out[2];     // transposed: rows [0, split) and [split, J); else out[0]
+  int split;
+};
+struct Contract {
+  ContractTask task[2]; int n_tasks;
+  int64_t T, M;
+  const uint16_t* tt; int64_t ldt; int R;  // R: where the second term's columns begin
+  Drop drop;
+  bool transposed;
+  bool out_bf16;
+  float* part;      // [task][S, M, J]
+};
+constexpr int kCtI = 256, kCtJ = 64, kCtT = 64;
+inline void contract_plan(int64_t T, int64_t M, int64_t slices, int* S, int64_t* chunk) {
+  const int64_t tiles = (M + kCtI - 1) / kCtI * slices;
+  int64_t s = tiles > 0 ? 256 / tiles : 1;
+  const int64_t smax = (T + 4 * kCtT - 1) / (4 * kCtT);
+  s = s < 1 ? 1 : (s > smax ? smax : s);
+  s = s < 1 ? 1 : (s > 64 ? 64 : s);
+  int64_t c = (T + s - 1) / s;
+  c = (c + kCtT - 1) / kCtT * kCtT;
+  *chunk = c < kCtT ? kCtT : c;
+  *S = T > 0 ? static_cast<int>((T + *chunk - 1) / *chunk) : 1;
+}
+inline int64_t contract_slices(int64_t J0, int64_t J1) { return (J0 + kCtJ - 1) / kCtJ + (J1 + kCtJ - 1) / kCtJ; }
+inline size_t contract_part_bytes(int64_t T, int64_t M, int64_t J0, int64_t J1) {
+  int S;
+  int64_t c;
+  contract_plan(T, M, contract_slices(J0, J1), &S, &c);
+  return static_cast<size_t>(S) * static_cast<size_t>(M) * static_cast<size_t>(J0 + J1) * 4;
+}
+hipError_t launch_contract(const Contract& p, hipStream_t s);
+
+}  // namespace lora

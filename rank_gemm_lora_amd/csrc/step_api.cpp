@@ -1,0 +1,517 @@
+// C-ABI of a fine-tuning step's operators: argument validation, workspace layout and the order of the launches. Every
+// check runs before any launch.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+
+#include "backward.hpp"
+#include "checks.hpp"
+#include "lora_mi355x.h"
+#include "step.hpp"
+
+namespace {
+
+using lora::aligned;
+using lora::Contract;
+using lora::Drop;
+using lora::kMaxRowBytes;
+using lora::overlaps;
+using lora::RankProduct;
+using lora::RingArgs;
+using lora::round_up;
+using lora::Span;
+using lora::span2d;
+
+constexpr int64_t kMaxTokens = int64_t(1) << 26;
+
+struct Take {  // regions of a workspace, each 256-byte aligned
+  size_t off = 0;
+  size_t operator()(size_t n) {
+    const size_t o = off;
+    off = round_up(off + n);
+    return o;
+  }
+};
+
+// One adapter of a call: its rank is 0 where it is absent or its combined scale is +-0.
+struct Side {
+  const void *A, *B;
+  int64_t given, rank;
+  float scale;
+};
+
+int make_side(Side& s, const void* A, const void* B, int32_t rank, double alpha, double strength, double request_scale) {
+  s = Side{A, B, 0, 0, 0.f};
+  if ((A == nullptr) != (B == nullptr)) return LORA_ERR_NULL_PTR;
+  if (!std::isfinite(alpha)) return LORA_ERR_NONFINITE;
+  if (A == nullptr) return LORA_OK;
+  if (rank < 1) return LORA_ERR_SHAPE;
+  if (rank > LORA_MAX_RANK) return LORA_ERR_UNSUPPORTED;
+  if (rank % 8 != 0) return LORA_ERR_ALIGN;
+  const double v = (alpha / static_cast<double>(rank)) * strength * request_scale;
+  if (std::fabs(v) > FLT_MAX) return LORA_ERR_NONFINITE;
+  s.given = rank;
+  s.rank = v == 0.0 ? 0 : rank;
+  s.scale = static_cast<float>(v);
+  return LORA_OK;
+}
+
+// Sizes that every call of T tokens, K inputs and N outputs keeps to (row strides: two more of its tensors').
+int check_sizes(int64_t T, int64_t K, int64_t N, int64_t ld0, int64_t ld1) {
+  if (T >= kMaxTokens || K * 4 > kMaxRowBytes || N * 4 > kMaxRowBytes || ld0 * 2 > kMaxRowBytes || ld1 * 2 > kMaxRowBytes)
+    return LORA_ERR_UNSUPPORTED;
+  return LORA_OK;
+}
+
+// No output overlaps an input, the workspace or another output.
+template <int NO, int NI>
+bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Span& in : ins)
+      if (overlaps(outs[i], in)) return true;
+    for (int j = i + 1; j < NO; ++j)
+      if (overlaps(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+Span bytes_at(const void* p, size_t n) {
+  return n ? Span{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + n} : Span{};
+}
+
+const uint16_t* bf(const void* p) { return static_cast<const uint16_t*>(p); }
+uint16_t* bf(void* p) { return static_cast<uint16_t*>(p); }
+
+size_t tt_bytes(int64_t T, int64_t R) { return R > 0 ? static_cast<size_t>(T) * lora::pair_ld(R) * 2 : 0; }
+
+int64_t stages(int64_t K0, int64_t K1, int64_t R) {
+  return (R > 0 ? lora::pair_ld(R) / 64 : 0) + (K0 + 63) / 64 + (K1 + 63) / 64;
+}
+
+hipError_t zero_grad(void* g, int64_t n, int32_t dtype, hipStream_t s) {
+  if (g == nullptr || n == 0) return hipSuccess;
+  // (bf16: pairs; n is a multiple of 8 and the buffer 4-byte aligned)
+  return lora::zero_fill(static_cast<float*>(g), dtype == LORA_F32 ? n : n / 2, s);
+}
+
+// ------------------------------------------------------------------------------------------- dropout
+
+struct DropLayout {
+  size_t tt = 0, ut = 0, part = 0, total = 0;
+};
+// one layout for both directions (the forward uses a part of it)
+DropLayout drop_layout(int64_t T, int64_t K, int64_t N, int64_t R, bool backward) {
+  DropLayout L;
+  Take take;
+  L.tt = take(tt_bytes(T, R));
+  size_t part = std::max(lora::rank_part_bytes(T, K, R, 0, false), lora::ring_part_bytes(T, N, stages(K, 0, R)));
+  if (backward) {
+    L.ut = take(tt_bytes(T, R));
+    part = std::max(part, lora::rank_part_bytes(T, N, R, 0, true));
+    part = std::max(part, lora::ring_part_bytes(T, K, stages(N, 0, R)));
+    part = std::max(part, std::max(lora::contract_part_bytes(T, K, R, 0), lora::contract_part_bytes(T, N, R, 0)));
+  }
+  // (an inactive adapter has no extension: fewer stages, other splits)
+  part = std::max(part, lora::ring_part_bytes(T, N, stages(K, 0, 0)));
+  if (backward) part = std::max(part, lora::ring_part_bytes(T, K, stages(N, 0, 0)));
+  L.part = take(part);
+  L.total = take.off;
+  return L;
+}
+
+int make_drop(Drop& d, double p, uint64_t seed, uint64_t offset, const uint64_t* rng) {
+  if (!std::isfinite(p)) return LORA_ERR_NONFINITE;
+  const double thr = std::nearbyint(p * 65536.0);
+  if (p < 0.0 || thr > 65535.0) return LORA_ERR_UNSUPPORTED;
+  if (!aligned(rng, 8)) return LORA_ERR_ALIGN;
+  d.thr = static_cast<uint32_t>(thr);
+  d.seed = seed;
+  d.offset = offset;
+  d.rng = rng;
+  return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_linear_dropout_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank) {
+  if (T <= 0 || K <= 0 || N <= 0 || rank < 1 || T >= kMaxTokens) return 0;
+  return drop_layout(T, K, N, rank, false).total;
+}
+
+size_t lora_linear_dropout_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank) {
+  if (T <= 0 || K <= 0 || N <= 0 || rank < 1 || T >= kMaxTokens) return 0;
+  return drop_layout(T, K, N, rank, true).total;
+}
+
+int lora_linear_dropout_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N, const void* bias,
+                            const void* A, const void* B, int32_t rank, double alpha, double strength,
+                            double request_scale, double p, uint64_t seed, uint64_t offset, const uint64_t* rng, void* y,
+                            int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || K < 1 || N < 1 || ldx < K || ldy < N) return LORA_ERR_SHAPE;
+  if (int e = check_sizes(T, K, N, ldx, ldy)) return e;
+  if (!std::isfinite(strength) || !std::isfinite(request_scale)) return LORA_ERR_NONFINITE;
+  Drop drop;
+  if (int e = make_drop(drop, p, seed, offset, rng)) return e;
+  Side a;
+  const double keep = 1.0 - static_cast<double>(drop.thr) / 65536.0;
+  if (int e = make_side(a, A, B, rank, alpha, strength, request_scale / keep)) return e;
+  if (A == nullptr || W == nullptr || (T > 0 && (x == nullptr || y == nullptr))) return LORA_ERR_NULL_PTR;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(workspace, 16) ||
+      !aligned(y, 2) || !aligned(bias, 2) || K % 8 != 0 || ldx % 8 != 0)
+    return LORA_ERR_ALIGN;
+  const DropLayout L = T > 0 ? drop_layout(T, K, N, a.given, false) : DropLayout{};
+  if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
+  const Span wsp = bytes_at(workspace, L.total);
+  const Span outs[2] = {span2d(y, T, ldy, N, 2), wsp};
+  const Span ins[6] = {span2d(x, T, ldx, K, 2), span2d(W, N, K, K, 2), span2d(bias, 1, N, N, 2),
+                       span2d(A, rank, K, K, 2), span2d(B, N, rank, rank, 2), span2d(rng, 1, 2, 2, 8)};
+  if (clash(outs, ins)) return LORA_ERR_OVERLAP;
+  if (T == 0) return LORA_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  RingArgs g;
+  std::memset(&g, 0, sizeof(g));
+  if (a.rank > 0) {
+    RankProduct r;
+    std::memset(&r, 0, sizeof(r));
+    r.x[0] = bf(x); r.ldx = ldx; r.A[0] = bf(A); r.rank[0] = rank; r.scale[0] = a.scale; r.T = T; r.K = K; r.drop = drop;
+    r.part = reinterpret_cast<float*>(ws + L.part);
+    r.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
+    if (lora::launch_rank_product(r, false, st) != hipSuccess) return LORA_ERR_HIP;
+    g.tt = r.tt; g.ldt = lora::pair_ld(rank); g.E[0] = bf(B); g.re[0] = rank;
+  }
+  g.x[0] = bf(x); g.ldx = ldx; g.W[0] = bf(W); g.K[0] = K; g.n_seg = 1; g.bias[0] = bf(bias); g.T = T; g.N = N;
+  g.y = bf(y); g.ldy = ldy; g.part = reinterpret_cast<float*>(ws + L.part);
+  return lora::launch_ring(g, false, st) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N, const void* A,
+                            const void* B, int32_t rank, double alpha, double strength, double request_scale, double p,
+                            uint64_t seed, uint64_t offset, const uint64_t* rng, const void* dy, int64_t lddy, void* dx,
+                            int64_t lddx, void* dA, void* dB, int32_t grad_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  if (T < 0 || K < 1 || N < 1 || ldx < K || lddy < N || (dx != nullptr && lddx < K)) return LORA_ERR_SHAPE;
+  if (int e = check_sizes(T, K, N, ldx, lddy)) return e;
+  if (dx != nullptr && lddx * 2 > kMaxRowBytes) return LORA_ERR_UNSUPPORTED;
+  if (!std::isfinite(strength) || !std::isfinite(request_scale)) return LORA_ERR_NONFINITE;
+  Drop drop;
+  if (int e = make_drop(drop, p, seed, offset, rng)) return e;
+  Side a;
+  const double keep = 1.0 - static_cast<double>(drop.thr) / 65536.0;
+  if (int e = make_side(a, A, B, rank, alpha, strength, request_scale / keep)) return e;
+  if (A == nullptr || (dx != nullptr && W == nullptr) || (T > 0 && (x == nullptr || dy == nullptr)))
+    return LORA_ERR_NULL_PTR;
+  const int eg = grad_dtype == LORA_F32 ? 4 : 2;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dy, 16) ||
+      !aligned(workspace, 16) || !aligned(dx, 2) || !aligned(dA, 4) || !aligned(dB, 4) || K % 8 != 0 || N % 8 != 0 ||
+      ldx % 8 != 0 || lddy % 8 != 0)
+    return LORA_ERR_ALIGN;
+  const DropLayout L = T > 0 ? drop_layout(T, K, N, a.given, true) : DropLayout{};
+  if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
+  const Span wsp = bytes_at(workspace, L.total);
+  const Span outs[4] = {span2d(dx, T, lddx, K, 2), span2d(dA, 1, rank * K, rank * K, eg),
+                        span2d(dB, 1, N * rank, N * rank, eg), wsp};
+  const Span ins[6] = {span2d(x, T, ldx, K, 2), span2d(W, N, K, K, 2), span2d(dy, T, lddy, N, 2),
+                       span2d(A, rank, K, K, 2), span2d(B, N, rank, rank, 2), span2d(rng, 1, 2, 2, 8)};
+  if (clash(outs, ins)) return LORA_ERR_OVERLAP;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (T == 0 || a.rank == 0) {
+    if (zero_grad(dA, static_cast<int64_t>(rank) * K, grad_dtype, st) != hipSuccess ||
+        zero_grad(dB, N * static_cast<int64_t>(rank), grad_dtype, st) != hipSuccess)
+      return LORA_ERR_HIP;
+    if (T == 0) return LORA_OK;
+  }
+  char* ws = static_cast<char*>(workspace);
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  const int64_t ldt = lora::pair_ld(rank);
+  RankProduct u;
+  std::memset(&u, 0, sizeof(u));
+  u.rank[0] = rank; u.scale[0] = a.scale; u.T = T; u.part = part;
+  RankProduct t = u;
+  if (a.rank > 0 && (dx != nullptr || dA != nullptr)) {  // u = s dy B
+    u.x[0] = bf(dy); u.ldx = lddy; u.A[0] = bf(B); u.K = N;
+    u.tt = reinterpret_cast<uint16_t*>(ws + L.ut);
+    if (lora::launch_rank_product(u, true, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (dx != nullptr) {
+    RingArgs g;
+    std::memset(&g, 0, sizeof(g));
+    if (a.rank > 0) {
+      g.tt = u.tt; g.ldt = ldt; g.E[0] = bf(A); g.re[0] = rank;
+      g.drop = drop;
+    }
+    g.x[0] = bf(dy); g.ldx = lddy; g.W[0] = bf(W); g.K[0] = N; g.n_seg = 1; g.T = T; g.N = K;
+    g.y = bf(dx); g.ldy = lddx; g.part = part;
+    if (lora::launch_ring(g, true, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (a.rank == 0) return LORA_OK;
+  Contract c;
+  std::memset(&c, 0, sizeof(c));
+  c.n_tasks = 1; c.T = T; c.ldt = ldt; c.R = rank; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part;
+  if (dB != nullptr) {  // dB = dy^T t, t = s x' A^T as the forward forms it
+    t.x[0] = bf(x); t.ldx = ldx; t.A[0] = bf(A); t.K = K; t.drop = drop;
+    t.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
+    if (lora::launch_rank_product(t, false, st) != hipSuccess) return LORA_ERR_HIP;
+    c.task[0] = lora::ContractTask{bf(dy), lddy, 0, rank, {dB, nullptr}, rank};
+    c.M = N; c.tt = t.tt;
+    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (dA != nullptr) {  // dA = u^T x'
+    c.task[0] = lora::ContractTask{bf(x), ldx, 0, rank, {dA, nullptr}, rank};
+    c.M = K; c.tt = u.tt; c.transposed = true; c.drop = drop;
+    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  return LORA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------- gated feed-forward
+
+namespace {
+
+struct GatedLayout {
+  size_t tt = 0, vt = 0, dg = 0, du = 0, saved = 0, part = 0, total = 0;
+};
+
+size_t gated_fwd_part(int64_t T, int64_t K, int64_t R) { return R > 0 ? lora::rank_part_bytes(T, K, R, 0, false) : 0; }
+
+GatedLayout gated_fwd_layout(int64_t T, int64_t K, int64_t rg, int64_t ru) {
+  GatedLayout L;
+  Take take;
+  L.tt = take(tt_bytes(T, rg + ru));
+  // (rank_tasks depends on the sum alone; an inactive adapter's split plan is never larger than 16 splits of the rest)
+  L.part = take(std::max(gated_fwd_part(T, K, rg + ru), std::max(gated_fwd_part(T, K, rg), gated_fwd_part(T, K, ru))));
+  L.total = take.off;
+  return L;
+}
+
+// What the forward keeps for the backward: the blocks of g and u, then the rank-wide rows.
+size_t saved_tt_at(int64_t T, int64_t F) { return round_up(lora::gated_saved_bytes(T, F)); }
+size_t saved_bytes(int64_t T, int64_t F, int64_t R) { return saved_tt_at(T, F) + round_up(tt_bytes(T, R)); }
+
+GatedLayout gated_bwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_t ru) {
+  GatedLayout L;
+  Take take;
+  const int64_t R = rg + ru;
+  L.dg = take(static_cast<size_t>(T) * F * 2);
+  L.du = take(static_cast<size_t>(T) * F * 2);
+  L.vt = take(tt_bytes(T, R));
+  size_t part = gated_fwd_layout(T, K, rg, ru).total;
+  for (int i = 0; i < 4; ++i) {  // both adapters, or either of them inactive
+    const int64_t a = i & 1 ? 0 : rg, b = i & 2 ? 0 : ru;
+    if (a + b > 0) {
+      part = std::max(part, gated_fwd_part(T, K, a + b));
+      part = std::max(part, lora::rank_part_bytes(T, F, a, b, true));
+      part = std::max(part, lora::contract_part_bytes(T, K, a + b, 0));
+      part = std::max(part, lora::contract_part_bytes(T, F, a, b));
+    }
+    part = std::max(part, lora::ring_part_bytes(T, K, stages(F, F, a + b)));
+  }
+  L.part = take(part);
+  L.saved = take(saved_bytes(T, F, R));  // (last: not used where the forward's is given)
+  L.total = take.off;
+  return L;
+}
+
+int check_gated(const lora_gated_layer* l, int64_t T, int64_t K, int64_t F, int32_t act, double strength,
+                double request_scale, Side (&s)[2]) {
+  if (l == nullptr) return LORA_ERR_NULL_PTR;
+  if (act != LORA_ACT_SILU && act != LORA_ACT_GELU && act != LORA_ACT_GELU_TANH) return LORA_ERR_UNSUPPORTED;
+  if (!std::isfinite(strength) || !std::isfinite(request_scale)) return LORA_ERR_NONFINITE;
+  if (int e = make_side(s[0], l->A_gate, l->B_gate, l->rank_gate, l->alpha_gate, strength, request_scale)) return e;
+  if (int e = make_side(s[1], l->A_up, l->B_up, l->rank_up, l->alpha_up, strength, request_scale)) return e;
+  if (l->W_gate == nullptr || l->W_up == nullptr) return LORA_ERR_NULL_PTR;
+  for (const void* p : {l->W_gate, l->W_up, l->A_gate, l->B_gate, l->A_up, l->B_up})
+    if (!aligned(p, 16)) return LORA_ERR_ALIGN;
+  if (!aligned(l->b_gate, 2) || !aligned(l->b_up, 2) || K % 8 != 0) return LORA_ERR_ALIGN;
+  return LORA_OK;
+}
+
+void gated_spans(const lora_gated_layer* l, int64_t K, int64_t F, const Side (&s)[2], Span* out) {
+  out[0] = span2d(l->W_gate, F, K, K, 2);
+  out[1] = span2d(l->W_up, F, K, K, 2);
+  out[2] = span2d(l->b_gate, 1, F, F, 2);
+  out[3] = span2d(l->b_up, 1, F, F, 2);
+  out[4] = span2d(l->A_gate, s[0].given, K, K, 2);
+  out[5] = span2d(l->B_gate, F, s[0].given, s[0].given, 2);
+  out[6] = span2d(l->A_up, s[1].given, K, K, 2);
+  out[7] = span2d(l->B_up, F, s[1].given, s[1].given, 2);
+}
+
+// The active adapters' sides of a problem with two: their count of columns, and each in its place.
+hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* l, const Side (&s)[2],
+                         int64_t F, int32_t act, void* h, int64_t ldh, float* saved, uint16_t* tt, float* part,
+                         hipStream_t st) {
+  RingArgs g;
+  std::memset(&g, 0, sizeof(g));
+  const int64_t R = s[0].rank + s[1].rank;
+  if (R > 0) {
+    RankProduct r;
+    std::memset(&r, 0, sizeof(r));
+    r.x[0] = bf(x); r.ldx = ldx; r.T = T; r.K = K; r.part = part; r.tt = tt;
+    for (int i = 0; i < 2; ++i) {
+      r.A[i] = bf(s[i].A); r.rank[i] = static_cast<int>(s[i].rank); r.scale[i] = s[i].scale;
+      g.E[i] = bf(s[i].B); g.re[i] = static_cast<int>(s[i].rank);
+    }
+    const hipError_t e = lora::launch_rank_product(r, false, st);
+    if (e != hipSuccess) return e;
+    g.tt = tt; g.ldt = lora::pair_ld(R);
+  }
+  g.x[0] = bf(x); g.ldx = ldx; g.W[0] = bf(l->W_gate); g.W[1] = bf(l->W_up); g.K[0] = K; g.n_seg = 1;
+  g.bias[0] = bf(l->b_gate); g.bias[1] = bf(l->b_up); g.T = T; g.N = F; g.y = bf(h); g.ldy = ldh; g.act = act;
+  g.saved = saved;
+  return lora::launch_gated(g, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_gated_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up) {
+  if (T <= 0 || K <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
+  return gated_fwd_layout(T, K, rank_gate, rank_up).total;
+}
+
+size_t lora_gated_saved_size(int64_t T, int64_t F, int32_t rank_gate, int32_t rank_up) {
+  if (T <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
+  return saved_bytes(T, F, rank_gate + rank_up);
+}
+
+size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up) {
+  if (T <= 0 || K <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
+  return gated_bwd_layout(T, K, F, rank_gate, rank_up).total;
+}
+
+int lora_gated_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* layer, int64_t F,
+                   int32_t act, double strength, double request_scale, void* h, int64_t ldh, void* saved,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || K < 1 || F < 1 || ldx < K || ldh < F) return LORA_ERR_SHAPE;
+  if (int e = check_sizes(T, K, F, ldx, ldh)) return e;
+  Side s[2];
+  if (int e = check_gated(layer, T, K, F, act, strength, request_scale, s)) return e;
+  if (T > 0 && (x == nullptr || h == nullptr)) return LORA_ERR_NULL_PTR;
+  if (!aligned(x, 16) || !aligned(h, 2) || !aligned(workspace, 16) || !aligned(saved, 16) || ldx % 8 != 0)
+    return LORA_ERR_ALIGN;
+  const GatedLayout L = T > 0 ? gated_fwd_layout(T, K, s[0].given, s[1].given) : GatedLayout{};
+  if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
+  const Span outs[3] = {span2d(h, T, ldh, F, 2), bytes_at(workspace, L.total),
+                        saved != nullptr && T > 0 ? bytes_at(saved, saved_bytes(T, F, s[0].given + s[1].given)) : Span{}};
+  Span ins[9];
+  gated_spans(layer, K, F, s, ins);
+  ins[8] = span2d(x, T, ldx, K, 2);
+  if (clash(outs, ins)) return LORA_ERR_OVERLAP;
+  if (T == 0) return LORA_OK;
+  char* ws = static_cast<char*>(workspace);
+  char* keep = static_cast<char*>(saved);
+  uint16_t* tt = reinterpret_cast<uint16_t*>(saved != nullptr ? keep + saved_tt_at(T, F) : ws + L.tt);
+  return gated_forward(x, T, K, ldx, layer, s, F, act, h, ldh, static_cast<float*>(saved), tt,
+                       reinterpret_cast<float*>(ws + L.part), static_cast<hipStream_t>(stream)) == hipSuccess
+             ? LORA_OK
+             : LORA_ERR_HIP;
+}
+
+int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* layer, int64_t F,
+                   int32_t act, double strength, double request_scale, const void* dh, int64_t lddh, const void* saved,
+                   void* dx, int64_t lddx, void* dA_gate, void* dB_gate, void* dA_up, void* dB_up, int32_t grad_dtype,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  if (T < 0 || K < 1 || F < 1 || ldx < K || lddh < F || (dx != nullptr && lddx < K)) return LORA_ERR_SHAPE;
+  if (int e = check_sizes(T, K, F, ldx, lddh)) return e;
+  if (dx != nullptr && lddx * 2 > kMaxRowBytes) return LORA_ERR_UNSUPPORTED;
+  Side s[2];
+  if (int e = check_gated(layer, T, K, F, act, strength, request_scale, s)) return e;
+  if (T > 0 && (x == nullptr || dh == nullptr)) return LORA_ERR_NULL_PTR;
+  void* grads[2][2] = {{dA_gate, dB_gate}, {dA_up, dB_up}};
+  for (int i = 0; i < 2; ++i)
+    if (s[i].given == 0 && (grads[i][0] != nullptr || grads[i][1] != nullptr)) return LORA_ERR_NULL_PTR;
+  if (!aligned(x, 16) || !aligned(dh, 16) || !aligned(workspace, 16) || !aligned(saved, 16) || !aligned(dx, 2) ||
+      !aligned(dA_gate, 4) || !aligned(dB_gate, 4) || !aligned(dA_up, 4) || !aligned(dB_up, 4) || ldx % 8 != 0 ||
+      lddh % 8 != 0 || F % 8 != 0)
+    return LORA_ERR_ALIGN;
+  const GatedLayout L = T > 0 ? gated_bwd_layout(T, K, F, s[0].given, s[1].given) : GatedLayout{};
+  const size_t need = saved != nullptr ? L.saved : L.total;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return LORA_ERR_WORKSPACE;
+  const int eg = grad_dtype == LORA_F32 ? 4 : 2;
+  Span outs[6] = {span2d(dx, T, lddx, K, 2), bytes_at(workspace, need)};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t na = s[i].given * K, nb = s[i].given * F;
+    outs[2 + 2 * i] = span2d(grads[i][0], 1, na, na, eg);
+    outs[3 + 2 * i] = span2d(grads[i][1], 1, nb, nb, eg);
+  }
+  Span ins[11];
+  gated_spans(layer, K, F, s, ins);
+  ins[8] = span2d(x, T, ldx, K, 2);
+  ins[9] = span2d(dh, T, lddh, F, 2);
+  ins[10] = saved != nullptr && T > 0 ? bytes_at(saved, saved_bytes(T, F, s[0].given + s[1].given)) : Span{};
+  if (clash(outs, ins)) return LORA_ERR_OVERLAP;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  for (int i = 0; i < 2; ++i)
+    if ((T == 0 || s[i].rank == 0) && (zero_grad(grads[i][0], s[i].given * K, grad_dtype, st) != hipSuccess ||
+                                       zero_grad(grads[i][1], s[i].given * F, grad_dtype, st) != hipSuccess))
+      return LORA_ERR_HIP;
+  if (T == 0) return LORA_OK;
+  char* ws = static_cast<char*>(workspace);
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  const char* keep = saved != nullptr ? static_cast<const char*>(saved) : ws + L.saved;
+  if (saved == nullptr) {  // g, u and the rank-wide rows once more
+    const hipError_t e = gated_forward(x, T, K, ldx, layer, s, F, act, nullptr, F, reinterpret_cast<float*>(ws + L.saved),
+                                       reinterpret_cast<uint16_t*>(ws + L.saved + saved_tt_at(T, F)), part, st);
+    if (e != hipSuccess) return LORA_ERR_HIP;
+  }
+  auto* dg = reinterpret_cast<uint16_t*>(ws + L.dg);
+  auto* du = reinterpret_cast<uint16_t*>(ws + L.du);
+  if (lora::launch_gated_grad(reinterpret_cast<const float*>(keep), bf(dh), lddh, T, F, act, dg, du, st) != hipSuccess)
+    return LORA_ERR_HIP;
+  const int64_t R = s[0].rank + s[1].rank, ldt = lora::pair_ld(R);
+  auto* vt = reinterpret_cast<uint16_t*>(ws + L.vt);
+  const bool want_a = dA_gate != nullptr || dA_up != nullptr, want_b = dB_gate != nullptr || dB_up != nullptr;
+  if (R > 0 && (dx != nullptr || want_a)) {  // v = s d B of each projection
+    RankProduct v;
+    std::memset(&v, 0, sizeof(v));
+    v.x[0] = dg; v.x[1] = du; v.ldx = F; v.T = T; v.K = F; v.part = part; v.tt = vt;
+    for (int i = 0; i < 2; ++i) {
+      v.A[i] = bf(s[i].B); v.rank[i] = static_cast<int>(s[i].rank); v.scale[i] = s[i].scale;
+    }
+    if (lora::launch_rank_product(v, true, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (dx != nullptr) {
+    RingArgs g;
+    std::memset(&g, 0, sizeof(g));
+    if (R > 0) {
+      g.tt = vt; g.ldt = ldt;
+      for (int i = 0; i < 2; ++i) {
+        g.E[i] = bf(s[i].A); g.re[i] = static_cast<int>(s[i].rank);
+      }
+    }
+    g.x[0] = dg; g.x[1] = du; g.ldx = F; g.W[0] = bf(layer->W_gate); g.W[1] = bf(layer->W_up); g.K[0] = g.K[1] = F;
+    g.n_seg = 2; g.T = T; g.N = K; g.y = bf(dx); g.ldy = lddx; g.part = part;
+    if (lora::launch_ring(g, true, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (R == 0) return LORA_OK;
+  Contract c;
+  std::memset(&c, 0, sizeof(c));
+  c.T = T; c.ldt = ldt; c.R = static_cast<int>(R); c.out_bf16 = grad_dtype == LORA_BF16; c.part = part;
+  const int r0 = static_cast<int>(s[0].rank), r1 = static_cast<int>(s[1].rank);
+  if (want_b) {  // dB = d^T t of each projection
+    c.M = F; c.tt = reinterpret_cast<const uint16_t*>(keep + saved_tt_at(T, F));
+    c.n_tasks = 0;
+    if (r0 > 0) c.task[c.n_tasks++] = lora::ContractTask{dg, F, 0, r0, {dB_gate, nullptr}, r0};
+    if (r1 > 0) c.task[c.n_tasks++] = lora::ContractTask{du, F, r0, r1, {dB_up, nullptr}, r1};
+    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  if (want_a) {  // dA = v^T x, both projections' rows in one pass over x
+    c.M = K; c.tt = vt; c.transposed = true; c.n_tasks = 1;
+    c.task[0] = lora::ContractTask{bf(x), ldx, 0, r0 + r1, {r0 > 0 ? dA_gate : nullptr, r1 > 0 ? dA_up : nullptr}, r0};
+    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
+  }
+  return LORA_OK;
+}
+
+}  // extern "C"
