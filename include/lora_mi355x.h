@@ -568,7 +568,8 @@ int lora_adamw_step(const lora_adamw_plan_t* plan, double lr, double beta1, doub
  * are fp32, and the same call gives the same bits. An adapter with a combined
  * scale of +-0 is inactive: its gradients are zeros.
  *   grad_dtype  of dA and dB: LORA_F32 or LORA_BF16 (rounded once; 4-byte aligned in both)
- * LORA_ERR_UNSUPPORTED from 2^26 tokens on. T == 0 is a valid call (zero gradients).
+ * LORA_ERR_UNSUPPORTED from 2^21 tokens or 2^35 elements of a [T, K], [T, N] or [T, F] tensor on. T == 0
+ * is a valid call (zero gradients).
  */
 
 /*
@@ -648,6 +649,32 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
 size_t lora_gated_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up);
 size_t lora_gated_saved_size(int64_t T, int64_t F, int32_t rank_gate, int32_t rank_up);
 size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up);
+
+/*
+ * lora_cross_entropy -- softmax cross entropy over a vocabulary from the hidden
+ * states h and the frozen output weight W, and its gradient, in pieces of the
+ * vocabulary: the logits l = h.W^T are never kept.
+ *
+ *     lse = log(sum over v of exp(l_v)),  loss = lse - l_target,
+ *     dh = RN_bf16(dloss . (sum over v != target of p_v W_v - (1 - p_target) W_target)),  p = exp(l - lse)
+ *
+ * Logits and sums are fp32; p_v of a token other than the target is rounded to
+ * bf16 for its product with W, 1 - p_target is the others' fp32 sum.
+ *   h       [T, K] bf16 (ldh), W [V, K] bf16, 16-byte aligned; K and ldh multiples of 8; V <= 2^24
+ *   target  [T] int64 (device). A token whose target is outside [0, V) (-100 by convention) has
+ *           loss 0, its lse all the same, and a zero gradient
+ *   dloss   [T] fp32 (device): the gradient with respect to each token's loss (1 / the number of
+ *           tokens that have one, for their mean), or NULL (1)
+ *   loss, lse [T] fp32, dh [T, K] bf16 (row stride lddh): each optional (NULL = not computed)
+ *   workspace at least lora_cross_entropy_workspace_size(T, K, V, dh != NULL) bytes
+ * A token whose logits are not all finite has a loss, lse and gradient that are not either; no other
+ * token's change. The same call gives the same bits. LORA_ERR_UNSUPPORTED from 2^21 tokens, 2^37 logits
+ * or 2^34 elements of h on.
+ */
+int lora_cross_entropy(const void* h, int64_t T, int64_t K, int64_t ldh, const void* W, int64_t V,
+                       const int64_t* target, const float* dloss, float* loss, float* lse, void* dh, int64_t lddh,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t lora_cross_entropy_workspace_size(int64_t T, int64_t K, int64_t V, int32_t want_grad);
 
 /*
  * Workspace bytes a call with T tokens, K inputs and N outputs needs for

@@ -43,6 +43,7 @@ __all__ = [
     "lora_gated_workspace_size", "lora_gated_saved_size", "lora_gated_bwd_workspace_size", "lora_gated",
     "lora_gated_backward", "lora_linear_dropout_fwd", "lora_linear_dropout_bwd", "lora_linear_dropout_workspace_size",
     "lora_linear_dropout_bwd_workspace_size", "lora_linear_dropout", "lora_linear_dropout_backward",
+    "lora_cross_entropy_fwd", "lora_cross_entropy_workspace_size", "lora_cross_entropy",
     "LoraAdamWTensor", "LoraAdamWPlan", "lora_adamw_table_size", "lora_adamw_plan", "lora_adamw_step", "LoraAdamW",
 ]
 
@@ -167,6 +168,10 @@ for _f in (_lib.lora_linear_dropout_workspace_size, _lib.lora_linear_dropout_bwd
 for _f in (_lib.lora_gated_workspace_size, _lib.lora_gated_bwd_workspace_size):
     _f.argtypes, _f.restype = [_i64, _i64, _i64, _i32, _i32], _sz
 _lib.lora_gated_saved_size.argtypes, _lib.lora_gated_saved_size.restype = [_i64, _i64, _i32, _i32], _sz
+_lib.lora_cross_entropy.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _i64, _p, _sz, _p]
+_lib.lora_cross_entropy.restype = ctypes.c_int
+_lib.lora_cross_entropy_workspace_size.argtypes = [_i64, _i64, _i64, _i32]
+_lib.lora_cross_entropy_workspace_size.restype = _sz
 _lib.lora_adamw_table_size.argtypes = [ctypes.POINTER(LoraAdamWTensor), _i32]
 _lib.lora_adamw_table_size.restype = _sz
 _lib.lora_adamw_plan.argtypes = [ctypes.POINTER(LoraAdamWTensor), _i32, _i32, _i32, _i32, _p, _sz,
@@ -312,6 +317,16 @@ def lora_gated_saved_size(T, F, rank_gate, rank_up) -> int:
 
 def lora_gated_bwd_workspace_size(T, K, F, rank_gate, rank_up) -> int:
     return int(_lib.lora_gated_bwd_workspace_size(T, K, F, rank_gate, rank_up))
+
+
+def lora_cross_entropy_fwd(h, T, K, ldh, W, V, target, dloss, loss, lse, dh, lddh, workspace, workspace_bytes, stream):
+    """C ``lora_cross_entropy`` (the plain name is the tensor-level helper's)."""
+    return _check(_lib.lora_cross_entropy(h, T, K, ldh, W, V, target, dloss, loss, lse, dh, lddh, workspace,
+                                          workspace_bytes, stream), "lora_cross_entropy")
+
+
+def lora_cross_entropy_workspace_size(T, K, V, want_grad=True) -> int:
+    return int(_lib.lora_cross_entropy_workspace_size(T, K, V, 1 if want_grad else 0))
 
 
 def lora_adamw_table_size(tensors) -> int:
@@ -852,6 +867,39 @@ def lora_gated_backward(x, W_gate, W_up, gate, up, dh, b_gate=None, b_up=None, a
                        _ptr(dB_up), _GRAD[grad_dtype], ws.data_ptr(), ws.numel() * ws.element_size(),
                        _stream_on(dev, stream))
     return dx, dA_gate, dB_gate, dA_up, dB_up
+
+
+def lora_cross_entropy(h, W, target, dloss=None, want=("loss", "lse", "dh"), loss=None, lse=None, dh=None,
+                       workspace=None, stream=None):
+    """Softmax cross entropy of hidden states ``h`` [T, K] under the frozen output weight ``W`` [V, K] (bf16), without
+    keeping the logits: returns (loss, lse, dh), each None unless named in ``want`` (loss and lse fp32 [T], dh bf16).
+
+    ``target``: int64 [T]; a token whose target is outside [0, V) (-100, say) has loss 0 and no gradient. ``dloss``:
+    fp32 [T], the gradient with respect to each token's loss (``1 / count`` for their mean), or None for ones: the
+    gradient dh is formed in the same pass as the loss."""
+    dev = h.device
+    if h.dim() != 2 or W.dim() != 2:
+        raise ValueError("h must be [T, K] and W [V, K]")
+    T, K = h.shape
+    V = W.shape[0]
+    ldh = _rows(h, "h", (T, K), dev)
+    _of(W, "W", (V, K), torch.bfloat16, dev)
+    _of(target, "target", (T,), torch.int64, dev)
+    if dloss is not None:
+        _of(dloss, "dloss", (T,), torch.float32, dev)
+    with _on(dev, stream):
+        loss = _grad(loss, "loss", (T,), torch.float32, dev, "loss" in want)
+        lse = _grad(lse, "lse", (T,), torch.float32, dev, "lse" in want)
+        if "dh" not in want:
+            dh = None
+        elif dh is None:
+            dh = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        lddh = _rows(dh, "dh", (T, K), dev) if dh is not None else K
+        ws = _bytes_on(workspace, lora_cross_entropy_workspace_size, (T, K, V, dh is not None), dev)
+        lora_cross_entropy_fwd(h.data_ptr(), T, K, ldh, W.data_ptr(), V, target.data_ptr(), _ptr(dloss), _ptr(loss),
+                               _ptr(lse), _ptr(dh), lddh, ws.data_ptr(), ws.numel() * ws.element_size(),
+                               _stream_on(dev, stream))
+    return loss, lse, dh
 
 
 class LoraAdamW:

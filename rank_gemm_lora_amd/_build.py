@@ -35,6 +35,7 @@ SOURCES = {
     "probe.hip": [],
     "noalloc.hip": [],
     "step.hip": [],
+    "loss.hip": [],
     "step_api.cpp": [],
     "routed.hip": [],
     "routed_api.cpp": [],

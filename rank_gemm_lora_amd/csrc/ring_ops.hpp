@@ -1,0 +1,203 @@
+// Operands of the ring GEMMs of a fine-tuning step (ring16.hpp runs the loop), and what their epilogues share.
+#pragma once
+
+#include "ring16.hpp"
+#include "step.hpp"
+
+namespace lora {
+namespace {
+using namespace pipe;
+
+// NT: rows of outputs. DUAL: the tile's rows are blocks of 16 gate rows and 16 up rows in turn, so that a lane holds the
+// gate and the up value of the same four outputs in acc[2 i] and acc[2 i + 1]; a copy instruction's 8 rows then belong
+// to one projection, the same for all of a wave's (waves 0 and 1 copy gate rows, 2 and 3 up rows).
+template <class P, bool DUAL>
+struct NtOp {
+  __amdgpu_buffer_rsrc_t xr, wr, xm, tr, wm, br;
+  uint32_t ldx_b, ldw_b, ldt_b, ldb_b, ax, aw, c16;
+  int NE, hi, seg, kb_total, rows_m, rows_n, per, ph0, ph1, lo;
+  NtRows<P> vx, vw;
+  __device__ __forceinline__ void init(const RingArgs& p, int64_t m0, int64_t n0, int s_lo, int s_hi) {
+    const int side = DUAL ? ring_wave() >> 1 : 0;
+    rows_m = static_cast<int>(min<int64_t>(P::BM, p.T - m0));
+    rows_n = static_cast<int>(min<int64_t>(DUAL ? P::BN / 2 : P::BN, p.N - n0));
+    kb_total = static_cast<int>(p.K[0] * 2);
+    ldx_b = static_cast<uint32_t>(p.ldx * 2);
+    ldw_b = static_cast<uint32_t>(p.K[0] * 2);
+    ldt_b = static_cast<uint32_t>(p.ldt * 2);
+    ldb_b = static_cast<uint32_t>(p.re[side] * 2);
+    xm = make_rsrc(p.x[0] + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+    wm = make_rsrc(p.W[side] + n0 * p.K[0], static_cast<uint32_t>(rows_n) * ldw_b);
+    tr = make_rsrc(p.tt + m0 * p.ldt, static_cast<uint32_t>(rows_m) * ldt_b);
+    br = make_rsrc(p.E[side] + n0 * p.re[side], static_cast<uint32_t>(rows_n) * ldb_b);
+    NE = p.tt != nullptr ? static_cast<int>(p.ldt / 64) : 0;
+    per = (p.re[0] + p.re[1]) * 2;  // bytes of a term's columns; this side's are [ph0, ph1) of them
+    ph0 = side ? p.re[0] * 2 : 0;
+    ph1 = ph0 + p.re[side] * 2;
+    c16 = ring_chunk<P>();
+    lo = s_lo;
+    hi = s_hi;
+    seg = -1;
+  }
+  __device__ __forceinline__ void w_rows(uint32_t ld) {
+    if constexpr (!DUAL) vw.init(ld, rows_n);
+    else {
+      const int lane = opaque_int(threadIdx.x & 63);
+      const int r0 = (ring_wave() & 1) * 8 + (lane >> 3);
+#pragma unroll
+      for (int l = 0; l < NtRows<P>::N; ++l) {
+        const int row = l * 16 + r0;
+        vw.v[l] = row < rows_n ? static_cast<uint32_t>(row) * ld + c16 : kMissing;
+      }
+    }
+  }
+  __device__ __forceinline__ void seek(int t) {
+    const int s = lo + t;
+    if (s < NE && s < hi) {
+      if (seg != 0) {
+        seg = 0;
+        xr = tr;
+        wr = br;
+        vx.init(ldt_b, rows_m);
+        w_rows(ldb_b);
+      }
+      ax = static_cast<uint32_t>(s) * 128u;
+      const int b = s * 128 + static_cast<int>(c16), ph = b < per ? b : b - per;
+      aw = b < 2 * per && ph >= ph0 && ph < ph1 ? static_cast<uint32_t>(ph - ph0) - c16 : kMissing;
+    } else {
+      if (seg != 1) {
+        seg = 1;
+        xr = xm;
+        wr = wm;
+        vx.init(ldx_b, rows_m);
+        w_rows(ldw_b);
+      }
+      const int kb = (s - NE) * 128;
+      ax = aw = s < hi && kb + static_cast<int>(c16) < kb_total ? static_cast<uint32_t>(kb) : kMissing;
+    }
+  }
+  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
+  __device__ __forceinline__ void load_w(int l, char* d) const { ring_copy<P>(l, d, wr, vw.v[l] + aw); }
+  __device__ __forceinline__ void before(int, f32x4 (&)[P::NI][P::NJ]) const {}
+};
+
+// NN: rows of the contraction. Extension rows are the adapters' A rows, once for each term; a copy instruction's rows
+// (2 or 4 of 8 consecutive ones) belong to one adapter.
+template <class P>
+struct NnOp {
+  const uint16_t *x[2], *W[2], *E[2];
+  const uint16_t* tt;
+  __amdgpu_buffer_rsrc_t xr, wr, er0, er1;
+  uint32_t ldx_b, ldw_b, ldt_b, ax, c16;
+  int64_t ldw;
+  int K[2], re0, per, NE, n0s, hi, seg, rows_m, cols, lo, second;
+  NtRows<P> vx;
+  NnRows<P> vw;
+  // x_i [T, K_i] (from row m0 on), W_i [K_i, N], E_i [re_i, N] (columns from n0 on)
+  __device__ __forceinline__ void init(const uint16_t* const* xs, int64_t ldx, const uint16_t* const* Ws, const int64_t* Ks,
+                                       int n_seg, const uint16_t* tt_, int64_t ldt, const uint16_t* const* Es,
+                                       const int* re, int64_t T, int64_t N, int64_t m0, int64_t n0, int s_lo, int s_hi) {
+    rows_m = static_cast<int>(min<int64_t>(P::BM, T - m0));
+    cols = static_cast<int>(min<int64_t>(P::BN, N - n0));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool on = i < n_seg;
+      x[i] = on ? xs[i] + m0 * ldx : nullptr;
+      W[i] = on ? Ws[i] + n0 : nullptr;
+      K[i] = on ? static_cast<int>(Ks[i]) : 0;
+      E[i] = Es[i] + n0;
+    }
+    ldx_b = static_cast<uint32_t>(ldx * 2);
+    ldt_b = static_cast<uint32_t>(ldt * 2);
+    ldw = N;
+    ldw_b = static_cast<uint32_t>(N * 2);
+    tt = tt_ + m0 * ldt;
+    NE = tt_ != nullptr ? static_cast<int>(ldt / 64) : 0;
+    re0 = re[0];
+    per = re[0] + re[1];
+    er0 = make_rsrc(E[0], re[0] > 0 ? static_cast<uint32_t>(re[0] - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    er1 = make_rsrc(E[1], re[1] > 0 ? static_cast<uint32_t>(re[1] - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    n0s = (K[0] + 63) / 64;
+    c16 = ring_chunk<P>();
+    lo = s_lo;
+    hi = s_hi;
+    seg = -1;
+    second = 0;
+  }
+  __device__ __forceinline__ void seek(int t) {
+    const int s = lo + t;
+    if (s < NE && s < hi) {
+      if (seg != 0) {
+        xr = make_rsrc(tt, static_cast<uint32_t>(rows_m) * ldt_b);
+        vx.init(ldt_b, rows_m);
+      }
+      seg = 0;
+      ax = static_cast<uint32_t>(s) * 128u;
+      vw.init(0u, cols);  // (the columns' part; missing ones keep kMissing)
+      second = 0;
+#pragma unroll
+      for (int l = 0; l < NnRows<P>::N; ++l) {
+        const int vr = s * 64 + vw.row[l], ph = vr < per ? vr : vr - per;
+        const bool is2 = ph >= re0;
+        vw.v[l] = vr < 2 * per ? vw.v[l] + static_cast<uint32_t>(is2 ? ph - re0 : ph) * ldw_b : kMissing;
+        second |= (__builtin_amdgcn_readfirstlane(is2 ? 1 : 0)) << l;
+      }
+    } else {
+      const int ms = s - NE;
+      const int sg = ms < n0s ? 1 : 2;
+      if (seg != sg) {
+        if (seg < 1) {
+          vx.init(ldx_b, rows_m);
+          vw.init(ldw_b, cols);
+        }
+        seg = sg;
+        xr = make_rsrc(x[sg - 1], static_cast<uint32_t>(rows_m) * ldx_b);
+        second = 0;
+      }
+      const int k0 = (sg == 1 ? ms : ms - n0s) * 64;
+      const int left = s < hi ? min(64, K[sg - 1] - k0) : 0;
+      ax = static_cast<int>(c16) < left * 2 ? static_cast<uint32_t>(k0) * 2u : kMissing;
+      wr = make_rsrc(W[sg - 1] + (left > 0 ? static_cast<int64_t>(k0) * ldw : 0),
+                     left > 0 ? static_cast<uint32_t>(left - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+    }
+  }
+  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
+  __device__ __forceinline__ void load_w(int l, char* d) const {
+    if (seg == 0) ring_copy<P>(l, d, (second >> l) & 1 ? er1 : er0, vw.v[l]);
+    else ring_copy<P>(l, d, wr, vw.v[l]);
+  }
+  __device__ __forceinline__ void before(int, f32x4 (&)[P::NI][P::NJ]) const {}
+};
+
+// Partial sums of a wave's block (add: added to those that are there).
+template <class P>
+__device__ __forceinline__ void store_part(const f32x4 (&acc)[P::NI][P::NJ], float* part, int64_t ld, int64_t m0,
+                                           int64_t n0, int64_t T, int64_t N, bool add = false) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < P::NJ; ++j) {
+    const int64_t m = m0 + j * 16 + r;
+    if (m >= T) continue;
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i) {
+      const int64_t n = n0 + i * 16 + q * 4;
+      float* dst = part + m * ld + n;
+      if (ld % 4 == 0 && n + 3 < N) {
+        f32x4* at = reinterpret_cast<f32x4*>(dst);
+        *at = add ? *at + acc[i][j] : acc[i][j];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) dst[e] = add ? dst[e] + acc[i][j][e] : acc[i][j][e];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void load_bias4(float (&bv)[4], const uint16_t* bias, int64_t n, int64_t N) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) bv[e] = bias != nullptr && n + e < N ? bf16_to_f32(bias[n + e]) : 0.f;
+}
+
+}  // namespace
+}  // namespace lora

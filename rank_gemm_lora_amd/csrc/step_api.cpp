@@ -10,6 +10,7 @@
 #include "backward.hpp"
 #include "checks.hpp"
 #include "lora_mi355x.h"
+#include "loss.hpp"
 #include "step.hpp"
 
 namespace {
@@ -25,7 +26,8 @@ using lora::round_up;
 using lora::Span;
 using lora::span2d;
 
-constexpr int64_t kMaxTokens = int64_t(1) << 26;
+// (a launch has at most 2^32 threads, one for 4 elements of the rank-wide rows, of which 2048 ranks have 4096)
+constexpr int64_t kMaxTokens = int64_t(1) << 21;
 
 struct Take {  // regions of a workspace, each 256-byte aligned
   size_t off = 0;
@@ -63,6 +65,8 @@ int make_side(Side& s, const void* A, const void* B, int32_t rank, double alpha,
 int check_sizes(int64_t T, int64_t K, int64_t N, int64_t ld0, int64_t ld1) {
   if (T >= kMaxTokens || K * 4 > kMaxRowBytes || N * 4 > kMaxRowBytes || ld0 * 2 > kMaxRowBytes || ld1 * 2 > kMaxRowBytes)
     return LORA_ERR_UNSUPPORTED;
+  // (a launch has at most 2^32 threads, one for 16 elements of [T, N] in the widest)
+  if (T * std::max(K, N) >= int64_t(1) << 35) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 
@@ -512,6 +516,81 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
     if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
   }
   return LORA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------- vocabulary loss
+
+namespace {
+
+struct LossLayout {
+  size_t m = 0, s = 0, tl = 0, lse = 0, rest = 0, share = 0, acc = 0, total = 0;
+  int64_t piece = 0;
+};
+
+LossLayout loss_layout(int64_t T, int64_t K, int64_t V, bool grad) {
+  LossLayout L;
+  Take take;
+  const size_t blocks = static_cast<size_t>(lora::loss_blocks(V)) * T * 4, tok = static_cast<size_t>(T) * 4;
+  L.m = take(blocks);
+  L.s = take(blocks);
+  L.tl = take(tok);
+  L.lse = take(tok);
+  L.rest = take(tok);
+  if (grad) {
+    L.piece = lora::loss_piece(T, V);
+    L.share = take(static_cast<size_t>(T) * L.piece * 2);
+    L.acc = take(lora::loss_acc_bytes(T, K, L.piece));
+  }
+  L.total = take.off;
+  return L;
+}
+
+constexpr int64_t kMaxVocab = int64_t(1) << 24;
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_cross_entropy_workspace_size(int64_t T, int64_t K, int64_t V, int32_t want_grad) {
+  if (T <= 0 || K <= 0 || V <= 0 || T >= kMaxTokens || V > kMaxVocab) return 0;
+  return loss_layout(T, K, V, want_grad != 0).total;
+}
+
+int lora_cross_entropy(const void* h, int64_t T, int64_t K, int64_t ldh, const void* W, int64_t V, const int64_t* target,
+                       const float* dloss, float* loss, float* lse, void* dh, int64_t lddh, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (T < 0 || K < 1 || V < 1 || ldh < K || (dh != nullptr && lddh < K)) return LORA_ERR_SHAPE;
+  if (int e = check_sizes(T, K, 1, ldh, dh != nullptr ? lddh : 0)) return e;
+  // (launches of at most 2^32 threads: one for 4 elements of dh, and 256 for 128 x 128 logits)
+  if (V > kMaxVocab || T * V >= int64_t(1) << 37 || T * K >= int64_t(1) << 34) return LORA_ERR_UNSUPPORTED;
+  if (W == nullptr || (T > 0 && (h == nullptr || target == nullptr))) return LORA_ERR_NULL_PTR;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(workspace, 16) || !aligned(target, 8) || !aligned(dloss, 4) ||
+      !aligned(loss, 4) || !aligned(lse, 4) || !aligned(dh, 2) || K % 8 != 0 || ldh % 8 != 0)
+    return LORA_ERR_ALIGN;
+  const LossLayout L = T > 0 ? loss_layout(T, K, V, dh != nullptr) : LossLayout{};
+  if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
+  const Span outs[4] = {span2d(loss, 1, T, T, 4), span2d(lse, 1, T, T, 4), span2d(dh, T, lddh, K, 2),
+                        bytes_at(workspace, L.total)};
+  const Span ins[4] = {span2d(h, T, ldh, K, 2), span2d(W, V, K, K, 2), span2d(target, 1, T, T, 8),
+                       span2d(dloss, 1, T, T, 4)};
+  if (clash(outs, ins)) return LORA_ERR_OVERLAP;
+  if (T == 0 || (loss == nullptr && lse == nullptr && dh == nullptr)) return LORA_OK;
+  char* ws = static_cast<char*>(workspace);
+  lora::VocabLoss p;
+  std::memset(&p, 0, sizeof(p));
+  p.h = bf(h); p.ldh = ldh; p.W = bf(W); p.target = target; p.dloss = dloss; p.T = T; p.K = K; p.V = V;
+  p.loss = loss; p.lse = lse; p.dh = bf(dh); p.lddh = lddh;
+  p.stat_m = reinterpret_cast<float*>(ws + L.m);
+  p.stat_s = reinterpret_cast<float*>(ws + L.s);
+  p.tlogit = reinterpret_cast<float*>(ws + L.tl);
+  p.wlse = reinterpret_cast<float*>(ws + L.lse);
+  p.rest = reinterpret_cast<float*>(ws + L.rest);
+  p.share = reinterpret_cast<uint16_t*>(ws + L.share);
+  p.piece = L.piece;
+  p.acc = reinterpret_cast<float*>(ws + L.acc);
+  return lora::launch_vocab_loss(p, static_cast<hipStream_t>(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
 }  // extern "C"

@@ -45,7 +45,7 @@ def drop_bwd(**kw):
 BOTH = [
     (dict(x=None), NULL), (dict(A=None, B=None), NULL), (dict(A=None), NULL), (dict(B=None), NULL), (dict(W=None), NULL),
     (dict(T=-1), SHAPE), (dict(K=0), SHAPE), (dict(N=0), SHAPE), (dict(ldx=255), SHAPE), (dict(rank=0), SHAPE),
-    (dict(rank=1032), UNSUP), (dict(T=1 << 26), UNSUP), (dict(K=1 << 21, ldx=1 << 21, lddx=1 << 21), UNSUP),
+    (dict(rank=1032), UNSUP), (dict(T=1 << 21), UNSUP), (dict(K=1 << 21, ldx=1 << 21, lddx=1 << 21), UNSUP),
     (dict(p=-0.1), UNSUP), (dict(p=1.0), UNSUP), (dict(p=0.999999), UNSUP),
     (dict(p=NAN), NONFIN), (dict(alpha=INF), NONFIN), (dict(strength=NAN), NONFIN), (dict(request=INF), NONFIN),
     (dict(alpha=1e300), NONFIN),
@@ -98,7 +98,7 @@ GATED_BOTH = [
     (dict(layer=False), NULL), (dict(x=None), NULL), (dict(Wg=None), NULL), (dict(Wu=None), NULL), (dict(Ag=None), NULL),
     (dict(Bu=None), NULL),
     (dict(T=-1), SHAPE), (dict(K=0), SHAPE), (dict(F=0), SHAPE), (dict(ldx=100), SHAPE), (dict(rg=0), SHAPE),
-    (dict(ru=-8), SHAPE), (dict(ru=1032), UNSUP), (dict(act=3), UNSUP), (dict(act=-1), UNSUP), (dict(T=1 << 26), UNSUP),
+    (dict(ru=-8), SHAPE), (dict(ru=1032), UNSUP), (dict(act=3), UNSUP), (dict(act=-1), UNSUP), (dict(T=1 << 21), UNSUP),
     (dict(strength=NAN), NONFIN), (dict(alu=INF), NONFIN), (dict(alg=1e300), NONFIN), (dict(request=-INF), NONFIN),
     (dict(rg=12), ALIGN), (dict(K=252, ldx=256), ALIGN), (dict(ldx=260), ALIGN), (dict(Wu=BASE * 11 + 8), ALIGN),
     (dict(x=BASE + 2), ALIGN), (dict(bg=BASE + 1), ALIGN), (dict(saved=BASE * 20 + 8), ALIGN), (dict(ws=BASE * 9 + 8), ALIGN),
@@ -129,7 +129,7 @@ def test_workspace_sizes():
     d, db = rg.lora_linear_dropout_workspace_size, rg.lora_linear_dropout_bwd_workspace_size
     g, gb, gs = rg.lora_gated_workspace_size, rg.lora_gated_bwd_workspace_size, rg.lora_gated_saved_size
     assert d(0, 64, 64, 8) == 0 and db(5, 0, 64, 8) == 0 and g(0, 64, 64, 8, 8) == 0 and gs(0, 64, 8, 8) == 0
-    assert d(1 << 26, 64, 64, 8) == 0 and gb(1 << 26, 64, 64, 8, 8) == 0
+    assert d(1 << 21, 64, 64, 8) == 0 and gb(1 << 21, 64, 64, 8, 8) == 0
     for T in (1, 65, 5000):
         assert 0 < d(T, 512, 256, 16) <= db(T, 512, 256, 16)
         assert g(T, 512, 256, 0, 0) == 0 < g(T, 512, 256, 16, 8) <= gb(T, 512, 256, 16, 8)
