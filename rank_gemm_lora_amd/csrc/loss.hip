@@ -28,7 +28,7 @@ template <class P, int MODE>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void logits_kernel(VocabLoss p, int64_t v0, int64_t cols, int mt, int nt) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
   const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
-  const int wave = ring_wave(), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * P::BN;
   const int NS = static_cast<int>((p.K + 63) / 64);
@@ -38,6 +38,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void logits_kernel(VocabLoss p,
   NtOp<P, false> op;
   op.init(g, m0, n0, 0, NS);
   ring_run<P, false>(acc, op, NS, smem, wm0, wn0);
+  const int lane = opaque_int(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
   const int64_t mw = m0 + wm0, nw = n0 + wn0;  // of this wave's block (columns within the piece)
   if (nw >= cols) return;
   const int left = static_cast<int>(min<int64_t>(P::WN, cols - nw));
@@ -150,11 +151,9 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void dh_kernel(VocabLoss p, int
   const int NS = static_cast<int>((cols + 63) / 64), s_lo = static_cast<int>(blockIdx.y) * ks, s_hi = min(NS, s_lo + ks);
   float* mine = p.acc + static_cast<int64_t>(blockIdx.y) * p.T * p.K;
   if (s_lo >= s_hi && !first) return;
-  const uint16_t *xs[2] = {p.share, nullptr}, *Ws[2] = {p.W + v0 * p.K, nullptr}, *Es[2] = {nullptr, nullptr};
-  const int64_t Ks[2] = {cols, 0};
-  const int re[2] = {0, 0};
-  NnOp<P> op;
-  op.init(xs, p.piece, Ws, Ks, 1, nullptr, 0, Es, re, p.T, p.K, m0, n0, s_lo, s_hi);
+  const uint16_t *x = p.share, *W = p.W + v0 * p.K;
+  NnOp<P, 1, 0> op;
+  op.init(&x, p.piece, &W, &cols, p.T, p.K, m0, n0, s_lo, s_hi);
   f32x4 acc[P::NI][P::NJ];
   ring_run<P, true>(acc, op, max(0, s_hi - s_lo), smem, wm0, wn0);
   store_part<P>(acc, mine, p.K, m0 + wm0, n0 + wn0, p.T, p.K, !first);

@@ -16,7 +16,7 @@
 //                                  form and its wait counts are constant)
 //   void load_x(int l, char* dst)  copy instruction l of NL of the x unit, and of the W unit
 //   void load_w(int l, char* dst)
-//   void before(int t, acc)        runs before the MFMAs of stage t
+//   void between(acc)              (with SPLIT) runs once, before a named stage
 #pragma once
 
 #include "pipe_dev.hpp"
@@ -79,7 +79,9 @@ struct NnRows {
   static constexpr int N = ring_loads<P>();
   static constexpr int LPR = P::BN * 2 / 16;  // lanes (16-byte pieces) per row
   uint32_t v[N];
-  int row[N];
+  __device__ __forceinline__ static int row(int l) {
+    return ((l * P::WAVES + ring_wave()) * 64 + opaque_int(threadIdx.x & 63)) / LPR;
+  }
   __device__ __forceinline__ void init(uint32_t ld_bytes, int cols_valid) {
     const int lane = opaque_int(threadIdx.x & 63);
 #pragma unroll
@@ -88,7 +90,6 @@ struct NnRows {
       const int k = sl / LPR, p = sl % LPR;
       const int f = (k & 3) | (((k >> 3) & 1) << 2);
       const int col = (((p >> 1) ^ f) * 2 + (p & 1)) * 8;
-      row[l] = k;
       v[l] = col < cols_valid ? static_cast<uint32_t>(k) * ld_bytes + static_cast<uint32_t>(col) * 2 : kMissing;
     }
   }
@@ -121,16 +122,74 @@ struct RingFrags {
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
+  // fragment f of k-step kk, in order of first use: a0, b0 .. b(NJ-1), a1 .. a(NI-1)
+  __device__ __forceinline__ void read(Frags16<P>& d, int f, const char* xs, const char* ws, int kk) const {
+    if (f == 0 || f > P::NJ) {
+      const int ia = f == 0 ? 0 : f - P::NJ;
+      d.a[ia] = read_w(ws, ia, kk);
+    } else {
+      d.b[f - 1] = read_x(xs, f - 1, kk);
+    }
+  }
 };
 
-// The loop. Behind it the LDS is free (every copy has landed, every wave has read its last fragments).
-// (Schedule as the hot GEMM's: x of stage t + 2 is copied beside k-step 0, W beside k-step 1, into the slots that the
-// barriers of stages t - 1 and t release; the wait of stage t leaves the x copies of stage t + 2 in flight.)
+// One stage: its MFMAs, the fragment reads of its second k-step and of the next stage's first, the copies of stage t + 2.
+// (ws and ws2 are restrict: nothing copies into the W slots that are read here, and without the compiler's knowing so it
+// waits for every copy in flight before each transposing read.)
 template <class P, bool NN, class Op>
-__device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int NS, char* smem, int wm0, int wn0) {
-  static_assert(P::WAVES == 4, "schedule written for 4 waves");
+__device__ __forceinline__ void ring_stage(f32x4 (&acc)[P::NI][P::NJ], Frags16<P> (&fr)[2], const Op& op,
+                                           const RingFrags<P, NN>& rf, const char* xs, const char* __restrict__ ws,
+                                           const char* xs2, const char* __restrict__ ws2, char* xdst, char* wdst) {
   constexpr int NL = ring_loads<P>(), NB = P::NI * P::NJ, RS = NB / (P::NI + P::NJ), LS = NB / NL;
   static_assert(NB % (P::NI + P::NJ) == 0 && NB % NL == 0 && LS % 2 == 0 && RS >= 2, "bundle schedule");
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int m = 0; m < NB; ++m) {
+    const int i = m / P::NJ, j = m % P::NJ;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[0].a[i], fr[0].b[j], acc[i][j], 0, 0, 0);
+    if (m % RS == 0) rf.read(fr[1], m / RS, xs, ws, 1);
+    if (m % LS == LS / 2) op.load_x(m / LS, xdst);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int m = 0; m < NB; ++m) {
+    const int i = m / P::NJ, j = m % P::NJ;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[1].a[i], fr[1].b[j], acc[i][j], 0, 0, 0);
+    if (m == 0) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL));
+      stage_barrier();  // stage t + 1 landed and visible; every wave is done reading stage t
+    } else if (m % RS == 1) {
+      rf.read(fr[0], m / RS, xs2, ws2, 0);
+    }
+    if (m % LS == LS / 2) op.load_w(m / LS, wdst);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The larger tile's accumulators fill the accumulation registers, all of them: what reads them behind the loop (an
+// epilogue with more values of its own) else moves some to others within it.
+template <class P>
+__device__ __forceinline__ void keep_acc(f32x4 (&acc)[P::NI][P::NJ]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (P::BM == 256) {
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i)
+#pragma unroll
+      for (int j = 0; j < P::NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+  }
+#endif
+}
+
+// The loop. Behind it the LDS is free (every copy has landed, every wave has read its last fragments). With SPLIT,
+// op.between(acc) runs before stage `at` (0 < at; not at all where at >= NS).
+// (Schedule as the hot GEMM's: x of stage t + 2 is copied beside k-step 0, W beside k-step 1, into the slots that the
+// barriers of stages t - 1 and t release; the wait of stage t leaves the x copies of stage t + 2 in flight.)
+template <class P, bool NN, bool SPLIT = false, class Op>
+__device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int NS, char* smem, int wm0, int wn0,
+                                         int at = 0) {
+  static_assert(P::WAVES == 4, "schedule written for 4 waves");
+  constexpr int NL = ring_loads<P>();
 #pragma unroll
   for (int i = 0; i < P::NI; ++i)
 #pragma unroll
@@ -150,56 +209,29 @@ __device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int
   RingFrags<P, NN> rf;
   rf.init(wm0, wn0);
   Frags16<P> fr[2];
-  // fragment f of a k-step, in order of first use: a0, b0 .. b(NJ-1), a1 .. a(NI-1)
-  auto read_frag = [&](Frags16<P>& d, int f, const char* xs, const char* ws, int kk) {
-    if (f == 0 || f > P::NJ) {
-      const int ia = f == 0 ? 0 : f - P::NJ;
-      d.a[ia] = rf.read_w(ws, ia, kk);
-    } else {
-      d.b[f - 1] = rf.read_x(xs, f - 1, kk);
-    }
-  };
-#pragma unroll
-  for (int f = 0; f < P::NI + P::NJ; ++f) read_frag(fr[0], f, smem, smem + P::SLOT_BYTES, 0);
   int a = 0;  // slot of x of stage t
-  for (int t = 0; t < NS; ++t) {
-    op.before(t, acc);
-    op.seek(t + 2);
-    const int b1 = a == 4 ? 0 : a + 1;      // W of stage t
-    const int a2 = a >= 3 ? a - 3 : a + 2;  // x of stage t + 1
-    const int b2 = a2 == 4 ? 0 : a2 + 1;    // W of stage t + 1
-    const int a3 = b2 == 4 ? 0 : b2 + 1;    // x of stage t + 2
-    const char* xs = smem + a * P::SLOT_BYTES;
-    const char* ws = smem + b1 * P::SLOT_BYTES;
-    const char* xs2 = smem + a2 * P::SLOT_BYTES;
-    const char* ws2 = smem + b2 * P::SLOT_BYTES;
-    char* const xdst = smem + a3 * P::SLOT_BYTES;
-    char* const wdst = smem + a * P::SLOT_BYTES;
-    __builtin_amdgcn_sched_barrier(0);
+  int t = 0;
+  auto after = [](int slot) { return slot == 4 ? 0 : slot + 1; };
+  auto run = [&](int end) {
 #pragma unroll
-    for (int m = 0; m < NB; ++m) {
-      const int i = m / P::NJ, j = m % P::NJ;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[0].a[i], fr[0].b[j], acc[i][j], 0, 0, 0);
-      if (m % RS == 0) read_frag(fr[1], m / RS, xs, ws, 1);
-      if (m % LS == LS / 2) op.load_x(m / LS, xdst);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int f = 0; f < P::NI + P::NJ; ++f)
+      rf.read(fr[0], f, smem + a * P::SLOT_BYTES, smem + after(a) * P::SLOT_BYTES, 0);
+    for (; t < end; ++t) {
+      op.seek(t + 2);
+      const int b1 = after(a), a2 = after(b1), b2 = after(a2), a3 = after(b2);  // W of t; x, W of t + 1; x of t + 2
+      ring_stage<P, NN>(acc, fr, op, rf, smem + a * P::SLOT_BYTES, smem + b1 * P::SLOT_BYTES, smem + a2 * P::SLOT_BYTES,
+                        smem + b2 * P::SLOT_BYTES, smem + a3 * P::SLOT_BYTES, smem + a * P::SLOT_BYTES);
+      a = a2;
     }
-#pragma unroll
-    for (int m = 0; m < NB; ++m) {
-      const int i = m / P::NJ, j = m % P::NJ;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[1].a[i], fr[1].b[j], acc[i][j], 0, 0, 0);
-      if (m == 0) {
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(NL));
-        stage_barrier();  // stage t + 1 landed and visible; every wave is done reading stage t
-      } else if (m % RS == 1) {
-        read_frag(fr[0], m / RS, xs2, ws2, 0);
-      }
-      if (m % LS == LS / 2) op.load_w(m / LS, wdst);
-      __builtin_amdgcn_sched_barrier(0);
+    keep_acc<P>(acc);
+  };
+  if constexpr (SPLIT) {
+    if (at > 0 && at < NS) {
+      run(at);
+      op.between(acc);
     }
-    a = a2;
   }
+  run(NS);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   __syncthreads();
 }

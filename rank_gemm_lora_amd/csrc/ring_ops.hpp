@@ -78,58 +78,65 @@ struct NtOp {
   }
   __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
   __device__ __forceinline__ void load_w(int l, char* d) const { ring_copy<P>(l, d, wr, vw.v[l] + aw); }
-  __device__ __forceinline__ void before(int, f32x4 (&)[P::NI][P::NJ]) const {}
 };
 
-// NN: rows of the contraction. Extension rows are the adapters' A rows, once for each term; a copy instruction's rows
-// (2 or 4 of 8 consecutive ones) belong to one adapter.
-template <class P>
+// NN: rows of the contraction: NSEG segments x_i . W_i behind an extension of NEXT adapters. Extension rows are the
+// adapters' A rows, once for each term; a copy instruction's rows (2 or 4 of 8 consecutive ones) belong to one adapter.
+// (What a form does not have is no member of it: scalar registers run out otherwise, and spill into vector ones.)
+template <class P, int NSEG, int NEXT>
 struct NnOp {
-  const uint16_t *x[2], *W[2], *E[2];
+  const uint16_t *x0, *x1, *W0, *W1;
   const uint16_t* tt;
-  __amdgpu_buffer_rsrc_t xr, wr, er0, er1;
+  __amdgpu_buffer_rsrc_t xr, wr, wr2, er0, er1;
   uint32_t ldx_b, ldw_b, ldt_b, ax, c16;
-  int64_t ldw;
-  int K[2], re0, per, NE, n0s, hi, seg, rows_m, cols, lo, second;
+  int K0, K1, re0, per, NE, n0s, hi, seg, rows_m, cols, lo;
+  uint32_t second;  // bit l: copy instruction l takes the second adapter's rows (wr2)
   NtRows<P> vx;
   NnRows<P> vw;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint16_t* base, int rows) const {
+    return make_rsrc(base, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+  }
   // x_i [T, K_i] (from row m0 on), W_i [K_i, N], E_i [re_i, N] (columns from n0 on)
   __device__ __forceinline__ void init(const uint16_t* const* xs, int64_t ldx, const uint16_t* const* Ws, const int64_t* Ks,
-                                       int n_seg, const uint16_t* tt_, int64_t ldt, const uint16_t* const* Es,
-                                       const int* re, int64_t T, int64_t N, int64_t m0, int64_t n0, int s_lo, int s_hi) {
+                                       int64_t T, int64_t N, int64_t m0, int64_t n0, int s_lo, int s_hi) {
     rows_m = static_cast<int>(min<int64_t>(P::BM, T - m0));
     cols = static_cast<int>(min<int64_t>(P::BN, N - n0));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool on = i < n_seg;
-      x[i] = on ? xs[i] + m0 * ldx : nullptr;
-      W[i] = on ? Ws[i] + n0 : nullptr;
-      K[i] = on ? static_cast<int>(Ks[i]) : 0;
-      E[i] = Es[i] + n0;
+    x0 = xs[0] + m0 * ldx;
+    W0 = Ws[0] + n0;
+    K0 = static_cast<int>(Ks[0]);
+    if constexpr (NSEG > 1) {
+      x1 = xs[1] + m0 * ldx;
+      W1 = Ws[1] + n0;
+      K1 = static_cast<int>(Ks[1]);
     }
     ldx_b = static_cast<uint32_t>(ldx * 2);
-    ldt_b = static_cast<uint32_t>(ldt * 2);
-    ldw = N;
     ldw_b = static_cast<uint32_t>(N * 2);
-    tt = tt_ + m0 * ldt;
-    NE = tt_ != nullptr ? static_cast<int>(ldt / 64) : 0;
-    re0 = re[0];
-    per = re[0] + re[1];
-    er0 = make_rsrc(E[0], re[0] > 0 ? static_cast<uint32_t>(re[0] - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
-    er1 = make_rsrc(E[1], re[1] > 0 ? static_cast<uint32_t>(re[1] - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
-    n0s = (K[0] + 63) / 64;
+    n0s = (K0 + 63) / 64;
     c16 = ring_chunk<P>();
+    NE = 0;
     lo = s_lo;
     hi = s_hi;
     seg = -1;
     second = 0;
   }
+  __device__ __forceinline__ void extend(const RingArgs& p, int64_t m0, int64_t n0) {
+    if (p.tt == nullptr) return;
+    tt = p.tt + m0 * p.ldt;
+    ldt_b = static_cast<uint32_t>(p.ldt * 2);
+    NE = static_cast<int>(p.ldt / 64);
+    re0 = p.re[0];
+    per = p.re[0] + (NEXT > 1 ? p.re[1] : 0);
+    er0 = rows_of(p.E[0] + n0, p.re[0]);
+    if constexpr (NEXT > 1) er1 = rows_of(p.E[1] + n0, p.re[1]);
+  }
   __device__ __forceinline__ void seek(int t) {
     const int s = lo + t;
-    if (s < NE && s < hi) {
+    if (NEXT > 0 && s < NE && s < hi) {
       if (seg != 0) {
         xr = make_rsrc(tt, static_cast<uint32_t>(rows_m) * ldt_b);
         vx.init(ldt_b, rows_m);
+        wr = er0;
+        if constexpr (NEXT > 1) wr2 = er1;
       }
       seg = 0;
       ax = static_cast<uint32_t>(s) * 128u;
@@ -137,43 +144,41 @@ struct NnOp {
       second = 0;
 #pragma unroll
       for (int l = 0; l < NnRows<P>::N; ++l) {
-        const int vr = s * 64 + vw.row[l], ph = vr < per ? vr : vr - per;
-        const bool is2 = ph >= re0;
+        const int vr = s * 64 + vw.row(l), ph = vr < per ? vr : vr - per;
+        const bool is2 = NEXT > 1 && ph >= re0;
         vw.v[l] = vr < 2 * per ? vw.v[l] + static_cast<uint32_t>(is2 ? ph - re0 : ph) * ldw_b : kMissing;
-        second |= (__builtin_amdgcn_readfirstlane(is2 ? 1 : 0)) << l;
+        if (NEXT > 1) second |= static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(is2 ? 1 : 0)) << l;
       }
     } else {
       const int ms = s - NE;
-      const int sg = ms < n0s ? 1 : 2;
+      const int sg = NSEG == 1 || ms < n0s ? 1 : 2;
       if (seg != sg) {
         if (seg < 1) {
           vx.init(ldx_b, rows_m);
           vw.init(ldw_b, cols);
         }
         seg = sg;
-        xr = make_rsrc(x[sg - 1], static_cast<uint32_t>(rows_m) * ldx_b);
+        xr = make_rsrc(NSEG > 1 && sg == 2 ? x1 : x0, static_cast<uint32_t>(rows_m) * ldx_b);
         second = 0;
       }
       const int k0 = (sg == 1 ? ms : ms - n0s) * 64;
-      const int left = s < hi ? min(64, K[sg - 1] - k0) : 0;
+      const int left = s < hi ? min(64, (NSEG > 1 && sg == 2 ? K1 : K0) - k0) : 0;
       ax = static_cast<int>(c16) < left * 2 ? static_cast<uint32_t>(k0) * 2u : kMissing;
-      wr = make_rsrc(W[sg - 1] + (left > 0 ? static_cast<int64_t>(k0) * ldw : 0),
-                     left > 0 ? static_cast<uint32_t>(left - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
+      wr = rows_of((NSEG > 1 && sg == 2 ? W1 : W0) + (left > 0 ? static_cast<int64_t>(k0) * (ldw_b / 2) : 0), left);
     }
   }
   __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
   __device__ __forceinline__ void load_w(int l, char* d) const {
-    if (seg == 0) ring_copy<P>(l, d, (second >> l) & 1 ? er1 : er0, vw.v[l]);
+    if constexpr (NEXT > 1) ring_copy<P>(l, d, (second >> l) & 1 ? wr2 : wr, vw.v[l]);
     else ring_copy<P>(l, d, wr, vw.v[l]);
   }
-  __device__ __forceinline__ void before(int, f32x4 (&)[P::NI][P::NJ]) const {}
 };
 
 // Partial sums of a wave's block (add: added to those that are there).
 template <class P>
 __device__ __forceinline__ void store_part(const f32x4 (&acc)[P::NI][P::NJ], float* part, int64_t ld, int64_t m0,
                                            int64_t n0, int64_t T, int64_t N, bool add = false) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int lane = opaque_int(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int j = 0; j < P::NJ; ++j) {
     const int64_t m = m0 + j * 16 + r;

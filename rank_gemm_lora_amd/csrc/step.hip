@@ -160,7 +160,7 @@ __device__ __forceinline__ void store_block(const f32x4 (&acc)[P::NI][P::NJ], co
 // q ^ 1 make the calls of blocks i and i + 1 and exchange halves.
 template <class P>
 __device__ __forceinline__ void drop_block(f32x4 (&acc)[P::NI][P::NJ], const Dropper& d, int64_t m0, int64_t n0) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int lane = opaque_int(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
   const bool odd = (q & 1) != 0;
 #pragma unroll
   for (int j = 0; j < P::NJ; ++j) {
@@ -182,22 +182,22 @@ __device__ __forceinline__ void drop_block(f32x4 (&acc)[P::NI][P::NJ], const Dro
           const bool keep = ((ms[h][e >> 1] >> (16 * (e & 1))) & 1u) != 0;
           acc[i + h][j][e] = keep ? acc[i + h][j][e] : 0.f;
         }
+#if defined(__HIP_DEVICE_COMPILE__)
+      if constexpr (P::BM == 256) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i + 1][j]));  // (back to where the MFMAs keep them)
+#endif
     }
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
 template <class P>
-struct DropNnOp : NnOp<P> {
+struct DropNnOp : NnOp<P, 1, 1> {
   Dropper d;
   int64_t mw, nw;
-  int at;  // before this stage (counted from the split's first)
-  __device__ __forceinline__ void before(int t, f32x4 (&acc)[P::NI][P::NJ]) const {
-    if (t == at) drop_block<P>(acc, d, mw, nw);
-  }
+  __device__ __forceinline__ void between(f32x4 (&acc)[P::NI][P::NJ]) const { drop_block<P>(acc, d, mw, nw); }
 };
 
-enum { kFormNt = 0, kFormNn = 1, kFormNnDrop = 2 };
+enum { kFormNt = 0, kFormNn = 1, kFormNn2 = 2, kFormNnDrop = 3 };  // (Nn2: two segments, two adapters)
 
 // One layer, grid (tiles, splits).
 template <class P, int FORM>
@@ -213,21 +213,24 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void ring_kernel(RingArgs p, in
     NtOp<P, false> op;
     op.init(p, m0, n0, s_lo, s_hi);
     ring_run<P, false>(acc, op, s_hi - s_lo, smem, wm0, wn0);
-  } else if constexpr (FORM == kFormNn) {
-    NnOp<P> op;
-    op.init(p.x, p.ldx, p.W, p.K, p.n_seg, p.tt, p.ldt, p.E, p.re, p.T, p.N, m0, n0, s_lo, s_hi);
+  } else if constexpr (FORM != kFormNnDrop) {
+    NnOp<P, FORM == kFormNn2 ? 2 : 1, FORM == kFormNn2 ? 2 : 1> op;
+    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, s_lo, s_hi);
+    op.extend(p, m0, n0);
     ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
   } else {
     DropNnOp<P> op;
-    op.init(p.x, p.ldx, p.W, p.K, p.n_seg, p.tt, p.ldt, p.E, p.re, p.T, p.N, m0, n0, s_lo, s_hi);
+    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, s_lo, s_hi);
+    op.extend(p, m0, n0);
     op.d.init(p.drop, p.N);
     op.mw = m0 + wm0;
     op.nw = n0 + wn0;
-    op.at = op.NE > s_lo ? op.NE - s_lo : -1;
-    ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
-    if (op.at >= s_hi - s_lo) drop_block<P>(acc, op.d, op.mw, op.nw);  // (this split ends before the base stages)
+    const int at = op.NE - s_lo;  // the first stage behind the extension
+    ring_run<P, true, true>(acc, op, s_hi - s_lo, smem, wm0, wn0, at);
+    if (at >= s_hi - s_lo) drop_block<P>(acc, op.d, op.mw, op.nw);  // (this split ends before the base stages)
   }
-  if (p.S > 1) store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.y) * p.T * p.N, p.N, m0 + wm0, n0 + wn0, p.T, p.N);
+  if (P::BM == 128 && p.S > 1)  // (splits are for the smaller tile)
+    store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.y) * p.T * p.N, p.N, m0 + wm0, n0 + wn0, p.T, p.N);
   else store_block<P>(acc, p, m0 + wm0, n0 + wn0, smem);
 }
 
@@ -273,11 +276,8 @@ __global__ __launch_bounds__(Ring128::THREADS, Ring128::OCC) void rank_nn_kernel
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
   const int64_t n0 = static_cast<int64_t>(static_cast<int>(blockIdx.y) - (side ? tiles0 : 0)) * P::BN;
   const int NS = static_cast<int>((p.K + 63) / 64), s_lo = static_cast<int>(blockIdx.z) * ks, s_hi = min(NS, s_lo + ks);
-  const uint16_t *xs[2] = {p.x[side], nullptr}, *Ws[2] = {p.A[side], nullptr}, *Es[2] = {nullptr, nullptr};
-  const int64_t Ks[2] = {p.K, 0};
-  const int re[2] = {0, 0};
-  NnOp<P> op;
-  op.init(xs, p.ldx, Ws, Ks, 1, nullptr, 0, Es, re, p.T, p.rank[side], m0, n0, s_lo, s_hi);
+  NnOp<P, 1, 0> op;
+  op.init(&p.x[side], p.ldx, &p.A[side], &p.K, p.T, p.rank[side], m0, n0, s_lo, s_hi);
   f32x4 acc[P::NI][P::NJ];
   ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
   const int R = p.rank[0] + p.rank[1], c0 = side ? p.rank[0] : 0;
@@ -416,6 +416,34 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict
 // chunks over grid y leave fp32 partial sums that contract_reduce_kernel adds in order. HBM-bound: P is read once.
 constexpr int kCtP = kCtT * kCtI * 2, kCtQ = kCtT * 2 * kCtJ * 2, kCtStage = kCtP + kCtQ;
 
+__device__ __forceinline__ bf16x8 tr_frag(const char* at, int row4) {
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + row4));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// (restrict: the copies in flight go to other slots; see ring_stage)
+__device__ __forceinline__ void contract_stage(f32x4 (&acc)[4][kCtJ / 16], const char* __restrict__ pb,
+                                               const char* __restrict__ qb, uint32_t pa, uint32_t qa, int nj) {
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    bf16x8 af[4];
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) af[ib] = tr_frag(pb + (pa ^ static_cast<uint32_t>(ib << 5)) + kk * 32 * 512, 4 * 512);
+#pragma unroll
+    for (int jb = 0; jb < kCtJ / 16; ++jb) {
+      if (jb >= nj) continue;
+#pragma unroll
+      for (int term = 0; term < 2; ++term) {
+        const bf16x8 bq = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)) + kk * 32 * 256, 4 * 256);
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib)
+          acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq, acc[ib][jb], 0, 0, 0);
+      }
+    }
+  }
+}
+
 template <bool DROP>
 __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_t chunk, int slices0) {
   __shared__ __attribute__((aligned(1024))) char smem[3 * kCtStage];
@@ -472,11 +500,6 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
   const int f = (r >> 2) | ((q & 1) << 2);
   const uint32_t pa = static_cast<uint32_t>((8 * q + (r >> 2)) * 512 + (((wave * 4) ^ f) * 32) + (r & 3) * 8);
   const uint32_t qa = static_cast<uint32_t>((8 * q + (r >> 2)) * 256 + f * 32 + (r & 3) * 8);
-  auto tr_frag = [](const char* at, int row4) {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + row4));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
   issue(0);
   issue(1);
   for (int s = 0; s < nst; ++s) {
@@ -492,24 +515,7 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
       }
       stage_barrier();
     }
-    const char *pb = b, *qb = b + kCtP;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 af[4];
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) af[ib] = tr_frag(pb + (pa ^ static_cast<uint32_t>(ib << 5)) + kk * 32 * 512, 4 * 512);
-#pragma unroll
-      for (int jb = 0; jb < kCtJ / 16; ++jb) {
-        if (jb >= nj) continue;
-#pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const bf16x8 bq = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)) + kk * 32 * 256, 4 * 256);
-#pragma unroll
-          for (int ib = 0; ib < 4; ++ib)
-            acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq, acc[ib][jb], 0, 0, 0);
-        }
-      }
-    }
+    contract_stage(acc, b, b + kCtP, pa, qa, nj);
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   // lane (r, q) of block (ib, jb): rows i = 64 wave + 16 ib + 4 q + e of P^T, column j = 16 jb + r
@@ -612,6 +618,7 @@ hipError_t launch_ring(const RingArgs& a, bool nn, hipStream_t s) {
   const bool drop = p.drop.thr != 0;
   hipError_t e;
   if (!nn) e = small ? launch_ring_cfg<Ring128, kFormNt>(p, NS, s) : launch_ring_cfg<Ring256, kFormNt>(p, NS, s);
+  else if (p.n_seg > 1) e = small ? launch_ring_cfg<Ring128, kFormNn2>(p, NS, s) : launch_ring_cfg<Ring256, kFormNn2>(p, NS, s);
   else if (!drop) e = small ? launch_ring_cfg<Ring128, kFormNn>(p, NS, s) : launch_ring_cfg<Ring256, kFormNn>(p, NS, s);
   else e = small ? launch_ring_cfg<Ring128, kFormNnDrop>(p, NS, s) : launch_ring_cfg<Ring256, kFormNnDrop>(p, NS, s);
   if (e != hipSuccess || p.S == 1) return e;
