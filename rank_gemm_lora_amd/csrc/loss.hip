@@ -27,7 +27,7 @@ enum { kStats = 0, kShare = 1 };
 template <class P, int MODE>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void logits_kernel(VocabLoss p, int64_t v0, int64_t cols, int mt, int nt) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
-  const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
+  const RingTile tile(xcd_remap(blockIdx.x, mt * nt), mt, nt, P::GROUP_M);
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * P::BN;
@@ -144,7 +144,7 @@ template <class P>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void dh_kernel(VocabLoss p, int64_t v0, int64_t cols, int ks, bool first,
                                                                 int mt, int nt) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
-  const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
+  const RingTile tile(xcd_remap(blockIdx.x, mt * nt), mt, nt, P::GROUP_M);
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * P::BN;
@@ -219,7 +219,7 @@ hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess || p.dh == nullptr) return e;
   int S, ks;
-  ring_plan(p.T, p.K, (p.piece + 63) / 64, &S, &ks);
+  loss_splits(p.T, p.K, (p.piece + 63) / 64, &S, &ks);
   const bool narrow = S > 1 || small_tile(p.T, p.K, cus);
   for (int64_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const int64_t cols = p.piece < p.V - v0 ? p.piece : p.V - v0;

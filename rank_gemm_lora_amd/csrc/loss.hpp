@@ -30,9 +30,19 @@ inline int64_t loss_piece(int64_t T, int64_t V) {
 }
 // Blocks of columns for which statistics are kept: 64 at a time with the smaller tile, 128 with the larger.
 inline int64_t loss_blocks(int64_t V) { return (V + 127) / 128 * 2; }
+inline void loss_splits(int64_t T, int64_t K, int64_t stages, int* S, int* ks) {
+  const int64_t tiles = (T + 127) / 128 * ((K + 127) / 128);
+  int64_t s = tiles > 0 ? 512 / tiles : 1;
+  const int64_t smax = stages / 8 > 1 ? stages / 8 : 1;
+  s = s < 1 ? 1 : (s > 16 ? 16 : s);
+  s = s > smax ? smax : s;
+  *ks = static_cast<int>((stages + s - 1) / s);
+  if (*ks < 1) *ks = 1;
+  *S = static_cast<int>((stages + *ks - 1) / *ks);
+}
 inline size_t loss_acc_bytes(int64_t T, int64_t K, int64_t piece) {
   int S, ks;
-  ring_plan(T, K, (piece + 63) / 64, &S, &ks);
+  loss_splits(T, K, (piece + 63) / 64, &S, &ks);
   return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(K) * 4;
 }
 hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t s);

@@ -236,11 +236,10 @@ __device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int
   __syncthreads();
 }
 
-// The tile of this workgroup: m-tiles in groups of GROUP_M over all n-tiles, a run of them to each XCD.
+// Tile L of mt x nt: m-tiles in groups of `group` over all n-tiles.
 struct RingTile {
   int m, n;
-  __device__ __forceinline__ RingTile(int pid, int mt, int nt, int group) {
-    const int L = xcd_remap(pid, mt * nt);
+  __device__ __forceinline__ RingTile(int L, int mt, int nt, int group) {
     const int gsize = group * nt;
     const int grp = L / gsize, first = grp * group;
     const int gm = min(group, mt - first), within = L - grp * gsize;
@@ -248,6 +247,50 @@ struct RingTile {
     n = within / gm;
   }
 };
+
+// A workgroup's work: a whole tile, or part `unit` of the tiles behind the first `full`, stages [lo, hi) of it. A run of
+// neighbours to each XCD.
+struct RingWork {
+  int tile, unit, lo, hi;
+  __device__ __forceinline__ RingWork(int b, int full, int tiles, int S, int ks, int NS) {
+    if (b < full) {
+      tile = xcd_remap(b, full);
+      unit = -1;
+      lo = 0;
+      hi = NS;
+    } else {
+      const int rem = tiles - full, r = xcd_remap(b - full, rem * S), z = r / rem;
+      tile = full + r - z * rem;
+      unit = (r - z * rem) * S + z;
+      lo = z * ks;
+      hi = min(NS, lo + ks);
+    }
+  }
+};
+
+// A part's sums as the registers hold them, [unit][wave][j][i][lane] of four, and the sum of a tile's parts in order for
+// column block j (16 tokens) of a wave.
+template <class P>
+__device__ __forceinline__ f32x4* part_at(float* part, int unit, int j, int i) {
+  return reinterpret_cast<f32x4*>(part) + (((static_cast<int64_t>(unit) * P::WAVES + ring_wave()) * P::NJ + j) * P::NI + i) * 64;
+}
+template <class P>
+__device__ __forceinline__ void put_part(const f32x4 (&acc)[P::NI][P::NJ], float* part, int unit) {
+  const int lane = opaque_int(threadIdx.x & 63);
+#pragma unroll
+  for (int j = 0; j < P::NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i) part_at<P>(part, unit, j, i)[lane] = acc[i][j];
+}
+template <class P>
+__device__ __forceinline__ void sum_parts(f32x4 (&acc)[P::NI][1], float* part, int rem_tile, int S, int j) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < P::NI; ++i) acc[i][0] = part_at<P>(part, rem_tile * S, j, i)[lane];
+  for (int z = 1; z < S; ++z)
+#pragma unroll
+    for (int i = 0; i < P::NI; ++i) acc[i][0] += part_at<P>(part, rem_tile * S + z, j, i)[lane];
+}
 
 // bf16 outputs of a wave's block through LDS: `put` 4 consecutive columns of a row, then `store` the block as whole
 // rows of 16-byte pieces. COLS columns, 16-byte chunks XOR-swizzled by row.

@@ -136,23 +136,24 @@ __global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct p, int S) 
   *reinterpret_cast<uint2*>(p.tt + t * ldt + c) = w;
 }
 
-template <class P>
-__device__ __forceinline__ void store_block(const f32x4 (&acc)[P::NI][P::NJ], const RingArgs& p, int64_t m0, int64_t n0,
+// (NJ: blocks of 16 tokens from m0 on)
+template <class P, int NJ>
+__device__ __forceinline__ void store_block(const f32x4 (&acc)[P::NI][NJ], const RingArgs& p, int64_t m0, int64_t n0,
                                             char* smem) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  BlockOut<P::WM, P::WN> out{smem + ring_wave() * P::WM * P::WN * 2};
+  BlockOut<NJ * 16, P::WN> out{smem + ring_wave() * NJ * 16 * P::WN * 2};
 #pragma unroll
   for (int i = 0; i < P::NI; ++i) {
     float bv[4];
     load_bias4(bv, p.bias[0], n0 + i * 16 + q * 4, p.N);
 #pragma unroll
-    for (int j = 0; j < P::NJ; ++j)
+    for (int j = 0; j < NJ; ++j)
       out.put(j * 16 + r, i * 16 + q * 4, pack_bf16x2(acc[i][j][0] + bv[0], acc[i][j][1] + bv[1]),
               pack_bf16x2(acc[i][j][2] + bv[2], acc[i][j][3] + bv[3]));
     __builtin_amdgcn_sched_barrier(0);
   }
   if (m0 < p.T && n0 < p.N)
-    out.store(p.y + m0 * p.ldy + n0, p.ldy, static_cast<int>(min<int64_t>(P::WM, p.T - m0)),
+    out.store(p.y + m0 * p.ldy + n0, p.ldy, static_cast<int>(min<int64_t>(NJ * 16, p.T - m0)),
               static_cast<int>(min<int64_t>(P::WN, p.N - n0)));
 }
 
@@ -199,69 +200,52 @@ struct DropNnOp : NnOp<P, 1, 1> {
 
 enum { kFormNt = 0, kFormNn = 1, kFormNn2 = 2, kFormNnDrop = 3 };  // (Nn2: two segments, two adapters)
 
-// One layer, grid (tiles, splits).
+// One layer: a workgroup per whole tile, then one per part of the others.
 template <class P, int FORM>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void ring_kernel(RingArgs p, int mt, int nt, int NS) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
-  const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
+  const RingWork work(blockIdx.x, p.full, mt * nt, p.S, p.ks, NS);
+  const RingTile tile(work.tile, mt, nt, P::GROUP_M);
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * P::BN;
-  const int s_lo = static_cast<int>(blockIdx.y) * p.ks, s_hi = min(NS, s_lo + p.ks);
+  const int ns = work.hi - work.lo;
   f32x4 acc[P::NI][P::NJ];
   if constexpr (FORM == kFormNt) {
     NtOp<P, false> op;
-    op.init(p, m0, n0, s_lo, s_hi);
-    ring_run<P, false>(acc, op, s_hi - s_lo, smem, wm0, wn0);
+    op.init(p, m0, n0, work.lo, work.hi);
+    ring_run<P, false>(acc, op, ns, smem, wm0, wn0);
   } else if constexpr (FORM != kFormNnDrop) {
     NnOp<P, FORM == kFormNn2 ? 2 : 1, FORM == kFormNn2 ? 2 : 1> op;
-    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, s_lo, s_hi);
+    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, work.lo, work.hi);
     op.extend(p, m0, n0);
-    ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
+    ring_run<P, true>(acc, op, ns, smem, wm0, wn0);
   } else {
     DropNnOp<P> op;
-    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, s_lo, s_hi);
+    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, work.lo, work.hi);
     op.extend(p, m0, n0);
     op.d.init(p.drop, p.N);
     op.mw = m0 + wm0;
     op.nw = n0 + wn0;
-    const int at = op.NE - s_lo;  // the first stage behind the extension
-    ring_run<P, true, true>(acc, op, s_hi - s_lo, smem, wm0, wn0, at);
-    if (at >= s_hi - s_lo) drop_block<P>(acc, op.d, op.mw, op.nw);  // (this split ends before the base stages)
+    const int at = op.NE - work.lo;  // the first stage behind the extension
+    ring_run<P, true, true>(acc, op, ns, smem, wm0, wn0, at);
+    if (at >= ns) drop_block<P>(acc, op.d, op.mw, op.nw);  // (this part ends before the base stages)
   }
-  if (P::BM == 128 && p.S > 1)  // (splits are for the smaller tile)
-    store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.y) * p.T * p.N, p.N, m0 + wm0, n0 + wn0, p.T, p.N);
-  else store_block<P>(acc, p, m0 + wm0, n0 + wn0, smem);
+  if (work.unit >= 0) put_part<P>(acc, p.part, work.unit);
+  else store_block<P, P::NJ>(acc, p, m0 + wm0, n0 + wn0, smem);
 }
 
-// y = the splits' sum in order + bias. 4 columns per thread.
-__global__ __launch_bounds__(256) void ring_finish_kernel(RingArgs p) {
-  const int64_t quads = (p.N + 3) / 4, idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (idx >= p.T * quads) return;
-  const int64_t t = idx / quads, n = (idx - t * quads) * 4;
-  const float* src = p.part + t * p.N + n;
-  uint16_t* dst = p.y + t * p.ldy + n;
-  float bv[4];
-  load_bias4(bv, p.bias[0], n, p.N);
-  if (p.N % 4 == 0) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < p.S; ++z) v += *reinterpret_cast<const f32x4*>(src + z * p.T * p.N);
-    const uint2 w = {pack_bf16x2(v[0] + bv[0], v[1] + bv[1]), pack_bf16x2(v[2] + bv[2], v[3] + bv[3])};
-    if (reinterpret_cast<uintptr_t>(dst) % 8 == 0) {
-      *reinterpret_cast<uint2*>(dst) = w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dst[e] = static_cast<uint16_t>((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (n + e >= p.N) break;
-    float v = 0.f;
-    for (int z = 0; z < p.S; ++z) v += src[z * p.T * p.N + e];
-    dst[e] = f32_to_bf16_rne(v + bv[e]);
-  }
+// The tiles that were cut: grid (tiles, column blocks of a wave).
+template <class P>
+__global__ __launch_bounds__(P::THREADS) void ring_join_kernel(RingArgs p, int mt, int nt) {
+  __shared__ __attribute__((aligned(16))) char smem[P::WAVES * 16 * P::WN * 2];
+  const RingTile tile(p.full + blockIdx.x, mt, nt, P::GROUP_M);
+  const int wave = ring_wave(), j = blockIdx.y;
+  const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM + (wave % P::WAVES_M) * P::WM + j * 16;
+  const int64_t n0 = static_cast<int64_t>(tile.n) * P::BN + (wave / P::WAVES_M) * P::WN;
+  f32x4 acc[P::NI][1];
+  sum_parts<P>(acc, p.part, blockIdx.x, p.S, j);
+  store_block<P, 1>(acc, p, m0, n0, smem);
 }
 
 // Rank-wide product over rows of the contraction (the gradient's, B [K, rank] as it lies): 128 tokens and up to 128
@@ -313,11 +297,11 @@ __device__ __forceinline__ void act_of(float g, float& a, float& da) {
   }
 }
 
-template <class P, int ACT>
-__device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][P::NJ], const RingArgs& p, int64_t m0, int64_t n0,
+template <class P, int ACT, int NJ>
+__device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][NJ], const RingArgs& p, int64_t m0, int64_t n0,
                                             char* smem) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  BlockOut<P::WM, P::WN / 2> out{smem + ring_wave() * P::WM * P::WN};
+  BlockOut<NJ * 16, P::WN / 2> out{smem + ring_wave() * NJ * 16 * P::WN};
   const int64_t fb = (p.N + 15) / 16;
 #pragma unroll
   for (int i = 0; i < P::NI / 2; ++i) {
@@ -326,7 +310,7 @@ __device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][P::NJ], co
     load_bias4(bg, p.bias[0], n, p.N);
     load_bias4(bu, p.bias[1], n, p.N);
 #pragma unroll
-    for (int j = 0; j < P::NJ; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       f32x4 g, u;
       float v[4];
 #pragma unroll
@@ -347,7 +331,7 @@ __device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][P::NJ], co
     __builtin_amdgcn_sched_barrier(0);
   }
   if (p.y != nullptr && m0 < p.T && n0 < p.N)
-    out.store(p.y + m0 * p.ldy + n0, p.ldy, static_cast<int>(min<int64_t>(P::WM, p.T - m0)),
+    out.store(p.y + m0 * p.ldy + n0, p.ldy, static_cast<int>(min<int64_t>(NJ * 16, p.T - m0)),
               static_cast<int>(min<int64_t>(P::WN / 2, p.N - n0)));
 }
 
@@ -355,15 +339,29 @@ __device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][P::NJ], co
 template <class P, int ACT>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void gated_kernel(RingArgs p, int mt, int nt, int NS) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
-  const RingTile tile(blockIdx.x, mt, nt, P::GROUP_M);
+  const RingWork work(blockIdx.x, p.full, mt * nt, p.S, p.ks, NS);
+  const RingTile tile(work.tile, mt, nt, P::GROUP_M);
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * (P::BN / 2);
   f32x4 acc[P::NI][P::NJ];
   NtOp<P, true> op;
-  op.init(p, m0, n0, 0, NS);
-  ring_run<P, false>(acc, op, NS, smem, wm0, wn0);
-  gated_store<P, ACT>(acc, p, m0 + wm0, n0 + wn0 / 2, smem);
+  op.init(p, m0, n0, work.lo, work.hi);
+  ring_run<P, false>(acc, op, work.hi - work.lo, smem, wm0, wn0);
+  if (work.unit >= 0) put_part<P>(acc, p.part, work.unit);
+  else gated_store<P, ACT, P::NJ>(acc, p, m0 + wm0, n0 + wn0 / 2, smem);
+}
+
+template <class P, int ACT>
+__global__ __launch_bounds__(P::THREADS) void gated_join_kernel(RingArgs p, int mt, int nt) {
+  __shared__ __attribute__((aligned(16))) char smem[P::WAVES * 16 * P::WN];
+  const RingTile tile(p.full + blockIdx.x, mt, nt, P::GROUP_M);
+  const int wave = ring_wave(), j = blockIdx.y;
+  const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM + (wave % P::WAVES_M) * P::WM + j * 16;
+  const int64_t n0 = static_cast<int64_t>(tile.n) * (P::BN / 2) + (wave / P::WAVES_M) * (P::WN / 2);
+  f32x4 acc[P::NI][1];
+  sum_parts<P>(acc, p.part, blockIdx.x, p.S, j);
+  gated_store<P, ACT, 1>(acc, p, m0, n0, smem);
 }
 
 // dg and du: a wave takes 16 tokens x 64 columns, from the blocks that the forward kept.
@@ -570,13 +568,6 @@ __global__ __launch_bounds__(256) void contract_reduce_kernel(Contract p, int S)
 
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
 
-int step_cus() {
-  int dev = 0, n = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 0;
-  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
-  return n;
-}
-
 }  // namespace
 
 hipError_t launch_rank_product(const RankProduct& p, bool nn, hipStream_t s) {
@@ -605,40 +596,50 @@ hipError_t launch_rank_product(const RankProduct& p, bool nn, hipStream_t s) {
 template <class P, int FORM>
 hipError_t launch_ring_cfg(const RingArgs& p, int NS, hipStream_t s) {
   const int mt = static_cast<int>((p.T + P::BM - 1) / P::BM), nt = static_cast<int>((p.N + P::BN - 1) / P::BN);
-  hipLaunchKernelGGL((ring_kernel<P, FORM>), dim3(static_cast<unsigned>(mt * nt), static_cast<unsigned>(p.S)),
-                     dim3(P::THREADS), 0, s, p, mt, nt, NS);
+  const int rem = mt * nt - p.full;
+  hipLaunchKernelGGL((ring_kernel<P, FORM>), dim3(static_cast<unsigned>(p.full + rem * p.S)), dim3(P::THREADS), 0, s, p, mt,
+                     nt, NS);
+  if (rem > 0)
+    hipLaunchKernelGGL(ring_join_kernel<P>, dim3(static_cast<unsigned>(rem), P::NJ), dim3(P::THREADS), 0, s, p, mt, nt);
   return hipGetLastError();
 }
 
 hipError_t launch_ring(const RingArgs& a, bool nn, hipStream_t s) {
   RingArgs p = a;
   const int NS = static_cast<int>(ring_stages(p));
-  ring_plan(p.T, p.N, NS, &p.S, &p.ks);
-  const bool small = p.S > 1 || small_tile(p.T, p.N, step_cus());
-  const bool drop = p.drop.thr != 0;
-  hipError_t e;
-  if (!nn) e = small ? launch_ring_cfg<Ring128, kFormNt>(p, NS, s) : launch_ring_cfg<Ring256, kFormNt>(p, NS, s);
-  else if (p.n_seg > 1) e = small ? launch_ring_cfg<Ring128, kFormNn2>(p, NS, s) : launch_ring_cfg<Ring256, kFormNn2>(p, NS, s);
-  else if (!drop) e = small ? launch_ring_cfg<Ring128, kFormNn>(p, NS, s) : launch_ring_cfg<Ring256, kFormNn>(p, NS, s);
-  else e = small ? launch_ring_cfg<Ring128, kFormNnDrop>(p, NS, s) : launch_ring_cfg<Ring256, kFormNnDrop>(p, NS, s);
-  if (e != hipSuccess || p.S == 1) return e;
-  hipLaunchKernelGGL(ring_finish_kernel, dim3(blocks_of(p.T * ((p.N + 3) / 4), 256)), dim3(256), 0, s, p);
-  return hipGetLastError();
+  const RingPlan plan = ring_plan(p.T, p.N, NS);
+  p.full = static_cast<int>(plan.full);
+  p.S = plan.S;
+  p.ks = plan.ks;
+  const bool big = plan.big;
+  if (!nn) return big ? launch_ring_cfg<Ring256, kFormNt>(p, NS, s) : launch_ring_cfg<Ring128, kFormNt>(p, NS, s);
+  if (p.n_seg > 1) return big ? launch_ring_cfg<Ring256, kFormNn2>(p, NS, s) : launch_ring_cfg<Ring128, kFormNn2>(p, NS, s);
+  if (p.drop.thr == 0) return big ? launch_ring_cfg<Ring256, kFormNn>(p, NS, s) : launch_ring_cfg<Ring128, kFormNn>(p, NS, s);
+  return big ? launch_ring_cfg<Ring256, kFormNnDrop>(p, NS, s) : launch_ring_cfg<Ring128, kFormNnDrop>(p, NS, s);
 }
 
-template <class P>
-hipError_t launch_gated_cfg(const RingArgs& p, hipStream_t s) {
+template <class P, int ACT>
+hipError_t launch_gated_cfg(const RingArgs& p, int NS, hipStream_t s) {
   const int mt = static_cast<int>((p.T + P::BM - 1) / P::BM), nt = static_cast<int>((2 * p.N + P::BN - 1) / P::BN);
-  const int NS = static_cast<int>(ring_stages(p));
-  const dim3 grid(static_cast<unsigned>(mt * nt)), block(P::THREADS);
-  if (p.act == 0) hipLaunchKernelGGL((gated_kernel<P, 0>), grid, block, 0, s, p, mt, nt, NS);
-  else if (p.act == 1) hipLaunchKernelGGL((gated_kernel<P, 1>), grid, block, 0, s, p, mt, nt, NS);
-  else hipLaunchKernelGGL((gated_kernel<P, 2>), grid, block, 0, s, p, mt, nt, NS);
+  const int rem = mt * nt - p.full;
+  hipLaunchKernelGGL((gated_kernel<P, ACT>), dim3(static_cast<unsigned>(p.full + rem * p.S)), dim3(P::THREADS), 0, s, p, mt,
+                     nt, NS);
+  if (rem > 0)
+    hipLaunchKernelGGL((gated_join_kernel<P, ACT>), dim3(static_cast<unsigned>(rem), P::NJ), dim3(P::THREADS), 0, s, p, mt,
+                       nt);
   return hipGetLastError();
 }
 
-hipError_t launch_gated(const RingArgs& p, hipStream_t s) {
-  return small_tile(p.T, 2 * p.N, step_cus()) ? launch_gated_cfg<Ring128>(p, s) : launch_gated_cfg<Ring256>(p, s);
+hipError_t launch_gated(const RingArgs& a, hipStream_t s) {
+  RingArgs p = a;
+  const int NS = static_cast<int>(ring_stages(p));
+  const RingPlan plan = ring_plan(p.T, 2 * p.N, NS);
+  p.full = static_cast<int>(plan.full);
+  p.S = plan.S;
+  p.ks = plan.ks;
+  if (p.act == 0) return plan.big ? launch_gated_cfg<Ring256, 0>(p, NS, s) : launch_gated_cfg<Ring128, 0>(p, NS, s);
+  if (p.act == 1) return plan.big ? launch_gated_cfg<Ring256, 1>(p, NS, s) : launch_gated_cfg<Ring128, 1>(p, NS, s);
+  return plan.big ? launch_gated_cfg<Ring256, 2>(p, NS, s) : launch_gated_cfg<Ring128, 2>(p, NS, s);
 }
 
 hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,

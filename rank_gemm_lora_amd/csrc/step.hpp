@@ -65,8 +65,8 @@ struct RingArgs {
   int64_t T, N;
   uint16_t* y; int64_t ldy;
   Drop drop;
-  float* part;    // S > 1: [S, T, N] fp32
-  int S, ks;      // splits of the stages, ks each
+  float* part;    // partial sums of the split tiles
+  int full, S, ks;  // RingPlan
   float* saved;   // gated: where the forward leaves g and u, or null
   int act;
 };
@@ -75,26 +75,51 @@ inline int64_t ring_stages(const RingArgs& p) {
   for (int i = 0; i < p.n_seg; ++i) n += (p.K[i] + 63) / 64;
   return n;
 }
-// Splits of a layer whose tiles leave compute units idle: 128 x 128 tiles, two on each of 256 units, at least 8 stages
-// each (fp32 partial sums cost a write and a read of T N 4 bytes per split).
-constexpr int kRingMaxSplits = 16;
-inline void ring_plan(int64_t T, int64_t N, int64_t stages, int* S, int* ks) {
-  const int64_t tiles = (T + 127) / 128 * ((N + 127) / 128);
-  int64_t s = tiles > 0 ? 512 / tiles : 1;
-  const int64_t smax = stages / 8 > 1 ? stages / 8 : 1;
-  s = s < 1 ? 1 : (s > kRingMaxSplits ? kRingMaxSplits : s);
-  s = s > smax ? smax : s;
-  *ks = static_cast<int>((stages + s - 1) / s);
-  if (*ks < 1) *ks = 1;
-  *S = static_cast<int>((stages + *ks - 1) / *ks);
+// How a layer's tiles are run: 256 x 256 tiles, one on a compute unit, or 128 x 128, two; the tiles of the last round,
+// which would leave units idle, each cut along the contraction into S parts of ks stages whose fp32 sums a second launch
+// joins. Chosen by an estimate of the time in microseconds (256 units; measured on MI355X: a stage of 64 indices takes a
+// 256 x 256 tile 1.7, two 128 x 128 tiles side by side 1.0; filling the ring and the epilogue take 8 and 5; the second
+// launch 6, and a sum is written and read at 4 TB/s). 4352 tokens, dx of 4096 -> 14336 in two segments: 272 tiles are one
+// round and 16 tiles; whole, 1222 us (in 128 x 128 tiles); the 16 cut into 16 parts each, 880.
+struct RingPlan {
+  bool big;
+  int64_t tiles;
+  int64_t full;  // tiles that are run whole; the others in S parts
+  int S, ks;
+};
+constexpr int kRingUnits = 256, kRingMaxSplits = 16, kRingMinStages = 4;
+inline RingPlan ring_plan(int64_t T, int64_t N, int64_t stages) {
+  RingPlan best = {false, 0, 0, 1, static_cast<int>(stages > 0 ? stages : 1)};
+  double least = 0.0;
+  for (int big = 0; big < 2; ++big) {
+    const int64_t bm = big ? 256 : 128, slots = big ? kRingUnits : 2 * kRingUnits;
+    const int64_t tiles = (T + bm - 1) / bm * ((N + bm - 1) / bm);
+    const double stage = big ? 1.7 : 1.0, ends = big ? 8.0 : 5.0;
+    for (int s = 1; s <= kRingMaxSplits; ++s) {
+      const int64_t ks = (stages + s - 1) / s;
+      if (s > 1 && (ks < kRingMinStages || (stages + ks - 1) / ks != s)) continue;
+      const int64_t full = s > 1 ? tiles / slots * slots : tiles, rem = tiles - full;
+      if (s > 1 && rem == 0) continue;
+      const double whole = static_cast<double>((full + slots - 1) / slots) * (static_cast<double>(stages) * stage + ends);
+      const double tail = rem > 0 ? static_cast<double>((rem * s + slots - 1) / slots) * (static_cast<double>(ks) * stage + ends) +
+                                        6.0 + static_cast<double>(rem * s * bm * bm) * 8.0 / 4e6
+                                  : 0.0;
+      if (best.tiles == 0 || whole + tail < least) {
+        least = whole + tail;
+        best = RingPlan{big != 0, tiles, full, s, static_cast<int>(ks)};
+      }
+    }
+  }
+  return best;
 }
 inline size_t ring_part_bytes(int64_t T, int64_t N, int64_t stages) {
-  int S, ks;
-  ring_plan(T, N, stages, &S, &ks);
-  return S > 1 ? static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(N) * 4 : 0;
+  const RingPlan p = ring_plan(T, N, stages);
+  const int64_t bm = p.big ? 256 : 128;
+  return p.S > 1 ? static_cast<size_t>((p.tiles - p.full) * p.S) * static_cast<size_t>(bm * bm) * 4 : 0;
 }
-hipError_t launch_ring(const RingArgs& p, bool nn, hipStream_t s);     // (plans the splits itself: p.part holds them)
+hipError_t launch_ring(const RingArgs& p, bool nn, hipStream_t s);  // (p.part: ring_part_bytes(T, N, ring_stages))
 // h = act(g) . u: W[0], E[0], bias[0] the gate's, [1] the up projection's; N columns of each; one segment.
+// (p.part: ring_part_bytes(T, 2 N, ring_stages))
 hipError_t launch_gated(const RingArgs& p, hipStream_t s);
 
 // g and u as the forward keeps them: fp32, in blocks of 16 tokens x 16 columns as the MFMA leaves them (block (a, b):

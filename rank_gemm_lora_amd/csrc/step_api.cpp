@@ -284,14 +284,19 @@ struct GatedLayout {
   size_t tt = 0, vt = 0, dg = 0, du = 0, saved = 0, part = 0, total = 0;
 };
 
-size_t gated_fwd_part(int64_t T, int64_t K, int64_t R) { return R > 0 ? lora::rank_part_bytes(T, K, R, 0, false) : 0; }
+// (partial sums of the rank-wide product, then of the GEMM's cut tiles)
+size_t gated_fwd_part(int64_t T, int64_t K, int64_t F, int64_t R) {
+  return std::max(R > 0 ? lora::rank_part_bytes(T, K, R, 0, false) : 0, lora::ring_part_bytes(T, 2 * F, stages(K, 0, R)));
+}
 
-GatedLayout gated_fwd_layout(int64_t T, int64_t K, int64_t rg, int64_t ru) {
+GatedLayout gated_fwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_t ru) {
   GatedLayout L;
   Take take;
   L.tt = take(tt_bytes(T, rg + ru));
-  // (rank_tasks depends on the sum alone; an inactive adapter's split plan is never larger than 16 splits of the rest)
-  L.part = take(std::max(gated_fwd_part(T, K, rg + ru), std::max(gated_fwd_part(T, K, rg), gated_fwd_part(T, K, ru))));
+  size_t part = 0;
+  for (int i = 0; i < 4; ++i)  // both adapters, or either of them inactive
+    part = std::max(part, gated_fwd_part(T, K, F, (i & 1 ? 0 : rg) + (i & 2 ? 0 : ru)));
+  L.part = take(part);
   L.total = take.off;
   return L;
 }
@@ -307,11 +312,10 @@ GatedLayout gated_bwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_
   L.dg = take(static_cast<size_t>(T) * F * 2);
   L.du = take(static_cast<size_t>(T) * F * 2);
   L.vt = take(tt_bytes(T, R));
-  size_t part = gated_fwd_layout(T, K, rg, ru).total;
+  size_t part = gated_fwd_layout(T, K, F, rg, ru).total;
   for (int i = 0; i < 4; ++i) {  // both adapters, or either of them inactive
     const int64_t a = i & 1 ? 0 : rg, b = i & 2 ? 0 : ru;
     if (a + b > 0) {
-      part = std::max(part, gated_fwd_part(T, K, a + b));
       part = std::max(part, lora::rank_part_bytes(T, F, a, b, true));
       part = std::max(part, lora::contract_part_bytes(T, K, a + b, 0));
       part = std::max(part, lora::contract_part_bytes(T, F, a, b));
@@ -370,7 +374,7 @@ hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const
   }
   g.x[0] = bf(x); g.ldx = ldx; g.W[0] = bf(l->W_gate); g.W[1] = bf(l->W_up); g.K[0] = K; g.n_seg = 1;
   g.bias[0] = bf(l->b_gate); g.bias[1] = bf(l->b_up); g.T = T; g.N = F; g.y = bf(h); g.ldy = ldh; g.act = act;
-  g.saved = saved;
+  g.saved = saved; g.part = part;
   return lora::launch_gated(g, st);
 }
 
@@ -380,7 +384,7 @@ extern "C" {
 
 size_t lora_gated_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up) {
   if (T <= 0 || K <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
-  return gated_fwd_layout(T, K, rank_gate, rank_up).total;
+  return gated_fwd_layout(T, K, F, rank_gate, rank_up).total;
 }
 
 size_t lora_gated_saved_size(int64_t T, int64_t F, int32_t rank_gate, int32_t rank_up) {
@@ -403,7 +407,7 @@ int lora_gated_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
   if (T > 0 && (x == nullptr || h == nullptr)) return LORA_ERR_NULL_PTR;
   if (!aligned(x, 16) || !aligned(h, 2) || !aligned(workspace, 16) || !aligned(saved, 16) || ldx % 8 != 0)
     return LORA_ERR_ALIGN;
-  const GatedLayout L = T > 0 ? gated_fwd_layout(T, K, s[0].given, s[1].given) : GatedLayout{};
+  const GatedLayout L = T > 0 ? gated_fwd_layout(T, K, F, s[0].given, s[1].given) : GatedLayout{};
   if (L.total > 0 && (workspace == nullptr || workspace_bytes < L.total)) return LORA_ERR_WORKSPACE;
   const Span outs[3] = {span2d(h, T, ldh, F, 2), bytes_at(workspace, L.total),
                         saved != nullptr && T > 0 ? bytes_at(saved, saved_bytes(T, F, s[0].given + s[1].given)) : Span{}};

@@ -132,7 +132,7 @@ def test_workspace_sizes():
     assert d(1 << 21, 64, 64, 8) == 0 and gb(1 << 21, 64, 64, 8, 8) == 0
     for T in (1, 65, 5000):
         assert 0 < d(T, 512, 256, 16) <= db(T, 512, 256, 16)
-        assert g(T, 512, 256, 0, 0) == 0 < g(T, 512, 256, 16, 8) <= gb(T, 512, 256, 16, 8)
+        assert 0 < g(T, 512, 256, 16, 8) <= gb(T, 512, 256, 16, 8)
         assert gs(T, 256, 16, 8) >= T * 256 * 8
 
 
