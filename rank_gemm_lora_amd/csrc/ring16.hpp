@@ -17,6 +17,8 @@
 //   void load_x(int l, char* dst)  copy instruction l of NL of the x unit, and of the W unit
 //   void load_w(int l, char* dst)
 //   void between(acc)              (with SPLIT) runs once, before a named stage
+//   void fetch(int t), next()      (with TOUCH) begins to load what stage t's fragments are changed with, at most one stage
+//   void touch(bf16x8& b, int j)   ahead; makes it current; changes fragment j of the x side before it is multiplied
 #pragma once
 
 #include "pipe_dev.hpp"
@@ -32,8 +34,8 @@ using Ring128 = QCfg<128, 128, 64, 64, 128, 5, 2>;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// A row or a chunk that does not exist gets this added to its offset: past every resource (at most 2^30 bytes: 256
-// rows of 4 MB), and a missing row and a missing chunk together do not wrap around.
+// A chunk that does not exist gets this added to its offset: past every resource (at most 2^30 bytes: 256 rows of 4 MB),
+// with no wrap around behind it.
 constexpr uint32_t kMissing = 0x40000000u;
 
 template <class P>
@@ -54,45 +56,42 @@ __device__ __forceinline__ uint32_t ring_chunk() {
   return static_cast<uint32_t>(((lane & 7) ^ (((ring_wave() * 8 + (lane >> 3)) >> 1) & 7)) * 16);
 }
 
-// Per-lane offsets of a unit whose tile row R is source row R (rows from `valid` on are missing).
+// A lane's offsets in a unit whose tile row R is source row R: `base` in copy instruction 0, `step` more in each after it.
+// (A row behind the last lies behind the resource, whose size is a whole number of row strides: it reads as zeros.)
 template <class P>
 struct NtRows {
-  static constexpr int N = ring_loads<P>();
-  uint32_t v[N];
-  __device__ __forceinline__ void init(uint32_t ld_bytes, int valid) {
+  uint32_t base, step;
+  __device__ __forceinline__ void init(uint32_t ld_bytes, int rows_per_copy = P::WAVES * 8, int first = -1) {
     const int lane = opaque_int(threadIdx.x & 63);
-    const int r0 = ring_wave() * 8 + (lane >> 3);
-    const uint32_t c = ring_chunk<P>();
-#pragma unroll
-    for (int l = 0; l < N; ++l) {
-      const int row = l * P::WAVES * 8 + r0;
-      v[l] = row < valid ? static_cast<uint32_t>(row) * ld_bytes + c : kMissing;
-    }
+    base = static_cast<uint32_t>((first < 0 ? ring_wave() * 8 : first) + (lane >> 3)) * ld_bytes + ring_chunk<P>();
+    step = static_cast<uint32_t>(rows_per_copy) * ld_bytes;
   }
+  __device__ __forceinline__ uint32_t at(int l, uint32_t add) const { return base + add + static_cast<uint32_t>(l) * step; }
 };
 
-// Per-lane offsets of an NN unit: tile row k is source row k of the stage (the resource ends behind its last row), and
+// A lane's offsets in an NN unit: tile row k is source row k of the stage (the resource ends behind its last row), and
 // 32-byte granule g of it sits at g ^ f(k), f(k) = (k & 3) | (k >> 3 & 1) << 2: the eight rows that half a wave's
-// transposing read touches then lie in eight different granules of the 256 bytes of the banks.
+// transposing read touches then lie in eight different granules of the 256 bytes of the banks. A copy instruction takes
+// ROWS rows of the tile per wave; f depends on its number by its last bit at most.
 template <class P>
 struct NnRows {
-  static constexpr int N = ring_loads<P>();
-  static constexpr int LPR = P::BN * 2 / 16;  // lanes (16-byte pieces) per row
-  uint32_t v[N];
+  static constexpr int LPR = P::BN * 2 / 16, ROWS = 64 / LPR;  // lanes (16-byte pieces) per row; rows per wave
+  uint32_t base[2], step;
+  static_assert(P::WAVES * ROWS == 8 || P::WAVES * ROWS == 16, "f by the parity of the instruction");
   __device__ __forceinline__ static int row(int l) {
-    return ((l * P::WAVES + ring_wave()) * 64 + opaque_int(threadIdx.x & 63)) / LPR;
+    return (l * P::WAVES + ring_wave()) * ROWS + opaque_int(threadIdx.x & 63) / LPR;
+  }
+  __device__ __forceinline__ static int col(int l) {
+    const int k = row(l), p = opaque_int(threadIdx.x & 63) % LPR, f = (k & 3) | (((k >> 3) & 1) << 2);
+    return (((p >> 1) ^ f) * 2 + (p & 1)) * 8;
   }
   __device__ __forceinline__ void init(uint32_t ld_bytes, int cols_valid) {
-    const int lane = opaque_int(threadIdx.x & 63);
 #pragma unroll
-    for (int l = 0; l < N; ++l) {
-      const int sl = (l * P::WAVES + ring_wave()) * 64 + lane;
-      const int k = sl / LPR, p = sl % LPR;
-      const int f = (k & 3) | (((k >> 3) & 1) << 2);
-      const int col = (((p >> 1) ^ f) * 2 + (p & 1)) * 8;
-      v[l] = col < cols_valid ? static_cast<uint32_t>(k) * ld_bytes + static_cast<uint32_t>(col) * 2 : kMissing;
-    }
+    for (int h = 0; h < 2; ++h)
+      base[h] = col(h) < cols_valid ? static_cast<uint32_t>(row(0)) * ld_bytes + static_cast<uint32_t>(col(h)) * 2 : kMissing;
+    step = static_cast<uint32_t>(P::WAVES * ROWS) * ld_bytes;
   }
+  __device__ __forceinline__ uint32_t at(int l) const { return base[l & 1] + static_cast<uint32_t>(l) * step; }
 };
 
 template <class P, bool NN>
@@ -136,7 +135,7 @@ struct RingFrags {
 // One stage: its MFMAs, the fragment reads of its second k-step and of the next stage's first, the copies of stage t + 2.
 // (ws and ws2 are restrict: nothing copies into the W slots that are read here, and without the compiler's knowing so it
 // waits for every copy in flight before each transposing read.)
-template <class P, bool NN, class Op>
+template <class P, bool NN, bool TOUCH, class Op>
 __device__ __forceinline__ void ring_stage(f32x4 (&acc)[P::NI][P::NJ], Frags16<P> (&fr)[2], const Op& op,
                                            const RingFrags<P, NN>& rf, const char* xs, const char* __restrict__ ws,
                                            const char* xs2, const char* __restrict__ ws2, char* xdst, char* wdst) {
@@ -146,6 +145,9 @@ __device__ __forceinline__ void ring_stage(f32x4 (&acc)[P::NI][P::NJ], Frags16<P
 #pragma unroll
   for (int m = 0; m < NB; ++m) {
     const int i = m / P::NJ, j = m % P::NJ;
+    if constexpr (TOUCH) {
+      if (i == 0) op.touch(fr[0].b[j], j);
+    }
     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[0].a[i], fr[0].b[j], acc[i][j], 0, 0, 0);
     if (m % RS == 0) rf.read(fr[1], m / RS, xs, ws, 1);
     if (m % LS == LS / 2) op.load_x(m / LS, xdst);
@@ -154,6 +156,9 @@ __device__ __forceinline__ void ring_stage(f32x4 (&acc)[P::NI][P::NJ], Frags16<P
 #pragma unroll
   for (int m = 0; m < NB; ++m) {
     const int i = m / P::NJ, j = m % P::NJ;
+    if constexpr (TOUCH) {
+      if (i == 0) op.touch(fr[1].b[j], j);
+    }
     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[1].a[i], fr[1].b[j], acc[i][j], 0, 0, 0);
     if (m == 0) {
       __builtin_amdgcn_sched_barrier(0);
@@ -185,7 +190,7 @@ __device__ __forceinline__ void keep_acc(f32x4 (&acc)[P::NI][P::NJ]) {
 // op.between(acc) runs before stage `at` (0 < at; not at all where at >= NS).
 // (Schedule as the hot GEMM's: x of stage t + 2 is copied beside k-step 0, W beside k-step 1, into the slots that the
 // barriers of stages t - 1 and t release; the wait of stage t leaves the x copies of stage t + 2 in flight.)
-template <class P, bool NN, bool SPLIT = false, class Op>
+template <class P, bool NN, bool SPLIT = false, bool TOUCH = false, class Op>
 __device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int NS, char* smem, int wm0, int wn0,
                                          int at = 0) {
   static_assert(P::WAVES == 4, "schedule written for 4 waves");
@@ -196,6 +201,7 @@ __device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int
     for (int j = 0; j < P::NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  if constexpr (TOUCH) op.fetch(0);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     op.seek(s);
@@ -218,8 +224,12 @@ __device__ __forceinline__ void ring_run(f32x4 (&acc)[P::NI][P::NJ], Op& op, int
       rf.read(fr[0], f, smem + a * P::SLOT_BYTES, smem + after(a) * P::SLOT_BYTES, 0);
     for (; t < end; ++t) {
       op.seek(t + 2);
+      if constexpr (TOUCH) {
+        op.next();
+        op.fetch(t + 1);
+      }
       const int b1 = after(a), a2 = after(b1), b2 = after(a2), a3 = after(b2);  // W of t; x, W of t + 1; x of t + 2
-      ring_stage<P, NN>(acc, fr, op, rf, smem + a * P::SLOT_BYTES, smem + b1 * P::SLOT_BYTES, smem + a2 * P::SLOT_BYTES,
+      ring_stage<P, NN, TOUCH>(acc, fr, op, rf, smem + a * P::SLOT_BYTES, smem + b1 * P::SLOT_BYTES, smem + a2 * P::SLOT_BYTES,
                         smem + b2 * P::SLOT_BYTES, smem + a3 * P::SLOT_BYTES, smem + a * P::SLOT_BYTES);
       a = a2;
     }
@@ -290,6 +300,19 @@ __device__ __forceinline__ void sum_parts(f32x4 (&acc)[P::NI][1], float* part, i
   for (int z = 1; z < S; ++z)
 #pragma unroll
     for (int i = 0; i < P::NI; ++i) acc[i][0] += part_at<P>(part, rem_tile * S + z, j, i)[lane];
+}
+
+// The kernel's first argument read again, for what comes behind the loop: its fields are then not kept in scalar registers
+// (and, where those run out, in vector ones) through it.
+template <class A>
+__device__ __forceinline__ A late_args() {
+  A v;
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto* at = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  __builtin_memcpy(&v, (const void*)at, sizeof(A));
+#endif
+  return v;
 }
 
 // bf16 outputs of a wave's block through LDS: `put` 4 consecutive columns of a row, then `store` the block as whole

@@ -40,16 +40,8 @@ struct NtOp {
     seg = -1;
   }
   __device__ __forceinline__ void w_rows(uint32_t ld) {
-    if constexpr (!DUAL) vw.init(ld, rows_n);
-    else {
-      const int lane = opaque_int(threadIdx.x & 63);
-      const int r0 = (ring_wave() & 1) * 8 + (lane >> 3);
-#pragma unroll
-      for (int l = 0; l < NtRows<P>::N; ++l) {
-        const int row = l * 16 + r0;
-        vw.v[l] = row < rows_n ? static_cast<uint32_t>(row) * ld + c16 : kMissing;
-      }
-    }
+    if constexpr (!DUAL) vw.init(ld);
+    else vw.init(ld, 16, (ring_wave() & 1) * 8);
   }
   __device__ __forceinline__ void seek(int t) {
     const int s = lo + t;
@@ -58,7 +50,7 @@ struct NtOp {
         seg = 0;
         xr = tr;
         wr = br;
-        vx.init(ldt_b, rows_m);
+        vx.init(ldt_b);
         w_rows(ldb_b);
       }
       ax = static_cast<uint32_t>(s) * 128u;
@@ -69,15 +61,15 @@ struct NtOp {
         seg = 1;
         xr = xm;
         wr = wm;
-        vx.init(ldx_b, rows_m);
+        vx.init(ldx_b);
         w_rows(ldw_b);
       }
       const int kb = (s - NE) * 128;
       ax = aw = s < hi && kb + static_cast<int>(c16) < kb_total ? static_cast<uint32_t>(kb) : kMissing;
     }
   }
-  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
-  __device__ __forceinline__ void load_w(int l, char* d) const { ring_copy<P>(l, d, wr, vw.v[l] + aw); }
+  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.at(l, ax)); }
+  __device__ __forceinline__ void load_w(int l, char* d) const { ring_copy<P>(l, d, wr, vw.at(l, aw)); }
 };
 
 // NN: rows of the contraction: NSEG segments x_i . W_i behind an extension of NEXT adapters. Extension rows are the
@@ -93,6 +85,7 @@ struct NnOp {
   uint32_t second;  // bit l: copy instruction l takes the second adapter's rows (wr2)
   NtRows<P> vx;
   NnRows<P> vw;
+  uint32_t ve[NEXT > 0 ? ring_loads<P>() : 1];  // with an extension: the offset of each instruction
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint16_t* base, int rows) const {
     return make_rsrc(base, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
   }
@@ -134,19 +127,20 @@ struct NnOp {
     if (NEXT > 0 && s < NE && s < hi) {
       if (seg != 0) {
         xr = make_rsrc(tt, static_cast<uint32_t>(rows_m) * ldt_b);
-        vx.init(ldt_b, rows_m);
+        vx.init(ldt_b);
         wr = er0;
         if constexpr (NEXT > 1) wr2 = er1;
       }
       seg = 0;
       ax = static_cast<uint32_t>(s) * 128u;
-      vw.init(0u, cols);  // (the columns' part; missing ones keep kMissing)
       second = 0;
 #pragma unroll
-      for (int l = 0; l < NnRows<P>::N; ++l) {
-        const int vr = s * 64 + vw.row(l), ph = vr < per ? vr : vr - per;
+      for (int l = 0; l < ring_loads<P>(); ++l) {
+        const int vr = s * 64 + vw.row(l), ph = vr < per ? vr : vr - per, c = vw.col(l);
         const bool is2 = NEXT > 1 && ph >= re0;
-        vw.v[l] = vr < 2 * per ? vw.v[l] + static_cast<uint32_t>(is2 ? ph - re0 : ph) * ldw_b : kMissing;
+        ve[NEXT > 0 ? l : 0] = vr < 2 * per && c < cols
+                                   ? static_cast<uint32_t>(c) * 2 + static_cast<uint32_t>(is2 ? ph - re0 : ph) * ldw_b
+                                   : kMissing;
         if (NEXT > 1) second |= static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(is2 ? 1 : 0)) << l;
       }
     } else {
@@ -154,8 +148,12 @@ struct NnOp {
       const int sg = NSEG == 1 || ms < n0s ? 1 : 2;
       if (seg != sg) {
         if (seg < 1) {
-          vx.init(ldx_b, rows_m);
+          vx.init(ldx_b);
           vw.init(ldw_b, cols);
+          if constexpr (NEXT > 0) {
+#pragma unroll
+            for (int l = 0; l < ring_loads<P>(); ++l) ve[l] = vw.at(l);
+          }
         }
         seg = sg;
         xr = make_rsrc(NSEG > 1 && sg == 2 ? x1 : x0, static_cast<uint32_t>(rows_m) * ldx_b);
@@ -167,17 +165,17 @@ struct NnOp {
       wr = rows_of((NSEG > 1 && sg == 2 ? W1 : W0) + (left > 0 ? static_cast<int64_t>(k0) * (ldw_b / 2) : 0), left);
     }
   }
-  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.v[l] + ax); }
+  __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.at(l, ax)); }
   __device__ __forceinline__ void load_w(int l, char* d) const {
-    if constexpr (NEXT > 1) ring_copy<P>(l, d, (second >> l) & 1 ? wr2 : wr, vw.v[l]);
-    else ring_copy<P>(l, d, wr, vw.v[l]);
+    if constexpr (NEXT > 1) ring_copy<P>(l, d, (second >> l) & 1 ? wr2 : wr, ve[l]);
+    else ring_copy<P>(l, d, wr, NEXT > 0 ? ve[l] : vw.at(l));
   }
 };
 
-// Partial sums of a wave's block (add: added to those that are there).
+// Partial sums of a wave's block.
 template <class P>
 __device__ __forceinline__ void store_part(const f32x4 (&acc)[P::NI][P::NJ], float* part, int64_t ld, int64_t m0,
-                                           int64_t n0, int64_t T, int64_t N, bool add = false) {
+                                           int64_t n0, int64_t T, int64_t N) {
   const int lane = opaque_int(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int j = 0; j < P::NJ; ++j) {
@@ -188,12 +186,11 @@ __device__ __forceinline__ void store_part(const f32x4 (&acc)[P::NI][P::NJ], flo
       const int64_t n = n0 + i * 16 + q * 4;
       float* dst = part + m * ld + n;
       if (ld % 4 == 0 && n + 3 < N) {
-        f32x4* at = reinterpret_cast<f32x4*>(dst);
-        *at = add ? *at + acc[i][j] : acc[i][j];
+        *reinterpret_cast<f32x4*>(dst) = acc[i][j];
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (n + e < N) dst[e] = add ? dst[e] + acc[i][j][e] : acc[i][j][e];
+          if (n + e < N) dst[e] = acc[i][j][e];
       }
     }
   }

@@ -529,23 +529,22 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
 namespace {
 
 struct LossLayout {
-  size_t m = 0, s = 0, tl = 0, lse = 0, rest = 0, share = 0, acc = 0, total = 0;
+  size_t ref = 0, sum = 0, tok[5] = {0, 0, 0, 0, 0}, share = 0, shift = 0, part = 0, total = 0;
   int64_t piece = 0;
 };
 
 LossLayout loss_layout(int64_t T, int64_t K, int64_t V, bool grad) {
   LossLayout L;
   Take take;
-  const size_t blocks = static_cast<size_t>(lora::loss_blocks(V)) * T * 4, tok = static_cast<size_t>(T) * 4;
-  L.m = take(blocks);
-  L.s = take(blocks);
-  L.tl = take(tok);
-  L.lse = take(tok);
-  L.rest = take(tok);
+  const size_t blocks = static_cast<size_t>(lora::loss_blocks(V)) * T * 4;
+  L.ref = take(blocks);
+  L.sum = take(blocks);
+  for (size_t& o : L.tok) o = take(static_cast<size_t>(T) * 4);
   if (grad) {
     L.piece = lora::loss_piece(T, V);
     L.share = take(static_cast<size_t>(T) * L.piece * 2);
-    L.acc = take(lora::loss_acc_bytes(T, K, L.piece));
+    L.shift = take(static_cast<size_t>(lora::loss_blocks(L.piece)) * lora::shift_ld(T));
+    L.part = take(lora::loss_part_bytes(T, K, V));
   }
   L.total = take.off;
   return L;
@@ -586,14 +585,14 @@ int lora_cross_entropy(const void* h, int64_t T, int64_t K, int64_t ldh, const v
   std::memset(&p, 0, sizeof(p));
   p.h = bf(h); p.ldh = ldh; p.W = bf(W); p.target = target; p.dloss = dloss; p.T = T; p.K = K; p.V = V;
   p.loss = loss; p.lse = lse; p.dh = bf(dh); p.lddh = lddh;
-  p.stat_m = reinterpret_cast<float*>(ws + L.m);
-  p.stat_s = reinterpret_cast<float*>(ws + L.s);
-  p.tlogit = reinterpret_cast<float*>(ws + L.tl);
-  p.wlse = reinterpret_cast<float*>(ws + L.lse);
-  p.rest = reinterpret_cast<float*>(ws + L.rest);
+  p.ref = reinterpret_cast<float*>(ws + L.ref);
+  p.sum = reinterpret_cast<float*>(ws + L.sum);
+  float** tok[5] = {&p.tlogit, &p.top, &p.fade, &p.rest, &p.scale};
+  for (int i = 0; i < 5; ++i) *tok[i] = reinterpret_cast<float*>(ws + L.tok[i]);
   p.share = reinterpret_cast<uint16_t*>(ws + L.share);
   p.piece = L.piece;
-  p.acc = reinterpret_cast<float*>(ws + L.acc);
+  p.shift = reinterpret_cast<uint8_t*>(ws + L.shift);
+  p.part = reinterpret_cast<float*>(ws + L.part);
   return lora::launch_vocab_loss(p, static_cast<hipStream_t>(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
