@@ -1,9 +1,9 @@
 // Kernels of a fine-tuning step, bf16: the linear layer with dropout before its adapter, and the gated half of a
 // feed-forward block whose two projections carry adapters, forward and backward, the base weights frozen.
 //
-//   dropout   t = s x' A^T, x' = x . keep                      rank_nt_kernel (the mask formed on its x fragments)
+//   dropout   t = s x' A^T, x' = x . keep                      rank_kernel (the mask formed on its x fragments)
 //             y = x W^T + b + t B^T                            ring_kernel NT, t as extension stages
-//             u = s dy B                                       rank_nn_kernel
+//             u = s dy B                                       rank_kernel
 //             dx = dy W + keep . (u A)                         ring_kernel NN, the mask between extension and base stages
 //             dA = u^T x', dB = dy^T t                         contract_kernel (the mask on the staged x)
 //   gated     h = act(x Wg^T + bg + tg Bg^T) . (x Wu^T + bu + tu Bu^T)      gated_kernel: one GEMM, one rounding
@@ -23,18 +23,18 @@ using namespace pipe;
 
 // ---------------------------------------------------------------------------
 // Rank-wide product over rows contiguous along the contraction (the forward's): 128 tokens and BN adapter rows per
-// workgroup through the LDS ring of the one-adapter producer, K split over grid z; fp32 partial sums. HBM-bound: x is
-// read once (R <= 128).
-using RankNarrow = PCfg<128, 64, 32, 64, 128, 5>;   // up to 64 columns
+// workgroup through the LDS ring of the one-adapter producer, K in splits; fp32 partial sums. HBM-bound: x is read once
+// (R <= 128). Two workgroups on a compute unit, so that the generator's arithmetic in one (as long as the reads) does not
+// keep the other's copies waiting.
+using RankNarrow = PCfg<128, 64, 32, 64, 128, 3>;   // up to 64 columns
 using RankWide = PCfg<128, 128, 32, 128, 128, 4>;
 
 template <class P, bool DROP>
-__global__ __launch_bounds__(P::THREADS) void rank_nt_kernel(RankProduct p, int ks) {
-  __shared__ __attribute__((aligned(1024))) char smem[P::S * P::STAGE_BYTES];
+__device__ __forceinline__ void rank_nt(const RankProduct& p, int ks, int bx, int by, int bz, char* smem) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm0 = wave * P::WM;
-  const int R = p.rank[0] + p.rank[1], q0 = blockIdx.y * P::BN;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
+  const int R = p.rank[0] + p.rank[1], q0 = by * P::BN;
+  const int64_t m0 = static_cast<int64_t>(bx) * P::BM;
   const int rows_m = static_cast<int>(min<int64_t>(P::BM, p.T - m0));
   const int kb_total = static_cast<int>(p.K * 2), nk = (kb_total + P::RB - 1) / P::RB;
   const bool k_tail = kb_total % P::RB != 0;
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(P::THREADS) void rank_nt_kernel(RankProduct p, int 
     const uint32_t c = static_cast<uint32_t>(((lane & 7) ^ ((row >> 1) & 7)) * 16);
     va[l] = g < R ? static_cast<uint32_t>(g < p.rank[0] ? g : g - p.rank[0]) * lda_b + c : 0x80000000u;
   }
-  const int s_lo = static_cast<int>(blockIdx.z) * ks, ns = min(nk, s_lo + ks) - s_lo;
+  const int s_lo = bz * ks, ns = min(nk, s_lo + ks) - s_lo;
   auto issue = [&](int s) {
     char* bx = smem + (s % P::S) * P::STAGE_BYTES;
     const int kb = (s_lo + s) * P::RB;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(P::THREADS) void rank_nt_kernel(RankProduct p, int 
   const int r = lane & 31, h = lane >> 5;
   const int64_t m = m0 + wm0 + r;
   if (m >= p.T) return;
-  float* row = p.part + (static_cast<int64_t>(blockIdx.z) * p.T + m) * R;
+  float* row = p.part + (static_cast<int64_t>(bz) * p.T + m) * R;
 #pragma unroll
   for (int i = 0; i < P::NI; ++i)
 #pragma unroll
@@ -107,9 +107,9 @@ __global__ __launch_bounds__(P::THREADS) void rank_nt_kernel(RankProduct p, int 
 }
 
 // tt = the two terms of scale . sum of the splits, in order; zeros behind them. 4 columns per thread.
-__global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct p, int S) {
+__device__ __forceinline__ void rank_finish(const RankProduct& p, int S, int64_t bx) {
   const int R = p.rank[0] + p.rank[1], ldt = static_cast<int>((2 * R + 63) / 64 * 64), quads = ldt / 4;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t idx = bx * 256 + threadIdx.x;
   if (idx >= p.T * quads) return;
   const int64_t t = idx / quads;
   const int c = static_cast<int>(idx - t * quads) * 4;
@@ -134,6 +134,11 @@ __global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct p, int S) 
     }
   }
   *reinterpret_cast<uint2*>(p.tt + t * ldt + c) = w;
+}
+
+__global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct a, int Sa, int blocks, RankProduct b, int Sb) {
+  if (static_cast<int>(blockIdx.x) < blocks) rank_finish(a, Sa, blockIdx.x);
+  else rank_finish(b, Sb, blockIdx.x - blocks);
 }
 
 // (NJ: blocks of 16 tokens from m0 on)
@@ -249,23 +254,39 @@ __global__ __launch_bounds__(P::THREADS) void ring_join_kernel(RingArgs p, int m
 }
 
 // Rank-wide product over rows of the contraction (the gradient's, B [K, rank] as it lies): 128 tokens and up to 128
-// columns of one adapter per workgroup, K split over grid z. Most of the MFMA's columns are empty for small ranks;
+// columns of one adapter per workgroup, K in splits. Most of the MFMA's columns are empty for small ranks;
 // the kernel is bound by reading x.
-__global__ __launch_bounds__(Ring128::THREADS, Ring128::OCC) void rank_nn_kernel(RankProduct p, int ks, int tiles0) {
+__device__ __forceinline__ void rank_nn(const RankProduct& p, int ks, int bx, int by, int bz, char* smem) {
   using P = Ring128;
-  __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
-  const int side = static_cast<int>(blockIdx.y) >= tiles0 ? 1 : 0;
+  const int tiles0 = (p.rank[0] + 127) / 128, side = by >= tiles0 ? 1 : 0;
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * P::BM;
-  const int64_t n0 = static_cast<int64_t>(static_cast<int>(blockIdx.y) - (side ? tiles0 : 0)) * P::BN;
-  const int NS = static_cast<int>((p.K + 63) / 64), s_lo = static_cast<int>(blockIdx.z) * ks, s_hi = min(NS, s_lo + ks);
+  const int64_t m0 = static_cast<int64_t>(bx) * P::BM;
+  const int64_t n0 = static_cast<int64_t>(by - (side ? tiles0 : 0)) * P::BN;
+  const int NS = static_cast<int>((p.K + 63) / 64), s_lo = bz * ks, s_hi = min(NS, s_lo + ks);
   NnOp<P, 1, 0> op;
   op.init(&p.x[side], p.ldx, &p.A[side], &p.K, p.T, p.rank[side], m0, n0, s_lo, s_hi);
   f32x4 acc[P::NI][P::NJ];
   ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
   const int R = p.rank[0] + p.rank[1], c0 = side ? p.rank[0] : 0;
-  store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.z) * p.T * R + c0, R, m0 + wm0, n0 + wn0, p.T, p.rank[side]);
+  store_part<P>(acc, p.part + static_cast<int64_t>(bz) * p.T * R + c0, R, m0 + wm0, n0 + wn0, p.T, p.rank[side]);
+}
+
+// The first n_nt workgroups make the one product (grid (m-tiles, rows, splits) counted x first), the others the other.
+template <class P, bool DROP>
+__global__ __launch_bounds__(256, P::BN == 64 ? 2 : 1) void rank_kernel(RankProduct a, int ks_a, int n_nt, int chunks_a,
+                                                                        RankProduct b, int ks_b, int chunks_b) {
+  static_assert(P::THREADS == 256 && Ring128::THREADS == 256, "one block size");
+  constexpr int kNt = P::S * P::STAGE_BYTES, kNn = Ring128::SLOTS * Ring128::SLOT_BYTES;
+  __shared__ __attribute__((aligned(1024))) char smem[kNt > kNn ? kNt : kNn];
+  const int id = blockIdx.x;
+  if (id < n_nt) {
+    const int mt = static_cast<int>((a.T + 127) / 128), rest = id / mt;
+    rank_nt<P, DROP>(a, ks_a, id - rest * mt, rest % chunks_a, rest / chunks_a, smem);
+  } else {
+    const int mt = static_cast<int>((b.T + 127) / 128), i = id - n_nt, rest = i / mt;
+    rank_nn(b, ks_b, i - rest * mt, rest % chunks_b, rest / chunks_b, smem);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -409,9 +430,10 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict
 }
 
 // ---------------------------------------------------------------------------
-// Token contraction: 256 rows of P^T x 64 columns of Q per workgroup, 64 tokens per stage, a ring of three stages
-// [64 t][256] of P and [64 t][64 first terms | 64 second terms] of Q, both read with the transposing LDS read. Token
-// chunks over grid y leave fp32 partial sums that contract_reduce_kernel adds in order. HBM-bound: P is read once.
+// Token contraction: 256 rows of P^T x 64 columns of Q per workgroup, 32 tokens per stage, a ring of three stages
+// [32 t][256] of P and [32 t][64 first terms | 64 second terms] of Q, both read with the transposing LDS read, two
+// workgroups on a compute unit. Token chunks over grid y leave fp32 partial sums that contract_reduce_kernel adds in
+// order. HBM-bound: P is read once (and, masked, the generator's arithmetic takes about as long).
 constexpr int kCtP = kCtT * kCtI * 2, kCtQ = kCtT * 2 * kCtJ * 2, kCtStage = kCtP + kCtQ;
 
 __device__ __forceinline__ bf16x8 tr_frag(const char* at, int row4) {
@@ -423,43 +445,49 @@ __device__ __forceinline__ bf16x8 tr_frag(const char* at, int row4) {
 // (restrict: the copies in flight go to other slots; see ring_stage)
 __device__ __forceinline__ void contract_stage(f32x4 (&acc)[4][kCtJ / 16], const char* __restrict__ pb,
                                                const char* __restrict__ qb, uint32_t pa, uint32_t qa, int nj) {
+  bf16x8 af[4];
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-    bf16x8 af[4];
+  for (int ib = 0; ib < 4; ++ib) af[ib] = tr_frag(pb + (pa ^ static_cast<uint32_t>(ib << 5)), 4 * 512);
 #pragma unroll
-    for (int ib = 0; ib < 4; ++ib) af[ib] = tr_frag(pb + (pa ^ static_cast<uint32_t>(ib << 5)) + kk * 32 * 512, 4 * 512);
+  for (int jb = 0; jb < kCtJ / 16; ++jb) {
+    if (jb >= nj) continue;
 #pragma unroll
-    for (int jb = 0; jb < kCtJ / 16; ++jb) {
-      if (jb >= nj) continue;
+    for (int term = 0; term < 2; ++term) {
+      const bf16x8 bq = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)), 4 * 256);
 #pragma unroll
-      for (int term = 0; term < 2; ++term) {
-        const bf16x8 bq = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)) + kk * 32 * 256, 4 * 256);
-#pragma unroll
-        for (int ib = 0; ib < 4; ++ib)
-          acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq, acc[ib][jb], 0, 0, 0);
-      }
+      for (int ib = 0; ib < 4; ++ib)
+        acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq, acc[ib][jb], 0, 0, 0);
     }
   }
 }
 
 template <bool DROP>
-__global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_t chunk, int slices0) {
+__global__ __launch_bounds__(256, 2) void contract_kernel(Contract p, int S, int64_t chunk) {
   __shared__ __attribute__((aligned(1024))) char smem[3 * kCtStage];
   const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
-  const int ti = static_cast<int>(blockIdx.z) >= slices0 ? 1 : 0;
+  int ti = 0, id = blockIdx.x;
+  int64_t before = 0;  // elements of the tasks before this one
+  while (ti + 1 < p.n_tasks) {
+    const int n = static_cast<int>((p.task[ti].M + kCtI - 1) / kCtI) * ((p.task[ti].J + kCtJ - 1) / kCtJ);
+    if (id < n) break;
+    id -= n;
+    before += p.task[ti].M * p.task[ti].J;
+    ++ti;
+  }
   const ContractTask& k = p.task[ti];
-  const int j0 = (static_cast<int>(blockIdx.z) - (ti ? slices0 : 0)) * kCtJ, jn = min(kCtJ, k.J - j0), nj = (jn + 15) / 16;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kCtI;
-  const int cols = static_cast<int>(min<int64_t>(kCtI, p.M - i0));
+  const int it = static_cast<int>((k.M + kCtI - 1) / kCtI);
+  const int j0 = id / it * kCtJ, jn = min(kCtJ, k.J - j0), nj = (jn + 15) / 16;
+  const int64_t i0 = static_cast<int64_t>(id % it) * kCtI;
+  const int cols = static_cast<int>(min<int64_t>(kCtI, k.M - i0));
   const int z = blockIdx.y;
   const int64_t t_lo = z * chunk, t_hi = min<int64_t>(p.T, t_lo + chunk);
   const int nst = t_hi > t_lo ? static_cast<int>((t_hi - t_lo + kCtT - 1) / kCtT) : 0;
-  const uint32_t ldp_b = static_cast<uint32_t>(k.ldp * 2), ldt_b = static_cast<uint32_t>(p.ldt * 2);
-  // per-lane offsets: 8 instructions of P (2 rows of 512 bytes each), 4 of Q (4 rows of 256)
-  uint32_t vp[8], vq[4];
-  int prow[8], pcol[8];
+  const uint32_t ldp_b = static_cast<uint32_t>(k.ldp * 2), ldt_b = static_cast<uint32_t>(k.ldt * 2);
+  // per-lane offsets: 4 instructions of P (2 rows of 512 bytes each), 2 of Q (4 rows of 256)
+  uint32_t vp[4], vq[2];
+  int prow[4], pcol[4];
 #pragma unroll
-  for (int l = 0; l < 8; ++l) {
+  for (int l = 0; l < 4; ++l) {
     const int sl = (l * 4 + wave) * 64 + lane, t = sl / 32, pc = sl % 32, f = (t & 3) | (((t >> 3) & 1) << 2);
     const int col = (((pc >> 1) ^ f) * 2 + (pc & 1)) * 8;
     vp[l] = col < cols ? static_cast<uint32_t>(t) * ldp_b + col * 2 : kMissing;
@@ -467,10 +495,10 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
     pcol[l] = col;
   }
 #pragma unroll
-  for (int l = 0; l < 4; ++l) {
+  for (int l = 0; l < 2; ++l) {
     const int sl = (l * 4 + wave) * 64 + lane, t = sl / 16, pc = sl % 16, f = (t & 3) | (((t >> 3) & 1) << 2);
     const int col = (((pc >> 1) ^ f) * 2 + (pc & 1)) * 8, c = col & 63;
-    vq[l] = c < jn ? static_cast<uint32_t>(t) * ldt_b + static_cast<uint32_t>((col < 64 ? 0 : p.R) + k.q_col + j0 + c) * 2
+    vq[l] = c < jn ? static_cast<uint32_t>(t) * ldt_b + static_cast<uint32_t>((col < 64 ? 0 : k.R) + k.q_col + j0 + c) * 2
                    : kMissing;
   }
   auto issue = [&](int s) {
@@ -480,16 +508,17 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
     const int64_t at = rows > 0 ? t0 : 0;
     const __amdgpu_buffer_rsrc_t pr = make_rsrc(
         k.P + at * k.ldp + i0, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldp_b + static_cast<uint32_t>(cols) * 2 : 0u);
-    const __amdgpu_buffer_rsrc_t qr = make_rsrc(p.tt + at * p.ldt, static_cast<uint32_t>(rows) * ldt_b);
-#pragma unroll
-    for (int l = 0; l < 8; ++l)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (lds_void*)(b + (l * 4 + wave) * 1024), 16, vp[l], 0, 0, 0);
+    const __amdgpu_buffer_rsrc_t qr = make_rsrc(k.tt + at * k.ldt, static_cast<uint32_t>(rows) * ldt_b);
 #pragma unroll
     for (int l = 0; l < 4; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (lds_void*)(b + (l * 4 + wave) * 1024), 16, vp[l], 0, 0, 0);
+#pragma unroll
+    for (int l = 0; l < 2; ++l)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, (lds_void*)(b + kCtP + (l * 4 + wave) * 1024), 16, vq[l], 0, 0, 0);
   };
   Dropper d;
-  if constexpr (DROP) d.init(p.drop, p.M);
+  const bool masked = DROP && k.masked;
+  if constexpr (DROP) d.init(p.drop, k.M);
   f32x4 acc[4][kCtJ / 16];
 #pragma unroll
   for (int ib = 0; ib < 4; ++ib)
@@ -501,23 +530,26 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
   issue(0);
   issue(1);
   for (int s = 0; s < nst; ++s) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(12));  // stage s landed; s + 1 may be in flight
-    stage_barrier();                             // (and every wave is done reading stage s - 1)
+    u32x4 mask[4];
+    if (masked) {  // (needs no data: formed while the stage's copies are on their way)
+#pragma unroll
+      for (int l = 0; l < 4; ++l)
+        mask[l] = d.masks(t_lo + static_cast<int64_t>(s) * kCtT + prow[l], (i0 + pcol[l]) / 8);
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(6));  // stage s landed; s + 1 may be in flight
+    stage_barrier();                            // (and every wave is done reading stage s - 1)
     issue(s + 2);
     char* b = smem + (s % 3) * kCtStage;
-    if constexpr (DROP) {
+    if (masked) {
 #pragma unroll
-      for (int l = 0; l < 8; ++l) {
-        u32x4* at = reinterpret_cast<u32x4*>(b + ((l * 4 + wave) * 64 + lane) * 16);
-        *at &= d.masks(t_lo + static_cast<int64_t>(s) * kCtT + prow[l], (i0 + pcol[l]) / 8);
-      }
+      for (int l = 0; l < 4; ++l) *reinterpret_cast<u32x4*>(b + ((l * 4 + wave) * 64 + lane) * 16) &= mask[l];
       stage_barrier();
     }
     contract_stage(acc, b, b + kCtP, pa, qa, nj);
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   // lane (r, q) of block (ib, jb): rows i = 64 wave + 16 ib + 4 q + e of P^T, column j = 16 jb + r
-  float* part = p.part + (ti ? static_cast<int64_t>(S) * p.M * p.task[0].J : 0) + static_cast<int64_t>(z) * p.M * k.J;
+  float* part = p.part + (before * S + z * k.M * k.J);
 #pragma unroll
   for (int jb = 0; jb < kCtJ / 16; ++jb) {
     const int j = j0 + jb * 16 + r;
@@ -525,9 +557,9 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
       const int64_t i = i0 + wave * 64 + ib * 16 + 4 * q;
-      if (i >= p.M) continue;  // (M is a multiple of 8: four rows exist together)
-      if (p.transposed) {
-        *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(j) * p.M + i) = acc[ib][jb];
+      if (i >= k.M) continue;  // (M is a multiple of 8: four rows exist together)
+      if (k.transposed) {
+        *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(j) * k.M + i) = acc[ib][jb];
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) part[(i + e) * k.J + j] = acc[ib][jb][e];
@@ -540,13 +572,15 @@ __global__ __launch_bounds__(256) void contract_kernel(Contract p, int S, int64_
 __global__ __launch_bounds__(256) void contract_reduce_kernel(Contract p, int S) {
   const int ti = blockIdx.y;
   const ContractTask& k = p.task[ti];
-  const int64_t n = p.M * k.J, idx = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int64_t n = k.M * k.J, idx = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (idx >= n) return;
-  const float* src = p.part + (ti ? static_cast<int64_t>(S) * p.M * p.task[0].J : 0) + idx;
+  int64_t before = 0;
+  for (int i = 0; i < ti; ++i) before += p.task[i].M * p.task[i].J;
+  const float* src = p.part + before * S + idx;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int z = 0; z < S; ++z) v += *reinterpret_cast<const f32x4*>(src + z * n);
-  const int64_t cut = p.transposed ? static_cast<int64_t>(k.split) * p.M : n;
+  const int64_t cut = k.transposed ? static_cast<int64_t>(k.split) * k.M : n;
   void* out = idx < cut ? k.out[0] : k.out[1];
   const int64_t at = idx < cut ? idx : idx - cut;
   if (out == nullptr) return;
@@ -570,26 +604,37 @@ unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + p
 
 }  // namespace
 
-hipError_t launch_rank_product(const RankProduct& p, bool nn, hipStream_t s) {
-  const int64_t R0 = p.rank[0], R1 = p.rank[1], R = R0 + R1;
-  int S, ks;
-  rank_plan(p.T, p.K, rank_tasks(R0, R1, nn), &S, &ks);
-  if (nn) {
-    const int t0 = static_cast<int>((R0 + 127) / 128);
-    hipLaunchKernelGGL(rank_nn_kernel, dim3(blocks_of(p.T, 128), static_cast<unsigned>(rank_tasks(R0, R1, true)),
-                                            static_cast<unsigned>(S)), dim3(256), 0, s, p, ks, t0);
-  } else {
-    const bool narrow = R <= 64;
-    const dim3 grid(blocks_of(p.T, 128), blocks_of(R, narrow ? 64 : 128), static_cast<unsigned>(S));
-    const bool drop = p.drop.thr != 0;
-    if (narrow && drop) hipLaunchKernelGGL((rank_nt_kernel<RankNarrow, true>), grid, dim3(256), 0, s, p, ks);
-    else if (narrow) hipLaunchKernelGGL((rank_nt_kernel<RankNarrow, false>), grid, dim3(256), 0, s, p, ks);
-    else if (drop) hipLaunchKernelGGL((rank_nt_kernel<RankWide, true>), grid, dim3(256), 0, s, p, ks);
-    else hipLaunchKernelGGL((rank_nt_kernel<RankWide, false>), grid, dim3(256), 0, s, p, ks);
+hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hipStream_t s) {
+  RankProduct a = {}, b = {};
+  int Sa = 0, ka = 1, n_nt = 0, ca = 1, Sb = 0, kb = 1, n_nn = 0, cb = 1;
+  bool narrow = true, drop = false;
+  if (nt != nullptr) {
+    a = *nt;
+    const int64_t R = a.rank[0] + a.rank[1];
+    narrow = R <= 64;
+    drop = a.drop.thr != 0;
+    rank_plan(a.T, a.K, rank_tasks(R, 0, false), &Sa, &ka);
+    ca = static_cast<int>(narrow ? 1 : (R + 127) / 128);
+    n_nt = static_cast<int>((a.T + 127) / 128) * ca * Sa;
   }
-  hipError_t e = hipGetLastError();
+  if (nn != nullptr) {
+    b = *nn;
+    rank_plan(b.T, b.K, rank_tasks(b.rank[0], b.rank[1], true), &Sb, &kb);
+    cb = static_cast<int>(rank_tasks(b.rank[0], b.rank[1], true));
+    n_nn = static_cast<int>((b.T + 127) / 128) * cb * Sb;
+  }
+  const dim3 grid(static_cast<unsigned>(n_nt + n_nn)), block(256);
+  if (narrow && drop) hipLaunchKernelGGL((rank_kernel<RankNarrow, true>), grid, block, 0, s, a, ka, n_nt, ca, b, kb, cb);
+  else if (narrow) hipLaunchKernelGGL((rank_kernel<RankNarrow, false>), grid, block, 0, s, a, ka, n_nt, ca, b, kb, cb);
+  else if (drop) hipLaunchKernelGGL((rank_kernel<RankWide, true>), grid, block, 0, s, a, ka, n_nt, ca, b, kb, cb);
+  else hipLaunchKernelGGL((rank_kernel<RankWide, false>), grid, block, 0, s, a, ka, n_nt, ca, b, kb, cb);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rank_finish_kernel, dim3(blocks_of(p.T * (pair_ld(R) / 4), 256)), dim3(256), 0, s, p, S);
+  auto blocks = [](const RankProduct& p, int S) {
+    return S > 0 ? blocks_of(p.T * (pair_ld(p.rank[0] + p.rank[1]) / 4), 256) : 0u;
+  };
+  const unsigned ba = blocks(a, Sa), bb = blocks(b, Sb);
+  hipLaunchKernelGGL(rank_finish_kernel, dim3(ba + bb), dim3(256), 0, s, a, Sa, static_cast<int>(ba), b, Sb);
   return hipGetLastError();
 }
 
@@ -652,18 +697,23 @@ hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t ldd
 }
 
 hipError_t launch_contract(const Contract& p, hipStream_t s) {
-  const int64_t J0 = p.task[0].J, J1 = p.n_tasks > 1 ? p.task[1].J : 0, slices = contract_slices(J0, J1);
+  int64_t tiles = 0, most = 0;
+  bool drop = false;
+  for (int i = 0; i < p.n_tasks; ++i) {
+    tiles += contract_tiles(p.task[i].M, p.task[i].J);
+    most = p.task[i].M * p.task[i].J > most ? p.task[i].M * p.task[i].J : most;
+    drop = drop || (p.task[i].masked && p.drop.thr != 0);
+  }
   int S;
   int64_t chunk;
-  contract_plan(p.T, p.M, slices, &S, &chunk);
-  const dim3 grid(blocks_of(p.M, kCtI), static_cast<unsigned>(S), static_cast<unsigned>(slices));
-  const int s0 = static_cast<int>(contract_slices(J0, 0));
-  if (p.drop.thr != 0) hipLaunchKernelGGL(contract_kernel<true>, grid, dim3(256), 0, s, p, S, chunk, s0);
-  else hipLaunchKernelGGL(contract_kernel<false>, grid, dim3(256), 0, s, p, S, chunk, s0);
+  contract_plan(p.T, tiles, &S, &chunk);
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(S));
+  if (drop) hipLaunchKernelGGL(contract_kernel<true>, grid, dim3(256), 0, s, p, S, chunk);
+  else hipLaunchKernelGGL(contract_kernel<false>, grid, dim3(256), 0, s, p, S, chunk);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(contract_reduce_kernel, dim3(blocks_of(p.M * (J0 > J1 ? J0 : J1), 1024), static_cast<unsigned>(p.n_tasks)),
-                     dim3(256), 0, s, p, S);
+  hipLaunchKernelGGL(contract_reduce_kernel, dim3(blocks_of(most, 1024), static_cast<unsigned>(p.n_tasks)), dim3(256), 0, s,
+                     p, S);
   return hipGetLastError();
 }
 

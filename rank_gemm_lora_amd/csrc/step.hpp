@@ -30,27 +30,36 @@ struct RankProduct {
   float* part;            // [S, T, R]
   uint16_t* tt;           // [T, pair_ld(R)]
 };
-// Splits of K, fixed by the sizes: enough workgroups of 128 tokens for two on each of 256 compute units, at least 4
-// stages of 64 each.
+// Splits of K, fixed by the sizes: as few rounds of workgroups of 128 tokens, two on each of 256 compute units, as make
+// the least stages of 64 one after the other (3 more for each round's start); a split's sums cost a write and a read.
+// (18871 tokens, 8960 inputs, masked: 3 splits, 444 workgroups one to a unit in two rounds, took 116 us.)
 constexpr int kRankMaxSplits = 16;
 inline void rank_plan(int64_t T, int64_t K, int64_t tasks, int* S, int* ks) {
   const int64_t mt = (T + 127) / 128 * tasks, nk = (K + 63) / 64;
-  int64_t s = mt > 0 ? 512 / mt : 1;
-  const int64_t smax = nk / 4 > 1 ? nk / 4 : 1;
-  s = s < 1 ? 1 : (s > kRankMaxSplits ? kRankMaxSplits : s);
-  s = s > smax ? smax : s;
-  *ks = static_cast<int>((nk + s - 1) / s);
-  *S = static_cast<int>((nk + *ks - 1) / *ks);
+  int64_t least = 0;
+  *S = 1;
+  *ks = static_cast<int>(nk);
+  for (int64_t s = 1; s <= kRankMaxSplits; ++s) {
+    const int64_t k = (nk + s - 1) / s;
+    if (s > 1 && (k < 3 || (nk + k - 1) / k != s)) continue;
+    const int64_t est = (mt * s + 511) / 512 * (k + 3);
+    if (least == 0 || est < least) {
+      least = est;
+      *S = static_cast<int>(s);
+      *ks = static_cast<int>(k);
+    }
+  }
 }
 inline int64_t rank_tasks(int64_t R0, int64_t R1, bool nn) {
-  return nn ? (R0 + 127) / 128 + (R1 + 127) / 128 : (R0 + R1 + 127) / 128;
+  return nn ? (R0 + 127) / 128 + (R1 + 127) / 128 : R0 + R1 <= 64 ? 1 : 2 * ((R0 + R1 + 127) / 128);
 }
 inline size_t rank_part_bytes(int64_t T, int64_t K, int64_t R0, int64_t R1, bool nn) {
   int S, ks;
   rank_plan(T, K, rank_tasks(R0, R1, nn), &S, &ks);
   return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R0 + R1) * 4;
 }
-hipError_t launch_rank_product(const RankProduct& p, bool nn, hipStream_t s);
+// Either or both (null: not there), of the same tokens; each with partial sums of its own.
+hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hipStream_t s);
 
 // ---------------------------------------------------------------- ring GEMMs
 // y [T, N] = sum over segments of x_i . W_i (NT: W [N, K], NN: W [K, N]) + tt . [E; E] (tt as above; NT: E_i [N, rank_i],
@@ -136,38 +145,47 @@ hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t ldd
 // out_i [J, M] (transposed: one adapter's rows behind the other's) or [M, J] = P^T . Q over the tokens, Q the columns
 // q_col .. of a rank-wide product's rows (both terms). P masked by drop when given.
 struct ContractTask {
-  const uint16_t* P; int64_t ldp;
+  const uint16_t* P; int64_t ldp, M;
+  const uint16_t* tt; int64_t ldt;
+  int R;            // where the second term's columns begin
   int q_col, J;
+  bool transposed, masked;
   void* out[2];     // transposed: rows [0, split) and [split, J); else out[0]
   int split;
 };
+constexpr int kMaxContract = 3;
 struct Contract {
-  ContractTask task[2]; int n_tasks;
-  int64_t T, M;
-  const uint16_t* tt; int64_t ldt; int R;  // R: where the second term's columns begin
-  Drop drop;
-  bool transposed;
+  ContractTask task[kMaxContract]; int n_tasks;
+  int64_t T;
+  Drop drop;        // of the masked tasks' P
   bool out_bf16;
   float* part;      // [task][S, M, J]
 };
-constexpr int kCtI = 256, kCtJ = 64, kCtT = 64;
-inline void contract_plan(int64_t T, int64_t M, int64_t slices, int* S, int64_t* chunk) {
-  const int64_t tiles = (M + kCtI - 1) / kCtI * slices;
-  int64_t s = tiles > 0 ? 256 / tiles : 1;
-  const int64_t smax = (T + 4 * kCtT - 1) / (4 * kCtT);
-  s = s < 1 ? 1 : (s > smax ? smax : s);
-  s = s < 1 ? 1 : (s > 64 ? 64 : s);
-  int64_t c = (T + s - 1) / s;
-  c = (c + kCtT - 1) / kCtT * kCtT;
-  *chunk = c < kCtT ? kCtT : c;
-  *S = T > 0 ? static_cast<int>((T + *chunk - 1) / *chunk) : 1;
+constexpr int kCtI = 256, kCtJ = 64, kCtT = 32;
+inline int64_t contract_tiles(int64_t M, int64_t J) { return (M + kCtI - 1) / kCtI * ((J + kCtJ - 1) / kCtJ); }
+// Token chunks: as rank_plan, tiles of 256 x 64 two to a compute unit, at most 64 chunks of whole stages of 32 tokens.
+inline void contract_plan(int64_t T, int64_t tiles, int* S, int64_t* chunk) {
+  const int64_t nst = (T + kCtT - 1) / kCtT;
+  int64_t least = 0;
+  *S = 1;
+  *chunk = (nst > 0 ? nst : 1) * kCtT;
+  for (int64_t s = 1; s <= 64 && s <= nst; ++s) {
+    const int64_t k = (nst + s - 1) / s;
+    if ((nst + k - 1) / k != s) continue;
+    // (a chunk's sums, 64 KB, cost about as much as four stages' reads)
+    const int64_t est = (tiles * s + 511) / 512 * (k + 7);
+    if (least == 0 || est < least) {
+      least = est;
+      *S = static_cast<int>(s);
+      *chunk = k * kCtT;
+    }
+  }
 }
-inline int64_t contract_slices(int64_t J0, int64_t J1) { return (J0 + kCtJ - 1) / kCtJ + (J1 + kCtJ - 1) / kCtJ; }
-inline size_t contract_part_bytes(int64_t T, int64_t M, int64_t J0, int64_t J1) {
+inline size_t contract_part_bytes(int64_t T, int64_t tiles, int64_t elements) {  // elements: M J of all tasks
   int S;
   int64_t c;
-  contract_plan(T, M, contract_slices(J0, J1), &S, &c);
-  return static_cast<size_t>(S) * static_cast<size_t>(M) * static_cast<size_t>(J0 + J1) * 4;
+  contract_plan(T, tiles, &S, &c);
+  return static_cast<size_t>(S) * static_cast<size_t>(elements) * 4;
 }
 hipError_t launch_contract(const Contract& p, hipStream_t s);
 

@@ -104,23 +104,24 @@ hipError_t zero_grad(void* g, int64_t n, int32_t dtype, hipStream_t s) {
 // ------------------------------------------------------------------------------------------- dropout
 
 struct DropLayout {
-  size_t tt = 0, ut = 0, part = 0, total = 0;
+  size_t tt = 0, ut = 0, part = 0, part2 = 0, total = 0;
 };
 // one layout for both directions (the forward uses a part of it)
 DropLayout drop_layout(int64_t T, int64_t K, int64_t N, int64_t R, bool backward) {
   DropLayout L;
   Take take;
   L.tt = take(tt_bytes(T, R));
-  size_t part = std::max(lora::rank_part_bytes(T, K, R, 0, false), lora::ring_part_bytes(T, N, stages(K, 0, R)));
+  // (an inactive adapter has no extension: fewer stages, other parts)
+  size_t part = std::max(lora::rank_part_bytes(T, K, R, 0, false),
+                         std::max(lora::ring_part_bytes(T, N, stages(K, 0, R)), lora::ring_part_bytes(T, N, stages(K, 0, 0))));
   if (backward) {
     L.ut = take(tt_bytes(T, R));
-    part = std::max(part, lora::rank_part_bytes(T, N, R, 0, true));
-    part = std::max(part, lora::ring_part_bytes(T, K, stages(N, 0, R)));
-    part = std::max(part, std::max(lora::contract_part_bytes(T, K, R, 0), lora::contract_part_bytes(T, N, R, 0)));
+    L.part2 = take(lora::rank_part_bytes(T, N, R, 0, true));
+    part = std::max(part, std::max(lora::ring_part_bytes(T, K, stages(N, 0, R)), lora::ring_part_bytes(T, K, stages(N, 0, 0))));
+    const int64_t ta = lora::contract_tiles(K, R), tb = lora::contract_tiles(N, R);
+    part = std::max(part, std::max(lora::contract_part_bytes(T, ta, K * R), lora::contract_part_bytes(T, tb, N * R)));
+    part = std::max(part, lora::contract_part_bytes(T, ta + tb, (K + N) * R));
   }
-  // (an inactive adapter has no extension: fewer stages, other splits)
-  part = std::max(part, lora::ring_part_bytes(T, N, stages(K, 0, 0)));
-  if (backward) part = std::max(part, lora::ring_part_bytes(T, K, stages(N, 0, 0)));
   L.part = take(part);
   L.total = take.off;
   return L;
@@ -186,7 +187,7 @@ int lora_linear_dropout_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
     r.x[0] = bf(x); r.ldx = ldx; r.A[0] = bf(A); r.rank[0] = rank; r.scale[0] = a.scale; r.T = T; r.K = K; r.drop = drop;
     r.part = reinterpret_cast<float*>(ws + L.part);
     r.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
-    if (lora::launch_rank_product(r, false, st) != hipSuccess) return LORA_ERR_HIP;
+    if (lora::launch_rank_products(&r, nullptr, st) != hipSuccess) return LORA_ERR_HIP;
     g.tt = r.tt; g.ldt = lora::pair_ld(rank); g.E[0] = bf(B); g.re[0] = rank;
   }
   g.x[0] = bf(x); g.ldx = ldx; g.W[0] = bf(W); g.K[0] = K; g.n_seg = 1; g.bias[0] = bf(bias); g.T = T; g.N = N;
@@ -236,13 +237,17 @@ int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
   const int64_t ldt = lora::pair_ld(rank);
   RankProduct u;
   std::memset(&u, 0, sizeof(u));
-  u.rank[0] = rank; u.scale[0] = a.scale; u.T = T; u.part = part;
+  u.rank[0] = rank; u.scale[0] = a.scale; u.T = T;
   RankProduct t = u;
-  if (a.rank > 0 && (dx != nullptr || dA != nullptr)) {  // u = s dy B
-    u.x[0] = bf(dy); u.ldx = lddy; u.A[0] = bf(B); u.K = N;
-    u.tt = reinterpret_cast<uint16_t*>(ws + L.ut);
-    if (lora::launch_rank_product(u, true, st) != hipSuccess) return LORA_ERR_HIP;
-  }
+  // u = s dy B, and t = s x' A^T as the forward forms it
+  u.x[0] = bf(dy); u.ldx = lddy; u.A[0] = bf(B); u.K = N; u.part = reinterpret_cast<float*>(ws + L.part2);
+  u.tt = reinterpret_cast<uint16_t*>(ws + L.ut);
+  t.x[0] = bf(x); t.ldx = ldx; t.A[0] = bf(A); t.K = K; t.drop = drop; t.part = part;
+  t.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
+  const bool need_u = a.rank > 0 && (dx != nullptr || dA != nullptr), need_t = a.rank > 0 && dB != nullptr;
+  if ((need_u || need_t) &&
+      lora::launch_rank_products(need_t ? &t : nullptr, need_u ? &u : nullptr, st) != hipSuccess)
+    return LORA_ERR_HIP;
   if (dx != nullptr) {
     RingArgs g;
     std::memset(&g, 0, sizeof(g));
@@ -254,24 +259,15 @@ int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
     g.y = bf(dx); g.ldy = lddx; g.part = part;
     if (lora::launch_ring(g, true, st) != hipSuccess) return LORA_ERR_HIP;
   }
-  if (a.rank == 0) return LORA_OK;
+  if (a.rank == 0 || (dA == nullptr && dB == nullptr)) return LORA_OK;
   Contract c;
   std::memset(&c, 0, sizeof(c));
-  c.n_tasks = 1; c.T = T; c.ldt = ldt; c.R = rank; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part;
-  if (dB != nullptr) {  // dB = dy^T t, t = s x' A^T as the forward forms it
-    t.x[0] = bf(x); t.ldx = ldx; t.A[0] = bf(A); t.K = K; t.drop = drop;
-    t.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
-    if (lora::launch_rank_product(t, false, st) != hipSuccess) return LORA_ERR_HIP;
-    c.task[0] = lora::ContractTask{bf(dy), lddy, 0, rank, {dB, nullptr}, rank};
-    c.M = N; c.tt = t.tt;
-    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
-  }
-  if (dA != nullptr) {  // dA = u^T x'
-    c.task[0] = lora::ContractTask{bf(x), ldx, 0, rank, {dA, nullptr}, rank};
-    c.M = K; c.tt = u.tt; c.transposed = true; c.drop = drop;
-    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
-  }
-  return LORA_OK;
+  c.T = T; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part; c.drop = drop;
+  if (dA != nullptr)  // u^T x'
+    c.task[c.n_tasks++] = lora::ContractTask{bf(x), ldx, K, u.tt, ldt, rank, 0, rank, true, true, {dA, nullptr}, rank};
+  if (dB != nullptr)  // dy^T t
+    c.task[c.n_tasks++] = lora::ContractTask{bf(dy), lddy, N, t.tt, ldt, rank, 0, rank, false, false, {dB, nullptr}, rank};
+  return lora::launch_contract(c, st) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
 }  // extern "C"
@@ -317,8 +313,9 @@ GatedLayout gated_bwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_
     const int64_t a = i & 1 ? 0 : rg, b = i & 2 ? 0 : ru;
     if (a + b > 0) {
       part = std::max(part, lora::rank_part_bytes(T, F, a, b, true));
-      part = std::max(part, lora::contract_part_bytes(T, K, a + b, 0));
-      part = std::max(part, lora::contract_part_bytes(T, F, a, b));
+      const int64_t ta = lora::contract_tiles(K, a + b), tb = lora::contract_tiles(F, a) + lora::contract_tiles(F, b);
+      part = std::max(part, std::max(lora::contract_part_bytes(T, ta, K * (a + b)), lora::contract_part_bytes(T, tb, F * (a + b))));
+      part = std::max(part, lora::contract_part_bytes(T, ta + tb, (K + F) * (a + b)));
     }
     part = std::max(part, lora::ring_part_bytes(T, K, stages(F, F, a + b)));
   }
@@ -368,7 +365,7 @@ hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const
       r.A[i] = bf(s[i].A); r.rank[i] = static_cast<int>(s[i].rank); r.scale[i] = s[i].scale;
       g.E[i] = bf(s[i].B); g.re[i] = static_cast<int>(s[i].rank);
     }
-    const hipError_t e = lora::launch_rank_product(r, false, st);
+    const hipError_t e = lora::launch_rank_products(&r, nullptr, st);
     if (e != hipSuccess) return e;
     g.tt = tt; g.ldt = lora::pair_ld(R);
   }
@@ -487,7 +484,7 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
     for (int i = 0; i < 2; ++i) {
       v.A[i] = bf(s[i].B); v.rank[i] = static_cast<int>(s[i].rank); v.scale[i] = s[i].scale;
     }
-    if (lora::launch_rank_product(v, true, st) != hipSuccess) return LORA_ERR_HIP;
+    if (lora::launch_rank_products(nullptr, &v, st) != hipSuccess) return LORA_ERR_HIP;
   }
   if (dx != nullptr) {
     RingArgs g;
@@ -503,23 +500,20 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
     if (lora::launch_ring(g, true, st) != hipSuccess) return LORA_ERR_HIP;
   }
   if (R == 0) return LORA_OK;
+  if (!want_a && !want_b) return LORA_OK;
   Contract c;
   std::memset(&c, 0, sizeof(c));
-  c.T = T; c.ldt = ldt; c.R = static_cast<int>(R); c.out_bf16 = grad_dtype == LORA_BF16; c.part = part;
-  const int r0 = static_cast<int>(s[0].rank), r1 = static_cast<int>(s[1].rank);
-  if (want_b) {  // dB = d^T t of each projection
-    c.M = F; c.tt = reinterpret_cast<const uint16_t*>(keep + saved_tt_at(T, F));
-    c.n_tasks = 0;
-    if (r0 > 0) c.task[c.n_tasks++] = lora::ContractTask{dg, F, 0, r0, {dB_gate, nullptr}, r0};
-    if (r1 > 0) c.task[c.n_tasks++] = lora::ContractTask{du, F, r0, r1, {dB_up, nullptr}, r1};
-    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
-  }
-  if (want_a) {  // dA = v^T x, both projections' rows in one pass over x
-    c.M = K; c.tt = vt; c.transposed = true; c.n_tasks = 1;
-    c.task[0] = lora::ContractTask{bf(x), ldx, 0, r0 + r1, {r0 > 0 ? dA_gate : nullptr, r1 > 0 ? dA_up : nullptr}, r0};
-    if (lora::launch_contract(c, st) != hipSuccess) return LORA_ERR_HIP;
-  }
-  return LORA_OK;
+  c.T = T; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part;
+  const int r0 = static_cast<int>(s[0].rank), r1 = static_cast<int>(s[1].rank), rr = r0 + r1;
+  if (want_a)  // v^T x, both projections' rows in one pass over x
+    c.task[c.n_tasks++] = lora::ContractTask{bf(x), ldx, K, vt, ldt, rr, 0, rr, true, false,
+                                             {r0 > 0 ? dA_gate : nullptr, r1 > 0 ? dA_up : nullptr}, r0};
+  const auto* tt = reinterpret_cast<const uint16_t*>(keep + saved_tt_at(T, F));
+  if (want_b && r0 > 0)  // d^T t of each projection
+    c.task[c.n_tasks++] = lora::ContractTask{dg, F, F, tt, ldt, rr, 0, r0, false, false, {dB_gate, nullptr}, r0};
+  if (want_b && r1 > 0)
+    c.task[c.n_tasks++] = lora::ContractTask{du, F, F, tt, ldt, rr, r0, r1, false, false, {dB_up, nullptr}, r1};
+  return lora::launch_contract(c, st) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
 }  // extern "C"
