@@ -385,6 +385,99 @@ __global__ __launch_bounds__(P::THREADS) void gated_join_kernel(RingArgs p, int 
   gated_store<P, ACT, 1>(acc, p, m0, n0, smem);
 }
 
+// Few tokens: grid (128-row tiles of gate, up, A_gate, A_up, one behind the other; parts of the contraction).
+__global__ __launch_bounds__(Ring128::THREADS, Ring128::OCC) void gated_few_kernel(GatedFew p) {
+  using P = Ring128;
+  __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
+  const int nf = static_cast<int>((p.F + 127) / 128), na = (p.rank[0] + 127) / 128;
+  int id = blockIdx.x;
+  const int64_t fc = (p.F + 3) / 4 * 4, ld = 2 * fc + p.rank[0] + p.rank[1];
+  RingArgs g = {};
+  g.x[0] = p.x; g.ldx = p.ldx; g.K[0] = p.K; g.T = p.T;
+  int64_t col;
+  if (id < 2 * nf) {
+    const int side = id >= nf ? 1 : 0;
+    g.W[0] = p.W[side];
+    g.N = p.F;
+    col = side * fc;
+    id -= side * nf;
+  } else {
+    id -= 2 * nf;
+    const int side = id >= na ? 1 : 0;
+    g.W[0] = p.A[side];
+    g.N = p.rank[side];
+    col = 2 * fc + (side ? p.rank[0] : 0);
+    id -= side * na;
+  }
+  const int wave = ring_wave();
+  const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
+  const int64_t n0 = static_cast<int64_t>(id) * P::BN;
+  const int NS = static_cast<int>((p.K + 63) / 64), lo = static_cast<int>(blockIdx.y) * p.ks, hi = min(NS, lo + p.ks);
+  f32x4 acc[P::NI][P::NJ];
+  NtOp<P, false> op;
+  op.init(g, 0, n0, lo, hi);
+  ring_run<P, false>(acc, op, hi - lo, smem, wm0, wn0);
+  store_part<P>(acc, p.part + static_cast<int64_t>(blockIdx.y) * p.T * ld + col, ld, wm0, n0 + wn0, p.T, g.N);
+}
+
+// h of 4 tokens and 256 columns per workgroup; the rank-wide products stay in fp32.
+template <int ACT>
+__global__ __launch_bounds__(256) void gated_few_finish_kernel(GatedFew p) {
+  extern __shared__ __attribute__((aligned(16))) float tt[];  // [4][R]
+  const int R = p.rank[0] + p.rank[1];
+  const int64_t fc = (p.F + 3) / 4 * 4, ld = 2 * fc + R;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 4, n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t nn = min<int64_t>(n, p.F - 1);
+  float g[4], u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = u[i] = 0.f;
+  for (int z = 0; z < p.S; ++z)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* row = p.part + (z * p.T + min<int64_t>(t0 + i, p.T - 1)) * ld + nn;
+      g[i] += row[0];
+      u[i] += row[fc];
+    }
+  for (int c = threadIdx.x; c < 4 * R; c += 256) {
+    const int i = c / R, q = c - i * R;
+    const float* row = p.part + min<int64_t>(t0 + i, p.T - 1) * ld + 2 * fc + q;
+    float v = 0.f;
+    for (int z = 0; z < p.S; ++z) v += row[z * p.T * ld];
+    tt[c] = v * (q < p.rank[0] ? p.scale[0] : p.scale[1]);
+  }
+  __syncthreads();
+  if (n >= p.F) return;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    float (&v)[4] = side ? u : g;
+    const int r = p.rank[side];
+    const uint16_t* b = p.B[side] + n * r;
+    const float* t = tt + (side ? p.rank[0] : 0);
+    for (int q = 0; q < r; q += 8) {  // (ranks are multiples of 8, B 16-byte aligned)
+      const u32x4 w = *reinterpret_cast<const u32x4*>(b + q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t pair = w[e >> 1];
+        const float bv = __uint_as_float(e & 1 ? pair & 0xffff0000u : pair << 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(t[i * R + q + e], bv, v[i]);
+      }
+    }
+    if (p.bias[side] != nullptr) {
+      const float bv = bf16_to_f32(p.bias[side][n]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += bv;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (t0 + i >= p.T) break;
+    float a, da;
+    act_of<ACT, false>(g[i], a, da);
+    p.h[(t0 + i) * p.ldh + n] = f32_to_bf16_rne(a * u[i]);
+  }
+}
+
 // dg and du: a wave takes 16 tokens x 64 columns, from the blocks that the forward kept.
 template <int ACT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
@@ -685,6 +778,22 @@ hipError_t launch_gated(const RingArgs& a, hipStream_t s) {
   if (p.act == 0) return plan.big ? launch_gated_cfg<Ring256, 0>(p, NS, s) : launch_gated_cfg<Ring128, 0>(p, NS, s);
   if (p.act == 1) return plan.big ? launch_gated_cfg<Ring256, 1>(p, NS, s) : launch_gated_cfg<Ring128, 1>(p, NS, s);
   return plan.big ? launch_gated_cfg<Ring256, 2>(p, NS, s) : launch_gated_cfg<Ring128, 2>(p, NS, s);
+}
+
+hipError_t launch_gated_few(const GatedFew& a, hipStream_t s) {
+  GatedFew p = a;
+  const int R = p.rank[0] + p.rank[1];
+  few_plan(p.T, p.K, p.F, R, &p.S, &p.ks);
+  const int tiles = static_cast<int>(2 * ((p.F + 127) / 128)) + (p.rank[0] + 127) / 128 + (p.rank[1] + 127) / 128;
+  hipLaunchKernelGGL(gated_few_kernel, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(p.S)), dim3(256), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid(blocks_of(p.F, 256), blocks_of(p.T, 4)), block(256);
+  const size_t lds = static_cast<size_t>(4 * R) * 4;  // (at most 2048 ranks: 32 KB)
+  if (p.act == 0) hipLaunchKernelGGL(gated_few_finish_kernel<0>, grid, block, lds, s, p);
+  else if (p.act == 1) hipLaunchKernelGGL(gated_few_finish_kernel<1>, grid, block, lds, s, p);
+  else hipLaunchKernelGGL(gated_few_finish_kernel<2>, grid, block, lds, s, p);
+  return hipGetLastError();
 }
 
 hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,

@@ -131,6 +131,51 @@ hipError_t launch_ring(const RingArgs& p, bool nn, hipStream_t s);  // (p.part: 
 // (p.part: ring_part_bytes(T, 2 N, ring_stages))
 hipError_t launch_gated(const RingArgs& p, hipStream_t s);
 
+// The same for few tokens: x against both weights and both adapters' A in one launch, each product whole or its
+// contraction in S parts, fp32 sums to memory; the second launch adds the adapters and the activation. Reading the weights
+// is the whole cost, and the products of A pass beside it, where the other way has them before it.
+struct GatedFew {
+  const uint16_t* x; int64_t ldx;
+  const uint16_t *W[2], *A[2], *B[2], *bias[2];
+  int rank[2];
+  float scale[2];
+  int64_t T, K, F;
+  uint16_t* h; int64_t ldh;
+  int act;
+  float* part;     // [S, T, few_ld]
+  int S, ks;
+};
+constexpr int64_t kGatedFewT = 64;
+inline int64_t few_cols(int64_t F) { return (F + 3) / 4 * 4; }
+inline int64_t few_ld(int64_t F, int64_t R) { return 2 * few_cols(F) + R; }
+// Parts of the contraction: the weights at 5.2 TB/s, or a workgroup's stages one after the other (0.45 us each and 4 for
+// the ring's start), whichever takes longer, and the sums written and read. (One token, 1536 -> 8960: 17.7 us whole, 140
+// workgroups with a long way each, against 12.)
+inline void few_plan(int64_t T, int64_t K, int64_t F, int64_t R, int* S, int* ks) {
+  const int64_t nk = (K + 63) / 64;
+  const double read = 4.0 * static_cast<double>(F) * static_cast<double>(K) / 5.2e6;
+  double least = 0.0;
+  *S = 1;
+  *ks = static_cast<int>(nk);
+  for (int64_t s = 1; s <= 16; ++s) {
+    const int64_t k = (nk + s - 1) / s;
+    if (s > 1 && (k < 3 || (nk + k - 1) / k != s)) continue;
+    const double chain = static_cast<double>(k) * 0.45 + 4.0;
+    const double est = (read > chain ? read : chain) + static_cast<double>(s * T * few_ld(F, R)) * 8.0 / 4e6;
+    if (least == 0.0 || est < least) {
+      least = est;
+      *S = static_cast<int>(s);
+      *ks = static_cast<int>(k);
+    }
+  }
+}
+inline size_t few_part_bytes(int64_t T, int64_t K, int64_t F, int64_t R) {
+  int S, ks;
+  few_plan(T, K, F, R, &S, &ks);
+  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(few_ld(F, R)) * 4;
+}
+hipError_t launch_gated_few(const GatedFew& p, hipStream_t s);
+
 // g and u as the forward keeps them: fp32, in blocks of 16 tokens x 16 columns as the MFMA leaves them (block (a, b):
 // 256 values of g, then 256 of u; lane l = 16 q + r holds token r, columns 4 q .. + 3).
 inline int64_t gated_blocks(int64_t n) { return (n + 15) / 16; }

@@ -290,8 +290,11 @@ GatedLayout gated_fwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_
   Take take;
   L.tt = take(tt_bytes(T, rg + ru));
   size_t part = 0;
-  for (int i = 0; i < 4; ++i)  // both adapters, or either of them inactive
-    part = std::max(part, gated_fwd_part(T, K, F, (i & 1 ? 0 : rg) + (i & 2 ? 0 : ru)));
+  for (int i = 0; i < 4; ++i) {  // both adapters, or either of them inactive
+    const int64_t R = (i & 1 ? 0 : rg) + (i & 2 ? 0 : ru);
+    part = std::max(part, gated_fwd_part(T, K, F, R));
+    if (T <= lora::kGatedFewT) part = std::max(part, lora::few_part_bytes(T, K, F, R));
+  }
   L.part = take(part);
   L.total = take.off;
   return L;
@@ -354,6 +357,16 @@ void gated_spans(const lora_gated_layer* l, int64_t K, int64_t F, const Side (&s
 hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* l, const Side (&s)[2],
                          int64_t F, int32_t act, void* h, int64_t ldh, float* saved, uint16_t* tt, float* part,
                          hipStream_t st) {
+  if (T <= lora::kGatedFewT && saved == nullptr) {
+    lora::GatedFew f;
+    std::memset(&f, 0, sizeof(f));
+    f.x = bf(x); f.ldx = ldx; f.W[0] = bf(l->W_gate); f.W[1] = bf(l->W_up); f.bias[0] = bf(l->b_gate);
+    f.bias[1] = bf(l->b_up); f.T = T; f.K = K; f.F = F; f.h = bf(h); f.ldh = ldh; f.act = act; f.part = part;
+    for (int i = 0; i < 2; ++i) {
+      f.A[i] = bf(s[i].A); f.B[i] = bf(s[i].B); f.rank[i] = static_cast<int>(s[i].rank); f.scale[i] = s[i].scale;
+    }
+    return lora::launch_gated_few(f, st);
+  }
   RingArgs g;
   std::memset(&g, 0, sizeof(g));
   const int64_t R = s[0].rank + s[1].rank;
