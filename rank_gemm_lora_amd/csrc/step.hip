@@ -162,35 +162,34 @@ __device__ __forceinline__ void store_block(const f32x4 (&acc)[P::NI][NJ], const
               static_cast<int>(min<int64_t>(P::WN, p.N - n0)));
 }
 
-// acc = 0 where the element of the [T, N] tensor is dropped. A lane holds 4 columns, half of a call's 8: lanes q and
-// q ^ 1 make the calls of blocks i and i + 1 and exchange halves.
+// acc = 0 where the element of the [T, N] tensor is dropped. A lane holds 4 columns, half of a call's 8: lanes of rows q
+// and q ^ 1 make the calls of blocks i and i + 1, and two swaps of 16-lane rows bring each the halves that it needs (a
+// row's own first words and its neighbour's, block i; the same of the other, block i + 1).
 template <class P>
 __device__ __forceinline__ void drop_block(f32x4 (&acc)[P::NI][P::NJ], const Dropper& d, int64_t m0, int64_t n0) {
   const int lane = opaque_int(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
-  const bool odd = (q & 1) != 0;
+  const uint32_t thr = d.thr2 & 0xffffu;
 #pragma unroll
   for (int j = 0; j < P::NJ; ++j) {
-    const int64_t row = (m0 + j * 16 + r) * d.blocks + n0 / 8 + (q >> 1);
+    const int64_t row = (m0 + j * 16 + r) * d.blocks + n0 / 8 + (q >> 1) + (q & 1) * 2;
 #pragma unroll
     for (int i = 0; i < P::NI; i += 2) {
-      // lane q makes block i + (q & 1), keeps its own half and gives the other
-      const u32x4 w = philox7(static_cast<uint64_t>(row + (i + (odd ? 1 : 0)) * 2), d.seed, d.offset);
-      const uint32_t give0 = odd ? w[0] : w[2], give1 = odd ? w[1] : w[3];
-      const uint32_t got0 = __shfl_xor(give0, 16), got1 = __shfl_xor(give1, 16);
-      // an even lane's columns are the first half of both blocks, an odd lane's the second half
-      const uint32_t a0 = d.mask(odd ? got0 : w[0]), a1 = d.mask(odd ? got1 : w[1]);
-      const uint32_t b0 = d.mask(odd ? w[2] : got0), b1 = d.mask(odd ? w[3] : got1);
-      const uint32_t ms[2][2] = {{a0, a1}, {b0, b1}};
+      const u32x4 w = philox7(static_cast<uint64_t>(row + i * 2), d.seed, d.offset);
+      // odd rows of the first operand change places with the even rows before them of the second
+      const auto lo = __builtin_amdgcn_permlane16_swap(w[0], w[2], false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(w[1], w[3], false, false);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool keep = ((ms[h][e >> 1] >> (16 * (e & 1))) & 1u) != 0;
-          acc[i + h][j][e] = keep ? acc[i + h][j][e] : 0.f;
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w0 = lo[h], w1 = hi[h];
+        f32x4& v = acc[i + h][j];
+        v[0] = (w0 & 0xffffu) >= thr ? v[0] : 0.f;
+        v[1] = (w0 >> 16) >= thr ? v[1] : 0.f;
+        v[2] = (w1 & 0xffffu) >= thr ? v[2] : 0.f;
+        v[3] = (w1 >> 16) >= thr ? v[3] : 0.f;
 #if defined(__HIP_DEVICE_COMPILE__)
-      if constexpr (P::BM == 256) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i + 1][j]));  // (back to where the MFMAs keep them)
+        if constexpr (P::BM == 256) asm volatile("" : "+a"(v));  // (back to where the MFMAs keep it)
 #endif
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -535,23 +534,25 @@ __device__ __forceinline__ bf16x8 tr_frag(const char* at, int row4) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// (restrict: the copies in flight go to other slots; see ring_stage)
+// NB blocks of 16 columns. (restrict: the copies in flight go to other slots; see ring_stage)
+template <int NB>
 __device__ __forceinline__ void contract_stage(f32x4 (&acc)[4][kCtJ / 16], const char* __restrict__ pb,
-                                               const char* __restrict__ qb, uint32_t pa, uint32_t qa, int nj) {
-  bf16x8 af[4];
+                                               const char* __restrict__ qb, uint32_t pa, uint32_t qa) {
+  bf16x8 af[4], bq[NB][2];
 #pragma unroll
   for (int ib = 0; ib < 4; ++ib) af[ib] = tr_frag(pb + (pa ^ static_cast<uint32_t>(ib << 5)), 4 * 512);
 #pragma unroll
-  for (int jb = 0; jb < kCtJ / 16; ++jb) {
-    if (jb >= nj) continue;
+  for (int jb = 0; jb < NB; ++jb)
 #pragma unroll
-    for (int term = 0; term < 2; ++term) {
-      const bf16x8 bq = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)), 4 * 256);
+    for (int term = 0; term < 2; ++term)
+      bq[jb][term] = tr_frag(qb + (qa ^ static_cast<uint32_t>((term * 4 + jb) << 5)), 4 * 256);
+#pragma unroll
+  for (int jb = 0; jb < NB; ++jb)
+#pragma unroll
+    for (int term = 0; term < 2; ++term)
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib)
-        acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq, acc[ib][jb], 0, 0, 0);
-    }
-  }
+        acc[ib][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[ib], bq[jb][term], acc[ib][jb], 0, 0, 0);
 }
 
 template <bool DROP>
@@ -629,16 +630,18 @@ __global__ __launch_bounds__(256, 2) void contract_kernel(Contract p, int S, int
       for (int l = 0; l < 4; ++l)
         mask[l] = d.masks(t_lo + static_cast<int64_t>(s) * kCtT + prow[l], (i0 + pcol[l]) / 8);
     }
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(6));  // stage s landed; s + 1 may be in flight
-    stage_barrier();                            // (and every wave is done reading stage s - 1)
-    issue(s + 2);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(6));  // this wave's copies of stage s landed; s + 1's may be in flight
     char* b = smem + (s % 3) * kCtStage;
-    if (masked) {
+    if (masked) {  // (each wave masks what it copied)
 #pragma unroll
       for (int l = 0; l < 4; ++l) *reinterpret_cast<u32x4*>(b + ((l * 4 + wave) * 64 + lane) * 16) &= mask[l];
-      stage_barrier();
     }
-    contract_stage(acc, b, b + kCtP, pa, qa, nj);
+    stage_barrier();  // stage s is there for every wave, and every wave is done reading stage s - 1
+    issue(s + 2);
+    if (nj == 4) contract_stage<4>(acc, b, b + kCtP, pa, qa);
+    else if (nj == 3) contract_stage<3>(acc, b, b + kCtP, pa, qa);
+    else if (nj == 2) contract_stage<2>(acc, b, b + kCtP, pa, qa);
+    else contract_stage<1>(acc, b, b + kCtP, pa, qa);
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   // lane (r, q) of block (ib, jb): rows i = 64 wave + 16 ib + 4 q + e of P^T, column j = 16 jb + r
