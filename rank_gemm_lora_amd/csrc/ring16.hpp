@@ -71,27 +71,29 @@ struct NtRows {
 
 // A lane's offsets in an NN unit: tile row k is source row k of the stage (the resource ends behind its last row), and
 // 32-byte granule g of it sits at g ^ f(k), f(k) = (k & 3) | (k >> 3 & 1) << 2: the eight rows that half a wave's
-// transposing read touches then lie in eight different granules of the 256 bytes of the banks. A copy instruction takes
-// ROWS rows of the tile per wave; f depends on its number by its last bit at most.
+// transposing read touches then lie in eight different granules of the 256 bytes of the banks. A wave's rows in one copy
+// instruction lie in one group of eight: `base` is the offset within the group (its columns by the group's last bit),
+// the rest the same for the whole wave.
 template <class P>
 struct NnRows {
   static constexpr int LPR = P::BN * 2 / 16, ROWS = 64 / LPR;  // lanes (16-byte pieces) per row; rows per wave
-  uint32_t base[2], step;
-  static_assert(P::WAVES * ROWS == 8 || P::WAVES * ROWS == 16, "f by the parity of the instruction");
-  __device__ __forceinline__ static int row(int l) {
-    return (l * P::WAVES + ring_wave()) * ROWS + opaque_int(threadIdx.x & 63) / LPR;
-  }
-  __device__ __forceinline__ static int col(int l) {
-    const int k = row(l), p = opaque_int(threadIdx.x & 63) % LPR, f = (k & 3) | (((k >> 3) & 1) << 2);
-    return (((p >> 1) ^ f) * 2 + (p & 1)) * 8;
-  }
+  static constexpr int GPC = P::WAVES * ROWS / 8;              // groups per copy instruction
+  uint32_t base[2];
+  static_assert(GPC == 1 || GPC == 2, "two or four rows per wave");
+  __device__ __forceinline__ static int group(int l) { return GPC == 1 ? l : 2 * l + (ring_wave() >> 1); }
   __device__ __forceinline__ void init(uint32_t ld_bytes, int cols_valid) {
+    const int lane = opaque_int(threadIdx.x & 63), p = lane % LPR;
+    const int in = (ring_wave() * ROWS + lane / LPR) & 7;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      base[h] = col(h) < cols_valid ? static_cast<uint32_t>(row(0)) * ld_bytes + static_cast<uint32_t>(col(h)) * 2 : kMissing;
-    step = static_cast<uint32_t>(P::WAVES * ROWS) * ld_bytes;
+    for (int h = 0; h < 2; ++h) {
+      const int col = (((p >> 1) ^ ((in & 3) | h << 2)) * 2 + (p & 1)) * 8;
+      base[h] = col < cols_valid ? static_cast<uint32_t>(in) * ld_bytes + static_cast<uint32_t>(col) * 2 : kMissing;
+    }
   }
-  __device__ __forceinline__ uint32_t at(int l) const { return base[l & 1] + static_cast<uint32_t>(l) * step; }
+  // (a group starts at `rows`, counted from the resource's first)
+  __device__ __forceinline__ uint32_t at(int l, uint32_t rows) const {
+    return (GPC == 1 ? base[l & 1] : (ring_wave() >> 1) ? base[1] : base[0]) + rows;
+  }
 };
 
 template <class P, bool NN>

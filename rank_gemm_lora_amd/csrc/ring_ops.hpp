@@ -82,10 +82,11 @@ struct NnOp {
   __amdgpu_buffer_rsrc_t xr, wr, wr2, er0, er1;
   uint32_t ldx_b, ldw_b, ldt_b, ax, c16;
   int K0, K1, re0, per, NE, n0s, hi, seg, rows_m, cols, lo;
+  bool inited = false;
   uint32_t second;  // bit l: copy instruction l takes the second adapter's rows (wr2)
   NtRows<P> vx;
   NnRows<P> vw;
-  uint32_t ve[NEXT > 0 ? ring_loads<P>() : 1];  // with an extension: the offset of each instruction
+  uint32_t first[NEXT > 0 ? ring_loads<P>() : 1];  // with an extension: where the rows of each instruction start
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint16_t* base, int rows) const {
     return make_rsrc(base, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldw_b + static_cast<uint32_t>(cols) * 2 : 0u);
   }
@@ -133,15 +134,15 @@ struct NnOp {
       }
       seg = 0;
       ax = static_cast<uint32_t>(s) * 128u;
+      if (!inited) vw.init(ldw_b, cols);
+      inited = true;
       second = 0;
 #pragma unroll
-      for (int l = 0; l < ring_loads<P>(); ++l) {
-        const int vr = s * 64 + vw.row(l), ph = vr < per ? vr : vr - per, c = vw.col(l);
-        const bool is2 = NEXT > 1 && ph >= re0;
-        ve[NEXT > 0 ? l : 0] = vr < 2 * per && c < cols
-                                   ? static_cast<uint32_t>(c) * 2 + static_cast<uint32_t>(is2 ? ph - re0 : ph) * ldw_b
-                                   : kMissing;
-        if (NEXT > 1) second |= static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(is2 ? 1 : 0)) << l;
+      for (int l = 0; l < ring_loads<P>(); ++l) {  // (groups of eight rows: ranks are multiples of 8)
+        const int gr = s * 8 + NnRows<P>::group(l), ph = gr < per / 8 ? gr : gr - per / 8;
+        const bool is2 = NEXT > 1 && ph >= re0 / 8;
+        first[NEXT > 0 ? l : 0] = gr < per / 4 ? static_cast<uint32_t>(is2 ? ph - re0 / 8 : ph) * 8u * ldw_b : kMissing;
+        if (NEXT > 1) second |= static_cast<uint32_t>(is2 ? 1 : 0) << l;
       }
     } else {
       const int ms = s - NE;
@@ -149,10 +150,11 @@ struct NnOp {
       if (seg != sg) {
         if (seg < 1) {
           vx.init(ldx_b);
-          vw.init(ldw_b, cols);
+          if (!inited) vw.init(ldw_b, cols);
+          inited = true;
           if constexpr (NEXT > 0) {
 #pragma unroll
-            for (int l = 0; l < ring_loads<P>(); ++l) ve[l] = vw.at(l);
+            for (int l = 0; l < ring_loads<P>(); ++l) first[l] = static_cast<uint32_t>(NnRows<P>::group(l)) * 8u * ldw_b;
           }
         }
         seg = sg;
@@ -167,8 +169,9 @@ struct NnOp {
   }
   __device__ __forceinline__ void load_x(int l, char* d) const { ring_copy<P>(l, d, xr, vx.at(l, ax)); }
   __device__ __forceinline__ void load_w(int l, char* d) const {
-    if constexpr (NEXT > 1) ring_copy<P>(l, d, (second >> l) & 1 ? wr2 : wr, ve[l]);
-    else ring_copy<P>(l, d, wr, NEXT > 0 ? ve[l] : vw.at(l));
+    const uint32_t off = vw.at(l, NEXT > 0 ? first[NEXT > 0 ? l : 0] : static_cast<uint32_t>(NnRows<P>::group(l)) * 8u * ldw_b);
+    if constexpr (NEXT > 1) ring_copy<P>(l, d, (second >> l) & 1 ? wr2 : wr, off);
+    else ring_copy<P>(l, d, wr, off);
   }
 };
 
