@@ -15,9 +15,8 @@
 //
 //   logits_kernel    l of a piece of the vocabulary in the accumulators; c and the sum per token and block, and the shares
 //                    2^(l log2 e - c) in bf16 (for the loss alone: no shares)
-//   piece_kernel     the token's largest c so far, and every block's distance from it
+//   piece_kernel     the token's largest c so far, and every block's distance from it; in the end lse, loss, 1 - p_target
 //   dh_kernel        sums over the piece of shares . W, fp32; where a piece is not the first, added to those before it
-//   lse_kernel       blocks -> lse, loss, 1 - p_target
 //   dh_join_kernel   the parts' sum, the target's part, dloss, one rounding (a whole tile of a single piece does so itself)
 #include "common.hpp"
 #include "loss.hpp"
@@ -102,57 +101,46 @@ __device__ __forceinline__ int64_t shift_at(int64_t t, int wm) {
   return base + (in & 15) * (wm / 16) + (in >> 4);
 }
 
-// 4 tokens per workgroup, 64 threads each: the piece's blocks [b0, b1); wm of dh_kernel.
-__global__ __launch_bounds__(256) void piece_kernel(VocabLoss p, int64_t b0, int64_t b1, bool first, int wm, int64_t ld) {
-  __shared__ float s[64][5];
-  const int lt = threadIdx.x & 3, part = threadIdx.x >> 2;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + lt, tt = min<int64_t>(t, p.T - 1);
-  float top = first ? kNoTerm : p.top[tt];
-  const float before = top;
+// 16 tokens per workgroup (64 bytes of each block's row), 64 threads each: the largest c of the piece's blocks [b0, b1) and
+// before, every block's distance from it where there are shares; behind the last piece (all its blocks: [0, b1)) lse and
+// what comes of it. A token without a target (one outside the vocabulary) has loss 0 and, by rest < 0, no gradient.
+// Bound by the reads' latency.
+template <bool SHARE, bool LAST>
+__global__ __launch_bounds__(1024) void piece_kernel(VocabLoss p, int64_t b0, int64_t b1, int wm, int64_t ld) {
+  __shared__ float s[2][16][16];
+  const int lt = threadIdx.x & 15, part = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + lt, tt = min<int64_t>(t, p.T - 1);
+  auto join = [&](float v, int which, auto op) {  // of the 64 threads of a token, in one order
+    v = op(v, __shfl_xor(v, 16));
+    v = op(v, __shfl_xor(v, 32));
+    if ((part & 3) == 0) s[which][wave][lt] = v;
+    __syncthreads();
+    v = s[which][0][lt];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) v = op(v, s[which][w][lt]);
+    return v;
+  };
+  const float before = b0 == 0 ? kNoTerm : p.top[tt];
+  float top = before;
+#pragma unroll 4
   for (int64_t b = b0 + part; b < b1; b += 64) top = fmaxf(top, p.ref[b * p.T + tt]);
-  s[part][lt] = top;
-  __syncthreads();
-  for (int h = 32; h > 0; h >>= 1) {
-    if (part < h) s[part][lt] = fmaxf(s[part][lt], s[part + h][lt]);
-    __syncthreads();
-  }
-  top = s[0][lt];
-  if (t >= p.T) return;
-  if (part == 0) {
-    p.top[t] = top;
-    p.fade[t] = exp2_of(before - top);
-  }
-  const int64_t at = shift_at(t, wm);
-  for (int64_t b = b0 + part; b < b1; b += 64)
-    p.shift[(b - b0) * ld + at] = static_cast<uint8_t>(fminf(top - p.ref[b * p.T + t], 255.f));
-}
-
-// 4 tokens per workgroup, 64 threads each: the blocks' sums joined. A token without a target (one outside the vocabulary)
-// has loss 0 and, by rest < 0, no gradient.
-__global__ __launch_bounds__(256) void lse_kernel(VocabLoss p, int64_t blocks) {
-  __shared__ float sc[64][5], ss[64][5];
-  const int lt = threadIdx.x & 3, part = threadIdx.x >> 2;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + lt, tt = min<int64_t>(t, p.T - 1);
-  float top = kNoTerm, sum = 0.f;
-  for (int64_t b = part; b < blocks; b += 64) {
-    const float c = p.ref[b * p.T + tt], s = p.sum[b * p.T + tt], now = fmaxf(top, c);
-    sum = sum * exp2_of(top - now) + s * exp2_of(c - now);
-    top = now;
-  }
-  sc[part][lt] = top;
-  ss[part][lt] = sum;
-  __syncthreads();
-  for (int h = 32; h > 0; h >>= 1) {
-    if (part < h) {
-      const float now = fmaxf(sc[part][lt], sc[part + h][lt]);
-      ss[part][lt] = ss[part][lt] * exp2_of(sc[part][lt] - now) + ss[part + h][lt] * exp2_of(sc[part + h][lt] - now);
-      sc[part][lt] = now;
+  top = join(top, 0, [](float x, float y) { return fmaxf(x, y); });
+  if (SHARE && t < p.T) {
+    if (part == 0) {
+      p.top[t] = top;
+      p.fade[t] = exp2_of(before - top);
     }
-    __syncthreads();
+    const int64_t at = shift_at(t, wm);
+#pragma unroll 4
+    for (int64_t b = b0 + part; b < b1; b += 64)
+      p.shift[(b - b0) * ld + at] = static_cast<uint8_t>(fminf(top - p.ref[b * p.T + t], 255.f));
   }
+  if (!LAST) return;
+  float others = 0.f;  // relative to 2^top
+#pragma unroll 4
+  for (int64_t b = part; b < b1; b += 64) others += p.sum[b * p.T + tt] * exp2_of(p.ref[b * p.T + tt] - top);
+  others = join(others, 1, [](float x, float y) { return x + y; });
   if (part != 0 || t >= p.T) return;
-  top = sc[0][lt];
-  const float others = ss[0][lt];  // relative to 2^top
   const int64_t target = p.target[t];
   const bool some = target >= 0 && target < p.V;
   const float mine = some ? p.tlogit[t] : 0.f;
@@ -306,7 +294,7 @@ hipError_t launch_dh(const VocabLoss& p, int64_t v0, int64_t cols, const RingPla
 }  // namespace
 
 hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t s) {
-  const unsigned tok4 = static_cast<unsigned>((p.T + 3) / 4);
+  const unsigned tok16 = static_cast<unsigned>((p.T + 15) / 16);
   const bool grad = p.dh != nullptr;
   const int64_t piece = grad ? p.piece : p.V;
   const bool big = ring_plan(p.T, piece < p.V ? piece : p.V, (p.K + 63) / 64).big;
@@ -318,10 +306,10 @@ hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t s) {
     const bool last = v0 + cols >= p.V;
     hipError_t e = big ? launch_logits<Ring256>(p, v0, cols, grad, s) : launch_logits<Ring128>(p, v0, cols, grad, s);
     if (e != hipSuccess) return e;
-    if (grad)
-      hipLaunchKernelGGL(piece_kernel, dim3(tok4), dim3(256), 0, s, p, v0 / bw, (v0 + cols + bw - 1) / bw, v0 == 0, wm,
-                         shift_ld(p.T));
-    if (last) hipLaunchKernelGGL(lse_kernel, dim3(tok4), dim3(256), 0, s, p, (p.V + bw - 1) / bw);
+    const int64_t b0 = v0 / bw, b1 = (v0 + cols + bw - 1) / bw, ld = shift_ld(p.T);
+    if (!grad) hipLaunchKernelGGL((piece_kernel<false, true>), dim3(tok16), dim3(1024), 0, s, p, b0, b1, wm, ld);
+    else if (last) hipLaunchKernelGGL((piece_kernel<true, true>), dim3(tok16), dim3(1024), 0, s, p, b0, b1, wm, ld);
+    else hipLaunchKernelGGL((piece_kernel<true, false>), dim3(tok16), dim3(1024), 0, s, p, b0, b1, wm, ld);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!grad) continue;
