@@ -141,6 +141,155 @@ __global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct a, int Sa,
   else rank_finish(b, Sb, blockIdx.x - blocks);
 }
 
+// Few tokens: 16 tokens by up to 64 columns per workgroup of 16 waves that share K, 32 indices at a time in turn, straight
+// from memory three steps ahead (two at 64 columns: 128 registers a lane). Rows along the contraction (A) are loaded as
+// the MFMA takes them; rows across it (B [K, rank]) go through a piece of LDS per wave and its transposing read. The
+// waves' sums are added in order in LDS, and the two terms written. Bound by the way to memory, once or twice over.
+constexpr int kFewWaves = 16;
+
+template <bool NN, bool DROP, int NB>
+__device__ __forceinline__ void rank_few_sum(f32x4 (&acc)[NB], const uint16_t* x, int64_t ldx, const uint16_t* const (&A)[2],
+                                             const int (&rank)[2], int64_t K, int64_t T, const Dropper& d, int64_t m0,
+                                             char* st) {
+  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const int R = rank[0] + rank[1];
+  const int rows_m = static_cast<int>(min<int64_t>(16, T - m0));
+  const uint32_t ldx_b = static_cast<uint32_t>(ldx * 2);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(x + m0 * ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+  const int nst = static_cast<int>((K + 31) / 32);
+  constexpr int D = NB == 4 ? 3 : 4;
+  u32x4 xv[D], av[D][NB];
+  // Lane's rows of A from its first index on. Columns that are not there read another's: no sum of theirs is used.
+  const uint16_t* rows[NB];
+  int64_t kin[NB];  // an index beyond K reads the last ones, and is zero below
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    if constexpr (!NN) {
+      const int g = min(i * 16 + r, R - 1);  // (one adapter's rows behind the other's)
+      rows[i] = g < rank[0] ? A[0] + static_cast<int64_t>(g) * K : A[1] + static_cast<int64_t>(g - rank[0]) * K;
+      kin[i] = 8 * q;
+    } else {
+      const int pc = i * 64 + lane;  // 32 rows of 16 NB columns, in pieces of 8
+      rows[i] = A[0] + min(pc % (NB * 2) * 8, R - 8);
+      kin[i] = pc / (NB * 2);
+    }
+  }
+  auto load = [&](int b, int s) {
+    const int64_t k = static_cast<int64_t>(s) * 32;
+    xv[b] = __builtin_amdgcn_raw_buffer_load_b128(
+        xr, k + 8 * q < K ? static_cast<uint32_t>(r) * ldx_b + static_cast<uint32_t>(k + 8 * q) * 2 : kMissing, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int64_t at = min(k + kin[i], NN ? K - 1 : K - 8);
+      av[b][i] = *reinterpret_cast<const u32x4*>(rows[i] + (NN ? at * R : at));
+    }
+  };
+  auto there = [&](const u32x4& v, int i, int64_t k) { return k + kin[i] < K ? v : u32x4{0u, 0u, 0u, 0u}; };
+#pragma unroll
+  for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int b = 0; b < D - 1; ++b) load(b, b * kFewWaves + wave);
+  for (int s0 = wave; s0 < nst; s0 += kFewWaves * D) {
+#pragma unroll
+    for (int b = 0; b < D; ++b) {
+      const int s = s0 + b * kFewWaves;
+      load((b + D - 1) % D, s + (D - 1) * kFewWaves);
+      u32x4 xb = xv[b];
+      if constexpr (DROP) {
+        if (s < nst) xb &= d.masks(m0 + r, static_cast<int64_t>(s) * 4 + q);
+      }
+      const int64_t k = static_cast<int64_t>(s) * 32;
+      bf16x8 af[NB];
+      if constexpr (NN) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int pc = i * 64 + lane, per = NB * 2, row = pc / per, c = pc % per;
+          // (granules of 16 columns; rows of NB granules)
+          *reinterpret_cast<u32x4*>(st + row * NB * 32 + c * 16) = there(av[b][i], i, k);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const char* at = st + (8 * q + (r >> 2)) * NB * 32 + i * 32 + (r & 3) * 8;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * NB * 32));
+          af[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) af[i] = __builtin_bit_cast(bf16x8, there(av[b][i], i, k));
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], __builtin_bit_cast(bf16x8, xb), acc[i], 0, 0, 0);
+    }
+  }
+}
+
+// Column block of a product (side of the gradient's): sums, then the two terms of its columns in the rows of tt. `pad`:
+// this one writes the zeros behind the terms too.
+template <bool NN, bool DROP, int NB>
+__device__ __forceinline__ void rank_few(const RankProduct& p, int side, bool pad, int64_t m0, char* smem) {
+  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const uint16_t* A[2] = {p.A[NN ? side : 0], NN ? nullptr : p.A[1]};
+  const int rank[2] = {p.rank[NN ? side : 0], NN ? 0 : p.rank[1]};
+  const int R = rank[0] + rank[1], Rall = p.rank[0] + p.rank[1], c0 = NN && side ? p.rank[0] : 0;
+  Dropper d;
+  d.blocks = p.K / 8;
+  if constexpr (DROP) d.init(p.drop, p.K);
+  f32x4 acc[NB];
+  rank_few_sum<NN, DROP, NB>(acc, p.x[NN ? side : 0], p.ldx, A, rank, p.K, p.T, d, m0, smem + wave * NB * 1024);
+  __syncthreads();  // (the waves' pieces become their sums)
+  float* sums = reinterpret_cast<float*>(smem);  // [wave][16 NB columns][16 tokens]
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[(wave * NB * 16 + i * 16 + 4 * q + e) * 16 + r] = acc[i][e];
+  __syncthreads();
+  const int ldt = (2 * Rall + 63) / 64 * 64;
+  for (int idx = threadIdx.x; idx < 16 * R; idx += kFewWaves * 64) {
+    const int t = idx / R, c = idx - t * R;
+    if (m0 + t >= p.T) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) v += sums[(w * NB * 16 + c) * 16 + t];
+    v *= c0 + c < p.rank[0] ? p.scale[0] : p.scale[1];
+    const uint16_t hi = f32_to_bf16_rne(v);
+    const float h = bf16_to_f32(hi);
+    uint16_t* row = p.tt + (m0 + t) * ldt + c0 + c;
+    row[0] = hi;
+    row[Rall] = __builtin_isfinite(h) ? f32_to_bf16_rne(v - h) : static_cast<uint16_t>(0);
+  }
+  if (pad) {
+    const int z = ldt - 2 * Rall;
+    for (int idx = threadIdx.x; idx < 16 * z; idx += kFewWaves * 64) {
+      const int t = idx / z;
+      if (m0 + t < p.T) p.tt[(m0 + t) * ldt + 2 * Rall + idx - t * z] = 0;
+    }
+  }
+}
+
+template <bool NN, bool DROP>
+__device__ __forceinline__ void rank_few_nb(const RankProduct& p, int side, bool pad, int64_t m0, char* smem) {
+  const int R = NN ? p.rank[side] : p.rank[0] + p.rank[1];
+  if (R <= 16) rank_few<NN, DROP, 1>(p, side, pad, m0, smem);
+  else if (R <= 32) rank_few<NN, DROP, 2>(p, side, pad, m0, smem);
+  else rank_few<NN, DROP, 4>(p, side, pad, m0, smem);
+}
+
+// Grid (blocks of 16 tokens, products): a's (where it is there), then b's one or two sides.
+template <bool DROP>
+__global__ __launch_bounds__(kFewWaves * 64) void rank_few_kernel(RankProduct a, int n_a, RankProduct b) {
+  __shared__ __attribute__((aligned(1024))) char smem[kFewWaves * 4 * 1024];
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int y = static_cast<int>(blockIdx.y) - n_a;
+  if (y < 0) {
+    rank_few_nb<false, DROP>(a, 0, true, m0, smem);
+  } else {
+    const int side = b.rank[0] == 0 ? 1 : y;
+    rank_few_nb<true, false>(b, side, y == 0, m0, smem);
+  }
+}
+
 // (NJ: blocks of 16 tokens from m0 on)
 template <class P, int NJ>
 __device__ __forceinline__ void store_block(const f32x4 (&acc)[P::NI][NJ], const RingArgs& p, int64_t m0, int64_t n0,
@@ -718,6 +867,14 @@ hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hi
     rank_plan(b.T, b.K, rank_tasks(b.rank[0], b.rank[1], true), &Sb, &kb);
     cb = static_cast<int>(rank_tasks(b.rank[0], b.rank[1], true));
     n_nn = static_cast<int>((b.T + 127) / 128) * cb * Sb;
+  }
+  if ((nt == nullptr || rank_few(a.T, a.K, a.rank[0], a.rank[1], false)) &&
+      (nn == nullptr || rank_few(b.T, b.K, b.rank[0], b.rank[1], true))) {
+    const int na = nt != nullptr ? 1 : 0, nb = nn != nullptr ? (b.rank[0] > 0 ? 1 : 0) + (b.rank[1] > 0 ? 1 : 0) : 0;
+    const dim3 fg(blocks_of(nt != nullptr ? a.T : b.T, 16), static_cast<unsigned>(na + nb));
+    if (drop) hipLaunchKernelGGL(rank_few_kernel<true>, fg, dim3(kFewWaves * 64), 0, s, a, na, b);
+    else hipLaunchKernelGGL(rank_few_kernel<false>, fg, dim3(kFewWaves * 64), 0, s, a, na, b);
+    return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(n_nt + n_nn)), block(256);
   if (narrow && drop) hipLaunchKernelGGL((rank_kernel<RankNarrow, true>), grid, block, 0, s, a, ka, n_nt, ca, b, kb, cb);

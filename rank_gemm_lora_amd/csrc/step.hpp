@@ -30,6 +30,15 @@ struct RankProduct {
   float* part;            // [S, T, R]
   uint16_t* tt;           // [T, pair_ld(R)]
 };
+// Few tokens (up to 1024, where 16 at a time leave no compute unit with two workgroups' work) and a K of up to 16 steps of
+// 32 for each of 16 waves: the product in one launch, without partial sums in memory. (333 tokens, rank 16, 1536 inputs:
+// 9 us with both of the backward's products, against 7.3 and 4.4 for the ring and its finishing launch. With 8960 inputs
+// a wave's steps one after the other take 20 us, and the ring is as fast.)
+constexpr int64_t kRankFewT = 1024, kRankFewK = 8192;
+constexpr int64_t kRankFewR = 64;  // columns of one workgroup: more go to the ring
+inline bool rank_few(int64_t T, int64_t K, int64_t R0, int64_t R1, bool nn) {
+  return T <= kRankFewT && K <= kRankFewK && (nn ? R0 <= kRankFewR && R1 <= kRankFewR : R0 + R1 <= kRankFewR);
+}
 // Splits of K, fixed by the sizes: as few rounds of workgroups of 128 tokens, two on each of 256 compute units, as make
 // the least stages of 64 one after the other (3 more for each round's start); a split's sums cost a write and a read.
 // (18871 tokens, 8960 inputs, masked: 3 splits, 444 workgroups one to a unit in two rounds, took 116 us.)
