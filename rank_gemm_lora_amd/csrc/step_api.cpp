@@ -63,11 +63,17 @@ int make_side(Side& s, const void* A, const void* B, int32_t rank, double alpha,
 
 // Sizes that every call of T tokens, K inputs and N outputs keeps to (row strides: two more of its tensors').
 int check_sizes(int64_t T, int64_t K, int64_t N, int64_t ld0, int64_t ld1) {
-  if (T >= kMaxTokens || K * 4 > kMaxRowBytes || N * 4 > kMaxRowBytes || ld0 * 2 > kMaxRowBytes || ld1 * 2 > kMaxRowBytes)
+  if (T >= kMaxTokens || K > kMaxRowBytes / 4 || N > kMaxRowBytes / 4 || ld0 > kMaxRowBytes / 2 || ld1 > kMaxRowBytes / 2)
     return LORA_ERR_UNSUPPORTED;
   // (a launch has at most 2^32 threads, one for 16 elements of [T, N] in the widest)
   if (T * std::max(K, N) >= int64_t(1) << 35) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
+}
+
+// Whether a size query is for sizes that a call takes (others have no workspace: 0).
+bool known_sizes(int64_t T, int64_t K, int64_t N, int32_t r0, int32_t r1) {
+  return T > 0 && K > 0 && N > 0 && r0 >= 0 && r1 >= 0 && r0 <= LORA_MAX_RANK && r1 <= LORA_MAX_RANK &&
+         check_sizes(T, K, N, 0, 0) == LORA_OK;
 }
 
 // No output overlaps an input, the workspace or another output.
@@ -144,12 +150,12 @@ int make_drop(Drop& d, double p, uint64_t seed, uint64_t offset, const uint64_t*
 extern "C" {
 
 size_t lora_linear_dropout_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank) {
-  if (T <= 0 || K <= 0 || N <= 0 || rank < 1 || T >= kMaxTokens) return 0;
+  if (!known_sizes(T, K, N, rank, 0) || rank == 0) return 0;
   return drop_layout(T, K, N, rank, false).total;
 }
 
 size_t lora_linear_dropout_bwd_workspace_size(int64_t T, int64_t K, int64_t N, int32_t rank) {
-  if (T <= 0 || K <= 0 || N <= 0 || rank < 1 || T >= kMaxTokens) return 0;
+  if (!known_sizes(T, K, N, rank, 0) || rank == 0) return 0;
   return drop_layout(T, K, N, rank, true).total;
 }
 
@@ -203,7 +209,7 @@ int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
   if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
   if (T < 0 || K < 1 || N < 1 || ldx < K || lddy < N || (dx != nullptr && lddx < K)) return LORA_ERR_SHAPE;
   if (int e = check_sizes(T, K, N, ldx, lddy)) return e;
-  if (dx != nullptr && lddx * 2 > kMaxRowBytes) return LORA_ERR_UNSUPPORTED;
+  if (dx != nullptr && lddx > kMaxRowBytes / 2) return LORA_ERR_UNSUPPORTED;
   if (!std::isfinite(strength) || !std::isfinite(request_scale)) return LORA_ERR_NONFINITE;
   Drop drop;
   if (int e = make_drop(drop, p, seed, offset, rng)) return e;
@@ -393,17 +399,17 @@ hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const
 extern "C" {
 
 size_t lora_gated_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up) {
-  if (T <= 0 || K <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
+  if (!known_sizes(T, K, F, rank_gate, rank_up)) return 0;
   return gated_fwd_layout(T, K, F, rank_gate, rank_up).total;
 }
 
 size_t lora_gated_saved_size(int64_t T, int64_t F, int32_t rank_gate, int32_t rank_up) {
-  if (T <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
+  if (!known_sizes(T, 1, F, rank_gate, rank_up)) return 0;
   return saved_bytes(T, F, rank_gate + rank_up);
 }
 
 size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t rank_gate, int32_t rank_up) {
-  if (T <= 0 || K <= 0 || F <= 0 || rank_gate < 0 || rank_up < 0 || T >= kMaxTokens) return 0;
+  if (!known_sizes(T, K, F, rank_gate, rank_up)) return 0;
   return gated_bwd_layout(T, K, F, rank_gate, rank_up).total;
 }
 
@@ -442,7 +448,7 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
   if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
   if (T < 0 || K < 1 || F < 1 || ldx < K || lddh < F || (dx != nullptr && lddx < K)) return LORA_ERR_SHAPE;
   if (int e = check_sizes(T, K, F, ldx, lddh)) return e;
-  if (dx != nullptr && lddx * 2 > kMaxRowBytes) return LORA_ERR_UNSUPPORTED;
+  if (dx != nullptr && lddx > kMaxRowBytes / 2) return LORA_ERR_UNSUPPORTED;
   Side s[2];
   if (int e = check_gated(layer, T, K, F, act, strength, request_scale, s)) return e;
   if (T > 0 && (x == nullptr || dh == nullptr)) return LORA_ERR_NULL_PTR;
@@ -558,13 +564,17 @@ LossLayout loss_layout(int64_t T, int64_t K, int64_t V, bool grad) {
 }
 
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
+// (launches of at most 2^32 threads: one for 4 elements of dh, and 256 for 128 x 128 logits)
+bool known_loss(int64_t T, int64_t K, int64_t V) {
+  return V <= kMaxVocab && T * V < int64_t(1) << 37 && T * K < int64_t(1) << 34;
+}
 
 }  // namespace
 
 extern "C" {
 
 size_t lora_cross_entropy_workspace_size(int64_t T, int64_t K, int64_t V, int32_t want_grad) {
-  if (T <= 0 || K <= 0 || V <= 0 || T >= kMaxTokens || V > kMaxVocab) return 0;
+  if (!known_sizes(T, K, 1, 0, 0) || V <= 0 || !known_loss(T, K, V)) return 0;
   return loss_layout(T, K, V, want_grad != 0).total;
 }
 
@@ -573,8 +583,7 @@ int lora_cross_entropy(const void* h, int64_t T, int64_t K, int64_t ldh, const v
                        size_t workspace_bytes, void* stream) {
   if (T < 0 || K < 1 || V < 1 || ldh < K || (dh != nullptr && lddh < K)) return LORA_ERR_SHAPE;
   if (int e = check_sizes(T, K, 1, ldh, dh != nullptr ? lddh : 0)) return e;
-  // (launches of at most 2^32 threads: one for 4 elements of dh, and 256 for 128 x 128 logits)
-  if (V > kMaxVocab || T * V >= int64_t(1) << 37 || T * K >= int64_t(1) << 34) return LORA_ERR_UNSUPPORTED;
+  if (!known_loss(T, K, V)) return LORA_ERR_UNSUPPORTED;
   if (W == nullptr || (T > 0 && (h == nullptr || target == nullptr))) return LORA_ERR_NULL_PTR;
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(workspace, 16) || !aligned(target, 8) || !aligned(dloss, 4) ||
       !aligned(loss, 4) || !aligned(lse, 4) || !aligned(dh, 2) || K % 8 != 0 || ldh % 8 != 0)
