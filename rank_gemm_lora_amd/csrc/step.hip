@@ -450,16 +450,21 @@ __device__ __forceinline__ void act_of(float g, float& a, float& da) {
     a = g * s;
     if (GRAD) da = s * (1.f + g * (1.f - s));
   } else if constexpr (ACT == 1) {
-    // g Phi(g): the tail Phi(-|g|) = erfc(|g| / sqrt 2) / 2 by formula 7.1.26 of Abramowitz and Stegun (error of erf at
-    // most 1.5e-7), whose exponential is also the derivative's density
+    // g Phi(g): the tail Phi(-|g|) = erfc(z) / 2, z = |g| / sqrt 2, whose exponential is also the derivative's density.
+    // erfc(z) exp(z^2) = t P(t), t = 1 / (1 + z / 2): P of degree 8 fitted to the least relative error over z in [0, 10]
+    // (4e-8; 4e-7 with fp32's roundings), so that the tail keeps its digits however small it is.
     const float z = __builtin_fabsf(g) * 0.70710678118655f;
-    const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * z), e = fast_exp(-z * z);
-    const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * poly * e, cdf = g < 0.f ? tail : 1.f - tail;
+    const float t = __builtin_amdgcn_rcpf(1.f + 0.5f * z), e = fast_exp(-z * z);
+    constexpr float kP[9] = {2.82088987e-01f, 2.82322961e-01f, 2.43534581e-01f, 2.00811248e-01f, -2.18574236e-02f,
+                             2.70748975e-01f, -4.80521969e-01f, 2.81239052e-01f, -5.83664508e-02f};
+    float poly = kP[8];
+#pragma unroll
+    for (int k = 7; k >= 0; --k) poly = fmaf(poly, t, kP[k]);
+    const float tail = 0.5f * t * poly * e, cdf = g < 0.f ? tail : 1.f - tail;
     a = g * cdf;
     if (GRAD) da = cdf + g * e * 0.39894228040143f;
   } else {  // g sigmoid(2 c (g + 0.044715 g^3)), which is g (1 + tanh(c (..))) / 2
-    const float c2 = 1.59576912160573f, g2 = g * g;
+    const float c2 = 1.59576912160573f, g2 = fminf(g * g, 1e4f);  // (far beyond, s is 0 or 1: no infinity below)
     const float s = __builtin_amdgcn_rcpf(1.f + fast_exp(-c2 * g * (1.f + 0.044715f * g2)));
     a = g * s;
     if (GRAD) da = s + g * s * (1.f - s) * c2 * (1.f + 0.134145f * g2);
