@@ -118,6 +118,7 @@ __device__ __forceinline__ void rank_finish(const RankProduct& p, int S, int64_t
     const bool mid = c >= R;
     const int q = mid ? c - R : c;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int z = 0; z < S; ++z) v += *reinterpret_cast<const f32x4*>(p.part + (z * p.T + t) * R + q);
     v *= q < p.rank[0] ? p.scale[0] : p.scale[1];
     w = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -631,48 +632,152 @@ __global__ __launch_bounds__(256) void gated_few_finish_kernel(GatedFew p) {
   }
 }
 
-// dg and du: a wave takes 16 tokens x 64 columns, from the blocks that the forward kept.
+// dg and du of 16 tokens x 64 columns, from the blocks that the forward kept, into a wave's LDS; then whole rows of them.
+template <int ACT>
+struct GradBlock {
+  const float* saved;
+  const uint16_t* dh;
+  int64_t lddh, T, F;
+  BlockOut<16, 64> og, ou;
+  f32x4 g[4], u[4];
+  uint2 d[4];
+  __device__ __forceinline__ void load(int64_t m0, int64_t n0) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int64_t fb = (F + 15) / 16, m = min<int64_t>(m0 + r, T - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + i * 16;
+      if (n >= F) continue;
+      const float* b = saved + ((m0 >> 4) * fb + (n >> 4)) * 512 + lane * 4;
+      g[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(b));
+      u[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(b + 256));
+      // (F is a multiple of 8, and so is the row stride: 8 bytes never cross the end)
+      d[i] = n + q * 4 < F ? *reinterpret_cast<const uint2*>(dh + m * lddh + n + q * 4) : uint2{0u, 0u};
+    }
+  }
+  __device__ __forceinline__ void form(int64_t n0) const {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n0 + i * 16 >= F) continue;
+      const float dv[4] = {__uint_as_float(d[i].x << 16), __uint_as_float(d[i].x & 0xffff0000u),
+                           __uint_as_float(d[i].y << 16), __uint_as_float(d[i].y & 0xffff0000u)};
+      float vg[4], vu[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, da;
+        act_of<ACT, true>(g[i][e], a, da);
+        vg[e] = dv[e] * u[i][e] * da;
+        vu[e] = dv[e] * a;
+      }
+      og.put(r, i * 16 + q * 4, pack_bf16x2(vg[0], vg[1]), pack_bf16x2(vg[2], vg[3]));
+      ou.put(r, i * 16 + q * 4, pack_bf16x2(vu[0], vu[1]), pack_bf16x2(vu[2], vu[3]));
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* dg, uint16_t* du, int64_t m0, int64_t n0) const {
+    const int rows = static_cast<int>(min<int64_t>(16, T - m0)), cols = static_cast<int>(min<int64_t>(64, F - n0));
+    og.store(dg + m0 * F + n0, F, rows, cols);
+    ou.store(du + m0 * F + n0, F, rows, cols);
+  }
+};
+
+// A wave for each 64 columns.
 template <int ACT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
                                                          int64_t lddh, int64_t T, int64_t F, uint16_t* __restrict__ dg,
                                                          uint16_t* __restrict__ du) {
   __shared__ __attribute__((aligned(16))) char smem[4][2][16 * 64 * 2];
-  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const int wave = ring_wave();
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, n0 = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 64;
   if (n0 >= F) return;
-  const int64_t fb = (F + 15) / 16, m = min<int64_t>(m0 + r, T - 1);
-  BlockOut<16, 64> og{smem[wave][0]}, ou{smem[wave][1]};
-  f32x4 g[4], u[4];
-  uint2 d[4];
+  GradBlock<ACT> b = {saved, dh, lddh, T, F, {smem[wave][0]}, {smem[wave][1]}, {}, {}, {}};
+  b.load(m0, n0);
+  b.form(n0);
+  b.store(dg, du, m0, n0);
+}
+
+// With the rank-wide product v = d . B: 64 tokens per workgroup, 16 to a wave, `per` runs of 64 columns one after the
+// other; the run's rows of both B in LDS, read across with the transposing read against the wave's own dg and du there.
+// (4352 tokens, 14336 wide, ranks 32 and 32: the separate product read the 250 MB of dg and du once more.)
+template <int ACT, int NB>
+__global__ __launch_bounds__(256) void gated_grad_rank_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
+                                                              int64_t lddh, uint16_t* __restrict__ dg,
+                                                              uint16_t* __restrict__ du, RankProduct v, int per) {
+  __shared__ __attribute__((aligned(16))) char smem[4][2][16 * 64 * 2], sb[64 * NB * 32];
+  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const int64_t T = v.T, F = v.K;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64 + wave * 16;
+  const int R = v.rank[0] + v.rank[1], ng = (v.rank[0] + 15) / 16, ppr = R / 8;  // (16-byte pieces of a row of both B)
+  const int64_t run0 = static_cast<int64_t>(blockIdx.y) * per, run1 = min<int64_t>((F + 63) / 64, run0 + per);
+  GradBlock<ACT> b = {saved, dh, lddh, T, F, {smem[wave][0]}, {smem[wave][1]}, {}, {}, {}};
+  u32x4 bv[2];  // at most 64 rows of 8 pieces: two each
+  auto piece = [&](int i, int& row, int& col, int& side) {
+    const int id = i * 256 + threadIdx.x;
+    row = id / ppr;
+    col = (id - row * ppr) * 8;
+    side = col >= v.rank[0] ? 1 : 0;
+    return id < 64 * ppr;
+  };
+  auto load_b = [&](int64_t n0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t n = n0 + i * 16;
-    if (n >= F) continue;
-    const float* b = saved + ((m0 >> 4) * fb + (n >> 4)) * 512 + lane * 4;
-    g[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(b));
-    u[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(b + 256));
-    // (F is a multiple of 8, and so is the row stride: 8 bytes never cross the end)
-    d[i] = n + q * 4 < F ? *reinterpret_cast<const uint2*>(dh + m * lddh + n + q * 4) : uint2{0u, 0u};
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n0 + i * 16 >= F) continue;
-    const float dv[4] = {__uint_as_float(d[i].x << 16), __uint_as_float(d[i].x & 0xffff0000u),
-                         __uint_as_float(d[i].y << 16), __uint_as_float(d[i].y & 0xffff0000u)};
-    float vg[4], vu[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float a, da;
-      act_of<ACT, true>(g[i][e], a, da);
-      vg[e] = dv[e] * u[i][e] * da;
-      vu[e] = dv[e] * a;
+    for (int i = 0; i < 2; ++i) {
+      int row, col, side;
+      const bool is = piece(i, row, col, side);
+      bv[i] = is && n0 + row < F ? *reinterpret_cast<const u32x4*>(v.A[side] + (n0 + row) * v.rank[side] +
+                                                                   (side ? col - v.rank[0] : col))
+                                 : u32x4{0u, 0u, 0u, 0u};
     }
-    og.put(r, i * 16 + q * 4, pack_bf16x2(vg[0], vg[1]), pack_bf16x2(vg[2], vg[3]));
-    ou.put(r, i * 16 + q * 4, pack_bf16x2(vu[0], vu[1]), pack_bf16x2(vu[2], vu[3]));
+  };
+  const bool here = m0 < T;  // (a wave without tokens still stages B)
+  f32x4 acc[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load_b(run0 * 64);
+  if (here) b.load(m0, run0 * 64);
+  for (int64_t run = run0; run < run1; ++run) {
+    const int64_t n0 = run * 64;
+    __syncthreads();  // (the last run's B has been read)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int row, col, side;
+      // (one adapter's columns behind the other's whole blocks; what lies between is no column that is kept)
+      if (piece(i, row, col, side))
+        *reinterpret_cast<u32x4*>(sb + row * NB * 32 + (side ? ng * 16 + col - v.rank[0] : col) * 2) = bv[i];
+    }
+    if (here) b.form(n0);
+    if (run + 1 < run1) {  // (on their way while this run is multiplied and stored)
+      load_b(n0 + 64);
+      if (here) b.load(m0, n0 + 64);
+    }
+    __syncthreads();
+    if (!here) continue;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const bool in = n0 + kk * 32 + 8 * q < F;
+      bf16x8 d[2];
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(smem[wave][side] + b.og.at(r, kk * 4 + q));
+        d[side] = __builtin_bit_cast(bf16x8, in ? w : u32x4{0u, 0u, 0u, 0u});
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const char* at = sb + (kk * 32 + 8 * q + (r >> 2)) * NB * 32 + i * 32 + (r & 3) * 8;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * NB * 32));
+        const bf16x8 a = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, i < ng ? d[0] : d[1], acc[i], 0, 0, 0);
+      }
+    }
+    b.store(dg, du, m0, n0);
   }
-  const int rows = static_cast<int>(min<int64_t>(16, T - m0)), cols = static_cast<int>(min<int64_t>(64, F - n0));
-  og.store(dg + m0 * F + n0, F, rows, cols);
-  ou.store(du + m0 * F + n0, F, rows, cols);
+  if (m0 + r >= T) return;
+  float* row = v.part + (static_cast<int64_t>(blockIdx.y) * T + m0 + r) * R;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int side = i < ng ? 0 : 1, c = (side ? i - ng : i) * 16 + 4 * q;
+    if (c < v.rank[side]) *reinterpret_cast<f32x4*>(row + (side ? v.rank[0] : 0) + c) = acc[i];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -961,13 +1066,34 @@ hipError_t launch_gated_few(const GatedFew& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,
-                             uint16_t* dg, uint16_t* du, hipStream_t s) {
-  const dim3 grid(blocks_of(T, 16), blocks_of(F, 256)), block(256);
-  if (act == 0) hipLaunchKernelGGL(gated_grad_kernel<0>, grid, block, 0, s, saved, dh, lddh, T, F, dg, du);
-  else if (act == 1) hipLaunchKernelGGL(gated_grad_kernel<1>, grid, block, 0, s, saved, dh, lddh, T, F, dg, du);
-  else hipLaunchKernelGGL(gated_grad_kernel<2>, grid, block, 0, s, saved, dh, lddh, T, F, dg, du);
+template <int ACT>
+static hipError_t launch_gated_grad_act(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F,
+                                        uint16_t* dg, uint16_t* du, const RankProduct* v, hipStream_t s) {
+  if (v == nullptr) {
+    hipLaunchKernelGGL(gated_grad_kernel<ACT>, dim3(blocks_of(T, 16), blocks_of(F, 256)), dim3(256), 0, s, saved, dh, lddh, T,
+                       F, dg, du);
+    return hipGetLastError();
+  }
+  int S, per;
+  grad_plan(T, F, &S, &per);
+  const dim3 grid(blocks_of(T, 64), static_cast<unsigned>(S)), block(256);
+  const int nb = (v->rank[0] + 15) / 16 + (v->rank[1] + 15) / 16;
+  if (nb == 1) hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 1>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
+  else if (nb == 2) hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 2>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
+  else if (nb == 3) hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 3>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
+  else hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 4>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned blocks = blocks_of(T * (pair_ld(v->rank[0] + v->rank[1]) / 4), 256);
+  hipLaunchKernelGGL(rank_finish_kernel, dim3(blocks), dim3(256), 0, s, *v, S, static_cast<int>(blocks), *v, 0);
   return hipGetLastError();
+}
+
+hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,
+                             uint16_t* dg, uint16_t* du, const RankProduct* v, hipStream_t s) {
+  if (act == 0) return launch_gated_grad_act<0>(saved, dh, lddh, T, F, dg, du, v, s);
+  if (act == 1) return launch_gated_grad_act<1>(saved, dh, lddh, T, F, dg, du, v, s);
+  return launch_gated_grad_act<2>(saved, dh, lddh, T, F, dg, du, v, s);
 }
 
 hipError_t launch_contract(const Contract& p, hipStream_t s) {

@@ -191,9 +191,27 @@ inline int64_t gated_blocks(int64_t n) { return (n + 15) / 16; }
 inline size_t gated_saved_bytes(int64_t T, int64_t F) {
   return static_cast<size_t>(gated_blocks(T)) * static_cast<size_t>(gated_blocks(F)) * 512 * 4;
 }
-// dg = dh . u . act'(g) and du = dh . act(g), bf16 [T, F] each.
+// dg = dh . u . act'(g) and du = dh . act(g), bf16 [T, F] each, and with v (its x are dg and du) the rank-wide product of
+// them: up to four blocks of 16 columns, formed from the values as they pass, in S parts of `per` runs of 64 columns
+// (grad_with_ranks; more columns take launch_rank_products). Workgroups of 64 tokens, four to each of 256 units
+// where F and 32 parts allow it.
+inline bool grad_with_ranks(int64_t R0, int64_t R1) { return R0 + R1 > 0 && (R0 + 15) / 16 + (R1 + 15) / 16 <= 4; }
+inline void grad_plan(int64_t T, int64_t F, int* S, int* per) {
+  const int64_t mt = (T + 63) / 64, runs = (F + 63) / 64;
+  int64_t s = (1024 + mt - 1) / mt;
+  s = s > 32 ? 32 : s;
+  s = s > runs ? runs : s;
+  *per = static_cast<int>((runs + s - 1) / s);
+  *S = static_cast<int>((runs + *per - 1) / *per);
+}
+inline size_t grad_part_bytes(int64_t T, int64_t F, int64_t R0, int64_t R1) {
+  if (!grad_with_ranks(R0, R1)) return 0;
+  int S, per;
+  grad_plan(T, F, &S, &per);
+  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R0 + R1) * 4;
+}
 hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,
-                             uint16_t* dg, uint16_t* du, hipStream_t s);
+                             uint16_t* dg, uint16_t* du, const RankProduct* v, hipStream_t s);
 
 // ---------------------------------------------------------------- token contractions
 // out_i [J, M] (transposed: one adapter's rows behind the other's) or [M, J] = P^T . Q over the tokens, Q the columns

@@ -322,6 +322,7 @@ GatedLayout gated_bwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_
     const int64_t a = i & 1 ? 0 : rg, b = i & 2 ? 0 : ru;
     if (a + b > 0) {
       part = std::max(part, lora::rank_part_bytes(T, F, a, b, true));
+      part = std::max(part, lora::grad_part_bytes(T, F, a, b));
       const int64_t ta = lora::contract_tiles(K, a + b), tb = lora::contract_tiles(F, a) + lora::contract_tiles(F, b);
       part = std::max(part, std::max(lora::contract_part_bytes(T, ta, K * (a + b)), lora::contract_part_bytes(T, tb, F * (a + b))));
       part = std::max(part, lora::contract_part_bytes(T, ta + tb, (K + F) * (a + b)));
@@ -491,20 +492,20 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
   }
   auto* dg = reinterpret_cast<uint16_t*>(ws + L.dg);
   auto* du = reinterpret_cast<uint16_t*>(ws + L.du);
-  if (lora::launch_gated_grad(reinterpret_cast<const float*>(keep), bf(dh), lddh, T, F, act, dg, du, st) != hipSuccess)
-    return LORA_ERR_HIP;
   const int64_t R = s[0].rank + s[1].rank, ldt = lora::pair_ld(R);
   auto* vt = reinterpret_cast<uint16_t*>(ws + L.vt);
   const bool want_a = dA_gate != nullptr || dA_up != nullptr, want_b = dB_gate != nullptr || dB_up != nullptr;
-  if (R > 0 && (dx != nullptr || want_a)) {  // v = s d B of each projection
-    RankProduct v;
-    std::memset(&v, 0, sizeof(v));
-    v.x[0] = dg; v.x[1] = du; v.ldx = F; v.T = T; v.K = F; v.part = part; v.tt = vt;
-    for (int i = 0; i < 2; ++i) {
-      v.A[i] = bf(s[i].B); v.rank[i] = static_cast<int>(s[i].rank); v.scale[i] = s[i].scale;
-    }
-    if (lora::launch_rank_products(nullptr, &v, st) != hipSuccess) return LORA_ERR_HIP;
+  const bool need_v = R > 0 && (dx != nullptr || want_a), joint = need_v && lora::grad_with_ranks(s[0].rank, s[1].rank);
+  RankProduct v;  // v = s d B of each projection
+  std::memset(&v, 0, sizeof(v));
+  v.x[0] = dg; v.x[1] = du; v.ldx = F; v.T = T; v.K = F; v.part = part; v.tt = vt;
+  for (int i = 0; i < 2; ++i) {
+    v.A[i] = bf(s[i].B); v.rank[i] = static_cast<int>(s[i].rank); v.scale[i] = s[i].scale;
   }
+  if (lora::launch_gated_grad(reinterpret_cast<const float*>(keep), bf(dh), lddh, T, F, act, dg, du,
+                              joint ? &v : nullptr, st) != hipSuccess)
+    return LORA_ERR_HIP;
+  if (need_v && !joint && lora::launch_rank_products(nullptr, &v, st) != hipSuccess) return LORA_ERR_HIP;
   if (dx != nullptr) {
     RingArgs g;
     std::memset(&g, 0, sizeof(g));

@@ -103,11 +103,20 @@ hipError_t launch_gated_few(const GatedFew& p, hipStream_t) {
   return hipSuccess;
 }
 hipError_t launch_gated_grad(const float* saved, const uint16_t*, int64_t, int64_t T, int64_t F, int, uint16_t* dg,
-                             uint16_t* du, hipStream_t) {
+                             uint16_t* du, const RankProduct* v, hipStream_t) {
   ++launches;
   reads(saved, gated_saved_bytes(T, F), "kept by the forward");
   writes(dg, rows(T, F, 2), "dg", true);
   writes(du, rows(T, F, 2), "du", true);
+  if (v != nullptr) {
+    if (!grad_with_ranks(v->rank[0], v->rank[1]) || v->x[0] != dg || v->x[1] != du || v->T != T || v->K != F) fail("product");
+    int S, per;
+    grad_plan(T, F, &S, &per);
+    if (S < 1 || S > 32 || static_cast<int64_t>(S - 1) * per >= (F + 63) / 64 || static_cast<int64_t>(S) * per < (F + 63) / 64)
+      fail("plan of the product");
+    writes(v->part, grad_part_bytes(T, F, v->rank[0], v->rank[1]), "its partial sums", false);
+    writes(v->tt, rows(T, pair_ld(v->rank[0] + v->rank[1]), 2), "its rows", true);
+  }
   return hipSuccess;
 }
 hipError_t launch_contract(const Contract& p, hipStream_t) {
