@@ -284,8 +284,9 @@ struct RingWork {
 // A part's sums as the registers hold them, [unit][wave][j][i][lane] of four, and the sum of a tile's parts in order for
 // column block j (16 tokens) of a wave.
 template <class P>
-__device__ __forceinline__ f32x4* part_at(float* part, int unit, int j, int i) {
-  return reinterpret_cast<f32x4*>(part) + (((static_cast<int64_t>(unit) * P::WAVES + ring_wave()) * P::NJ + j) * P::NI + i) * 64;
+__device__ __forceinline__ f32x4* part_at(float* part, int unit, int j, int i, int other = 0) {  // (of wave + other)
+  return reinterpret_cast<f32x4*>(part) +
+         (((static_cast<int64_t>(unit) * P::WAVES + ring_wave() + other) * P::NJ + j) * P::NI + i) * 64;
 }
 template <class P>
 __device__ __forceinline__ void put_part(const f32x4 (&acc)[P::NI][P::NJ], float* part, int unit) {
@@ -296,13 +297,13 @@ __device__ __forceinline__ void put_part(const f32x4 (&acc)[P::NI][P::NJ], float
     for (int i = 0; i < P::NI; ++i) part_at<P>(part, unit, j, i)[lane] = acc[i][j];
 }
 template <class P>
-__device__ __forceinline__ void sum_parts(f32x4 (&acc)[P::NI][1], float* part, int rem_tile, int S, int j) {
+__device__ __forceinline__ void sum_parts(f32x4 (&acc)[P::NI][1], float* part, int rem_tile, int S, int j, int other = 0) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < P::NI; ++i) acc[i][0] = part_at<P>(part, rem_tile * S, j, i)[lane];
+  for (int i = 0; i < P::NI; ++i) acc[i][0] = part_at<P>(part, rem_tile * S, j, i, other)[lane];
   for (int z = 1; z < S; ++z)
 #pragma unroll
-    for (int i = 0; i < P::NI; ++i) acc[i][0] += part_at<P>(part, rem_tile * S + z, j, i)[lane];
+    for (int i = 0; i < P::NI; ++i) acc[i][0] += part_at<P>(part, rem_tile * S + z, j, i, other)[lane];
 }
 
 // The kernel's first argument read again, for what comes behind the loop: its fields are then not kept in scalar registers

@@ -39,7 +39,7 @@ __device__ __forceinline__ void rank_nt(const RankProduct& p, int ks, int bx, in
   const int kb_total = static_cast<int>(p.K * 2), nk = (kb_total + P::RB - 1) / P::RB;
   const bool k_tail = kb_total % P::RB != 0;
   const uint32_t ldx_b = static_cast<uint32_t>(p.ldx * 2), lda_b = static_cast<uint32_t>(p.K * 2);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x[0] + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.ldx, static_cast<uint32_t>(rows_m) * ldx_b);
   const __amdgpu_buffer_rsrc_t ar0 = make_rsrc(p.A[0], static_cast<uint32_t>(p.rank[0]) * lda_b);
   const __amdgpu_buffer_rsrc_t ar1 = make_rsrc(p.A[1], static_cast<uint32_t>(p.rank[1]) * lda_b);
   TileOffsets<P, P::BM> ox;
@@ -107,7 +107,8 @@ __device__ __forceinline__ void rank_nt(const RankProduct& p, int ks, int bx, in
 }
 
 // tt = the two terms of scale . sum of the splits, in order; zeros behind them. 4 columns per thread.
-__device__ __forceinline__ void rank_finish(const RankProduct& p, int S, int64_t bx) {
+// (`terms`: rows of zeros that many behind.)
+__device__ __forceinline__ void rank_finish(const RankProduct& p, int S, int64_t bx, int terms = 0) {
   const int R = p.rank[0] + p.rank[1], ldt = static_cast<int>((2 * R + 63) / 64 * 64), quads = ldt / 4;
   const int64_t idx = bx * 256 + threadIdx.x;
   if (idx >= p.T * quads) return;
@@ -135,11 +136,16 @@ __device__ __forceinline__ void rank_finish(const RankProduct& p, int S, int64_t
     }
   }
   *reinterpret_cast<uint2*>(p.tt + t * ldt + c) = w;
+  if (terms > 0) *reinterpret_cast<uint2*>(p.tt + (terms + t) * ldt + c) = uint2{0u, 0u};
 }
 
 __global__ __launch_bounds__(256) void rank_finish_kernel(RankProduct a, int Sa, int blocks, RankProduct b, int Sb) {
   if (static_cast<int>(blockIdx.x) < blocks) rank_finish(a, Sa, blockIdx.x);
   else rank_finish(b, Sb, blockIdx.x - blocks);
+}
+
+__global__ __launch_bounds__(256) void grad_rank_finish_kernel(RankProduct v, int S, int terms) {
+  rank_finish(v, S, blockIdx.x, terms);
 }
 
 // Few tokens: 16 tokens by up to 64 columns per workgroup of 16 waves that share K, 32 indices at a time in turn, straight
@@ -226,19 +232,16 @@ __device__ __forceinline__ void rank_few_sum(f32x4 (&acc)[NB], const uint16_t* x
   }
 }
 
-// Column block of a product (side of the gradient's): sums, then the two terms of its columns in the rows of tt. `pad`:
-// this one writes the zeros behind the terms too.
+// A product's sums, then the two terms in the rows of tt and zeros behind them.
 template <bool NN, bool DROP, int NB>
-__device__ __forceinline__ void rank_few(const RankProduct& p, int side, bool pad, int64_t m0, char* smem) {
+__device__ __forceinline__ void rank_few(const RankProduct& p, int64_t m0, char* smem) {
   const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
-  const uint16_t* A[2] = {p.A[NN ? side : 0], NN ? nullptr : p.A[1]};
-  const int rank[2] = {p.rank[NN ? side : 0], NN ? 0 : p.rank[1]};
-  const int R = rank[0] + rank[1], Rall = p.rank[0] + p.rank[1], c0 = NN && side ? p.rank[0] : 0;
+  const int R = p.rank[0] + p.rank[1];
   Dropper d;
   d.blocks = p.K / 8;
   if constexpr (DROP) d.init(p.drop, p.K);
   f32x4 acc[NB];
-  rank_few_sum<NN, DROP, NB>(acc, p.x[NN ? side : 0], p.ldx, A, rank, p.K, p.T, d, m0, smem + wave * NB * 1024);
+  rank_few_sum<NN, DROP, NB>(acc, p.x, p.ldx, p.A, p.rank, p.K, p.T, d, m0, smem + wave * NB * 1024);
   __syncthreads();  // (the waves' pieces become their sums)
   float* sums = reinterpret_cast<float*>(smem);  // [wave][16 NB columns][16 tokens]
 #pragma unroll
@@ -246,49 +249,42 @@ __device__ __forceinline__ void rank_few(const RankProduct& p, int side, bool pa
 #pragma unroll
     for (int e = 0; e < 4; ++e) sums[(wave * NB * 16 + i * 16 + 4 * q + e) * 16 + r] = acc[i][e];
   __syncthreads();
-  const int ldt = (2 * Rall + 63) / 64 * 64;
+  const int ldt = (2 * R + 63) / 64 * 64;
   for (int idx = threadIdx.x; idx < 16 * R; idx += kFewWaves * 64) {
     const int t = idx / R, c = idx - t * R;
     if (m0 + t >= p.T) continue;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) v += sums[(w * NB * 16 + c) * 16 + t];
-    v *= c0 + c < p.rank[0] ? p.scale[0] : p.scale[1];
+    v *= c < p.rank[0] ? p.scale[0] : p.scale[1];
     const uint16_t hi = f32_to_bf16_rne(v);
     const float h = bf16_to_f32(hi);
-    uint16_t* row = p.tt + (m0 + t) * ldt + c0 + c;
+    uint16_t* row = p.tt + (m0 + t) * ldt + c;
     row[0] = hi;
-    row[Rall] = __builtin_isfinite(h) ? f32_to_bf16_rne(v - h) : static_cast<uint16_t>(0);
+    row[R] = __builtin_isfinite(h) ? f32_to_bf16_rne(v - h) : static_cast<uint16_t>(0);
   }
-  if (pad) {
-    const int z = ldt - 2 * Rall;
-    for (int idx = threadIdx.x; idx < 16 * z; idx += kFewWaves * 64) {
-      const int t = idx / z;
-      if (m0 + t < p.T) p.tt[(m0 + t) * ldt + 2 * Rall + idx - t * z] = 0;
-    }
+  const int z = ldt - 2 * R;
+  for (int idx = threadIdx.x; idx < 16 * z; idx += kFewWaves * 64) {
+    const int t = idx / z;
+    if (m0 + t < p.T) p.tt[(m0 + t) * ldt + 2 * R + idx - t * z] = 0;
   }
 }
 
 template <bool NN, bool DROP>
-__device__ __forceinline__ void rank_few_nb(const RankProduct& p, int side, bool pad, int64_t m0, char* smem) {
-  const int R = NN ? p.rank[side] : p.rank[0] + p.rank[1];
-  if (R <= 16) rank_few<NN, DROP, 1>(p, side, pad, m0, smem);
-  else if (R <= 32) rank_few<NN, DROP, 2>(p, side, pad, m0, smem);
-  else rank_few<NN, DROP, 4>(p, side, pad, m0, smem);
+__device__ __forceinline__ void rank_few_nb(const RankProduct& p, int64_t m0, char* smem) {
+  const int R = p.rank[0] + p.rank[1];
+  if (R <= 16) rank_few<NN, DROP, 1>(p, m0, smem);
+  else if (R <= 32) rank_few<NN, DROP, 2>(p, m0, smem);
+  else rank_few<NN, DROP, 4>(p, m0, smem);
 }
 
-// Grid (blocks of 16 tokens, products): a's (where it is there), then b's one or two sides.
+// Grid (blocks of 16 tokens, products): a's (where it is there), then b's.
 template <bool DROP>
 __global__ __launch_bounds__(kFewWaves * 64) void rank_few_kernel(RankProduct a, int n_a, RankProduct b) {
   __shared__ __attribute__((aligned(1024))) char smem[kFewWaves * 4 * 1024];
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const int y = static_cast<int>(blockIdx.y) - n_a;
-  if (y < 0) {
-    rank_few_nb<false, DROP>(a, 0, true, m0, smem);
-  } else {
-    const int side = b.rank[0] == 0 ? 1 : y;
-    rank_few_nb<true, false>(b, side, y == 0, m0, smem);
-  }
+  if (static_cast<int>(blockIdx.y) < n_a) rank_few_nb<false, DROP>(a, m0, smem);
+  else rank_few_nb<true, false>(b, m0, smem);
 }
 
 // (NJ: blocks of 16 tokens from m0 on)
@@ -371,7 +367,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void ring_kernel(RingArgs p, in
     ring_run<P, false>(acc, op, ns, smem, wm0, wn0);
   } else if constexpr (FORM != kFormNnDrop) {
     NnOp<P, FORM == kFormNn2 ? 2 : 1, FORM == kFormNn2 ? 2 : 1> op;
-    op.init(p.x, p.ldx, p.W, p.K, p.T, p.N, m0, n0, work.lo, work.hi);
+    op.init(p.x, p.ldx, p.W, p.K, FORM == kFormNn2 ? p.T + p.terms : p.T, p.N, m0, n0, work.lo, work.hi);
     op.extend(p, m0, n0);
     ring_run<P, true>(acc, op, ns, smem, wm0, wn0);
   } else {
@@ -399,26 +395,33 @@ __global__ __launch_bounds__(P::THREADS) void ring_join_kernel(RingArgs p, int m
   const int64_t n0 = static_cast<int64_t>(tile.n) * P::BN + (wave / P::WAVES_M) * P::WN;
   f32x4 acc[P::NI][1];
   sum_parts<P>(acc, p.part, blockIdx.x, p.S, j);
+  if constexpr (P::BM == 2 * kTerms && P::WM == kTerms) {
+    if (p.terms > 0) {  // the second terms are the next wave's tokens
+      if (wave % P::WAVES_M != 0) return;
+      f32x4 mid[P::NI][1];
+      sum_parts<P>(mid, p.part, blockIdx.x, p.S, j, 1);
+#pragma unroll
+      for (int i = 0; i < P::NI; ++i) acc[i][0] += mid[i][0];
+    }
+  }
   store_block<P, 1>(acc, p, m0, n0, smem);
 }
 
 // Rank-wide product over rows of the contraction (the gradient's, B [K, rank] as it lies): 128 tokens and up to 128
-// columns of one adapter per workgroup, K in splits. Most of the MFMA's columns are empty for small ranks;
-// the kernel is bound by reading x.
+// columns per workgroup, K in splits. Most of the MFMA's columns are empty for small ranks; the kernel is bound by
+// reading x.
 __device__ __forceinline__ void rank_nn(const RankProduct& p, int ks, int bx, int by, int bz, char* smem) {
   using P = Ring128;
-  const int tiles0 = (p.rank[0] + 127) / 128, side = by >= tiles0 ? 1 : 0;
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
-  const int64_t m0 = static_cast<int64_t>(bx) * P::BM;
-  const int64_t n0 = static_cast<int64_t>(by - (side ? tiles0 : 0)) * P::BN;
+  const int64_t m0 = static_cast<int64_t>(bx) * P::BM, n0 = static_cast<int64_t>(by) * P::BN;
   const int NS = static_cast<int>((p.K + 63) / 64), s_lo = bz * ks, s_hi = min(NS, s_lo + ks);
   NnOp<P, 1, 0> op;
-  op.init(&p.x[side], p.ldx, &p.A[side], &p.K, p.T, p.rank[side], m0, n0, s_lo, s_hi);
+  op.init(&p.x, p.ldx, &p.A[0], &p.K, p.T, p.rank[0], m0, n0, s_lo, s_hi);
   f32x4 acc[P::NI][P::NJ];
   ring_run<P, true>(acc, op, s_hi - s_lo, smem, wm0, wn0);
-  const int R = p.rank[0] + p.rank[1], c0 = side ? p.rank[0] : 0;
-  store_part<P>(acc, p.part + static_cast<int64_t>(bz) * p.T * R + c0, R, m0 + wm0, n0 + wn0, p.T, p.rank[side]);
+  const int R = p.rank[0];
+  store_part<P>(acc, p.part + static_cast<int64_t>(bz) * p.T * R, R, m0 + wm0, n0 + wn0, p.T, R);
 }
 
 // The first n_nt workgroups make the one product (grid (m-tiles, rows, splits) counted x first), the others the other.
@@ -632,18 +635,28 @@ __global__ __launch_bounds__(256) void gated_few_finish_kernel(GatedFew p) {
   }
 }
 
-// dg and du of 16 tokens x 64 columns, from the blocks that the forward kept, into a wave's LDS; then whole rows of them.
-template <int ACT>
-struct GradBlock {
-  const float* saved;
-  const uint16_t* dh;
-  int64_t lddh, T, F;
-  BlockOut<16, 64> og, ou;
+// dg and du, and v = dg . B_gate beside du . B_up (NB blocks of 16 of its columns; 0: none): 64 tokens per workgroup, 16 to
+// a wave, `per` runs of 64 columns one after the other, from the blocks that the forward kept. A wave's values go through
+// LDS as two bf16 terms each, which the MFMAs take from there, against the run's rows of both B, read across with the
+// transposing read; the first terms are stored (up to 64 tokens both). More blocks than eight are further grid layers,
+// which form the values again and store none. HBM-bound: 4352 tokens, 14336 wide, ranks 32 and 32: 204 us, 873 MB at
+// 4.3 TB/s (without second terms 189); a product of its own, from the stored values, took 75 us beside 195.
+template <int ACT, int NB>
+__global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
+                                                         int64_t lddh, int64_t T, int64_t F, uint16_t* __restrict__ dg,
+                                                         uint16_t* __restrict__ du, RankProduct v, int per) {
+  constexpr int PPR = NB > 0 ? 2 * NB : 1;  // 16-byte pieces of a run's row of B
+  __shared__ __attribute__((aligned(16))) char smem[4][2][2][16 * 64 * 2], sb[64 * PPR * 16];  // [wave][side][term]
+  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64 + wave * 16;
+  const int ng = (v.rank[0] + 15) / 16, first = static_cast<int>(blockIdx.z) * NB;
+  const int64_t run0 = static_cast<int64_t>(blockIdx.y) * per, run1 = min<int64_t>((F + 63) / 64, run0 + per);
+  const bool here = m0 < T, both = T <= kTerms;  // (a wave without tokens still stages B)
+  const bool stores = blockIdx.z == 0;
+  const int64_t fb = (F + 15) / 16, m = min<int64_t>(m0 + r, T - 1);
   f32x4 g[4], u[4];
   uint2 d[4];
-  __device__ __forceinline__ void load(int64_t m0, int64_t n0) {
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int64_t fb = (F + 15) / 16, m = min<int64_t>(m0 + r, T - 1);
+  auto load = [&](int64_t n0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t n = n0 + i * 16;
@@ -654,9 +667,22 @@ struct GradBlock {
       // (F is a multiple of 8, and so is the row stride: 8 bytes never cross the end)
       d[i] = n + q * 4 < F ? *reinterpret_cast<const uint2*>(dh + m * lddh + n + q * 4) : uint2{0u, 0u};
     }
-  }
-  __device__ __forceinline__ void form(int64_t n0) const {
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  };
+  auto put = [&](int side, int col, const float (&x)[4]) {
+    BlockOut<16, 64> hi{smem[wave][side][0]}, mid{smem[wave][side][1]};
+    const uint32_t lo2 = pack_bf16x2(x[0], x[1]), hi2 = pack_bf16x2(x[2], x[3]);
+    hi.put(r, col, lo2, hi2);
+    if (NB == 0 && !both) return;
+    float rest[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // (nothing behind an infinity)
+      const uint32_t w = e < 2 ? lo2 : hi2;
+      const float h = __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+      rest[e] = __builtin_isfinite(h) ? x[e] - h : 0.f;
+    }
+    mid.put(r, col, pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
+  };
+  auto form = [&](int64_t n0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (n0 + i * 16 >= F) continue;
@@ -670,112 +696,87 @@ struct GradBlock {
         vg[e] = dv[e] * u[i][e] * da;
         vu[e] = dv[e] * a;
       }
-      og.put(r, i * 16 + q * 4, pack_bf16x2(vg[0], vg[1]), pack_bf16x2(vg[2], vg[3]));
-      ou.put(r, i * 16 + q * 4, pack_bf16x2(vu[0], vu[1]), pack_bf16x2(vu[2], vu[3]));
+      put(0, i * 16 + q * 4, vg);
+      put(1, i * 16 + q * 4, vu);
     }
-  }
-  __device__ __forceinline__ void store(uint16_t* dg, uint16_t* du, int64_t m0, int64_t n0) const {
-    const int rows = static_cast<int>(min<int64_t>(16, T - m0)), cols = static_cast<int>(min<int64_t>(64, F - n0));
-    og.store(dg + m0 * F + n0, F, rows, cols);
-    ou.store(du + m0 * F + n0, F, rows, cols);
-  }
-};
-
-// A wave for each 64 columns.
-template <int ACT>
-__global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
-                                                         int64_t lddh, int64_t T, int64_t F, uint16_t* __restrict__ dg,
-                                                         uint16_t* __restrict__ du) {
-  __shared__ __attribute__((aligned(16))) char smem[4][2][16 * 64 * 2];
-  const int wave = ring_wave();
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, n0 = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 64;
-  if (n0 >= F) return;
-  GradBlock<ACT> b = {saved, dh, lddh, T, F, {smem[wave][0]}, {smem[wave][1]}, {}, {}, {}};
-  b.load(m0, n0);
-  b.form(n0);
-  b.store(dg, du, m0, n0);
-}
-
-// With the rank-wide product v = d . B: 64 tokens per workgroup, 16 to a wave, `per` runs of 64 columns one after the
-// other; the run's rows of both B in LDS, read across with the transposing read against the wave's own dg and du there.
-// (4352 tokens, 14336 wide, ranks 32 and 32: the separate product read the 250 MB of dg and du once more.)
-template <int ACT, int NB>
-__global__ __launch_bounds__(256) void gated_grad_rank_kernel(const float* __restrict__ saved, const uint16_t* __restrict__ dh,
-                                                              int64_t lddh, uint16_t* __restrict__ dg,
-                                                              uint16_t* __restrict__ du, RankProduct v, int per) {
-  __shared__ __attribute__((aligned(16))) char smem[4][2][16 * 64 * 2], sb[64 * NB * 32];
-  const int lane = threadIdx.x & 63, wave = ring_wave(), r = lane & 15, q = lane >> 4;
-  const int64_t T = v.T, F = v.K;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64 + wave * 16;
-  const int R = v.rank[0] + v.rank[1], ng = (v.rank[0] + 15) / 16, ppr = R / 8;  // (16-byte pieces of a row of both B)
-  const int64_t run0 = static_cast<int64_t>(blockIdx.y) * per, run1 = min<int64_t>((F + 63) / 64, run0 + per);
-  GradBlock<ACT> b = {saved, dh, lddh, T, F, {smem[wave][0]}, {smem[wave][1]}, {}, {}, {}};
-  u32x4 bv[2];  // at most 64 rows of 8 pieces: two each
-  auto piece = [&](int i, int& row, int& col, int& side) {
-    const int id = i * 256 + threadIdx.x;
-    row = id / ppr;
-    col = (id - row * ppr) * 8;
-    side = col >= v.rank[0] ? 1 : 0;
-    return id < 64 * ppr;
   };
+  // this thread's pieces of a run's rows of B (zeros where a column is none of an adapter's)
+  constexpr int NP = NB > 0 ? (64 * PPR + 255) / 256 : 1;
+  u32x4 bv[NP];
   auto load_b = [&](int64_t n0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int row, col, side;
-      const bool is = piece(i, row, col, side);
-      bv[i] = is && n0 + row < F ? *reinterpret_cast<const u32x4*>(v.A[side] + (n0 + row) * v.rank[side] +
-                                                                   (side ? col - v.rank[0] : col))
-                                 : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < NP; ++i) {
+      const int id = i * 256 + threadIdx.x, row = id / PPR, pc = id - row * PPR, blk = first + pc / 2;
+      const int side = blk >= ng ? 1 : 0, col = (side ? blk - ng : blk) * 16 + (pc & 1) * 8;
+      bv[i] = row < 64 && n0 + row < F && col < v.rank[side]
+                  ? *reinterpret_cast<const u32x4*>(v.A[side] + (n0 + row) * v.rank[side] + col)
+                  : u32x4{0u, 0u, 0u, 0u};
     }
   };
-  const bool here = m0 < T;  // (a wave without tokens still stages B)
-  f32x4 acc[NB];
+  f32x4 acc[NB > 0 ? NB : 1];
 #pragma unroll
   for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load_b(run0 * 64);
-  if (here) b.load(m0, run0 * 64);
+  if (NB > 0) load_b(run0 * 64);
+  if (here) load(run0 * 64);
   for (int64_t run = run0; run < run1; ++run) {
     const int64_t n0 = run * 64;
-    __syncthreads();  // (the last run's B has been read)
+    if (NB > 0) {
+      __syncthreads();  // (the last run's B has been read)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int row, col, side;
-      // (one adapter's columns behind the other's whole blocks; what lies between is no column that is kept)
-      if (piece(i, row, col, side))
-        *reinterpret_cast<u32x4*>(sb + row * NB * 32 + (side ? ng * 16 + col - v.rank[0] : col) * 2) = bv[i];
+      for (int i = 0; i < NP; ++i) {
+        const int id = i * 256 + threadIdx.x;
+        if (id < 64 * PPR) *reinterpret_cast<u32x4*>(sb + id * 16) = bv[i];
+      }
     }
-    if (here) b.form(n0);
+    if (here) form(n0);
     if (run + 1 < run1) {  // (on their way while this run is multiplied and stored)
-      load_b(n0 + 64);
-      if (here) b.load(m0, n0 + 64);
+      if (NB > 0) load_b(n0 + 64);
+      if (here) load(n0 + 64);
     }
-    __syncthreads();
+    if (NB > 0) __syncthreads();
     if (!here) continue;
+    if constexpr (NB > 0) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const bool in = n0 + kk * 32 + 8 * q < F;
-      bf16x8 d[2];
+      for (int kk = 0; kk < 2; ++kk) {
+        const bool in = n0 + kk * 32 + 8 * q < F;
+        bf16x8 x[2][2];
 #pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(smem[wave][side] + b.og.at(r, kk * 4 + q));
-        d[side] = __builtin_bit_cast(bf16x8, in ? w : u32x4{0u, 0u, 0u, 0u});
-      }
+        for (int side = 0; side < 2; ++side)
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const char* at = sb + (kk * 32 + 8 * q + (r >> 2)) * NB * 32 + i * 32 + (r & 3) * 8;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * NB * 32));
-        const bf16x8 a = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, i < ng ? d[0] : d[1], acc[i], 0, 0, 0);
+          for (int term = 0; term < 2; ++term) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(smem[wave][side][term] + BlockOut<16, 64>::at(r, kk * 4 + q));
+            x[side][term] = __builtin_bit_cast(bf16x8, in ? w : u32x4{0u, 0u, 0u, 0u});
+          }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const char* at = sb + (kk * 32 + 8 * q + (r >> 2)) * NB * 32 + i * 32 + (r & 3) * 8;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * NB * 32));
+          const bf16x8 a = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          const bool up = first + i >= ng;
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, up ? x[1][term] : x[0][term], acc[i], 0, 0, 0);
+        }
       }
     }
-    b.store(dg, du, m0, n0);
+    if (!stores) continue;
+    const int rows = static_cast<int>(min<int64_t>(16, T - m0)), cols = static_cast<int>(min<int64_t>(64, F - n0));
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int term = 0; term < 2; ++term) {
+        if (term > 0 && !both) continue;
+        const BlockOut<16, 64> out{smem[wave][side][term]};
+        out.store((side ? du : dg) + (m0 + term * kTerms) * F + n0, F, rows, cols);
+      }
   }
-  if (m0 + r >= T) return;
+  if (NB == 0 || m0 + r >= T) return;
+  const int R = v.rank[0] + v.rank[1];
   float* row = v.part + (static_cast<int64_t>(blockIdx.y) * T + m0 + r) * R;
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int side = i < ng ? 0 : 1, c = (side ? i - ng : i) * 16 + 4 * q;
+    const int blk = first + i, side = blk >= ng ? 1 : 0, c = (side ? blk - ng : blk) * 16 + 4 * q;
     if (c < v.rank[side]) *reinterpret_cast<f32x4*>(row + (side ? v.rank[0] : 0) + c) = acc[i];
   }
 }
@@ -832,9 +833,11 @@ __global__ __launch_bounds__(256, 2) void contract_kernel(Contract p, int S, int
   const int j0 = id / it * kCtJ, jn = min(kCtJ, k.J - j0), nj = (jn + 15) / 16;
   const int64_t i0 = static_cast<int64_t>(id % it) * kCtI;
   const int cols = static_cast<int>(min<int64_t>(kCtI, k.M - i0));
-  const int z = blockIdx.y;
-  const int64_t t_lo = z * chunk, t_hi = min<int64_t>(p.T, t_lo + chunk);
-  const int nst = t_hi > t_lo ? static_cast<int>((t_hi - t_lo + kCtT - 1) / kCtT) : 0;
+  const int z = blockIdx.y, S1 = S / p.halves, half = z >= S1 ? 1 : 0;
+  const int64_t t_lo = (z - half * S1) * chunk, t_hi = min<int64_t>(p.T, t_lo + chunk);
+  const bool none = half > 0 && k.terms == 0;
+  const int nst = t_hi > t_lo && !none ? static_cast<int>((t_hi - t_lo + kCtT - 1) / kCtT) : 0;
+  const uint16_t* P = k.P + (half ? k.terms * k.ldp : 0);
   const uint32_t ldp_b = static_cast<uint32_t>(k.ldp * 2), ldt_b = static_cast<uint32_t>(k.ldt * 2);
   // per-lane offsets: 4 instructions of P (2 rows of 512 bytes each), 2 of Q (4 rows of 256)
   uint32_t vp[4], vq[2];
@@ -860,7 +863,7 @@ __global__ __launch_bounds__(256, 2) void contract_kernel(Contract p, int S, int
     const int rows = s < nst ? static_cast<int>(min<int64_t>(kCtT, t_hi - t0)) : 0;
     const int64_t at = rows > 0 ? t0 : 0;
     const __amdgpu_buffer_rsrc_t pr = make_rsrc(
-        k.P + at * k.ldp + i0, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldp_b + static_cast<uint32_t>(cols) * 2 : 0u);
+        P + at * k.ldp + i0, rows > 0 ? static_cast<uint32_t>(rows - 1) * ldp_b + static_cast<uint32_t>(cols) * 2 : 0u);
     const __amdgpu_buffer_rsrc_t qr = make_rsrc(k.tt + at * k.ldt, static_cast<uint32_t>(rows) * ldt_b);
 #pragma unroll
     for (int l = 0; l < 4; ++l)
@@ -962,28 +965,29 @@ unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + p
 hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hipStream_t s) {
   RankProduct a = {}, b = {};
   int Sa = 0, ka = 1, n_nt = 0, ca = 1, Sb = 0, kb = 1, n_nn = 0, cb = 1;
-  bool narrow = true, drop = false;
+  bool narrow = true, drop = false, few = true;
   if (nt != nullptr) {
     a = *nt;
     const int64_t R = a.rank[0] + a.rank[1];
     narrow = R <= 64;
     drop = a.drop.thr != 0;
-    rank_plan(a.T, a.K, rank_tasks(R, 0, false), &Sa, &ka);
+    few = rank_few(a.T, a.K, R);
+    rank_plan(a.T, a.K, rank_tasks(R, false), &Sa, &ka);
     ca = static_cast<int>(narrow ? 1 : (R + 127) / 128);
     n_nt = static_cast<int>((a.T + 127) / 128) * ca * Sa;
   }
   if (nn != nullptr) {
     b = *nn;
-    rank_plan(b.T, b.K, rank_tasks(b.rank[0], b.rank[1], true), &Sb, &kb);
-    cb = static_cast<int>(rank_tasks(b.rank[0], b.rank[1], true));
+    few = few && rank_few(b.T, b.K, b.rank[0]);
+    cb = static_cast<int>(rank_tasks(b.rank[0], true));
+    rank_plan(b.T, b.K, cb, &Sb, &kb);
     n_nn = static_cast<int>((b.T + 127) / 128) * cb * Sb;
   }
-  if ((nt == nullptr || rank_few(a.T, a.K, a.rank[0], a.rank[1], false)) &&
-      (nn == nullptr || rank_few(b.T, b.K, b.rank[0], b.rank[1], true))) {
-    const int na = nt != nullptr ? 1 : 0, nb = nn != nullptr ? (b.rank[0] > 0 ? 1 : 0) + (b.rank[1] > 0 ? 1 : 0) : 0;
-    const dim3 fg(blocks_of(nt != nullptr ? a.T : b.T, 16), static_cast<unsigned>(na + nb));
-    if (drop) hipLaunchKernelGGL(rank_few_kernel<true>, fg, dim3(kFewWaves * 64), 0, s, a, na, b);
-    else hipLaunchKernelGGL(rank_few_kernel<false>, fg, dim3(kFewWaves * 64), 0, s, a, na, b);
+  if (few) {
+    const unsigned na = nt != nullptr ? 1 : 0, nb = nn != nullptr ? 1 : 0;
+    const dim3 fg(blocks_of(nt != nullptr ? a.T : b.T, 16), na + nb), fb(kFewWaves * 64);
+    if (drop) hipLaunchKernelGGL(rank_few_kernel<true>, fg, fb, 0, s, a, static_cast<int>(na), b);
+    else hipLaunchKernelGGL(rank_few_kernel<false>, fg, fb, 0, s, a, static_cast<int>(na), b);
     return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(n_nt + n_nn)), block(256);
@@ -1003,7 +1007,7 @@ hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hi
 
 template <class P, int FORM>
 hipError_t launch_ring_cfg(const RingArgs& p, int NS, hipStream_t s) {
-  const int mt = static_cast<int>((p.T + P::BM - 1) / P::BM), nt = static_cast<int>((p.N + P::BN - 1) / P::BN);
+  const int mt = static_cast<int>((p.T + p.terms + P::BM - 1) / P::BM), nt = static_cast<int>((p.N + P::BN - 1) / P::BN);
   const int rem = mt * nt - p.full;
   hipLaunchKernelGGL((ring_kernel<P, FORM>), dim3(static_cast<unsigned>(p.full + rem * p.S)), dim3(P::THREADS), 0, s, p, mt,
                      nt, NS);
@@ -1015,7 +1019,7 @@ hipError_t launch_ring_cfg(const RingArgs& p, int NS, hipStream_t s) {
 hipError_t launch_ring(const RingArgs& a, bool nn, hipStream_t s) {
   RingArgs p = a;
   const int NS = static_cast<int>(ring_stages(p));
-  const RingPlan plan = ring_plan(p.T, p.N, NS);
+  const RingPlan plan = p.terms > 0 ? terms_plan(p.N, NS) : ring_plan(p.T, p.N, NS);
   p.full = static_cast<int>(plan.full);
   p.S = plan.S;
   p.ks = plan.ks;
@@ -1069,23 +1073,20 @@ hipError_t launch_gated_few(const GatedFew& a, hipStream_t s) {
 template <int ACT>
 static hipError_t launch_gated_grad_act(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F,
                                         uint16_t* dg, uint16_t* du, const RankProduct* v, hipStream_t s) {
-  if (v == nullptr) {
-    hipLaunchKernelGGL(gated_grad_kernel<ACT>, dim3(blocks_of(T, 16), blocks_of(F, 256)), dim3(256), 0, s, saved, dh, lddh, T,
-                       F, dg, du);
-    return hipGetLastError();
-  }
   int S, per;
   grad_plan(T, F, &S, &per);
-  const dim3 grid(blocks_of(T, 64), static_cast<unsigned>(S)), block(256);
-  const int nb = (v->rank[0] + 15) / 16 + (v->rank[1] + 15) / 16;
-  if (nb == 1) hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 1>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
-  else if (nb == 2) hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 2>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
-  else if (nb == 3) hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 3>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
-  else hipLaunchKernelGGL((gated_grad_rank_kernel<ACT, 4>), grid, block, 0, s, saved, dh, lddh, dg, du, *v, per);
+  const RankProduct p = v != nullptr ? *v : RankProduct{};
+  const unsigned nb = v != nullptr ? static_cast<unsigned>(grad_blocks(p.rank[0], p.rank[1])) : 0;
+  const dim3 grid(blocks_of(T, 64), static_cast<unsigned>(S), nb > 8 ? (nb + 7) / 8 : 1), block(256);
+  if (nb == 0) hipLaunchKernelGGL((gated_grad_kernel<ACT, 0>), grid, block, 0, s, saved, dh, lddh, T, F, dg, du, p, per);
+  else if (nb == 1) hipLaunchKernelGGL((gated_grad_kernel<ACT, 1>), grid, block, 0, s, saved, dh, lddh, T, F, dg, du, p, per);
+  else if (nb == 2) hipLaunchKernelGGL((gated_grad_kernel<ACT, 2>), grid, block, 0, s, saved, dh, lddh, T, F, dg, du, p, per);
+  else if (nb <= 4) hipLaunchKernelGGL((gated_grad_kernel<ACT, 4>), grid, block, 0, s, saved, dh, lddh, T, F, dg, du, p, per);
+  else hipLaunchKernelGGL((gated_grad_kernel<ACT, 8>), grid, block, 0, s, saved, dh, lddh, T, F, dg, du, p, per);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const unsigned blocks = blocks_of(T * (pair_ld(v->rank[0] + v->rank[1]) / 4), 256);
-  hipLaunchKernelGGL(rank_finish_kernel, dim3(blocks), dim3(256), 0, s, *v, S, static_cast<int>(blocks), *v, 0);
+  if (e != hipSuccess || v == nullptr) return e;
+  hipLaunchKernelGGL(grad_rank_finish_kernel, dim3(blocks_of(T * (pair_ld(p.rank[0] + p.rank[1]) / 4), 256)), dim3(256), 0, s,
+                     p, S, T <= kTerms ? kTerms : 0);
   return hipGetLastError();
 }
 
@@ -1107,6 +1108,7 @@ hipError_t launch_contract(const Contract& p, hipStream_t s) {
   int S;
   int64_t chunk;
   contract_plan(p.T, tiles, &S, &chunk);
+  S *= p.halves;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(S));
   if (drop) hipLaunchKernelGGL(contract_kernel<true>, grid, dim3(256), 0, s, p, S, chunk);
   else hipLaunchKernelGGL(contract_kernel<false>, grid, dim3(256), 0, s, p, S, chunk);

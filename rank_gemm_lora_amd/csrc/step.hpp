@@ -19,9 +19,9 @@ inline int64_t pair_ld(int64_t R) { return (2 * R + 63) / 64 * 64; }
 
 // ---------------------------------------------------------------- rank-wide products
 // tt[t] = scale . x[t] . A^T (x masked by drop when given) for up to two adapters side by side, or with `nn`
-// scale . x_i[t] . B_i for B_i [K, rank_i] (the gradient's side: every adapter has its own x).
+// scale . x[t] . B for B [K, rank] (the gradient's side: one adapter).
 struct RankProduct {
-  const uint16_t* x[2]; int64_t ldx;
+  const uint16_t* x; int64_t ldx;
   const uint16_t* A[2];   // [rank, K], or nn: [K, rank]
   int rank[2];            // rank[1] 0: one adapter
   float scale[2];
@@ -36,9 +36,7 @@ struct RankProduct {
 // a wave's steps one after the other take 20 us, and the ring is as fast.)
 constexpr int64_t kRankFewT = 1024, kRankFewK = 8192;
 constexpr int64_t kRankFewR = 64;  // columns of one workgroup: more go to the ring
-inline bool rank_few(int64_t T, int64_t K, int64_t R0, int64_t R1, bool nn) {
-  return T <= kRankFewT && K <= kRankFewK && (nn ? R0 <= kRankFewR && R1 <= kRankFewR : R0 + R1 <= kRankFewR);
-}
+inline bool rank_few(int64_t T, int64_t K, int64_t R) { return T <= kRankFewT && K <= kRankFewK && R <= kRankFewR; }
 // Splits of K, fixed by the sizes: as few rounds of workgroups of 128 tokens, two on each of 256 compute units, as make
 // the least stages of 64 one after the other (3 more for each round's start); a split's sums cost a write and a read.
 // (18871 tokens, 8960 inputs, masked: 3 splits, 444 workgroups one to a unit in two rounds, took 116 us.)
@@ -59,13 +57,11 @@ inline void rank_plan(int64_t T, int64_t K, int64_t tasks, int* S, int* ks) {
     }
   }
 }
-inline int64_t rank_tasks(int64_t R0, int64_t R1, bool nn) {
-  return nn ? (R0 + 127) / 128 + (R1 + 127) / 128 : R0 + R1 <= 64 ? 1 : 2 * ((R0 + R1 + 127) / 128);
-}
-inline size_t rank_part_bytes(int64_t T, int64_t K, int64_t R0, int64_t R1, bool nn) {
+inline int64_t rank_tasks(int64_t R, bool nn) { return nn ? (R + 127) / 128 : R <= 64 ? 1 : 2 * ((R + 127) / 128); }
+inline size_t rank_part_bytes(int64_t T, int64_t K, int64_t R, bool nn) {
   int S, ks;
-  rank_plan(T, K, rank_tasks(R0, R1, nn), &S, &ks);
-  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R0 + R1) * 4;
+  rank_plan(T, K, rank_tasks(R, nn), &S, &ks);
+  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R) * 4;
 }
 // Either or both (null: not there), of the same tokens; each with partial sums of its own.
 hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hipStream_t s);
@@ -83,6 +79,7 @@ struct RingArgs {
   int64_t T, N;
   uint16_t* y; int64_t ldy;
   Drop drop;
+  int terms;      // kTerms: the x_i have second terms (below); tt has zeros there
   float* part;    // partial sums of the split tiles
   int full, S, ks;  // RingPlan
   float* saved;   // gated: where the forward leaves g and u, or null
@@ -129,6 +126,25 @@ inline RingPlan ring_plan(int64_t T, int64_t N, int64_t stages) {
     }
   }
   return best;
+}
+// x of two bf16 terms, for up to 64 tokens: the second terms are 64 rows behind the first and pass as tokens of their own in
+// the same 128-token tile; the joining launch adds the two. (The gated gradients are rounded to bf16 for dx and dB, which
+// brings those 1.4 times the error of their own rounding alone; over few values the ratio strays from that, and for few
+// tokens the second term costs nothing.)
+constexpr int kTerms = 64;
+inline int64_t term_rows(int64_t T) { return T <= kTerms ? kTerms + T : T; }
+inline RingPlan terms_plan(int64_t N, int64_t stages) {  // every tile in parts, two workgroups a unit
+  const int64_t tiles = (N + 127) / 128;
+  int64_t s = 2 * kRingUnits / tiles;
+  s = s > kRingMaxSplits ? kRingMaxSplits : s;
+  s = s > stages / kRingMinStages ? stages / kRingMinStages : s;
+  s = s < 1 ? 1 : s;
+  const int64_t ks = (stages + s - 1) / s;
+  return RingPlan{false, tiles, 0, static_cast<int>((stages + ks - 1) / ks), static_cast<int>(ks)};
+}
+inline size_t terms_part_bytes(int64_t N, int64_t stages) {
+  const RingPlan p = terms_plan(N, stages);
+  return static_cast<size_t>(p.tiles * p.S) * 128 * 128 * 4;
 }
 inline size_t ring_part_bytes(int64_t T, int64_t N, int64_t stages) {
   const RingPlan p = ring_plan(T, N, stages);
@@ -191,11 +207,11 @@ inline int64_t gated_blocks(int64_t n) { return (n + 15) / 16; }
 inline size_t gated_saved_bytes(int64_t T, int64_t F) {
   return static_cast<size_t>(gated_blocks(T)) * static_cast<size_t>(gated_blocks(F)) * 512 * 4;
 }
-// dg = dh . u . act'(g) and du = dh . act(g), bf16 [T, F] each, and with v (its x are dg and du) the rank-wide product of
-// them: up to four blocks of 16 columns, formed from the values as they pass, in S parts of `per` runs of 64 columns
-// (grad_with_ranks; more columns take launch_rank_products). Workgroups of 64 tokens, four to each of 256 units
-// where F and 32 parts allow it.
-inline bool grad_with_ranks(int64_t R0, int64_t R1) { return R0 + R1 > 0 && (R0 + 15) / 16 + (R1 + 15) / 16 <= 4; }
+// dg = dh . u . act'(g) and du = dh . act(g), bf16 [T, F] each (up to 64 tokens two terms of each: [term_rows, F]), and with
+// v (whose x is not used) the rank-wide product of them, dg . B_gate beside du . B_up, formed from the values as they pass
+// before that rounding, in S parts of `per` runs of 64 columns. (From the rounded values the gradients of A had 1.5 times
+// the error of their own rounding.) Workgroups of 64 tokens, four to each of 256 units where F and 32 parts allow it.
+inline int64_t grad_blocks(int64_t R0, int64_t R1) { return (R0 + 15) / 16 + (R1 + 15) / 16; }
 inline void grad_plan(int64_t T, int64_t F, int* S, int* per) {
   const int64_t mt = (T + 63) / 64, runs = (F + 63) / 64;
   int64_t s = (1024 + mt - 1) / mt;
@@ -204,11 +220,10 @@ inline void grad_plan(int64_t T, int64_t F, int* S, int* per) {
   *per = static_cast<int>((runs + s - 1) / s);
   *S = static_cast<int>((runs + *per - 1) / *per);
 }
-inline size_t grad_part_bytes(int64_t T, int64_t F, int64_t R0, int64_t R1) {
-  if (!grad_with_ranks(R0, R1)) return 0;
+inline size_t grad_part_bytes(int64_t T, int64_t F, int64_t R) {
   int S, per;
   grad_plan(T, F, &S, &per);
-  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R0 + R1) * 4;
+  return static_cast<size_t>(S) * static_cast<size_t>(T) * static_cast<size_t>(R) * 4;
 }
 hipError_t launch_gated_grad(const float* saved, const uint16_t* dh, int64_t lddh, int64_t T, int64_t F, int act,
                              uint16_t* dg, uint16_t* du, const RankProduct* v, hipStream_t s);
@@ -224,6 +239,7 @@ struct ContractTask {
   bool transposed, masked;
   void* out[2];     // transposed: rows [0, split) and [split, J); else out[0]
   int split;
+  int terms;        // kTerms: P has second terms that many rows behind the first
 };
 constexpr int kMaxContract = 3;
 struct Contract {
@@ -231,7 +247,8 @@ struct Contract {
   int64_t T;
   Drop drop;        // of the masked tasks' P
   bool out_bf16;
-  float* part;      // [task][S, M, J]
+  int halves;       // 2: some task has second terms (the others have none of its half of the parts)
+  float* part;      // [task][halves S, M, J]
 };
 constexpr int kCtI = 256, kCtJ = 64, kCtT = 32;
 inline int64_t contract_tiles(int64_t M, int64_t J) { return (M + kCtI - 1) / kCtI * ((J + kCtJ - 1) / kCtJ); }

@@ -118,11 +118,11 @@ DropLayout drop_layout(int64_t T, int64_t K, int64_t N, int64_t R, bool backward
   Take take;
   L.tt = take(tt_bytes(T, R));
   // (an inactive adapter has no extension: fewer stages, other parts)
-  size_t part = std::max(lora::rank_part_bytes(T, K, R, 0, false),
+  size_t part = std::max(lora::rank_part_bytes(T, K, R, false),
                          std::max(lora::ring_part_bytes(T, N, stages(K, 0, R)), lora::ring_part_bytes(T, N, stages(K, 0, 0))));
   if (backward) {
     L.ut = take(tt_bytes(T, R));
-    L.part2 = take(lora::rank_part_bytes(T, N, R, 0, true));
+    L.part2 = take(lora::rank_part_bytes(T, N, R, true));
     part = std::max(part, std::max(lora::ring_part_bytes(T, K, stages(N, 0, R)), lora::ring_part_bytes(T, K, stages(N, 0, 0))));
     const int64_t ta = lora::contract_tiles(K, R), tb = lora::contract_tiles(N, R);
     part = std::max(part, std::max(lora::contract_part_bytes(T, ta, K * R), lora::contract_part_bytes(T, tb, N * R)));
@@ -190,7 +190,7 @@ int lora_linear_dropout_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
   if (a.rank > 0) {
     RankProduct r;
     std::memset(&r, 0, sizeof(r));
-    r.x[0] = bf(x); r.ldx = ldx; r.A[0] = bf(A); r.rank[0] = rank; r.scale[0] = a.scale; r.T = T; r.K = K; r.drop = drop;
+    r.x = bf(x); r.ldx = ldx; r.A[0] = bf(A); r.rank[0] = rank; r.scale[0] = a.scale; r.T = T; r.K = K; r.drop = drop;
     r.part = reinterpret_cast<float*>(ws + L.part);
     r.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
     if (lora::launch_rank_products(&r, nullptr, st) != hipSuccess) return LORA_ERR_HIP;
@@ -246,9 +246,9 @@ int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
   u.rank[0] = rank; u.scale[0] = a.scale; u.T = T;
   RankProduct t = u;
   // u = s dy B, and t = s x' A^T as the forward forms it
-  u.x[0] = bf(dy); u.ldx = lddy; u.A[0] = bf(B); u.K = N; u.part = reinterpret_cast<float*>(ws + L.part2);
+  u.x = bf(dy); u.ldx = lddy; u.A[0] = bf(B); u.K = N; u.part = reinterpret_cast<float*>(ws + L.part2);
   u.tt = reinterpret_cast<uint16_t*>(ws + L.ut);
-  t.x[0] = bf(x); t.ldx = ldx; t.A[0] = bf(A); t.K = K; t.drop = drop; t.part = part;
+  t.x = bf(x); t.ldx = ldx; t.A[0] = bf(A); t.K = K; t.drop = drop; t.part = part;
   t.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
   const bool need_u = a.rank > 0 && (dx != nullptr || dA != nullptr), need_t = a.rank > 0 && dB != nullptr;
   if ((need_u || need_t) &&
@@ -268,11 +268,11 @@ int lora_linear_dropout_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, co
   if (a.rank == 0 || (dA == nullptr && dB == nullptr)) return LORA_OK;
   Contract c;
   std::memset(&c, 0, sizeof(c));
-  c.T = T; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part; c.drop = drop;
+  c.T = T; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part; c.drop = drop; c.halves = 1;
   if (dA != nullptr)  // u^T x'
-    c.task[c.n_tasks++] = lora::ContractTask{bf(x), ldx, K, u.tt, ldt, rank, 0, rank, true, true, {dA, nullptr}, rank};
+    c.task[c.n_tasks++] = lora::ContractTask{bf(x), ldx, K, u.tt, ldt, rank, 0, rank, true, true, {dA, nullptr}, rank, 0};
   if (dB != nullptr)  // dy^T t
-    c.task[c.n_tasks++] = lora::ContractTask{bf(dy), lddy, N, t.tt, ldt, rank, 0, rank, false, false, {dB, nullptr}, rank};
+    c.task[c.n_tasks++] = lora::ContractTask{bf(dy), lddy, N, t.tt, ldt, rank, 0, rank, false, false, {dB, nullptr}, rank, 0};
   return lora::launch_contract(c, st) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
@@ -288,7 +288,7 @@ struct GatedLayout {
 
 // (partial sums of the rank-wide product, then of the GEMM's cut tiles)
 size_t gated_fwd_part(int64_t T, int64_t K, int64_t F, int64_t R) {
-  return std::max(R > 0 ? lora::rank_part_bytes(T, K, R, 0, false) : 0, lora::ring_part_bytes(T, 2 * F, stages(K, 0, R)));
+  return std::max(R > 0 ? lora::rank_part_bytes(T, K, R, false) : 0, lora::ring_part_bytes(T, 2 * F, stages(K, 0, R)));
 }
 
 GatedLayout gated_fwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_t ru) {
@@ -314,20 +314,23 @@ GatedLayout gated_bwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_
   GatedLayout L;
   Take take;
   const int64_t R = rg + ru;
-  L.dg = take(static_cast<size_t>(T) * F * 2);
-  L.du = take(static_cast<size_t>(T) * F * 2);
-  L.vt = take(tt_bytes(T, R));
+  const int64_t rows = lora::term_rows(T);
+  L.dg = take(static_cast<size_t>(rows) * F * 2);
+  L.du = take(static_cast<size_t>(rows) * F * 2);
+  L.vt = take(tt_bytes(rows, R));
   size_t part = gated_fwd_layout(T, K, F, rg, ru).total;
   for (int i = 0; i < 4; ++i) {  // both adapters, or either of them inactive
     const int64_t a = i & 1 ? 0 : rg, b = i & 2 ? 0 : ru;
     if (a + b > 0) {
-      part = std::max(part, lora::rank_part_bytes(T, F, a, b, true));
-      part = std::max(part, lora::grad_part_bytes(T, F, a, b));
+      part = std::max(part, lora::grad_part_bytes(T, F, a + b));
+      const size_t halves = T <= lora::kTerms ? 2 : 1;
       const int64_t ta = lora::contract_tiles(K, a + b), tb = lora::contract_tiles(F, a) + lora::contract_tiles(F, b);
-      part = std::max(part, std::max(lora::contract_part_bytes(T, ta, K * (a + b)), lora::contract_part_bytes(T, tb, F * (a + b))));
-      part = std::max(part, lora::contract_part_bytes(T, ta + tb, (K + F) * (a + b)));
+      part = std::max(part, lora::contract_part_bytes(T, ta, K * (a + b)));
+      part = std::max(part, halves * lora::contract_part_bytes(T, tb, F * (a + b)));
+      part = std::max(part, halves * lora::contract_part_bytes(T, ta + tb, (K + F) * (a + b)));
     }
-    part = std::max(part, lora::ring_part_bytes(T, K, stages(F, F, a + b)));
+    const int64_t ns = stages(F, F, a + b);
+    part = std::max(part, T <= lora::kTerms ? lora::terms_part_bytes(K, ns) : lora::ring_part_bytes(T, K, ns));
   }
   L.part = take(part);
   L.saved = take(saved_bytes(T, F, R));  // (last: not used where the forward's is given)
@@ -380,7 +383,7 @@ hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const
   if (R > 0) {
     RankProduct r;
     std::memset(&r, 0, sizeof(r));
-    r.x[0] = bf(x); r.ldx = ldx; r.T = T; r.K = K; r.part = part; r.tt = tt;
+    r.x = bf(x); r.ldx = ldx; r.T = T; r.K = K; r.part = part; r.tt = tt;
     for (int i = 0; i < 2; ++i) {
       r.A[i] = bf(s[i].A); r.rank[i] = static_cast<int>(s[i].rank); r.scale[i] = s[i].scale;
       g.E[i] = bf(s[i].B); g.re[i] = static_cast<int>(s[i].rank);
@@ -495,17 +498,16 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
   const int64_t R = s[0].rank + s[1].rank, ldt = lora::pair_ld(R);
   auto* vt = reinterpret_cast<uint16_t*>(ws + L.vt);
   const bool want_a = dA_gate != nullptr || dA_up != nullptr, want_b = dB_gate != nullptr || dB_up != nullptr;
-  const bool need_v = R > 0 && (dx != nullptr || want_a), joint = need_v && lora::grad_with_ranks(s[0].rank, s[1].rank);
   RankProduct v;  // v = s d B of each projection
   std::memset(&v, 0, sizeof(v));
-  v.x[0] = dg; v.x[1] = du; v.ldx = F; v.T = T; v.K = F; v.part = part; v.tt = vt;
+  v.T = T; v.K = F; v.part = part; v.tt = vt;
   for (int i = 0; i < 2; ++i) {
     v.A[i] = bf(s[i].B); v.rank[i] = static_cast<int>(s[i].rank); v.scale[i] = s[i].scale;
   }
   if (lora::launch_gated_grad(reinterpret_cast<const float*>(keep), bf(dh), lddh, T, F, act, dg, du,
-                              joint ? &v : nullptr, st) != hipSuccess)
+                              R > 0 && (dx != nullptr || want_a) ? &v : nullptr, st) != hipSuccess)
     return LORA_ERR_HIP;
-  if (need_v && !joint && lora::launch_rank_products(nullptr, &v, st) != hipSuccess) return LORA_ERR_HIP;
+  const int terms = T <= lora::kTerms ? lora::kTerms : 0;
   if (dx != nullptr) {
     RingArgs g;
     std::memset(&g, 0, sizeof(g));
@@ -516,23 +518,23 @@ int lora_gated_bwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_
       }
     }
     g.x[0] = dg; g.x[1] = du; g.ldx = F; g.W[0] = bf(layer->W_gate); g.W[1] = bf(layer->W_up); g.K[0] = g.K[1] = F;
-    g.n_seg = 2; g.T = T; g.N = K; g.y = bf(dx); g.ldy = lddx; g.part = part;
+    g.n_seg = 2; g.T = T; g.N = K; g.y = bf(dx); g.ldy = lddx; g.part = part; g.terms = terms;
     if (lora::launch_ring(g, true, st) != hipSuccess) return LORA_ERR_HIP;
   }
   if (R == 0) return LORA_OK;
   if (!want_a && !want_b) return LORA_OK;
   Contract c;
   std::memset(&c, 0, sizeof(c));
-  c.T = T; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part;
+  c.T = T; c.out_bf16 = grad_dtype == LORA_BF16; c.part = part; c.halves = want_b && terms > 0 ? 2 : 1;
   const int r0 = static_cast<int>(s[0].rank), r1 = static_cast<int>(s[1].rank), rr = r0 + r1;
   if (want_a)  // v^T x, both projections' rows in one pass over x
     c.task[c.n_tasks++] = lora::ContractTask{bf(x), ldx, K, vt, ldt, rr, 0, rr, true, false,
-                                             {r0 > 0 ? dA_gate : nullptr, r1 > 0 ? dA_up : nullptr}, r0};
+                                             {r0 > 0 ? dA_gate : nullptr, r1 > 0 ? dA_up : nullptr}, r0, 0};
   const auto* tt = reinterpret_cast<const uint16_t*>(keep + saved_tt_at(T, F));
   if (want_b && r0 > 0)  // d^T t of each projection
-    c.task[c.n_tasks++] = lora::ContractTask{dg, F, F, tt, ldt, rr, 0, r0, false, false, {dB_gate, nullptr}, r0};
+    c.task[c.n_tasks++] = lora::ContractTask{dg, F, F, tt, ldt, rr, 0, r0, false, false, {dB_gate, nullptr}, r0, terms};
   if (want_b && r1 > 0)
-    c.task[c.n_tasks++] = lora::ContractTask{du, F, F, tt, ldt, rr, r0, r1, false, false, {dB_up, nullptr}, r1};
+    c.task[c.n_tasks++] = lora::ContractTask{du, F, F, tt, ldt, rr, r0, r1, false, false, {dB_up, nullptr}, r1, terms};
   return lora::launch_contract(c, st) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 

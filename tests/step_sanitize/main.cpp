@@ -58,15 +58,11 @@ hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hi
     const RankProduct* p = i ? nn : nt;
     if (p == nullptr) continue;
     const int64_t R = p->rank[0] + p->rank[1];
-    if (R < 8) fail("rank");
+    if (R < 8 || (i && p->rank[1] != 0)) fail("rank");
     for (int s = 0; s < 2; ++s)
-      if (p->rank[s] > 0 && (p->A[s] == nullptr || (i && p->x[s] == nullptr))) fail("an adapter that is not there");
-    if (i) {
-      for (int s = 0; s < 2; ++s)
-        if (p->rank[s] > 0) reads(p->x[s], rows(p->T, p->ldx, 2), "x of the gradient's product");
-    }
+      if (p->rank[s] > 0 && p->A[s] == nullptr) fail("an adapter that is not there");
     // (the partial sums of both are in use together, and the results)
-    writes(p->part, rank_part_bytes(p->T, p->K, p->rank[0], p->rank[1], i == 1), "partial sums", true);
+    writes(p->part, rank_part_bytes(p->T, p->K, R, i == 1), "partial sums", true);
     writes(p->tt, rows(p->T, pair_ld(R), 2), "rank-wide rows", true);
   }
   std::vector<std::pair<uintptr_t, uintptr_t>> stay(live.begin(), live.begin() + mark);
@@ -79,15 +75,18 @@ hipError_t launch_rank_products(const RankProduct* nt, const RankProduct* nn, hi
 
 static void check_ring(const RingArgs& p, int64_t columns) {
   ++launches;
-  if (p.tt != nullptr) reads(p.tt, rows(p.T, p.ldt, 2), "rank-wide rows of a GEMM");
+  if (p.tt != nullptr) reads(p.tt, rows(p.T + p.terms, p.ldt, 2), "rank-wide rows of a GEMM");
   if (p.tt != nullptr && p.ldt != pair_ld(p.re[0] + p.re[1])) fail("their stride");
-  writes(p.part, ring_part_bytes(p.T, columns, ring_stages(p)), "parts of tiles", false);
-  const RingPlan r = ring_plan(p.T, columns, ring_stages(p));
+  if (p.terms != 0 && (p.terms != kTerms || p.T > kTerms || p.n_seg != 2)) fail("second terms");
+  writes(p.part, p.terms ? terms_part_bytes(columns, ring_stages(p)) : ring_part_bytes(p.T, columns, ring_stages(p)),
+         "parts of tiles", false);
+  const RingPlan r = p.terms ? terms_plan(columns, ring_stages(p)) : ring_plan(p.T, columns, ring_stages(p));
+  if (r.S < 1 || static_cast<int64_t>(r.S - 1) * r.ks >= ring_stages(p)) fail("parts of a plan");
   if (r.full < 0 || r.full > r.tiles || static_cast<int64_t>(r.S) * r.ks < ring_stages(p)) fail("plan");
 }
 hipError_t launch_ring(const RingArgs& p, bool, hipStream_t) {
   for (int i = 0; i < p.n_seg; ++i)
-    if (p.n_seg == 2) reads(p.x[i], rows(p.T, p.ldx, 2), "segments");
+    if (p.n_seg == 2) reads(p.x[i], rows(p.T + p.terms, p.ldx, 2), "segments");
   check_ring(p, p.N);
   return hipSuccess;
 }
@@ -106,16 +105,17 @@ hipError_t launch_gated_grad(const float* saved, const uint16_t*, int64_t, int64
                              uint16_t* du, const RankProduct* v, hipStream_t) {
   ++launches;
   reads(saved, gated_saved_bytes(T, F), "kept by the forward");
-  writes(dg, rows(T, F, 2), "dg", true);
-  writes(du, rows(T, F, 2), "du", true);
+  writes(dg, rows(term_rows(T), F, 2), "dg", true);
+  writes(du, rows(term_rows(T), F, 2), "du", true);
+  int S, per;
+  grad_plan(T, F, &S, &per);
+  if (S < 1 || S > 32 || static_cast<int64_t>(S - 1) * per >= (F + 63) / 64 || static_cast<int64_t>(S) * per < (F + 63) / 64)
+    fail("plan of the gradient");
   if (v != nullptr) {
-    if (!grad_with_ranks(v->rank[0], v->rank[1]) || v->x[0] != dg || v->x[1] != du || v->T != T || v->K != F) fail("product");
-    int S, per;
-    grad_plan(T, F, &S, &per);
-    if (S < 1 || S > 32 || static_cast<int64_t>(S - 1) * per >= (F + 63) / 64 || static_cast<int64_t>(S) * per < (F + 63) / 64)
-      fail("plan of the product");
-    writes(v->part, grad_part_bytes(T, F, v->rank[0], v->rank[1]), "its partial sums", false);
-    writes(v->tt, rows(T, pair_ld(v->rank[0] + v->rank[1]), 2), "its rows", true);
+    const int64_t R = v->rank[0] + v->rank[1];
+    if (R < 8 || v->T != T || v->K != F) fail("product");
+    writes(v->part, grad_part_bytes(T, F, R), "its partial sums", false);
+    writes(v->tt, rows(term_rows(T), pair_ld(R), 2), "its rows", true);
   }
   return hipSuccess;
 }
@@ -127,11 +127,13 @@ hipError_t launch_contract(const Contract& p, hipStream_t) {
     tiles += contract_tiles(k.M, k.J);
     elements += k.M * k.J;
     reads(k.tt, rows(p.T, k.ldt, 2), "rank-wide rows of a contraction");
-    reads(k.P, rows(p.T - 1, k.ldp, 2) + k.M * 2, "the other side of a contraction");
+    reads(k.P, rows(p.T + k.terms - 1, k.ldp, 2) + k.M * 2, "the other side of a contraction");
+    if (k.terms != 0 && p.halves != 2) fail("halves of a contraction");
     if (k.q_col + k.J > k.R || 2 * k.R > k.ldt || k.M % 8 != 0 || k.J % 8 != 0) fail("columns of a contraction");
   }
   if (p.n_tasks < 1 || p.n_tasks > kMaxContract) fail("tasks");
-  writes(p.part, contract_part_bytes(p.T, tiles, elements), "sums of a contraction", false);
+  if (p.halves < 1 || p.halves > 2) fail("halves");
+  writes(p.part, p.halves * contract_part_bytes(p.T, tiles, elements), "sums of a contraction", false);
   return hipSuccess;
 }
 hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t) {
