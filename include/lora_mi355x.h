@@ -588,6 +588,8 @@ int lora_adamw_step(const lora_adamw_plan_t* plan, double lr, double beta1, doub
  *   rng     NULL, or DEVICE {seed, offset} (8-byte aligned), read by the kernels in place of the two
  *           arguments, so that a captured call draws anew where the caller advances the offset
  *   A, B    required; other arguments as lora_linear_fwd / lora_linear_bwd (dx, dA, dB optional)
+ * A dropped element counts as zero whatever it holds. The rank, K and ldx are multiples of 8, in the backward
+ * call N and lddy too. LORA_ERR_UNSUPPORTED from 2^21 tokens or T max(K, N) = 2^35 on.
  */
 int lora_linear_dropout_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const void* W, int64_t N,
                             const void* bias, const void* A, const void* B, int32_t rank, double alpha,
@@ -628,14 +630,16 @@ typedef struct lora_gated_layer {
  *
  * lora_gated_bwd -- for an output gradient dh:
  *
- *     dg = RN_bf16(dh . u . act'(g)),  du = RN_bf16(dh . act(g)),  v = s . d.B of each,
+ *     dg = dh . u . act'(g),  du = dh . act(g), rounded to bf16,  v = s . d.B of each,
  *     dx = dg.W_gate + du.W_up + v_gate.A_gate + v_up.A_up,  dA = v^T.x,  dB = d^T.(s x.A^T)
  *
  *   saved   as a forward call with the same x, layer and scales filled it, or NULL: the
  *           forward GEMM runs once more (and the workspace holds what it keeps)
  *   dx, dA_*, dB_*  each optional (NULL = not computed)
- * dg and du are rounded to bf16 for the products that follow: the gradients are off by
- * those roundings whatever grad_dtype is.
+ * v is formed from dg and du before that rounding (as two bf16 terms), and up to 64 tokens so are dx and
+ * dB; above, dx and dB are off by it whatever grad_dtype is.
+ * Ranks, K and ldx are multiples of 8, in the backward call F and lddh too; x, the weights, A and B 16-byte
+ * aligned, dh as well. LORA_ERR_UNSUPPORTED from 2^21 tokens or T max(K, F) = 2^35 on.
  */
 int lora_gated_fwd(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* layer, int64_t F,
                    int32_t act, double strength, double request_scale, void* h, int64_t ldh, void* saved,
@@ -667,7 +671,7 @@ size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t ra
  *           tokens that have one, for their mean), or NULL (1)
  *   loss, lse [T] fp32, dh [T, K] bf16 (row stride lddh): each optional (NULL = not computed)
  *   workspace at least lora_cross_entropy_workspace_size(T, K, V, dh != NULL) bytes
- * A token whose logits are not all finite has a loss, lse and gradient that are not either; no other
+ * A token with an infinite or NaN logit has a loss, lse and gradient that need not be finite; no other
  * token's change. The same call gives the same bits. LORA_ERR_UNSUPPORTED from 2^21 tokens, 2^37 logits
  * or 2^34 elements of h on.
  */

@@ -25,7 +25,8 @@ using namespace pipe;
 // Rank-wide product over rows contiguous along the contraction (the forward's): 128 tokens and BN adapter rows per
 // workgroup through the LDS ring of the one-adapter producer, K in splits; fp32 partial sums. HBM-bound: x is read once
 // (R <= 128). Two workgroups on a compute unit, so that the generator's arithmetic in one (as long as the reads) does not
-// keep the other's copies waiting.
+// keep the other's copies waiting. 18871 tokens, 8960 inputs, rank 64, masked: 94 us, x at 3.6 TB/s (one workgroup a unit:
+// 116); 12288 tokens, 4096 inputs, two of rank 32, unmasked: 24 us, 4.2 TB/s.
 using RankNarrow = PCfg<128, 64, 32, 64, 128, 3>;   // up to 64 columns
 using RankWide = PCfg<128, 128, 32, 128, 128, 4>;
 
@@ -350,7 +351,10 @@ struct DropNnOp : NnOp<P, 1, 1> {
 
 enum { kFormNt = 0, kFormNn = 1, kFormNn2 = 2, kFormNnDrop = 3 };  // (Nn2: two segments, two adapters)
 
-// One layer: a workgroup per whole tile, then one per part of the others.
+// One layer: a workgroup per whole tile, then one per part of the others. Bound by the matrix pipes and the power they may
+// draw. NT, 18871 tokens, 8960 -> 1536: 464 us, 1.12 PFLOP/s (444 tiles of 256 units: the last round is cut); NN, the gated
+// dx of 4352 tokens, two times 14336 -> 4096: 901 us, 1.13; NN masked, dx of 18871 tokens, 1536 -> 8960: 651 us, of which
+// the masks are 66.
 template <class P, int FORM>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void ring_kernel(RingArgs p, int mt, int nt, int NS) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
@@ -513,7 +517,11 @@ __device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][NJ], const
               static_cast<int>(min<int64_t>(P::WN / 2, p.N - n0)));
 }
 
-// BN / 2 outputs per tile: gate and up blocks of 16 rows in turn.
+// BN / 2 outputs per tile: gate and up blocks of 16 rows in turn, so that a lane has g and u of the same outputs and the
+// activation needs no exchange. Bound by the matrix pipes: 12288 tokens, 4096 -> 14336: 2.15 ms, 1.34 PFLOP/s; pipes 68% busy
+// at 1.8 GHz. A tile's start and epilogue are 15 of its 115 us (ring filling 4, activation and stores 10); a stage takes 1.5,
+// 1.1 of it MFMAs. All operands from L2 made it 4% faster; what a stage computes for the next, spread between its MFMAs
+// instead of before them, 1% slower.
 template <class P, int ACT>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void gated_kernel(RingArgs p, int mt, int nt, int NS) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
@@ -542,7 +550,8 @@ __global__ __launch_bounds__(P::THREADS) void gated_join_kernel(RingArgs p, int 
   gated_store<P, ACT, 1>(acc, p, m0, n0, smem);
 }
 
-// Few tokens: grid (128-row tiles of gate, up, A_gate, A_up, one behind the other; parts of the contraction).
+// Few tokens: grid (128-row tiles of gate, up, A_gate, A_up, one behind the other; parts of the contraction). Bound by
+// reading the weights: 48 tokens, 4096 -> 14336: 58 us from memory (42 where the Infinity Cache holds a part), 235 MB.
 __global__ __launch_bounds__(Ring128::THREADS, Ring128::OCC) void gated_few_kernel(GatedFew p) {
   using P = Ring128;
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];
@@ -785,7 +794,8 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const float* __restrict
 // Token contraction: 256 rows of P^T x 64 columns of Q per workgroup, 32 tokens per stage, a ring of three stages
 // [32 t][256] of P and [32 t][64 first terms | 64 second terms] of Q, both read with the transposing LDS read, two
 // workgroups on a compute unit. Token chunks over grid y leave fp32 partial sums that contract_reduce_kernel adds in
-// order. HBM-bound: P is read once (and, masked, the generator's arithmetic takes about as long).
+// order. HBM-bound: P is read once (and, masked, the generator's arithmetic takes about as long): 285 MB of x, dg and du
+// (4352 tokens, 4096 -> 14336) in 58 us, 4.9 TB/s; 396 MB of x and dy (18871 tokens, 8960 -> 1536) in 85, masked 130.
 constexpr int kCtP = kCtT * kCtI * 2, kCtQ = kCtT * 2 * kCtJ * 2, kCtStage = kCtP + kCtQ;
 
 __device__ __forceinline__ bf16x8 tr_frag(const char* at, int row4) {

@@ -39,7 +39,7 @@ constexpr int64_t kRankFewR = 64;  // columns of one workgroup: more go to the r
 inline bool rank_few(int64_t T, int64_t K, int64_t R) { return T <= kRankFewT && K <= kRankFewK && R <= kRankFewR; }
 // Splits of K, fixed by the sizes: as few rounds of workgroups of 128 tokens, two on each of 256 compute units, as make
 // the least stages of 64 one after the other (3 more for each round's start); a split's sums cost a write and a read.
-// (18871 tokens, 8960 inputs, masked: 3 splits, 444 workgroups one to a unit in two rounds, took 116 us.)
+// (18871 tokens, 8960 inputs, masked: 94 us; 3 splits, 444 workgroups one to a unit in two rounds, took 116.)
 constexpr int kRankMaxSplits = 16;
 inline void rank_plan(int64_t T, int64_t K, int64_t tasks, int* S, int* ks) {
   const int64_t mt = (T + 127) / 128 * tasks, nk = (K + 63) / 64;
@@ -95,7 +95,7 @@ inline int64_t ring_stages(const RingArgs& p) {
 // joins. Chosen by an estimate of the time in microseconds (256 units; measured on MI355X: a stage of 64 indices takes a
 // 256 x 256 tile 1.7, two 128 x 128 tiles side by side 1.0; filling the ring and the epilogue take 8 and 5; the second
 // launch 6, and a sum is written and read at 4 TB/s). 4352 tokens, dx of 4096 -> 14336 in two segments: 272 tiles are one
-// round and 16 tiles; whole, 1222 us (in 128 x 128 tiles); the 16 cut into 16 parts each, 880.
+// round and 16 tiles; whole, 1222 us (in 128 x 128 tiles); the 16 cut into 16 parts each, 901 and 15 for the joining.
 struct RingPlan {
   bool big;
   int64_t tiles;
@@ -175,7 +175,7 @@ inline int64_t few_cols(int64_t F) { return (F + 3) / 4 * 4; }
 inline int64_t few_ld(int64_t F, int64_t R) { return 2 * few_cols(F) + R; }
 // Parts of the contraction: the weights at 5.2 TB/s, or a workgroup's stages one after the other (0.45 us each and 4 for
 // the ring's start), whichever takes longer, and the sums written and read. (One token, 1536 -> 8960: 17.7 us whole, 140
-// workgroups with a long way each, against 12.)
+// workgroups with a long way each, against 13.7. 48 tokens, 4096 -> 14336, were 68 us in 1 to 4 parts alike.)
 inline void few_plan(int64_t T, int64_t K, int64_t F, int64_t R, int* S, int* ks) {
   const int64_t nk = (K + 63) / 64;
   const double read = 4.0 * static_cast<double>(F) * static_cast<double>(K) / 5.2e6;
