@@ -30,13 +30,16 @@ struct RankProduct {
   float* part;            // [S, T, R]
   uint16_t* tt;           // [T, pair_ld(R)]
 };
-// Few tokens (up to 1024, where 16 at a time leave no compute unit with two workgroups' work) and a K of up to 16 steps of
-// 32 for each of 16 waves: the product in one launch, without partial sums in memory. (333 tokens, rank 16, 1536 inputs:
-// 9 us with both of the backward's products, against 7.3 and 4.4 for the ring and its finishing launch. With 8960 inputs
-// a wave's steps one after the other take 20 us, and the ring is as fast.)
-constexpr int64_t kRankFewT = 1024, kRankFewK = 8192;
-constexpr int64_t kRankFewR = 64;  // columns of one workgroup: more go to the ring
-inline bool rank_few(int64_t T, int64_t K, int64_t R) { return T <= kRankFewT && K <= kRankFewK && R <= kRankFewR; }
+// Few tokens and ranks, and a K of up to 16 steps of 32 for each of 16 waves: the product in one launch, without partial sums
+// in memory, every 16 tokens reading all of A. Up to 65536 elements of the result and 4096 tokens. Whole dropout steps, this
+// against the ring and its finishing launch, rank 16: 333 tokens 1536 -> 1536 59 against 66 us, 2500 tokens 75 against 82,
+// 4000 tokens 4096 -> 4096 279 against 285 (1500 tokens 8192 -> 1536: 164 against 159); rank 64: 600 tokens 8192 -> 8192 341
+// against 344, 2000 tokens 1536 -> 1536 95 against 87, 4000 130 against 120. With 8960 inputs the ring is as fast.
+constexpr int64_t kRankFewT = 4096, kRankFewK = 8192, kRankFewElements = 65536;
+constexpr int64_t kRankFewR = 64;  // columns of one workgroup
+inline bool rank_few(int64_t T, int64_t K, int64_t R) {
+  return T <= kRankFewT && K <= kRankFewK && R <= kRankFewR && T * R <= kRankFewElements;
+}
 // Splits of K, fixed by the sizes: as few rounds of workgroups of 128 tokens, two on each of 256 compute units, as make
 // the least stages of 64 one after the other (3 more for each round's start); a split's sums cost a write and a read.
 // (18871 tokens, 8960 inputs, masked: 94 us; 3 splits, 444 workgroups one to a unit in two rounds, took 116.)
@@ -170,7 +173,13 @@ struct GatedFew {
   float* part;     // [S, T, few_ld]
   int S, ks;
 };
-constexpr int64_t kGatedFewT = 64;
+// Up to 64 tokens, and up to 128 (one tile) where the weights are long: whole calls, this against the other way, 4096 ->
+// 14336: 1 token 66 against 86 us, 64 tokens 72 against 88, 65 71 against 88, 128 79 against 90; 1536 -> 8960: 1 token 21
+// against 28, 64 tokens 26 against 30, 65 27 against 29, 100 32 against 30.
+constexpr int64_t kGatedFewT = 64, kGatedFewLongT = 128, kGatedFewLong = int64_t(1) << 25;
+inline bool gated_few(int64_t T, int64_t K, int64_t F) {
+  return T <= kGatedFewT || (T <= kGatedFewLongT && K * F >= kGatedFewLong);
+}
 inline int64_t few_cols(int64_t F) { return (F + 3) / 4 * 4; }
 inline int64_t few_ld(int64_t F, int64_t R) { return 2 * few_cols(F) + R; }
 // Parts of the contraction: the weights at 5.2 TB/s, or a workgroup's stages one after the other (0.45 us each and 4 for

@@ -299,7 +299,7 @@ GatedLayout gated_fwd_layout(int64_t T, int64_t K, int64_t F, int64_t rg, int64_
   for (int i = 0; i < 4; ++i) {  // both adapters, or either of them inactive
     const int64_t R = (i & 1 ? 0 : rg) + (i & 2 ? 0 : ru);
     part = std::max(part, gated_fwd_part(T, K, F, R));
-    if (T <= lora::kGatedFewT) part = std::max(part, lora::few_part_bytes(T, K, F, R));
+    if (lora::gated_few(T, K, F)) part = std::max(part, lora::few_part_bytes(T, K, F, R));
   }
   L.part = take(part);
   L.total = take.off;
@@ -367,7 +367,7 @@ void gated_spans(const lora_gated_layer* l, int64_t K, int64_t F, const Side (&s
 hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* l, const Side (&s)[2],
                          int64_t F, int32_t act, void* h, int64_t ldh, float* saved, uint16_t* tt, float* part,
                          hipStream_t st) {
-  if (T <= lora::kGatedFewT && saved == nullptr) {
+  if (saved == nullptr && lora::gated_few(T, K, F)) {
     lora::GatedFew f;
     std::memset(&f, 0, sizeof(f));
     f.x = bf(x); f.ldx = ldx; f.W[0] = bf(l->W_gate); f.W[1] = bf(l->W_up); f.bias[0] = bf(l->b_gate);

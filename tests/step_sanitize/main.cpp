@@ -97,7 +97,7 @@ hipError_t launch_gated(const RingArgs& p, hipStream_t) {
 }
 hipError_t launch_gated_few(const GatedFew& p, hipStream_t) {
   ++launches;
-  if (p.T > kGatedFewT) fail("few tokens");
+  if (p.T > 128 || !gated_few(p.T, p.K, p.F)) fail("few tokens");
   writes(p.part, few_part_bytes(p.T, p.K, p.F, p.rank[0] + p.rank[1]), "sums of few tokens", false);
   return hipSuccess;
 }

@@ -86,7 +86,8 @@ def test_activations_far_out_have_their_limits(act):
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,N,R", [
     (1024, 520, 264, 64), (1025, 520, 264, 64), (40, 8192, 8192, 16), (40, 8200, 64, 16), (40, 64, 8200, 16),
-    (40, 520, 136, 72), (30, 264, 136, 1024), (130, 136, 264, 512),
+    (40, 520, 136, 72), (30, 264, 136, 1024), (130, 136, 264, 512), (4096, 264, 136, 16), (4097, 264, 136, 16), (2730, 136, 264, 24),
+    (2731, 136, 264, 24),
 ])
 def test_dropout_on_both_sides_of_the_choices(T, K, N, R):
     say("dropout choices", T, K, N, R)
@@ -108,6 +109,15 @@ def test_gated_on_both_sides_of_the_choices(T, K, F, rg_, ru):
     for save in (True, False):
         for k, t in ts.run_gated(c, "silu", torch.float32, save).items():
             sr.check(t, want[k], BF if k in ("h", "dx") else torch.float32, f"{save} {k}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,F", [(64, 8192), (65, 8192), (128, 8192), (129, 8192), (100, 8185), (128, 8200)])
+def test_gated_forward_with_long_weights(T, F):
+    """65 to 128 tokens where the weights are long (from 2^25 elements on), and beside it."""
+    say("gated long", T, F)
+    c = ts.gated_case(T, 4096, F, 16, 8, 39)
+    sr.check(ts.run_gated(c, "silu", backward=False, save=False)["h"], ts.want_gated(c, "silu", backward=False)["h"], BF, "h")
 
 
 @pytest.mark.gpu
