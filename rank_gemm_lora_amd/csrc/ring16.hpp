@@ -34,9 +34,12 @@ using Ring128 = QCfg<128, 128, 64, 64, 128, 5, 2>;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// A chunk that does not exist gets this added to its offset: past every resource (at most 2^30 bytes: 256 rows of 4 MB),
+// A chunk that does not exist gets this added to its offset: past a tile's resource (at most 2^30 bytes: 256 rows of 4 MB),
 // with no wrap around behind it.
 constexpr uint32_t kMissing = 0x40000000u;
+// A row that does not exist of a resource of up to 2^31 bytes (all rows of an adapter: 1024 of 2 MB). The columns that do
+// not exist keep kMissing and may lie inside such a resource: what they read reaches outputs that do not exist.
+constexpr uint32_t kMissingRow = 0x80000000u;
 
 template <class P>
 constexpr int ring_loads() { return P::BM * P::CPR / 64 / P::WAVES; }

@@ -141,7 +141,7 @@ struct NnOp {
       for (int l = 0; l < ring_loads<P>(); ++l) {  // (groups of eight rows: ranks are multiples of 8)
         const int gr = s * 8 + NnRows<P>::group(l), ph = gr < per / 8 ? gr : gr - per / 8;
         const bool is2 = NEXT > 1 && ph >= re0 / 8;
-        first[NEXT > 0 ? l : 0] = gr < per / 4 ? static_cast<uint32_t>(is2 ? ph - re0 / 8 : ph) * 8u * ldw_b : kMissing;
+        first[NEXT > 0 ? l : 0] = gr < per / 4 ? static_cast<uint32_t>(is2 ? ph - re0 / 8 : ph) * 8u * ldw_b : kMissingRow;
         if (NEXT > 1) second |= static_cast<uint32_t>(is2 ? 1 : 0) << l;
       }
     } else {
