@@ -229,6 +229,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void dh_kernel(VocabLoss p, int
   const int wave = ring_wave();
   const int wm0 = (wave % P::WAVES_M) * P::WM, wn0 = (wave / P::WAVES_M) * P::WN;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM, n0 = static_cast<int64_t>(tile.n) * P::BN;
+  const int unit = work.unit < 0 && p.piece < p.V ? (mt * nt - full) * S + work.tile : work.unit;
   const int ns = max(0, work.hi - work.lo);  // (a last piece may have none for the last parts; theirs still fade)
   const uint16_t *x = p.share, *W = p.W + v0 * p.K;
   f32x4 acc[P::NI][P::NJ];
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void dh_kernel(VocabLoss p, int
   op.sh = p.shift + m0 + wm0 + (threadIdx.x & 15) * P::NJ;
   ring_run<P, true, false, true>(acc, op, ns, smem, wm0, wn0);
   const VocabLoss a = late_args<VocabLoss>();
-  if (work.unit < 0) {
+  if (unit < 0) {
     store_dh<P, P::NJ>(acc, a, m0 + wm0, n0 + wn0, smem);
     return;
   }
@@ -249,7 +250,7 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void dh_kernel(VocabLoss p, int
     const float f = v0 == 0 ? 0.f : a.fade[min<int64_t>(m0 + wm0 + j * 16 + r, a.T - 1)];
 #pragma unroll
     for (int i = 0; i < P::NI; ++i) {
-      f32x4* at = part_at<P>(a.part, work.unit, j, i) + lane;
+      f32x4* at = part_at<P>(a.part, unit, j, i) + lane;
       if (v0 == 0) *at = acc[i][j];
       else *at = *at * f + acc[i][j];
     }
@@ -257,16 +258,18 @@ __global__ __launch_bounds__(P::THREADS, P::OCC) void dh_kernel(VocabLoss p, int
   }
 }
 
-// The tiles in parts: grid (tiles, column blocks of a wave).
+// The tiles with sums in memory: grid (tiles, column blocks of a wave). All of them behind several pieces, else the cut ones.
 template <class P>
 __global__ __launch_bounds__(P::THREADS) void dh_join_kernel(VocabLoss p, int full, int S, int mt, int nt) {
   __shared__ __attribute__((aligned(16))) char smem[P::WAVES * 16 * P::WN * 2];
-  const RingTile tile(full + blockIdx.x, mt, nt, P::GROUP_M);
+  const int L = (p.piece < p.V ? 0 : full) + static_cast<int>(blockIdx.x);
+  const RingTile tile(L, mt, nt, P::GROUP_M);
   const int wave = ring_wave(), j = blockIdx.y;
   const int64_t m0 = static_cast<int64_t>(tile.m) * P::BM + (wave % P::WAVES_M) * P::WM + j * 16;
   const int64_t n0 = static_cast<int64_t>(tile.n) * P::BN + (wave / P::WAVES_M) * P::WN;
   f32x4 acc[P::NI][1];
-  sum_parts<P>(acc, p.part, blockIdx.x, S, j);
+  if (L < full) sum_parts<P>(acc, p.part, (mt * nt - full) * S + L, 1, j);
+  else sum_parts<P>(acc, p.part, L - full, S, j);
   store_dh<P, 1>(acc, p, m0, n0, smem);
 }
 
@@ -285,8 +288,9 @@ hipError_t launch_dh(const VocabLoss& p, int64_t v0, int64_t cols, const RingPla
   const int full = static_cast<int>(r.full), rem = mt * nt - full;
   hipLaunchKernelGGL(dh_kernel<P>, dim3(static_cast<unsigned>(full + rem * r.S)), dim3(P::THREADS), 0, s, p, v0, cols, full,
                      r.S, r.ks, bw, mt, nt);
-  if (last && rem > 0)
-    hipLaunchKernelGGL(dh_join_kernel<P>, dim3(static_cast<unsigned>(rem), P::NJ), dim3(P::THREADS), 0, s, p, full, r.S, mt,
+  const int join = p.piece < p.V ? mt * nt : rem;
+  if (last && join > 0)
+    hipLaunchKernelGGL(dh_join_kernel<P>, dim3(static_cast<unsigned>(join), P::NJ), dim3(P::THREADS), 0, s, p, full, r.S, mt,
                        nt);
   return hipGetLastError();
 }

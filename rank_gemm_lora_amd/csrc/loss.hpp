@@ -23,29 +23,29 @@ struct VocabLoss {
   float* part;                        // parts of dh's tiles
 };
 
-// Columns of the vocabulary per piece: the shares of a piece take at most 1 GiB, and the sums over a piece are added to
-// those before it in memory (T K 8 bytes per piece, which a piece of 8192 columns outweighs eight times over in its
-// products).
+// Columns of the vocabulary per piece: as few pieces of equal width as keep the shares of one at 1 GiB (above 131072 tokens
+// at 8192 bytes a token: 4096 columns). From the second piece on, the sums of every tile of dh pass through memory once
+// each way per piece (T K 8 bytes and those of the cut tiles), which a piece of 4096 columns outweighs four times over in
+// its products.
 inline int64_t loss_piece(int64_t T, int64_t V) {
-  int64_t p = (int64_t(1) << 29) / (T > 0 ? T : 1) / 256 * 256;
-  p = p < 4096 ? 4096 : (p > 524288 ? 524288 : p);  // (its row stride stays below 4 MB)
-  const int64_t all = (V + 255) / 256 * 256;
-  return p < all ? p : all;
+  int64_t most = (int64_t(1) << 29) / (T > 0 ? T : 1) / 256 * 256;
+  most = most < 4096 ? 4096 : (most > 524288 ? 524288 : most);  // (its row stride stays below 4 MB)
+  const int64_t n = (V + most - 1) / most;
+  return ((V + n - 1) / n + 255) / 256 * 256;
 }
 // Blocks of columns for which a power of two and a sum are kept: 64 at a time with the smaller tile, 128 with the larger.
 inline int64_t loss_blocks(int64_t V) { return (V + 127) / 128 * 2; }
 inline int64_t shift_ld(int64_t T) { return (T + 255) / 256 * 256; }
-// The tiles of dh: as a layer's where one piece holds the vocabulary, else each in parts that later pieces are added to.
+// The tiles of dh: as a layer's of a piece's stages. Where there are several pieces the whole tiles have sums in memory too,
+// one part each behind the parts of the cut ones.
 inline RingPlan loss_plan(int64_t T, int64_t K, int64_t V) {
   const int64_t piece = loss_piece(T, V);
-  RingPlan p = ring_plan(T, K, ((V < piece ? V : piece) + 63) / 64);
-  if (V > piece) p.full = 0;
-  return p;
+  return ring_plan(T, K, ((V < piece ? V : piece) + 63) / 64);
 }
 inline size_t loss_part_bytes(int64_t T, int64_t K, int64_t V) {
   const RingPlan p = loss_plan(T, K, V);
-  const int64_t bm = p.big ? 256 : 128;
-  return static_cast<size_t>((p.tiles - p.full) * p.S) * static_cast<size_t>(bm * bm) * 4;
+  const int64_t bm = p.big ? 256 : 128, whole = V > loss_piece(T, V) ? p.full : 0;
+  return static_cast<size_t>((p.tiles - p.full) * p.S + whole) * static_cast<size_t>(bm * bm) * 4;
 }
 hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t s);
 
