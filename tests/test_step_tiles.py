@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import rank_gemm_lora_amd as rg
+from tests import step_ref as sr
 from tests import test_loss as tl
 from tests import test_step as ts
 
@@ -103,6 +104,11 @@ def test_zeros_behind_the_second_term_of_an_adapter_of_two_gigabytes():
 
 # ((T, K, V), its plan)
 LOSS = [
+    # the larger tile of dh, whole behind both tiles of the logits, and cut
+    ((8200, 904, 200), (256, 200, 128, 256, 132, 132, 1, 4)),
+    ((8200, 904, 904), (1024, 904, 256, 256, 132, 132, 1, 15)),
+    ((7300, 2200, 832), (1024, 832, 128, 256, 261, 256, 4, 4)),
+    ((4352, 4096, 3000), (3072, 3000, 256, 256, 272, 256, 6, 8)),
     # several pieces: whole tiles with sums in memory, alone and beside cut ones; all cut
     ((16384, 1024, 33000), (16640, 16360, 256, 256, 256, 256, 1, 260)),
     ((16500, 1032, 33000), (16640, 16360, 256, 256, 325, 256, 3, 87)),
@@ -111,10 +117,13 @@ LOSS = [
     ((8300, 520, 65000), (32512, 32488, 256, 128, 325, 0, 3, 170)),
     ((131100, 64, 128017), (4096, 1041, 256, 128, 1025, 1024, 16, 4)),
 ]
+LOSS_ALONE = ((900, 128, 8200), 256)  # (the logits' tile over the whole vocabulary)
 
 
 def test_plans_of_the_loss(tmp_path):
     assert plans(tmp_path, ["loss %d %d %d" % c for c, _ in LOSS]) == [p for _, p in LOSS]
+    T, K, V = LOSS_ALONE[0]
+    assert plans(tmp_path, [f"ring {T} {V} {stages(K, 0)}"])[0][0] == LOSS_ALONE[1]
 
 
 @pytest.mark.gpu
@@ -129,3 +138,80 @@ def test_loss_with_larger_tiles_and_several_pieces(T, K, V):
     tl.check({k: v[rows] for k, v in got.items()}, tl.reference(c, rows))
     for k, v in got.items():
         assert bool(torch.isfinite(v).all()), k
+
+
+# ----------------------------------------------------------------------------- larger tiles of the layers
+
+def stages(K, R):
+    """Stages of 64 of a contraction of K behind adapters of R columns in two terms."""
+    return -(-K // 64) + -(-2 * R // 64)
+
+
+# (T, K, F, ranks, activation), the forward's plan, dx's
+WHOLE = (256, 132, 132, 1)
+GATED = [((900, 64, 4100, 16, 0, act), WHOLE, None) for act in ("silu", "gelu", "gelu_tanh")]  # (F of no multiple of 8)
+GATED += [((2200, 704, 3656, 24, 16, act), (256, 261, 256, 4), None) for act in ("silu", "gelu", "gelu_tanh")]
+GATED += [((8200, 904, 72, 16, 8, "gelu"), None, WHOLE), ((7300, 2200, 328, 8, 24, "silu"), None, (256, 261, 256, 4)),
+          ((7300, 2200, 264, 0, 72, "gelu_tanh"), None, (256, 261, 256, 4))]
+# (T, K, N, rank, p), the forward's plan, dx's. At rank 136 the extension is five stages of dx: its first part (of four
+# stages) ends before the base stages, and the second part has the mask between its first stage and the others.
+DROP = [((8200, 200, 904, 16, 0.1), WHOLE, None), ((7300, 768, 2200, 16, 0.1), (256, 261, 256, 4), None)]
+DROP += [((8200, 904, 200, 16, p), None, WHOLE) for p in (0.1, 0.0)]
+DROP += [((7300, 2200, 512, 136, p), None, (256, 261, 256, 4)) for p in (0.1, 0.0)]
+DROP += [((7300, 2200, 768, 16, 0.1), None, (256, 261, 256, 4))]
+
+
+def test_plans_of_the_layers(tmp_path):
+    lines, want = [], []
+    for (T, K, F, rg_, ru, _), fwd, bwd in GATED:
+        R = rg_ + ru
+        for plan, line in ((fwd, (T, 2 * F, stages(K, R))), (bwd, (T, K, 2 * stages(F, 0) + stages(0, R)))):
+            if plan is not None:
+                lines.append("ring %d %d %d" % line)
+                want.append(plan)
+    for (T, K, N, R, _), fwd, bwd in DROP:
+        for plan, line in ((fwd, (T, N, stages(K, R))), (bwd, (T, K, stages(N, R)))):
+            if plan is not None:
+                lines.append("ring %d %d %d" % line)
+                want.append(plan)
+    got = plans(tmp_path, lines)
+    assert [p[:4] for p in got] == want
+    assert all(p[4] == 4 for p in got if p[3] == 4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,F,rg_,ru,act", [c for c, _, _ in GATED])
+def test_gated_with_larger_tiles(T, K, F, rg_, ru, act):
+    """Every output whole, from g and u that the larger tile kept."""
+    say("gated tiles", T, K, F, rg_, ru, act)
+    c = ts.gated_case(T, K, F, rg_, ru, 43)
+    backward = F % 8 == 0
+    got = ts.run_gated(c, act, torch.float32, backward=backward)
+    say("reference")
+    want = ts.want_gated(c, act, backward=backward)
+    assert set(got) == set(want)
+    for k, t in got.items():
+        sr.check(t, want[k], BF if k in ("h", "dx") else torch.float32, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,R,p", [c for c, _, _ in DROP])
+def test_dropout_with_larger_tiles(T, K, N, R, p):
+    say("dropout tiles", T, K, N, R, p)
+    c = ts.drop_case(T, K, N, R, 44)
+    how = dict(alpha=1.0 * R, p=p, seed=21, offset=4)
+    got = ts.run_drop(c, torch.float32, **how)
+    say("reference")
+    want = sr.dropout(c["x"], c["W"], c["b"], c["A"], c["B"], 1.0 * R, p, 21, 4, dy=c["dy"])
+    ts.check_drop(got, want, torch.float32, "tiles")
+
+
+@pytest.mark.gpu
+def test_loss_alone_with_larger_tiles():
+    """The loss without its gradient: 256 x 256 tiles of logits, ragged on both sides."""
+    T, K, V = LOSS_ALONE[0]
+    say("loss alone", T, K, V)
+    c = tl.case(T, K, V, 45)
+    got = tl.run(c, want=("loss", "lse"))
+    assert got.pop("dh") is None
+    tl.check(got, tl.reference(c))
