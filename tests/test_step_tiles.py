@@ -215,3 +215,41 @@ def test_loss_alone_with_larger_tiles():
     got = tl.run(c, want=("loss", "lse"))
     assert got.pop("dh") is None
     tl.check(got, tl.reference(c))
+
+
+# ----------------------------------------------------------------------------- the largest extents
+
+MOST_T, MOST_K = (1 << 21) - 1, 1 << 20
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,R", [(MOST_T, 8, 8, 8), (2, 8, MOST_K, 16), (2, MOST_K, 8, 16)])
+def test_dropout_at_the_largest_extents(T, K, N, R):
+    say("dropout extents", T, K, N, R)
+    c = ts.drop_case(T, K, N, R, 46)
+    got = ts.run_drop(c, torch.float32, alpha=1.0 * R, p=0.1, seed=1 << 63, offset=(1 << 64) - 1)
+    say("reference")
+    want = sr.dropout(c["x"], c["W"], c["b"], c["A"], c["B"], 1.0 * R, 0.1, 1 << 63, (1 << 64) - 1, dy=c["dy"])
+    ts.check_drop(got, want, torch.float32, "extents")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,F", [(MOST_T, 8, 8), (3, 8, MOST_K), (3, MOST_K, 8)])
+def test_gated_at_the_largest_extents(T, K, F):
+    say("gated extents", T, K, F)
+    c = ts.gated_case(T, K, F, 16, 8, 47)
+    got = ts.run_gated(c, "silu", torch.float32, save=T > 3)
+    say("reference")
+    want = ts.want_gated(c, "silu")
+    for k, t in got.items():
+        sr.check(t, want[k], BF if k in ("h", "dx") else torch.float32, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,V", [(MOST_T, 8, 9), (1, 8, 1 << 24), (2, MOST_K, 9)])
+def test_loss_at_the_largest_extents(T, K, V):
+    say("loss extents", T, K, V)
+    c = tl.case(T, K, V, 48)
+    got = tl.run(c)
+    say("reference")
+    tl.check(got, tl.reference(c))
