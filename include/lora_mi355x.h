@@ -657,7 +657,9 @@ size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t ra
 /*
  * lora_cross_entropy -- softmax cross entropy over a vocabulary from the hidden
  * states h and the frozen output weight W, and its gradient, in pieces of the
- * vocabulary: the logits l = h.W^T are never kept.
+ * vocabulary. The logits l = h.W^T are not kept; for dh the workspace holds the
+ * exponentials of one piece in bf16, 2 T V bytes up to 2^29 logits (one piece)
+ * and at most max(2^30, 8192 T) beyond.
  *
  *     lse = log(sum over v of exp(l_v)),  loss = lse - l_target,
  *     dh = RN_bf16(dloss . (sum over v != target of p_v W_v - (1 - p_target) W_target)),  p = exp(l - lse)
@@ -670,7 +672,9 @@ size_t lora_gated_bwd_workspace_size(int64_t T, int64_t K, int64_t F, int32_t ra
  *   dloss   [T] fp32 (device): the gradient with respect to each token's loss (1 / the number of
  *           tokens that have one, for their mean), or NULL (1)
  *   loss, lse [T] fp32, dh [T, K] bf16 (row stride lddh): each optional (NULL = not computed)
- *   workspace at least lora_cross_entropy_workspace_size(T, K, V, dh != NULL) bytes
+ *   workspace at least lora_cross_entropy_workspace_size(T, K, V, dh != NULL) bytes: about T V / 8 for the
+ *           statistics, and for dh the exponentials above and partial sums of dh (4 T K bytes where there are
+ *           several pieces, and those of cut tiles, a few hundred MB at most)
  * A token with an infinite or NaN logit has a loss, lse and gradient that need not be finite; no other
  * token's change. The same call gives the same bits. LORA_ERR_UNSUPPORTED from 2^21 tokens, 2^37 logits
  * or 2^34 elements of h on.

@@ -877,6 +877,7 @@ def lora_cross_entropy(h, W, target, dloss=None, want=("loss", "lse", "dh"), los
                        workspace=None, stream=None):
     """Softmax cross entropy of hidden states ``h`` [T, K] under the frozen output weight ``W`` [V, K] (bf16), without
     keeping the logits: returns (loss, lse, dh), each None unless named in ``want`` (loss and lse fp32 [T], dh bf16).
+    (For dh the workspace holds exponentials in bf16: 2 T V bytes up to 2^29 logits, at most max(2^30, 8192 T) beyond.)
 
     ``target``: int64 [T]; a token whose target is outside [0, V) (-100, say) has loss 0 and no gradient. ``dloss``:
     fp32 [T], the gradient with respect to each token's loss (``1 / count`` for their mean), or None for ones: the

@@ -301,6 +301,8 @@ hipError_t launch_vocab_loss(const VocabLoss& p, hipStream_t s) {
   const unsigned tok16 = static_cast<unsigned>((p.T + 15) / 16);
   const bool grad = p.dh != nullptr;
   const int64_t piece = grad ? p.piece : p.V;
+  // (The estimate may count a cut of the last round, which the logits do not make: 13 of 560 sizes tried take a tile that it
+  // puts 2 to 18% behind the other without cuts, 512 tokens of 5120 inputs over 50257 words the smaller one.)
   const bool big = ring_plan(p.T, piece < p.V ? piece : p.V, (p.K + 63) / 64).big;
   const int bw = big ? Ring256::WN : Ring128::WN;
   const RingPlan r = loss_plan(p.T, p.K, p.V);

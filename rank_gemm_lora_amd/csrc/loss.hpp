@@ -25,7 +25,7 @@ struct VocabLoss {
 
 // Columns of the vocabulary per piece: as few pieces of equal width as keep the shares of one at 1 GiB (above 131072 tokens
 // at 8192 bytes a token: 4096 columns). From the second piece on, the sums of every tile of dh pass through memory once
-// each way per piece (T K 8 bytes and those of the cut tiles), which a piece of 4096 columns outweighs four times over in
+// each way per piece (T K 8 bytes and those of the cut tiles), which a piece of 4096 columns outweighs six times over in
 // its products.
 inline int64_t loss_piece(int64_t T, int64_t V) {
   int64_t most = (int64_t(1) << 29) / (T > 0 ? T : 1) / 256 * 256;

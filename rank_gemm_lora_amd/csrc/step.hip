@@ -352,7 +352,7 @@ struct DropNnOp : NnOp<P, 1, 1> {
 enum { kFormNt = 0, kFormNn = 1, kFormNn2 = 2, kFormNnDrop = 3 };  // (Nn2: two segments, two adapters)
 
 // One layer: a workgroup per whole tile, then one per part of the others. Bound by the matrix pipes and the power they may
-// draw. NT, 18871 tokens, 8960 -> 1536: 464 us, 1.12 PFLOP/s (444 tiles of 256 units: the last round is cut); NN, the gated
+// draw. NT, 18871 tokens, 8960 -> 1536: 464 us, 1.12 PFLOP/s (444 whole tiles, 1.7 rounds of 256 units); NN, the gated
 // dx of 4352 tokens, two times 14336 -> 4096: 901 us, 1.13; NN masked, dx of 18871 tokens, 1536 -> 8960: 651 us, of which
 // the masks are 66.
 template <class P, int FORM>
@@ -460,7 +460,7 @@ __device__ __forceinline__ void act_of(float g, float& a, float& da) {
   } else if constexpr (ACT == 1) {
     // g Phi(g): the tail Phi(-|g|) = erfc(z) / 2, z = |g| / sqrt 2, whose exponential is also the derivative's density.
     // erfc(z) exp(z^2) = t P(t), t = 1 / (1 + z / 2): P of degree 8 fitted to the least relative error over z in [0, 10]
-    // (4e-8; 4e-7 with fp32's roundings), so that the tail keeps its digits however small it is.
+    // (1.3e-7 with these coefficients; 4e-7 with fp32's roundings), so that the tail keeps its digits however small it is.
     const float z = __builtin_fabsf(g) * 0.70710678118655f;
     const float t = __builtin_amdgcn_rcpf(1.f + 0.5f * z), e = fast_exp(-z * z);
     constexpr float kP[9] = {2.82088987e-01f, 2.82322961e-01f, 2.43534581e-01f, 2.00811248e-01f, -2.18574236e-02f,
@@ -518,8 +518,8 @@ __device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][NJ], const
 }
 
 // BN / 2 outputs per tile: gate and up blocks of 16 rows in turn, so that a lane has g and u of the same outputs and the
-// activation needs no exchange. Bound by the matrix pipes: 12288 tokens, 4096 -> 14336: 2.15 ms, 1.34 PFLOP/s; pipes 68% busy
-// at 1.8 GHz. A tile's start and epilogue are 15 of its 115 us (ring filling 4, activation and stores 10); a stage takes 1.5,
+// activation needs no exchange. Bound by the matrix pipes: 12288 tokens, 4096 -> 14336: 2.15 to 2.25 ms by the card, 1.28 to
+// 1.34 PFLOP/s (2.40 ms under the profiler); pipes 68% busy at 1.8 GHz. A tile's start and epilogue are 15 of its 115 us (ring filling 4, activation and stores 10); a stage takes 1.5,
 // 1.1 of it MFMAs. All operands from L2 made it 4% faster; what a stage computes for the next, spread between its MFMAs
 // instead of before them, 1% slower.
 template <class P, int ACT>

@@ -98,7 +98,7 @@ inline int64_t ring_stages(const RingArgs& p) {
 // joins. Chosen by an estimate of the time in microseconds (256 units; measured on MI355X: a stage of 64 indices takes a
 // 256 x 256 tile 1.7, two 128 x 128 tiles side by side 1.0; filling the ring and the epilogue take 8 and 5; the second
 // launch 6, and a sum is written and read at 4 TB/s). 4352 tokens, dx of 4096 -> 14336 in two segments: 272 tiles are one
-// round and 16 tiles; whole, 1222 us (in 128 x 128 tiles); the 16 cut into 16 parts each, 901 and 15 for the joining.
+// round and 16 tiles; whole, 1222 us (in 128 x 128 tiles); the 16 cut into 15 parts each, 901 and 15 for the joining.
 struct RingPlan {
   bool big;
   int64_t tiles;
@@ -175,7 +175,8 @@ struct GatedFew {
 };
 // Up to 64 tokens, and up to 128 (one tile) where the weights are long: whole calls, this against the other way, 4096 ->
 // 14336: 1 token 66 against 86 us, 64 tokens 72 against 88, 65 71 against 88, 128 79 against 90; 1536 -> 8960: 1 token 21
-// against 28, 64 tokens 26 against 30, 65 27 against 29, 100 32 against 30.
+// against 28, 64 tokens 26 against 30, 65 27 against 29, 100 32 against 30. (Long: between these two layers, of 2^23.7 and
+// 2^25.8 elements; the crossing itself was not located.)
 constexpr int64_t kGatedFewT = 64, kGatedFewLongT = 128, kGatedFewLong = int64_t(1) << 25;
 inline bool gated_few(int64_t T, int64_t K, int64_t F) {
   return T <= kGatedFewT || (T <= kGatedFewLongT && K * F >= kGatedFewLong);

@@ -363,7 +363,6 @@ void gated_spans(const lora_gated_layer* l, int64_t K, int64_t F, const Side (&s
   out[7] = span2d(l->B_up, F, s[1].given, s[1].given, 2);
 }
 
-// The active adapters' sides of a problem with two: their count of columns, and each in its place.
 hipError_t gated_forward(const void* x, int64_t T, int64_t K, int64_t ldx, const lora_gated_layer* l, const Side (&s)[2],
                          int64_t F, int32_t act, void* h, int64_t ldh, float* saved, uint16_t* tt, float* part,
                          hipStream_t st) {
