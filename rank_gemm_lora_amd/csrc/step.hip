@@ -519,9 +519,9 @@ __device__ __forceinline__ void gated_store(const f32x4 (&acc)[P::NI][NJ], const
 
 // BN / 2 outputs per tile: gate and up blocks of 16 rows in turn, so that a lane has g and u of the same outputs and the
 // activation needs no exchange. Bound by the matrix pipes: 12288 tokens, 4096 -> 14336: 2.15 to 2.25 ms by the card, 1.28 to
-// 1.34 PFLOP/s (2.40 ms under the profiler); pipes 68% busy at 1.8 GHz. A tile's start and epilogue are 15 of its 115 us (ring filling 4, activation and stores 10); a stage takes 1.5,
-// 1.1 of it MFMAs. All operands from L2 made it 4% faster; what a stage computes for the next, spread between its MFMAs
-// instead of before them, 1% slower.
+// 1.34 PFLOP/s (2.40 ms under the profiler); pipes 68% busy at 1.8 GHz. A tile's start and epilogue are 15 of its 115 us
+// (ring filling 4, activation and stores 10); a stage takes 1.5, 1.1 of it MFMAs. All operands from L2 made it 4% faster;
+// what a stage computes for the next, spread between its MFMAs instead of before them, 1% slower.
 template <class P, int ACT>
 __global__ __launch_bounds__(P::THREADS, P::OCC) void gated_kernel(RingArgs p, int mt, int nt, int NS) {
   __shared__ __attribute__((aligned(1024))) char smem[P::SLOTS * P::SLOT_BYTES];

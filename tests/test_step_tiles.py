@@ -108,7 +108,7 @@ LOSS = [
     ((8200, 904, 200), (256, 200, 128, 256, 132, 132, 1, 4)),
     ((8200, 904, 904), (1024, 904, 256, 256, 132, 132, 1, 15)),
     ((7300, 2200, 832), (1024, 832, 128, 256, 261, 256, 4, 4)),
-    ((4352, 4096, 3000), (3072, 3000, 256, 256, 272, 256, 6, 8)),
+    ((4352, 4096, 2600), (2816, 2600, 256, 256, 272, 256, 6, 7)),
     # several pieces: whole tiles with sums in memory, alone and beside cut ones; all cut
     ((16384, 1024, 33000), (16640, 16360, 256, 256, 256, 256, 1, 260)),
     ((16500, 1032, 33000), (16640, 16360, 256, 256, 325, 256, 3, 87)),
